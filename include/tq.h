@@ -75,6 +75,7 @@ typedef enum tq_status {
 #define TQ_DEV_SEQ_LEN 0x2   /* decode: seq_lens[b] < 0 or > max_seq_len; clamped into range */
 #define TQ_DEV_TIMEOUT 0x4   /* a pipeline wait exceeded its time limit; the CTA gave up */
 #define TQ_DEV_PAGE 0x8      /* paged cache: a block-table entry outside [0, num_pages); page 0 used instead */
+#define TQ_DEV_BLOCK 0x10    /* tq_sdpa_blocks_decode: a listed block starts at or past seq_lens[b]; left out */
 
 /* Rotation flags ("Running and Evaluating TurboQuant optimized Gemma 4",
  * TurboQuant section: vectors are rotated by the normalised Sylvester Hadamard
@@ -472,6 +473,169 @@ tq_status tq_sdpa_int4_decode_noalloc(const tq_kv_cache* cache, const uint16_t* 
                                       int32_t max_seq_len, float attn_scale,
                                       int32_t chunk, uint16_t* out,
                                       int32_t* status, void* stream);
+
+/* ------------------------------------------------------- rotary positions --
+ * Turns query and key rows by rotary positions with up to four axes (time,
+ * height, width, ... of text, images and video), from the projections' layout
+ * into the append's ("turboquant-llama3.170B" README, decode-step listing:
+ * RoPE comes before the quantize-on-store).
+ * Pair i (0 <= i < rotary_dim / 2) of a row at position t of sequence b turns by
+ *   angle = positions[axis(i)][b][t] * inv_freq[i],
+ * where the first sections[0] pairs follow axis 0, the next sections[1] axis 1,
+ * and so on.  A pair is (x_i, x_{i + rotary_dim/2}), or with TQ_ROPE_PAIRS
+ * (x_{2i}, x_{2i+1}); it becomes (x1 cos - x2 sin, x2 cos + x1 sin), computed
+ * in fp32 from an angle reduced in fp64 and rounded once.  Elements from
+ * rotary_dim on are copied.  TQ_ROPE_INVERSE turns by -angle: the transpose,
+ * hence also the gradient of the rows.
+ *   q, k       tq_rope_rows each (k may be NULL): x[b * stride_b + t * stride_t
+ *              + h * stride_h + d] in, out [batch][num_heads][n][head_dim]
+ *              contiguous; strides in elements, multiples of 8, not negative
+ *   positions  device int32 [n_axes][batch][n] (any value, also negative)
+ *   inv_freq   device fp32 [rotary_dim / 2]
+ *   sections   HOST int32 [n_axes], sum rotary_dim / 2 (zeros allowed)
+ * head_dim 64, 128 or 256; rotary_dim a multiple of 16 up to head_dim; batch
+ * up to 65,535; n = 0 launches nothing.  An out that overlaps an x or the other
+ * out: TQ_ERR_SHAPE. */
+#define TQ_ROPE_PAIRS 0x1u
+#define TQ_ROPE_INVERSE 0x2u
+#define TQ_ROPE_MAX_AXES 4
+typedef struct tq_rope_rows {
+    const uint16_t* x;
+    uint16_t* out;
+    int64_t stride_b, stride_t, stride_h;
+    int32_t num_heads;
+} tq_rope_rows;
+tq_status tq_rope_axes(const tq_rope_rows* q, const tq_rope_rows* k, const int32_t* positions,
+                       const float* inv_freq, int32_t n_axes, const int32_t* sections, int32_t batch,
+                       int32_t n, int32_t head_dim, int32_t rotary_dim, uint32_t flags, void* stream);
+
+/* ----------------------------------------------------------- sparse decode --
+ * Decode attention over the blocks of cached tokens that a cheap score selects
+ * for the query, instead of all of them.  Blocks are block_tokens = 32, 64 or
+ * 128 consecutive tokens of a sequence; block j holds rows
+ * [j * block_tokens, (j + 1) * block_tokens).  Works on every cache the decode
+ * works on (int4 and int8, contiguous and paged, rotated with the flags it was
+ * written with).
+ *
+ * Bounds: for every block and kv head the least and the greatest cached key of
+ * each channel, fp16 [batch][num_kv_heads][ceil(capacity / block_tokens)][2]
+ * [head_dim] (0: least, 1: greatest), of fp16(scale * code + bias); of the
+ * rotated keys where keys are stored rotated.  tq_block_bounds_bytes: their
+ * size (0 for invalid sizes).
+ * tq_kv_block_bounds recomputes the bounds of every block that rows
+ * [start[b], start[b] + n_rows) of sequence b touch, from the block's rows
+ * below start[b] + n_rows: call it after each append with its write_pos and
+ * n_new.  Other blocks are left as they were.  A range outside the cache sets
+ * TQ_DEV_WRITE_POS and leaves that sequence out. */
+size_t tq_block_bounds_bytes(int32_t batch, int32_t num_kv_heads, int32_t head_dim, int32_t capacity,
+                             int32_t block_tokens);
+tq_status tq_kv_block_bounds(const tq_kv_cache* cache, int32_t block_tokens, const int32_t* start,
+                             int32_t n_rows, uint16_t* bounds, int32_t* status, void* stream);
+tq_status tq_paged_kv_block_bounds(const tq_paged_kv_cache* cache, int32_t block_tokens,
+                                   const int32_t* start, int32_t n_rows, uint16_t* bounds,
+                                   int32_t* status, void* stream);
+
+/* Selection: blocks [batch][num_kv_heads][n_select], ascending, -1 behind the
+ * last where a sequence has fewer.  With nb = ceil(seq_lens[b] / block_tokens):
+ * all of them if nb <= n_select; else the first n_first, the last n_last and,
+ * of the others, the n_select - n_first - n_last of greatest score
+ *   max over the kv head's query heads of  sum_d max(q_d least_d, q_d greatest_d),
+ * no q.k of the block exceeds it.  Equal scores: the lowest index first.  The
+ * order is that of the exact scores (blocks whose fp32 scores are too close to
+ * the border are scored again in fp64, in the workspace).
+ * n_first + n_last <= n_select; at most 49,152 blocks (TQ_ERR_UNSUPPORTED).
+ * What the bounds of always listed blocks hold does not matter.
+ * The bounds are those of a cache of `capacity` tokens.  flags: TQ_ROTATE_K
+ * where its keys are stored rotated (TQ_ROTATE_V is ignored).
+ * workspace: tq_sparse_workspace_bytes(...) bytes, 256-byte aligned, one per
+ * call in flight. */
+size_t tq_sparse_workspace_bytes(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
+                                 int32_t head_dim, int32_t max_seq_len, int32_t n_select,
+                                 int32_t block_tokens);
+tq_status tq_select_blocks(const uint16_t* bounds, const uint16_t* q, int32_t batch, int32_t num_q_heads,
+                           int32_t num_kv_heads, int32_t head_dim, int32_t capacity,
+                           const int32_t* seq_lens, int32_t max_seq_len, int32_t block_tokens,
+                           int32_t n_select, int32_t n_first, int32_t n_last, uint32_t flags,
+                           void* workspace, size_t workspace_bytes, int32_t* blocks, int32_t* status,
+                           void* stream);
+
+/* The decode (tq_sdpa_int4_decode_ex) over the rows below seq_lens[b] of the
+ * listed blocks: blocks [batch][num_kv_heads][n_select], entries below 0 are
+ * empty, an entry that starts at or past seq_lens[b] sets TQ_DEV_BLOCK and is
+ * left out.  Any order; a block listed twice counts twice.  A kv head whose
+ * list is empty gives zero output rows.  Precision as the decode's. */
+tq_status tq_sdpa_blocks_decode(const tq_kv_cache* cache, const uint16_t* q, int32_t num_q_heads,
+                                const int32_t* seq_lens, int32_t max_seq_len, float attn_scale,
+                                const int32_t* blocks, int32_t n_select, int32_t block_tokens,
+                                uint32_t flags, void* workspace, size_t workspace_bytes, uint16_t* out,
+                                int32_t* status, void* stream);
+tq_status tq_paged_sdpa_blocks_decode(const tq_paged_kv_cache* cache, const uint16_t* q,
+                                      int32_t num_q_heads, const int32_t* seq_lens, int32_t max_seq_len,
+                                      float attn_scale, const int32_t* blocks, int32_t n_select,
+                                      int32_t block_tokens, uint32_t flags, void* workspace,
+                                      size_t workspace_bytes, uint16_t* out, int32_t* status,
+                                      void* stream);
+
+/* Both in one call: the selection into `blocks`, then the decode over it. */
+tq_status tq_sparse_decode(const tq_kv_cache* cache, const uint16_t* bounds, const uint16_t* q,
+                           int32_t num_q_heads, const int32_t* seq_lens, int32_t max_seq_len,
+                           float attn_scale, int32_t block_tokens, int32_t n_select, int32_t n_first,
+                           int32_t n_last, uint32_t flags, void* workspace, size_t workspace_bytes,
+                           int32_t* blocks, uint16_t* out, int32_t* status, void* stream);
+tq_status tq_paged_sparse_decode(const tq_paged_kv_cache* cache, const uint16_t* bounds, const uint16_t* q,
+                                 int32_t num_q_heads, const int32_t* seq_lens, int32_t max_seq_len,
+                                 float attn_scale, int32_t block_tokens, int32_t n_select,
+                                 int32_t n_first, int32_t n_last, uint32_t flags, void* workspace,
+                                 size_t workspace_bytes, int32_t* blocks, uint16_t* out, int32_t* status,
+                                 void* stream);
+
+/* --------------------------------------------------------------- eviction --
+ * The decode (tq_sdpa_int4_decode_ex) that also keeps account of what was
+ * attended to: for every row t < seq_lens[b] of kv head h
+ *   weights[b][h][t] = decay * weights[b][h][t] + sum over the kv head's query
+ *                      heads of softmax(attn_scale q.K)_t
+ * (decay = 0: the old value is not read).  weights: fp32 [batch][num_kv_heads]
+ * [capacity]; rows from seq_lens[b] on are neither read nor written, so the
+ * caller zeroes a row's weight no later than its append (an array that starts
+ * as zeros, or that tq_kv_evict wrote, is ready).  The weights' fp32 values are
+ * within 1e-5 relative (L2) of fp64 over the same cache.
+ * workspace: tq_weights_workspace_bytes(...) bytes (the scores, 4 bytes per
+ * query head and token of max_seq_len, and the decode's), 256-byte aligned. */
+size_t tq_weights_workspace_bytes(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
+                                  int32_t head_dim, int32_t max_seq_len);
+tq_status tq_sdpa_decode_weights(const tq_kv_cache* cache, const uint16_t* q, int32_t num_q_heads,
+                                 const int32_t* seq_lens, int32_t max_seq_len, float attn_scale,
+                                 float decay, float* weights, uint32_t flags, void* workspace,
+                                 size_t workspace_bytes, uint16_t* out, int32_t* status, void* stream);
+tq_status tq_paged_sdpa_decode_weights(const tq_paged_kv_cache* cache, const uint16_t* q,
+                                       int32_t num_q_heads, const int32_t* seq_lens, int32_t max_seq_len,
+                                       float attn_scale, float decay, float* weights, uint32_t flags,
+                                       void* workspace, size_t workspace_bytes, uint16_t* out,
+                                       int32_t* status, void* stream);
+
+/* Eviction by weight: of every (sequence, kv head) of src with more than `keep`
+ * rows, the last `recent` rows and, of the rows before them, the keep - recent
+ * of greatest weight (equal weights, and -0 and 0, the lowest row first) move,
+ * in their order, to rows [0, keep) of dst; one with at most `keep` rows moves
+ * whole.  Codes, scales and biases are copied as they are.
+ *   weights      fp32 [batch][num_kv_heads][src capacity]
+ *   dst_weights  fp32 [batch][num_kv_heads][dst capacity]: the kept rows'
+ *                weights, zeros behind them
+ *   dst_lens     int32 [batch]: min(seq_lens[b], keep)
+ *   kept         int32 [batch][num_kv_heads][keep]: the src row of each dst
+ *                row, -1 behind the last
+ * Rows of dst behind the kept ones are left as they were.  Both caches have
+ * the same batch, heads, head_dim and bits; 0 <= recent <= keep <= dst
+ * capacity; batch * num_kv_heads <= 65,535.  What is written must not overlap
+ * what is read (TQ_ERR_SHAPE); paged caches may share a pool, but a page in
+ * both tables (or twice in dst's) gives undefined rows. */
+tq_status tq_kv_evict(const tq_kv_cache* src, const tq_kv_cache* dst, const float* weights,
+                      const int32_t* seq_lens, int32_t max_seq_len, int32_t keep, int32_t recent,
+                      float* dst_weights, int32_t* dst_lens, int32_t* kept, int32_t* status, void* stream);
+tq_status tq_paged_kv_evict(const tq_paged_kv_cache* src, const tq_paged_kv_cache* dst,
+                            const float* weights, const int32_t* seq_lens, int32_t max_seq_len,
+                            int32_t keep, int32_t recent, float* dst_weights, int32_t* dst_lens,
+                            int32_t* kept, int32_t* status, void* stream);
 
 #ifdef __cplusplus
 }

@@ -22,6 +22,9 @@ __all__ = [
     "tq_sdpa_plan", "tq_split_plan", "tq_sdpa_int4_decode_noalloc", "NOALLOC_SCRATCH_BYTES", "tq_decode_step",
     "tq_dequantize_kv", "tq_hadamard_rotate", "TQ_ROTATE_K", "TQ_ROTATE_V", "TQ_STEP_ADVANCE", "TQ_DEV_PAGE",
     "tq_paged_kv_cache", "PagedKVCache", "tq_decode_step_host", "tq_host_staging_bytes",
+    "TQ_DEV_BLOCK", "TQ_ROPE_PAIRS", "TQ_ROPE_INVERSE", "tq_rope_axes", "block_bounds", "tq_kv_block_bounds",
+    "sparse_workspace", "tq_select_blocks", "tq_sdpa_blocks_decode", "tq_sparse_decode", "weights_workspace",
+    "tq_sdpa_decode_weights", "tq_kv_evict",
 ]
 
 TQ_OK = 0
@@ -30,6 +33,8 @@ TQ_DEV_WRITE_POS, TQ_DEV_SEQ_LEN, TQ_DEV_TIMEOUT = 0x1, 0x2, 0x4
 TQ_ROTATE_K, TQ_ROTATE_V = 0x1, 0x2
 TQ_STEP_ADVANCE = 0x100
 TQ_DEV_PAGE = 0x8
+TQ_DEV_BLOCK = 0x10
+TQ_ROPE_PAIRS, TQ_ROPE_INVERSE = 0x1, 0x2
 GROUP_SIZE = 64
 DEFAULT_CHUNK = 512
 NOALLOC_SCRATCH_BYTES = 4 << 20
@@ -71,6 +76,14 @@ class tq_paged_kv_cache(ctypes.Structure):
         ("head_dim", ctypes.c_int32), ("group_size", ctypes.c_int32),
         ("page_tokens", ctypes.c_int32), ("num_pages", ctypes.c_int32),
         ("max_pages_per_seq", ctypes.c_int32), ("bits", ctypes.c_int32),
+    ]
+
+
+class tq_rope_rows(ctypes.Structure):
+    _fields_ = [
+        ("x", ctypes.c_void_p), ("out", ctypes.c_void_p),
+        ("stride_b", ctypes.c_int64), ("stride_t", ctypes.c_int64), ("stride_h", ctypes.c_int64),
+        ("num_heads", ctypes.c_int32),
     ]
 
 
@@ -120,6 +133,18 @@ def lib() -> ctypes.CDLL:
             "tq_paged_sdpa_int4_decode": ([PC, P, i32, P, i32, f32, i32, u32, P, sz, P, P, P], i32),
             "tq_paged_decode_step": ([PC, P, P, i32, P, P, i32, P, i32, f32, i32, u32, P, sz, P, P, P], i32),
         }
+        R = ctypes.POINTER(tq_rope_rows)
+        for pre, cache in (("tq_", C), ("tq_paged_", PC)):
+            sig[pre + "kv_block_bounds"] = ([cache, i32, P, i32, P, P, P], i32)
+            sig[pre + "sdpa_blocks_decode"] = ([cache, P, i32, P, i32, f32, P, i32, i32, u32, P, sz, P, P, P], i32)
+            sig[pre + "sparse_decode"] = ([cache, P, P, i32, P, i32, f32, i32, i32, i32, i32, u32, P, sz, P, P, P, P], i32)
+            sig[pre + "sdpa_decode_weights"] = ([cache, P, i32, P, i32, f32, f32, P, u32, P, sz, P, P, P], i32)
+            sig[pre + "kv_evict"] = ([cache, cache, P, P, i32, i32, i32, P, P, P, P, P], i32)
+        sig["tq_rope_axes"] = ([R, R, P, P, i32, P, i32, i32, i32, i32, u32, P], i32)
+        sig["tq_block_bounds_bytes"] = ([i32] * 5, sz)
+        sig["tq_sparse_workspace_bytes"] = ([i32] * 7, sz)
+        sig["tq_select_blocks"] = ([P, P] + [i32] * 5 + [P] + [i32] * 5 + [u32, P, sz, P, P, P], i32)
+        sig["tq_weights_workspace_bytes"] = ([i32] * 5, sz)
         for name, (args, res) in sig.items():
             fn = getattr(L, name)
             fn.argtypes = args
@@ -540,3 +565,245 @@ def tq_decode_step_host(cache: KVCache, h_k_new: torch.Tensor, h_v_new: torch.Te
         int(max_seq_len), float(attn_scale), int(chunk), int(flags), _ptr(workspace), workspace.numel(),
         _ptr(staging), staging.numel(), _ptr(h_out), _ptr(status), _stream(stream)))
     return h_out
+
+
+# ------------------------------------------------- rotary positions, sparse decode, eviction
+def _same_device(first: torch.Tensor, *others) -> None:
+    dev = first.device
+    for t in others:
+        if t is not None and t.device != dev:
+            raise ValueError(f"tensors on different devices: {dev} and {t.device}")
+    if dev.index != torch.cuda.current_device():
+        raise ValueError(f"tensors on {dev}, but the current device is cuda:{torch.cuda.current_device()}")
+
+
+def _rope_rows(x: torch.Tensor, out: torch.Tensor, name: str) -> tq_rope_rows:
+    if not x.is_cuda or x.dtype != torch.float16 or x.dim() != 4 or x.stride(3) != 1:
+        raise ValueError(f"{name}: expected a CUDA float16 tensor [B, n, heads, D] with a contiguous last dimension")
+    sb, st, sh, _ = x.stride()
+    b, n, h, _ = x.shape
+    # a dimension of one is never stepped along, whatever its stride says
+    return tq_rope_rows(x.data_ptr(), out.data_ptr(), sb if b > 1 else 0, st if n > 1 else 0, sh if h > 1 else 0, h)
+
+
+def tq_rope_axes(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tensor, inv_freq: torch.Tensor, sections,
+                 q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None, flags: int = 0, stream=None):
+    """Rotary positions with several axes: q [B, n, Hq, D] and k [B, n, Hkv, D]
+    (or None) fp16, any strides of whole 8-element steps, -> [B, Hq, n, D] and
+    [B, Hkv, n, D].  positions int32 [axes, B, n]; inv_freq fp32
+    [rotary_dim / 2]; sections: how many of the pairs follow each axis.  flags:
+    TQ_ROPE_PAIRS (neighbouring elements form a pair), TQ_ROPE_INVERSE (turn back;
+    the gradient of the rows)."""
+    _need(positions, torch.int32, "positions")
+    _need(inv_freq, torch.float32, "inv_freq")
+    if q.dim() != 4 or (k is not None and (k.dim() != 4 or k.shape[:2] != q.shape[:2] or k.shape[3] != q.shape[3])):
+        raise ValueError("q and k must be [B, n, heads, D] with the same B, n and D")
+    b, n, hq, d = q.shape
+    if tuple(positions.shape) != (len(sections), b, n):
+        raise ValueError(f"positions must be [axes, B, n] = {(len(sections), b, n)}; got {tuple(positions.shape)}")
+    if q_out is None:
+        q_out = torch.empty((b, hq, n, d), dtype=torch.float16, device=q.device)
+    if k is not None and k_out is None:
+        k_out = torch.empty((b, k.shape[2], n, d), dtype=torch.float16, device=q.device)
+    for x, o, name in ((q, q_out, "q_out"), (k, k_out, "k_out")):
+        if x is None:
+            continue
+        _need(o, torch.float16, name)
+        if tuple(o.shape) != (b, x.shape[2], n, d):
+            raise ValueError(f"{name} must be [B, heads, n, D] = {(b, x.shape[2], n, d)}; got {tuple(o.shape)}")
+    _same_device(q, k, positions, inv_freq, q_out, k_out if k is not None else None)
+    if n == 0:
+        return (q_out, k_out) if k is not None else q_out
+    rq = _rope_rows(q, q_out, "q")
+    rk = None if k is None else ctypes.byref(_rope_rows(k, k_out, "k"))
+    sec = (ctypes.c_int32 * len(sections))(*sections)
+    _check("tq_rope_axes", lib().tq_rope_axes(ctypes.byref(rq), rk, _ptr(positions), _ptr(inv_freq), len(sections), sec, b, n,
+                                              d, 2 * inv_freq.numel(), int(flags), _stream(stream)))
+    return (q_out, k_out) if k is not None else q_out
+
+
+def _fn(cache, name: str):
+    """The entry point of the cache's layout."""
+    return getattr(lib(), ("tq_paged_" if getattr(cache, "paged", False) else "tq_") + name)
+
+
+def block_bounds(cache, block_tokens: int = 64) -> torch.Tensor:
+    """The bounds of every block of a cache, fp16 [B, Hkv, ceil(capacity / block_tokens), 2, D] (zero-filled;
+    tq_kv_block_bounds fills them as rows arrive)."""
+    if int(lib().tq_block_bounds_bytes(cache.batch, cache.num_kv_heads, cache.head_dim, cache.capacity, block_tokens)) == 0:
+        raise ValueError("block_tokens must be 32, 64 or 128")
+    return torch.zeros((cache.batch, cache.num_kv_heads, -(-cache.capacity // block_tokens), 2, cache.head_dim),
+                       dtype=torch.float16, device=cache.buffer.device)
+
+
+def _need_bounds(cache, bounds: torch.Tensor, block_tokens: int) -> None:
+    _need(bounds, torch.float16, "bounds")
+    shape = (cache.batch, cache.num_kv_heads, -(-cache.capacity // block_tokens), 2, cache.head_dim)
+    if bounds.shape != shape:
+        raise ValueError(f"bounds must be {shape}; got {tuple(bounds.shape)}")
+
+
+def _need_lens(t: torch.Tensor, batch: int, name: str) -> None:
+    _need(t, torch.int32, name)
+    if t.numel() != batch:
+        raise ValueError(f"{name} must hold one entry per sequence; got {tuple(t.shape)}")
+
+
+def tq_kv_block_bounds(cache, bounds: torch.Tensor, start: torch.Tensor, n_rows: int, block_tokens: int = 64,
+                       status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Recompute the bounds of the blocks that rows [start[b], start[b] + n_rows) touch
+    (after an append: its write_pos and n_new)."""
+    _need_bounds(cache, bounds, block_tokens)
+    _need_lens(start, cache.batch, "start")
+    if status is not None:
+        _need(status, torch.int32, "status")
+    _same_device(cache.buffer, bounds, start, status)
+    _check("tq_kv_block_bounds", _fn(cache, "kv_block_bounds")(cache.ref(), int(block_tokens), _ptr(start), int(n_rows),
+                                                              _ptr(bounds), _ptr(status), _stream(stream)))
+    return bounds
+
+
+def sparse_workspace(batch: int, num_q_heads: int, num_kv_heads: int, head_dim: int, max_seq_len: int, n_select: int,
+                     block_tokens: int = 64, device="cuda") -> torch.Tensor:
+    """A workspace for tq_select_blocks, tq_sdpa_blocks_decode and tq_sparse_decode of these sizes."""
+    n = int(lib().tq_sparse_workspace_bytes(batch, num_q_heads, num_kv_heads, head_dim, max_seq_len, n_select, block_tokens))
+    if n == 0:
+        raise ValueError("invalid sizes")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def _need_blocks(cache, blocks: torch.Tensor) -> None:
+    _need(blocks, torch.int32, "blocks")
+    if blocks.dim() != 3 or blocks.shape[0] != cache.batch or blocks.shape[1] != cache.num_kv_heads:
+        raise ValueError(f"blocks must be [B, Hkv, n_select]; got {tuple(blocks.shape)}")
+
+
+def _need_query(cache, q: torch.Tensor, out: Optional[torch.Tensor]) -> torch.Tensor:
+    _need(q, torch.float16, "q")
+    if out is None:
+        out = torch.empty_like(q)
+    _need(out, torch.float16, "out")
+    if q.dim() != 3 or q.shape[0] != cache.batch or q.shape[2] != cache.head_dim or out.shape != q.shape:
+        raise ValueError(f"q must be [B, Hq, D]; got {tuple(q.shape)}")
+    return out
+
+
+def tq_select_blocks(bounds: torch.Tensor, q: torch.Tensor, seq_lens: torch.Tensor, max_seq_len: int, workspace: torch.Tensor,
+                     blocks: torch.Tensor, capacity: int, block_tokens: int = 64, n_first: int = 1, n_last: int = 1,
+                     status: Optional[torch.Tensor] = None, stream=None, flags: int = 0) -> torch.Tensor:
+    """The blocks [B, Hkv, n_select] that the query's score against the bounds of a cache of ``capacity`` tokens
+    selects (ascending, -1 behind the last), written to ``blocks``."""
+    _need(bounds, torch.float16, "bounds")
+    _need(q, torch.float16, "q")
+    _need(blocks, torch.int32, "blocks")
+    _need(workspace, torch.uint8, "workspace")
+    if status is not None:
+        _need(status, torch.int32, "status")
+    if q.dim() != 3 or blocks.dim() != 3 or bounds.dim() != 5 or blocks.shape[0] != q.shape[0]:
+        raise ValueError("q must be [B, Hq, D], blocks [B, Hkv, n_select] and bounds [B, Hkv, n_blocks, 2, D]")
+    b, hkv, n_select = blocks.shape
+    if tuple(bounds.shape) != (b, hkv, -(-int(capacity) // block_tokens), 2, q.shape[2]):
+        raise ValueError(f"bounds do not match blocks, q and capacity; got {tuple(bounds.shape)}")
+    _need_lens(seq_lens, b, "seq_lens")
+    _same_device(q, bounds, seq_lens, workspace, blocks, status)
+    _check("tq_select_blocks", lib().tq_select_blocks(
+        _ptr(bounds), _ptr(q), b, q.shape[1], hkv, q.shape[2], int(capacity), _ptr(seq_lens), int(max_seq_len),
+        int(block_tokens), n_select, int(n_first), int(n_last), int(flags), _ptr(workspace), workspace.numel(),
+        _ptr(blocks), _ptr(status), _stream(stream)))
+    return blocks
+
+
+def tq_sdpa_blocks_decode(cache, q: torch.Tensor, blocks: torch.Tensor, seq_lens: torch.Tensor, max_seq_len: int,
+                          attn_scale: float, workspace: torch.Tensor, out: Optional[torch.Tensor] = None,
+                          block_tokens: int = 64, status: Optional[torch.Tensor] = None, stream=None,
+                          flags: int = 0) -> torch.Tensor:
+    """Decode attention over the rows below seq_lens of the listed blocks [B, Hkv, n_select] (entries below 0: none)."""
+    out = _need_query(cache, q, out)
+    _need_blocks(cache, blocks)
+    _need_lens(seq_lens, cache.batch, "seq_lens")
+    _need(workspace, torch.uint8, "workspace")
+    if status is not None:
+        _need(status, torch.int32, "status")
+    _same_device(cache.buffer, q, blocks, seq_lens, workspace, out, status)
+    _check("tq_sdpa_blocks_decode", _fn(cache, "sdpa_blocks_decode")(
+        cache.ref(), _ptr(q), q.shape[1], _ptr(seq_lens), int(max_seq_len), float(attn_scale), _ptr(blocks),
+        blocks.shape[2], int(block_tokens), int(flags), _ptr(workspace), workspace.numel(), _ptr(out), _ptr(status),
+        _stream(stream)))
+    return out
+
+
+def tq_sparse_decode(cache, bounds: torch.Tensor, q: torch.Tensor, seq_lens: torch.Tensor, max_seq_len: int,
+                     attn_scale: float, workspace: torch.Tensor, blocks: torch.Tensor, out: Optional[torch.Tensor] = None,
+                     block_tokens: int = 64, n_first: int = 1, n_last: int = 1, status: Optional[torch.Tensor] = None,
+                     stream=None, flags: int = 0):
+    """tq_select_blocks into ``blocks`` [B, Hkv, n_select], then tq_sdpa_blocks_decode over it; (out, blocks)."""
+    out = _need_query(cache, q, out)
+    _need_bounds(cache, bounds, block_tokens)
+    _need_blocks(cache, blocks)
+    _need_lens(seq_lens, cache.batch, "seq_lens")
+    _need(workspace, torch.uint8, "workspace")
+    if status is not None:
+        _need(status, torch.int32, "status")
+    _same_device(cache.buffer, bounds, q, blocks, seq_lens, workspace, out, status)
+    _check("tq_sparse_decode", _fn(cache, "sparse_decode")(
+        cache.ref(), _ptr(bounds), _ptr(q), q.shape[1], _ptr(seq_lens), int(max_seq_len), float(attn_scale),
+        int(block_tokens), blocks.shape[2], int(n_first), int(n_last), int(flags), _ptr(workspace), workspace.numel(),
+        _ptr(blocks), _ptr(out), _ptr(status), _stream(stream)))
+    return out, blocks
+
+
+def weights_workspace(batch: int, num_q_heads: int, num_kv_heads: int, head_dim: int, max_seq_len: int,
+                      device="cuda") -> torch.Tensor:
+    """A workspace for tq_sdpa_decode_weights of these sizes."""
+    n = int(lib().tq_weights_workspace_bytes(batch, num_q_heads, num_kv_heads, head_dim, max_seq_len))
+    if n == 0:
+        raise ValueError("invalid sizes")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def _need_weights(cache, t: torch.Tensor, name: str) -> None:
+    _need(t, torch.float32, name)
+    if t.shape != (cache.batch, cache.num_kv_heads, cache.capacity):
+        raise ValueError(f"{name} must be [B, Hkv, capacity]; got {tuple(t.shape)}")
+
+
+def tq_sdpa_decode_weights(cache, q: torch.Tensor, seq_lens: torch.Tensor, max_seq_len: int, attn_scale: float,
+                           weights: torch.Tensor, workspace: torch.Tensor, out: Optional[torch.Tensor] = None,
+                           decay: float = 1.0, status: Optional[torch.Tensor] = None, stream=None,
+                           flags: int = 0) -> torch.Tensor:
+    """Fused decode attention that also sets weights[b, h, t] (fp32 [B, Hkv, capacity]) to decay times itself plus the
+    attention weight of row t summed over the kv head's query heads, for t < seq_lens[b]."""
+    out = _need_query(cache, q, out)
+    _need_weights(cache, weights, "weights")
+    _need_lens(seq_lens, cache.batch, "seq_lens")
+    _need(workspace, torch.uint8, "workspace")
+    if status is not None:
+        _need(status, torch.int32, "status")
+    _same_device(cache.buffer, q, seq_lens, weights, workspace, out, status)
+    _check("tq_sdpa_decode_weights", _fn(cache, "sdpa_decode_weights")(
+        cache.ref(), _ptr(q), q.shape[1], _ptr(seq_lens), int(max_seq_len), float(attn_scale), float(decay),
+        _ptr(weights), int(flags), _ptr(workspace), workspace.numel(), _ptr(out), _ptr(status), _stream(stream)))
+    return out
+
+
+def tq_kv_evict(src, dst, weights: torch.Tensor, seq_lens: torch.Tensor, max_seq_len: int, keep: int, recent: int,
+                dst_weights: torch.Tensor, dst_lens: torch.Tensor, kept: torch.Tensor,
+                status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Move the last ``recent`` rows and the keep - recent others of greatest weight of every (sequence, kv head) of
+    ``src`` to rows [0, keep) of ``dst`` (another cache of the same layout), with their weights; dst_lens int32 [B],
+    kept int32 [B, Hkv, keep]: the src row of each dst row, -1 behind the last."""
+    if getattr(src, "paged", False) != getattr(dst, "paged", False):
+        raise ValueError("src and dst must both be contiguous or both be paged")
+    _need_weights(src, weights, "weights")
+    _need_weights(dst, dst_weights, "dst_weights")
+    _need_lens(seq_lens, src.batch, "seq_lens")
+    _need_lens(dst_lens, src.batch, "dst_lens")
+    _need(kept, torch.int32, "kept")
+    if kept.shape != (src.batch, src.num_kv_heads, int(keep)):
+        raise ValueError(f"kept must be [B, Hkv, keep]; got {tuple(kept.shape)}")
+    if status is not None:
+        _need(status, torch.int32, "status")
+    _same_device(src.buffer, dst.buffer, weights, seq_lens, dst_weights, dst_lens, kept, status)
+    _check("tq_kv_evict", _fn(src, "kv_evict")(
+        src.ref(), dst.ref(), _ptr(weights), _ptr(seq_lens), int(max_seq_len), int(keep), int(recent), _ptr(dst_weights),
+        _ptr(dst_lens), _ptr(kept), _ptr(status), _stream(stream)))

@@ -10,23 +10,20 @@
 #include <mutex>
 
 #include "tq.h"
+#include "tq_host.h"
 #include "tq_internal.h"
 
-namespace {
+namespace tq {
 
+namespace {
 thread_local int32_t g_last_cuda_error = 0;
+}  // namespace
 
 tq_status cuda_status(cudaError_t e) {
     if (e == cudaSuccess) return TQ_OK;
     g_last_cuda_error = static_cast<int32_t>(e);
     return TQ_ERR_CUDA;
 }
-
-size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-bool supported_dim(int32_t d) { return d == 64 || d == 128 || d == 256; }
 
 bool valid_impl(tq_impl impl) { return impl == TQ_IMPL_AUTO || impl == TQ_IMPL_MMA || impl == TQ_IMPL_SIMT; }
 
@@ -45,23 +42,6 @@ tq_status check_cache(const tq_kv_cache* c) {
     if (rows128 >= (1LL << 31)) return TQ_ERR_SHAPE;
     return TQ_OK;
 }
-
-// The cache as the kernels see it: the arrays, the sizes, and where each
-// logical row lives (tq::RowMap).  A contiguous cache is one page per
-// sequence; `capacity` is the logical capacity (max_pages * page_tokens when
-// paged).  Field names follow tq_kv_cache so the code below reads the same
-// for both layouts.
-struct Store {
-    uint8_t* k_codes;
-    uint8_t* v_codes;
-    uint16_t* k_scale;
-    uint16_t* k_bias;
-    uint16_t* v_scale;
-    uint16_t* v_bias;
-    int32_t batch, num_kv_heads, head_dim, group_size, capacity, bits;
-    tq::RowMap map;
-    bool paged;
-};
 
 // Sizes and pointers only (no checks): for planning queries.
 Store shape_of(const tq_kv_cache* c) {
@@ -89,10 +69,6 @@ tq_status store_of(const tq_kv_cache* c, Store* st) {
     *st = shape_of(c);
     return TQ_OK;
 }
-
-// Pages hold whole pipeline tiles (128 tokens; 64 for head_dim 256), so a
-// tile never crosses a page.
-constexpr int kPageTokenMultiple = 128;
 
 tq_status store_of(const tq_paged_kv_cache* c, Store* st) {
     if (c == nullptr) return TQ_ERR_NULL;
@@ -189,17 +165,6 @@ tq_status make_rows_map(CUtensorMap* map, const void* base, unsigned long long r
 }
 
 // ------------------------------------------------------------ device facts --
-struct DeviceFacts {
-    int sms = 0;
-    int mma_ctas[2][3] = {{0, 0, 0}, {0, 0, 0}};  // per code width (4, 8) and head_dim 64 / 128 / 256
-    int wide_ctas = 0;  // the one-CTA-per-SM layout (contiguous int4, head_dim 128)
-    int simt_ctas[3] = {0, 0, 0};
-    // clusters of n CTAs of the cluster-merging kernel held at once, per code
-    // width, head_dim, layout (contiguous, paged) and n
-    int clusters[2][3][2][tq::kMaxClusterRuns + 1] = {};
-    int wide_clusters[tq::kMaxClusterRuns + 1] = {};
-};
-
 int dim_index(int d) { return d == 64 ? 0 : (d == 128 ? 1 : 2); }
 
 tq_status device_facts(DeviceFacts** out) {
@@ -242,17 +207,6 @@ tq_status device_facts(DeviceFacts** out) {
 }
 
 // ------------------------------------------------------------- decode plan --
-struct Plan {
-    int n_splits, unit_tokens, units;
-    bool merged = false;  // the decode merges the runs itself (one run, or one cluster per sequence and kv head)
-    int tile_tokens = 0;  // the kernel's pipeline tile
-    long long resident = 0;  // CTAs the device holds at once for this kernel
-    bool wide = false;    // one 12-warp CTA per SM (else several 4-warp CTAs)
-    long long waves = 1;  // ceil(CTAs / resident)
-};
-
-int ceil_div(long long a, long long b) { return static_cast<int>((a + b - 1) / b); }
-
 // Balanced runs of whole units (the kernel's pipeline tile, or the chunk if
 // that is smaller, so that runs cover the sequence evenly whatever its length
 // in chunks), as many per (sequence, kv head) as minimise a model of the
@@ -280,7 +234,7 @@ constexpr long long kReduceTiles = 1;
 // cluster_cap[n]: clusters of n CTAs the device holds at once (null: every
 // grid of one wave, the host rule).
 Plan make_plan(int batch, int hkv, int max_seq_len, int chunk, int tile_tokens, int resident, bool merge,
-               const int* cluster_cap = nullptr) {
+               const int* cluster_cap) {
     Plan pl;
     pl.unit_tokens = chunk < tile_tokens ? chunk : tile_tokens;
     pl.units = ceil_div(max_seq_len, pl.unit_tokens);
@@ -333,7 +287,7 @@ Plan chunk_plan(int max_seq_len, int chunk, int cps) {
 }
 
 tq_status device_plan(const Store* cache, int max_seq_len, int chunk, tq_impl impl, Plan* pl,
-                      bool merge = true) {
+                      bool merge) {
     DeviceFacts* f = nullptr;
     tq_status s = device_facts(&f);
     if (s != TQ_OK) return s;
@@ -388,12 +342,11 @@ tq_status check_decode_args(const Store* cache, const uint16_t* q, int32_t hq, c
     return TQ_OK;
 }
 
-tq_status run_phase1(const Store* cache, const uint16_t* q, int32_t hq, const int32_t* seq_lens,
-                     int32_t max_seq_len, float attn_scale, const Plan& pl, float* pm, float* plv, float* pa,
-                     int32_t* status, tq_impl impl, cudaStream_t stream, const int32_t* dep_write_pos = nullptr,
-                     int32_t dep_n_new = 0, const tq::AppendParams* fused_append = nullptr, bool rotate_q = false,
-                     int2* order_buf = nullptr, uint16_t* direct_out = nullptr) {
-    if (pl.n_splits > 65535 || cache->num_kv_heads > 65535 || cache->batch > 65535) return TQ_ERR_SHAPE;
+// The parameters every phase-1 launch shares: the cache, the query, the plan's
+// runs and where the partial states go.
+DecodeParams decode_params(const Store* cache, const uint16_t* q, int32_t hq, const int32_t* seq_lens,
+                           int32_t max_seq_len, float attn_scale, const Plan& pl, float* pm, float* plv, float* pa,
+                           int32_t* status) {
     tq::DecodeParams p{};
     p.q = q;
     p.seq_lens = seq_lens;
@@ -417,12 +370,22 @@ tq_status run_phase1(const Store* cache, const uint16_t* q, int32_t hq, const in
     p.units = pl.units;
     p.n_splits = pl.n_splits;
     p.score_scale_log2 = attn_scale * 1.4426950408889634f;
-    p.dep_write_pos = dep_write_pos;
-    p.dep_n_new = dep_n_new;
     p.map = cache->map;
     p.bits = cache->bits;
-    p.rotate_q = rotate_q ? 1 : 0;
     p.rot_scale = tq::rotation_scale(cache->head_dim);
+    return p;
+}
+
+tq_status run_phase1(const Store* cache, const uint16_t* q, int32_t hq, const int32_t* seq_lens,
+                     int32_t max_seq_len, float attn_scale, const Plan& pl, float* pm, float* plv, float* pa,
+                     int32_t* status, tq_impl impl, cudaStream_t stream, const int32_t* dep_write_pos = nullptr,
+                     int32_t dep_n_new = 0, const tq::AppendParams* fused_append = nullptr, bool rotate_q = false,
+                     int2* order_buf = nullptr, uint16_t* direct_out = nullptr) {
+    if (pl.n_splits > 65535 || cache->num_kv_heads > 65535 || cache->batch > 65535) return TQ_ERR_SHAPE;
+    tq::DecodeParams p = decode_params(cache, q, hq, seq_lens, max_seq_len, attn_scale, pl, pm, plv, pa, status);
+    p.dep_write_pos = dep_write_pos;
+    p.dep_n_new = dep_n_new;
+    p.rotate_q = rotate_q ? 1 : 0;
     p.app = {};
     if (fused_append != nullptr) {
         if (impl == TQ_IMPL_SIMT) return TQ_ERR_UNSUPPORTED;
@@ -471,10 +434,6 @@ tq_status run_phase1(const Store* cache, const uint16_t* q, int32_t hq, const in
     return cuda_status(tq::launch_decode_mma(p, cache->head_dim, tm_k, tm_v, stream, true));
 }
 
-}  // namespace
-
-namespace tq {
-
 // Phase 1 + phase 2 with the partial states placed in `partials`
 // (`partials_bytes` long, 256-byte aligned) instead of a caller workspace.
 // Requests whose partial states do not fit are refused with TQ_ERR_WORKSPACE
@@ -522,6 +481,8 @@ tq_status decode_into_partials(const tq_kv_cache* raw, const uint16_t* q, int32_
 tq_status record_cuda_status(cudaError_t e) { return cuda_status(e); }
 
 }  // namespace tq
+
+using namespace tq;
 
 extern "C" {
 

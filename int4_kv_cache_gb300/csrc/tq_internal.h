@@ -163,6 +163,12 @@ struct DecodeParams {
     uint16_t* out;
     // The plan's SM layout: one 12-warp CTA per SM (mma_wide_supported only).
     int32_t wide;
+    // Listed blocks (launch_decode_blocks): n_list block indices for every
+    // (sequence, kv head), blocks of block_tokens = 1 << block_shift tokens.
+    const int32_t* blocks;    // [B][Hkv][n_list]
+    int32_t n_list, block_tokens, block_shift;
+    // Scores kept (launch_decode_scores): [B][Hkv][max_seq_len][group_q], log2 units
+    float* scores;
 };
 constexpr int32_t kWaitForAppend = 0, kWaitAtStart = 1;
 // Most rows per sequence the decode kernel appends itself; longer appends
@@ -205,8 +211,102 @@ struct ReduceParams {
     int32_t adv_n;
 };
 
+// Rotary positions (rope.cu): rows in the projections' layout (strides in
+// elements), out [B][heads][n][D].
+constexpr int kRopeAxes = 4;
+struct RopeRows {
+    const uint16_t* x;
+    uint16_t* out;
+    long long stride_b, stride_t, stride_h;
+    int32_t heads;
+};
+struct RopeParams {
+    RopeRows q, k;             // k.heads = 0: no keys
+    const int32_t* positions;  // [axes][B][n]
+    const float* inv_freq;     // [rotary_dim / 2]
+    int32_t batch, n, head_dim, rotary_dim;
+    int32_t section_end[kRopeAxes];  // first pair behind each axis (the last ones: rotary_dim / 2)
+    int32_t pairs, inverse, tokens_per_cta;
+};
+
+// Key bounds of the blocks that rows [start[b], start[b] + n_rows) touch (bounds.cu).
+struct BoundsParams {
+    const uint8_t* k_codes;
+    const uint16_t* k_scale;
+    const uint16_t* k_bias;
+    uint16_t* bounds;          // [B][Hkv][blocks_per_seq][2][D]
+    const int32_t* start;      // [B]
+    int32_t* status;
+    int32_t batch, num_kv_heads, head_dim, capacity, bits;
+    int32_t n_rows, block_shift, blocks_per_seq;
+    int32_t touched;           // blocks per sequence at most
+    RowMap map;
+};
+
+// Block selection (select.cu).
+constexpr int kMaxSelectBlocks = 49152;  // blocks of a sequence (192 KB of scores)
+struct SelectParams {
+    const uint16_t* bounds;    // [B][Hkv][blocks_per_seq][2][D]
+    const uint16_t* q;         // [B][Hq][D]
+    const int32_t* seq_lens;   // [B]
+    int32_t* blocks;           // [B][Hkv][n_select]
+    double* exact;             // [B][Hkv][exact_stride] scratch
+    int32_t* status;
+    int32_t batch, num_kv_heads, group_q, head_dim, max_seq_len;
+    int32_t block_shift, blocks_per_seq, exact_stride, n_select, n_first, n_last;
+    int32_t ctas;              // CTAs per (sequence, kv head): one cluster, at most 8
+};
+
+// Eviction (evict.cu).
+constexpr int kMaxEvictHeldBytes = 160 * 1024;
+struct EvictParams {
+    const float* weights;      // [B][Hkv][weight_stride]
+    const int32_t* seq_lens;   // [B]
+    float* out_weights;        // [B][Hkv][out_weight_stride]
+    int32_t* out_lens;         // [B]
+    int32_t* kept;             // [B][Hkv][keep]
+    int32_t* status;
+    int32_t batch, num_kv_heads, max_seq_len, weight_stride, out_weight_stride;
+    int32_t keep, recent;
+    int32_t ctas;              // CTAs per (sequence, kv head): one cluster, at most 8
+    int32_t held;              // weights a CTA may hold in shared memory
+};
+struct EvictCopyParams {
+    const uint8_t* src_k;
+    const uint8_t* src_v;
+    uint8_t* dst_k;
+    uint8_t* dst_v;
+    const uint16_t* src_sb[4]; // k_scale, k_bias, v_scale, v_bias
+    uint16_t* dst_sb[4];
+    const int32_t* kept;       // [B][Hkv][keep]
+    const int32_t* lens;       // [B] kept rows
+    int32_t* status;
+    int32_t num_kv_heads, batch, head_dim, bits, keep;
+    RowMap src_map, dst_map;
+};
+
+// Phase 2 of the weight-accumulating decode (weights.cu).
+struct WeightsParams {
+    const float* part_m;       // [B][Hq][n_parts], log2 units
+    const float* part_l;
+    const float* part_acc;     // [B][Hq][n_parts][D]
+    const float* scores;       // [B][Hkv][max_seq_len][group_q], log2 units
+    const int32_t* seq_lens;
+    float* weights;            // [B][Hkv][weight_stride]
+    uint16_t* out;             // [B][Hq][D]
+    int32_t batch, num_q_heads, num_kv_heads, group_q, max_seq_len, weight_stride, n_parts, chunks;
+    float decay;
+    int32_t rotate_out;
+    float rot_scale;
+};
 
 // Launchers (return the cudaError_t of the launch).
+cudaError_t launch_rope(const RopeParams& p, cudaStream_t stream);
+cudaError_t launch_bounds(const BoundsParams& p, cudaStream_t stream);
+cudaError_t launch_select(const SelectParams& p, cudaStream_t stream);
+cudaError_t launch_evict_select(const EvictParams& p, int held_bytes, cudaStream_t stream);
+cudaError_t launch_evict_copy(const EvictCopyParams& p, cudaStream_t stream);
+cudaError_t launch_weights(const WeightsParams& p, int head_dim, cudaStream_t stream);
 cudaError_t launch_quantize_append(const AppendParams& p, cudaStream_t stream);
 // The same for large appends: a persistent grid (a few CTAs per SM of `sms`)
 // streaming the fp16 rows through TMA.  tm_k / tm_v: k_new / v_new as
@@ -219,6 +319,13 @@ cudaError_t launch_quantize_append_tma(const AppendParams& p, const CUtensorMap&
 cudaError_t launch_decode_simt(const DecodeParams& p, int head_dim, cudaStream_t stream);
 cudaError_t launch_decode_mma(const DecodeParams& p, int head_dim, const CUtensorMap& tm_k,
                               const CUtensorMap& tm_v, cudaStream_t stream, bool pdl_secondary);
+// The same over the blocks p.blocks lists (one of the dense kernel's four-warp
+// layouts; tensor maps with boxes of min(tile, block) tokens), and with the
+// scores kept in p.scores (partial states only, part_m in log2 units).
+cudaError_t launch_decode_blocks(const DecodeParams& p, int head_dim, const CUtensorMap& tm_k,
+                                 const CUtensorMap& tm_v, cudaStream_t stream);
+cudaError_t launch_decode_scores(const DecodeParams& p, int head_dim, const CUtensorMap& tm_k,
+                                 const CUtensorMap& tm_v, cudaStream_t stream);
 // The append kernel, optionally letting the next launch start early (the
 // decode kernel then waits only where it reads the appended rows).
 cudaError_t launch_quantize_append_primary(const AppendParams& p, cudaStream_t stream);

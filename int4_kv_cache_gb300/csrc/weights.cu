@@ -1,0 +1,169 @@
+// weights.cu -- phase 2 of the decode that accumulates attention weights: the
+// log-sum-exp merge of the runs' partial states into the output, and for every
+// cached token of a kv head
+//     w_t = decay * w_t + sum over the group's heads of e^{s_t - M} / L,
+// from the scores s_t that phase 1 kept (log2 units) and the merged maximum M
+// and sum L of each head.
+//
+// One launch: the first CTAs of the grid merge outputs (a CTA per query head,
+// a warp per stretch of its parts), the others take kWeightTokens tokens of a
+// kv head each; every one of them merges the heads' m and l itself (a few
+// hundred numbers from L2) rather than wait for another kernel.  Bound by the
+// scores: 4 bytes a head and token, written by phase 1 and read here from L2
+// while they fit there.
+#include <math.h>
+
+#include "tq_device.cuh"
+#include "tq_hadamard.cuh"
+#include "tq_internal.h"
+
+namespace tq {
+
+namespace {
+
+constexpr int kWeightThreads = 256;
+constexpr int kWeightWarps = kWeightThreads / 32;
+constexpr int kWeightTokens = 4 * kWeightThreads;
+
+// The merged maximum (log2 units) and sum of one head's parts, by a warp.
+__device__ __forceinline__ void merge_parts(const float* m, const float* l, int n, float& M, float& L) {
+    const int lane = threadIdx.x & 31;
+    M = -INFINITY;
+    for (int c = lane; c < n; c += 32)
+        if (__ldcg(l + c) > 0.0f) M = fmaxf(M, __ldcg(m + c));
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+    L = 0.0f;
+    for (int c = lane; c < n; c += 32) {
+        const float lc = __ldcg(l + c);
+        if (lc > 0.0f) L = fmaf(exp2f(__ldcg(m + c) - M), lc, L);
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
+}
+
+template <int D>
+__device__ __forceinline__ void merge_output(const WeightsParams& p, long long bh) {
+    constexpr int V = D / 32;
+    __shared__ float acc_s[kWeightWarps][D];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int n = p.n_parts;
+    const float* m = p.part_m + bh * n;
+    float M, L;
+    merge_parts(m, p.part_l + bh * n, n, M, L);
+    float a[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) a[i] = 0.0f;
+#pragma unroll 4
+    for (int c = warp; c < n; c += kWeightWarps) {
+        const float w = __ldcg(p.part_l + bh * n + c) > 0.0f ? exp2f(__ldcg(m + c) - M) : 0.0f;
+        const float* src = p.part_acc + (bh * n + c) * D + lane * V;
+        float x[V];
+        if constexpr (V == 2) {
+            const float2 v = __ldcg(reinterpret_cast<const float2*>(src));
+            x[0] = v.x;
+            x[1] = v.y;
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; i += 4) {
+                const float4 v = __ldcg(reinterpret_cast<const float4*>(src + i));
+                x[i] = v.x;
+                x[i + 1] = v.y;
+                x[i + 2] = v.z;
+                x[i + 3] = v.w;
+            }
+        }
+        if (w != 0.0f) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) a[i] = fmaf(w, x[i], a[i]);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) acc_s[warp][lane * V + i] = a[i];
+    __syncthreads();
+    if (warp != 0) return;
+    float o[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        float t = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kWeightWarps; ++w) t += acc_s[w][lane * V + i];
+        o[i] = L > 0.0f ? __fdiv_rn(t, L) : 0.0f;
+    }
+    if (p.rotate_out) hadamard_warp<V>(o, lane, p.rot_scale);
+#pragma unroll
+    for (int i = 0; i < V; ++i) p.out[bh * D + lane * V + i] = __half_as_ushort(__float2half_rn(o[i]));
+}
+
+template <int D>
+__global__ void __launch_bounds__(kWeightThreads) weights_kernel(const WeightsParams p) {
+    __shared__ float head_m[8], head_r[8];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    pdl_wait_primary();
+    pdl_launch_dependents();
+    const int heads = p.batch * p.num_q_heads;
+    if (static_cast<int>(blockIdx.x) < heads) {
+        merge_output<D>(p, blockIdx.x);
+        return;
+    }
+    const int G = p.group_q;
+    const int item = static_cast<int>(blockIdx.x) - heads;
+    const int bh = item / p.chunks, b = bh / p.num_kv_heads;  // (sequence, kv head)
+    const int t0 = (item - bh * p.chunks) * kWeightTokens;
+    const int len = min(max(__ldcg(p.seq_lens + b), 0), p.max_seq_len);
+    if (t0 >= len) return;
+    if (warp < G) {
+        const long long ph = static_cast<long long>(bh) * G + warp;
+        float M, L;
+        merge_parts(p.part_m + ph * p.n_parts, p.part_l + ph * p.n_parts, p.n_parts, M, L);
+        if (lane == 0) {
+            head_m[warp] = M;
+            head_r[warp] = L > 0.0f ? __fdiv_rn(1.0f, L) : 0.0f;
+        }
+    }
+    __syncthreads();
+    const float* scores = p.scores + static_cast<long long>(bh) * p.max_seq_len * G;
+    float* weights = p.weights + static_cast<long long>(bh) * p.weight_stride;
+#pragma unroll
+    for (int j = 0; j < kWeightTokens / kWeightThreads; ++j) {
+        const int t = t0 + j * kWeightThreads + threadIdx.x;
+        if (t >= len) break;
+        const float* s = scores + static_cast<long long>(t) * G;
+        float sum = 0.0f;
+        if (G == 8) {
+            const float4 a = __ldcg(reinterpret_cast<const float4*>(s)), c = __ldcg(reinterpret_cast<const float4*>(s) + 1);
+            const float x[8] = {a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w};
+#pragma unroll
+            for (int g = 0; g < 8; ++g) sum = fmaf(ex2_approx(x[g] - head_m[g]), head_r[g], sum);
+        } else {
+            for (int g = 0; g < G; ++g) sum = fmaf(ex2_approx(__ldcg(s + g) - head_m[g]), head_r[g], sum);
+        }
+        weights[t] = p.decay != 0.0f ? fmaf(p.decay, weights[t], sum) : sum;
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_weights(const WeightsParams& p, int head_dim, cudaStream_t stream) {
+    WeightsParams q = p;
+    q.chunks = (p.max_seq_len + kWeightTokens - 1) / kWeightTokens;
+    const long long ctas = static_cast<long long>(p.batch) * (p.num_q_heads + static_cast<long long>(p.num_kv_heads) * q.chunks);
+    if (ctas > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+    cfg.blockDim = dim3(kWeightThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    switch (head_dim) {
+        case 64: return cudaLaunchKernelEx(&cfg, weights_kernel<64>, q);
+        case 128: return cudaLaunchKernelEx(&cfg, weights_kernel<128>, q);
+        case 256: return cudaLaunchKernelEx(&cfg, weights_kernel<256>, q);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+}  // namespace tq
