@@ -618,7 +618,7 @@ tq_status tq_paged_sdpa_decode_weights(const tq_paged_kv_cache* cache, const uin
  * of greatest weight (equal weights, and -0 and 0, the lowest row first) move,
  * in their order, to rows [0, keep) of dst; one with at most `keep` rows moves
  * whole.  Codes, scales and biases are copied as they are.
- *   weights      fp32 [batch][num_kv_heads][src capacity]
+ *   weights      fp32 [batch][num_kv_heads][src capacity], 16-byte aligned
  *   dst_weights  fp32 [batch][num_kv_heads][dst capacity]: the kept rows'
  *                weights, zeros behind them
  *   dst_lens     int32 [batch]: min(seq_lens[b], keep)

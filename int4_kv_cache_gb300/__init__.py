@@ -569,21 +569,43 @@ def tq_decode_step_host(cache: KVCache, h_k_new: torch.Tensor, h_v_new: torch.Te
 
 # ------------------------------------------------- rotary positions, sparse decode, eviction
 def _same_device(first: torch.Tensor, *others) -> None:
-    dev = first.device
+    """All tensors on one device, the current one (the kernels and the stream are the current device's)."""
+    dev = first.get_device()
     for t in others:
-        if t is not None and t.device != dev:
-            raise ValueError(f"tensors on different devices: {dev} and {t.device}")
-    if dev.index != torch.cuda.current_device():
-        raise ValueError(f"tensors on {dev}, but the current device is cuda:{torch.cuda.current_device()}")
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"tensors on different devices: {first.device} and {t.device}")
+    if dev != _current_device():
+        raise ValueError(f"tensors on {first.device}, but the current device is cuda:{_current_device()}")
 
 
-def _rope_rows(x: torch.Tensor, out: torch.Tensor, name: str) -> tq_rope_rows:
-    if not x.is_cuda or x.dtype != torch.float16 or x.dim() != 4 or x.stride(3) != 1:
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _stream_of(t: torch.Tensor, stream):
+    """The given stream's handle, else that of the current stream of t's device (checked to be the current one)."""
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None:
+        return _raw_stream(t.get_device())
+    return torch.cuda.current_stream().cuda_stream
+
+
+def _rope_rows(x: torch.Tensor, out: Optional[torch.Tensor], b: int, n: int, d: int, stream, name: str):
+    """(the rows as the library takes them, their output [B, heads, n, D])."""
+    if not x.is_cuda or x.dtype != torch.float16 or x.stride(3) != 1:
         raise ValueError(f"{name}: expected a CUDA float16 tensor [B, n, heads, D] with a contiguous last dimension")
+    h = x.shape[2]
+    if out is None:
+        out = x.new_empty((b, h, n, d))
+        if stream is not None:
+            out.record_stream(stream)
+    else:
+        _need(out, torch.float16, name + "_out")
+        if out.shape != (b, h, n, d):
+            raise ValueError(f"{name}_out must be [B, heads, n, D] = {(b, h, n, d)}; got {tuple(out.shape)}")
     sb, st, sh, _ = x.stride()
-    b, n, h, _ = x.shape
     # a dimension of one is never stepped along, whatever its stride says
-    return tq_rope_rows(x.data_ptr(), out.data_ptr(), sb if b > 1 else 0, st if n > 1 else 0, sh if h > 1 else 0, h)
+    return tq_rope_rows(x.data_ptr(), out.data_ptr(), sb if b > 1 else 0, st if n > 1 else 0, sh if h > 1 else 0, h), out
 
 
 def tq_rope_axes(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tensor, inv_freq: torch.Tensor, sections,
@@ -598,27 +620,18 @@ def tq_rope_axes(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Te
     _need(inv_freq, torch.float32, "inv_freq")
     if q.dim() != 4 or (k is not None and (k.dim() != 4 or k.shape[:2] != q.shape[:2] or k.shape[3] != q.shape[3])):
         raise ValueError("q and k must be [B, n, heads, D] with the same B, n and D")
-    b, n, hq, d = q.shape
-    if tuple(positions.shape) != (len(sections), b, n):
+    b, n, _, d = q.shape
+    if positions.shape != (len(sections), b, n):
         raise ValueError(f"positions must be [axes, B, n] = {(len(sections), b, n)}; got {tuple(positions.shape)}")
-    if q_out is None:
-        q_out = torch.empty((b, hq, n, d), dtype=torch.float16, device=q.device)
-    if k is not None and k_out is None:
-        k_out = torch.empty((b, k.shape[2], n, d), dtype=torch.float16, device=q.device)
-    for x, o, name in ((q, q_out, "q_out"), (k, k_out, "k_out")):
-        if x is None:
-            continue
-        _need(o, torch.float16, name)
-        if tuple(o.shape) != (b, x.shape[2], n, d):
-            raise ValueError(f"{name} must be [B, heads, n, D] = {(b, x.shape[2], n, d)}; got {tuple(o.shape)}")
-    _same_device(q, k, positions, inv_freq, q_out, k_out if k is not None else None)
-    if n == 0:
-        return (q_out, k_out) if k is not None else q_out
-    rq = _rope_rows(q, q_out, "q")
-    rk = None if k is None else ctypes.byref(_rope_rows(k, k_out, "k"))
-    sec = (ctypes.c_int32 * len(sections))(*sections)
-    _check("tq_rope_axes", lib().tq_rope_axes(ctypes.byref(rq), rk, _ptr(positions), _ptr(inv_freq), len(sections), sec, b, n,
-                                              d, 2 * inv_freq.numel(), int(flags), _stream(stream)))
+    rq, q_out = _rope_rows(q, q_out, b, n, d, stream, "q")
+    rk = None
+    if k is not None:
+        rk, k_out = _rope_rows(k, k_out, b, n, d, stream, "k")
+    _same_device(q, k, positions, inv_freq, q_out, k_out)
+    if n > 0:
+        _check("tq_rope_axes", lib().tq_rope_axes(rq, rk, positions.data_ptr(), inv_freq.data_ptr(), len(sections),
+                                                  (ctypes.c_int32 * len(sections))(*sections), b, n, d, 2 * inv_freq.numel(),
+                                                  int(flags), _stream_of(q, stream)))
     return (q_out, k_out) if k is not None else q_out
 
 
@@ -658,8 +671,8 @@ def tq_kv_block_bounds(cache, bounds: torch.Tensor, start: torch.Tensor, n_rows:
     if status is not None:
         _need(status, torch.int32, "status")
     _same_device(cache.buffer, bounds, start, status)
-    _check("tq_kv_block_bounds", _fn(cache, "kv_block_bounds")(cache.ref(), int(block_tokens), _ptr(start), int(n_rows),
-                                                              _ptr(bounds), _ptr(status), _stream(stream)))
+    _check("tq_kv_block_bounds", _fn(cache, "kv_block_bounds")(cache.ref(), int(block_tokens), start.data_ptr(), int(n_rows),
+                                                              bounds.data_ptr(), status.data_ptr() if status is not None else None, _stream_of(bounds, stream)))
     return bounds
 
 
@@ -678,10 +691,12 @@ def _need_blocks(cache, blocks: torch.Tensor) -> None:
         raise ValueError(f"blocks must be [B, Hkv, n_select]; got {tuple(blocks.shape)}")
 
 
-def _need_query(cache, q: torch.Tensor, out: Optional[torch.Tensor]) -> torch.Tensor:
+def _need_query(cache, q: torch.Tensor, out: Optional[torch.Tensor], stream) -> torch.Tensor:
     _need(q, torch.float16, "q")
     if out is None:
         out = torch.empty_like(q)
+        if stream is not None:
+            out.record_stream(stream)
     _need(out, torch.float16, "out")
     if q.dim() != 3 or q.shape[0] != cache.batch or q.shape[2] != cache.head_dim or out.shape != q.shape:
         raise ValueError(f"q must be [B, Hq, D]; got {tuple(q.shape)}")
@@ -707,9 +722,9 @@ def tq_select_blocks(bounds: torch.Tensor, q: torch.Tensor, seq_lens: torch.Tens
     _need_lens(seq_lens, b, "seq_lens")
     _same_device(q, bounds, seq_lens, workspace, blocks, status)
     _check("tq_select_blocks", lib().tq_select_blocks(
-        _ptr(bounds), _ptr(q), b, q.shape[1], hkv, q.shape[2], int(capacity), _ptr(seq_lens), int(max_seq_len),
-        int(block_tokens), n_select, int(n_first), int(n_last), int(flags), _ptr(workspace), workspace.numel(),
-        _ptr(blocks), _ptr(status), _stream(stream)))
+        bounds.data_ptr(), q.data_ptr(), b, q.shape[1], hkv, q.shape[2], int(capacity), seq_lens.data_ptr(), int(max_seq_len),
+        int(block_tokens), n_select, int(n_first), int(n_last), int(flags), workspace.data_ptr(), workspace.numel(),
+        blocks.data_ptr(), status.data_ptr() if status is not None else None, _stream_of(q, stream)))
     return blocks
 
 
@@ -718,7 +733,7 @@ def tq_sdpa_blocks_decode(cache, q: torch.Tensor, blocks: torch.Tensor, seq_lens
                           block_tokens: int = 64, status: Optional[torch.Tensor] = None, stream=None,
                           flags: int = 0) -> torch.Tensor:
     """Decode attention over the rows below seq_lens of the listed blocks [B, Hkv, n_select] (entries below 0: none)."""
-    out = _need_query(cache, q, out)
+    out = _need_query(cache, q, out, stream)
     _need_blocks(cache, blocks)
     _need_lens(seq_lens, cache.batch, "seq_lens")
     _need(workspace, torch.uint8, "workspace")
@@ -726,9 +741,9 @@ def tq_sdpa_blocks_decode(cache, q: torch.Tensor, blocks: torch.Tensor, seq_lens
         _need(status, torch.int32, "status")
     _same_device(cache.buffer, q, blocks, seq_lens, workspace, out, status)
     _check("tq_sdpa_blocks_decode", _fn(cache, "sdpa_blocks_decode")(
-        cache.ref(), _ptr(q), q.shape[1], _ptr(seq_lens), int(max_seq_len), float(attn_scale), _ptr(blocks),
-        blocks.shape[2], int(block_tokens), int(flags), _ptr(workspace), workspace.numel(), _ptr(out), _ptr(status),
-        _stream(stream)))
+        cache.ref(), q.data_ptr(), q.shape[1], seq_lens.data_ptr(), int(max_seq_len), float(attn_scale), blocks.data_ptr(),
+        blocks.shape[2], int(block_tokens), int(flags), workspace.data_ptr(), workspace.numel(), out.data_ptr(), status.data_ptr() if status is not None else None,
+        _stream_of(q, stream)))
     return out
 
 
@@ -737,7 +752,7 @@ def tq_sparse_decode(cache, bounds: torch.Tensor, q: torch.Tensor, seq_lens: tor
                      block_tokens: int = 64, n_first: int = 1, n_last: int = 1, status: Optional[torch.Tensor] = None,
                      stream=None, flags: int = 0):
     """tq_select_blocks into ``blocks`` [B, Hkv, n_select], then tq_sdpa_blocks_decode over it; (out, blocks)."""
-    out = _need_query(cache, q, out)
+    out = _need_query(cache, q, out, stream)
     _need_bounds(cache, bounds, block_tokens)
     _need_blocks(cache, blocks)
     _need_lens(seq_lens, cache.batch, "seq_lens")
@@ -746,9 +761,9 @@ def tq_sparse_decode(cache, bounds: torch.Tensor, q: torch.Tensor, seq_lens: tor
         _need(status, torch.int32, "status")
     _same_device(cache.buffer, bounds, q, blocks, seq_lens, workspace, out, status)
     _check("tq_sparse_decode", _fn(cache, "sparse_decode")(
-        cache.ref(), _ptr(bounds), _ptr(q), q.shape[1], _ptr(seq_lens), int(max_seq_len), float(attn_scale),
-        int(block_tokens), blocks.shape[2], int(n_first), int(n_last), int(flags), _ptr(workspace), workspace.numel(),
-        _ptr(blocks), _ptr(out), _ptr(status), _stream(stream)))
+        cache.ref(), bounds.data_ptr(), q.data_ptr(), q.shape[1], seq_lens.data_ptr(), int(max_seq_len), float(attn_scale),
+        int(block_tokens), blocks.shape[2], int(n_first), int(n_last), int(flags), workspace.data_ptr(), workspace.numel(),
+        blocks.data_ptr(), out.data_ptr(), status.data_ptr() if status is not None else None, _stream_of(q, stream)))
     return out, blocks
 
 
@@ -773,7 +788,7 @@ def tq_sdpa_decode_weights(cache, q: torch.Tensor, seq_lens: torch.Tensor, max_s
                            flags: int = 0) -> torch.Tensor:
     """Fused decode attention that also sets weights[b, h, t] (fp32 [B, Hkv, capacity]) to decay times itself plus the
     attention weight of row t summed over the kv head's query heads, for t < seq_lens[b]."""
-    out = _need_query(cache, q, out)
+    out = _need_query(cache, q, out, stream)
     _need_weights(cache, weights, "weights")
     _need_lens(seq_lens, cache.batch, "seq_lens")
     _need(workspace, torch.uint8, "workspace")
@@ -781,8 +796,8 @@ def tq_sdpa_decode_weights(cache, q: torch.Tensor, seq_lens: torch.Tensor, max_s
         _need(status, torch.int32, "status")
     _same_device(cache.buffer, q, seq_lens, weights, workspace, out, status)
     _check("tq_sdpa_decode_weights", _fn(cache, "sdpa_decode_weights")(
-        cache.ref(), _ptr(q), q.shape[1], _ptr(seq_lens), int(max_seq_len), float(attn_scale), float(decay),
-        _ptr(weights), int(flags), _ptr(workspace), workspace.numel(), _ptr(out), _ptr(status), _stream(stream)))
+        cache.ref(), q.data_ptr(), q.shape[1], seq_lens.data_ptr(), int(max_seq_len), float(attn_scale), float(decay),
+        weights.data_ptr(), int(flags), workspace.data_ptr(), workspace.numel(), out.data_ptr(), status.data_ptr() if status is not None else None, _stream_of(q, stream)))
     return out
 
 
@@ -805,5 +820,5 @@ def tq_kv_evict(src, dst, weights: torch.Tensor, seq_lens: torch.Tensor, max_seq
         _need(status, torch.int32, "status")
     _same_device(src.buffer, dst.buffer, weights, seq_lens, dst_weights, dst_lens, kept, status)
     _check("tq_kv_evict", _fn(src, "kv_evict")(
-        src.ref(), dst.ref(), _ptr(weights), _ptr(seq_lens), int(max_seq_len), int(keep), int(recent), _ptr(dst_weights),
-        _ptr(dst_lens), _ptr(kept), _ptr(status), _stream(stream)))
+        src.ref(), dst.ref(), weights.data_ptr(), seq_lens.data_ptr(), int(max_seq_len), int(keep), int(recent), dst_weights.data_ptr(),
+        dst_lens.data_ptr(), kept.data_ptr(), status.data_ptr() if status is not None else None, _stream_of(weights, stream)))

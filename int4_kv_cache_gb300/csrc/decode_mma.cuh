@@ -232,9 +232,11 @@ __global__ void __launch_bounds__(Cfg<D, BITS, WIDE>::THREADS, Cfg<D, BITS, WIDE
     __shared__ unsigned int done_cnt[C::STAGES];  // warps finished with the stage, cumulative
     __shared__ float mrg_m[C::NWC][8], mrg_l[C::NWC][8], mrg_t[C::NWC][8];
     // paged: the block-table entries of this run's pages, loaded once
-    // listed blocks: this run's list entries, -1 for none
-    constexpr int kPageWindow = PAGED || BLK ? 256 : 1;
+    // listed blocks: this run's list entries (-1 for none) and the cache rows
+    // where they begin, in units of 16
+    constexpr int kPageWindow = BLK ? 128 : (PAGED ? 256 : 1);
     __shared__ int32_t page_s[kPageWindow];
+    __shared__ int32_t blk_row[BLK ? kPageWindow : 1];
     __shared__ int blk_used;  // listed blocks: entries of the window up to the last block that holds rows
     // kOutCluster: this CTA's merged state, read by the cluster (acc after the
     // warps' merge buffer in the dynamic shared memory)
@@ -261,24 +263,32 @@ __global__ void __launch_bounds__(Cfg<D, BITS, WIDE>::THREADS, Cfg<D, BITS, WIDE
         split = item % gridDim.x;
     }
     const int G = p.group_q;
-    const int len = clamp_len(p, len_src);
-    const int t_begin = run_begin(split, p.units, p.n_splits, p.unit_tokens);
     // listed blocks: positions count along the list, n_list of them for every run
     const int n_list = BLK ? p.n_list * p.block_tokens : 0;
+    const int32_t* list = BLK ? p.blocks + (static_cast<long long>(b) * p.num_kv_heads + kvh) * p.n_list : nullptr;
+    int raw_entry = -1;  // this thread's entry of the window, asked for together with the length
+    if constexpr (BLK) {
+        const int e = (run_begin(split, p.units, p.n_splits, p.unit_tokens) >> p.block_shift) + threadIdx.x;
+        if (e < p.n_list) raw_entry = __ldcg(list + e);
+    }
+    const int len = clamp_len(p, len_src);
+    const int t_begin = run_begin(split, p.units, p.n_splits, p.unit_tokens);
     const int t_end = min(run_begin(split + 1, p.units, p.n_splits, p.unit_tokens), BLK ? n_list : len);
     int n_tiles = t_end > t_begin ? (t_end - t_begin + C::T - 1) / C::T : 0;
     const long long row_base = (static_cast<long long>(b) * p.num_kv_heads + kvh) * p.capacity;  // contiguous
 
     int first_page = 0, n_win = 0;
-    // the list's entry at index e: a block with rows below len, or -1
-    auto listed_block = [&](int e) -> int {
-        const int blk = __ldcg(p.blocks + (static_cast<long long>(b) * p.num_kv_heads + kvh) * p.n_list + e);
+    // a list entry as a block with rows below len, or -1
+    auto listed_block = [&](int blk) -> int {
         if (blk < 0) return -1;
         if (blk > (len - 1) >> p.block_shift || len == 0) {
             if (p.status != nullptr) atomicOr(p.status, TQ_DEV_BLOCK);
             return -1;
         }
         return blk;
+    };
+    auto block_row = [&](int blk) -> long long {
+        return kv_row(p.map, p.num_kv_heads, b, kvh, blk << p.block_shift, p.status);
     };
     if constexpr (BLK) {
         first_page = t_begin >> p.block_shift;
@@ -287,10 +297,14 @@ __global__ void __launch_bounds__(Cfg<D, BITS, WIDE>::THREADS, Cfg<D, BITS, WIDE
         n_win = min(n_win, kPageWindow);
         if (threadIdx.x == 0) blk_used = 0;
         __syncthreads();
-        for (int i = threadIdx.x; i < n_win; i += C::THREADS) {
-            const int blk = listed_block(first_page + i);
+        static_assert(!BLK || kPageWindow <= C::THREADS, "a thread per entry of the window");
+        if (const int i = threadIdx.x; i < n_win) {
+            const int blk = listed_block(raw_entry);
             page_s[i] = blk;
-            if (blk >= 0) atomicMax(&blk_used, i + 1);
+            if (blk >= 0) {
+                blk_row[i] = static_cast<int32_t>(block_row(blk) >> 4);
+                atomicMax(&blk_used, i + 1);
+            }
         }
         __syncthreads();
         // tiles behind the last block that holds rows are not run at all
@@ -357,64 +371,52 @@ __global__ void __launch_bounds__(Cfg<D, BITS, WIDE>::THREADS, Cfg<D, BITS, WIDE
     // rows lie below len (0: no block there).
     const int seg_rows = BLK ? min(C::T, p.block_tokens) : C::T;
     const int n_seg = BLK ? C::T / seg_rows : 1;
-    auto segment = [&](int t0, int j, int& tok) -> int {
+    auto segment = [&](int t0, int j, int& tok, long long* row = nullptr) -> int {
         const int v = t0 + j * seg_rows;
         if (v >= t_end) return 0;
         const int e = v >> p.block_shift, w = e - first_page;
-        const int blk = w < n_win ? page_s[w] : listed_block(e);
+        const int blk = w < n_win ? page_s[w] : listed_block(__ldcg(list + e));
         if (blk < 0) return 0;
-        tok = (blk << p.block_shift) + (v & (p.block_tokens - 1));
+        const int off = v & (p.block_tokens - 1);
+        tok = (blk << p.block_shift) + off;
+        if (row != nullptr) *row = (w < n_win ? static_cast<long long>(blk_row[w]) << 4 : block_row(blk)) + off;
         return max(0, min(len - tok, seg_rows));
     };
+    // Fill stage it % STAGES, by a whole warp: lane kCopies j + c issues copy c
+    // of segment j (code tiles of K, then V, then the four scale and bias
+    // rows), so that the addresses are formed side by side (one lane after the
+    // other, a tile of two segments kept its warp for about 1.5 us).
+    constexpr int kCopies = 2 * C::HALVES + 4;
     auto issue_blocks = [&](int it, uint64_t policy) {
         const int stage = it % C::STAGES;
-        const int t0 = t_begin + it * C::T;
         uint8_t* st = smem + stage * C::STAGE_BYTES;
-        uint8_t* sb = st + 2 * C::CODE_BYTES;
-        const uint32_t code_bytes = static_cast<uint32_t>(seg_rows) * C::BPT;
-        uint32_t bytes = 0;
-        for (int pass = 0; pass < 2; ++pass) {  // the stage's bytes, then its copies
-            if (pass == 1) mbar_arrive_expect_tx(&full_bar[stage], bytes);
-            for (int j = 0; j < n_seg; ++j) {
-                int tok = 0;
-                if (segment(t0, j, tok) == 0) continue;
-                const uint32_t sb_bytes = static_cast<uint32_t>(PAGED ? seg_rows : min(seg_rows, p.capacity - tok)) * NG * 2;
-                if (pass == 0) {
-                    bytes += 2 * code_bytes + 4 * sb_bytes;
-                    continue;
-                }
-                const long long row =
-                    PAGED ? kv_row(p.map, p.num_kv_heads, b, kvh, tok, p.status) : row_base + tok;
-                uint8_t* kd = st + j * seg_rows * C::ROWB;
-                if constexpr (C::HALVES == 1) {
-                    const int y = static_cast<int>((row * C::BPT) / 128);
-                    tma_load_2d(kd, &tm_k, 0, y, &full_bar[stage], policy);
-                    tma_load_2d(kd + C::CODE_BYTES, &tm_v, 0, y, &full_bar[stage], policy);
-                } else {
-                    const int y = static_cast<int>(row);
-#pragma unroll
-                    for (int h = 0; h < C::HALVES; ++h) {
-                        tma_load_2d(kd + h * C::HALF_BYTES, &tm_k, h * 128, y, &full_bar[stage], policy);
-                        tma_load_2d(kd + C::CODE_BYTES + h * C::HALF_BYTES, &tm_v, h * 128, y, &full_bar[stage], policy);
-                    }
-                }
-                const long long sb_off = row * NG;
-                uint8_t* sd = sb + j * seg_rows * NG * 2;
-                bulk_load(sd + 0 * C::SB_BYTES, p.k_scale + sb_off, sb_bytes, &full_bar[stage], policy);
-                bulk_load(sd + 1 * C::SB_BYTES, p.k_bias + sb_off, sb_bytes, &full_bar[stage], policy);
-                bulk_load(sd + 2 * C::SB_BYTES, p.v_scale + sb_off, sb_bytes, &full_bar[stage], policy);
-                bulk_load(sd + 3 * C::SB_BYTES, p.v_bias + sb_off, sb_bytes, &full_bar[stage], policy);
-            }
+        const int j = lane / kCopies, c = lane - j * kCopies;
+        int tok = 0, n = 0;
+        long long row = 0;
+        if (j < n_seg) n = segment(t_begin + it * C::T, j, tok, &row);
+        const uint32_t sb_bytes = static_cast<uint32_t>(PAGED ? seg_rows : min(seg_rows, p.capacity - tok)) * NG * 2;
+        const uint32_t bytes = n == 0 ? 0u : (c < 2 * C::HALVES ? static_cast<uint32_t>(seg_rows) * C::ROWB : sb_bytes);
+        const uint32_t total = __reduce_add_sync(0xffffffffu, bytes);
+        if (lane == 0) mbar_arrive_expect_tx(&full_bar[stage], total);
+        __syncwarp();
+        if (n == 0) return;
+        if (c < 2 * C::HALVES) {
+            const int kv = c / C::HALVES, h = c % C::HALVES;
+            const int y = C::HALVES == 1 ? static_cast<int>((row * C::BPT) / 128) : static_cast<int>(row);
+            tma_load_2d(st + kv * C::CODE_BYTES + h * C::HALF_BYTES + j * seg_rows * C::ROWB, kv ? &tm_v : &tm_k, h * 128, y,
+                        &full_bar[stage], policy);
+        } else {
+            const int a = c - 2 * C::HALVES;
+            const uint16_t* src = a == 0 ? p.k_scale : (a == 1 ? p.k_bias : (a == 2 ? p.v_scale : p.v_bias));
+            bulk_load(st + 2 * C::CODE_BYTES + a * C::SB_BYTES + j * seg_rows * NG * 2, src + row * NG, sb_bytes,
+                      &full_bar[stage], policy);
         }
     };
+    static_assert(!BLK || kCopies * (C::T / 32) <= 32, "a lane per copy, blocks of 32 tokens or more");
 
     // Fill stage it % STAGES with tile it: both code tiles by TMA, the four
     // scale/bias rows by bulk copies; completion counted in bytes on full_bar.
     auto issue_tile = [&](int it, uint64_t policy) {
-        if constexpr (BLK) {
-            issue_blocks(it, policy);
-            return;
-        }
         const int stage = it % C::STAGES;
         const int t0 = t_begin + it * C::T;
         if (tile_uses(it, dep_lo, dep_hi)) pdl_wait_primary();
@@ -479,7 +481,12 @@ __global__ void __launch_bounds__(Cfg<D, BITS, WIDE>::THREADS, Cfg<D, BITS, WIDE
     uint4 app_raw = make_uint4(0, 0, 0, 0);
     if (static_cast<int>(threadIdx.x >> 3) < app_tasks)
         app_raw = __ldcs(reinterpret_cast<const uint4*>(app_src(threadIdx.x >> 3)));
-    if (threadIdx.x == 0 && n_tiles > 0) {
+    if constexpr (BLK) {
+        if (warp == 0 && n_tiles > 0) {
+            const uint64_t policy = policy_evict_first();
+            for (int it = 0; it < min(n_tiles, C::STAGES); ++it) issue_blocks(it, policy);
+        }
+    } else if (threadIdx.x == 0 && n_tiles > 0) {
         prefetch_tensormap(&tm_k);
         prefetch_tensormap(&tm_v);
         const uint64_t policy = policy_evict_first();
@@ -937,7 +944,20 @@ __global__ void __launch_bounds__(Cfg<D, BITS, WIDE>::THREADS, Cfg<D, BITS, WIDE
         // visible by their fences before the counter update) before the
         // asynchronous copies that overwrite it.
         __syncwarp();
-        if (lane == 0) {
+        if constexpr (BLK) {
+            unsigned int before = 0;
+            if (lane == 0) {
+                __threadfence_block();
+                before = atomicAdd(&done_cnt[stage], 1u);
+                __threadfence_block();
+            }
+            before = __shfl_sync(0xffffffffu, before, 0);
+            if (before % C::NWC == C::NWC - 1 && it + C::STAGES < n_tiles) {
+                __syncwarp();
+                fence_proxy_async_shared();
+                issue_blocks(it + C::STAGES, policy_evict_first());
+            }
+        } else if (lane == 0) {
             __threadfence_block();
             const unsigned int before = atomicAdd(&done_cnt[stage], 1u);
             if (before % C::NWC == C::NWC - 1 && it + C::STAGES < n_tiles) {

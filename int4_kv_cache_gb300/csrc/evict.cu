@@ -4,15 +4,15 @@
 // their order, into another cache.
 //
 // Two kernels.  select: one cluster of CTAs per (sequence, kv head), each with
-// a stretch of the weights (held in shared memory where they fit, else read
-// again); the threshold weight by radix selection (11, 11 and 10 bits of the
-// ordered fp32 key) over the cluster's histograms, then the kept rows'
-// indices in order (counts per warp, prefix sums over warps and CTAs).
-// copy: the kept rows, codes and scales, 16 bytes a thread, into consecutive
-// rows of the destination.  Bound by the kept rows' bytes for a batch, by the
-// selection's latency for one sequence.
-#include <atomic>
-
+// a stretch of the weights, 8 or 32 a thread in registers (longer stretches are read
+// again, from L2, in every step); the threshold weight by radix selection (11,
+// 11 and 10 bits of the ordered fp32 key): every CTA counts into its own
+// histogram and adds what is not zero to the first CTA's, which picks the digit
+// and tells the others; then the kept rows' indices in order, from counts per
+// warp and prefix sums over warps and CTAs.  copy: the kept rows, codes and
+// scales, 16 bytes a thread, into consecutive rows of the destination.  Bound
+// by the kept rows' bytes for a batch, by the selection's latency for one
+// sequence.
 #include "tq_device.cuh"
 #include "tq_internal.h"
 
@@ -23,22 +23,30 @@ namespace {
 constexpr int kEvThreads = 512;
 constexpr int kEvWarps = kEvThreads / 32;
 constexpr int kBins = 2048;
+static_assert(kBins == 4 * kEvThreads, "four bins a thread");
 
 __device__ __forceinline__ uint32_t weight_key(float x) {
     const uint32_t u = __float_as_uint(x + 0.0f);  // -0 -> +0
     return (u & 0x80000000u) != 0u ? ~u : (u | 0x80000000u);
 }
 
-__global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const EvictParams p) {
-    extern __shared__ float held[];  // this CTA's stretch of weights, if it fits
-    __shared__ uint32_t hist[kBins];
-    __shared__ uint32_t wcount[2][kEvWarps];
+// V: 16-byte loads of a thread, 2,048 weights of the CTA's stretch each.  ONE:
+// they cover the stretch, which is read once.
+template <int V, bool ONE>
+__global__ void __launch_bounds__(kEvThreads, V == 8 ? 1 : 2) evict_select_kernel(const EvictParams p) {
+    constexpr int kStretch = V * 4 * kEvThreads;
+    constexpr int kRoundWarps = V * kEvWarps;       // 128-weight pieces of a round
+    __shared__ uint32_t hist[kBins];                // this CTA's counts
+    __shared__ uint32_t sums[kBins];                // the first CTA's: the cluster's counts
+    __shared__ uint32_t wcount[kEvWarps];
+    __shared__ uint32_t piece[kRoundWarps];         // above (low half) and equal (high half) of each piece
     __shared__ int pick[2];
-    __shared__ uint32_t cta_count[2];  // this CTA's rows above the threshold, and equal to it
+    __shared__ uint32_t cta_count[2];               // this CTA's rows above the threshold, and equal to it
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int n_cta = p.ctas, rank = static_cast<int>(blockIdx.x) % n_cta;
     const int bh = static_cast<int>(blockIdx.x) / n_cta;
     const int b = bh / p.num_kv_heads;
+    for (int i = threadIdx.x; i < kBins; i += kEvThreads) hist[i] = sums[i] = 0;
     pdl_wait_primary();
     pdl_launch_dependents();
     int len = __ldcg(p.seq_lens + b);
@@ -52,147 +60,240 @@ __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const EvictPar
     int32_t* list = p.kept + static_cast<long long>(bh) * p.keep;
     float* out_w = p.out_weights + static_cast<long long>(bh) * p.out_weight_stride;
     const int part = rank * kEvThreads + threadIdx.x, parts = n_cta * kEvThreads;
+    const bool all = len <= p.keep;      // the whole cluster: every row stays
+    const int old = len - p.recent;      // else: rows that compete, old > want
+    const int want = p.keep - p.recent;  // of them stay
+    const bool choose = !all && want > 0;
+
+    // this CTA's stretch [s0, s1), in rounds of kStretch weights
+    const int per = choose ? ((old + n_cta - 1) / n_cta + 3) & ~3 : 0;
+    const int s0 = min(rank * per, old), s1 = min(s0 + per, old);
+    float4 held[V];
+    auto load_round = [&](int base) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int i = base + (v * kEvThreads + threadIdx.x) * 4;
+            if (i < s1) held[v] = __ldg(reinterpret_cast<const float4*>(weights + i));
+        }
+    };
+    // f(weight, its row) for each of this thread's weights of a round
+    auto visit_round = [&](int base, auto f) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int i = base + (v * kEvThreads + threadIdx.x) * 4;
+            const float w[4] = {held[v].x, held[v].y, held[v].z, held[v].w};
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                if (i + c < s1) f(w[c]);
+        }
+    };
+    if (choose) load_round(s0);
+
+    // what needs no selection
     for (int i = kept + part; i < p.out_weight_stride; i += parts) out_w[i] = 0.0f;
     for (int i = kept + part; i < p.keep; i += parts) list[i] = -1;
     if (bh % p.num_kv_heads == 0 && part == 0) p.out_lens[b] = kept;
-    if (len <= p.keep) {  // the whole cluster: every row stays
+    if (all) {
         for (int i = part; i < len; i += parts) {
             list[i] = i;
             out_w[i] = weights[i];
         }
         return;
     }
-    const int old = len - p.recent;           // rows that compete; old > want
-    const int want = p.keep - p.recent;       // of them stay
     for (int i = part; i < p.recent; i += parts) {
         list[want + i] = old + i;
         out_w[want + i] = weights[old + i];
     }
-    if (want == 0) return;
+    if (!choose) return;
 
-    // this CTA's stretch [s0, s1)
-    const int per = ((old + n_cta - 1) / n_cta + 31) & ~31;
-    const int s0 = min(rank * per, old), s1 = min(s0 + per, old), n = s1 - s0;
-    const float* src = weights + s0;
-    const bool fits = n <= p.held;
+    if (n_cta > 1) cluster_sync();  // every CTA runs, its counts are zero
+    else __syncthreads();
     uint32_t value = 0, mask = 0;
     int above = 0;
     for (int pass = 0; pass < 3; ++pass) {
         const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
         const uint32_t bins = pass == 2 ? 1024u : 2048u;
-        for (int i = threadIdx.x; i < kBins; i += kEvThreads) hist[i] = 0;
-        __syncthreads();
-        for (int i = threadIdx.x; i < n; i += kEvThreads) {
-            float w;
-            if (pass == 0) {
-                w = __ldg(src + i);
-                if (fits) held[i] = w;
-            } else {
-                w = fits ? held[i] : __ldg(src + i);
-            }
-            const uint32_t k = weight_key(w);
-            if ((k & mask) == value) atomicAdd(&hist[(k >> shift) & (bins - 1u)], 1u);
+        for (int base = s0; base < s1; base += kStretch) {
+            if (!ONE) load_round(base);
+            visit_round(base, [&](float w) {
+                const uint32_t k = weight_key(w);
+                if ((k & mask) == value) atomicAdd(&hist[(k >> shift) & (bins - 1u)], 1u);
+            });
+            if (ONE) break;
         }
-        __syncthreads();
-        if (n_cta > 1) cluster_sync();
-        // every CTA: thread t sums bins [base, base + 4) over the cluster, largest bins first
-        uint32_t c[4], sum = 0;
-        const int top = kBins - 1 - 4 * threadIdx.x;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) c[j] = 0;
-        for (int r = 0; r < n_cta; ++r) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) c[j] += n_cta > 1 ? ld_cluster_u32(&hist[top - j], r) : hist[top - j];
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) sum += c[j];
-        uint32_t before = sum;
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const uint32_t o = __shfl_up_sync(0xffffffffu, before, off);
-            if (lane >= off) before += o;
-        }
-        if (lane == 31) wcount[0][warp] = before;
-        __syncthreads();
-        before -= sum;
-        for (int w = 0; w < warp; ++w) before += wcount[0][w];
-        const uint32_t need = static_cast<uint32_t>(want - above);
-        if (before < need && need <= before + sum) {
+        const int top = kBins - 1 - 4 * threadIdx.x;  // this thread's four bins, largest first
+        if (n_cta > 1) {
+            __syncthreads();
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                if (before < need && need <= before + c[j]) {
-                    pick[0] = top - j;
-                    pick[1] = above + static_cast<int>(before);
+                const uint32_t c = hist[top - j];
+                if (c != 0) {
+                    red_cluster_add_u32(&sums[top - j], 0, c);
+                    hist[top - j] = 0;
                 }
-                before += c[j];
+            }
+            cluster_sync();
+        } else {
+            __syncthreads();
+        }
+        uint32_t* from = n_cta > 1 ? sums : hist;
+        if (rank == 0) {
+            uint32_t c[4], sum = 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                c[j] = from[top - j];
+                from[top - j] = 0;
+                sum += c[j];
+            }
+            uint32_t before = sum;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const uint32_t o = __shfl_up_sync(0xffffffffu, before, off);
+                if (lane >= off) before += o;
+            }
+            if (lane == 31) wcount[warp] = before;
+            __syncthreads();
+            before -= sum;
+            for (int w = 0; w < warp; ++w) before += wcount[w];
+            const uint32_t need = static_cast<uint32_t>(want - above);
+            if (before < need && need <= before + sum) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if (before < need && need <= before + c[j]) {
+                        for (int r = 0; r < n_cta; ++r) {
+                            if (n_cta > 1) {
+                                st_cluster_u32(&pick[0], r, top - j);
+                                st_cluster_u32(&pick[1], r, above + before);
+                            } else {
+                                pick[0] = top - j;
+                                pick[1] = above + static_cast<int>(before);
+                            }
+                        }
+                    }
+                    before += c[j];
+                }
             }
         }
-        if (n_cta > 1) cluster_sync();  // also: every CTA has read this histogram
+        if (n_cta > 1) cluster_sync();
         else __syncthreads();
         value |= static_cast<uint32_t>(pick[0]) << shift;
         above = pick[1];
         mask |= (bins - 1u) << shift;
+        if (n_cta == 1) __syncthreads();  // pick and wcount are read before the next pass writes them
     }
-    const int ties = want - above;  // rows equal to the threshold that stay, lowest index first
+    const uint32_t ties = static_cast<uint32_t>(want - above);  // rows equal to the threshold that stay, lowest index first
 
-    // ---- the list: counts per warp (each a consecutive stretch), then places
-    const int span = ((n + kEvWarps - 1) / kEvWarps + 31) & ~31;
-    const int w0 = min(warp * span, n), w1 = min(w0 + span, n);
-    uint32_t n_gt = 0, n_eq = 0;
-    for (int i = w0 + lane; i < w1; i += 32) {
-        const uint32_t k = weight_key(fits ? held[i] : __ldg(src + i));
-        n_gt += k > value;
-        n_eq += k == value;
-    }
-    n_gt = __reduce_add_sync(0xffffffffu, n_gt);
-    n_eq = __reduce_add_sync(0xffffffffu, n_eq);
-    if (lane == 0) {
-        wcount[0][warp] = n_gt;
-        wcount[1][warp] = n_eq;
-    }
-    __syncthreads();
-    uint32_t gt = 0, eq = 0, all_gt = 0, all_eq = 0;
+    // ---- the list.  Rows in order: round, then piece (v, warp) of 128, then lane, then the lane's four.
+    auto counts_of = [&](int base, int v) -> uint32_t {  // of this thread's four: above | equal << 16
+        const int i = base + (v * kEvThreads + threadIdx.x) * 4;
+        const float w[4] = {held[v].x, held[v].y, held[v].z, held[v].w};
+        uint32_t n = 0;
 #pragma unroll
-    for (int w = 0; w < kEvWarps; ++w) {
-        if (w < warp) {
-            gt += wcount[0][w];
-            eq += wcount[1][w];
+        for (int c = 0; c < 4; ++c) {
+            if (i + c < s1) {
+                const uint32_t k = weight_key(w[c]);
+                n += (k > value ? 1u : 0u) + (k == value ? 0x10000u : 0u);
+            }
         }
-        all_gt += wcount[0][w];
-        all_eq += wcount[1][w];
-    }
-    if (n_cta > 1) {
-        if (threadIdx.x == 0) {
-            cta_count[0] = all_gt;
-            cta_count[1] = all_eq;
+        return n;
+    };
+    uint32_t gt = 0, eq = 0;  // above and equal before the current round
+    if (n_cta > 1) {          // the CTAs before this one
+        uint32_t n_gt = 0, n_eq = 0;
+        for (int base = s0; base < s1; base += kStretch) {
+            if (!ONE) load_round(base);
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const uint32_t n = counts_of(base, v);
+                n_gt += n & 0xffffu;
+                n_eq += n >> 16;
+            }
+            if (ONE) break;
+        }
+        if (threadIdx.x < 2) cta_count[threadIdx.x] = 0;
+        __syncthreads();
+        n_gt = __reduce_add_sync(0xffffffffu, n_gt);
+        n_eq = __reduce_add_sync(0xffffffffu, n_eq);
+        if (lane == 0) {
+            atomicAdd(&cta_count[0], n_gt);
+            atomicAdd(&cta_count[1], n_eq);
         }
         cluster_sync();
-        for (int r = 0; r < rank; ++r) {
-            gt += ld_cluster_u32(&cta_count[0], r);
-            eq += ld_cluster_u32(&cta_count[1], r);
+        uint32_t c_gt = 0, c_eq = 0;
+        if (lane < rank) {
+            c_gt = ld_cluster_u32(&cta_count[0], lane);
+            c_eq = ld_cluster_u32(&cta_count[1], lane);
         }
-        cluster_sync();  // no CTA leaves while another reads its counts
+        gt = __reduce_add_sync(0xffffffffu, c_gt);
+        eq = __reduce_add_sync(0xffffffffu, c_eq);
+        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");  // this CTA has read the others' counts
     }
-    const uint32_t below = (1u << lane) - 1u;
-    for (int i0 = w0; i0 < w1; i0 += 32) {
-        const int i = i0 + lane;
-        float w = 0.0f;
-        uint32_t k = 0;
-        if (i < w1) {
-            w = fits ? held[i] : __ldg(src + i);
-            k = weight_key(w);
+    for (int base = s0; base < s1; base += kStretch) {
+        if (!ONE) load_round(base);
+        uint32_t before[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const uint32_t n = counts_of(base, v);
+            uint32_t incl = n;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const uint32_t o = __shfl_up_sync(0xffffffffu, incl, off);
+                if (lane >= off) incl += o;
+            }
+            before[v] = incl - n;
+            if (lane == 31) piece[v * kEvWarps + warp] = incl;
         }
-        const bool is_gt = i < w1 && k > value, is_eq = i < w1 && k == value;
-        const uint32_t bg = __ballot_sync(0xffffffffu, is_gt), be = __ballot_sync(0xffffffffu, is_eq);
-        const uint32_t rank_eq = eq + __popc(be & below);
-        const uint32_t at = gt + __popc(bg & below) + min(rank_eq, static_cast<uint32_t>(ties));
-        if (is_gt || (is_eq && rank_eq < static_cast<uint32_t>(ties))) {
-            list[at] = s0 + i;
-            out_w[at] = w;
+        __syncthreads();
+        // exclusive prefix over the pieces (a round holds at most 16,384 rows: no carry between the halves)
+        if (warp == 0) {
+            constexpr int P = kRoundWarps / 32;
+            static_assert(kRoundWarps % 32 == 0 && kStretch <= 16384, "whole lanes; counts fit 16 bits");
+            uint32_t c[P], sum = 0;
+#pragma unroll
+            for (int j = 0; j < P; ++j) {
+                c[j] = piece[lane * P + j];
+                sum += c[j];
+            }
+            uint32_t run = sum;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const uint32_t o = __shfl_up_sync(0xffffffffu, run, off);
+                if (lane >= off) run += o;
+            }
+            if (lane == 31) wcount[0] = run;
+            run -= sum;
+#pragma unroll
+            for (int j = 0; j < P; ++j) {
+                piece[lane * P + j] = run;
+                run += c[j];
+            }
         }
-        gt += __popc(bg);
-        eq += __popc(be);
+        __syncthreads();
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int i = base + (v * kEvThreads + threadIdx.x) * 4;
+            const uint32_t at0 = before[v] + piece[v * kEvWarps + warp];
+            uint32_t g = gt + (at0 & 0xffffu), e = eq + (at0 >> 16);
+            const float w[4] = {held[v].x, held[v].y, held[v].z, held[v].w};
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                if (i + c >= s1) break;
+                const uint32_t k = weight_key(w[c]);
+                if (k > value || (k == value && e < ties)) {
+                    const uint32_t at = g + min(e, ties);
+                    list[at] = i + c;
+                    out_w[at] = w[c];
+                }
+                g += k > value ? 1u : 0u;
+                e += k == value ? 1u : 0u;
+            }
+        }
+        gt += wcount[0] & 0xffffu;
+        eq += wcount[0] >> 16;
+        if (ONE) break;
+        __syncthreads();
     }
+    if (n_cta > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // nobody reads this CTA's memory any more
 }
 
 constexpr int kCopyThreads = 256;
@@ -242,20 +343,10 @@ __global__ void __launch_bounds__(kCopyThreads) evict_copy_kernel(const EvictCop
 
 }  // namespace
 
-cudaError_t launch_evict_select(const EvictParams& p, int held_bytes, cudaStream_t stream) {
-    static std::atomic<bool> done[64];
-    int dev = 0;
-    cudaGetDevice(&dev);
-    if (dev < 0 || dev >= 64 || !done[dev].load(std::memory_order_acquire)) {
-        const cudaError_t e =
-            cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxEvictHeldBytes);
-        if (e != cudaSuccess) return e;
-        if (dev >= 0 && dev < 64) done[dev].store(true, std::memory_order_release);
-    }
+cudaError_t launch_evict_select(const EvictParams& p, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(p.batch) * p.num_kv_heads * p.ctas);
     cfg.blockDim = dim3(kEvThreads);
-    cfg.dynamicSmemBytes = static_cast<size_t>(held_bytes);
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -266,7 +357,11 @@ cudaError_t launch_evict_select(const EvictParams& p, int held_bytes, cudaStream
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, evict_select_kernel, p);
+    const long long most = (static_cast<long long>(p.max_seq_len) - p.recent + p.ctas - 1) / p.ctas;  // a CTA's stretch
+    using Kern = void (*)(EvictParams);
+    const Kern k = most <= kEvStretch / 4 ? evict_select_kernel<2, true>
+                                          : (most <= kEvStretch ? evict_select_kernel<8, true> : evict_select_kernel<8, false>);
+    return cudaLaunchKernelEx(&cfg, k, p);
 }
 
 cudaError_t launch_evict_copy(const EvictCopyParams& p, cudaStream_t stream) {

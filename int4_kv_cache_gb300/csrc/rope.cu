@@ -76,26 +76,41 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) 
     // consecutive threads: the units of a row, then the tokens of a head (whose
     // output rows are neighbours), then the heads
     const int per_head = units * nt, total = heads * per_head;
-    for (int i = threadIdx.x; i < total; i += kRopeThreads) {
-        int h = i / per_head;
-        const int r = i - h * per_head;
-        const int t = r / units, u = r - t * units;
-        const bool is_k = h >= p.q.heads;
-        const RopeRows& rows = is_k ? p.k : p.q;
-        if (is_k) h -= p.q.heads;
-        const uint16_t* src = rows.x + b * rows.stride_b + static_cast<long long>(t0 + t) * rows.stride_t + h * rows.stride_h;
-        uint16_t* dst = rows.out + ((static_cast<long long>(b) * rows.heads + h) * p.n + t0 + t) * p.head_dim;
-        const bool split = !PAIRS && u < turning;
-        const int e0 = split ? 8 * u : 16 * u, e1 = split ? half + 8 * u : 16 * u + 8;
-        uint4 x = __ldcs(reinterpret_cast<const uint4*>(src + e0));
-        uint4 y = __ldcs(reinterpret_cast<const uint4*>(src + e1));
-        const float* c = table + t * 2 * half + 8 * u;
-        if (u < turning) {
-            if (PAIRS) turn_pairs8(x, y, c, c + half);
-            else turn8(x, y, c, c + half);
+    constexpr int U = 3;  // units of a thread in flight
+    for (int i0 = threadIdx.x; i0 < total; i0 += U * kRopeThreads) {
+        uint4 x[U], y[U];
+        uint16_t* dst[U];
+        int e0[U], e1[U], at[U];
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const int i = i0 + k * kRopeThreads;
+            if (i >= total) break;
+            int h = i / per_head;
+            const int r = i - h * per_head;
+            const int t = r / units, u = r - t * units;
+            const bool is_k = h >= p.q.heads;
+            const RopeRows& rows = is_k ? p.k : p.q;
+            if (is_k) h -= p.q.heads;
+            const uint16_t* src = rows.x + b * rows.stride_b + static_cast<long long>(t0 + t) * rows.stride_t + h * rows.stride_h;
+            dst[k] = rows.out + ((static_cast<long long>(b) * rows.heads + h) * p.n + t0 + t) * p.head_dim;
+            const bool turns = u < turning, split = !PAIRS && turns;
+            e0[k] = split ? 8 * u : 16 * u;
+            e1[k] = split ? half + 8 * u : 16 * u + 8;
+            at[k] = turns ? t * 2 * half + 8 * u : -1;
+            x[k] = __ldcs(reinterpret_cast<const uint4*>(src + e0[k]));
+            y[k] = __ldcs(reinterpret_cast<const uint4*>(src + e1[k]));
         }
-        *reinterpret_cast<uint4*>(dst + e0) = x;
-        *reinterpret_cast<uint4*>(dst + e1) = y;
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            if (i0 + k * kRopeThreads >= total) break;
+            if (at[k] >= 0) {
+                const float* c = table + at[k];
+                if (PAIRS) turn_pairs8(x[k], y[k], c, c + half);
+                else turn8(x[k], y[k], c, c + half);
+            }
+            *reinterpret_cast<uint4*>(dst[k] + e0[k]) = x[k];
+            *reinterpret_cast<uint4*>(dst[k] + e1[k]) = y[k];
+        }
     }
 }
 

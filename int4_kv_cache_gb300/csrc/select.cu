@@ -34,8 +34,7 @@ namespace tq {
 
 namespace {
 
-constexpr int kSelThreads = 256;
-constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kFew = 32;  // keys that a warp ranks by itself
 
 __device__ __forceinline__ uint32_t ordered_key(float x) {
     const uint32_t u = __float_as_uint(x + 0.0f);  // -0 -> +0
@@ -49,88 +48,99 @@ __device__ __forceinline__ uint64_t ordered_key(double x) {
     return (u >> 63) != 0u ? ~u : (u | 0x8000000000000000ull);
 }
 
-// The n-th largest (n >= 1) of the keys visit() hands out, by digits of eight
-// bits from the highest in which the keys differ.  `above`: keys larger than
-// it.  Every thread calls; visit(f) calls f(key) for this thread's keys.
-template <typename K, typename Visit>
-__device__ __forceinline__ K nth_largest(int n, Visit visit, uint32_t* hist, int& above) {
-    __shared__ K red_lo[kSelWarps], red_hi[kSelWarps];
-    __shared__ int pick[2];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    K lo = ~static_cast<K>(0), hi = 0;
-    visit([&](K k) {
-        lo = k < lo ? k : lo;
-        hi = k > hi ? k : hi;
-    });
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
-        const K a = __shfl_xor_sync(0xffffffffu, lo, off), c = __shfl_xor_sync(0xffffffffu, hi, off);
-        lo = a < lo ? a : lo;
-        hi = c > hi ? c : hi;
-    }
-    __syncthreads();  // pick and red_* of an earlier call have been read
-    if (lane == 0) {
-        red_lo[warp] = lo;
-        red_hi[warp] = hi;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kSelWarps; ++w) {
-        lo = red_lo[w] < lo ? red_lo[w] : lo;
-        hi = red_hi[w] > hi ? red_hi[w] : hi;
-    }
+// The n-th largest (n >= 1) of the keys visit() hands out, all of them in [lo,
+// hi], by digits of eight bits from the highest in which lo and hi differ, until
+// kFew keys or fewer share the digits so far; those are gathered and ranked
+// directly.  `above`: how many keys are larger.  Every thread of the CTA calls
+// with hist zeroed (both halves) a barrier ago; visit(f) calls f(key) for this
+// thread's keys.
+template <int THREADS, typename K, typename Visit>
+__device__ __forceinline__ K nth_largest(int n, K lo, K hi, Visit visit, uint32_t (*hist)[256], int& above) {
+    __shared__ K few[kFew];
+    __shared__ int n_few;
+    const int lane = threadIdx.x & 31;
     above = 0;
     const K diff = lo ^ hi;
-    int bits = 0;  // the low bits in which keys differ
-    for (K d = diff; d != 0; d >>= 1) ++bits;
+    int bits;  // the low bits in which keys may differ
+    if constexpr (sizeof(K) == 8) bits = diff == 0 ? 0 : 64 - __clzll(static_cast<long long>(diff));
+    else bits = 32 - __clz(static_cast<int>(diff));
     const K ones = ~static_cast<K>(0);
-    K mask = bits == static_cast<int>(sizeof(K) * 8) ? 0 : ones << bits;  // bits already decided
+    K mask = bits == static_cast<int>(sizeof(K) * 8) ? 0 : ones << bits;
     K value = hi & mask;
-    while (bits > 0) {
-        const int take = bits < 8 ? bits : 8, shift = bits - take;
-        for (int i = threadIdx.x; i < 256; i += kSelThreads) hist[i] = 0;
-        __syncthreads();
+    if (threadIdx.x == 0) n_few = 0;
+    for (int pass = 0; bits > 0; ++pass) {
+        const int take = bits < 8 ? bits : 8, shift = bits - take, h = pass & 1;
         visit([&](K k) {
-            if ((k & mask) == value) atomicAdd(&hist[static_cast<uint32_t>(k >> shift) & ((1u << take) - 1u)], 1u);
+            if ((k & mask) == value) atomicAdd(&hist[h][static_cast<uint32_t>(k >> shift) & ((1u << take) - 1u)], 1u);
         });
         __syncthreads();
-        if (warp == 0) {  // lane l holds bins 255 - 8l .. 248 - 8l: counts from the largest digit down
-            uint32_t c[8], sum = 0;
+        for (int i = threadIdx.x; i < 256; i += THREADS) hist[h ^ 1][i] = 0;  // read a barrier ago
+        // every warp finds the digit: lane l holds bins 255 - 8l .. 248 - 8l, counts from the largest down
+        uint32_t c[8], sum = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            c[j] = hist[h][255 - 8 * lane - j];
+            sum += c[j];
+        }
+        uint32_t before = sum;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const uint32_t o = __shfl_up_sync(0xffffffffu, before, off);
+            if (lane >= off) before += o;
+        }
+        before -= sum;
+        const uint32_t want = static_cast<uint32_t>(n - above);
+        uint32_t bin = 0, ahead = 0, here = 0;
+        const bool mine = before < want && want <= before + sum;
+        if (mine) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                c[j] = hist[255 - 8 * lane - j];
-                sum += c[j];
-            }
-            uint32_t before = sum;
-#pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-                const uint32_t o = __shfl_up_sync(0xffffffffu, before, off);
-                if (lane >= off) before += o;
-            }
-            before -= sum;
-            const uint32_t want = static_cast<uint32_t>(n - above);
-            if (before < want && want <= before + sum) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    if (before < want && want <= before + c[j]) {
-                        pick[0] = 255 - 8 * lane - j;
-                        pick[1] = above + static_cast<int>(before);
-                    }
-                    before += c[j];
+                if (before < want && want <= before + c[j]) {
+                    bin = 255 - 8 * lane - j;
+                    ahead = before;
+                    here = c[j];
                 }
+                before += c[j];
             }
         }
-        __syncthreads();
-        value |= static_cast<K>(pick[0]) << shift;
-        above = pick[1];
+        const uint32_t who = __ballot_sync(0xffffffffu, mine);
+        const int src = who != 0 ? __ffs(who) - 1 : 0;
+        bin = __shfl_sync(0xffffffffu, bin, src);
+        above += static_cast<int>(__shfl_sync(0xffffffffu, ahead, src));
+        here = __shfl_sync(0xffffffffu, here, src);
+        value |= static_cast<K>(bin) << shift;
         bits = shift;
         mask = shift == 0 ? ones : ones << shift;
+        if (bits > 0 && here <= kFew) {  // the same for the CTA
+            visit([&](K k) {
+                if ((k & mask) == value) {
+                    const int at = atomicAdd(&n_few, 1);
+                    if (at < kFew) few[at] = k;
+                }
+            });
+            __syncthreads();
+            const int m = min(n_few, kFew);
+            const K mine_k = lane < m ? few[lane] : 0;
+            int greater = 0, equal = 0;
+            for (int j = 0; j < m; ++j) {
+                const K o = __shfl_sync(0xffffffffu, mine_k, j);
+                greater += o > mine_k ? 1 : 0;
+                equal += o == mine_k ? 1 : 0;
+            }
+            const int need = n - above;
+            const uint32_t it = __ballot_sync(0xffffffffu, lane < m && greater < need && need <= greater + equal);
+            const int at = it != 0 ? __ffs(it) - 1 : 0;
+            above += __shfl_sync(0xffffffffu, greater, at);
+            return __shfl_sync(0xffffffffu, mine_k, at);
+        }
+        __syncthreads();  // the other half is zero, this one has been read
     }
     return value;
 }
 
-template <int D>
-__global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams p) {
+template <int D, int THREADS>
+__global__ void __launch_bounds__(THREADS, (D == 256 ? 512 : 768) / THREADS) select_kernel(const SelectParams p) {
+    constexpr int WARPS = THREADS / 32;
     constexpr int NJ = D / 32;  // 16-byte pieces of a row per lane
     // Every product of 16 terms starts from zero and is added to the sum in
     // fp32: 16 terms cut at 2^-23 of the largest, and D / 8 additions rounded to
@@ -138,18 +148,33 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
     // (8 * 2^-23 more for the sums that give those magnitudes).
     constexpr float kEps = static_cast<float>(24 + D / 16) * 0x1p-23f;
     extern __shared__ uint32_t keys[];  // the first CTA's: one per block of the sequence
-    __shared__ float warp_abs[8 * kSelWarps];  // the first CTA's: largest sum |terms| of every warp
-    __shared__ uint32_t hist[256];
-    __shared__ int wsum[2][kSelWarps];
+    // the first CTA's: every warp's largest sum |terms|, least and greatest key
+    __shared__ uint32_t warp_abs[8 * WARPS], warp_lo[8 * WARPS], warp_hi[8 * WARPS];
+    __shared__ uint32_t hist[2][256];
+    __shared__ int wsum[2][WARPS];
+    __shared__ uint64_t red_lo[WARPS], red_hi[WARPS];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int gid = lane >> 2, tig = lane & 3;
     const int n_cta = p.ctas, rank = static_cast<int>(blockIdx.x) % n_cta;
     const int bh = static_cast<int>(blockIdx.x) / n_cta;
     const int b = bh / p.num_kv_heads;
     const int G = p.group_q;
+    // every CTA of the cluster runs once all have arrived: then the first one's
+    // shared memory may be written
+    if (n_cta > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
     pdl_wait_primary();
     pdl_launch_dependents();
     int len = __ldcg(p.seq_lens + b);
+    if (rank == 0) {
+        for (int i = threadIdx.x; i < 512; i += THREADS) hist[i >> 8][i & 255] = 0;
+    }
+    uint4 qraw[NJ];  // this lane's dims 32 j + 8 tig .. + 7 of head gid
+    {
+        const uint16_t* q = p.q + (static_cast<long long>(bh) * G + (gid < G ? gid : 0)) * D + 8 * tig;
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) qraw[j] = __ldcg(reinterpret_cast<const uint4*>(q + 32 * j));
+    }
+    if (n_cta > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
     if (len < 0 || len > p.max_seq_len) {
         if (p.status != nullptr && threadIdx.x == 0 && rank == 0 && bh % p.num_kv_heads == 0)
             atomicOr(p.status, TQ_DEV_SEQ_LEN);
@@ -158,23 +183,19 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
     const int nb = (len + (1 << p.block_shift) - 1) >> p.block_shift;
     int32_t* list = p.blocks + static_cast<long long>(bh) * p.n_select;
     if (nb <= p.n_select) {  // the whole cluster: every block is listed
-        for (int i = rank * kSelThreads + threadIdx.x; i < p.n_select; i += n_cta * kSelThreads) list[i] = i < nb ? i : -1;
+        for (int i = rank * THREADS + threadIdx.x; i < p.n_select; i += n_cta * THREADS) list[i] = i < nb ? i : -1;
         return;
     }
     const int c0 = p.n_first, c1 = nb - p.n_last;  // the blocks that compete
-    if (n_cta > 1) cluster_sync();  // the first CTA runs: its shared memory may be written
 
     // ---- scores
     const uint16_t* bounds = p.bounds + static_cast<long long>(bh) * p.blocks_per_seq * (2 * D);
     {
-        uint4 qp[NJ], qn[NJ];  // this lane's dims 32 j + 8 tig .. + 7 of head gid: positive and negative parts
-        const bool hv = gid < G;
-        const uint16_t* q = p.q + (static_cast<long long>(bh) * G + (hv ? gid : 0)) * D + 8 * tig;
+        uint4 qp[NJ], qn[NJ];  // the positive and the negative parts (no head: zeros)
         const __half2 zero = __float2half2_rn(0.0f);
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
-            uint4 x = make_uint4(0, 0, 0, 0);
-            if (hv) x = *reinterpret_cast<const uint4*>(q + 32 * j);
+            const uint4 x = gid < G ? qraw[j] : make_uint4(0, 0, 0, 0);
             const __half2* h = reinterpret_cast<const __half2*>(&x);
             __half2* hp = reinterpret_cast<__half2*>(&qp[j]);
             __half2* hn = reinterpret_cast<__half2*>(&qn[j]);
@@ -187,7 +208,8 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
         const int tiles = (nb + 15) / 16, per = (tiles + n_cta - 1) / n_cta;
         const int end = min((rank + 1) * per, tiles);
         float most = 0.0f;
-        for (int tile = rank * per + warp; tile < end; tile += kSelWarps) {
+        uint32_t least = 0xffffffffu, greatest = 0u;
+        for (int tile = rank * per + warp; tile < end; tile += WARPS) {
             const int r0 = tile * 16 + gid, r1 = r0 + 8;
             const uint16_t* a0 = bounds + static_cast<long long>(min(r0, nb - 1)) * (2 * D) + 8 * tig;
             const uint16_t* a1 = bounds + static_cast<long long>(min(r1, nb - 1)) * (2 * D) + 8 * tig;
@@ -198,7 +220,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
                 const uint4 l1 = __ldcg(reinterpret_cast<const uint4*>(a1 + 32 * j));
                 const uint4 h0 = __ldcg(reinterpret_cast<const uint4*>(a0 + D + 32 * j));
                 const uint4 h1 = __ldcg(reinterpret_cast<const uint4*>(a1 + D + 32 * j));
-                constexpr uint32_t A = 0x7fff7fffu;
+                constexpr uint32_t A = 0x7fff7fffu;  // absolute values
                 float f[4][4] = {};
                 mma_16816(f[0], h0.x, h1.x, h0.y, h1.y, qp[j].x, qp[j].y);
                 mma_16816(f[1], h0.z, h1.z, h0.w, h1.w, qp[j].z, qp[j].w);
@@ -223,12 +245,26 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
                 m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, off));
                 m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, off));
             }
-            if (tig == 0 && r0 < nb) st_cluster_u32(&keys[r0], 0, ordered_key(m0));
-            if (tig == 1 && r1 < nb) st_cluster_u32(&keys[r1], 0, ordered_key(m1));
+            // lanes tig = 0 pass row r0 on, tig = 1 row r1
+            const int r = tig == 0 ? r0 : r1;
+            if (tig < 2 && r < nb) {
+                const uint32_t k = ordered_key(tig == 0 ? m0 : m1);
+                st_cluster_u32(&keys[r], 0, k);
+                if (r >= c0 && r < c1) {
+                    least = min(least, k);
+                    greatest = max(greatest, k);
+                }
+            }
         }
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, off));
-        if (lane == 0) st_cluster_u32(&warp_abs[rank * kSelWarps + warp], 0, __float_as_uint(most));
+        least = __reduce_min_sync(0xffffffffu, least);
+        greatest = __reduce_max_sync(0xffffffffu, greatest);
+        if (lane == 0) {
+            st_cluster_u32(&warp_abs[rank * WARPS + warp], 0, __float_as_uint(most));
+            st_cluster_u32(&warp_lo[rank * WARPS + warp], 0, least);
+            st_cluster_u32(&warp_hi[rank * WARPS + warp], 0, greatest);
+        }
     }
     if (n_cta > 1) cluster_sync();
     else __syncthreads();
@@ -236,138 +272,159 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
 
     // ---- selection (the first CTA): R of the competing blocks
     const int R = p.n_select - p.n_first - p.n_last;
+    for (int i = threadIdx.x; i < p.n_first; i += THREADS) list[i] = i;
+    for (int i = threadIdx.x; i < p.n_last; i += THREADS) list[p.n_select - p.n_last + i] = c1 + i;
+    if (R == 0) return;
     float eps = 0.0f;
-    for (int i = 0; i < n_cta * kSelWarps; ++i) eps = fmaxf(eps, warp_abs[i]);
+    uint32_t key_lo = 0xffffffffu, key_hi = 0u;
+    for (int i = lane; i < n_cta * WARPS; i += 32) {
+        eps = fmaxf(eps, __uint_as_float(warp_abs[i]));
+        key_lo = min(key_lo, warp_lo[i]);
+        key_hi = max(key_hi, warp_hi[i]);
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) eps = fmaxf(eps, __shfl_xor_sync(0xffffffffu, eps, off));
     eps *= 2.0f * kEps;
-    constexpr uint32_t kIn = 0xffffffffu, kOut = 0u, kOpen = 1u;  // what keys[] becomes (no finite score's key)
-    uint64_t open_at = 0;  // the exact score's key from which open blocks are in ...
-    int open_ties = 0;     // ... and how many of those equal to it, lowest index first
-    double* exact = p.exact + static_cast<long long>(bh) * p.exact_stride;
-    if (R > 0) {
-        int above;
-        const uint32_t tau = nth_largest<uint32_t>(
-            R, [&](auto f) { for (int i = c0 + threadIdx.x; i < c1; i += kSelThreads) f(keys[i]); }, hist, above);
-        const float t = ordered_value(tau);
-        const float up = t + eps, down = t - eps;
-        int n_in = 0, n_open = 0;
-        for (int i = c0 + threadIdx.x; i < c1; i += kSelThreads) {
-            const float v = ordered_value(keys[i]);
-            const uint32_t k = v > up ? kIn : (v < down ? kOut : kOpen);
-            keys[i] = k;
-            n_in += k == kIn;
-            n_open += k == kOpen;
+    key_lo = __reduce_min_sync(0xffffffffu, key_lo);
+    key_hi = __reduce_max_sync(0xffffffffu, key_hi);
+    int above;
+    const uint32_t tau = nth_largest<THREADS, uint32_t>(
+        R, key_lo, key_hi, [&](auto f) { for (int i = c0 + threadIdx.x; i < c1; i += THREADS) f(keys[i]); }, hist, above);
+    const float up = ordered_value(tau) + eps, down = ordered_value(tau) - eps;
+    // each warp a stretch of consecutive blocks [w0, w1): in, or open
+    const int span = ((c1 - c0 + WARPS - 1) / WARPS + 31) & ~31;
+    const int w0 = min(c0 + warp * span, c1), w1 = min(w0 + span, c1);
+    auto is_in = [&](int i) { return ordered_value(keys[i]) > up; };
+    auto is_open = [&](int i) {
+        const float v = ordered_value(keys[i]);
+        return !(v > up) && !(v < down);
+    };
+    auto count = [&](auto a, auto c) {  // how many blocks of each stretch satisfy a, and how many c
+        int na = 0, nc = 0;
+        for (int i = w0 + lane; i < w1; i += 32) {
+            na += a(i) ? 1 : 0;
+            nc += c(i) ? 1 : 0;
         }
-        n_in = __reduce_add_sync(0xffffffffu, n_in);
-        n_open = __reduce_add_sync(0xffffffffu, n_open);
+        na = __reduce_add_sync(0xffffffffu, na);
+        nc = __reduce_add_sync(0xffffffffu, nc);
         if (lane == 0) {
-            wsum[0][warp] = n_in;
-            wsum[1][warp] = n_open;
+            wsum[0][warp] = na;
+            wsum[1][warp] = nc;
         }
-        __syncthreads();
-        n_in = n_open = 0;
+    };
+    auto totals = [&](int& before_a, int& before_c, int& all_a, int& all_c) {
+        before_a = before_c = all_a = all_c = 0;
 #pragma unroll
-        for (int w = 0; w < kSelWarps; ++w) {
-            n_in += wsum[0][w];
-            n_open += wsum[1][w];
+        for (int w = 0; w < WARPS; ++w) {
+            const int na = wsum[0][w], nc = wsum[1][w];
+            before_a += w < warp ? na : 0;
+            before_c += w < warp ? nc : 0;
+            all_a += na;
+            all_c += nc;
         }
-        if (n_in + n_open > R) {  // the same for the CTA
-            // exact scores of the open blocks, a warp each
-            for (int i0 = c0 + warp * 32; i0 < c1; i0 += kSelThreads) {
-                const int i = i0 + lane;
-                uint32_t todo = __ballot_sync(0xffffffffu, i < c1 && keys[i] == kOpen);
-                while (todo != 0) {
-                    const int blk = i0 + __ffs(todo) - 1;
-                    todo &= todo - 1;
-                    const uint16_t* row = bounds + static_cast<long long>(blk) * (2 * D);
-                    double best = -INFINITY;
-                    for (int g = 0; g < G; ++g) {
-                        const uint16_t* q = p.q + (static_cast<long long>(bh) * G + g) * D;
-                        double sum = 0.0;
-                        for (int d = lane; d < D; d += 32) {
-                            const float x = __half2float(__ushort_as_half(q[d]));
-                            const float y = __half2float(__ushort_as_half(row[x > 0.0f ? D + d : d]));
-                            sum = fma(static_cast<double>(x), static_cast<double>(y), sum);
-                        }
-#pragma unroll
-                        for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-                        best = sum > best ? sum : best;
-                    }
-                    if (lane == 0) exact[blk] = best;
-                }
-            }
-            __syncthreads();
-            int over;
-            open_at = nth_largest<uint64_t>(
-                R - n_in,
-                [&](auto f) {
-                    for (int i = c0 + threadIdx.x; i < c1; i += kSelThreads)
-                        if (keys[i] == kOpen) f(ordered_key(exact[i]));
-                },
-                hist, over);
-            open_ties = R - n_in - over;
-        } else {
-            open_at = 0;
-            open_ties = n_open;
+    };
+    // the listed blocks in order: those of a, and of those of c the first `most`
+    auto list_them = [&](auto a, auto c, int na, int nc, int most) {
+        for (int i0 = w0; i0 < w1; i0 += 32) {
+            const int i = i0 + lane;
+            const bool ia = i < w1 && a(i), ic = i < w1 && c(i);
+            const uint32_t ba = __ballot_sync(0xffffffffu, ia), bc = __ballot_sync(0xffffffffu, ic);
+            const uint32_t below = (1u << lane) - 1u;
+            const int rank_c = nc + __popc(bc & below);
+            const int at = na + __popc(ba & below) + min(rank_c, most);
+            if ((ia || (ic && rank_c < most)) && at < R) list[p.n_first + at] = i;
+            na += __popc(ba);
+            nc += __popc(bc);
         }
-        if (n_in + n_open <= R) {  // all of them
-            for (int i = c0 + threadIdx.x; i < c1; i += kSelThreads)
-                if (keys[i] == kOpen) keys[i] = kIn;
-        }
-    }
+    };
+    int before_in, before_open, n_in, n_open;
+    count(is_in, is_open);
     __syncthreads();
-
-    // ---- the list, in order: first blocks, the selected, last blocks
-    for (int i = threadIdx.x; i < p.n_first; i += kSelThreads) list[i] = i;
-    for (int i = threadIdx.x; i < p.n_last; i += kSelThreads) list[p.n_select - p.n_last + i] = c1 + i;
-    int listed = 0, ties = 0;
-    for (int i0 = c0; i0 < c1 && R > 0; i0 += kSelThreads) {
-        const int i = i0 + threadIdx.x;
-        bool in = false, tie = false;
-        if (i < c1) {
-            in = keys[i] == kIn;
-            if (keys[i] == kOpen) {
-                const uint64_t e = ordered_key(exact[i]);
-                in = e > open_at;
-                tie = e == open_at;
-            }
-        }
-        const uint32_t before = (1u << lane) - 1u;
-        const uint32_t bt = __ballot_sync(0xffffffffu, tie);
-        if (lane == 0) wsum[1][warp] = __popc(bt);
-        __syncthreads();
-        int tie_rank = ties + __popc(bt & before);
-        for (int w = 0; w < kSelWarps; ++w) {
-            if (w < warp) tie_rank += wsum[1][w];
-            ties += wsum[1][w];
-        }
-        in = in || (tie && tie_rank < open_ties);
-        const uint32_t bi = __ballot_sync(0xffffffffu, in);
-        if (lane == 0) wsum[0][warp] = __popc(bi);
-        __syncthreads();
-        int at = listed + __popc(bi & before);
-        for (int w = 0; w < kSelWarps; ++w) {
-            if (w < warp) at += wsum[0][w];
-            listed += wsum[0][w];
-        }
-        if (in && at < R) list[p.n_first + at] = i;
-        __syncthreads();
+    totals(before_in, before_open, n_in, n_open);
+    if (n_in + n_open <= R) {  // all of them
+        list_them(is_in, is_open, before_in, before_open, n_open);
+        // scores that are no numbers may leave places: empty ones
+        for (int i = n_in + n_open + threadIdx.x; i < R; i += THREADS) list[p.n_first + i] = -1;
+        return;
     }
-    // scores that are no numbers may leave places: empty ones
-    for (int i = listed + threadIdx.x; i < R; i += kSelThreads) list[p.n_first + i] = -1;
+    // ---- exact scores of the open blocks, a warp each, and their rank
+    double* exact = p.exact + static_cast<long long>(bh) * p.exact_stride;
+    uint64_t ex_lo = ~0ull, ex_hi = 0ull;
+    for (int i0 = c0 + warp * 32; i0 < c1; i0 += THREADS) {
+        uint32_t todo = __ballot_sync(0xffffffffu, i0 + lane < c1 && is_open(i0 + lane));
+        while (todo != 0) {
+            const int blk = i0 + __ffs(todo) - 1;
+            todo &= todo - 1;
+            const uint16_t* row = bounds + static_cast<long long>(blk) * (2 * D);
+            float lo[NJ], hi[NJ];
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) {
+                lo[j] = __half2float(__ushort_as_half(__ldcg(row + 32 * j + lane)));
+                hi[j] = __half2float(__ushort_as_half(__ldcg(row + D + 32 * j + lane)));
+            }
+            double best = -INFINITY;
+#pragma unroll
+            for (int g = 0; g < 8; ++g) {
+                if (g >= G) break;
+                const uint16_t* q = p.q + (static_cast<long long>(bh) * G + g) * D + lane;
+                double sum = 0.0;
+#pragma unroll
+                for (int j = 0; j < NJ; ++j) {
+                    const float x = __half2float(__ushort_as_half(__ldcg(q + 32 * j)));
+                    sum = fma(static_cast<double>(x), static_cast<double>(x > 0.0f ? hi[j] : lo[j]), sum);
+                }
+#pragma unroll
+                for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+                best = sum > best ? sum : best;
+            }
+            if (lane == 0) exact[blk] = best;
+            const uint64_t k = ordered_key(best);
+            ex_lo = k < ex_lo ? k : ex_lo;
+            ex_hi = k > ex_hi ? k : ex_hi;
+        }
+    }
+    if (lane == 0) {
+        red_lo[warp] = ex_lo;
+        red_hi[warp] = ex_hi;
+    }
+    for (int i = threadIdx.x; i < 512; i += THREADS) hist[i >> 8][i & 255] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+        ex_lo = red_lo[w] < ex_lo ? red_lo[w] : ex_lo;
+        ex_hi = red_hi[w] > ex_hi ? red_hi[w] : ex_hi;
+    }
+    int over;
+    const uint64_t border = nth_largest<THREADS, uint64_t>(
+        R - n_in, ex_lo, ex_hi,
+        [&](auto f) {
+            for (int i = c0 + threadIdx.x; i < c1; i += THREADS)
+                if (is_open(i)) f(ordered_key(exact[i]));
+        },
+        hist, over);
+    auto beats = [&](int i) { return is_in(i) || (is_open(i) && ordered_key(exact[i]) > border); };
+    auto ties = [&](int i) { return is_open(i) && ordered_key(exact[i]) == border; };
+    count(beats, ties);
+    __syncthreads();
+    int before_tie, n_tie;
+    totals(before_in, before_tie, n_in, n_tie);
+    list_them(beats, ties, before_in, before_tie, R - n_in);
 }
 
-template <int D>
+template <int D, int THREADS>
 cudaError_t launch_select_d(cudaLaunchConfig_t& cfg, const SelectParams& p) {
     static std::atomic<bool> done[64];
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev < 0 || dev >= 64 || !done[dev].load(std::memory_order_acquire)) {
-        const cudaError_t e = cudaFuncSetAttribute(select_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   kMaxSelectBlocks * static_cast<int>(sizeof(uint32_t)));
+        const cudaError_t e =
+            cudaFuncSetAttribute(select_kernel<D, THREADS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 kMaxSelectBlocks * static_cast<int>(sizeof(uint32_t)));
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) done[dev].store(true, std::memory_order_release);
     }
-    return cudaLaunchKernelEx(&cfg, select_kernel<D>, p);
+    cfg.blockDim = dim3(THREADS);
+    return cudaLaunchKernelEx(&cfg, select_kernel<D, THREADS>, p);
 }
 
 }  // namespace
@@ -375,7 +432,6 @@ cudaError_t launch_select_d(cudaLaunchConfig_t& cfg, const SelectParams& p) {
 cudaError_t launch_select(const SelectParams& p, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(p.batch) * p.num_kv_heads * p.ctas);
-    cfg.blockDim = dim3(kSelThreads);
     const int nb = (p.max_seq_len + (1 << p.block_shift) - 1) >> p.block_shift;
     cfg.dynamicSmemBytes = static_cast<size_t>(nb) * sizeof(uint32_t);
     cfg.stream = stream;
@@ -389,9 +445,9 @@ cudaError_t launch_select(const SelectParams& p, cudaStream_t stream) {
     cfg.attrs = attr;
     cfg.numAttrs = 2;
     switch (p.head_dim) {
-        case 64: return launch_select_d<64>(cfg, p);
-        case 128: return launch_select_d<128>(cfg, p);
-        case 256: return launch_select_d<256>(cfg, p);
+        case 64: return p.wide ? launch_select_d<64, 512>(cfg, p) : launch_select_d<64, 256>(cfg, p);
+        case 128: return p.wide ? launch_select_d<128, 512>(cfg, p) : launch_select_d<128, 256>(cfg, p);
+        case 256: return p.wide ? launch_select_d<256, 512>(cfg, p) : launch_select_d<256, 256>(cfg, p);
         default: return cudaErrorInvalidValue;
     }
 }

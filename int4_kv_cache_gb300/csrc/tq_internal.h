@@ -255,10 +255,11 @@ struct SelectParams {
     int32_t batch, num_kv_heads, group_q, head_dim, max_seq_len;
     int32_t block_shift, blocks_per_seq, exact_stride, n_select, n_first, n_last;
     int32_t ctas;              // CTAs per (sequence, kv head): one cluster, at most 8
+    int32_t wide;              // CTAs of 512 threads, else of 256
 };
 
 // Eviction (evict.cu).
-constexpr int kMaxEvictHeldBytes = 160 * 1024;
+constexpr int kEvStretch = 16384;  // weights a CTA of the selection keeps in registers
 struct EvictParams {
     const float* weights;      // [B][Hkv][weight_stride]
     const int32_t* seq_lens;   // [B]
@@ -269,7 +270,6 @@ struct EvictParams {
     int32_t batch, num_kv_heads, max_seq_len, weight_stride, out_weight_stride;
     int32_t keep, recent;
     int32_t ctas;              // CTAs per (sequence, kv head): one cluster, at most 8
-    int32_t held;              // weights a CTA may hold in shared memory
 };
 struct EvictCopyParams {
     const uint8_t* src_k;
@@ -304,7 +304,7 @@ struct WeightsParams {
 cudaError_t launch_rope(const RopeParams& p, cudaStream_t stream);
 cudaError_t launch_bounds(const BoundsParams& p, cudaStream_t stream);
 cudaError_t launch_select(const SelectParams& p, cudaStream_t stream);
-cudaError_t launch_evict_select(const EvictParams& p, int held_bytes, cudaStream_t stream);
+cudaError_t launch_evict_select(const EvictParams& p, cudaStream_t stream);
 cudaError_t launch_evict_copy(const EvictCopyParams& p, cudaStream_t stream);
 cudaError_t launch_weights(const WeightsParams& p, int head_dim, cudaStream_t stream);
 cudaError_t launch_quantize_append(const AppendParams& p, cudaStream_t stream);

@@ -119,9 +119,16 @@ tq_status run_select(const SelectArgs& a, void* workspace, cudaStream_t stream) 
     p.n_select = a.n_select;
     p.n_first = a.n_first;
     p.n_last = a.n_last;
-    // One tile of 16 blocks for each of a CTA's eight warps, up to eight CTAs
+    // Rows that leave SMs free take CTAs of sixteen warps, as many (up to eight)
+    // as give every warp a tile of 16 blocks while no SM has two; more rows
+    // take one CTA of eight warps each, three of which run on an SM.
+    DeviceFacts* f = nullptr;
+    const tq_status s = device_facts(&f);
+    if (s != TQ_OK) return s;
+    const long long rows = static_cast<long long>(a.batch) * a.hkv;
+    p.wide = rows <= f->sms ? 1 : 0;
     p.ctas = 1;
-    while (p.ctas < 8 && p.exact_stride > 128 * p.ctas) p.ctas *= 2;
+    while (p.ctas < 8 && p.exact_stride > 256 * p.ctas && 2 * rows * p.ctas <= f->sms) p.ctas *= 2;
     cudaError_t e = launch_select(p, stream);
     if (e != cudaSuccess && p.ctas > 1) {  // a cluster the device refused: nothing was queued
         cudaGetLastError();
@@ -332,7 +339,7 @@ tq_status evict(const Store& src, const Store& dst, const float* weights, const 
     if (max_seq_len > src.capacity || keep > dst.capacity) return TQ_ERR_CAPACITY;
     const long long heads = static_cast<long long>(src.batch) * src.num_kv_heads;
     if (heads > 65535) return TQ_ERR_SHAPE;
-    if (!aligned4(weights) || !aligned4(seq_lens) || !aligned4(dst_weights) || !aligned4(dst_lens) || !aligned4(kept))
+    if (!aligned16(weights) || !aligned4(seq_lens) || !aligned4(dst_weights) || !aligned4(dst_lens) || !aligned4(kept))
         return TQ_ERR_ALIGN;
     const unsigned long long in_w = heads * src.capacity * 4ull, out_w = heads * dst.capacity * 4ull,
                              n_kept = heads * keep * 4ull, n_len = src.batch * 4ull;
@@ -370,22 +377,22 @@ tq_status evict(const Store& src, const Store& dst, const float* weights, const 
     p.out_weight_stride = dst.capacity;
     p.keep = keep;
     p.recent = recent;
-    // Up to eight CTAs, each with at least 2,048 weights
+    // As many CTAs (up to eight) as hold the weights in registers, and up to
+    // eight with 2,048 weights or more each while every SM still has at most one
+    DeviceFacts* f = nullptr;
+    tq_status s = device_facts(&f);
+    if (s != TQ_OK) return s;
     p.ctas = 1;
-    while (p.ctas < 8 && max_seq_len > 4096 * p.ctas) p.ctas *= 2;
-    auto launch = [&]() {
-        const long long per = ((static_cast<long long>(max_seq_len) + p.ctas - 1) / p.ctas + 31) & ~31LL;
-        const int bytes = per * 4 <= kMaxEvictHeldBytes ? static_cast<int>(per * 4) : 0;
-        p.held = bytes / 4;
-        return launch_evict_select(p, bytes, stream);
-    };
-    cudaError_t e = launch();
+    while (p.ctas < 8 && (max_seq_len > static_cast<long long>(kEvStretch) * p.ctas ||
+                          (max_seq_len > 4096 * p.ctas && 2 * heads * p.ctas <= f->sms)))
+        p.ctas *= 2;
+    cudaError_t e = launch_evict_select(p, stream);
     if (e != cudaSuccess && p.ctas > 1) {  // a cluster the device refused: nothing was queued
         cudaGetLastError();
         p.ctas = 1;
-        e = launch();
+        e = launch_evict_select(p, stream);
     }
-    tq_status s = cuda_status(e);
+    s = cuda_status(e);
     if (s != TQ_OK) return s;
     EvictCopyParams c{};
     c.src_k = src.k_codes;

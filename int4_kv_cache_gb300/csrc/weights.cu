@@ -25,18 +25,33 @@ constexpr int kWeightThreads = 256;
 constexpr int kWeightWarps = kWeightThreads / 32;
 constexpr int kWeightTokens = 4 * kWeightThreads;
 
-// The merged maximum (log2 units) and sum of one head's parts, by a warp.
+// The merged maximum (log2 units) and sum of one head's parts, by a warp: the
+// first 128 parts (m and l read once, at the same time) in registers.
 __device__ __forceinline__ void merge_parts(const float* m, const float* l, int n, float& M, float& L) {
+    constexpr int H = 4;
     const int lane = threadIdx.x & 31;
+    float mc[H], lc[H];
+#pragma unroll
+    for (int i = 0; i < H; ++i) {
+        const int c = lane + 32 * i;
+        mc[i] = c < n ? __ldcg(m + c) : -INFINITY;
+        lc[i] = c < n ? __ldcg(l + c) : 0.0f;
+    }
     M = -INFINITY;
-    for (int c = lane; c < n; c += 32)
+#pragma unroll
+    for (int i = 0; i < H; ++i)
+        if (lc[i] > 0.0f) M = fmaxf(M, mc[i]);
+    for (int c = lane + 32 * H; c < n; c += 32)
         if (__ldcg(l + c) > 0.0f) M = fmaxf(M, __ldcg(m + c));
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
     L = 0.0f;
-    for (int c = lane; c < n; c += 32) {
-        const float lc = __ldcg(l + c);
-        if (lc > 0.0f) L = fmaf(exp2f(__ldcg(m + c) - M), lc, L);
+#pragma unroll
+    for (int i = 0; i < H; ++i)
+        if (lc[i] > 0.0f) L = fmaf(exp2f(mc[i] - M), lc[i], L);
+    for (int c = lane + 32 * H; c < n; c += 32) {
+        const float x = __ldcg(l + c);
+        if (x > 0.0f) L = fmaf(exp2f(__ldcg(m + c) - M), x, L);
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
@@ -112,33 +127,50 @@ __global__ void __launch_bounds__(kWeightThreads) weights_kernel(const WeightsPa
     const int t0 = (item - bh * p.chunks) * kWeightTokens;
     const int len = min(max(__ldcg(p.seq_lens + b), 0), p.max_seq_len);
     if (t0 >= len) return;
-    if (warp < G) {
-        const long long ph = static_cast<long long>(bh) * G + warp;
-        float M, L;
-        merge_parts(p.part_m + ph * p.n_parts, p.part_l + ph * p.n_parts, p.n_parts, M, L);
+    // The scores are asked for before the heads' parts are merged: neither
+    // waits for the other.
+    constexpr int N = kWeightTokens / kWeightThreads;
+    const float* scores = p.scores + static_cast<long long>(bh) * p.max_seq_len * G;
+    float* weights = p.weights + static_cast<long long>(bh) * p.weight_stride;
+    float x[N][8], old[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        const int t = min(t0 + j * kWeightThreads + static_cast<int>(threadIdx.x), len - 1);
+        const float* s = scores + static_cast<long long>(t) * G;
+        if (G == 8) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float4 v = __ldcg(reinterpret_cast<const float4*>(s) + i);
+                x[j][4 * i] = v.x;
+                x[j][4 * i + 1] = v.y;
+                x[j][4 * i + 2] = v.z;
+                x[j][4 * i + 3] = v.w;
+            }
+        } else {
+#pragma unroll
+            for (int g = 0; g < 8; ++g) x[j][g] = g < G ? __ldcg(s + g) : -INFINITY;
+        }
+        old[j] = p.decay != 0.0f ? __ldcg(weights + t) : 0.0f;
+    }
+    if (warp < 8) {
+        float M = 0.0f, L = 0.0f;
+        if (warp < G) {
+            const long long ph = static_cast<long long>(bh) * G + warp;
+            merge_parts(p.part_m + ph * p.n_parts, p.part_l + ph * p.n_parts, p.n_parts, M, L);
+        }
         if (lane == 0) {
             head_m[warp] = M;
             head_r[warp] = L > 0.0f ? __fdiv_rn(1.0f, L) : 0.0f;
         }
     }
     __syncthreads();
-    const float* scores = p.scores + static_cast<long long>(bh) * p.max_seq_len * G;
-    float* weights = p.weights + static_cast<long long>(bh) * p.weight_stride;
 #pragma unroll
-    for (int j = 0; j < kWeightTokens / kWeightThreads; ++j) {
+    for (int j = 0; j < N; ++j) {
         const int t = t0 + j * kWeightThreads + threadIdx.x;
-        if (t >= len) break;
-        const float* s = scores + static_cast<long long>(t) * G;
         float sum = 0.0f;
-        if (G == 8) {
-            const float4 a = __ldcg(reinterpret_cast<const float4*>(s)), c = __ldcg(reinterpret_cast<const float4*>(s) + 1);
-            const float x[8] = {a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w};
 #pragma unroll
-            for (int g = 0; g < 8; ++g) sum = fmaf(ex2_approx(x[g] - head_m[g]), head_r[g], sum);
-        } else {
-            for (int g = 0; g < G; ++g) sum = fmaf(ex2_approx(__ldcg(s + g) - head_m[g]), head_r[g], sum);
-        }
-        weights[t] = p.decay != 0.0f ? fmaf(p.decay, weights[t], sum) : sum;
+        for (int g = 0; g < 8; ++g) sum = fmaf(ex2_approx(x[j][g] - head_m[g]), head_r[g], sum);
+        if (t < len) weights[t] = p.decay != 0.0f ? fmaf(p.decay, old[j], sum) : sum;
     }
 }
 
