@@ -542,8 +542,8 @@ tq_status tq_paged_kv_block_bounds(const tq_paged_kv_cache* cache, int32_t block
  *   max over the kv head's query heads of  sum_d max(q_d least_d, q_d greatest_d),
  * no q.k of the block exceeds it.  Equal scores: the lowest index first.  The
  * order is that of the exact scores (blocks whose fp32 scores are too close to
- * the border are scored again in fp64, in the workspace).
- * n_first + n_last <= n_select; at most 49,152 blocks (TQ_ERR_UNSUPPORTED).
+ * the border are scored again to 48 bits, in the workspace).
+ * n_first + n_last <= n_select; at most 22,528 blocks (TQ_ERR_UNSUPPORTED).
  * What the bounds of always listed blocks hold does not matter.
  * The bounds are those of a cache of `capacity` tokens.  flags: TQ_ROTATE_K
  * where its keys are stored rotated (TQ_ROTATE_V is ignored).

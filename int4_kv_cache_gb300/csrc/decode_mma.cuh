@@ -328,7 +328,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS, WIDE>::THREADS, Cfg<D, BITS, WIDE
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::STAGES; ++s) {
-            mbar_init(&full_bar[s], 1);
+            mbar_init(&full_bar[s], BLK ? 1 + 32 : 1);  // listed blocks: and each lane's scale copies
             done_cnt[s] = 0;
         }
         fence_mbarrier_init();
@@ -383,34 +383,42 @@ __global__ void __launch_bounds__(Cfg<D, BITS, WIDE>::THREADS, Cfg<D, BITS, WIDE
         return max(0, min(len - tok, seg_rows));
     };
     // Fill stage it % STAGES, by a whole warp: lane kCopies j + c issues copy c
-    // of segment j (code tiles of K, then V, then the four scale and bias
-    // rows), so that the addresses are formed side by side (one lane after the
-    // other, a tile of two segments kept its warp for about 1.5 us).
-    constexpr int kCopies = 2 * C::HALVES + 4;
+    // of segment j (the code tiles of K, then of V), and every lane copies
+    // 16-byte pieces of the scale and bias rows, arriving on the stage's barrier
+    // when they have landed.  (As bulk copies, 256 bytes each and three quarters
+    // of all the copies, they took a warp 1 us a tile to issue.)
+    constexpr int kCopies = 2 * C::HALVES;
+    constexpr int kPieces = C::SB_BYTES / 16;  // of one of the four arrays
+    static_assert(!BLK || kPieces == 16 || kPieces == 32, "a lane's pieces lie in one segment");
     auto issue_blocks = [&](int it, uint64_t policy) {
-        const int stage = it % C::STAGES;
+        const int stage = it % C::STAGES, t0 = t_begin + it * C::T;
         uint8_t* st = smem + stage * C::STAGE_BYTES;
         const int j = lane / kCopies, c = lane - j * kCopies;
         int tok = 0, n = 0;
         long long row = 0;
-        if (j < n_seg) n = segment(t_begin + it * C::T, j, tok, &row);
-        const uint32_t sb_bytes = static_cast<uint32_t>(PAGED ? seg_rows : min(seg_rows, p.capacity - tok)) * NG * 2;
-        const uint32_t bytes = n == 0 ? 0u : (c < 2 * C::HALVES ? static_cast<uint32_t>(seg_rows) * C::ROWB : sb_bytes);
-        const uint32_t total = __reduce_add_sync(0xffffffffu, bytes);
+        if (j < n_seg) n = segment(t0, j, tok, &row);
+        const uint32_t total = __reduce_add_sync(0xffffffffu, n == 0 ? 0u : static_cast<uint32_t>(seg_rows) * C::ROWB);
         if (lane == 0) mbar_arrive_expect_tx(&full_bar[stage], total);
         __syncwarp();
-        if (n == 0) return;
-        if (c < 2 * C::HALVES) {
+        if (n != 0) {
             const int kv = c / C::HALVES, h = c % C::HALVES;
             const int y = C::HALVES == 1 ? static_cast<int>((row * C::BPT) / 128) : static_cast<int>(row);
             tma_load_2d(st + kv * C::CODE_BYTES + h * C::HALF_BYTES + j * seg_rows * C::ROWB, kv ? &tm_v : &tm_k, h * 128, y,
                         &full_bar[stage], policy);
-        } else {
-            const int a = c - 2 * C::HALVES;
-            const uint16_t* src = a == 0 ? p.k_scale : (a == 1 ? p.k_bias : (a == 2 ? p.v_scale : p.v_bias));
-            bulk_load(st + 2 * C::CODE_BYTES + a * C::SB_BYTES + j * seg_rows * NG * 2, src + row * NG, sb_bytes,
-                      &full_bar[stage], policy);
         }
+        const int piece = lane % kPieces, r = piece * (8 / NG);  // its first row within the tile
+        const int js = r / seg_rows, off = r - js * seg_rows;
+        n = segment(t0, js, tok, &row);
+        if (n != 0 && (PAGED || tok + off < p.capacity)) {
+            const uint16_t* arrays[4] = {p.k_scale, p.k_bias, p.v_scale, p.v_bias};
+#pragma unroll
+            for (int i = 0; i < 4; i += 32 / kPieces) {
+                const int a = i + lane / kPieces;  // kPieces = 16: two arrays side by side
+                const uint16_t* src = kPieces == 32 ? arrays[i] : (lane < 16 ? arrays[i] : arrays[(i + 1) & 3]);
+                cp_async16(st + 2 * C::CODE_BYTES + a * C::SB_BYTES + piece * 16, src + (row + off) * NG);
+            }
+        }
+        cp_async_arrive(&full_bar[stage]);
     };
     static_assert(!BLK || kCopies * (C::T / 32) <= 32, "a lane per copy, blocks of 32 tokens or more");
 

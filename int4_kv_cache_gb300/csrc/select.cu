@@ -13,11 +13,13 @@
 //
 // The list must be that of the exact scores, whatever the order of summation:
 // the product's fp32 sums are off by at most kEps * sum |terms|, which a second
-// accumulation over absolute values gives.  With eps the largest such bound of
-// the row and T the R-th largest fp32 score, the exact R-th largest lies within
-// eps of T, so blocks above T + 2 eps are in and those below T - 2 eps are out.
-// What lies between (rarely more than one or two blocks) is scored again in
-// fp64 (fp16 products are exact there) and ranked by that.
+// accumulation over absolute values gives.  With eps twice the largest such
+// bound of the row and T the R-th largest fp32 score, blocks above T + eps are
+// in and those below T - eps are out.  What lies between (rarely more than one
+// or two blocks) is summed again in pairs of fp32 numbers, each step with its
+// exact error (fp16 products are exact in fp32), 48 bits in all, and ranked by
+// that.  (In fp64, whose rate is 1/64 here, the few rows with such blocks took
+// 12 us longer than the others.)
 //
 // One cluster of CTAs per (sequence, kv head): each CTA scores a stretch of
 // blocks and writes the scores into the first CTA's shared memory, which
@@ -43,9 +45,29 @@ __device__ __forceinline__ uint32_t ordered_key(float x) {
 __device__ __forceinline__ float ordered_value(uint32_t k) {
     return __uint_as_float((k & 0x80000000u) != 0u ? (k ^ 0x80000000u) : ~k);
 }
-__device__ __forceinline__ uint64_t ordered_key(double x) {
-    const uint64_t u = static_cast<uint64_t>(__double_as_longlong(x + 0.0));
-    return (u >> 63) != 0u ? ~u : (u | 0x8000000000000000ull);
+
+// A sum held as hi + lo, lo the rounding errors of hi (Knuth's two-sum).
+struct Pair {
+    float hi, lo;
+};
+__device__ __forceinline__ void add(Pair& a, float x, float x_lo) {
+    const float s = __fadd_rn(a.hi, x), t = __fsub_rn(s, a.hi);
+    const float e = __fadd_rn(__fsub_rn(a.hi, __fsub_rn(s, t)), __fsub_rn(x, t));
+    a.lo = __fadd_rn(__fadd_rn(a.lo, x_lo), e);
+    a.hi = s;
+}
+// A key in the order of the sums: hi the sum rounded to fp32, lo the rest.
+__device__ __forceinline__ uint64_t ordered_key(const Pair& a) {
+    const float hi = __fadd_rn(a.hi, a.lo), lo = __fsub_rn(a.lo, __fsub_rn(hi, a.hi));
+    return (static_cast<uint64_t>(ordered_key(hi)) << 32) | ordered_key(lo);
+}
+
+// 1-D bulk copy into shared memory, completion counted in bytes on bar.
+__device__ __forceinline__ void bulk_fetch(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                     smem_u32(dst)),
+                 "l"(src), "r"(bytes), "r"(smem_u32(bar))
+                 : "memory");
 }
 
 // The n-th largest (n >= 1) of the keys visit() hands out, all of them in [lo,
@@ -139,7 +161,7 @@ __device__ __forceinline__ K nth_largest(int n, K lo, K hi, Visit visit, uint32_
 }
 
 template <int D, int THREADS>
-__global__ void __launch_bounds__(THREADS, (D == 256 ? 512 : 768) / THREADS) select_kernel(const SelectParams p) {
+__global__ void __launch_bounds__(THREADS, D == 256 ? 1 : 768 / THREADS) select_kernel(const SelectParams p) {
     constexpr int WARPS = THREADS / 32;
     constexpr int NJ = D / 32;  // 16-byte pieces of a row per lane
     // Every product of 16 terms starts from zero and is added to the sum in
@@ -147,7 +169,11 @@ __global__ void __launch_bounds__(THREADS, (D == 256 ? 512 : 768) / THREADS) sel
     // 2^-24, together below (16 + D / 16) * 2^-23 of the terms' magnitudes
     // (8 * 2^-23 more for the sums that give those magnitudes).
     constexpr float kEps = static_cast<float>(24 + D / 16) * 0x1p-23f;
-    extern __shared__ uint32_t keys[];  // the first CTA's: one per block of the sequence
+    constexpr int kTileBytes = 16 * 4 * D;  // the bounds of 16 blocks
+    extern __shared__ __align__(128) uint8_t dyn[];
+    uint8_t* stage = dyn + (threadIdx.x >> 5) * kTileBytes;              // this warp's tile
+    uint32_t* keys = reinterpret_cast<uint32_t*>(dyn + WARPS * kTileBytes);  // the first CTA's: one per block of the sequence
+    __shared__ uint64_t bar[WARPS];
     // the first CTA's: every warp's largest sum |terms|, least and greatest key
     __shared__ uint32_t warp_abs[8 * WARPS], warp_lo[8 * WARPS], warp_hi[8 * WARPS];
     __shared__ uint32_t hist[2][256];
@@ -168,6 +194,9 @@ __global__ void __launch_bounds__(THREADS, (D == 256 ? 512 : 768) / THREADS) sel
     if (rank == 0) {
         for (int i = threadIdx.x; i < 512; i += THREADS) hist[i >> 8][i & 255] = 0;
     }
+    if (lane == 0) mbar_init(&bar[warp], 1);
+    fence_mbarrier_init();
+    __syncwarp();
     uint4 qraw[NJ];  // this lane's dims 32 j + 8 tig .. + 7 of head gid
     {
         const uint16_t* q = p.q + (static_cast<long long>(bh) * G + (gid < G ? gid : 0)) * D + 8 * tig;
@@ -208,18 +237,30 @@ __global__ void __launch_bounds__(THREADS, (D == 256 ? 512 : 768) / THREADS) sel
         const int tiles = (nb + 15) / 16, per = (tiles + n_cta - 1) / n_cta;
         const int end = min((rank + 1) * per, tiles);
         float most = 0.0f;
-        uint32_t least = 0xffffffffu, greatest = 0u;
+        uint32_t least = 0xffffffffu, greatest = 0u, parity = 0u;
         for (int tile = rank * per + warp; tile < end; tile += WARPS) {
+            const int rows = min(16, nb - tile * 16);
+            if (lane == 0) {
+                const uint32_t bytes = static_cast<uint32_t>(rows) * 4 * D;
+                fence_proxy_async_shared();  // the last tile has been read (by the warp: __syncwarp below)
+                mbar_arrive_expect_tx(&bar[warp], bytes);
+                bulk_fetch(stage, bounds + static_cast<long long>(tile) * 16 * (2 * D), bytes, &bar[warp]);
+            }
             const int r0 = tile * 16 + gid, r1 = r0 + 8;
-            const uint16_t* a0 = bounds + static_cast<long long>(min(r0, nb - 1)) * (2 * D) + 8 * tig;
-            const uint16_t* a1 = bounds + static_cast<long long>(min(r1, nb - 1)) * (2 * D) + 8 * tig;
+            const uint8_t* a0 = stage + min(gid, rows - 1) * (4 * D) + 16 * tig;
+            const uint8_t* a1 = stage + min(gid + 8, rows - 1) * (4 * D) + 16 * tig;
             float s[4] = {0.0f, 0.0f, 0.0f, 0.0f}, up[4] = {0.0f, 0.0f, 0.0f, 0.0f}, un[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            if (!mbar_wait_bounded(&bar[warp], parity)) {
+                if (p.status != nullptr) atomicOr(p.status, TQ_DEV_TIMEOUT);
+                break;
+            }
+            parity ^= 1u;
 #pragma unroll
             for (int j = 0; j < NJ; ++j) {
-                const uint4 l0 = __ldcg(reinterpret_cast<const uint4*>(a0 + 32 * j));
-                const uint4 l1 = __ldcg(reinterpret_cast<const uint4*>(a1 + 32 * j));
-                const uint4 h0 = __ldcg(reinterpret_cast<const uint4*>(a0 + D + 32 * j));
-                const uint4 h1 = __ldcg(reinterpret_cast<const uint4*>(a1 + D + 32 * j));
+                const uint4 l0 = *reinterpret_cast<const uint4*>(a0 + 64 * j);
+                const uint4 l1 = *reinterpret_cast<const uint4*>(a1 + 64 * j);
+                const uint4 h0 = *reinterpret_cast<const uint4*>(a0 + 2 * D + 64 * j);
+                const uint4 h1 = *reinterpret_cast<const uint4*>(a1 + 2 * D + 64 * j);
                 constexpr uint32_t A = 0x7fff7fffu;  // absolute values
                 float f[4][4] = {};
                 mma_16816(f[0], h0.x, h1.x, h0.y, h1.y, qp[j].x, qp[j].y);
@@ -255,6 +296,7 @@ __global__ void __launch_bounds__(THREADS, (D == 256 ? 512 : 768) / THREADS) sel
                     greatest = max(greatest, k);
                 }
             }
+            __syncwarp();
         }
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, off));
@@ -348,7 +390,7 @@ __global__ void __launch_bounds__(THREADS, (D == 256 ? 512 : 768) / THREADS) sel
         return;
     }
     // ---- exact scores of the open blocks, a warp each, and their rank
-    double* exact = p.exact + static_cast<long long>(bh) * p.exact_stride;
+    uint64_t* exact = p.exact + static_cast<long long>(bh) * p.exact_stride;
     uint64_t ex_lo = ~0ull, ex_hi = 0ull;
     for (int i0 = c0 + warp * 32; i0 < c1; i0 += THREADS) {
         uint32_t todo = __ballot_sync(0xffffffffu, i0 + lane < c1 && is_open(i0 + lane));
@@ -362,25 +404,28 @@ __global__ void __launch_bounds__(THREADS, (D == 256 ? 512 : 768) / THREADS) sel
                 lo[j] = __half2float(__ushort_as_half(__ldcg(row + 32 * j + lane)));
                 hi[j] = __half2float(__ushort_as_half(__ldcg(row + D + 32 * j + lane)));
             }
-            double best = -INFINITY;
+            uint64_t best = 0;
 #pragma unroll
             for (int g = 0; g < 8; ++g) {
                 if (g >= G) break;
                 const uint16_t* q = p.q + (static_cast<long long>(bh) * G + g) * D + lane;
-                double sum = 0.0;
+                Pair sum = {0.0f, 0.0f};
 #pragma unroll
                 for (int j = 0; j < NJ; ++j) {
                     const float x = __half2float(__ushort_as_half(__ldcg(q + 32 * j)));
-                    sum = fma(static_cast<double>(x), static_cast<double>(x > 0.0f ? hi[j] : lo[j]), sum);
+                    add(sum, __fmul_rn(x, x > 0.0f ? hi[j] : lo[j]), 0.0f);
                 }
 #pragma unroll
-                for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-                best = sum > best ? sum : best;
+                for (int off = 16; off > 0; off >>= 1) {
+                    const float oh = __shfl_xor_sync(0xffffffffu, sum.hi, off), ol = __shfl_xor_sync(0xffffffffu, sum.lo, off);
+                    add(sum, oh, ol);
+                }
+                const uint64_t k = ordered_key(sum);
+                best = k > best ? k : best;
             }
             if (lane == 0) exact[blk] = best;
-            const uint64_t k = ordered_key(best);
-            ex_lo = k < ex_lo ? k : ex_lo;
-            ex_hi = k > ex_hi ? k : ex_hi;
+            ex_lo = best < ex_lo ? best : ex_lo;
+            ex_hi = best > ex_hi ? best : ex_hi;
         }
     }
     if (lane == 0) {
@@ -399,11 +444,11 @@ __global__ void __launch_bounds__(THREADS, (D == 256 ? 512 : 768) / THREADS) sel
         R - n_in, ex_lo, ex_hi,
         [&](auto f) {
             for (int i = c0 + threadIdx.x; i < c1; i += THREADS)
-                if (is_open(i)) f(ordered_key(exact[i]));
+                if (is_open(i)) f(exact[i]);
         },
         hist, over);
-    auto beats = [&](int i) { return is_in(i) || (is_open(i) && ordered_key(exact[i]) > border); };
-    auto ties = [&](int i) { return is_open(i) && ordered_key(exact[i]) == border; };
+    auto beats = [&](int i) { return is_in(i) || (is_open(i) && exact[i] > border); };
+    auto ties = [&](int i) { return is_open(i) && exact[i] == border; };
     count(beats, ties);
     __syncthreads();
     int before_tie, n_tie;
@@ -419,11 +464,13 @@ cudaError_t launch_select_d(cudaLaunchConfig_t& cfg, const SelectParams& p) {
     if (dev < 0 || dev >= 64 || !done[dev].load(std::memory_order_acquire)) {
         const cudaError_t e =
             cudaFuncSetAttribute(select_kernel<D, THREADS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 kMaxSelectBlocks * static_cast<int>(sizeof(uint32_t)));
+                                 kSelectStageBytes + kMaxSelectBlocks * static_cast<int>(sizeof(uint32_t)));
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) done[dev].store(true, std::memory_order_release);
     }
+    static_assert(THREADS / 32 * 64 * D <= kSelectStageBytes, "the warps' tiles");
     cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes += static_cast<size_t>(THREADS / 32) * 64 * D;
     return cudaLaunchKernelEx(&cfg, select_kernel<D, THREADS>, p);
 }
 
@@ -447,7 +494,7 @@ cudaError_t launch_select(const SelectParams& p, cudaStream_t stream) {
     switch (p.head_dim) {
         case 64: return p.wide ? launch_select_d<64, 512>(cfg, p) : launch_select_d<64, 256>(cfg, p);
         case 128: return p.wide ? launch_select_d<128, 512>(cfg, p) : launch_select_d<128, 256>(cfg, p);
-        case 256: return p.wide ? launch_select_d<256, 512>(cfg, p) : launch_select_d<256, 256>(cfg, p);
+        case 256: return launch_select_d<256, 256>(cfg, p);  // 16 KB a warp
         default: return cudaErrorInvalidValue;
     }
 }

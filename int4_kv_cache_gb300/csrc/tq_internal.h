@@ -244,13 +244,14 @@ struct BoundsParams {
 };
 
 // Block selection (select.cu).
-constexpr int kMaxSelectBlocks = 49152;  // blocks of a sequence (192 KB of scores)
+constexpr int kMaxSelectBlocks = 22528;        // blocks of a sequence (88 KB of scores)
+constexpr int kSelectStageBytes = 128 * 1024;  // the warps' tiles of bounds at most
 struct SelectParams {
     const uint16_t* bounds;    // [B][Hkv][blocks_per_seq][2][D]
     const uint16_t* q;         // [B][Hq][D]
     const int32_t* seq_lens;   // [B]
     int32_t* blocks;           // [B][Hkv][n_select]
-    double* exact;             // [B][Hkv][exact_stride] scratch
+    uint64_t* exact;           // [B][Hkv][exact_stride] scratch
     int32_t* status;
     int32_t batch, num_kv_heads, group_q, head_dim, max_seq_len;
     int32_t block_shift, blocks_per_seq, exact_stride, n_select, n_first, n_last;

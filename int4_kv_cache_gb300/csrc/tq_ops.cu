@@ -78,18 +78,18 @@ tq_status check_select(const SelectArgs& a) {
     return TQ_OK;
 }
 
-// The workspace of a selection: the fp64 scores of blocks near the border and
+// The workspace of a selection: the exact scores of blocks near the border and
 // the rotated query.
 size_t select_bytes(int32_t batch, int32_t hq, int32_t hkv, int32_t head_dim, int32_t max_seq_len, int32_t block_tokens) {
     const size_t nb = static_cast<size_t>(ceil_div(max_seq_len, block_tokens));
-    return align256(static_cast<size_t>(batch) * hkv * nb * sizeof(double)) +
+    return align256(static_cast<size_t>(batch) * hkv * nb * sizeof(uint64_t)) +
            align256(static_cast<size_t>(batch) * hq * head_dim * sizeof(uint16_t));
 }
 
 uint16_t* rotated_query(const SelectArgs& a, void* workspace) {
     const size_t nb = static_cast<size_t>(ceil_div(a.max_seq_len, a.block_tokens));
     return reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(workspace) +
-                                       align256(static_cast<size_t>(a.batch) * a.hkv * nb * sizeof(double)));
+                                       align256(static_cast<size_t>(a.batch) * a.hkv * nb * sizeof(uint64_t)));
 }
 
 tq_status rotate_query(SelectArgs& a, void* workspace, cudaStream_t stream) {
@@ -106,7 +106,7 @@ tq_status run_select(const SelectArgs& a, void* workspace, cudaStream_t stream) 
     p.q = a.q;
     p.seq_lens = a.seq_lens;
     p.blocks = a.blocks;
-    p.exact = static_cast<double*>(workspace);
+    p.exact = static_cast<uint64_t*>(workspace);
     p.status = a.status;
     p.batch = a.batch;
     p.num_kv_heads = a.hkv;
@@ -119,16 +119,18 @@ tq_status run_select(const SelectArgs& a, void* workspace, cudaStream_t stream) 
     p.n_select = a.n_select;
     p.n_first = a.n_first;
     p.n_last = a.n_last;
-    // Rows that leave SMs free take CTAs of sixteen warps, as many (up to eight)
-    // as give every warp a tile of 16 blocks while no SM has two; more rows
-    // take one CTA of eight warps each, three of which run on an SM.
+    // Rows that leave SMs free take CTAs of sixteen warps (eight at head_dim
+    // 256, whose tiles are larger), as many (up to eight) as give every warp a
+    // tile of 16 blocks while no SM has two; more rows take one CTA of eight
+    // warps each, three of which run on an SM.
     DeviceFacts* f = nullptr;
     const tq_status s = device_facts(&f);
     if (s != TQ_OK) return s;
     const long long rows = static_cast<long long>(a.batch) * a.hkv;
     p.wide = rows <= f->sms ? 1 : 0;
     p.ctas = 1;
-    while (p.ctas < 8 && p.exact_stride > 256 * p.ctas && 2 * rows * p.ctas <= f->sms) p.ctas *= 2;
+    const int each = a.head_dim == 256 ? 128 : 256;
+    while (p.ctas < 8 && p.exact_stride > each * p.ctas && 2 * rows * p.ctas <= f->sms) p.ctas *= 2;
     cudaError_t e = launch_select(p, stream);
     if (e != cudaSuccess && p.ctas > 1) {  // a cluster the device refused: nothing was queued
         cudaGetLastError();

@@ -103,7 +103,7 @@ def select(L, **kw):
     (dict(B=0), SHAPE), (dict(hq=30), SHAPE), (dict(n=0), SHAPE), (dict(first=-1), SHAPE), (dict(last=-1), SHAPE),
     (dict(first=9, last=8), SHAPE), (dict(first=2 ** 31 - 1, last=2 ** 31 - 1), SHAPE), (dict(max_len=0), SHAPE),
     (dict(hq=36), UNSUPPORTED), (dict(d=96), UNSUPPORTED), (dict(block=256), UNSUPPORTED), (dict(flags=4), UNSUPPORTED),
-    (dict(cap=1 << 22, max_len=32 * 49152 + 1, block=32), UNSUPPORTED),
+    (dict(cap=1 << 22, max_len=32 * 22528 + 1, block=32), UNSUPPORTED),
     (dict(max_len=4097), CAPACITY), (dict(ws=None), WORKSPACE), (dict(nbytes=100), WORKSPACE),
     (dict(bounds=addr(2, 2)), ALIGN), (dict(q=addr(3, 2)), ALIGN), (dict(ws=addr(5, 16)), ALIGN), (dict(blocks=addr(6, 2)), ALIGN),
 ])
@@ -136,7 +136,7 @@ def test_sparse_refusals(L, fused, layout, kw, want):
 
 def test_sparse_workspace_bytes(L):
     n = L.tq_sparse_workspace_bytes(1, 64, 8, 128, 131072, 64, 64)
-    # the fp64 scores of every block, the rotated query, the decode's workspace over the listed rows
+    # the exact scores of every block, 8 bytes each, the rotated query, the decode's workspace over the listed rows
     assert n == 8 * 2048 * 8 + 64 * 128 * 2 + tq.tq_sdpa_workspace_bytes(1, 64, 8, 128, 64 * 64)
     for bad in ((0, 64, 8, 128, 4096, 8, 64), (1, 64, 8, 96, 4096, 8, 64), (1, 64, 8, 128, 0, 8, 64), (1, 64, 8, 128, 4096, 0, 64),
                 (1, 64, 8, 128, 4096, 8, 65), (1, 64, 8, 128, 4096, 1 << 24, 128)):
