@@ -211,9 +211,9 @@ constexpr int kOutParts = 0, kOutDirect = 1, kOutCluster = 2;
 //  kModeDense   all rows below seq_lens[b] (the decode);
 //  kModeBlocks  the rows of the blocks listed for this (sequence, kv head).
 //               The runs cut the list as if its blocks stood one after the
-//               other; a tile is filled by one copy per block (or part of a
-//               block longer than a tile), and rows are masked block by block,
-//               so the list may hold partial, empty and repeated blocks;
+//               other; each warp fetches the rows of the tile that it uses
+//               itself and masks them by their block, so the list may hold
+//               partial, empty and repeated blocks;
 //  kModeScores  kModeDense that also writes every scaled score (log2 units) to
 //               p.scores [B][Hkv][max_seq_len][group], and its part_m in log2
 //               units (a rounding less for who turns the scores into weights).
@@ -328,7 +328,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS, WIDE>::THREADS, Cfg<D, BITS, WIDE
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::STAGES; ++s) {
-            mbar_init(&full_bar[s], BLK ? 1 + 32 : 1);  // listed blocks: and each lane's scale copies
+            mbar_init(&full_bar[s], 1);
             done_cnt[s] = 0;
         }
         fence_mbarrier_init();
@@ -366,61 +366,50 @@ __global__ void __launch_bounds__(Cfg<D, BITS, WIDE>::THREADS, Cfg<D, BITS, WIDE
         return lo < min(t0 + C::T, t_end) && hi > t0;
     };
 
-    // Listed blocks: a tile is kSeg segments of seg_rows rows, each inside one
-    // block.  Segment j of the tile at t0: its first token, and how many of its
-    // rows lie below len (0: no block there).
-    const int seg_rows = BLK ? min(C::T, p.block_tokens) : C::T;
-    const int n_seg = BLK ? C::T / seg_rows : 1;
-    auto segment = [&](int t0, int j, int& tok, long long* row = nullptr) -> int {
-        const int v = t0 + j * seg_rows;
+    // Listed blocks.  A warp uses the same kWarpRows rows of a tile for the
+    // scores and for P.V, and they lie in one block (blocks hold 32 tokens or
+    // more), so each warp fetches its own rows, 16 bytes a lane, STAGES - 1
+    // tiles ahead and waits for nobody else's.  (One warp issuing TMA copies
+    // for the CTA took 0.9 us a tile.)  warp_rows: where the rows of tile it
+    // begin, and how many of them lie below len (0: no block there).
+    constexpr int kWarpRows = C::MT * 16;
+    auto warp_rows = [&](int it, long long& row) -> int {
+        const int v = t_begin + it * C::T + warp * kWarpRows;
         if (v >= t_end) return 0;
         const int e = v >> p.block_shift, w = e - first_page;
         const int blk = w < n_win ? page_s[w] : listed_block(__ldcg(list + e));
         if (blk < 0) return 0;
         const int off = v & (p.block_tokens - 1);
-        tok = (blk << p.block_shift) + off;
-        if (row != nullptr) *row = (w < n_win ? static_cast<long long>(blk_row[w]) << 4 : block_row(blk)) + off;
-        return max(0, min(len - tok, seg_rows));
+        row = (w < n_win ? static_cast<long long>(blk_row[w]) << 4 : block_row(blk)) + off;
+        return max(0, min(len - ((blk << p.block_shift) + off), kWarpRows));
     };
-    // Fill stage it % STAGES, by a whole warp: lane kCopies j + c issues copy c
-    // of segment j (the code tiles of K, then of V), and every lane copies
-    // 16-byte pieces of the scale and bias rows, arriving on the stage's barrier
-    // when they have landed.  (As bulk copies, 256 bytes each and three quarters
-    // of all the copies, they took a warp 1 us a tile to issue.)
-    constexpr int kCopies = 2 * C::HALVES;
-    constexpr int kPieces = C::SB_BYTES / 16;  // of one of the four arrays
-    static_assert(!BLK || kPieces == 16 || kPieces == 32, "a lane's pieces lie in one segment");
-    auto issue_blocks = [&](int it, uint64_t policy) {
-        const int stage = it % C::STAGES, t0 = t_begin + it * C::T;
-        uint8_t* st = smem + stage * C::STAGE_BYTES;
-        const int j = lane / kCopies, c = lane - j * kCopies;
-        int tok = 0, n = 0;
+    auto fetch_rows = [&](int it) {
         long long row = 0;
-        if (j < n_seg) n = segment(t0, j, tok, &row);
-        const uint32_t total = __reduce_add_sync(0xffffffffu, n == 0 ? 0u : static_cast<uint32_t>(seg_rows) * C::ROWB);
-        if (lane == 0) mbar_arrive_expect_tx(&full_bar[stage], total);
-        __syncwarp();
-        if (n != 0) {
-            const int kv = c / C::HALVES, h = c % C::HALVES;
-            const int y = C::HALVES == 1 ? static_cast<int>((row * C::BPT) / 128) : static_cast<int>(row);
-            tma_load_2d(st + kv * C::CODE_BYTES + h * C::HALF_BYTES + j * seg_rows * C::ROWB, kv ? &tm_v : &tm_k, h * 128, y,
-                        &full_bar[stage], policy);
-        }
-        const int piece = lane % kPieces, r = piece * (8 / NG);  // its first row within the tile
-        const int js = r / seg_rows, off = r - js * seg_rows;
-        n = segment(t0, js, tok, &row);
-        if (n != 0 && (PAGED || tok + off < p.capacity)) {
-            const uint16_t* arrays[4] = {p.k_scale, p.k_bias, p.v_scale, p.v_bias};
+        const int n = it < n_tiles ? warp_rows(it, row) : 0;
+        if (n > 0) {
+            uint8_t* st = smem + (it % C::STAGES) * C::STAGE_BYTES;
+            const int tb = warp * kWarpRows;
+            constexpr int kPieces = kWarpRows * C::SPT;  // 16-byte pieces of the codes of K or V
 #pragma unroll
-            for (int i = 0; i < 4; i += 32 / kPieces) {
-                const int a = i + lane / kPieces;  // kPieces = 16: two arrays side by side
-                const uint16_t* src = kPieces == 32 ? arrays[i] : (lane < 16 ? arrays[i] : arrays[(i + 1) & 3]);
-                cp_async16(st + 2 * C::CODE_BYTES + a * C::SB_BYTES + piece * 16, src + (row + off) * NG);
+            for (int i = 0; i < kPieces; i += 32) {
+                const int t = (i + lane) / C::SPT, s = (i + lane) % C::SPT;
+                if (t < n) {
+                    const uint32_t at = code_addr<C>(0u, tb + t, s);
+                    const long long from = (row + t) * C::BPT + s * 16;
+                    cp_async16(st + at, p.k_codes + from);
+                    cp_async16(st + C::CODE_BYTES + at, p.v_codes + from);
+                }
+            }
+            constexpr int kSbPieces = kWarpRows * NG / 8;  // of each scale or bias array
+            const int a = lane / kSbPieces, s = lane % kSbPieces;
+            if (a < 4 && s * (8 / NG) < n) {
+                const uint16_t* src = a < 2 ? (a == 0 ? p.k_scale : p.k_bias) : (a == 2 ? p.v_scale : p.v_bias);
+                cp_async16(st + 2 * C::CODE_BYTES + a * C::SB_BYTES + tb * NG * 2 + s * 16, src + row * NG + s * 8);
             }
         }
-        cp_async_arrive(&full_bar[stage]);
+        cp_async_commit();
     };
-    static_assert(!BLK || kCopies * (C::T / 32) <= 32, "a lane per copy, blocks of 32 tokens or more");
+    static_assert(!BLK || 4 * kWarpRows * NG / 8 <= 32, "a lane per piece of the scales");
 
     // Fill stage it % STAGES with tile it: both code tiles by TMA, the four
     // scale/bias rows by bulk copies; completion counted in bytes on full_bar.
@@ -490,10 +479,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS, WIDE>::THREADS, Cfg<D, BITS, WIDE
     if (static_cast<int>(threadIdx.x >> 3) < app_tasks)
         app_raw = __ldcs(reinterpret_cast<const uint4*>(app_src(threadIdx.x >> 3)));
     if constexpr (BLK) {
-        if (warp == 0 && n_tiles > 0) {
-            const uint64_t policy = policy_evict_first();
-            for (int it = 0; it < min(n_tiles, C::STAGES); ++it) issue_blocks(it, policy);
-        }
+        for (int it = 0; it < C::STAGES - 1; ++it) fetch_rows(it);
     } else if (threadIdx.x == 0 && n_tiles > 0) {
         prefetch_tensormap(&tm_k);
         prefetch_tensormap(&tm_v);
@@ -701,7 +687,16 @@ __global__ void __launch_bounds__(Cfg<D, BITS, WIDE>::THREADS, Cfg<D, BITS, WIDE
 
     for (int it = 0; it < n_tiles; ++it) {
         const int stage = it % C::STAGES;
-        if (!mbar_wait_bounded(&full_bar[stage], (it / C::STAGES) & 1)) {
+        int blk_n = 0;  // listed blocks: this warp's rows of the tile that count
+        if constexpr (BLK) {
+            __syncwarp();  // the stage fetched into next has been read by every lane
+            fetch_rows(it + C::STAGES - 1);
+            cp_async_wait<C::STAGES - 1>();
+            __syncwarp();
+            long long row = 0;
+            blk_n = warp_rows(it, row);
+            if (blk_n == 0) continue;  // the same for the warp
+        } else if (!mbar_wait_bounded(&full_bar[stage], (it / C::STAGES) & 1)) {
             // the fill never completed: report, stop consuming (no further
             // refills are issued, so the other warps give up the same way)
             if (p.status) atomicOr(p.status, TQ_DEV_TIMEOUT);
@@ -721,8 +716,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS, WIDE>::THREADS, Cfg<D, BITS, WIDE
         // whether row r of the m-tile at tb counts
         auto counts = [&](int tb, int r) -> bool {
             if constexpr (BLK) {
-                int tok = 0;
-                return r < segment(t0, tb / seg_rows, tok) - (tb & (seg_rows - 1));
+                return tb - warp * kWarpRows + r < blk_n;
             } else {
                 return t0 + tb + r < t_end;
             }
@@ -937,14 +931,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS, WIDE>::THREADS, Cfg<D, BITS, WIDE
                 }
             }
         };
-        bool whole = t0 + C::T <= t_end;
-        if constexpr (BLK) {
-            for (int j = 0; j < n_seg; ++j) {
-                int tok = 0;
-                whole &= segment(t0, j, tok) == seg_rows;
-            }
-        }
-        if (whole) stage_body(std::false_type{});
+        if (BLK ? blk_n == kWarpRows : t0 + C::T <= t_end) stage_body(std::false_type{});
         else stage_body(std::true_type{});
 
         // Release the stage.  The last warp to finish it refills it with tile
@@ -952,20 +939,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS, WIDE>::THREADS, Cfg<D, BITS, WIDE
         // visible by their fences before the counter update) before the
         // asynchronous copies that overwrite it.
         __syncwarp();
-        if constexpr (BLK) {
-            unsigned int before = 0;
-            if (lane == 0) {
-                __threadfence_block();
-                before = atomicAdd(&done_cnt[stage], 1u);
-                __threadfence_block();
-            }
-            before = __shfl_sync(0xffffffffu, before, 0);
-            if (before % C::NWC == C::NWC - 1 && it + C::STAGES < n_tiles) {
-                __syncwarp();
-                fence_proxy_async_shared();
-                issue_blocks(it + C::STAGES, policy_evict_first());
-            }
-        } else if (lane == 0) {
+        if (!BLK && lane == 0) {
             __threadfence_block();
             const unsigned int before = atomicAdd(&done_cnt[stage], 1u);
             if (before % C::NWC == C::NWC - 1 && it + C::STAGES < n_tiles) {
@@ -1059,7 +1033,79 @@ __global__ void __launch_bounds__(Cfg<D, BITS, WIDE>::THREADS, Cfg<D, BITS, WIDE
     }
     __syncthreads();
     const float ln2 = 0.69314718055994531f;
-    for (int idx = threadIdx.x; idx < G * D; idx += C::NWC * 32) {
+    if constexpr (BLK) {
+        // The warps' weights for each head once, then four elements a thread
+        // with 16-byte loads and stores (element by element, each forming the
+        // weights again, this end of a CTA took 1.6 us).
+        __shared__ float wt_s[C::NWC][8], l_s[8];
+        if (threadIdx.x < 8) {
+            const int h = threadIdx.x;
+            float M = -INFINITY, L = 0.0f;
+#pragma unroll
+            for (int w = 0; w < C::NWC; ++w) M = fmaxf(M, mrg_t[w][h]);
+#pragma unroll
+            for (int w = 0; w < C::NWC; ++w) {
+                const float wt = mrg_m[w][h] == -INFINITY ? 0.0f : ex2_approx(mrg_m[w][h] - M);
+                wt_s[w][h] = wt;
+                L = fmaf(wt, mrg_l[w][h], L);
+            }
+            l_s[h] = L;
+            if constexpr (OUT == kOutCluster) {
+                cl_m[h] = M == -INFINITY ? -INFINITY : M * ln2;
+                cl_l[h] = L;
+            } else if constexpr (OUT == kOutParts) {
+                const long long ph = (static_cast<long long>(b) * p.num_q_heads + kvh * G + h) * p.n_splits + split;
+                if (h < G) {
+                    p.part_m[ph] = M == -INFINITY ? -INFINITY : M * ln2;
+                    p.part_l[ph] = L;
+                }
+            }
+        }
+        __syncthreads();
+        for (int idx = threadIdx.x * 4; idx < G * D; idx += C::THREADS * 4) {
+            const int h = idx / D, d = idx % D, x = merge_xor<BITS>(h >> 1 & 3);
+            float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int w = 0; w < C::NWC; ++w) {
+                const float4 a = *reinterpret_cast<const float4*>(mrg_acc + (w * 8 + h) * D + (d ^ (x & ~3)));
+                const float wt = wt_s[w][h];
+                v[0] = fmaf(wt, a.x, v[0]);
+                v[1] = fmaf(wt, a.y, v[1]);
+                v[2] = fmaf(wt, a.z, v[2]);
+                v[3] = fmaf(wt, a.w, v[3]);
+            }
+            if ((x & 1) != 0) {  // element d + i sits at d + (i ^ x)
+                const float s0 = v[0], s2 = v[2];
+                v[0] = v[1];
+                v[1] = s0;
+                v[2] = v[3];
+                v[3] = s2;
+            }
+            if ((x & 2) != 0) {
+                const float s0 = v[0], s1 = v[1];
+                v[0] = v[2];
+                v[1] = v[3];
+                v[2] = s0;
+                v[3] = s1;
+            }
+            const long long ph = (static_cast<long long>(b) * p.num_q_heads + kvh * G + h) * p.n_splits + split;
+            if constexpr (OUT == kOutDirect) {
+                const float L = l_s[h];
+                uint2 o;
+                o.x = pack_half2(L > 0.0f ? __fdiv_rn(v[0], L) : 0.0f, L > 0.0f ? __fdiv_rn(v[1], L) : 0.0f);
+                o.y = pack_half2(L > 0.0f ? __fdiv_rn(v[2], L) : 0.0f, L > 0.0f ? __fdiv_rn(v[3], L) : 0.0f);
+                uint16_t* to = p.out + ph * D + d;  // out: any 2-byte alignment
+                to[0] = static_cast<uint16_t>(o.x);
+                to[1] = static_cast<uint16_t>(o.x >> 16);
+                to[2] = static_cast<uint16_t>(o.y);
+                to[3] = static_cast<uint16_t>(o.y >> 16);
+            } else {
+                float* to = OUT == kOutCluster ? cl_acc + h * D + d : p.part_acc + ph * D + d;
+                *reinterpret_cast<float4*>(to) = make_float4(v[0], v[1], v[2], v[3]);
+            }
+        }
+    }
+    for (int idx = threadIdx.x; !BLK && idx < G * D; idx += C::NWC * 32) {
         const int h = idx / D, d = idx % D;
         float M = -INFINITY;
 #pragma unroll

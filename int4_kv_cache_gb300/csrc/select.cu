@@ -71,13 +71,13 @@ __device__ __forceinline__ void bulk_fetch(void* dst, const void* src, uint32_t 
 }
 
 // The n-th largest (n >= 1) of the keys visit() hands out, all of them in [lo,
-// hi], by digits of eight bits from the highest in which lo and hi differ, until
-// kFew keys or fewer share the digits so far; those are gathered and ranked
-// directly.  `above`: how many keys are larger.  Every thread of the CTA calls
+// hi] and `count` in number, by digits of eight bits from the highest in which
+// lo and hi differ, until kFew keys or fewer share the digits so far; those are
+// gathered and ranked directly.  `above`: how many keys are larger.  Every thread of the CTA calls
 // with hist zeroed (both halves) a barrier ago; visit(f) calls f(key) for this
 // thread's keys.
 template <int THREADS, typename K, typename Visit>
-__device__ __forceinline__ K nth_largest(int n, K lo, K hi, Visit visit, uint32_t (*hist)[256], int& above) {
+__device__ __forceinline__ K nth_largest(int n, int count, K lo, K hi, Visit visit, uint32_t (*hist)[256], int& above) {
     __shared__ K few[kFew];
     __shared__ int n_few;
     const int lane = threadIdx.x & 31;
@@ -90,6 +90,30 @@ __device__ __forceinline__ K nth_largest(int n, K lo, K hi, Visit visit, uint32_
     K mask = bits == static_cast<int>(sizeof(K) * 8) ? 0 : ones << bits;
     K value = hi & mask;
     if (threadIdx.x == 0) n_few = 0;
+    __syncthreads();
+    auto rank_few = [&]() -> K {  // of the keys that share the digits so far
+        visit([&](K k) {
+            if ((k & mask) == value) {
+                const int at = atomicAdd(&n_few, 1);
+                if (at < kFew) few[at] = k;
+            }
+        });
+        __syncthreads();
+        const int m = min(n_few, kFew);
+        const K mine = lane < m ? few[lane] : 0;
+        int greater = 0, equal = 0;
+        for (int j = 0; j < m; ++j) {
+            const K o = __shfl_sync(0xffffffffu, mine, j);
+            greater += o > mine ? 1 : 0;
+            equal += o == mine ? 1 : 0;
+        }
+        const int need = n - above;
+        const uint32_t it = __ballot_sync(0xffffffffu, lane < m && greater < need && need <= greater + equal);
+        const int at = it != 0 ? __ffs(it) - 1 : 0;
+        above += __shfl_sync(0xffffffffu, greater, at);
+        return __shfl_sync(0xffffffffu, mine, at);
+    };
+    if (bits > 0 && count <= kFew) return rank_few();
     for (int pass = 0; bits > 0; ++pass) {
         const int take = bits < 8 ? bits : 8, shift = bits - take, h = pass & 1;
         visit([&](K k) {
@@ -133,28 +157,7 @@ __device__ __forceinline__ K nth_largest(int n, K lo, K hi, Visit visit, uint32_
         value |= static_cast<K>(bin) << shift;
         bits = shift;
         mask = shift == 0 ? ones : ones << shift;
-        if (bits > 0 && here <= kFew) {  // the same for the CTA
-            visit([&](K k) {
-                if ((k & mask) == value) {
-                    const int at = atomicAdd(&n_few, 1);
-                    if (at < kFew) few[at] = k;
-                }
-            });
-            __syncthreads();
-            const int m = min(n_few, kFew);
-            const K mine_k = lane < m ? few[lane] : 0;
-            int greater = 0, equal = 0;
-            for (int j = 0; j < m; ++j) {
-                const K o = __shfl_sync(0xffffffffu, mine_k, j);
-                greater += o > mine_k ? 1 : 0;
-                equal += o == mine_k ? 1 : 0;
-            }
-            const int need = n - above;
-            const uint32_t it = __ballot_sync(0xffffffffu, lane < m && greater < need && need <= greater + equal);
-            const int at = it != 0 ? __ffs(it) - 1 : 0;
-            above += __shfl_sync(0xffffffffu, greater, at);
-            return __shfl_sync(0xffffffffu, mine_k, at);
-        }
+        if (bits > 0 && here <= kFew) return rank_few();  // the same for the CTA
         __syncthreads();  // the other half is zero, this one has been read
     }
     return value;
@@ -174,6 +177,7 @@ __global__ void __launch_bounds__(THREADS, D == 256 ? 1 : 768 / THREADS) select_
     uint8_t* stage = dyn + (threadIdx.x >> 5) * kTileBytes;              // this warp's tile
     uint32_t* keys = reinterpret_cast<uint32_t*>(dyn + WARPS * kTileBytes);  // the first CTA's: one per block of the sequence
     __shared__ uint64_t bar[WARPS];
+    __shared__ __align__(16) uint16_t q_s[8 * D];  // the first CTA's: the group's query heads
     // the first CTA's: every warp's largest sum |terms|, least and greatest key
     __shared__ uint32_t warp_abs[8 * WARPS], warp_lo[8 * WARPS], warp_hi[8 * WARPS];
     __shared__ uint32_t hist[2][256];
@@ -202,6 +206,10 @@ __global__ void __launch_bounds__(THREADS, D == 256 ? 1 : 768 / THREADS) select_
         const uint16_t* q = p.q + (static_cast<long long>(bh) * G + (gid < G ? gid : 0)) * D + 8 * tig;
 #pragma unroll
         for (int j = 0; j < NJ; ++j) qraw[j] = __ldcg(reinterpret_cast<const uint4*>(q + 32 * j));
+    }
+    if (rank == 0 && warp == 0 && gid < G) {
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) *reinterpret_cast<uint4*>(q_s + gid * D + 32 * j + 8 * tig) = qraw[j];
     }
     if (n_cta > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
     if (len < 0 || len > p.max_seq_len) {
@@ -331,7 +339,7 @@ __global__ void __launch_bounds__(THREADS, D == 256 ? 1 : 768 / THREADS) select_
     key_hi = __reduce_max_sync(0xffffffffu, key_hi);
     int above;
     const uint32_t tau = nth_largest<THREADS, uint32_t>(
-        R, key_lo, key_hi, [&](auto f) { for (int i = c0 + threadIdx.x; i < c1; i += THREADS) f(keys[i]); }, hist, above);
+        R, c1 - c0, key_lo, key_hi, [&](auto f) { for (int i = c0 + threadIdx.x; i < c1; i += THREADS) f(keys[i]); }, hist, above);
     const float up = ordered_value(tau) + eps, down = ordered_value(tau) - eps;
     // each warp a stretch of consecutive blocks [w0, w1): in, or open
     const int span = ((c1 - c0 + WARPS - 1) / WARPS + 31) & ~31;
@@ -408,11 +416,10 @@ __global__ void __launch_bounds__(THREADS, D == 256 ? 1 : 768 / THREADS) select_
 #pragma unroll
             for (int g = 0; g < 8; ++g) {
                 if (g >= G) break;
-                const uint16_t* q = p.q + (static_cast<long long>(bh) * G + g) * D + lane;
                 Pair sum = {0.0f, 0.0f};
 #pragma unroll
                 for (int j = 0; j < NJ; ++j) {
-                    const float x = __half2float(__ushort_as_half(__ldcg(q + 32 * j)));
+                    const float x = __half2float(__ushort_as_half(q_s[g * D + 32 * j + lane]));
                     add(sum, __fmul_rn(x, x > 0.0f ? hi[j] : lo[j]), 0.0f);
                 }
 #pragma unroll
@@ -441,7 +448,7 @@ __global__ void __launch_bounds__(THREADS, D == 256 ? 1 : 768 / THREADS) select_
     }
     int over;
     const uint64_t border = nth_largest<THREADS, uint64_t>(
-        R - n_in, ex_lo, ex_hi,
+        R - n_in, n_open, ex_lo, ex_hi,
         [&](auto f) {
             for (int i = c0 + threadIdx.x; i < c1; i += THREADS)
                 if (is_open(i)) f(exact[i]);

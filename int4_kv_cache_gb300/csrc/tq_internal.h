@@ -320,11 +320,10 @@ cudaError_t launch_quantize_append_tma(const AppendParams& p, const CUtensorMap&
 cudaError_t launch_decode_simt(const DecodeParams& p, int head_dim, cudaStream_t stream);
 cudaError_t launch_decode_mma(const DecodeParams& p, int head_dim, const CUtensorMap& tm_k,
                               const CUtensorMap& tm_v, cudaStream_t stream, bool pdl_secondary);
-// The same over the blocks p.blocks lists (one of the dense kernel's four-warp
-// layouts; tensor maps with boxes of min(tile, block) tokens), and with the
-// scores kept in p.scores (partial states only, part_m in log2 units).
-cudaError_t launch_decode_blocks(const DecodeParams& p, int head_dim, const CUtensorMap& tm_k,
-                                 const CUtensorMap& tm_v, cudaStream_t stream);
+// The same over the blocks p.blocks lists (the dense kernel's four-warp
+// layouts, without TMA), and with the scores kept in p.scores (partial states
+// only, part_m in log2 units).
+cudaError_t launch_decode_blocks(const DecodeParams& p, int head_dim, cudaStream_t stream);
 cudaError_t launch_decode_scores(const DecodeParams& p, int head_dim, const CUtensorMap& tm_k,
                                  const CUtensorMap& tm_v, cudaStream_t stream);
 // The append kernel, optionally letting the next launch start early (the

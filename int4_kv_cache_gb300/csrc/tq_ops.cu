@@ -176,19 +176,14 @@ tq_status run_blocks(const Store& c, const uint16_t* q, int32_t hq, const int32_
     p.n_list = n_select;
     p.block_tokens = block_tokens;
     p.block_shift = block_shift_of(block_tokens);
-    CUtensorMap tm_k, tm_v;
-    const int box = block_tokens < tile ? block_tokens : tile;
-    s = make_code_map(&tm_k, c.k_codes, &c, box);
-    if (s == TQ_OK) s = make_code_map(&tm_v, c.v_codes, &c, box);
-    if (s != TQ_OK) return s;
     if (pl.merged) {
         p.out = out;
-        const cudaError_t e = launch_decode_blocks(p, c.head_dim, tm_k, tm_v, stream);
+        const cudaError_t e = launch_decode_blocks(p, c.head_dim, stream);
         if (e == cudaSuccess || pl.n_splits == 1) return cuda_status(e);
         cudaGetLastError();  // a refused cluster launch: partial states and the reduce
         p.out = nullptr;
     }
-    s = cuda_status(launch_decode_blocks(p, c.head_dim, tm_k, tm_v, stream));
+    s = cuda_status(launch_decode_blocks(p, c.head_dim, stream));
     if (s != TQ_OK) return s;
     ReduceParams r{};
     r.part_m = pm;
