@@ -240,6 +240,7 @@ struct BoundsParams {
     int32_t batch, num_kv_heads, head_dim, capacity, bits;
     int32_t n_rows, block_shift, blocks_per_seq;
     int32_t touched;           // blocks per sequence at most
+    int32_t items;             // blocks of all sequences and heads (set by the launch)
     RowMap map;
 };
 
@@ -303,7 +304,7 @@ struct WeightsParams {
 
 // Launchers (return the cudaError_t of the launch).
 cudaError_t launch_rope(const RopeParams& p, cudaStream_t stream);
-cudaError_t launch_bounds(const BoundsParams& p, cudaStream_t stream);
+cudaError_t launch_bounds(const BoundsParams& p, int sms, cudaStream_t stream);
 cudaError_t launch_select(const SelectParams& p, cudaStream_t stream);
 cudaError_t launch_evict_select(const EvictParams& p, cudaStream_t stream);
 cudaError_t launch_evict_copy(const EvictCopyParams& p, cudaStream_t stream);

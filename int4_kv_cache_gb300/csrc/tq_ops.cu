@@ -49,7 +49,10 @@ tq_status block_bounds(const Store& c, int32_t block_tokens, const int32_t* star
     p.touched = (n_rows + block_tokens - 2) / block_tokens + 1;  // rows that start at a block's last row
     if (p.touched > p.blocks_per_seq) p.touched = p.blocks_per_seq;
     p.map = c.map;
-    return cuda_status(launch_bounds(p, stream));
+    DeviceFacts* f = nullptr;
+    const tq_status s = device_facts(&f);
+    if (s != TQ_OK) return s;
+    return cuda_status(launch_bounds(p, f->sms, stream));
 }
 
 // ---------------------------------------------------------------- selection --
