@@ -494,7 +494,7 @@ tq_status tq_sdpa_int4_decode_noalloc(const tq_kv_cache* cache, const uint16_t* 
  *   inv_freq   device fp32 [rotary_dim / 2]
  *   sections   HOST int32 [n_axes], sum rotary_dim / 2 (zeros allowed)
  * head_dim 64, 128 or 256; rotary_dim a multiple of 16 up to head_dim; batch
- * up to 65,535; n = 0 launches nothing.  An out that overlaps an x or the other
+ * and heads up to 65,535; n = 0 launches nothing.  An out that overlaps an x or the other
  * out: TQ_ERR_SHAPE. */
 #define TQ_ROPE_PAIRS 0x1u
 #define TQ_ROPE_INVERSE 0x2u

@@ -596,7 +596,7 @@ def _rope_rows(x: torch.Tensor, out: Optional[torch.Tensor], b: int, n: int, d: 
         raise ValueError(f"{name}: expected a CUDA float16 tensor [B, n, heads, D] with a contiguous last dimension")
     h = x.shape[2]
     if out is None:
-        out = x.new_empty((b, h, n, d))
+        out = torch.empty((b, h, n, d), dtype=torch.float16, device=x.device)
         if stream is not None:
             out.record_stream(stream)
     else:

@@ -5,16 +5,19 @@
 //
 // Two kernels.  select: one cluster of CTAs per (sequence, kv head), each with
 // a stretch of the weights, 8 or 32 a thread in registers (longer stretches are read
-// again, from L2, in every step); the threshold weight by radix selection (11,
-// 11 and 10 bits of the ordered fp32 key): every CTA counts into its own
+// again, from L2, in every step); the threshold weight by radix selection on
+// the ordered fp32 key: for its first 11 bits every CTA counts into its own
 // histogram and adds what is not zero to the first CTA's, which picks the digit
-// and tells the others; then the kept rows' indices in order, from counts per
-// warp and prefix sums over warps and CTAs.  copy: the kept rows, codes and
+// and tells the others; a cluster then gathers the keys that share it in the
+// first CTA, which finds the threshold among them (one CTA, or more than kGather
+// such keys: two more steps of 11 and 10 bits); then the kept rows' indices in order, from counts per warp
+// and prefix sums over warps and CTAs.  copy: the kept rows, codes and
 // scales, 16 bytes a thread, into consecutive rows of the destination.  Bound
 // by the kept rows' bytes for a batch, by the selection's latency for one
 // sequence.
 #include "tq_device.cuh"
 #include "tq_internal.h"
+#include "tq_radix.cuh"
 
 namespace tq {
 
@@ -23,7 +26,8 @@ namespace {
 constexpr int kEvThreads = 512;
 constexpr int kEvWarps = kEvThreads / 32;
 constexpr int kBins = 2048;
-static_assert(kBins == 4 * kEvThreads, "four bins a thread");
+constexpr int kGather = 4096;  // keys that the first CTA takes over
+static_assert(kBins == 4 * kEvThreads && kEvThreads == 512, "four bins, one digit count a thread");
 
 __device__ __forceinline__ uint32_t weight_key(float x) {
     const uint32_t u = __float_as_uint(x + 0.0f);  // -0 -> +0
@@ -40,13 +44,18 @@ __global__ void __launch_bounds__(kEvThreads, V == 8 ? 1 : 2) evict_select_kerne
     __shared__ uint32_t sums[kBins];                // the first CTA's: the cluster's counts
     __shared__ uint32_t wcount[kEvWarps];
     __shared__ uint32_t piece[kRoundWarps];         // above (low half) and equal (high half) of each piece
-    __shared__ int pick[2];
+    __shared__ uint32_t pick[3];
+    __shared__ uint32_t found[kGather];             // the first CTA's: keys that share the first digit
+    __shared__ uint32_t n_found;
+    __shared__ uint32_t digits[2][256];
     __shared__ uint32_t cta_count[2];               // this CTA's rows above the threshold, and equal to it
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int n_cta = p.ctas, rank = static_cast<int>(blockIdx.x) % n_cta;
     const int bh = static_cast<int>(blockIdx.x) / n_cta;
     const int b = bh / p.num_kv_heads;
     for (int i = threadIdx.x; i < kBins; i += kEvThreads) hist[i] = sums[i] = 0;
+    digits[threadIdx.x >> 8][threadIdx.x & 255] = 0;
+    if (threadIdx.x == 0) n_found = 0;
     pdl_wait_primary();
     pdl_launch_dependents();
     int len = __ldcg(p.seq_lens + b);
@@ -164,9 +173,11 @@ __global__ void __launch_bounds__(kEvThreads, V == 8 ? 1 : 2) evict_select_kerne
                             if (n_cta > 1) {
                                 st_cluster_u32(&pick[0], r, top - j);
                                 st_cluster_u32(&pick[1], r, above + before);
+                                st_cluster_u32(&pick[2], r, c[j]);
                             } else {
                                 pick[0] = top - j;
-                                pick[1] = above + static_cast<int>(before);
+                                pick[1] = above + before;
+                                pick[2] = c[j];
                             }
                         }
                     }
@@ -176,9 +187,36 @@ __global__ void __launch_bounds__(kEvThreads, V == 8 ? 1 : 2) evict_select_kerne
         }
         if (n_cta > 1) cluster_sync();
         else __syncthreads();
-        value |= static_cast<uint32_t>(pick[0]) << shift;
-        above = pick[1];
+        value |= pick[0] << shift;
+        above = static_cast<int>(pick[1]);
         mask |= (bins - 1u) << shift;
+        const uint32_t share = pick[2];
+        if (pass == 0 && n_cta > 1 && share <= kGather) {  // the same for the cluster
+            for (int base = s0; base < s1; base += kStretch) {
+                if (!ONE) load_round(base);
+                visit_round(base, [&](float w) {
+                    const uint32_t k = weight_key(w);
+                    if ((k & mask) != value) return;
+                    st_cluster_u32(&found[min(atom_cluster_add_u32(&n_found, 0, 1), kGather - 1u)], 0, k);
+                });
+                if (ONE) break;
+            }
+            cluster_sync();
+            if (rank == 0) {
+                int larger;
+                const uint32_t t = nth_largest<kEvThreads, uint32_t>(
+                    want - above, static_cast<int>(share), value, value | ~mask,
+                    [&](auto f) { for (uint32_t i = threadIdx.x; i < share; i += kEvThreads) f(found[i]); }, digits, larger);
+                if (threadIdx.x < n_cta) {
+                    st_cluster_u32(&pick[0], threadIdx.x, t);
+                    st_cluster_u32(&pick[1], threadIdx.x, above + larger);
+                }
+            }
+            cluster_sync();
+            value = pick[0];
+            above = static_cast<int>(pick[1]);
+            break;
+        }
         if (n_cta == 1) __syncthreads();  // pick and wcount are read before the next pass writes them
     }
     const uint32_t ties = static_cast<uint32_t>(want - above);  // rows equal to the threshold that stay, lowest index first

@@ -10,9 +10,12 @@
 // far into a sequence.  What is left of the turn is rounded to fp32 (2^-25 of
 // half a turn), where sincospif takes over.
 //
-// Bound by bytes: every row is read and written once.  A CTA takes kTok tokens
-// of one sequence; their cosines and sines are computed once into shared
-// memory and serve every head of q and k.
+// Bound by bytes: every row is read and written once.  A CTA takes a token of a
+// sequence, whose cosines and sines are computed once into shared memory and
+// serve every head of q and k; a thread turns 16 elements at a time.  8,192
+// tokens of 64 + 8 heads x 128 (302 MB) take 47.5 us, 6.4 TB/s.  (With two to
+// sixteen tokens a CTA, whose output rows are neighbours, or two to six units a
+// thread in flight, it took 51 to 74 us; without streaming stores 56 us.)
 #include <cuda_fp16.h>
 
 #include "tq_device.cuh"
@@ -23,6 +26,7 @@ namespace tq {
 namespace {
 
 constexpr int kRopeThreads = 256;
+constexpr int kRopeMaxPairs = 128;  // of a row of 256
 
 // A unit: 16 elements that turn together (eight pairs), or 16 plain ones.
 __device__ __forceinline__ void turn8(uint4& a, uint4& b, const float* c, const float* s) {
@@ -51,66 +55,44 @@ __device__ __forceinline__ void turn_pairs8(uint4& a, uint4& b, const float* c, 
 
 template <bool PAIRS>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) {
-    extern __shared__ float table[];  // [tokens][2][half]: cosines, sines
+    __shared__ __align__(16) float table[2 * kRopeMaxPairs];  // cosines, then sines
     const int half = p.rotary_dim / 2;
-    const int b = blockIdx.y;
-    const int t0 = blockIdx.x * p.tokens_per_cta;
-    const int nt = min(p.tokens_per_cta, p.n - t0);
+    const int b = blockIdx.y, t = blockIdx.x;
     pdl_wait_primary();
     pdl_launch_dependents();
-    for (int i = threadIdx.x; i < nt * half; i += kRopeThreads) {
-        const int t = i / half, j = i - t * half;
+    for (int j = threadIdx.x; j < half; j += blockDim.x) {
         int axis = 0;
 #pragma unroll
         for (int a = 1; a < kRopeAxes; ++a) axis += j >= p.section_end[a - 1] ? 1 : 0;
-        const int pos = __ldg(p.positions + (static_cast<long long>(axis) * p.batch + b) * p.n + t0 + t);
+        const int pos = __ldg(p.positions + (static_cast<long long>(axis) * p.batch + b) * p.n + t);
         const double turns = static_cast<double>(pos) * (static_cast<double>(__ldg(p.inv_freq + j)) * 0.15915494309189535);
         float s, c;
         sincospif(2.0f * static_cast<float>(turns - rint(turns)), &s, &c);
-        table[t * 2 * half + j] = c;
-        table[t * 2 * half + half + j] = p.inverse ? -s : s;
+        table[j] = c;
+        table[kRopeMaxPairs + j] = p.inverse ? -s : s;
     }
     __syncthreads();
     const int units = p.head_dim / 16, turning = half / 8;
-    const int heads = p.q.heads + p.k.heads;
-    // consecutive threads: the units of a row, then the tokens of a head (whose
-    // output rows are neighbours), then the heads
-    const int per_head = units * nt, total = heads * per_head;
-    constexpr int U = 3;  // units of a thread in flight
-    for (int i0 = threadIdx.x; i0 < total; i0 += U * kRopeThreads) {
-        uint4 x[U], y[U];
-        uint16_t* dst[U];
-        int e0[U], e1[U], at[U];
-#pragma unroll
-        for (int k = 0; k < U; ++k) {
-            const int i = i0 + k * kRopeThreads;
-            if (i >= total) break;
-            int h = i / per_head;
-            const int r = i - h * per_head;
-            const int t = r / units, u = r - t * units;
-            const bool is_k = h >= p.q.heads;
-            const RopeRows& rows = is_k ? p.k : p.q;
-            if (is_k) h -= p.q.heads;
-            const uint16_t* src = rows.x + b * rows.stride_b + static_cast<long long>(t0 + t) * rows.stride_t + h * rows.stride_h;
-            dst[k] = rows.out + ((static_cast<long long>(b) * rows.heads + h) * p.n + t0 + t) * p.head_dim;
-            const bool turns = u < turning, split = !PAIRS && turns;
-            e0[k] = split ? 8 * u : 16 * u;
-            e1[k] = split ? half + 8 * u : 16 * u + 8;
-            at[k] = turns ? t * 2 * half + 8 * u : -1;
-            x[k] = __ldcs(reinterpret_cast<const uint4*>(src + e0[k]));
-            y[k] = __ldcs(reinterpret_cast<const uint4*>(src + e1[k]));
+    const int total = (p.q.heads + p.k.heads) * units;
+    for (int i = threadIdx.x; i < total; i += blockDim.x) {
+        int h = i / units;
+        const int u = i - h * units;
+        const bool is_k = h >= p.q.heads;
+        const RopeRows& rows = is_k ? p.k : p.q;
+        if (is_k) h -= p.q.heads;
+        const uint16_t* src = rows.x + b * rows.stride_b + t * rows.stride_t + h * rows.stride_h;
+        uint16_t* dst = rows.out + ((static_cast<long long>(b) * rows.heads + h) * p.n + t) * p.head_dim;
+        const bool turns = u < turning, split = !PAIRS && turns;
+        const int e0 = split ? 8 * u : 16 * u, e1 = split ? half + 8 * u : 16 * u + 8;
+        uint4 x = __ldcs(reinterpret_cast<const uint4*>(src + e0));
+        uint4 y = __ldcs(reinterpret_cast<const uint4*>(src + e1));
+        if (turns) {
+            const float* c = table + 8 * u;
+            if (PAIRS) turn_pairs8(x, y, c, c + kRopeMaxPairs);
+            else turn8(x, y, c, c + kRopeMaxPairs);
         }
-#pragma unroll
-        for (int k = 0; k < U; ++k) {
-            if (i0 + k * kRopeThreads >= total) break;
-            if (at[k] >= 0) {
-                const float* c = table + at[k];
-                if (PAIRS) turn_pairs8(x[k], y[k], c, c + half);
-                else turn8(x[k], y[k], c, c + half);
-            }
-            *reinterpret_cast<uint4*>(dst[k] + e0[k]) = x[k];
-            *reinterpret_cast<uint4*>(dst[k] + e1[k]) = y[k];
-        }
+        __stcs(reinterpret_cast<uint4*>(dst + e0), x);
+        __stcs(reinterpret_cast<uint4*>(dst + e1), y);
     }
 }
 
@@ -118,10 +100,11 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) 
 
 cudaError_t launch_rope(const RopeParams& p, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>((p.n + p.tokens_per_cta - 1) / p.tokens_per_cta),
-                       static_cast<unsigned>(p.batch));
-    cfg.blockDim = dim3(kRopeThreads);
-    cfg.dynamicSmemBytes = static_cast<size_t>(p.tokens_per_cta) * p.rotary_dim * sizeof(float);
+    cfg.gridDim = dim3(static_cast<unsigned>(p.n), static_cast<unsigned>(p.batch));
+    // as many threads as share a token's units evenly
+    const long long total = (static_cast<long long>(p.q.heads) + p.k.heads) * (p.head_dim / 16);
+    const long long rounds = (total + kRopeThreads - 1) / kRopeThreads;
+    cfg.blockDim = dim3(static_cast<unsigned>(((total + rounds - 1) / rounds + 31) / 32 * 32));
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

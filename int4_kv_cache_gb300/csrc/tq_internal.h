@@ -226,7 +226,7 @@ struct RopeParams {
     const float* inv_freq;     // [rotary_dim / 2]
     int32_t batch, n, head_dim, rotary_dim;
     int32_t section_end[kRopeAxes];  // first pair behind each axis (the last ones: rotary_dim / 2)
-    int32_t pairs, inverse, tokens_per_cta;
+    int32_t pairs, inverse;
 };
 
 // Key bounds of the blocks that rows [start[b], start[b] + n_rows) touch (bounds.cu).
@@ -296,7 +296,8 @@ struct WeightsParams {
     const int32_t* seq_lens;
     float* weights;            // [B][Hkv][weight_stride]
     uint16_t* out;             // [B][Hq][D]
-    int32_t batch, num_q_heads, num_kv_heads, group_q, max_seq_len, weight_stride, n_parts, chunks;
+    int32_t batch, num_q_heads, num_kv_heads, group_q, max_seq_len, weight_stride, n_parts;
+    int32_t chunks, chunk_tokens;  // set by the launch
     float decay;
     int32_t rotate_out;
     float rot_scale;
@@ -308,7 +309,7 @@ cudaError_t launch_bounds(const BoundsParams& p, int sms, cudaStream_t stream);
 cudaError_t launch_select(const SelectParams& p, cudaStream_t stream);
 cudaError_t launch_evict_select(const EvictParams& p, cudaStream_t stream);
 cudaError_t launch_evict_copy(const EvictCopyParams& p, cudaStream_t stream);
-cudaError_t launch_weights(const WeightsParams& p, int head_dim, cudaStream_t stream);
+cudaError_t launch_weights(const WeightsParams& p, int head_dim, int sms, cudaStream_t stream);
 cudaError_t launch_quantize_append(const AppendParams& p, cudaStream_t stream);
 // The same for large appends: a persistent grid (a few CTAs per SM of `sms`)
 // streaming the fp16 rows through TMA.  tm_k / tm_v: k_new / v_new as

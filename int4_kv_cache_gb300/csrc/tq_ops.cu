@@ -323,7 +323,10 @@ tq_status decode_weights(const Store& c, const uint16_t* q, int32_t hq, const in
     w.decay = decay;
     w.rotate_out = (flags & TQ_ROTATE_V) ? 1 : 0;
     w.rot_scale = rotation_scale(c.head_dim);
-    return cuda_status(launch_weights(w, c.head_dim, stream));
+    DeviceFacts* f = nullptr;
+    s = device_facts(&f);
+    if (s != TQ_OK) return s;
+    return cuda_status(launch_weights(w, c.head_dim, f->sms, stream));
 }
 
 // ----------------------------------------------------------------- eviction --
@@ -427,7 +430,7 @@ unsigned long long rope_extent(const tq_rope_rows* r, int32_t batch, int32_t n, 
 
 tq_status check_rope_rows(const tq_rope_rows* r) {
     if (r->x == nullptr || r->out == nullptr) return TQ_ERR_NULL;
-    if (r->num_heads < 1 || r->stride_b < 0 || r->stride_t < 0 || r->stride_h < 0) return TQ_ERR_SHAPE;
+    if (r->num_heads < 1 || r->num_heads > 65535 || r->stride_b < 0 || r->stride_t < 0 || r->stride_h < 0) return TQ_ERR_SHAPE;
     if (!aligned16(r->x) || !aligned16(r->out) || r->stride_b % 8 != 0 || r->stride_t % 8 != 0 || r->stride_h % 8 != 0)
         return TQ_ERR_ALIGN;
     return TQ_OK;
@@ -467,9 +470,6 @@ tq_status tq_rope_axes(const tq_rope_rows* q, const tq_rope_rows* k, const int32
                 return TQ_ERR_SHAPE;
         }
     }
-    DeviceFacts* f = nullptr;
-    s = device_facts(&f);
-    if (s != TQ_OK) return s;
     RopeParams p{};
     p.q = {q->x, q->out, q->stride_b, q->stride_t, q->stride_h, q->num_heads};
     if (k != nullptr) p.k = {k->x, k->out, k->stride_b, k->stride_t, k->stride_h, k->num_heads};
@@ -486,11 +486,6 @@ tq_status tq_rope_axes(const tq_rope_rows* q, const tq_rope_rows* k, const int32
     }
     p.pairs = (flags & TQ_ROPE_PAIRS) ? 1 : 0;
     p.inverse = (flags & TQ_ROPE_INVERSE) ? 1 : 0;
-    // Tokens of a CTA: as many as leave eight CTAs for every SM (a table of
-    // cosines then serves more rows and the output rows of a head are longer
-    // stretches), one where tokens are few.
-    p.tokens_per_cta = 1;
-    while (p.tokens_per_cta < 8 && static_cast<long long>(batch) * n >= 16LL * f->sms * p.tokens_per_cta) p.tokens_per_cta *= 2;
     return cuda_status(launch_rope(p, static_cast<cudaStream_t>(stream)));
 }
 
