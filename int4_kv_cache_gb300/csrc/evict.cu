@@ -12,7 +12,8 @@
 // first CTA, which finds the threshold among them (one CTA, or more than kGather
 // such keys: two more steps of 11 and 10 bits); then the kept rows' indices in order, from counts per warp
 // and prefix sums over warps and CTAs.  copy: the kept rows, codes and
-// scales, 16 bytes a thread, into consecutive rows of the destination.  Bound
+// scales, 16 bytes a thread, into consecutive rows of the destination, with
+// streaming stores (32 sequences of 4,096 rows 64.1 -> 61.4 us).  Bound
 // by the kept rows' bytes for a batch, by the selection's latency for one
 // sequence.
 #include "tq_device.cuh"
@@ -374,7 +375,7 @@ __global__ void __launch_bounds__(kCopyThreads) evict_copy_kernel(const EvictCop
     for (int j = 0; j < PER; ++j) {
         const int i = j * kCopyThreads + threadIdx.x;
         const int kv = i / (kCopyRows * PIECES), rr = i / PIECES % kCopyRows, c = i % PIECES;
-        if (kv < 2 && rr < n) *(reinterpret_cast<uint4*>((kv ? p.dst_v : p.dst_k) + to[rr] * BPT) + c) = x[j];
+        if (kv < 2 && rr < n) __stcs(reinterpret_cast<uint4*>((kv ? p.dst_v : p.dst_k) + to[rr] * BPT) + c, x[j]);
     }
     if (r < n) *reinterpret_cast<Row*>(p.dst_sb[a] + to[r] * NG) = s;
 }
