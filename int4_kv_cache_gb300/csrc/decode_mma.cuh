@@ -383,31 +383,38 @@ __global__ void __launch_bounds__(Cfg<D, BITS, WIDE>::THREADS, Cfg<D, BITS, WIDE
         row = (w < n_win ? static_cast<long long>(blk_row[w]) << 4 : block_row(blk)) + off;
         return max(0, min(len - ((blk << p.block_shift) + off), kWarpRows));
     };
-    auto fetch_rows = [&](int it) {
+    constexpr int kCodePieces = kWarpRows * C::SPT;    // 16-byte pieces of the codes of K or V, consecutive in the cache
+    constexpr int kSbPieces = kWarpRows * NG / 8;      // of each scale or bias array
+    uint32_t put[BLK ? kCodePieces / 32 : 1];          // where this lane's pieces go in a stage
+    const int sb_s = lane % kSbPieces;
+    const uint16_t* sb_src = nullptr;
+    if constexpr (BLK) {
+#pragma unroll
+        for (int i = 0; i < kCodePieces / 32; ++i)
+            put[i] = smem_u32(smem) + code_addr<C>(0u, warp * kWarpRows + (32 * i + lane) / C::SPT, (32 * i + lane) % C::SPT);
+        const int a = lane / kSbPieces;
+        sb_src = (a < 2 ? (a == 0 ? p.k_scale : p.k_bias) : (a == 2 ? p.v_scale : p.v_bias)) + sb_s * 8;
+    }
+    const uint32_t sb_put = smem_u32(smem) + 2 * C::CODE_BYTES + (lane / kSbPieces) * C::SB_BYTES + warp * kWarpRows * NG * 2 +
+                            sb_s * 16;
+    auto fetch_rows = [&](int it, int stage) -> int {
         long long row = 0;
         const int n = it < n_tiles ? warp_rows(it, row) : 0;
         if (n > 0) {
-            uint8_t* st = smem + (it % C::STAGES) * C::STAGE_BYTES;
-            const int tb = warp * kWarpRows;
-            constexpr int kPieces = kWarpRows * C::SPT;  // 16-byte pieces of the codes of K or V
+            const uint32_t st = stage * C::STAGE_BYTES;
+            const uint8_t* k = p.k_codes + row * C::BPT + lane * 16;
+            const uint8_t* v = p.v_codes + row * C::BPT + lane * 16;
 #pragma unroll
-            for (int i = 0; i < kPieces; i += 32) {
-                const int t = (i + lane) / C::SPT, s = (i + lane) % C::SPT;
-                if (t < n) {
-                    const uint32_t at = code_addr<C>(0u, tb + t, s);
-                    const long long from = (row + t) * C::BPT + s * 16;
-                    cp_async16(st + at, p.k_codes + from);
-                    cp_async16(st + C::CODE_BYTES + at, p.v_codes + from);
+            for (int i = 0; i < kCodePieces / 32; ++i) {
+                if (n == kWarpRows || (32 * i + lane) / C::SPT < n) {
+                    cp_async16(put[i] + st, k + i * 512);
+                    cp_async16(put[i] + st + C::CODE_BYTES, v + i * 512);
                 }
             }
-            constexpr int kSbPieces = kWarpRows * NG / 8;  // of each scale or bias array
-            const int a = lane / kSbPieces, s = lane % kSbPieces;
-            if (a < 4 && s * (8 / NG) < n) {
-                const uint16_t* src = a < 2 ? (a == 0 ? p.k_scale : p.k_bias) : (a == 2 ? p.v_scale : p.v_bias);
-                cp_async16(st + 2 * C::CODE_BYTES + a * C::SB_BYTES + tb * NG * 2 + s * 16, src + row * NG + s * 8);
-            }
+            if (lane < 4 * kSbPieces && sb_s * (8 / NG) < n) cp_async16(sb_put + st, sb_src + row * NG);
         }
         cp_async_commit();
+        return n;
     };
     static_assert(!BLK || 4 * kWarpRows * NG / 8 <= 32, "a lane per piece of the scales");
 
@@ -475,11 +482,13 @@ __global__ void __launch_bounds__(Cfg<D, BITS, WIDE>::THREADS, Cfg<D, BITS, WIDE
                (((static_cast<long long>(b) * p.num_kv_heads + kvh) * p.app.n_new + (a.r - app_wp)) * D +
                 a.g * kGroup + app_part * 8);
     };
+    int blk_rows[C::STAGES] = {};  // listed blocks: this warp's rows that count in the tile at hand and those ahead
     uint4 app_raw = make_uint4(0, 0, 0, 0);
     if (static_cast<int>(threadIdx.x >> 3) < app_tasks)
         app_raw = __ldcs(reinterpret_cast<const uint4*>(app_src(threadIdx.x >> 3)));
     if constexpr (BLK) {
-        for (int it = 0; it < C::STAGES - 1; ++it) fetch_rows(it);
+#pragma unroll
+        for (int it = 0; it < C::STAGES - 1; ++it) blk_rows[it] = fetch_rows(it, it);
     } else if (threadIdx.x == 0 && n_tiles > 0) {
         prefetch_tensormap(&tm_k);
         prefetch_tensormap(&tm_v);
@@ -690,11 +699,12 @@ __global__ void __launch_bounds__(Cfg<D, BITS, WIDE>::THREADS, Cfg<D, BITS, WIDE
         int blk_n = 0;  // listed blocks: this warp's rows of the tile that count
         if constexpr (BLK) {
             __syncwarp();  // the stage fetched into next has been read by every lane
-            fetch_rows(it + C::STAGES - 1);
+            blk_rows[C::STAGES - 1] = fetch_rows(it + C::STAGES - 1, stage == 0 ? C::STAGES - 1 : stage - 1);
             cp_async_wait<C::STAGES - 1>();
             __syncwarp();
-            long long row = 0;
-            blk_n = warp_rows(it, row);
+            blk_n = blk_rows[0];
+#pragma unroll
+            for (int i = 0; i + 1 < C::STAGES; ++i) blk_rows[i] = blk_rows[i + 1];
             if (blk_n == 0) continue;  // the same for the warp
         } else if (!mbar_wait_bounded(&full_bar[stage], (it / C::STAGES) & 1)) {
             // the fill never completed: report, stop consuming (no further

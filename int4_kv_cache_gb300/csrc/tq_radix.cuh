@@ -61,13 +61,13 @@ __device__ __forceinline__ K nth_largest(int n, int count, K lo, K hi, Visit vis
         });
         __syncthreads();
         for (int i = threadIdx.x; i < 256; i += THREADS) hist[h ^ 1][i] = 0;  // read a barrier ago
-        // every warp finds the digit: lane l holds bins 255 - 8l .. 248 - 8l, counts from the largest down
-        uint32_t c[8], sum = 0;
+        // Every warp finds the digit: lane l holds bins 255 - 8 l .. 248 - 8 l,
+        // counts from the largest down.  (Their sum in an order of the lane's
+        // own, so that the lanes' banks differ.)
+        const uint32_t* bins = &hist[h][255 - 8 * lane];
+        uint32_t sum = 0;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            c[j] = hist[h][255 - 8 * lane - j];
-            sum += c[j];
-        }
+        for (int j = 0; j < 8; ++j) sum += bins[-((j + (lane >> 2)) & 7)];
         uint32_t before = sum;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
@@ -81,12 +81,13 @@ __device__ __forceinline__ K nth_largest(int n, int count, K lo, K hi, Visit vis
         if (mine) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                if (before < want && want <= before + c[j]) {
+                const uint32_t c = bins[-j];
+                if (before < want && want <= before + c) {
                     bin = 255 - 8 * lane - j;
                     ahead = before;
-                    here = c[j];
+                    here = c;
                 }
-                before += c[j];
+                before += c;
             }
         }
         const uint32_t who = __ballot_sync(0xffffffffu, mine);
