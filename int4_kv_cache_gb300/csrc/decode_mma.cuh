@@ -144,6 +144,19 @@ __device__ __forceinline__ uint32_t code_addr(uint32_t tile, int tok, int seg) {
     return tile + half * C::HALF_BYTES + row * 128 + ((chunk ^ (row & 7)) << 4);
 }
 
+// The nibbles at bits 0..3 / 16..19, or 4..7 / 20..23, as packed halves 0..15:
+// placed in the mantissa of 1024, which is then taken off (exact).
+__device__ __forceinline__ uint32_t low_nibbles(uint32_t x) {
+    x = (x & kLoNib) | 0x64006400u;
+    const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&x), __float2half2_rn(1024.0f));
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t high_nibbles(uint32_t x) {
+    x = (x & kHiNib) | 0x64006400u;  // 1024 + 16 n
+    const __half2 h = __hfma2(*reinterpret_cast<const __half2*>(&x), __float2half2_rn(0.0625f), __float2half2_rn(-64.0f));
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
 struct alignas(8) Half4 {
     __half2 a, b;
 };
@@ -228,6 +241,11 @@ __global__ void __launch_bounds__(Cfg<D, BITS, WIDE>::THREADS, Cfg<D, BITS, WIDE
     constexpr int NG = C::NG;
     constexpr bool BLK = MODE == kModeBlocks;
     static_assert(!(BLK && WIDE), "listed blocks take the four-warp layout");
+    // Kept scores become fp32 weights, and a product of a subnormal operand
+    // loses the bits above the operand's leading one in the tensor core's sums
+    // (weights off by 4e-6 for int4 keys, by 1e-6 at most with normal ones): the
+    // score operands of int4 keys are made normal, one packed operation each.
+    constexpr bool kNormal = MODE == kModeScores && BITS == 4;
     __shared__ uint64_t full_bar[C::STAGES];
     __shared__ unsigned int done_cnt[C::STAGES];  // warps finished with the stage, cumulative
     __shared__ float mrg_m[C::NWC][8], mrg_l[C::NWC][8], mrg_t[C::NWC][8];
@@ -507,7 +525,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS, WIDE>::THREADS, Cfg<D, BITS, WIDE
     {
         const bool hv = gid < G;
         const uint16_t* qrow = p.q + (static_cast<long long>(b) * p.num_q_heads + kvh * G + (hv ? gid : 0)) * D;
-        const __half sixteenth = __float2half_rn(0.0625f);
+        const __half sixteenth = __float2half_rn(kNormal ? 1.0f : 0.0625f);
 #pragma unroll
         for (int g = 0; g < NG; ++g) qsum_own[g] = 0.0f;
         // This lane's dims of head gid: E consecutive ones at E * tig in each
@@ -600,7 +618,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS, WIDE>::THREADS, Cfg<D, BITS, WIDE
         qs_l2[g][0] = __shfl_sync(0xffffffffu, qsum_own[g], (2 * tig) * 4) * sl2;
         qs_l2[g][1] = __shfl_sync(0xffffffffu, qsum_own[g], (2 * tig + 1) * 4) * sl2;
     }
-    const float k_coef = sl2 * 16777216.0f;  // undo the 2^-24 of the subnormal operands
+    const float k_coef = kNormal ? sl2 : sl2 * 16777216.0f;  // undo the 2^-24 of the subnormal operands
     const int r0 = tok_of_row<C>(gid), r1 = tok_of_row<C>(gid + 8);
 
     float m_run[2] = {-INFINITY, -INFINITY};  // reference max of l, acc (lazy)
@@ -757,11 +775,18 @@ __global__ void __launch_bounds__(Cfg<D, BITS, WIDE>::THREADS, Cfg<D, BITS, WIDE
                             mma_16816(cg[g], xa & kByte, xb & kByte, (xa >> 8) & kByte, (xb >> 8) & kByte, qb[s][0],
                                       qb[s][1]);
                         } else {
+                            const uint32_t ya = xa >> 8, yb = xb >> 8;
+                            if constexpr (kNormal) {
+                                mma_16816(cg[g], low_nibbles(xa), low_nibbles(xb), high_nibbles(xa), high_nibbles(xb),
+                                          qb[2 * s][0], qb[2 * s][1]);
+                                mma_16816(cg[g], low_nibbles(ya), low_nibbles(yb), high_nibbles(ya), high_nibbles(yb),
+                                          qb[2 * s + 1][0], qb[2 * s + 1][1]);
+                            } else {
                             mma_16816(cg[g], xa & kLoNib, xb & kLoNib, xa & kHiNib, xb & kHiNib, qb[2 * s][0],
                                       qb[2 * s][1]);
-                            const uint32_t ya = xa >> 8, yb = xb >> 8;
                             mma_16816(cg[g], ya & kLoNib, yb & kLoNib, ya & kHiNib, yb & kHiNib, qb[2 * s + 1][0],
                                       qb[2 * s + 1][1]);
+                            }
                         }
                     }
                 }
