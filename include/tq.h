@@ -525,7 +525,8 @@ tq_status tq_rope_axes(const tq_rope_rows* q, const tq_rope_rows* k, const int32
  * tq_kv_block_bounds recomputes the bounds of every block that rows
  * [start[b], start[b] + n_rows) of sequence b touch, from the block's rows
  * below start[b] + n_rows: call it after each append with its write_pos and
- * n_new.  Other blocks are left as they were.  A range outside the cache sets
+ * n_new.  Caches of up to 2^30 tokens (all the entry points from here on).
+ * Other blocks are left as they were.  A range outside the cache sets
  * TQ_DEV_WRITE_POS and leaves that sequence out. */
 size_t tq_block_bounds_bytes(int32_t batch, int32_t num_kv_heads, int32_t head_dim, int32_t capacity,
                              int32_t block_tokens);
@@ -600,7 +601,8 @@ tq_status tq_paged_sparse_decode(const tq_paged_kv_cache* cache, const uint16_t*
  * as zeros, or that tq_kv_evict wrote, is ready).  The weights' fp32 values are
  * within 1e-5 relative (L2) of fp64 over the same cache.
  * workspace: tq_weights_workspace_bytes(...) bytes (the scores, 4 bytes per
- * query head and token of max_seq_len, and the decode's), 256-byte aligned. */
+ * query head and token of max_seq_len, and the decode's), 256-byte aligned, one
+ * per call in flight. */
 size_t tq_weights_workspace_bytes(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
                                   int32_t head_dim, int32_t max_seq_len);
 tq_status tq_sdpa_decode_weights(const tq_kv_cache* cache, const uint16_t* q, int32_t num_q_heads,
@@ -627,8 +629,8 @@ tq_status tq_paged_sdpa_decode_weights(const tq_paged_kv_cache* cache, const uin
  * Rows of dst behind the kept ones are left as they were.  Both caches have
  * the same batch, heads, head_dim and bits; 0 <= recent <= keep <= dst
  * capacity; batch * num_kv_heads <= 65,535.  What is written must not overlap
- * what is read (TQ_ERR_SHAPE); paged caches may share a pool, but a page in
- * both tables (or twice in dst's) gives undefined rows. */
+ * what is read (TQ_ERR_SHAPE); paged caches may share a pool (not the table),
+ * but a page in both tables (or twice in dst's) gives undefined rows. */
 tq_status tq_kv_evict(const tq_kv_cache* src, const tq_kv_cache* dst, const float* weights,
                       const int32_t* seq_lens, int32_t max_seq_len, int32_t keep, int32_t recent,
                       float* dst_weights, int32_t* dst_lens, int32_t* kept, int32_t* status, void* stream);

@@ -70,13 +70,15 @@ __device__ __forceinline__ void bulk_fetch(void* dst, const void* src, uint32_t 
 }
 
 template <int D, int THREADS>
-__global__ void __launch_bounds__(THREADS, D == 256 ? 1 : 768 / THREADS) select_kernel(const SelectParams p) {
+__global__ void __launch_bounds__(THREADS, D == 256 ? 1 : 512 / THREADS) select_kernel(const SelectParams p) {
     constexpr int WARPS = THREADS / 32;
     constexpr int NJ = D / 32;  // 16-byte pieces of a row per lane
     // Every product of 16 terms starts from zero and is added to the sum in
     // fp32: 16 terms cut at 2^-23 of the largest, and D / 8 additions rounded to
     // 2^-24, together below (16 + D / 16) * 2^-23 of the terms' magnitudes
-    // (8 * 2^-23 more for the sums that give those magnitudes).
+    // (8 * 2^-23 more for the sums that give those magnitudes).  A factor below
+    // 2^-14 counts as 2^-14 there: the terms are aligned by their operands'
+    // exponents, which end at that of the smallest normal number.
     constexpr float kEps = static_cast<float>(24 + D / 16) * 0x1p-23f;
     constexpr int kTileBytes = 16 * 4 * D;  // the bounds of 16 blocks
     extern __shared__ __align__(128) uint8_t dyn[];
@@ -151,6 +153,13 @@ __global__ void __launch_bounds__(THREADS, D == 256 ? 1 : 768 / THREADS) select_
         const int tiles = (nb + 15) / 16, per = (tiles + n_cta - 1) / n_cta;
         const int end = min((rank + 1) * per, tiles);
         float most = 0.0f;
+        uint32_t q_max = 0u, b_max = 0u;  // largest magnitudes, as pairs of fp16 bit patterns
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+            const uint32_t w[4] = {qp[j].x | qn[j].x, qp[j].y | qn[j].y, qp[j].z | qn[j].z, qp[j].w | qn[j].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) q_max = __vmaxu2(q_max, w[i] & 0x7fff7fffu);
+        }
         uint32_t least = 0xffffffffu, greatest = 0u, parity = 0u;
         for (int tile = rank * per + warp; tile < end; tile += WARPS) {
             const int rows = min(16, nb - tile * 16);
@@ -164,6 +173,7 @@ __global__ void __launch_bounds__(THREADS, D == 256 ? 1 : 768 / THREADS) select_
             const uint8_t* a0 = stage + min(gid, rows - 1) * (4 * D) + 16 * tig;
             const uint8_t* a1 = stage + min(gid + 8, rows - 1) * (4 * D) + 16 * tig;
             float s[4] = {0.0f, 0.0f, 0.0f, 0.0f}, up[4] = {0.0f, 0.0f, 0.0f, 0.0f}, un[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            uint32_t m0 = 0u, m1 = 0u;  // largest magnitudes of the two rows
             if (!mbar_wait_bounded(&bar[warp], parity)) {
                 if (p.status != nullptr) atomicOr(p.status, TQ_DEV_TIMEOUT);
                 break;
@@ -176,6 +186,8 @@ __global__ void __launch_bounds__(THREADS, D == 256 ? 1 : 768 / THREADS) select_
                 const uint4 h0 = *reinterpret_cast<const uint4*>(a0 + 2 * D + 64 * j);
                 const uint4 h1 = *reinterpret_cast<const uint4*>(a1 + 2 * D + 64 * j);
                 constexpr uint32_t A = 0x7fff7fffu;  // absolute values
+                const uint4 ah0 = make_uint4(h0.x & A, h0.y & A, h0.z & A, h0.w & A), ah1 = make_uint4(h1.x & A, h1.y & A, h1.z & A, h1.w & A);
+                const uint4 al0 = make_uint4(l0.x & A, l0.y & A, l0.z & A, l0.w & A), al1 = make_uint4(l1.x & A, l1.y & A, l1.z & A, l1.w & A);
                 float f[4][4] = {};
                 mma_16816(f[0], h0.x, h1.x, h0.y, h1.y, qp[j].x, qp[j].y);
                 mma_16816(f[1], h0.z, h1.z, h0.w, h1.w, qp[j].z, qp[j].w);
@@ -183,27 +195,37 @@ __global__ void __launch_bounds__(THREADS, D == 256 ? 1 : 768 / THREADS) select_
                 mma_16816(f[3], l0.z, l1.z, l0.w, l1.w, qn[j].z, qn[j].w);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) s[i] = __fadd_rn(s[i], __fadd_rn(__fadd_rn(f[0][i], f[1][i]), __fadd_rn(f[2][i], f[3][i])));
-                mma_16816(up, h0.x & A, h1.x & A, h0.y & A, h1.y & A, qp[j].x, qp[j].y);
-                mma_16816(up, h0.z & A, h1.z & A, h0.w & A, h1.w & A, qp[j].z, qp[j].w);
-                mma_16816(un, l0.x & A, l1.x & A, l0.y & A, l1.y & A, qn[j].x, qn[j].y);
-                mma_16816(un, l0.z & A, l1.z & A, l0.w & A, l1.w & A, qn[j].z, qn[j].w);
+                mma_16816(up, ah0.x, ah1.x, ah0.y, ah1.y, qp[j].x, qp[j].y);
+                mma_16816(up, ah0.z, ah1.z, ah0.w, ah1.w, qp[j].z, qp[j].w);
+                mma_16816(un, al0.x, al1.x, al0.y, al1.y, qn[j].x, qn[j].y);
+                mma_16816(un, al0.z, al1.z, al0.w, al1.w, qn[j].z, qn[j].w);
+                m0 = __vmaxu2(m0, __vmaxu2(__vmaxu2(ah0.x, ah0.y), __vmaxu2(ah0.z, ah0.w)));
+                m0 = __vmaxu2(m0, __vmaxu2(__vmaxu2(al0.x, al0.y), __vmaxu2(al0.z, al0.w)));
+                m1 = __vmaxu2(m1, __vmaxu2(__vmaxu2(ah1.x, ah1.y), __vmaxu2(ah1.z, ah1.w)));
+                m1 = __vmaxu2(m1, __vmaxu2(__vmaxu2(al1.x, al1.y), __vmaxu2(al1.z, al1.w)));
             }
             // columns 2 tig, 2 tig + 1 of rows gid (0, 1) and gid + 8 (2, 3)
             const bool v0 = 2 * tig < G, v1 = 2 * tig + 1 < G;
-            float m0 = fmaxf(v0 ? s[0] : -INFINITY, v1 ? s[1] : -INFINITY);
-            float m1 = fmaxf(v0 ? s[2] : -INFINITY, v1 ? s[3] : -INFINITY);
+            float x0 = fmaxf(v0 ? s[0] : -INFINITY, v1 ? s[1] : -INFINITY);
+            float x1 = fmaxf(v0 ? s[2] : -INFINITY, v1 ? s[3] : -INFINITY);
             // (blocks that are always listed do not compete: whatever their bounds hold)
-            if (r0 >= c0 && r0 < c1) most = fmaxf(most, fmaxf(up[0] - un[0], up[1] - un[1]));
-            if (r1 >= c0 && r1 < c1) most = fmaxf(most, fmaxf(up[2] - un[2], up[3] - un[3]));
+            if (r0 >= c0 && r0 < c1) {
+                most = fmaxf(most, fmaxf(up[0] - un[0], up[1] - un[1]));
+                b_max = __vmaxu2(b_max, m0);
+            }
+            if (r1 >= c0 && r1 < c1) {
+                most = fmaxf(most, fmaxf(up[2] - un[2], up[3] - un[3]));
+                b_max = __vmaxu2(b_max, m1);
+            }
 #pragma unroll
             for (int off = 1; off < 4; off <<= 1) {
-                m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, off));
-                m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, off));
+                x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, off));
+                x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, off));
             }
             // lanes tig = 0 pass row r0 on, tig = 1 row r1
             const int r = tig == 0 ? r0 : r1;
             if (tig < 2 && r < nb) {
-                const uint32_t k = ordered_key(tig == 0 ? m0 : m1);
+                const uint32_t k = ordered_key(tig == 0 ? x0 : x1);
                 st_cluster_u32(&keys[r], 0, k);
                 if (r >= c0 && r < c1) {
                     least = min(least, k);
@@ -214,6 +236,13 @@ __global__ void __launch_bounds__(THREADS, D == 256 ? 1 : 768 / THREADS) select_
         }
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, off));
+        {   // what factors below 2^-14 add: at most 2 D terms of 2^-14 (max |q| + max |bound| + 2^-14)
+            const uint32_t qm = __reduce_max_sync(0xffffffffu, max(q_max & 0xffffu, q_max >> 16));
+            const uint32_t bm = __reduce_max_sync(0xffffffffu, max(b_max & 0xffffu, b_max >> 16));
+            most += 2.0f * D * 0x1p-14f *
+                    (__half2float(__ushort_as_half(static_cast<uint16_t>(qm))) +
+                     __half2float(__ushort_as_half(static_cast<uint16_t>(bm))) + 0x1p-14f);
+        }
         least = __reduce_min_sync(0xffffffffu, least);
         greatest = __reduce_max_sync(0xffffffffu, greatest);
         if (lane == 0) {

@@ -19,6 +19,11 @@ bool overlap(const void* a, unsigned long long na, const void* b, unsigned long 
     return x < y + nb && y < x + na;
 }
 
+// Tokens of a cache that the operators here take (their index arithmetic leaves
+// room for blocks, CTAs and pieces behind the last one).
+constexpr int32_t kMaxTokens = 1 << 30;
+constexpr int32_t kMaxListed = 1 << 24;
+
 int block_shift_of(int32_t block_tokens) { return block_tokens == 32 ? 5 : (block_tokens == 64 ? 6 : (block_tokens == 128 ? 7 : -1)); }
 
 // ------------------------------------------------------------------- bounds --
@@ -29,6 +34,7 @@ tq_status block_bounds(const Store& c, int32_t block_tokens, const int32_t* star
     if (shift < 0) return TQ_ERR_UNSUPPORTED;
     if (!aligned16(bounds) || !aligned4(start)) return TQ_ERR_ALIGN;
     if (n_rows < 0) return TQ_ERR_SHAPE;
+    if (c.capacity > kMaxTokens) return TQ_ERR_UNSUPPORTED;
     if (n_rows > c.capacity) return TQ_ERR_CAPACITY;
     if (n_rows == 0) return TQ_OK;
     BoundsParams p{};
@@ -71,8 +77,9 @@ tq_status check_select(const SelectArgs& a) {
     if (a.batch < 1 || a.hkv < 1 || a.hq < 1 || a.hq % a.hkv != 0 || a.capacity < 1 || a.max_seq_len < 1) return TQ_ERR_SHAPE;
     if (!supported_dim(a.head_dim) || a.hq / a.hkv > 8) return TQ_ERR_UNSUPPORTED;
     if (block_shift_of(a.block_tokens) < 0) return TQ_ERR_UNSUPPORTED;
+    if (a.capacity > kMaxTokens) return TQ_ERR_UNSUPPORTED;
     if (a.max_seq_len > a.capacity) return TQ_ERR_CAPACITY;
-    if (a.n_select < 1 || a.n_first < 0 || a.n_last < 0 || a.n_first > a.n_select || a.n_last > a.n_select - a.n_first)
+    if (a.n_select < 1 || a.n_select > kMaxListed || a.n_first < 0 || a.n_last < 0 || a.n_first > a.n_select || a.n_last > a.n_select - a.n_first)
         return TQ_ERR_SHAPE;
     const int nb = ceil_div(a.max_seq_len, a.block_tokens);
     if (nb > kMaxSelectBlocks) return TQ_ERR_UNSUPPORTED;
@@ -125,7 +132,7 @@ tq_status run_select(const SelectArgs& a, void* workspace, cudaStream_t stream) 
     // Rows that leave SMs free take CTAs of sixteen warps (eight at head_dim
     // 256, whose tiles are larger), as many (up to eight) as give every warp a
     // tile of 16 blocks while no SM has two; more rows take one CTA of eight
-    // warps each, three of which run on an SM.
+    // warps each, two of which run on an SM.
     DeviceFacts* f = nullptr;
     const tq_status s = device_facts(&f);
     if (s != TQ_OK) return s;
@@ -149,8 +156,9 @@ tq_status check_blocks(const Store& c, const uint16_t* q, int32_t hq, const int3
     tq_status s = check_decode_args(&c, q, hq, seq_lens, max_seq_len, TQ_DEFAULT_CHUNK, out);
     if (s != TQ_OK) return s;
     if (blocks == nullptr) return TQ_ERR_NULL;
+    if (c.capacity > kMaxTokens) return TQ_ERR_UNSUPPORTED;
     if (block_shift_of(block_tokens) < 0) return TQ_ERR_UNSUPPORTED;
-    if (n_select < 1 || static_cast<long long>(n_select) * block_tokens >= (1LL << 30)) return TQ_ERR_SHAPE;
+    if (n_select < 1 || n_select > kMaxListed || static_cast<long long>(n_select) * block_tokens >= (1LL << 30)) return TQ_ERR_SHAPE;
     if (!aligned4(blocks) || !aligned4(seq_lens)) return TQ_ERR_ALIGN;
     return TQ_OK;
 }
@@ -258,6 +266,7 @@ tq_status decode_weights(const Store& c, const uint16_t* q, int32_t hq, const in
     tq_status s = check_decode_args(&c, q, hq, seq_lens, max_seq_len, TQ_DEFAULT_CHUNK, out);
     if (s != TQ_OK) return s;
     if (weights == nullptr) return TQ_ERR_NULL;
+    if (c.capacity > kMaxTokens) return TQ_ERR_UNSUPPORTED;
     if (!aligned4(weights) || !aligned4(seq_lens)) return TQ_ERR_ALIGN;
     if (!rotation_flags(flags)) return TQ_ERR_UNSUPPORTED;
     if (decay != decay) return TQ_ERR_SHAPE;
@@ -339,6 +348,7 @@ tq_status evict(const Store& src, const Store& dst, const float* weights, const 
         src.bits != dst.bits)
         return TQ_ERR_SHAPE;
     if (max_seq_len < 1 || keep < 1 || recent < 0 || recent > keep) return TQ_ERR_SHAPE;
+    if (src.capacity > kMaxTokens || dst.capacity > kMaxTokens) return TQ_ERR_UNSUPPORTED;
     if (max_seq_len > src.capacity || keep > dst.capacity) return TQ_ERR_CAPACITY;
     const long long heads = static_cast<long long>(src.batch) * src.num_kv_heads;
     if (heads > 65535) return TQ_ERR_SHAPE;
@@ -357,6 +367,7 @@ tq_status evict(const Store& src, const Store& dst, const float* weights, const 
         for (int j = i + 1; j < 3; ++j)
             if (overlap(writes[i], write_bytes[i], writes[j], write_bytes[j])) return TQ_ERR_SHAPE;
     }
+    if (src.paged && src.k_codes == dst.k_codes && src.map.block_table == dst.map.block_table) return TQ_ERR_SHAPE;
     if (!src.paged && !dst.paged) {
         const unsigned long long bpt = src.head_dim * src.bits / 8, sb = src.head_dim / kGroup * 2ull;
         const void* s_[6] = {src.k_codes, src.v_codes, src.k_scale, src.k_bias, src.v_scale, src.v_bias};

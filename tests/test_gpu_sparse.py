@@ -152,6 +152,21 @@ def test_selection_near_and_equal_scores(D):
         assert np.array_equal(got, select_reference(scores_reference(bounds, q), lens, block, K, 1, 1)), K
 
 
+@pytest.mark.parametrize("scale_q,scale_b", [(1.0, 2.0 ** -20), (2.0 ** -20, 1.0), (2.0 ** -18, 2.0 ** -18), (1e-3, 2.0 ** -16)])
+def test_selection_of_subnormal_numbers(scale_q, scale_b):
+    """fp16 subnormals, whose products the tensor core sums with fewer bits: still the exact order."""
+    torch = need_gpu()
+    import int4_kv_cache_gb300 as tq
+
+    rng = np.random.default_rng(77)
+    B, H, G, D, block, nb, K = 2, 2, 4, 128, 32, 1500, 40
+    x = rng.standard_normal((2, B, H, nb, D)) * 8 * scale_b
+    bounds = np.stack((x.min(0), x.max(0)), 3).astype(np.float16)
+    q = (rng.standard_normal((B, H * G, D)) * 4 * scale_q).astype(np.float16)
+    got = run_select(tq, torch, bounds, q, [nb * block, nb * block - 5], nb * block, block, K, 1, 1, nb * block)
+    assert np.array_equal(got, select_reference(scores_reference(bounds, q), [nb * block, nb * block - 5], block, K, 1, 1))
+
+
 def test_selection_ignores_the_bounds_of_listed_blocks_and_clamps_lengths():
     torch = need_gpu()
     import int4_kv_cache_gb300 as tq

@@ -216,3 +216,17 @@ def test_python_checks_come_before_the_library(L):
         tq.sparse_workspace(1, 8, 2, 128, 1024, 4, block_tokens=48)
     with pytest.raises(ValueError):
         tq.weights_workspace(0, 8, 2, 128, 1024)
+
+
+def test_caches_and_lists_past_the_limits(L):
+    """More than 2^30 tokens, more than 2^24 listed blocks, a paged cache into itself."""
+    big = cache(1, B=1, Hkv=1, D=64, cap=(1 << 30) + 16)
+    small = cache(20, B=1, Hkv=1, D=64, cap=256)
+    assert L.tq_kv_block_bounds(ctypes.byref(big), 64, addr(2), 1, addr(3), None, None) == UNSUPPORTED
+    assert select(L, B=1, hq=1, hkv=1, d=64, cap=(1 << 30) + 16) == UNSUPPORTED
+    assert select(L, n=(1 << 24) + 1) == SHAPE
+    assert L.tq_sdpa_decode_weights(ctypes.byref(big), addr(3), 1, addr(4), 1024, 0.1, 1.0, addr(6), 0, addr(5), 1 << 40, addr(7), None,
+                                    None) == UNSUPPORTED
+    assert evict(L, "contiguous", big, small) == UNSUPPORTED
+    src = paged(1)
+    assert evict(L, "paged", src, src) == SHAPE
