@@ -228,6 +228,8 @@ class KVCache:
     fp16 [B, Hkv, cap, D/64].  ``struct`` is the tq_kv_cache handed to the ABI.
     """
 
+    paged = False
+
     def __init__(self, batch: int, num_kv_heads: int, head_dim: int, capacity: int,
                  device=None, group_size: int = GROUP_SIZE, bits: int = 4):
         nbytes = int(lib().tq_kv_cache_bytes_ex(batch, num_kv_heads, head_dim, group_size, bits, capacity))
@@ -568,26 +570,19 @@ def tq_decode_step_host(cache: KVCache, h_k_new: torch.Tensor, h_v_new: torch.Te
 
 
 # ------------------------------------------------- rotary positions, sparse decode, eviction
-def _same_device(first: torch.Tensor, *others) -> None:
-    """All tensors on one device, the current one (the kernels and the stream are the current device's)."""
-    dev = first.get_device()
-    for t in others:
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"tensors on different devices: {first.device} and {t.device}")
-    if dev != _current_device():
-        raise ValueError(f"tensors on {first.device}, but the current device is cuda:{_current_device()}")
-
-
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
-def _stream_of(t: torch.Tensor, stream):
-    """The given stream's handle, else that of the current stream of t's device (checked to be the current one)."""
+def _on(stream, *tensors):
+    """The handle of the stream to use (None: the current one); all tensors on one device, the current one (the kernels
+    run there)."""
+    dev = _current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"a tensor on {t.device}, but the current device is cuda:{dev}")
     if stream is not None:
         return stream.cuda_stream
-    if _raw_stream is not None:
-        return _raw_stream(t.get_device())
-    return torch.cuda.current_stream().cuda_stream
+    return _raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream().cuda_stream
 
 
 def _rope_rows(x: torch.Tensor, out: Optional[torch.Tensor], b: int, n: int, d: int, stream, name: str):
@@ -618,26 +613,34 @@ def tq_rope_axes(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Te
     the gradient of the rows)."""
     _need(positions, torch.int32, "positions")
     _need(inv_freq, torch.float32, "inv_freq")
-    if q.dim() != 4 or (k is not None and (k.dim() != 4 or k.shape[:2] != q.shape[:2] or k.shape[3] != q.shape[3])):
-        raise ValueError("q and k must be [B, n, heads, D] with the same B, n and D")
+    if q.dim() != 4:
+        raise ValueError(f"q must be [B, n, Hq, D]; got {tuple(q.shape)}")
     b, n, _, d = q.shape
+    if k is not None and (k.dim() != 4 or k.shape != (b, n, k.shape[2], d)):
+        raise ValueError(f"k must be [B, n, Hkv, D] with q's B, n and D; got {tuple(k.shape)}")
     if positions.shape != (len(sections), b, n):
         raise ValueError(f"positions must be [axes, B, n] = {(len(sections), b, n)}; got {tuple(positions.shape)}")
     rq, q_out = _rope_rows(q, q_out, b, n, d, stream, "q")
     rk = None
     if k is not None:
         rk, k_out = _rope_rows(k, k_out, b, n, d, stream, "k")
-    _same_device(q, k, positions, inv_freq, q_out, k_out)
+    on = _on(stream, q, k, positions, inv_freq, q_out, k_out)
     if n > 0:
         _check("tq_rope_axes", lib().tq_rope_axes(rq, rk, positions.data_ptr(), inv_freq.data_ptr(), len(sections),
                                                   (ctypes.c_int32 * len(sections))(*sections), b, n, d, 2 * inv_freq.numel(),
-                                                  int(flags), _stream_of(q, stream)))
+                                                  int(flags), on))
     return (q_out, k_out) if k is not None else q_out
+
+
+_layout_fns = {}
 
 
 def _fn(cache, name: str):
     """The entry point of the cache's layout."""
-    return getattr(lib(), ("tq_paged_" if getattr(cache, "paged", False) else "tq_") + name)
+    fns = _layout_fns.get(name)
+    if fns is None:
+        fns = _layout_fns[name] = (getattr(lib(), "tq_" + name), getattr(lib(), "tq_paged_" + name))
+    return fns[cache.paged]
 
 
 def block_bounds(cache, block_tokens: int = 64) -> torch.Tensor:
@@ -651,9 +654,8 @@ def block_bounds(cache, block_tokens: int = 64) -> torch.Tensor:
 
 def _need_bounds(cache, bounds: torch.Tensor, block_tokens: int) -> None:
     _need(bounds, torch.float16, "bounds")
-    shape = (cache.batch, cache.num_kv_heads, -(-cache.capacity // block_tokens), 2, cache.head_dim)
-    if bounds.shape != shape:
-        raise ValueError(f"bounds must be {shape}; got {tuple(bounds.shape)}")
+    if bounds.shape != (cache.batch, cache.num_kv_heads, -(-cache.capacity // block_tokens), 2, cache.head_dim):
+        raise ValueError(f"bounds must be [B, Hkv, ceil(capacity / block_tokens), 2, D]; got {tuple(bounds.shape)}")
 
 
 def _need_lens(t: torch.Tensor, batch: int, name: str) -> None:
@@ -670,9 +672,9 @@ def tq_kv_block_bounds(cache, bounds: torch.Tensor, start: torch.Tensor, n_rows:
     _need_lens(start, cache.batch, "start")
     if status is not None:
         _need(status, torch.int32, "status")
-    _same_device(cache.buffer, bounds, start, status)
+    on = _on(stream, cache.buffer, bounds, start, status)
     _check("tq_kv_block_bounds", _fn(cache, "kv_block_bounds")(cache.ref(), int(block_tokens), start.data_ptr(), int(n_rows),
-                                                              bounds.data_ptr(), status.data_ptr() if status is not None else None, _stream_of(bounds, stream)))
+                                                              bounds.data_ptr(), status.data_ptr() if status is not None else None, on))
     return bounds
 
 
@@ -720,11 +722,11 @@ def tq_select_blocks(bounds: torch.Tensor, q: torch.Tensor, seq_lens: torch.Tens
     if tuple(bounds.shape) != (b, hkv, -(-int(capacity) // block_tokens), 2, q.shape[2]):
         raise ValueError(f"bounds do not match blocks, q and capacity; got {tuple(bounds.shape)}")
     _need_lens(seq_lens, b, "seq_lens")
-    _same_device(q, bounds, seq_lens, workspace, blocks, status)
+    on = _on(stream, q, bounds, seq_lens, workspace, blocks, status)
     _check("tq_select_blocks", lib().tq_select_blocks(
         bounds.data_ptr(), q.data_ptr(), b, q.shape[1], hkv, q.shape[2], int(capacity), seq_lens.data_ptr(), int(max_seq_len),
         int(block_tokens), n_select, int(n_first), int(n_last), int(flags), workspace.data_ptr(), workspace.numel(),
-        blocks.data_ptr(), status.data_ptr() if status is not None else None, _stream_of(q, stream)))
+        blocks.data_ptr(), status.data_ptr() if status is not None else None, on))
     return blocks
 
 
@@ -739,11 +741,11 @@ def tq_sdpa_blocks_decode(cache, q: torch.Tensor, blocks: torch.Tensor, seq_lens
     _need(workspace, torch.uint8, "workspace")
     if status is not None:
         _need(status, torch.int32, "status")
-    _same_device(cache.buffer, q, blocks, seq_lens, workspace, out, status)
+    on = _on(stream, cache.buffer, q, blocks, seq_lens, workspace, out, status)
     _check("tq_sdpa_blocks_decode", _fn(cache, "sdpa_blocks_decode")(
         cache.ref(), q.data_ptr(), q.shape[1], seq_lens.data_ptr(), int(max_seq_len), float(attn_scale), blocks.data_ptr(),
         blocks.shape[2], int(block_tokens), int(flags), workspace.data_ptr(), workspace.numel(), out.data_ptr(), status.data_ptr() if status is not None else None,
-        _stream_of(q, stream)))
+        on))
     return out
 
 
@@ -759,11 +761,11 @@ def tq_sparse_decode(cache, bounds: torch.Tensor, q: torch.Tensor, seq_lens: tor
     _need(workspace, torch.uint8, "workspace")
     if status is not None:
         _need(status, torch.int32, "status")
-    _same_device(cache.buffer, bounds, q, blocks, seq_lens, workspace, out, status)
+    on = _on(stream, cache.buffer, bounds, q, blocks, seq_lens, workspace, out, status)
     _check("tq_sparse_decode", _fn(cache, "sparse_decode")(
         cache.ref(), bounds.data_ptr(), q.data_ptr(), q.shape[1], seq_lens.data_ptr(), int(max_seq_len), float(attn_scale),
         int(block_tokens), blocks.shape[2], int(n_first), int(n_last), int(flags), workspace.data_ptr(), workspace.numel(),
-        blocks.data_ptr(), out.data_ptr(), status.data_ptr() if status is not None else None, _stream_of(q, stream)))
+        blocks.data_ptr(), out.data_ptr(), status.data_ptr() if status is not None else None, on))
     return out, blocks
 
 
@@ -794,10 +796,10 @@ def tq_sdpa_decode_weights(cache, q: torch.Tensor, seq_lens: torch.Tensor, max_s
     _need(workspace, torch.uint8, "workspace")
     if status is not None:
         _need(status, torch.int32, "status")
-    _same_device(cache.buffer, q, seq_lens, weights, workspace, out, status)
+    on = _on(stream, cache.buffer, q, seq_lens, weights, workspace, out, status)
     _check("tq_sdpa_decode_weights", _fn(cache, "sdpa_decode_weights")(
         cache.ref(), q.data_ptr(), q.shape[1], seq_lens.data_ptr(), int(max_seq_len), float(attn_scale), float(decay),
-        weights.data_ptr(), int(flags), workspace.data_ptr(), workspace.numel(), out.data_ptr(), status.data_ptr() if status is not None else None, _stream_of(q, stream)))
+        weights.data_ptr(), int(flags), workspace.data_ptr(), workspace.numel(), out.data_ptr(), status.data_ptr() if status is not None else None, on))
     return out
 
 
@@ -818,7 +820,7 @@ def tq_kv_evict(src, dst, weights: torch.Tensor, seq_lens: torch.Tensor, max_seq
         raise ValueError(f"kept must be [B, Hkv, keep]; got {tuple(kept.shape)}")
     if status is not None:
         _need(status, torch.int32, "status")
-    _same_device(src.buffer, dst.buffer, weights, seq_lens, dst_weights, dst_lens, kept, status)
+    on = _on(stream, src.buffer, dst.buffer, weights, seq_lens, dst_weights, dst_lens, kept, status)
     _check("tq_kv_evict", _fn(src, "kv_evict")(
         src.ref(), dst.ref(), weights.data_ptr(), seq_lens.data_ptr(), int(max_seq_len), int(keep), int(recent), dst_weights.data_ptr(),
-        dst_lens.data_ptr(), kept.data_ptr(), status.data_ptr() if status is not None else None, _stream_of(weights, stream)))
+        dst_lens.data_ptr(), kept.data_ptr(), status.data_ptr() if status is not None else None, on))
