@@ -297,7 +297,7 @@ struct WeightsParams {
     float* weights;            // [B][Hkv][weight_stride]
     uint16_t* out;             // [B][Hq][D]
     int32_t batch, num_q_heads, num_kv_heads, group_q, max_seq_len, weight_stride, n_parts;
-    int32_t chunks, chunk_tokens;  // set by the launch
+    int32_t chunks, chunk_tokens, heads_per_cta;  // set by the launch
     float decay;
     int32_t rotate_out;
     float rot_scale;

@@ -5,8 +5,8 @@
 // from the scores s_t that phase 1 kept (log2 units) and the merged maximum M
 // and sum L of each head.
 //
-// One launch: the first CTAs of the grid merge outputs (a CTA per query head,
-// a warp per stretch of its parts), the others take a stretch of a kv head's
+// One launch: the first CTAs of the grid merge outputs (a CTA per query head, or
+// a warp where there are few parts), the others take a stretch of a kv head's
 // tokens each, for one sequence as long as leaves one wave of them; every one of them merges the
 // heads' m and l itself (a few hundred numbers from L2, while its first scores
 // are on their way) rather than wait for another kernel.  Bound by the
@@ -58,11 +58,16 @@ __device__ __forceinline__ void merge_parts(const float* m, const float* l, int 
     for (int off = 16; off > 0; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
 }
 
+// The output rows of this CTA's query heads: one head, its parts shared by the
+// eight warps, or (few parts) eight heads, a warp each.
 template <int D>
-__device__ __forceinline__ void merge_output(const WeightsParams& p, long long bh) {
+__device__ __forceinline__ void merge_outputs(const WeightsParams& p, int heads) {
     constexpr int V = D / 32;
     __shared__ float acc_s[kWeightWarps][D];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const bool alone = p.heads_per_cta > 1;  // a warp has a head to itself
+    const long long bh = static_cast<long long>(blockIdx.x) * p.heads_per_cta + (alone ? warp : 0);
+    if (bh >= heads) return;  // the whole warp; no barrier is ahead of it (alone), or the whole CTA
     const int n = p.n_parts;
     const float* m = p.part_m + bh * n;
     float M, L;
@@ -70,8 +75,9 @@ __device__ __forceinline__ void merge_output(const WeightsParams& p, long long b
     float a[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) a[i] = 0.0f;
+    const int step = alone ? 1 : kWeightWarps;
 #pragma unroll 4
-    for (int c = warp; c < n; c += kWeightWarps) {
+    for (int c = alone ? 0 : warp; c < n; c += step) {
         const float w = __ldcg(p.part_l + bh * n + c) > 0.0f ? exp2f(__ldcg(m + c) - M) : 0.0f;
         const float* src = p.part_acc + (bh * n + c) * D + lane * V;
         float x[V];
@@ -94,21 +100,23 @@ __device__ __forceinline__ void merge_output(const WeightsParams& p, long long b
             for (int i = 0; i < V; ++i) a[i] = fmaf(w, x[i], a[i]);
         }
     }
+    if (!alone) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) acc_s[warp][lane * V + i] = a[i];
-    __syncthreads();
-    if (warp != 0) return;
-    float o[V];
+        for (int i = 0; i < V; ++i) acc_s[warp][lane * V + i] = a[i];
+        __syncthreads();
+        if (warp != 0) return;
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        float t = 0.0f;
+        for (int i = 0; i < V; ++i) {
+            a[i] = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kWeightWarps; ++w) t += acc_s[w][lane * V + i];
-        o[i] = L > 0.0f ? __fdiv_rn(t, L) : 0.0f;
+            for (int w = 0; w < kWeightWarps; ++w) a[i] += acc_s[w][lane * V + i];
+        }
     }
-    if (p.rotate_out) hadamard_warp<V>(o, lane, p.rot_scale);
 #pragma unroll
-    for (int i = 0; i < V; ++i) p.out[bh * D + lane * V + i] = __half_as_ushort(__float2half_rn(o[i]));
+    for (int i = 0; i < V; ++i) a[i] = L > 0.0f ? __fdiv_rn(a[i], L) : 0.0f;
+    if (p.rotate_out) hadamard_warp<V>(a, lane, p.rot_scale);
+#pragma unroll
+    for (int i = 0; i < V; ++i) p.out[bh * D + lane * V + i] = __half_as_ushort(__float2half_rn(a[i]));
 }
 
 template <int D>
@@ -118,12 +126,13 @@ __global__ void __launch_bounds__(kWeightThreads) weights_kernel(const WeightsPa
     pdl_wait_primary();
     pdl_launch_dependents();
     const int heads = p.batch * p.num_q_heads;
-    if (static_cast<int>(blockIdx.x) < heads) {
-        merge_output<D>(p, blockIdx.x);
+    const int merging = (heads + p.heads_per_cta - 1) / p.heads_per_cta;  // CTAs
+    if (static_cast<int>(blockIdx.x) < merging) {
+        merge_outputs<D>(p, heads);
         return;
     }
     const int G = p.group_q;
-    const int item = static_cast<int>(blockIdx.x) - heads;
+    const int item = static_cast<int>(blockIdx.x) - merging;
     const int bh = item / p.chunks, b = bh / p.num_kv_heads;  // (sequence, kv head)
     const int t0 = (item - bh * p.chunks) * p.chunk_tokens;
     const int len = min(max(__ldcg(p.seq_lens + b), 0), p.max_seq_len);
@@ -198,7 +207,10 @@ cudaError_t launch_weights(const WeightsParams& p, int head_dim, int sms, cudaSt
     // sequences of up to 8,192 tokens 54.1 us in one wave, 52.0 us in pieces)
     q.chunk_tokens = p.batch > 1 ? kWeightTokens : static_cast<int32_t>(each < pieces ? each : pieces) * kWeightTokens;
     q.chunks = (p.max_seq_len + q.chunk_tokens - 1) / q.chunk_tokens;
-    const long long ctas = static_cast<long long>(p.batch) * (p.num_q_heads + static_cast<long long>(p.num_kv_heads) * q.chunks);
+    // (few: eight at most; with the 15 parts of one short sequence a warp alone
+    // takes 2 us longer than eight)
+    q.heads_per_cta = p.n_parts <= 8 ? kWeightWarps : 1;
+    const long long ctas = (static_cast<long long>(p.batch) * p.num_q_heads + q.heads_per_cta - 1) / q.heads_per_cta + rows * q.chunks;
     if (ctas > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(ctas));
