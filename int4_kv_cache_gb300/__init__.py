@@ -643,18 +643,22 @@ def _fn(cache, name: str):
     return fns[cache.paged]
 
 
+def _block_count(capacity: int, block_tokens: int) -> int:
+    if block_tokens not in (32, 64, 128):
+        raise ValueError(f"block_tokens must be 32, 64 or 128; got {block_tokens}")
+    return -(-int(capacity) // block_tokens)
+
+
 def block_bounds(cache, block_tokens: int = 64) -> torch.Tensor:
     """The bounds of every block of a cache, fp16 [B, Hkv, ceil(capacity / block_tokens), 2, D] (zero-filled;
     tq_kv_block_bounds fills them as rows arrive)."""
-    if int(lib().tq_block_bounds_bytes(cache.batch, cache.num_kv_heads, cache.head_dim, cache.capacity, block_tokens)) == 0:
-        raise ValueError("block_tokens must be 32, 64 or 128")
-    return torch.zeros((cache.batch, cache.num_kv_heads, -(-cache.capacity // block_tokens), 2, cache.head_dim),
+    return torch.zeros((cache.batch, cache.num_kv_heads, _block_count(cache.capacity, block_tokens), 2, cache.head_dim),
                        dtype=torch.float16, device=cache.buffer.device)
 
 
 def _need_bounds(cache, bounds: torch.Tensor, block_tokens: int) -> None:
     _need(bounds, torch.float16, "bounds")
-    if bounds.shape != (cache.batch, cache.num_kv_heads, -(-cache.capacity // block_tokens), 2, cache.head_dim):
+    if bounds.shape != (cache.batch, cache.num_kv_heads, _block_count(cache.capacity, block_tokens), 2, cache.head_dim):
         raise ValueError(f"bounds must be [B, Hkv, ceil(capacity / block_tokens), 2, D]; got {tuple(bounds.shape)}")
 
 
@@ -719,7 +723,7 @@ def tq_select_blocks(bounds: torch.Tensor, q: torch.Tensor, seq_lens: torch.Tens
     if q.dim() != 3 or blocks.dim() != 3 or bounds.dim() != 5 or blocks.shape[0] != q.shape[0]:
         raise ValueError("q must be [B, Hq, D], blocks [B, Hkv, n_select] and bounds [B, Hkv, n_blocks, 2, D]")
     b, hkv, n_select = blocks.shape
-    if tuple(bounds.shape) != (b, hkv, -(-int(capacity) // block_tokens), 2, q.shape[2]):
+    if tuple(bounds.shape) != (b, hkv, _block_count(capacity, block_tokens), 2, q.shape[2]):
         raise ValueError(f"bounds do not match blocks, q and capacity; got {tuple(bounds.shape)}")
     _need_lens(seq_lens, b, "seq_lens")
     on = _on(stream, q, bounds, seq_lens, workspace, blocks, status)

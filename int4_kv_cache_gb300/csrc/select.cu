@@ -55,9 +55,12 @@ __device__ __forceinline__ void add(Pair& a, float x, float x_lo) {
     a.lo = __fadd_rn(__fadd_rn(a.lo, x_lo), e);
     a.hi = s;
 }
-// A key in the order of the sums: hi the sum rounded to fp32, lo the rest.
+// A key in the order of the sums: hi the sum rounded to fp32, lo the rest (an
+// infinite sum has none; its lo is no number).
 __device__ __forceinline__ uint64_t ordered_key(const Pair& a) {
-    const float hi = __fadd_rn(a.hi, a.lo), lo = __fsub_rn(a.lo, __fsub_rn(hi, a.hi));
+    const bool finite = fabsf(a.hi) < INFINITY;
+    const float hi = finite ? __fadd_rn(a.hi, a.lo) : a.hi;
+    const float lo = finite ? __fsub_rn(a.lo, __fsub_rn(hi, a.hi)) : 0.0f;
     return (static_cast<uint64_t>(ordered_key(hi)) << 32) | ordered_key(lo);
 }
 
@@ -242,6 +245,9 @@ __global__ void __launch_bounds__(THREADS, D == 256 ? 1 : 512 / THREADS) select_
             most += 2.0f * D * 0x1p-14f *
                     (__half2float(__ushort_as_half(static_cast<uint16_t>(qm))) +
                      __half2float(__ushort_as_half(static_cast<uint16_t>(bm))) + 0x1p-14f);
+            // an infinite bound (a key above fp16's range), whose zeros times
+            // infinity are no numbers in the sums above: every block is open
+            if (max(qm, bm) >= 0x7c00u) most = INFINITY;
         }
         least = __reduce_min_sync(0xffffffffu, least);
         greatest = __reduce_max_sync(0xffffffffu, greatest);
@@ -355,7 +361,7 @@ __global__ void __launch_bounds__(THREADS, D == 256 ? 1 : 512 / THREADS) select_
 #pragma unroll
                 for (int j = 0; j < NJ; ++j) {
                     const float x = __half2float(__ushort_as_half(q_s[g * D + 32 * j + lane]));
-                    add(sum, __fmul_rn(x, x > 0.0f ? hi[j] : lo[j]), 0.0f);
+                    add(sum, x == 0.0f ? 0.0f : __fmul_rn(x, x > 0.0f ? hi[j] : lo[j]), 0.0f);
                 }
 #pragma unroll
                 for (int off = 16; off > 0; off >>= 1) {

@@ -198,6 +198,30 @@ def test_selection_of_scores_that_are_no_numbers_ends_in_bounds():
     assert ((got >= -1) & (got < 300)).all()
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_selection_with_infinite_bounds(D):
+    """Keys above fp16's range (an infinite greatest or least key): a head that turns away from the channel scores by the other
+    bound, a channel of zero adds nothing, and infinite scores come first, the lowest index first."""
+    torch = need_gpu()
+    import int4_kv_cache_gb300 as tq
+
+    rng = np.random.default_rng(D + 7)
+    B, H, G, block, nb, K = 2, 2, 3, 64, 333, 20
+    bounds = random_bounds(rng, B, H, nb, D)
+    bounds[:, :, 5::9, 1, 3] = np.inf
+    bounds[0, :, 7::31, 0, 4] = -np.inf
+    q = rng.standard_normal((B, H * G, D)).astype(np.float16)
+    q[:, :, 3] = -np.abs(q[:, :, 3]) - np.float16(0.25)  # nobody gains from the infinite channel 3 ...
+    q[1, 1, 3] = 1.0                                     # ... but one head
+    q[0, :, 4] = 0.0                                     # channel 4 counts for nobody
+    g, lo, hi = (x.astype(np.float64) for x in (q.reshape(B, H, G, 1, D), bounds[:, :, None, :, 0], bounds[:, :, None, :, 1]))
+    with np.errstate(invalid="ignore"):
+        scores = np.where(g == 0, 0.0, np.where(g > 0, g * hi, g * lo)).sum(-1).max(2)
+    assert np.isinf(scores[1, 0]).any() and np.isfinite(scores[0]).all() and not np.isnan(scores).any()
+    got = run_select(tq, torch, bounds, q, [nb * block] * B, nb * block, block, K, 1, 1, nb * block)
+    assert np.array_equal(got, select_reference(scores, [nb * block] * B, block, K, 1, 1))
+
+
 # ------------------------------------------------------------ listed attention
 def attend_reference(cache, q, blocks, lens, block, scale, flags=0, tq=None):
     k, v = values(cache, "k"), values(cache, "v")
