@@ -4,18 +4,27 @@
 // their order, into another cache.
 //
 // Two kernels.  select: one cluster of CTAs per (sequence, kv head), each with
-// a stretch of the weights, 8 or 32 a thread in registers (longer stretches are read
-// again, from L2, in every step); the threshold weight by radix selection on
-// the ordered fp32 key: for its first 11 bits every CTA counts into its own
-// histogram and adds what is not zero to the first CTA's, which picks the digit
-// and tells the others; a cluster then gathers the keys that share it in the
-// first CTA, which finds the threshold among them (one CTA, or more than kGather
-// such keys: two more steps of 11 and 10 bits); then the kept rows' indices in order, from counts per warp
-// and prefix sums over warps and CTAs.  copy: the kept rows, codes and
-// scales, 16 bytes a thread, into consecutive rows of the destination, with
-// streaming stores (32 sequences of 4,096 rows 64.1 -> 61.4 us).  Bound
-// by the kept rows' bytes for a batch, by the selection's latency for one
-// sequence.
+// a stretch of the weights, 8 or 16 a thread in registers (longer stretches are
+// read again, from L2, in every step); the threshold weight by radix selection
+// on the ordered fp32 key.  A step costs one exchange: every CTA counts its
+// keys' digit into its own histogram and adds what is not zero to every CTA's
+// sums, from which each finds the digit by itself.  When few enough keys share
+// the digits so far, every CTA sends its own ones, and how many it has above
+// them, to all, and each finds the threshold and its place in the list by
+// itself.  Then the kept rows' indices in order, from counts per warp and
+// prefix sums.  copy: the kept rows and their weights, codes and scales 16
+// bytes a thread, into consecutive rows of the destination, with streaming
+// stores; rows that stay whatever their weight (the last ones; all of a short
+// sequence) are copied while the selection runs.
+//
+// Bound by the kept rows' bytes for a batch: 32 sequences x 8 heads, 4,096 of
+// 4,608 rows each (320 MB), 58.4 us, 5.5 TB/s.  By the selection's chain of
+// steps for one sequence: 4,096 of 131,072 rows x 8 heads 16.0 us, 11 of them
+// the selection.  (With one CTA that finds each digit and the threshold and
+// tells the others, 19.7; the keys in shared memory instead of registers 18.2;
+// 512 threads of 32 keys, whose code is twice as long and fetched once, 17.2.)
+#include <atomic>
+
 #include "tq_device.cuh"
 #include "tq_internal.h"
 #include "tq_radix.cuh"
@@ -24,39 +33,41 @@ namespace tq {
 
 namespace {
 
-constexpr int kEvThreads = 512;
-constexpr int kEvWarps = kEvThreads / 32;
 constexpr int kBins = 2048;
-constexpr int kGather = 4096;  // keys that the first CTA takes over
-static_assert(kBins == 4 * kEvThreads && kEvThreads == 512, "four bins, one digit count a thread");
+constexpr int kShare = 2048;   // keys of a digit that the CTAs send each other
 
+// A key in the order of the weights; 0 is kept for places without one.
 __device__ __forceinline__ uint32_t weight_key(float x) {
     const uint32_t u = __float_as_uint(x + 0.0f);  // -0 -> +0
-    return (u & 0x80000000u) != 0u ? ~u : (u | 0x80000000u);
+    return (u & 0x80000000u) != 0u ? max(~u, 1u) : (u | 0x80000000u);
 }
 
-// V: 16-byte loads of a thread, 2,048 weights of the CTA's stretch each.  ONE:
-// they cover the stretch, which is read once.
-template <int V, bool ONE>
-__global__ void __launch_bounds__(kEvThreads, V == 8 ? 1 : 2) evict_select_kernel(const EvictParams p) {
-    constexpr int kStretch = V * 4 * kEvThreads;
-    constexpr int kRoundWarps = V * kEvWarps;       // 128-weight pieces of a round
+// V: 16-byte loads of a thread.  ONE: they cover the CTA's stretch, which is
+// read once.
+template <int V, int THREADS, bool ONE>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) evict_select_kernel(const EvictParams p) {
+    constexpr int kWarps = THREADS / 32;
+    constexpr int kLoad = 4 * THREADS;              // weights that the CTA loads at a time
+    constexpr int kRound = V * kLoad;               // and holds
+    constexpr int kPieces = V * kWarps;             // of 128 weights
+    constexpr int kOwnBins = kBins / THREADS;       // a thread's
+    extern __shared__ uint32_t found[];             // cluster: kShare keys of each CTA
     __shared__ uint32_t hist[kBins];                // this CTA's counts
-    __shared__ uint32_t sums[kBins];                // the first CTA's: the cluster's counts
-    __shared__ uint32_t wcount[kEvWarps];
-    __shared__ uint32_t piece[kRoundWarps];         // above (low half) and equal (high half) of each piece
+    __shared__ uint32_t sums[2][kBins];             // the cluster's counts, of even and odd steps
+    __shared__ uint32_t wcount[kWarps];
+    __shared__ uint32_t piece[kPieces];             // above (low half) and equal (high half) of each piece
     __shared__ uint32_t pick[3];
-    __shared__ uint32_t found[kGather];             // the first CTA's: keys that share the first digit
-    __shared__ uint32_t n_found;
+    __shared__ uint32_t own[2];                     // this CTA's keys above the digits so far, and those that share them
+    __shared__ uint32_t above_of[8], share_of[8];   // every CTA's
+    __shared__ uint32_t before_cta[2];              // rows of the CTAs before this one: above the threshold, equal to it
     __shared__ uint32_t digits[2][256];
-    __shared__ uint32_t cta_count[2];               // this CTA's rows above the threshold, and equal to it
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int n_cta = p.ctas, rank = static_cast<int>(blockIdx.x) % n_cta;
     const int bh = static_cast<int>(blockIdx.x) / n_cta;
     const int b = bh / p.num_kv_heads;
-    for (int i = threadIdx.x; i < kBins; i += kEvThreads) hist[i] = sums[i] = 0;
-    digits[threadIdx.x >> 8][threadIdx.x & 255] = 0;
-    if (threadIdx.x == 0) n_found = 0;
+    for (int i = threadIdx.x; i < kBins; i += THREADS) hist[i] = sums[0][i] = sums[1][i] = 0;
+    if (threadIdx.x < 512) digits[threadIdx.x >> 8][threadIdx.x & 255] = 0;
+    if (threadIdx.x < 2) own[threadIdx.x] = before_cta[threadIdx.x] = 0;
     pdl_wait_primary();
     pdl_launch_dependents();
     int len = __ldcg(p.seq_lens + b);
@@ -69,224 +80,232 @@ __global__ void __launch_bounds__(kEvThreads, V == 8 ? 1 : 2) evict_select_kerne
     const float* weights = p.weights + static_cast<long long>(bh) * p.weight_stride;
     int32_t* list = p.kept + static_cast<long long>(bh) * p.keep;
     float* out_w = p.out_weights + static_cast<long long>(bh) * p.out_weight_stride;
-    const int part = rank * kEvThreads + threadIdx.x, parts = n_cta * kEvThreads;
+    const int part = rank * THREADS + threadIdx.x, parts = n_cta * THREADS;
     const bool all = len <= p.keep;      // the whole cluster: every row stays
     const int old = len - p.recent;      // else: rows that compete, old > want
     const int want = p.keep - p.recent;  // of them stay
     const bool choose = !all && want > 0;
 
-    // this CTA's stretch [s0, s1), in rounds of kStretch weights
+    // this CTA's stretch [s0, s1), in rounds
     const int per = choose ? ((old + n_cta - 1) / n_cta + 3) & ~3 : 0;
     const int s0 = min(rank * per, old), s1 = min(s0 + per, old);
-    float4 held[V];
-    auto load_round = [&](int base) {
+    float4 w[V];
+    uint32_t keys[V][4];
+    auto load = [&](int base) {
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const int i = base + (v * kEvThreads + threadIdx.x) * 4;
-            if (i < s1) held[v] = __ldg(reinterpret_cast<const float4*>(weights + i));
+            const int i = base + v * kLoad + 4 * threadIdx.x;
+            w[v] = i < s1 ? __ldg(reinterpret_cast<const float4*>(weights + i)) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         }
     };
-    // f(weight, its row) for each of this thread's weights of a round
-    auto visit_round = [&](int base, auto f) {
+    auto make_keys = [&](int base) {
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const int i = base + (v * kEvThreads + threadIdx.x) * 4;
-            const float w[4] = {held[v].x, held[v].y, held[v].z, held[v].w};
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-                if (i + c < s1) f(w[c]);
+            const int n = s1 - base - v * kLoad - 4 * static_cast<int>(threadIdx.x);
+            keys[v][0] = n > 0 ? weight_key(w[v].x) : 0u;
+            keys[v][1] = n > 1 ? weight_key(w[v].y) : 0u;
+            keys[v][2] = n > 2 ? weight_key(w[v].z) : 0u;
+            keys[v][3] = n > 3 ? weight_key(w[v].w) : 0u;
         }
     };
-    if (choose) load_round(s0);
+    // f(key) for each of this thread's weights, and 0 for places without one
+    auto visit = [&](auto f) {
+        for (int base = s0; base < s1; base += kRound) {
+            if (!ONE) {
+                load(base);
+                make_keys(base);
+            }
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) f(keys[v][c]);
+            }
+            if (ONE) break;
+        }
+    };
+    if (ONE && choose) load(s0);
 
     // what needs no selection
-    for (int i = kept + part; i < p.out_weight_stride; i += parts) out_w[i] = 0.0f;
+    for (int i = kept + part; i < p.out_weight_stride; i += parts) out_w[i] = 0.0f;  // (the copy writes the others)
     for (int i = kept + part; i < p.keep; i += parts) list[i] = -1;
     if (bh % p.num_kv_heads == 0 && part == 0) p.out_lens[b] = kept;
     if (all) {
-        for (int i = part; i < len; i += parts) {
-            list[i] = i;
-            out_w[i] = weights[i];
-        }
+        for (int i = part; i < len; i += parts) list[i] = i;
         return;
     }
-    for (int i = part; i < p.recent; i += parts) {
-        list[want + i] = old + i;
-        out_w[want + i] = weights[old + i];
-    }
+    for (int i = part; i < p.recent; i += parts) list[want + i] = old + i;
     if (!choose) return;
 
     if (n_cta > 1) cluster_sync();  // every CTA runs, its counts are zero
     else __syncthreads();
-    uint32_t value = 0, mask = 0;
+    if (ONE) make_keys(s0);
+    // The threshold lies among the keys lo + d, 0 <= d <= last; all keys at first.
+    uint32_t lo = 1u, last = 0xfffffffeu, share = 0;
     int above = 0;
-    for (int pass = 0; pass < 3; ++pass) {
-        const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
-        const uint32_t bins = pass == 2 ? 1024u : 2048u;
-        for (int base = s0; base < s1; base += kStretch) {
-            if (!ONE) load_round(base);
-            visit_round(base, [&](float w) {
-                const uint32_t k = weight_key(w);
-                if ((k & mask) == value) atomicAdd(&hist[(k >> shift) & (bins - 1u)], 1u);
-            });
-            if (ONE) break;
-        }
-        const int top = kBins - 1 - 4 * threadIdx.x;  // this thread's four bins, largest first
+    // digits of 11, 11 and 10 bits, or in a cluster 11, 8, 8 and 5 (what is
+    // sent to every CTA is a histogram at most)
+    for (int pass = 0, shift = 32; shift > 0; ++pass) {
+        shift -= min(shift, pass == 0 || n_cta == 1 ? 11 : 8);
+        visit([&](uint32_t k) {
+            const uint32_t d = k - lo;
+            if (d <= last) atomicAdd(&hist[d >> shift], 1u);
+        });
+        __syncthreads();
+        const int top = kBins - 1 - kOwnBins * threadIdx.x;  // this thread's bins, largest first
+        uint32_t* from = hist;
         if (n_cta > 1) {
-            __syncthreads();
+            from = sums[pass & 1];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < kOwnBins; ++j) {
                 const uint32_t c = hist[top - j];
                 if (c != 0) {
-                    red_cluster_add_u32(&sums[top - j], 0, c);
+                    for (int r = 0; r < n_cta; ++r) red_cluster_add_u32(&from[top - j], r, c);
                     hist[top - j] = 0;
                 }
             }
             cluster_sync();
-        } else {
-            __syncthreads();
         }
-        uint32_t* from = n_cta > 1 ? sums : hist;
-        if (rank == 0) {
-            uint32_t c[4], sum = 0;
+        uint32_t c[kOwnBins], sum = 0;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                c[j] = from[top - j];
-                from[top - j] = 0;
-                sum += c[j];
-            }
-            uint32_t before = sum;
+        for (int j = 0; j < kOwnBins; ++j) {
+            c[j] = from[top - j];
+            from[top - j] = 0;  // (the others add to these sums again after the next step's barrier)
+            sum += c[j];
+        }
+        uint32_t before = sum;
 #pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-                const uint32_t o = __shfl_up_sync(0xffffffffu, before, off);
-                if (lane >= off) before += o;
-            }
-            if (lane == 31) wcount[warp] = before;
-            __syncthreads();
-            before -= sum;
-            for (int w = 0; w < warp; ++w) before += wcount[w];
-            const uint32_t need = static_cast<uint32_t>(want - above);
-            if (before < need && need <= before + sum) {
+        for (int off = 1; off < 32; off <<= 1) {
+            const uint32_t o = __shfl_up_sync(0xffffffffu, before, off);
+            if (lane >= off) before += o;
+        }
+        if (lane == 31) wcount[warp] = before;
+        __syncthreads();
+        before -= sum;
+        for (int w = 0; w < warp; ++w) before += wcount[w];
+        const uint32_t need = static_cast<uint32_t>(want - above);
+        if (before < need && need <= before + sum) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    if (before < need && need <= before + c[j]) {
-                        for (int r = 0; r < n_cta; ++r) {
-                            if (n_cta > 1) {
-                                st_cluster_u32(&pick[0], r, top - j);
-                                st_cluster_u32(&pick[1], r, above + before);
-                                st_cluster_u32(&pick[2], r, c[j]);
-                            } else {
-                                pick[0] = top - j;
-                                pick[1] = above + before;
-                                pick[2] = c[j];
-                            }
-                        }
-                    }
-                    before += c[j];
+            for (int j = 0; j < kOwnBins; ++j) {
+                if (before < need && need <= before + c[j]) {
+                    pick[0] = top - j;
+                    pick[1] = above + before;
+                    pick[2] = c[j];
                 }
+                before += c[j];
             }
         }
-        if (n_cta > 1) cluster_sync();
-        else __syncthreads();
-        value |= pick[0] << shift;
+        __syncthreads();
+        lo += pick[0] << shift;
+        last = min((1u << shift) - 1u, 0xffffffffu - lo);  // (the last digit of the first step ends a key earlier)
         above = static_cast<int>(pick[1]);
-        mask |= (bins - 1u) << shift;
-        const uint32_t share = pick[2];
-        if (pass == 0 && n_cta > 1 && share <= kGather) {  // the same for the cluster
-            for (int base = s0; base < s1; base += kStretch) {
-                if (!ONE) load_round(base);
-                visit_round(base, [&](float w) {
-                    const uint32_t k = weight_key(w);
-                    if ((k & mask) != value) return;
-                    st_cluster_u32(&found[min(atom_cluster_add_u32(&n_found, 0, 1), kGather - 1u)], 0, k);
-                });
-                if (ONE) break;
-            }
-            cluster_sync();
-            if (rank == 0) {
-                int larger;
-                const uint32_t t = nth_largest<kEvThreads, uint32_t>(
-                    want - above, static_cast<int>(share), value, value | ~mask,
-                    [&](auto f) { for (uint32_t i = threadIdx.x; i < share; i += kEvThreads) f(found[i]); }, digits, larger);
-                if (threadIdx.x < n_cta) {
-                    st_cluster_u32(&pick[0], threadIdx.x, t);
-                    st_cluster_u32(&pick[1], threadIdx.x, above + larger);
+        share = pick[2];
+        if (n_cta > 1 && share <= kShare) break;  // the same for the cluster
+        __syncthreads();  // pick and wcount are read before the next step writes them
+    }
+    uint32_t value = lo;      // the threshold
+    uint32_t gt = 0, eq = 0;  // rows above and equal to it before the current round
+    if (n_cta > 1) {
+        const bool sent = share <= kShare;  // (else all bits are known: that many rows equal the threshold)
+        const uint32_t top = lo + last;
+        uint32_t n_above = 0, n_share = 0;
+        visit([&](uint32_t k) {
+            n_above += k > top ? 1u : 0u;
+            if (k - lo > last) return;
+            if (sent) found[rank * kShare + min(atomicAdd(&own[1], 1u), kShare - 1u)] = k;
+            else ++n_share;
+        });
+        n_above = __reduce_add_sync(0xffffffffu, n_above);
+        n_share = __reduce_add_sync(0xffffffffu, n_share);
+        if (lane == 0) {
+            atomicAdd(&own[0], n_above);
+            if (n_share != 0) atomicAdd(&own[1], n_share);
+        }
+        __syncthreads();
+        const int who = warp % n_cta, first = warp / n_cta * 32 + lane, step = THREADS / n_cta;  // a warp or more per CTA
+        if (sent && who != rank) {
+            const int n = static_cast<int>(min(own[1], static_cast<uint32_t>(kShare)));
+            for (int i = first; i < n; i += step) st_cluster_u32(&found[rank * kShare + i], who, found[rank * kShare + i]);
+        }
+        if (threadIdx.x < n_cta) {
+            st_cluster_u32(&above_of[rank], threadIdx.x, own[0]);
+            st_cluster_u32(&share_of[rank], threadIdx.x, own[1]);
+        }
+        cluster_sync();  // (the last one: nothing is written to another CTA from here on)
+        if (sent) {
+            const int n = static_cast<int>(min(share_of[who], static_cast<uint32_t>(kShare)));
+            const uint32_t* theirs = found + who * kShare;
+            int larger;
+            value = lo + nth_largest<THREADS, uint32_t>(
+                want - above, static_cast<int>(share), 0u, last,
+                [&](auto f) { for (int i = first; i < n; i += step) f(theirs[i] - lo); }, digits, larger);
+            above += larger;
+            uint32_t g = 0, e = 0;
+            if (who < rank) {
+                for (int i = first; i < n; i += step) {
+                    g += theirs[i] > value ? 1u : 0u;
+                    e += theirs[i] == value ? 1u : 0u;
                 }
             }
-            cluster_sync();
-            value = pick[0];
-            above = static_cast<int>(pick[1]);
-            break;
+            g = __reduce_add_sync(0xffffffffu, g);
+            e = __reduce_add_sync(0xffffffffu, e);
+            if (lane == 0 && who < rank) {
+                atomicAdd(&before_cta[0], g + (warp < n_cta ? above_of[who] : 0u));
+                atomicAdd(&before_cta[1], e);
+            }
+        } else if (threadIdx.x < rank) {
+            atomicAdd(&before_cta[0], above_of[threadIdx.x]);
+            atomicAdd(&before_cta[1], share_of[threadIdx.x]);
         }
-        if (n_cta == 1) __syncthreads();  // pick and wcount are read before the next pass writes them
+        __syncthreads();
+        gt = before_cta[0];
+        eq = before_cta[1];
     }
     const uint32_t ties = static_cast<uint32_t>(want - above);  // rows equal to the threshold that stay, lowest index first
 
-    // ---- the list.  Rows in order: round, then piece (v, warp) of 128, then lane, then the lane's four.
-    auto counts_of = [&](int base, int v) -> uint32_t {  // of this thread's four: above | equal << 16
-        const int i = base + (v * kEvThreads + threadIdx.x) * 4;
-        const float w[4] = {held[v].x, held[v].y, held[v].z, held[v].w};
-        uint32_t n = 0;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            if (i + c < s1) {
-                const uint32_t k = weight_key(w[c]);
-                n += (k > value ? 1u : 0u) + (k == value ? 0x10000u : 0u);
-            }
+    // ---- the list.  Rows in order: round, then load (v), then warp, then lane, then the lane's four.
+    uint32_t* place = sums[0];  // (free by now) [v][thread]: above | equal << 16 before this thread's four in its piece
+    static_assert(V * THREADS <= 2 * kBins, "a word per thread and load");
+    for (int base = s0; base < s1; base += kRound) {
+        if (!ONE) {
+            load(base);
+            make_keys(base);
         }
-        return n;
-    };
-    uint32_t gt = 0, eq = 0;  // above and equal before the current round
-    if (n_cta > 1) {          // the CTAs before this one
-        uint32_t n_gt = 0, n_eq = 0;
-        for (int base = s0; base < s1; base += kStretch) {
-            if (!ONE) load_round(base);
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const uint32_t n = counts_of(base, v);
-                n_gt += n & 0xffffu;
-                n_eq += n >> 16;
-            }
-            if (ONE) break;
-        }
-        if (threadIdx.x < 2) cta_count[threadIdx.x] = 0;
-        __syncthreads();
-        n_gt = __reduce_add_sync(0xffffffffu, n_gt);
-        n_eq = __reduce_add_sync(0xffffffffu, n_eq);
-        if (lane == 0) {
-            atomicAdd(&cta_count[0], n_gt);
-            atomicAdd(&cta_count[1], n_eq);
-        }
-        cluster_sync();
-        uint32_t c_gt = 0, c_eq = 0;
-        if (lane < rank) {
-            c_gt = ld_cluster_u32(&cta_count[0], lane);
-            c_eq = ld_cluster_u32(&cta_count[1], lane);
-        }
-        gt = __reduce_add_sync(0xffffffffu, c_gt);
-        eq = __reduce_add_sync(0xffffffffu, c_eq);
-        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");  // this CTA has read the others' counts
-    }
-    for (int base = s0; base < s1; base += kStretch) {
-        if (!ONE) load_round(base);
-        uint32_t before[V];
+        uint32_t is_above = 0, is_equal = 0;  // bit 4 v + c
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const uint32_t n = counts_of(base, v);
-            uint32_t incl = n;
 #pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-                const uint32_t o = __shfl_up_sync(0xffffffffu, incl, off);
-                if (lane >= off) incl += o;
+            for (int c = 0; c < 4; ++c) {
+                is_above |= keys[v][c] > value ? 1u << (4 * v + c) : 0u;
+                is_equal |= keys[v][c] == value ? 1u << (4 * v + c) : 0u;
             }
-            before[v] = incl - n;
-            if (lane == 31) piece[v * kEvWarps + warp] = incl;
+        }
+        // the counts of the loads (128 at most in a piece), eight bits each
+        static_assert(V <= 4, "a word of counts");
+        uint32_t n[2] = {0u, 0u};
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            n[0] |= static_cast<uint32_t>(__popc(is_above >> (4 * v) & 15u)) << (8 * v);
+            n[1] |= static_cast<uint32_t>(__popc(is_equal >> (4 * v) & 15u)) << (8 * v);
+        }
+        uint32_t s[2] = {n[0], n[1]};
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const uint32_t o = __shfl_up_sync(0xffffffffu, s[j], off);
+                if (lane >= off) s[j] += o;
+            }
+        }
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            place[v * THREADS + threadIdx.x] = ((s[0] - n[0]) >> (8 * v) & 255u) | ((s[1] - n[1]) >> (8 * v) & 255u) << 16;
+            if (lane == 31) piece[v * kWarps + warp] = (s[0] >> (8 * v) & 255u) | (s[1] >> (8 * v) & 255u) << 16;
         }
         __syncthreads();
         // exclusive prefix over the pieces (a round holds at most 16,384 rows: no carry between the halves)
         if (warp == 0) {
-            constexpr int P = kRoundWarps / 32;
-            static_assert(kRoundWarps % 32 == 0 && kStretch <= 16384, "whole lanes; counts fit 16 bits");
+            constexpr int P = kPieces / 32;
+            static_assert(kPieces % 32 == 0 && kRound <= 16384, "whole lanes; counts fit 16 bits");
             uint32_t c[P], sum = 0;
 #pragma unroll
             for (int j = 0; j < P; ++j) {
@@ -308,31 +327,20 @@ __global__ void __launch_bounds__(kEvThreads, V == 8 ? 1 : 2) evict_select_kerne
             }
         }
         __syncthreads();
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int i = base + (v * kEvThreads + threadIdx.x) * 4;
-            const uint32_t at0 = before[v] + piece[v * kEvWarps + warp];
-            uint32_t g = gt + (at0 & 0xffffu), e = eq + (at0 >> 16);
-            const float w[4] = {held[v].x, held[v].y, held[v].z, held[v].w};
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                if (i + c >= s1) break;
-                const uint32_t k = weight_key(w[c]);
-                if (k > value || (k == value && e < ties)) {
-                    const uint32_t at = g + min(e, ties);
-                    list[at] = i + c;
-                    out_w[at] = w[c];
-                }
-                g += k > value ? 1u : 0u;
-                e += k == value ? 1u : 0u;
-            }
+        for (uint32_t todo = is_above | is_equal; todo != 0; todo &= todo - 1) {
+            const int bit = __ffs(todo) - 1, v = bit >> 2;
+            const uint32_t at0 = place[v * THREADS + threadIdx.x] + piece[v * kWarps + warp];
+            const uint32_t below = (1u << bit) - (1u << (4 * v));  // this thread's rows of the same load before it
+            const uint32_t e = eq + (at0 >> 16) + __popc(is_equal & below);
+            const uint32_t at = gt + (at0 & 0xffffu) + __popc(is_above & below) + min(e, ties);
+            if (((is_above >> bit & 1u) != 0 || e < ties) && at < static_cast<uint32_t>(want))
+                list[at] = base + v * kLoad + 4 * static_cast<int>(threadIdx.x) + (bit & 3);
         }
         gt += wcount[0] & 0xffffu;
         eq += wcount[0] >> 16;
         if (ONE) break;
         __syncthreads();
     }
-    if (n_cta > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // nobody reads this CTA's memory any more
 }
 
 constexpr int kCopyThreads = 256;
@@ -341,16 +349,39 @@ constexpr int kCopyRows = 64;  // destination rows of a CTA
 template <int BPT, int NG>
 __global__ void __launch_bounds__(kCopyThreads) evict_copy_kernel(const EvictCopyParams p) {
     __shared__ long long from[kCopyRows], to[kCopyRows];
-    const int bh = blockIdx.y, b = bh / p.num_kv_heads, h = bh - b * p.num_kv_heads;
-    const int r0 = blockIdx.x * kCopyRows;
-    pdl_wait_primary();
+    const int heads = p.batch * p.num_kv_heads;
+    // the tiles that hold only last rows come first, then each head's others
+    const int others = (p.keep - p.recent + kCopyRows - 1) / kCopyRows, lasts = p.tiles - others;
+    int i = blockIdx.x, tile, bh;
+    if (i < heads * lasts) {
+        bh = i / lasts;
+        tile = others + i - bh * lasts;
+    } else {
+        i -= heads * lasts;
+        bh = i / others;
+        tile = i - bh * others;
+    }
+    const int b = bh / p.num_kv_heads, h = bh - b * p.num_kv_heads;
+    const int r0 = tile * kCopyRows;
+    // The grid starts once every CTA of the selection has seen the launches
+    // before it end.  CTAs whose rows its list does not decide go ahead; the
+    // others wait for it, and every one does before it ends, so that who waits
+    // for this grid has waited for both.
+    const int len = min(max(__ldcg(p.seq_lens + b), 0), p.max_seq_len);
+    const int n = min(kCopyRows, min(len, p.keep) - r0);
+    const bool all = len <= p.keep;
+    const int want = p.keep - p.recent;
+    const bool listed = !all && r0 < want && n > 0;
     pdl_launch_dependents();
-    const int n = min(kCopyRows, min(__ldcg(p.lens + b), p.keep) - r0);
+    if (listed || n <= 0) pdl_wait_primary();
     if (n <= 0) return;
     if (threadIdx.x < n) {
-        const int t = __ldcg(p.kept + static_cast<long long>(bh) * p.keep + r0 + threadIdx.x);
+        const int r = r0 + threadIdx.x;
+        const int t = all ? r : (r < want ? __ldcg(p.kept + static_cast<long long>(bh) * p.keep + r) : len - p.keep + r);
         from[threadIdx.x] = kv_row(p.src_map, p.num_kv_heads, b, h, t, p.status);
-        to[threadIdx.x] = kv_row(p.dst_map, p.num_kv_heads, b, h, r0 + threadIdx.x, p.status);
+        to[threadIdx.x] = kv_row(p.dst_map, p.num_kv_heads, b, h, r, p.status);
+        p.out_weights[static_cast<long long>(bh) * p.out_weight_stride + r] =
+            __ldg(p.weights + static_cast<long long>(bh) * p.weight_stride + t);
     }
     __syncthreads();
     constexpr int PIECES = BPT / 16;
@@ -378,6 +409,23 @@ __global__ void __launch_bounds__(kCopyThreads) evict_copy_kernel(const EvictCop
         if (kv < 2 && rr < n) __stcs(reinterpret_cast<uint4*>((kv ? p.dst_v : p.dst_k) + to[rr] * BPT) + c, x[j]);
     }
     if (r < n) *reinterpret_cast<Row*>(p.dst_sb[a] + to[r] * NG) = s;
+    if (!listed) pdl_wait_primary();
+}
+
+template <int V, int THREADS, bool ONE>
+cudaError_t launch_select_v(cudaLaunchConfig_t& cfg, const EvictParams& p) {
+    static std::atomic<bool> done[64];
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (p.ctas > 1 && (dev < 0 || dev >= 64 || !done[dev].load(std::memory_order_acquire))) {
+        const cudaError_t e = cudaFuncSetAttribute(evict_select_kernel<V, THREADS, ONE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   8 * kShare * static_cast<int>(sizeof(uint32_t)));
+        if (e != cudaSuccess) return e;
+        if (dev >= 0 && dev < 64) done[dev].store(true, std::memory_order_release);
+    }
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = p.ctas > 1 ? static_cast<size_t>(p.ctas) * kShare * sizeof(uint32_t) : 0;
+    return cudaLaunchKernelEx(&cfg, evict_select_kernel<V, THREADS, ONE>, p);
 }
 
 }  // namespace
@@ -385,7 +433,6 @@ __global__ void __launch_bounds__(kCopyThreads) evict_copy_kernel(const EvictCop
 cudaError_t launch_evict_select(const EvictParams& p, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(p.batch) * p.num_kv_heads * p.ctas);
-    cfg.blockDim = dim3(kEvThreads);
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -396,17 +443,19 @@ cudaError_t launch_evict_select(const EvictParams& p, cudaStream_t stream) {
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    const long long most = (static_cast<long long>(p.max_seq_len) - p.recent + p.ctas - 1) / p.ctas;  // a CTA's stretch
-    using Kern = void (*)(EvictParams);
-    const Kern k = most <= kEvStretch / 4 ? evict_select_kernel<2, true>
-                                          : (most <= kEvStretch ? evict_select_kernel<8, true> : evict_select_kernel<8, false>);
-    return cudaLaunchKernelEx(&cfg, k, p);
+    // a CTA's stretch; short ones (batches) leave room for two CTAs on an SM
+    const long long most = ((static_cast<long long>(p.max_seq_len) - p.recent + p.ctas - 1) / p.ctas + 3) / 4 * 4;
+    if (most <= kEvStretch / 4) return launch_select_v<2, 512, true>(cfg, p);
+    return most <= kEvStretch ? launch_select_v<4, 1024, true>(cfg, p) : launch_select_v<4, 1024, false>(cfg, p);
 }
 
 cudaError_t launch_evict_copy(const EvictCopyParams& p, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>((p.keep + kCopyRows - 1) / kCopyRows),
-                       static_cast<unsigned>(p.batch) * p.num_kv_heads);
+    EvictCopyParams q = p;
+    q.tiles = (p.keep + kCopyRows - 1) / kCopyRows;
+    const long long ctas = static_cast<long long>(q.tiles) * p.batch * p.num_kv_heads;
+    if (ctas > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas));
     cfg.blockDim = dim3(kCopyThreads);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -422,7 +471,7 @@ cudaError_t launch_evict_copy(const EvictCopyParams& p, cudaStream_t stream) {
         case 256: k = p.bits == 8 ? evict_copy_kernel<256, 4> : evict_copy_kernel<128, 4>; break;
         default: return cudaErrorInvalidValue;
     }
-    return cudaLaunchKernelEx(&cfg, k, p);
+    return cudaLaunchKernelEx(&cfg, k, q);
 }
 
 }  // namespace tq

@@ -126,25 +126,10 @@ __device__ __forceinline__ float ld_cluster_f32(const void* local, uint32_t rank
 }
 
 // The 32-bit word at the same shared-memory address in CTA `rank`.
-__device__ __forceinline__ uint32_t ld_cluster_u32(const void* local, uint32_t rank) {
-    uint32_t remote, v;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_u32(local)), "r"(rank));
-    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(remote) : "memory");
-    return v;
-}
-
 __device__ __forceinline__ void st_cluster_u32(void* local, uint32_t rank, uint32_t v) {
     uint32_t remote;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_u32(local)), "r"(rank));
     asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(remote), "r"(v) : "memory");
-}
-
-// Adds to the 32-bit word at the same shared-memory address in CTA `rank`; what it held before.
-__device__ __forceinline__ uint32_t atom_cluster_add_u32(void* local, uint32_t rank, uint32_t v) {
-    uint32_t remote, old;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_u32(local)), "r"(rank));
-    asm volatile("atom.relaxed.cluster.shared::cluster.add.u32 %0, [%1], %2;" : "=r"(old) : "r"(remote), "r"(v) : "memory");
-    return old;
 }
 
 // Adds to the 32-bit word at the same shared-memory address in CTA `rank`.

@@ -261,7 +261,7 @@ struct SelectParams {
 };
 
 // Eviction (evict.cu).
-constexpr int kEvStretch = 16384;  // weights a CTA of the selection keeps in registers
+constexpr int kEvStretch = 16384;  // weights a CTA of the selection holds in registers at most
 struct EvictParams {
     const float* weights;      // [B][Hkv][weight_stride]
     const int32_t* seq_lens;   // [B]
@@ -281,9 +281,12 @@ struct EvictCopyParams {
     const uint16_t* src_sb[4]; // k_scale, k_bias, v_scale, v_bias
     uint16_t* dst_sb[4];
     const int32_t* kept;       // [B][Hkv][keep]
-    const int32_t* lens;       // [B] kept rows
+    const int32_t* seq_lens;   // [B], of src
+    const float* weights;      // [B][Hkv][weight_stride]
+    float* out_weights;        // [B][Hkv][out_weight_stride]
     int32_t* status;
-    int32_t num_kv_heads, batch, head_dim, bits, keep;
+    int32_t num_kv_heads, batch, head_dim, bits, max_seq_len, keep, recent, weight_stride, out_weight_stride;
+    int32_t tiles;             // set by the launch
     RowMap src_map, dst_map;
 };
 

@@ -393,8 +393,8 @@ tq_status evict(const Store& src, const Store& dst, const float* weights, const 
     p.recent = recent;
     // As many CTAs (up to eight) as hold the weights in registers, and up to
     // eight with 2,048 weights or more each while every SM still has at most
-    // one.  (Sixteen, past the portable cluster size: 31 us instead of 20 for
-    // one sequence of 131,072 tokens, the clusters not all running at once.)
+    // one.  (Sixteen, past the portable cluster size, took 31 us where eight
+    // took 20 for one sequence of 131,072 tokens: not all clusters ran at once.)
     DeviceFacts* f = nullptr;
     tq_status s = device_facts(&f);
     if (s != TQ_OK) return s;
@@ -422,7 +422,13 @@ tq_status evict(const Store& src, const Store& dst, const float* weights, const 
         c.dst_sb[i] = dsb[i];
     }
     c.kept = kept;
-    c.lens = dst_lens;
+    c.seq_lens = seq_lens;
+    c.weights = weights;
+    c.out_weights = dst_weights;
+    c.weight_stride = src.capacity;
+    c.out_weight_stride = dst.capacity;
+    c.max_seq_len = max_seq_len;
+    c.recent = recent;
     c.status = status;
     c.num_kv_heads = src.num_kv_heads;
     c.batch = src.batch;

@@ -84,6 +84,66 @@ def test_evict_long(n, keep, recent):
     evict_and_check(tq, torch, src, dst, heavy(rng, (1, Hkv, src.capacity)), [n], n, keep, recent)
 
 
+@pytest.mark.parametrize("n,keep,recent", [(131072, 4096, 256), (150001, 70000, 5)])
+@pytest.mark.parametrize("kind", ["equal", "two values", "narrow"])
+def test_evict_long_ties(kind, n, keep, recent):
+    """More keys of one digit than the CTAs of a head send each other, down to the last bit."""
+    torch = need_gpu()
+    import int4_kv_cache_gb300 as tq
+
+    src, dst = tq.KVCache(1, 2, 64, -(-n // 16) * 16), tq.KVCache(1, 2, 64, -(-keep // 16) * 16)
+    src.buffer.random_(0, 256)
+    dst.buffer.zero_()
+    rng = np.random.default_rng(n)
+    shape = (1, 2, src.capacity)
+    w = {"equal": np.full(shape, 3.5), "two values": rng.integers(0, 2, shape) * 0.5,
+         "narrow": 1.0 + rng.integers(0, 30, shape) * 2.0 ** -23}[kind].astype(np.float32)
+    evict_and_check(tq, torch, src, dst, w, [n], n, keep, recent)
+
+
+@pytest.mark.parametrize("graph", [False, True])
+@pytest.mark.parametrize("keep,recent", [(640, 640), (640, 500)])
+def test_evict_between_appends(keep, recent, graph):
+    """Rows that the weights do not decide are copied beside the selection, but after the append before the call and before the
+    one behind it: nothing is waited for on the host."""
+    torch = need_gpu()
+    import int4_kv_cache_gb300 as tq
+
+    B, Hkv, D, n, cap = 3, 2, 128, 2000, 2048
+    src, dst = make_cache(tq, torch, B, Hkv, D, 0, seed=8, capacity=cap), make_cache(tq, torch, B, Hkv, D, 0, seed=9, capacity=1024)
+    rng = np.random.default_rng(keep + recent)
+    rows_of = [dev(torch, rng.standard_normal((2, B, Hkv, n, D)).astype(np.float16)) for _ in range(4)]
+    zero, lens = torch.zeros(B, dtype=torch.int32, device="cuda"), dev(torch, np.array([n, 1500, 600], np.int32))
+    w = dev(torch, heavy(rng, (B, Hkv, cap)))
+    dw, dl = torch.zeros((B, Hkv, 1024), device="cuda"), torch.zeros(B, dtype=torch.int32, device="cuda")
+    kept = torch.zeros((B, Hkv, keep), dtype=torch.int32, device="cuda")
+    want = []
+    for x in rows_of:
+        tq.tq_quantize_kv_append(src, x[0], x[1], zero)
+        want.append(rows(src, "v_codes"))
+    got = [torch.empty_like(dst.v_codes) for _ in rows_of]
+
+    def go():
+        for x, g in zip(rows_of, got):
+            tq.tq_quantize_kv_append(src, x[0], x[1], zero)
+            tq.tq_kv_evict(src, dst, w, lens, n, keep, recent, dw, dl, kept)
+            tq.tq_quantize_kv_append(src, rows_of[0][1], rows_of[0][0], zero)
+            g.copy_(dst.v_codes)
+
+    if graph:
+        c = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(c):
+            go()
+        c.replay()
+    else:
+        go()
+    for x, g in zip(want, got):
+        for b, ln in enumerate((n, 1500, 600)):
+            for h in range(Hkv):
+                r = kept_reference(w.cpu().numpy()[b, h], ln, keep, recent)
+                assert np.array_equal(g.cpu().numpy()[b, h, : len(r)], x[b, h, r])
+
+
 @pytest.mark.parametrize("kind", ["equal", "two values", "signed zeros", "negative", "infinite", "tiny steps"])
 def test_evict_ties_and_odd_weights(kind):
     torch = need_gpu()
