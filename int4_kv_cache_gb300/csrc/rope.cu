@@ -13,7 +13,7 @@
 // Bound by bytes: every row is read and written once.  A CTA takes a token of a
 // sequence, whose cosines and sines are computed once into shared memory and
 // serve every head of q and k; a thread turns 16 elements at a time.  8,192
-// tokens of 64 + 8 heads x 128 (302 MB) take 47.5 us, 6.4 TB/s.  (With two to
+// tokens of 64 + 8 heads x 128 (302 MB) take 47.7 us, 6.3 TB/s.  (With two to
 // sixteen tokens a CTA, whose output rows are neighbours, or two to six units a
 // thread in flight, it took 51 to 74 us; without streaming stores 56 us.)
 #include <cuda_fp16.h>
