@@ -19,12 +19,14 @@
 // or two blocks) is summed again in pairs of fp32 numbers, each step with its
 // exact error (fp16 products are exact in fp32), 48 bits in all, and ranked by
 // that.  (In fp64, whose rate is 1/64 here, the few rows with such blocks took
-// 12 us longer than the others.)
+// 12 us longer than the others; with a general ranking even of a few blocks 6 us
+// longer, now 2: a batch's step 44.3 -> 41.2 us.)
 //
 // One cluster of CTAs per (sequence, kv head): each CTA scores a stretch of
 // blocks and writes the scores into the first CTA's shared memory, which
 // selects.  Bound by latency: 64 of 2,048 blocks x 8 heads (8.4 MB of bounds)
-// take 8.7 us, 32 of up to 512 for each of 32 ragged sequences (35 MB) 15 us.
+// take 8.7 us, 32 of up to 512 for each of 32 ragged sequences (35 MB) 13 us,
+// 8 of them the longest rows' scores.
 #include <cuda_fp16.h>
 
 #include <atomic>
@@ -94,6 +96,8 @@ __global__ void __launch_bounds__(THREADS, D == 256 ? 1 : 512 / THREADS) select_
     __shared__ uint32_t hist[2][256];
     __shared__ int wsum[2][WARPS];
     __shared__ uint64_t red_lo[WARPS], red_hi[WARPS];
+    __shared__ int open_s[32];        // few open blocks, and their exact scores
+    __shared__ uint64_t exact_s[32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int gid = lane >> 2, tig = lane & 3;
     const int n_cta = p.ctas, rank = static_cast<int>(blockIdx.x) % n_cta;
@@ -339,6 +343,80 @@ __global__ void __launch_bounds__(THREADS, D == 256 ? 1 : 512 / THREADS) select_
         return;
     }
     // ---- exact scores of the open blocks, a warp each, and their rank
+    auto exact_score = [&](int blk) -> uint64_t {
+        const uint16_t* row = bounds + static_cast<long long>(blk) * (2 * D);
+        float lo[NJ], hi[NJ];
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+            lo[j] = __half2float(__ushort_as_half(__ldcg(row + 32 * j + lane)));
+            hi[j] = __half2float(__ushort_as_half(__ldcg(row + D + 32 * j + lane)));
+        }
+        Pair sum[8];  // of the heads
+#pragma unroll
+        for (int g = 0; g < 8; ++g) {
+            sum[g] = {0.0f, 0.0f};
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) {
+                const float x = g < G ? __half2float(__ushort_as_half(q_s[g * D + 32 * j + lane])) : 0.0f;
+                add(sum[g], x == 0.0f ? 0.0f : __fmul_rn(x, x > 0.0f ? hi[j] : lo[j]), 0.0f);
+            }
+        }
+        // the lanes halve the heads among themselves: lane bits 4, 3, 2 name this lane's
+#pragma unroll
+        for (int off = 16, half = 4; off >= 4; off >>= 1, half >>= 1) {
+            const bool upper = (lane & off) != 0;
+#pragma unroll
+            for (int i = 0; i < half; ++i) {
+                const Pair give = upper ? sum[i] : sum[half + i];
+                if (upper) sum[i] = sum[half + i];
+                add(sum[i], __shfl_xor_sync(0xffffffffu, give.hi, off), __shfl_xor_sync(0xffffffffu, give.lo, off));
+            }
+        }
+#pragma unroll
+        for (int off = 2; off > 0; off >>= 1)
+            add(sum[0], __shfl_xor_sync(0xffffffffu, sum[0].hi, off), __shfl_xor_sync(0xffffffffu, sum[0].lo, off));
+        uint64_t best = lane >> 2 < G ? ordered_key(sum[0]) : 0;
+#pragma unroll
+        for (int off = 16; off >= 4; off >>= 1) {
+            const uint64_t o = __shfl_xor_sync(0xffffffffu, best, off);
+            best = o > best ? o : best;
+        }
+        return best;
+    };
+    if (n_open <= 32) {  // nearly always: every warp ranks all of them, a lane each
+        for (int i0 = w0, at = before_open; i0 < w1; i0 += 32) {
+            const bool open = i0 + lane < w1 && is_open(i0 + lane);
+            const uint32_t who = __ballot_sync(0xffffffffu, open);
+            if (open) open_s[at + __popc(who & ((1u << lane) - 1u))] = i0 + lane;
+            at += __popc(who);
+        }
+        __syncthreads();
+        for (int j = warp; j < n_open; j += WARPS) {
+            const uint64_t k = exact_score(open_s[j]);
+            if (lane == 0) exact_s[j] = k;
+        }
+        __syncthreads();
+        const uint64_t mine = lane < n_open ? exact_s[lane] : 0;
+        int ahead = 0;
+#pragma unroll 4
+        for (int j = 0; j < n_open; ++j) {
+            const uint64_t o = exact_s[j];
+            ahead += o > mine || (o == mine && j < lane) ? 1 : 0;
+        }
+        const uint32_t chosen = __ballot_sync(0xffffffffu, lane < n_open && ahead < R - n_in);
+        for (int i0 = w0, na = before_in, no = before_open; i0 < w1; i0 += 32) {
+            const int i = i0 + lane;
+            const bool in = i < w1 && is_in(i), open = i < w1 && is_open(i);
+            const uint32_t bi = __ballot_sync(0xffffffffu, in), bo = __ballot_sync(0xffffffffu, open);
+            const uint32_t below = (1u << lane) - 1u;
+            const int rank_o = no + __popc(bo & below);  // open blocks before this one
+            const int at = na + __popc(bi & below) + __popc(rank_o < 32 ? chosen & ((1u << rank_o) - 1u) : chosen);
+            if ((in || (open && (chosen >> (rank_o & 31) & 1u) != 0)) && at < R) list[p.n_first + at] = i;
+            na += __popc(bi);
+            no += __popc(bo);
+        }
+        return;
+    }
     uint64_t* exact = p.exact + static_cast<long long>(bh) * p.exact_stride;
     uint64_t ex_lo = ~0ull, ex_hi = 0ull;
     for (int i0 = c0 + warp * 32; i0 < c1; i0 += THREADS) {
@@ -346,31 +424,7 @@ __global__ void __launch_bounds__(THREADS, D == 256 ? 1 : 512 / THREADS) select_
         while (todo != 0) {
             const int blk = i0 + __ffs(todo) - 1;
             todo &= todo - 1;
-            const uint16_t* row = bounds + static_cast<long long>(blk) * (2 * D);
-            float lo[NJ], hi[NJ];
-#pragma unroll
-            for (int j = 0; j < NJ; ++j) {
-                lo[j] = __half2float(__ushort_as_half(__ldcg(row + 32 * j + lane)));
-                hi[j] = __half2float(__ushort_as_half(__ldcg(row + D + 32 * j + lane)));
-            }
-            uint64_t best = 0;
-#pragma unroll
-            for (int g = 0; g < 8; ++g) {
-                if (g >= G) break;
-                Pair sum = {0.0f, 0.0f};
-#pragma unroll
-                for (int j = 0; j < NJ; ++j) {
-                    const float x = __half2float(__ushort_as_half(q_s[g * D + 32 * j + lane]));
-                    add(sum, x == 0.0f ? 0.0f : __fmul_rn(x, x > 0.0f ? hi[j] : lo[j]), 0.0f);
-                }
-#pragma unroll
-                for (int off = 16; off > 0; off >>= 1) {
-                    const float oh = __shfl_xor_sync(0xffffffffu, sum.hi, off), ol = __shfl_xor_sync(0xffffffffu, sum.lo, off);
-                    add(sum, oh, ol);
-                }
-                const uint64_t k = ordered_key(sum);
-                best = k > best ? k : best;
-            }
+            const uint64_t best = exact_score(blk);
             if (lane == 0) exact[blk] = best;
             ex_lo = best < ex_lo ? best : ex_lo;
             ex_hi = best > ex_hi ? best : ex_hi;

@@ -42,8 +42,9 @@ __device__ __forceinline__ K nth_largest(int n, int count, K lo, K hi, Visit vis
         const int m = min(n_few, kFew);
         const K mine = lane < m ? few[lane] : 0;
         int greater = 0, equal = 0;
+#pragma unroll 4
         for (int j = 0; j < m; ++j) {
-            const K o = __shfl_sync(0xffffffffu, mine, j);
+            const K o = few[j];
             greater += o > mine ? 1 : 0;
             equal += o == mine ? 1 : 0;
         }
