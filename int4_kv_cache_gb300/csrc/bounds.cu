@@ -5,20 +5,21 @@
 //     k_td = fp16(scale_t * code_td + bias_t)
 //
 // A warp takes a block, 128 channels of it at most, 32 tokens at a time, copied
-// (cp.async, three pieces of 32 tokens ahead and on into its next block) into
+// (cp.async, two pieces of 32 tokens ahead and on into its next block) into
 // its own shared memory; the grid is as many warps as run at once.  A lane
 // reads 8 bytes of codes (16 int4 or 8 int8 elements) of every TOK-th token.  A
 // code becomes a packed half in the mantissa of 1024 (1024 + n, or 1024 + 16 n
 // for the odd int4 elements, which saves their shift; both are exact, and so is
-// taking it off again), the value one packed fused multiply-add: 21 operations
-// for the eight elements of an int4 word, shared evenly by the two pipes that
-// do them.  A block that ends early repeats its last row, which changes neither
-// extreme.  The lanes that share channels halve them among themselves at the
-// end.  Bound by those operations: the extremes alone run at 64 lanes a clock
-// and SM, 13 us for 131,072 tokens of 8 int4 heads x 128 (84 MB), which take
-// 25.9 us, 3.2 TB/s.  (As diag(scale) codes + bias on the tensor cores, with
-// fp32 minima and maxima, they took 36 us: the extremes of fp32 values are twice
-// as many operations.)
+// taking it off again), the value one packed fused multiply-add, and the
+// extremes of two tokens' values and those so far one operation each: 17
+// operations for the eight elements of an int4 word.  A block that ends early
+// repeats its last row, which changes neither extreme.  The lanes that share
+// channels halve them among themselves at the end.  Bound by those operations
+// (about a third of the instructions are a piece's copies and a block's end):
+// 131,072 tokens of 8 int4 heads x 128 (84 MB) take 22.0 us, 3.8 TB/s.  (With
+// the extremes token by token 25.9, three pieces ahead 22.1; as diag(scale)
+// codes + bias on the tensor cores, with fp32 minima and maxima, 36: the
+// extremes of fp32 values are twice as many operations.)
 #include <cuda_fp16.h>
 
 #include <atomic>
@@ -34,7 +35,7 @@ namespace {
 constexpr int kBoundsThreads = 128;
 constexpr int kBoundsWarps = kBoundsThreads / 32;
 constexpr int kPiece = 32;   // tokens copied at a time
-constexpr int kAhead = 3;    // pieces in flight
+constexpr int kAhead = 2;    // pieces in flight
 
 __device__ __forceinline__ __half2 as_half2(uint32_t x) { return *reinterpret_cast<__half2*>(&x); }
 __device__ __forceinline__ uint32_t as_u32(__half2 x) { return *reinterpret_cast<uint32_t*>(&x); }
@@ -199,20 +200,26 @@ __global__ void __launch_bounds__(kBoundsThreads) bounds_kernel(const BoundsPara
             auto values = [&](auto partial) {
                 const uint8_t* codes = st + lane * 8;  // row i TOK + tok, 8 bytes from seg
 #pragma unroll
-                for (int i = 0; i < kPiece / C::TOK; ++i) {
-                    const int t = i * C::TOK + tok, ts = (decltype(partial)::value ? min(t, n - 1) : t) * NG;
-                    const uint2 w = *reinterpret_cast<const uint2*>(codes + i * 256);
-                    const __half2 s2 = __half2half2(__ushort_as_half(sc[ts]));
-                    const __half2 z2 = __half2half2(__ushort_as_half(sc[C::SB_BYTES / 2 + ts]));
+                for (int i = 0; i < kPiece / C::TOK; i += 2) {
+                    __half2 s2[2], z2[2];  // two rows at a time: an extreme of three values is one operation
+                    uint2 w[2];
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const int tk = (i + u) * C::TOK + tok, ts = (decltype(partial)::value ? min(tk, n - 1) : tk) * NG;
+                        w[u] = *reinterpret_cast<const uint2*>(codes + (i + u) * 256);
+                        s2[u] = __half2half2(__ushort_as_half(sc[ts]));
+                        z2[u] = __half2half2(__ushort_as_half(sc[C::SB_BYTES / 2 + ts]));
+                    }
 #pragma unroll
                     for (int wd = 0; wd < 2; ++wd) {
-                        __half2 c[C::PW];
-                        code_halves<BITS>(wd ? w.y : w.x, c);
+                        __half2 c0[C::PW], c1[C::PW];
+                        code_halves<BITS>(wd ? w[0].y : w[0].x, c0);
+                        code_halves<BITS>(wd ? w[1].y : w[1].x, c1);
 #pragma unroll
                         for (int j = 0; j < C::PW; ++j) {
-                            const __half2 v = __hfma2(c[j], s2, z2);
-                            lo[wd * C::PW + j] = __hmin2(lo[wd * C::PW + j], v);
-                            hi[wd * C::PW + j] = __hmax2(hi[wd * C::PW + j], v);
+                            const __half2 v0 = __hfma2(c0[j], s2[0], z2[0]), v1 = __hfma2(c1[j], s2[1], z2[1]);
+                            lo[wd * C::PW + j] = __hmin2(lo[wd * C::PW + j], __hmin2(v0, v1));
+                            hi[wd * C::PW + j] = __hmax2(hi[wd * C::PW + j], __hmax2(v0, v1));
                         }
                     }
                 }
