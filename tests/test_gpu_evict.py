@@ -72,7 +72,7 @@ def test_evict(D, bits, keep, recent, paged):
 
 @pytest.mark.parametrize("n,keep,recent", [(131072, 4096, 256), (50000, 1000, 0), (4097, 4096, 1), (9001, 33, 32), (400000, 3000, 100)])
 def test_evict_long(n, keep, recent):
-    """Several CTAs a head; 400,000 weights do not fit their shared memory."""
+    """Several CTAs a head; 400,000 weights do not fit their registers."""
     torch = need_gpu()
     import int4_kv_cache_gb300 as tq
 
