@@ -156,6 +156,12 @@ __device__ __forceinline__ uint32_t high_nibbles(uint32_t x) {
     const __half2 h = __hfma2(*reinterpret_cast<const __half2*>(&x), __float2half2_rn(0.0625f), __float2half2_rn(-64.0f));
     return *reinterpret_cast<const uint32_t*>(&h);
 }
+// The bytes at bits 0..7 / 16..23 as packed halves 0..255, the same way.
+__device__ __forceinline__ uint32_t byte_halves(uint32_t x) {
+    x = (x & kByte) | 0x64006400u;
+    const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&x), __float2half2_rn(1024.0f));
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
 
 struct alignas(8) Half4 {
     __half2 a, b;
@@ -241,11 +247,16 @@ __global__ void __launch_bounds__(Cfg<D, BITS, WIDE>::THREADS, Cfg<D, BITS, WIDE
     constexpr int NG = C::NG;
     constexpr bool BLK = MODE == kModeBlocks;
     static_assert(!(BLK && WIDE), "listed blocks take the four-warp layout");
-    // Kept scores become fp32 weights, and a product of a subnormal operand
-    // loses the bits above the operand's leading one in the tensor core's sums
-    // (weights off by 4e-6 for int4 keys, by 1e-6 at most with normal ones): the
-    // score operands of int4 keys are made normal, one packed operation each.
-    constexpr bool kNormal = MODE == kModeScores && BITS == 4;
+    // Kept scores become fp32 weights, and the tensor core aligns a sum's terms
+    // by their operands' exponents: next to a subnormal operand the others lose
+    // as many bits as it has zeros above its leading one (weights off by 3e-6
+    // instead of 6e-7 for int4 keys of a normal distribution; by 1.4e-4 instead
+    // of 4e-6 for int8 keys whose codes an outlier makes small, head_dim 64,
+    // scores whose terms' magnitudes sum up to 50).  The score operands are made
+    // normal, one packed operation each: 38.2 -> 41.8 us for 131,072 int4 tokens;
+    // 16 ragged int8 sequences of up to 8,192 tokens 52.3 -> 52.4, at head_dim 64
+    // 34.7 -> 36.9, at 256 51.0 -> 55.9.
+    constexpr bool kNormal = MODE == kModeScores;
     __shared__ uint64_t full_bar[C::STAGES];
     __shared__ unsigned int done_cnt[C::STAGES];  // warps finished with the stage, cumulative
     __shared__ float mrg_m[C::NWC][8], mrg_l[C::NWC][8], mrg_t[C::NWC][8];
@@ -772,8 +783,13 @@ __global__ void __launch_bounds__(Cfg<D, BITS, WIDE>::THREADS, Cfg<D, BITS, WIDE
                         const uint32_t xb = e ? x3 : x1;  // rows 8..15
                         if constexpr (BITS == 8) {
                             // bytes 0, 2 -> k 2tig, 2tig+1; bytes 1, 3 -> k 2tig+8, 2tig+9
-                            mma_16816(cg[g], xa & kByte, xb & kByte, (xa >> 8) & kByte, (xb >> 8) & kByte, qb[s][0],
-                                      qb[s][1]);
+                            if constexpr (kNormal) {
+                                mma_16816(cg[g], byte_halves(xa), byte_halves(xb), byte_halves(xa >> 8),
+                                          byte_halves(xb >> 8), qb[s][0], qb[s][1]);
+                            } else {
+                                mma_16816(cg[g], xa & kByte, xb & kByte, (xa >> 8) & kByte, (xb >> 8) & kByte, qb[s][0],
+                                          qb[s][1]);
+                            }
                         } else {
                             const uint32_t ya = xa >> 8, yb = xb >> 8;
                             if constexpr (kNormal) {

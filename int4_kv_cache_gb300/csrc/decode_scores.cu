@@ -1,9 +1,9 @@
 // decode_scores.cu -- the score-keeping instantiations of the phase-1 kernel
 // (decode_mma.cuh, kModeScores): partial states plus every scaled score, for
 // the decode that accumulates attention weights.  Bound as the decode is, by
-// instruction issue, with one operation more per operand word (int4) and the
-// stores of the scores: 131,072 tokens of 64 heads (151 MB read, 33.5 MB
-// written) take 33 to 35 us where the decode's phase 1 takes 29.
+// instruction issue, with one operation more per operand word and the stores of
+// the scores: 131,072 tokens of 64 heads (151 MB read, 33.5 MB written) take 33
+// to 35 us where the decode's phase 1 takes 29.
 #include "decode_mma.cuh"
 
 namespace tq {

@@ -1,0 +1,62 @@
+"""Attention weights of the decode that accumulates them, for the scores that are
+hardest to keep in fp32: keys whose codes an outlier makes small, non-negative
+keys, large queries, two rows that share the softmax.
+
+S is the largest attn_scale * sum_d |q_d| (scale * code_d + |bias_d|) of a row: the
+magnitude of what a score is the sum of.  A weight's relative error is at most
+twice the absolute error of a score (its own, and the rows' in the sum it is
+divided by), plus 2^-20 for the exponential, the sums and the division."""
+import math
+
+import numpy as np
+import pytest
+
+from tests.gpu_helpers import need_gpu
+from tests.operator_helpers import dev, host, rows, values
+
+pytestmark = pytest.mark.gpu
+
+LAYOUTS = [(64, 4), (128, 4), (256, 4), (64, 8), (128, 8), (256, 8)]
+B, HKV, N = 2, 2, 2048
+
+
+def weights_and_reference(tq, torch, k, q, bits):
+    """(kernel's weights, fp64 weights [B, Hkv, N], S [B, Hkv]) of keys k [B, Hkv, N, D] and queries q [B, Hq, D]."""
+    D, G = k.shape[3], q.shape[1] // HKV
+    c = tq.KVCache(B, HKV, D, N, bits=bits)
+    c.buffer.zero_()
+    kt = dev(torch, k.astype(np.float16))
+    tq.tq_quantize_kv_append(c, kt, kt.flip(2).contiguous(), torch.zeros(B, dtype=torch.int32, device="cuda"))
+    q = q.astype(np.float16)
+    w, scale = torch.zeros((B, HKV, N), device="cuda"), 1 / math.sqrt(D)
+    lens = torch.full((B,), N, dtype=torch.int32, device="cuda")
+    tq.tq_sdpa_decode_weights(c, dev(torch, q), lens, N, scale, w, tq.weights_workspace(B, HKV * G, HKV, D, N), decay=0.0)
+    kk, bias = values(c, "k"), np.abs(np.repeat(rows(c, "k_bias").astype(np.float64), 64, -1))
+    parts = kk - np.repeat(rows(c, "k_bias").astype(np.float64), 64, -1) + bias
+    qd = q.astype(np.float64).reshape(B, HKV, G, D)
+    x = qd @ kk.swapaxes(2, 3) * scale
+    p = np.exp(x - x.max(-1, keepdims=True))
+    p = (p / p.sum(-1, keepdims=True)).sum(2)
+    S = (np.abs(qd) @ parts.swapaxes(2, 3) * scale).max((2, 3))
+    return host(w), p, S
+
+
+def small_codes(rng, D, size):
+    """Non-negative keys with one outlier in each group of 64, whose channels the query hardly uses."""
+    k, q = 0.3 * np.abs(rng.standard_normal((B, HKV, N, D))), size * rng.standard_normal((B, 2 * HKV, D))
+    k[..., 5::64] = 60.0
+    q[..., 5::64] *= 0.001
+    return k, q
+
+
+@pytest.mark.parametrize("D,bits", LAYOUTS)
+def test_weights_of_keys_with_small_codes(D, bits):
+    """The contract, 1e-5 over a head's rows (relative L2) where S is at most 64."""
+    torch = need_gpu()
+    import int4_kv_cache_gb300 as tq
+
+    for seed in range(3):
+        k, q = small_codes(np.random.default_rng(seed), D, {64: 22.0, 128: 19.0, 256: 14.0}[D])
+        got, want, S = weights_and_reference(tq, torch, k, q, bits)
+        assert 2 < S.max() <= 64
+        assert (np.linalg.norm(got - want, axis=-1) <= 1e-5 * np.linalg.norm(want, axis=-1)).all()
