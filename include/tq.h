@@ -598,8 +598,13 @@ tq_status tq_paged_sparse_decode(const tq_paged_kv_cache* cache, const uint16_t*
  * (decay = 0: the old value is not read).  weights: fp32 [batch][num_kv_heads]
  * [capacity]; rows from seq_lens[b] on are neither read nor written, so the
  * caller zeroes a row's weight no later than its append (an array that starts
- * as zeros, or that tq_kv_evict wrote, is ready).  The weights' fp32 values are
- * within 1e-5 relative (L2) of fp64 over the same cache.
+ * as zeros, or that tq_kv_evict wrote, is ready).  A weight is as exact as the
+ * scores in fp32 leave it.  With S the largest |attn_scale| sum_d |q_d| (scale
+ * code_d + |bias_d|) of a row (q as it meets the keys: rotated and rounded where
+ * they are), a head's weights are within 1e-5 relative (L2) of fp64 over the same
+ * cache where S is at most 64.  Above, the error grows with S: 1e-7 S over a
+ * head's rows, 2.5e-7 S for a single one are the most that was measured, 2e-5 S
+ * what the sums allow.
  * workspace: tq_weights_workspace_bytes(...) bytes (the scores, 4 bytes per
  * query head and token of max_seq_len, and the decode's), 256-byte aligned, one
  * per call in flight. */

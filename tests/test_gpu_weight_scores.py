@@ -60,3 +60,33 @@ def test_weights_of_keys_with_small_codes(D, bits):
         got, want, S = weights_and_reference(tq, torch, k, q, bits)
         assert 2 < S.max() <= 64
         assert (np.linalg.norm(got - want, axis=-1) <= 1e-5 * np.linalg.norm(want, axis=-1)).all()
+
+
+def two_rows(rng, D, size):
+    """Two rows whose scores differ by little share nearly all of the weight."""
+    k, q = rng.standard_normal((B, HKV, N, D)), size * rng.standard_normal((B, HKV, D))
+    k[:, :, 100] = 3 * np.abs(k[:, :, 100]) * np.sign(q)
+    k[:, :, 1700] = k[:, :, 100] * (1 + 0.002 / size * rng.standard_normal((B, HKV, D)))
+    return k, q
+
+
+def positive(rng, D, size):
+    return np.abs(rng.standard_normal((B, HKV, N, D))), size * np.abs(rng.standard_normal((B, 3 * HKV, D)))
+
+
+@pytest.mark.parametrize("make,size,least", [(two_rows, 1, 60), (two_rows, 20, 1000), (positive, 10, 60), (positive, 60, 300), (small_codes, 100, 10)])
+@pytest.mark.parametrize("D,bits", LAYOUTS)
+def test_weights_of_large_scores(D, bits, make, size, least):
+    """A score sums, for each group of 64 channels, four products of 16 terms one after another (each of whose at most 17
+    addends is cut below 2^-23 of the largest: 68 * 2^-23 of the magnitudes), the query's sum, and the groups with their scale
+    and bias (fewer than 24 roundings, 12 * 2^-23): 80 * 2^-23 S at most, twice that for a weight.  The sums of the weights are
+    at most 64 roundings deep here, and with the exponential and the division below 2^-17."""
+    torch = need_gpu()
+    import int4_kv_cache_gb300 as tq
+
+    k, q = make(np.random.default_rng(D + bits), D, float(size))
+    got, want, S = weights_and_reference(tq, torch, k, q, bits)
+    assert S.max() >= least
+    tol = (160 * 2.0 ** -23 * S + 2.0 ** -17)[..., None]
+    assert (np.abs(got - want) <= tol * want + 1e-37).all()
+    assert np.abs(got.sum(-1) - q.shape[1] // HKV).max() <= 2.0 ** -17 * q.shape[1] // HKV + 160 * 2.0 ** -23 * S.max()
