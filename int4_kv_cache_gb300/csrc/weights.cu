@@ -173,7 +173,8 @@ __global__ void __launch_bounds__(kWeightThreads) weights_kernel(const WeightsPa
             merge_parts(p.part_m + ph * p.n_parts, p.part_l + ph * p.n_parts, p.n_parts, M, L);
         }
         if (lane == 0) {
-            head_m[warp] = M;
+            // (a head without a sum, every score -inf, adds nothing: no -inf - -inf)
+            head_m[warp] = L > 0.0f ? M : 0.0f;
             head_r[warp] = L > 0.0f ? __fdiv_rn(1.0f, L) : 0.0f;
         }
     }

@@ -90,3 +90,34 @@ def test_weights_of_large_scores(D, bits, make, size, least):
     tol = (160 * 2.0 ** -23 * S + 2.0 ** -17)[..., None]
     assert (np.abs(got - want) <= tol * want + 1e-37).all()
     assert np.abs(got.sum(-1) - q.shape[1] // HKV).max() <= 2.0 ** -17 * q.shape[1] // HKV + 160 * 2.0 ** -23 * S.max()
+
+
+@pytest.mark.parametrize("G,D,bits", [(1, 64, 8), (1, 128, 4), (3, 256, 4), (8, 128, 8)])
+def test_heads_whose_every_score_is_minus_infinity_add_nothing(G, D, bits):
+    """Keys of minus infinity (a bias of -inf in every group) under queries that are positive in every channel: the softmax has no
+    sum, the output is zeros, and the weights are decay times themselves.  One of the two kv heads has such keys, in all rows or
+    in the first ones of every run."""
+    torch = need_gpu()
+    import int4_kv_cache_gb300 as tq
+
+    rng = np.random.default_rng(G + D)
+    c = tq.KVCache(B, HKV, D, N, bits=bits)
+    k = dev(torch, rng.standard_normal((B, HKV, N, D)).astype(np.float16))
+    tq.tq_quantize_kv_append(c, k, k.flip(2).contiguous(), torch.zeros(B, dtype=torch.int32, device="cuda"))
+    c.k_bias[0, 0] = -math.inf
+    c.k_bias[1, 1, :700] = -math.inf
+    q = (0.25 + rng.random((B, HKV * G, D))).astype(np.float16)
+    old = rng.random((B, HKV, N)).astype(np.float32)
+    w, ws = dev(torch, old), tq.weights_workspace(B, HKV * G, HKV, D, N)
+    lens, scale = torch.full((B,), N, dtype=torch.int32, device="cuda"), 1 / math.sqrt(D)
+    out = host(tq.tq_sdpa_decode_weights(c, dev(torch, q), lens, N, scale, w, ws, decay=0.5)).reshape(B, HKV, G, D)
+    got = host(w)
+    assert not out[0, 0].any() and np.array_equal(got[0, 0], 0.5 * old[0, 0].astype(np.float64))
+    assert np.array_equal(got[1, 1, :700], 0.5 * old[1, 1, :700].astype(np.float64))
+    kk = values(c, "k")
+    for b, h in ((0, 1), (1, 0), (1, 1)):
+        x = q.reshape(B, HKV, G, D)[b, h].astype(np.float64) @ kk[b, h].T * scale
+        p = np.exp(x - x.max(-1, keepdims=True))
+        want = 0.5 * old[b, h] + (p / p.sum(-1, keepdims=True)).sum(0)
+        # (at most 2^-24 for the sum's rounding, the contract's 1e-5 for the weights: S is below 64 in the finite rows)
+        assert np.linalg.norm(got[b, h] - want) <= 1e-5 * np.linalg.norm(want)
