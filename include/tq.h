@@ -545,7 +545,8 @@ tq_status tq_paged_kv_block_bounds(const tq_paged_kv_cache* cache, int32_t block
  * order is that of the exact scores (blocks whose fp32 scores are too close to
  * the border are scored again to 48 bits, in the workspace).
  * n_first + n_last <= n_select; at most 22,528 blocks (TQ_ERR_UNSUPPORTED).
- * What the bounds of always listed blocks hold does not matter.
+ * What the bounds of always listed blocks hold does not matter.  Where a copy
+ * gave up (TQ_DEV_TIMEOUT), the places of the scored blocks are -1.
  * The bounds are those of a cache of `capacity` tokens.  flags: TQ_ROTATE_K
  * where its keys are stored rotated (TQ_ROTATE_V is ignored).
  * workspace: tq_sparse_workspace_bytes(...) bytes, 256-byte aligned, one per

@@ -86,6 +86,7 @@ __global__ void __launch_bounds__(THREADS, D == 256 ? 1 : 512 / THREADS) select_
     // exponents, which end at that of the smallest normal number.
     constexpr float kEps = static_cast<float>(24 + D / 16) * 0x1p-23f;
     constexpr int kTileBytes = 16 * 4 * D;  // the bounds of 16 blocks
+    constexpr uint32_t kLost = 0xffffffffu;  // in place of a sum of magnitudes (which has no sign bit)
     extern __shared__ __align__(128) uint8_t dyn[];
     uint8_t* stage = dyn + (threadIdx.x >> 5) * kTileBytes;              // this warp's tile
     uint32_t* keys = reinterpret_cast<uint32_t*>(dyn + WARPS * kTileBytes);  // the first CTA's: one per block of the sequence
@@ -181,8 +182,10 @@ __global__ void __launch_bounds__(THREADS, D == 256 ? 1 : 512 / THREADS) select_
             const uint8_t* a1 = stage + min(gid + 8, rows - 1) * (4 * D) + 16 * tig;
             float s[4] = {0.0f, 0.0f, 0.0f, 0.0f}, up[4] = {0.0f, 0.0f, 0.0f, 0.0f}, un[4] = {0.0f, 0.0f, 0.0f, 0.0f};
             uint32_t m0 = 0u, m1 = 0u;  // largest magnitudes of the two rows
-            if (!mbar_wait_bounded(&bar[warp], parity)) {
-                if (p.status != nullptr) atomicOr(p.status, TQ_DEV_TIMEOUT);
+            // (each lane has a time limit of its own: the warp goes on or gives up as one)
+            if (!__all_sync(0xffffffffu, mbar_wait_bounded(&bar[warp], parity))) {
+                if (p.status != nullptr && lane == 0) atomicOr(p.status, TQ_DEV_TIMEOUT);
+                parity = 2u;  // a tile never arrived: the warp's other blocks have no scores
                 break;
             }
             parity ^= 1u;
@@ -256,7 +259,7 @@ __global__ void __launch_bounds__(THREADS, D == 256 ? 1 : 512 / THREADS) select_
         least = __reduce_min_sync(0xffffffffu, least);
         greatest = __reduce_max_sync(0xffffffffu, greatest);
         if (lane == 0) {
-            st_cluster_u32(&warp_abs[rank * WARPS + warp], 0, __float_as_uint(most));
+            st_cluster_u32(&warp_abs[rank * WARPS + warp], 0, parity > 1u ? kLost : __float_as_uint(most));
             st_cluster_u32(&warp_lo[rank * WARPS + warp], 0, least);
             st_cluster_u32(&warp_hi[rank * WARPS + warp], 0, greatest);
         }
@@ -272,10 +275,16 @@ __global__ void __launch_bounds__(THREADS, D == 256 ? 1 : 512 / THREADS) select_
     if (R == 0) return;
     float eps = 0.0f;
     uint32_t key_lo = 0xffffffffu, key_hi = 0u;
+    bool no_scores = false;
     for (int i = lane; i < n_cta * WARPS; i += 32) {
+        no_scores |= warp_abs[i] == kLost;
         eps = fmaxf(eps, __uint_as_float(warp_abs[i]));
         key_lo = min(key_lo, warp_lo[i]);
         key_hi = max(key_hi, warp_hi[i]);
+    }
+    if (__any_sync(0xffffffffu, no_scores)) {  // the same for the CTA: places without a block instead of unknown ones
+        for (int i = threadIdx.x; i < R; i += THREADS) list[p.n_first + i] = -1;
+        return;
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) eps = fmaxf(eps, __shfl_xor_sync(0xffffffffu, eps, off));
