@@ -634,9 +634,11 @@ tq_status tq_paged_sdpa_decode_weights(const tq_paged_kv_cache* cache, const uin
  *                row, -1 behind the last
  * Rows of dst behind the kept ones are left as they were.  Both caches have
  * the same batch, heads, head_dim and bits; 0 <= recent <= keep <= dst
- * capacity; batch * num_kv_heads <= 65,535.  What is written must not overlap
- * what is read (TQ_ERR_SHAPE); paged caches may share a pool (not the table),
- * but a page in both tables (or twice in dst's) gives undefined rows. */
+ * capacity; batch * num_kv_heads <= 65,535.  What is written (dst's arrays,
+ * dst_weights, dst_lens, kept) must not overlap what is read (src's arrays, the
+ * tables, weights, seq_lens) or one another (TQ_ERR_SHAPE); paged caches may
+ * share a pool (the same six arrays and page size; not the table), but a page
+ * in both tables (or twice in dst's) gives undefined rows. */
 tq_status tq_kv_evict(const tq_kv_cache* src, const tq_kv_cache* dst, const float* weights,
                       const int32_t* seq_lens, int32_t max_seq_len, int32_t keep, int32_t recent,
                       float* dst_weights, int32_t* dst_lens, int32_t* kept, int32_t* status, void* stream);

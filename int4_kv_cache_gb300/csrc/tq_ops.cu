@@ -15,6 +15,7 @@ bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0
 
 // Whether [a, a + na) and [b, b + nb) share a byte.
 bool overlap(const void* a, unsigned long long na, const void* b, unsigned long long nb) {
+    if (na == 0 || nb == 0) return false;
     const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
     return x < y + nb && y < x + na;
 }
@@ -354,28 +355,40 @@ tq_status evict(const Store& src, const Store& dst, const float* weights, const 
     if (heads > 65535) return TQ_ERR_SHAPE;
     if (!aligned16(weights) || !aligned4(seq_lens) || !aligned4(dst_weights) || !aligned4(dst_lens) || !aligned4(kept))
         return TQ_ERR_ALIGN;
-    const unsigned long long in_w = heads * src.capacity * 4ull, out_w = heads * dst.capacity * 4ull,
-                             n_kept = heads * keep * 4ull, n_len = src.batch * 4ull;
-    // the rows are read by some CTAs while others write: nothing written may be read
-    const void* reads[2] = {weights, seq_lens};
-    const unsigned long long read_bytes[2] = {in_w, n_len};
-    const void* writes[3] = {dst_weights, dst_lens, kept};
-    const unsigned long long write_bytes[3] = {out_w, n_len, n_kept};
-    for (int i = 0; i < 3; ++i) {
-        for (int j = 0; j < 2; ++j)
-            if (overlap(writes[i], write_bytes[i], reads[j], read_bytes[j])) return TQ_ERR_SHAPE;
-        for (int j = i + 1; j < 3; ++j)
-            if (overlap(writes[i], write_bytes[i], writes[j], write_bytes[j])) return TQ_ERR_SHAPE;
-    }
-    if (src.paged && src.k_codes == dst.k_codes && src.map.block_table == dst.map.block_table) return TQ_ERR_SHAPE;
-    if (!src.paged && !dst.paged) {
-        const unsigned long long bpt = src.head_dim * src.bits / 8, sb = src.head_dim / kGroup * 2ull;
-        const void* s_[6] = {src.k_codes, src.v_codes, src.k_scale, src.k_bias, src.v_scale, src.v_bias};
-        const void* d_[6] = {dst.k_codes, dst.v_codes, dst.k_scale, dst.k_bias, dst.v_scale, dst.v_bias};
-        for (int i = 0; i < 6; ++i)
-            for (int j = 0; j < 6; ++j)
-                if (overlap(s_[i], heads * src.capacity * (i < 2 ? bpt : sb), d_[j], heads * dst.capacity * (j < 2 ? bpt : sb)))
-                    return TQ_ERR_SHAPE;
+    // The rows are read by some CTAs while others write: nothing written may be
+    // read, or written twice.  (Rows of one pool are told apart by their pages.)
+    struct Range {
+        const void* at;
+        unsigned long long bytes;
+    };
+    auto arrays = [](const Store& c, Range* r) {
+        const unsigned long long rows = static_cast<unsigned long long>(c.map.num_pages) * c.num_kv_heads * c.map.page_tokens;
+        const unsigned long long codes = rows * (c.head_dim * c.bits / 8), sb = rows * (c.head_dim / kGroup * 2);
+        const void* at[6] = {c.k_codes, c.v_codes, c.k_scale, c.k_bias, c.v_scale, c.v_bias};
+        for (int i = 0; i < 6; ++i) r[i] = {at[i], i < 2 ? codes : sb};
+    };
+    const unsigned long long lens_bytes = src.batch * 4ull, table_bytes = src.paged ? lens_bytes * src.map.max_pages : 0,
+                             dst_table_bytes = dst.paged ? lens_bytes * dst.map.max_pages : 0;
+    Range reads[10], writes[9];
+    arrays(src, reads);
+    arrays(dst, writes);
+    reads[6] = {weights, heads * src.capacity * 4ull};
+    reads[7] = {seq_lens, lens_bytes};
+    reads[8] = {src.map.block_table, table_bytes};
+    reads[9] = {dst.map.block_table, dst_table_bytes};
+    writes[6] = {dst_weights, heads * dst.capacity * 4ull};
+    writes[7] = {dst_lens, lens_bytes};
+    writes[8] = {kept, heads * keep * 4ull};
+    bool one_pool = src.paged && src.map.page_tokens == dst.map.page_tokens;
+    for (int i = 0; i < 6; ++i) one_pool = one_pool && reads[i].at == writes[i].at;
+    if (one_pool && src.map.block_table == dst.map.block_table) return TQ_ERR_SHAPE;
+    for (int i = 0; i < 9; ++i) {
+        for (int j = 0; j < 10; ++j) {
+            if (one_pool && i < 6 && j < 6) continue;
+            if (overlap(writes[i].at, writes[i].bytes, reads[j].at, reads[j].bytes)) return TQ_ERR_SHAPE;
+        }
+        for (int j = i + 1; j < 9; ++j)
+            if (overlap(writes[i].at, writes[i].bytes, writes[j].at, writes[j].bytes)) return TQ_ERR_SHAPE;
     }
     EvictParams p{};
     p.weights = weights;
