@@ -177,6 +177,18 @@ def _stream(stream: Optional[torch.cuda.Stream]):
     return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
 
 
+def _new(shape, dtype, device, stream) -> torch.Tensor:
+    """An output that a call on ``stream`` makes.  On another stream than the current one it is that stream's memory (memory of
+    the current one may still be in use there by what its last owner queued), kept until the current stream, where the caller
+    goes on with it, is past its use."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        out = torch.empty(shape, dtype=dtype, device=device)
+    out.record_stream(torch.cuda.current_stream(out.device))
+    return out
+
+
 def _need(t: torch.Tensor, dtype, name: str) -> None:
     if not t.is_cuda or t.dtype != dtype or not t.is_contiguous():
         raise ValueError(f"{name}: expected a contiguous CUDA {dtype} tensor, got {t.dtype} on {t.device}")
@@ -357,7 +369,7 @@ def tq_sdpa_int4_decode(cache: KVCache, q: torch.Tensor, seq_lens: torch.Tensor,
     _need(seq_lens, torch.int32, "seq_lens")
     _need(workspace, torch.uint8, "workspace")
     if out is None:
-        out = torch.empty_like(q)
+        out = torch.empty_like(q) if stream is None else _new(q.shape, q.dtype, q.device, stream)
     _need(out, torch.float16, "out")
     if status is not None:
         _need(status, torch.int32, "status")
@@ -394,7 +406,7 @@ def tq_decode_step(cache: KVCache, k_new: torch.Tensor, v_new: torch.Tensor, wri
                      (workspace, "workspace", torch.uint8)):
         _need(t, dt, n)
     if out is None:
-        out = torch.empty_like(q)
+        out = torch.empty_like(q) if stream is None else _new(q.shape, q.dtype, q.device, stream)
     _need(out, torch.float16, "out")
     if status is not None:
         _need(status, torch.int32, "status")
@@ -458,9 +470,8 @@ def tq_sdpa_int4_partial(cache: KVCache, q: torch.Tensor, seq_lens: torch.Tensor
     else:
         n_parts = tq_sdpa_plan(cache, Hq, max_seq_len, chunk, impl)[0]
     if out is None:
-        m = torch.empty((B, Hq, n_parts), dtype=torch.float32, device=q.device)
-        l = torch.empty_like(m)
-        acc = torch.empty((B, Hq, n_parts, D), dtype=torch.float32, device=q.device)
+        m, l = (_new((B, Hq, n_parts), torch.float32, q.device, stream) for _ in range(2))
+        acc = _new((B, Hq, n_parts, D), torch.float32, q.device, stream)
     else:
         m, l, acc = out
         if m.numel() < B * Hq * n_parts or acc.numel() < B * Hq * n_parts * D:
@@ -479,7 +490,7 @@ def tq_sdpa_int4_reduce(m: torch.Tensor, l: torch.Tensor, acc: torch.Tensor, out
         _need(t, torch.float32, n)
     B, Hq, n, D = acc.shape
     if out is None:
-        out = torch.empty((B, Hq, D), dtype=torch.float16, device=acc.device)
+        out = _new((B, Hq, D), torch.float16, acc.device, stream)
     _need(out, torch.float16, "out")
     _check("tq_sdpa_int4_reduce", lib().tq_sdpa_int4_reduce(_ptr(m), _ptr(l), _ptr(acc), B, Hq, D, n, _ptr(out),
                                                             _stream(stream)))
@@ -495,7 +506,7 @@ def tq_sdpa_int4_decode_noalloc(cache: KVCache, q: torch.Tensor, seq_lens: torch
     _need(q, torch.float16, "q")
     _need(seq_lens, torch.int32, "seq_lens")
     if out is None:
-        out = torch.empty_like(q)
+        out = torch.empty_like(q) if stream is None else _new(q.shape, q.dtype, q.device, stream)
     _need(out, torch.float16, "out")
     if status is not None:
         _need(status, torch.int32, "status")
@@ -514,7 +525,7 @@ def tq_dequantize_kv(cache: KVCache, n_rows: int, out=None, stream=None):
     shape = (cache.batch, cache.num_kv_heads, int(n_rows), cache.head_dim)
     if out is None:
         dev = cache.buffer.device
-        out = (torch.empty(shape, dtype=torch.float16, device=dev), torch.empty(shape, dtype=torch.float16, device=dev))
+        out = (_new(shape, torch.float16, dev, stream), _new(shape, torch.float16, dev, stream))
     k, v = out
     for t, n in ((k, "k_out"), (v, "v_out")):
         _need(t, torch.float16, n)
@@ -529,7 +540,7 @@ def tq_hadamard_rotate(x: torch.Tensor, out: Optional[torch.Tensor] = None, stre
     normalised Sylvester Hadamard matrix (out may be x)."""
     _need(x, torch.float16, "x")
     if out is None:
-        out = torch.empty_like(x)
+        out = torch.empty_like(x) if stream is None else _new(x.shape, x.dtype, x.device, stream)
     _need(out, torch.float16, "out")
     if out.shape != x.shape:
         raise ValueError("out must have the shape of x")
@@ -591,9 +602,8 @@ def _rope_rows(x: torch.Tensor, out: Optional[torch.Tensor], b: int, n: int, d: 
         raise ValueError(f"{name}: expected a CUDA float16 tensor [B, n, heads, D] with a contiguous last dimension")
     h = x.shape[2]
     if out is None:
-        out = torch.empty((b, h, n, d), dtype=torch.float16, device=x.device)
-        if stream is not None:
-            out.record_stream(stream)
+        shape = (b, h, n, d)
+        out = torch.empty(shape, dtype=torch.float16, device=x.device) if stream is None else _new(shape, torch.float16, x.device, stream)
     else:
         _need(out, torch.float16, name + "_out")
         if out.shape != (b, h, n, d):
@@ -700,9 +710,7 @@ def _need_blocks(cache, blocks: torch.Tensor) -> None:
 def _need_query(cache, q: torch.Tensor, out: Optional[torch.Tensor], stream) -> torch.Tensor:
     _need(q, torch.float16, "q")
     if out is None:
-        out = torch.empty_like(q)
-        if stream is not None:
-            out.record_stream(stream)
+        out = torch.empty_like(q) if stream is None else _new(q.shape, q.dtype, q.device, stream)
     _need(out, torch.float16, "out")
     if q.dim() != 3 or q.shape[0] != cache.batch or q.shape[2] != cache.head_dim or out.shape != q.shape:
         raise ValueError(f"q must be [B, Hq, D]; got {tuple(q.shape)}")
