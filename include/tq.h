@@ -519,9 +519,11 @@ tq_status tq_rope_axes(const tq_rope_rows* q, const tq_rope_rows* k, const int32
  *
  * Bounds: for every block and kv head the least and the greatest cached key of
  * each channel, fp16 [batch][num_kv_heads][ceil(capacity / block_tokens)][2]
- * [head_dim] (0: least, 1: greatest), of fp16(scale * code + bias); of the
- * rotated keys where keys are stored rotated.  tq_block_bounds_bytes: their
- * size (0 for invalid sizes).
+ * [head_dim] (0: least, 1: greatest), of the keys scale * code + bias rounded to
+ * the nearest fp16 (the decode does not round them); of the rotated keys where
+ * keys are stored rotated.  Keys that are no numbers (an infinite scale times
+ * code 0, say) are left out of them.  tq_block_bounds_bytes: their size (0 for
+ * invalid sizes).
  * tq_kv_block_bounds recomputes the bounds of every block that rows
  * [start[b], start[b] + n_rows) of sequence b touch, from the block's rows
  * below start[b] + n_rows: call it after each append with its write_pos and
@@ -541,9 +543,12 @@ tq_status tq_paged_kv_block_bounds(const tq_paged_kv_cache* cache, int32_t block
  * all of them if nb <= n_select; else the first n_first, the last n_last and,
  * of the others, the n_select - n_first - n_last of greatest score
  *   max over the kv head's query heads of  sum_d max(q_d least_d, q_d greatest_d),
- * no q.k of the block exceeds it.  Equal scores: the lowest index first.  The
- * order is that of the exact scores (blocks whose fp32 scores are too close to
- * the border are scored again to 48 bits, in the workspace).
+ * which no q.k of the block exceeds by more than its keys' rounding, 2^-11
+ * sum_d |q_d k_d| (2^-25 |q_d| where fp16 is subnormal).  Equal scores: the
+ * lowest index first.  The order is that of the exact scores of these bounds
+ * (blocks whose fp32 scores are too close to the border are scored again to 48
+ * bits, in the workspace).  With a query or bounds that are no numbers the list
+ * holds blocks of the sequence or -1, but which is not said.
  * n_first + n_last <= n_select; at most 22,528 blocks (TQ_ERR_UNSUPPORTED).
  * What the bounds of always listed blocks hold does not matter.  Where a copy
  * gave up (TQ_DEV_TIMEOUT), the places of the scored blocks are -1.
@@ -565,7 +570,9 @@ tq_status tq_select_blocks(const uint16_t* bounds, const uint16_t* q, int32_t ba
  * listed blocks: blocks [batch][num_kv_heads][n_select], entries below 0 are
  * empty, an entry that starts at or past seq_lens[b] sets TQ_DEV_BLOCK and is
  * left out.  Any order; a block listed twice counts twice.  A kv head whose
- * list is empty gives zero output rows.  Precision as the decode's. */
+ * list is empty gives zero output rows.  Precision as the decode's, and as
+ * there rows whose scale or bias is not finite leave their heads' outputs
+ * undefined. */
 tq_status tq_sdpa_blocks_decode(const tq_kv_cache* cache, const uint16_t* q, int32_t num_q_heads,
                                 const int32_t* seq_lens, int32_t max_seq_len, float attn_scale,
                                 const int32_t* blocks, int32_t n_select, int32_t block_tokens,
@@ -599,7 +606,9 @@ tq_status tq_paged_sparse_decode(const tq_paged_kv_cache* cache, const uint16_t*
  * (decay = 0: the old value is not read).  weights: fp32 [batch][num_kv_heads]
  * [capacity]; rows from seq_lens[b] on are neither read nor written, so the
  * caller zeroes a row's weight no later than its append (an array that starts
- * as zeros, or that tq_kv_evict wrote, is ready).  A weight is as exact as the
+ * as zeros, or that tq_kv_evict wrote, is ready).  A query head whose every
+ * score is -inf adds nothing; where scores are no numbers, outputs and weights
+ * of their kv head are undefined.  A weight is as exact as the
  * scores in fp32 leave it.  With S the largest |attn_scale| sum_d |q_d| (scale
  * code_d + |bias_d|) of a row (q as it meets the keys: rotated and rounded where
  * they are), a head's weights are within 1e-5 relative (L2) of fp64 over the same

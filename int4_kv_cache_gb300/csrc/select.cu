@@ -1,15 +1,16 @@
 // select.cu -- the blocks of a sequence that a cheap score selects for its
 // query ("sparse attention"): for a kv head, a block's score is
 //     max over the group's query heads of  sum_d max(q_d lo_d, q_d hi_d),
-// an upper bound of q.k over the block's keys (lo, hi: bounds.cu).  The first
-// n_first and the last n_last blocks are always listed, the others by score,
+// an upper bound of q.k over the block's keys (lo, hi: bounds.cu), but for the
+// bounds' rounding to the nearest fp16.  The first n_first and the last n_last blocks are always listed, the others by score,
 // equal scores the lowest index first; the list is ascending.
 //
 // The sum splits into q+ . hi + q- . lo (q+ = max(q, 0), q- = min(q, 0)), a
-// matrix product: mma.sync m16n8k16 with M = 16 blocks, N = the group's heads,
-// the bounds going from global memory straight into the A fragments (a lane's
-// 16 bytes are two k-steps of one row; the query fragments use the same
-// order), so every byte of the bounds is read once, by 16-byte loads.
+// matrix product: mma.sync m16n8k16 with M = 16 blocks, N = the group's heads.
+// Each warp copies its tiles of 16 blocks into shared memory (one bulk copy
+// each, every byte of the bounds read once) and takes the A fragments from
+// there by 16-byte loads (a lane's 16 bytes are two k-steps of one row; the query
+// fragments use the same order).
 //
 // The list must be that of the exact scores, whatever the order of summation:
 // the product's fp32 sums are off by at most kEps * sum |terms|, which a second

@@ -174,6 +174,9 @@ tq_status run_blocks(const Store& c, const uint16_t* q, int32_t hq, const int32_
     const int di = dim_index(c.head_dim), bi = c.bits == 8 ? 1 : 0;
     const int tile = mma_tile_tokens(c.head_dim, c.bits, false);
     const bool merge = !(flags & TQ_ROTATE_V);
+    // (The plan's slots and clusters are those of the decode's paged kernel,
+    // whose layout this one has; where they differed the plan would be a slower
+    // one, and a cluster too many is refused and handled below.)
     const Plan pl = make_plan(c.batch, c.num_kv_heads, n_select * block_tokens, tile, tile, f->sms * f->mma_ctas[bi][di],
                               merge, f->clusters[bi][di][1]);
     if (pl.n_splits > kMaxReduceParts || c.num_kv_heads > 65535 || c.batch > 65535) return TQ_ERR_SHAPE;
