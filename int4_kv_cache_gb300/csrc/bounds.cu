@@ -14,12 +14,15 @@
 // extremes of two tokens' values and those so far one operation each: 17
 // operations for the eight elements of an int4 word.  A block that ends early
 // repeats its last row, which changes neither extreme.  The lanes that share
-// channels halve them among themselves at the end.  Bound by those operations
-// (about a third of the instructions are a piece's copies and a block's end):
-// 131,072 tokens of 8 int4 heads x 128 (84 MB) take 22.0 us, 3.8 TB/s.  (With
-// the extremes token by token 25.9, three pieces ahead 22.1; as diag(scale)
-// codes + bias on the tensor cores, with fp32 minima and maxima, 36: the
-// extremes of fp32 values are twice as many operations.)
+// channels halve them among themselves at the end.  Bound by instructions:
+// 131,072 tokens of 8 int4 heads x 128 (84 MB) take 23.5 us, 3.6 TB/s, and 18.7
+// million warp instructions, of which those operations are 8.9 and the loads
+// from shared memory 1.3; the rest, nearly half, are the copies, each block's
+// place and end, and the loops (blocks of 128 tokens 22.6 us, of 32 27.7; int8
+// 28.0 for 151 MB, 5.4 TB/s; paged 24.6).  With the cache's last tokens still in
+// L2 22.0; there the extremes token by token took 25.9, three pieces ahead 22.1;
+// as diag(scale) codes + bias on the tensor cores, with fp32 minima and maxima, 36:
+// the extremes of fp32 values are twice as many operations.
 #include <cuda_fp16.h>
 
 #include <atomic>

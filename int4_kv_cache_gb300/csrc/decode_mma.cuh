@@ -255,7 +255,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS, WIDE>::THREADS, Cfg<D, BITS, WIDE
     // scores whose terms' magnitudes sum up to 50).  The score operands are made
     // normal, one packed operation each: 38.2 -> 41.8 us for 131,072 int4 tokens;
     // 16 ragged int8 sequences of up to 8,192 tokens 52.3 -> 52.4, at head_dim 64
-    // 34.7 -> 36.9, at 256 51.0 -> 55.9.
+    // 34.7 -> 36.9, at 256 (16 query and 4 kv heads) 51.0 -> 55.9.
     constexpr bool kNormal = MODE == kModeScores;
     __shared__ uint64_t full_bar[C::STAGES];
     __shared__ unsigned int done_cnt[C::STAGES];  // warps finished with the stage, cumulative

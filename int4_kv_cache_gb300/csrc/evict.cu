@@ -18,9 +18,10 @@
 // sequence) are copied while the selection runs.
 //
 // Bound by the kept rows' bytes for a batch: 32 sequences x 8 heads, 4,096 of
-// 4,608 rows each (320 MB), 58.4 us, 5.5 TB/s.  By the selection's chain of
-// steps for one sequence: 4,096 of 131,072 rows x 8 heads 16.0 us, 11 of them
-// the selection.  (With one CTA that finds each digit and the threshold and
+// 4,608 rows each (320 MB), 62.6 us, 5.1 TB/s (pages of 128 rows: 64.7).  By the
+// selection's chain of steps for one sequence: 4,096 of 131,072 rows x 8 heads
+// 18.3 us (paged 18.9); 16.0 with the weights and rows in L2, 11 of them the
+// selection.  (There, with one CTA that finds each digit and the threshold and
 // tells the others, 19.7; the keys in shared memory instead of registers 18.2;
 // 512 threads of 32 keys, whose code is twice as long and fetched once, 17.2.)
 #include <atomic>
