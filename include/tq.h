@@ -526,8 +526,9 @@ tq_status tq_rope_axes(const tq_rope_rows* q, const tq_rope_rows* k, const int32
  * invalid sizes).
  * tq_kv_block_bounds recomputes the bounds of every block that rows
  * [start[b], start[b] + n_rows) of sequence b touch, from the block's rows
- * below start[b] + n_rows: call it after each append with its write_pos and
- * n_new.  Caches of up to 2^30 tokens (all the entry points from here on).
+ * below start[b] + n_rows: call it after each append (the prompt's too) with
+ * where it wrote and n_new.  (A step with TQ_STEP_ADVANCE has moved write_pos on:
+ * where it wrote is the value before.)  Caches of up to 2^30 tokens (all the entry points from here on).
  * Other blocks are left as they were.  A range outside the cache sets
  * TQ_DEV_WRITE_POS and leaves that sequence out. */
 size_t tq_block_bounds_bytes(int32_t batch, int32_t num_kv_heads, int32_t head_dim, int32_t capacity,
@@ -641,13 +642,14 @@ tq_status tq_paged_sdpa_decode_weights(const tq_paged_kv_cache* cache, const uin
  *   dst_lens     int32 [batch]: min(seq_lens[b], keep)
  *   kept         int32 [batch][num_kv_heads][keep]: the src row of each dst
  *                row, -1 behind the last
- * Rows of dst behind the kept ones are left as they were.  Both caches have
- * the same batch, heads, head_dim and bits; 0 <= recent <= keep <= dst
- * capacity; batch * num_kv_heads <= 65,535.  What is written (dst's arrays,
- * dst_weights, dst_lens, kept) must not overlap what is read (src's arrays, the
- * tables, weights, seq_lens) or one another (TQ_ERR_SHAPE); paged caches may
- * share a pool (the same six arrays and page size; not the table), but a page
- * in both tables (or twice in dst's) gives undefined rows. */
+ * Rows of dst behind the kept ones are left as they were; dst's block bounds are
+ * the caller's to recompute.  Weights that are no numbers may rank anywhere.
+ * Both caches have the same batch, heads, head_dim and bits; 0 <= recent <= keep
+ * <= dst capacity; batch * num_kv_heads <= 65,535.  What is written (dst's
+ * arrays, dst_weights, dst_lens, kept) must not overlap what is read (src's
+ * arrays, the tables, weights, seq_lens) or one another (TQ_ERR_SHAPE); paged
+ * caches may share a pool (the same six arrays and page size; not the table),
+ * but a page in both tables (or twice in dst's) gives undefined rows. */
 tq_status tq_kv_evict(const tq_kv_cache* src, const tq_kv_cache* dst, const float* weights,
                       const int32_t* seq_lens, int32_t max_seq_len, int32_t keep, int32_t recent,
                       float* dst_weights, int32_t* dst_lens, int32_t* kept, int32_t* status, void* stream);
