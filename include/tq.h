@@ -73,7 +73,7 @@ typedef enum tq_status {
 /* Bits ORed into the optional device status word. */
 #define TQ_DEV_WRITE_POS 0x1 /* append: write_pos[b] < 0 or write_pos[b] + n_new > capacity; rows skipped */
 #define TQ_DEV_SEQ_LEN 0x2   /* decode: seq_lens[b] < 0 or > max_seq_len; clamped into range */
-#define TQ_DEV_TIMEOUT 0x4   /* a pipeline wait exceeded its time limit; the CTA gave up */
+#define TQ_DEV_TIMEOUT 0x4   /* a pipeline wait exceeded its time limit; the CTA gave up, what the call wrote (also accumulated weights) is undefined */
 #define TQ_DEV_PAGE 0x8      /* paged cache: a block-table entry outside [0, num_pages); page 0 used instead */
 #define TQ_DEV_BLOCK 0x10    /* tq_sdpa_blocks_decode: a listed block starts at or past seq_lens[b]; left out */
 
