@@ -76,6 +76,8 @@ typedef enum tq_status {
 #define TQ_DEV_TIMEOUT 0x4   /* a pipeline wait exceeded its time limit; the CTA gave up, what the call wrote (also accumulated weights) is undefined */
 #define TQ_DEV_PAGE 0x8      /* paged cache: a block-table entry outside [0, num_pages); page 0 used instead */
 #define TQ_DEV_BLOCK 0x10    /* tq_sdpa_blocks_decode: a listed block starts at or past seq_lens[b]; left out */
+#define TQ_DEV_NO_PAGE 0x20  /* tq_pages_reserve: fewer free pages than wanted; nothing was changed */
+#define TQ_DEV_SOURCE 0x40   /* tq_pages_fork: sources[b] outside [-1, batch); the sequence keeps its own pages */
 
 /* Rotation flags ("Running and Evaluating TurboQuant optimized Gemma 4",
  * TurboQuant section: vectors are rotated by the normalised Sylvester Hadamard
@@ -657,6 +659,110 @@ tq_status tq_paged_kv_evict(const tq_paged_kv_cache* src, const tq_paged_kv_cach
                             const float* weights, const int32_t* seq_lens, int32_t max_seq_len,
                             int32_t keep, int32_t recent, float* dst_weights, int32_t* dst_lens,
                             int32_t* kept, int32_t* status, void* stream);
+
+/* ------------------------------------------------------ several query rows --
+ * Attention of a chunk of new tokens over the cache that already holds them (a
+ * prompt, a piece of one, drafted tokens to be checked), and cross attention
+ * over an encoder's states held in a cache.
+ *   q         tq_query_rows: x[b * stride_b + h * stride_h + t * stride_t + d],
+ *             n rows of num_heads heads per sequence; strides in elements,
+ *             multiples of 8, not negative.  (tq_rope_axes writes rows so:
+ *             [batch][num_heads][n][head_dim].)
+ *   q_lens    device int32 [batch]: how many of the n rows are sequence b's; NULL:
+ *             all.  Rows behind them are not read, and out is left as it was there.
+ *   seq_lens  device int32 [batch]: the rows of the cache, the chunk's included
+ * Row i < q_lens[b] stands at position p = seq_lens[b] - q_lens[b] + i and attends
+ * to the cached rows t <= p, of them the last `window` ones where window > 0.
+ * TQ_CHUNK_FULL: every row attends to all of [0, seq_lens[b]) (window must be 0).
+ * A row with nothing to attend to (p < 0, an empty sequence) is a row of zeros.
+ *   out       fp16 [batch][n][num_heads][head_dim], contiguous: the rows that an
+ *             output projection takes; must not overlap q's rows
+ * Head grouping, lengths and max_seq_len, attn_scale and the rotation flags as in
+ * tq_sdpa_int4_decode_ex; lengths outside [0, n] and [0, max_seq_len] are clamped
+ * and set TQ_DEV_SEQ_LEN.
+ * Cached values enter as scale * code + bias rounded to fp16 (above 65,504: that),
+ * softmax weights as fp16; sums and softmax states are fp32.  So against fp64
+ * attention over the dequantised cache a score is off by 2^-11 attn_scale
+ * sum_d |q_d K_d| at most, and an output by what such scores make of it, 2^-10
+ * sum_t p_t |V_t| and its own rounding (all rows together: 4e-4 rel-L2 for normally
+ * distributed rows, up to 1.5e-3 with a key channel twenty times as large).  Cached rows whose scale or bias is not finite leave the
+ * outputs of the rows that attend to them undefined, and no others; so do query rows
+ * that are not finite for themselves.
+ * workspace: tq_chunk_workspace_bytes(...) bytes, 256-byte aligned, one per call in
+ * flight (0 bytes where n = 0).  n = 0 launches nothing.  batch and kv heads up to
+ * 65,535, n * num_heads up to 2^28, caches up to 2^30 tokens. */
+#define TQ_CHUNK_FULL 0x200u
+typedef struct tq_query_rows {
+    const uint16_t* x;
+    int64_t stride_b, stride_h, stride_t;
+    int32_t num_heads;
+    int32_t n;
+} tq_query_rows;
+size_t tq_chunk_workspace_bytes(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
+                                int32_t head_dim, int32_t n, int32_t max_seq_len);
+tq_status tq_sdpa_chunk(const tq_kv_cache* cache, const tq_query_rows* q, const int32_t* q_lens,
+                        const int32_t* seq_lens, int32_t max_seq_len, float attn_scale, int32_t window,
+                        uint32_t flags, void* workspace, size_t workspace_bytes, uint16_t* out,
+                        int32_t* status, void* stream);
+tq_status tq_paged_sdpa_chunk(const tq_paged_kv_cache* cache, const tq_query_rows* q, const int32_t* q_lens,
+                              const int32_t* seq_lens, int32_t max_seq_len, float attn_scale,
+                              int32_t window, uint32_t flags, void* workspace, size_t workspace_bytes,
+                              uint16_t* out, int32_t* status, void* stream);
+
+/* --------------------------------------------------------- pages of a pool --
+ * Keeps account of a paged cache's pages on the device.  The caller owns
+ *   refs   int32 [num_pages]: how many table entries name each page (0: free); a
+ *          caller that keeps a page in a list of its own adds to it
+ *   held   int32 [batch]: sequence b's pages are the first held[b] entries of its
+ *          row of cache->block_table, which these calls write
+ * all zeros for a pool without sequences.  A pool that several caches share (tables
+ * of their own over the same arrays) takes one refs.  Entries outside the pool and
+ * held[b] outside [0, max_pages_per_seq] set TQ_DEV_PAGE and count for nothing.
+ * The arrays, the workspace, the tables and the cache's arrays must not overlap
+ * (TQ_ERR_SHAPE; but see tq_pages_compact).
+ * workspace: tq_pages_workspace_bytes(...) bytes, 256-byte aligned, one per call in
+ * flight. */
+size_t tq_pages_workspace_bytes(int32_t batch, int32_t num_pages, int32_t max_pages_per_seq);
+
+/* Every sequence b takes over the pages that sequence sources[b] held before the
+ * call (sources[b] = b: its own; -1: none), and lets go of the others: table rows,
+ * held, lens (int32 [batch], may be NULL) and refs follow; entries behind the held
+ * ones become -1, lens of a sequence without a source 0.  No row is copied: pages
+ * that several sequences name are shared until one of them writes there
+ * (tq_pages_reserve).  Beam search reorders its beams so, a prompt is forked into
+ * several answers, a sequence that ended is freed. */
+tq_status tq_pages_fork(const tq_paged_kv_cache* cache, int32_t* refs, int32_t* held, int32_t* lens,
+                        const int32_t* sources, void* workspace, size_t workspace_bytes,
+                        int32_t* status, void* stream);
+
+/* Makes rows [start[b], start[b] + n_rows) of every sequence writable: call it
+ * before each append with its write_pos and n_new.
+ *   - Entries from held[b] up to the last of these rows' get free pages.
+ *   - A held page with refs > 1 that these rows fall into is replaced by a free one,
+ *     into which its rows below start[b] are copied (the rest of the new page is left
+ *     as it was).  Where all that name a page write to it in this call, the last
+ *     sequence keeps it.
+ * Sequence by sequence and entry by entry the free page of the lowest number is
+ * taken.  Where there are not enough nothing changes and TQ_DEV_NO_PAGE is set.  A
+ * sequence whose rows are not in [0, capacity] sets TQ_DEV_WRITE_POS and is left
+ * out (start[b] = -1 for a slot without a sequence: the append leaves it out, too). */
+tq_status tq_pages_reserve(const tq_paged_kv_cache* cache, int32_t* refs, int32_t* held,
+                           const int32_t* start, int32_t n_rows, void* workspace,
+                           size_t workspace_bytes, int32_t* status, void* stream);
+
+/* Moves the pages in use (refs > 0) to the lowest numbers: with n_live of them, the
+ * i-th used page at or behind n_live moves, rows and all, to the i-th free page
+ * before it; the others stay.
+ *   table_out  int32 [batch][max_pages_per_seq], may be cache->block_table: the held
+ *              entries by their new numbers, the others as they are
+ *   refs_out   int32 [num_pages], may be refs
+ *   n_live     int32 [1]
+ *   moved      int32 [num_pages], may be NULL: each used page's new number (its own
+ *              where it stayed), -1 for free ones; for page lists of the caller's
+ * Rows of the pages that were moved from are left as they were. */
+tq_status tq_pages_compact(const tq_paged_kv_cache* cache, const int32_t* refs, const int32_t* held,
+                           int32_t* table_out, int32_t* refs_out, int32_t* n_live, int32_t* moved,
+                           void* workspace, size_t workspace_bytes, int32_t* status, void* stream);
 
 #ifdef __cplusplus
 }

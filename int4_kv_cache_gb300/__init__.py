@@ -24,7 +24,8 @@ __all__ = [
     "tq_paged_kv_cache", "PagedKVCache", "tq_decode_step_host", "tq_host_staging_bytes",
     "TQ_DEV_BLOCK", "TQ_ROPE_PAIRS", "TQ_ROPE_INVERSE", "tq_rope_axes", "block_bounds", "tq_kv_block_bounds",
     "sparse_workspace", "tq_select_blocks", "tq_sdpa_blocks_decode", "tq_sparse_decode", "weights_workspace",
-    "tq_sdpa_decode_weights", "tq_kv_evict",
+    "tq_sdpa_decode_weights", "tq_kv_evict", "TQ_DEV_NO_PAGE", "TQ_DEV_SOURCE", "TQ_CHUNK_FULL", "chunk_workspace", "tq_sdpa_chunk",
+    "page_state", "pages_workspace", "tq_pages_fork", "tq_pages_reserve", "tq_pages_compact",
 ]
 
 TQ_OK = 0
@@ -34,6 +35,8 @@ TQ_ROTATE_K, TQ_ROTATE_V = 0x1, 0x2
 TQ_STEP_ADVANCE = 0x100
 TQ_DEV_PAGE = 0x8
 TQ_DEV_BLOCK = 0x10
+TQ_DEV_NO_PAGE, TQ_DEV_SOURCE = 0x20, 0x40
+TQ_CHUNK_FULL = 0x200
 TQ_ROPE_PAIRS, TQ_ROPE_INVERSE = 0x1, 0x2
 GROUP_SIZE = 64
 DEFAULT_CHUNK = 512
@@ -84,6 +87,14 @@ class tq_rope_rows(ctypes.Structure):
         ("x", ctypes.c_void_p), ("out", ctypes.c_void_p),
         ("stride_b", ctypes.c_int64), ("stride_t", ctypes.c_int64), ("stride_h", ctypes.c_int64),
         ("num_heads", ctypes.c_int32),
+    ]
+
+
+class tq_query_rows(ctypes.Structure):
+    _fields_ = [
+        ("x", ctypes.c_void_p),
+        ("stride_b", ctypes.c_int64), ("stride_h", ctypes.c_int64), ("stride_t", ctypes.c_int64),
+        ("num_heads", ctypes.c_int32), ("n", ctypes.c_int32),
     ]
 
 
@@ -139,12 +150,18 @@ def lib() -> ctypes.CDLL:
             sig[pre + "sdpa_blocks_decode"] = ([cache, P, i32, P, i32, f32, P, i32, i32, u32, P, sz, P, P, P], i32)
             sig[pre + "sparse_decode"] = ([cache, P, P, i32, P, i32, f32, i32, i32, i32, i32, u32, P, sz, P, P, P, P], i32)
             sig[pre + "sdpa_decode_weights"] = ([cache, P, i32, P, i32, f32, f32, P, u32, P, sz, P, P, P], i32)
+            sig[pre + "sdpa_chunk"] = ([cache, ctypes.POINTER(tq_query_rows), P, P, i32, f32, i32, u32, P, sz, P, P, P], i32)
             sig[pre + "kv_evict"] = ([cache, cache, P, P, i32, i32, i32, P, P, P, P, P], i32)
         sig["tq_rope_axes"] = ([R, R, P, P, i32, P, i32, i32, i32, i32, u32, P], i32)
         sig["tq_block_bounds_bytes"] = ([i32] * 5, sz)
         sig["tq_sparse_workspace_bytes"] = ([i32] * 7, sz)
         sig["tq_select_blocks"] = ([P, P] + [i32] * 5 + [P] + [i32] * 5 + [u32, P, sz, P, P, P], i32)
         sig["tq_weights_workspace_bytes"] = ([i32] * 5, sz)
+        sig["tq_chunk_workspace_bytes"] = ([i32] * 6, sz)
+        sig["tq_pages_workspace_bytes"] = ([i32] * 3, sz)
+        sig["tq_pages_fork"] = ([PC, P, P, P, P, P, sz, P, P], i32)
+        sig["tq_pages_reserve"] = ([PC, P, P, P, i32, P, sz, P, P], i32)
+        sig["tq_pages_compact"] = ([PC, P, P, P, P, P, P, P, sz, P, P], i32)
         for name, (args, res) in sig.items():
             fn = getattr(L, name)
             fn.argtypes = args
@@ -836,3 +853,125 @@ def tq_kv_evict(src, dst, weights: torch.Tensor, seq_lens: torch.Tensor, max_seq
     _check("tq_kv_evict", _fn(src, "kv_evict")(
         src.ref(), dst.ref(), weights.data_ptr(), seq_lens.data_ptr(), int(max_seq_len), int(keep), int(recent), dst_weights.data_ptr(),
         dst_lens.data_ptr(), kept.data_ptr(), status.data_ptr() if status is not None else None, on))
+
+
+# ------------------------------------------------- several query rows, pages of a pool
+def _at(t: Optional[torch.Tensor]):
+    return t.data_ptr() if t is not None else None
+
+
+def chunk_workspace(batch: int, num_q_heads: int, num_kv_heads: int, head_dim: int, n: int, max_seq_len: int,
+                    device="cuda") -> torch.Tensor:
+    """A workspace for tq_sdpa_chunk of these sizes (or of fewer rows and shorter sequences of the same heads)."""
+    size = int(lib().tq_chunk_workspace_bytes(batch, num_q_heads, num_kv_heads, head_dim, n, max_seq_len))
+    if size == 0:
+        raise ValueError("invalid sizes")
+    return torch.empty(size, dtype=torch.uint8, device=device)
+
+
+def tq_sdpa_chunk(cache, q: torch.Tensor, seq_lens: torch.Tensor, max_seq_len: int, attn_scale: float, workspace: torch.Tensor,
+                  out: Optional[torch.Tensor] = None, q_lens: Optional[torch.Tensor] = None, window: int = 0,
+                  status: Optional[torch.Tensor] = None, stream=None, flags: int = 0) -> torch.Tensor:
+    """Attention of the last q_lens[b] (None: n) rows of every sequence, q [B, Hq, n, D] fp16 (strides of whole 8-element
+    steps), over the cache that holds them: causal, the last ``window`` rows only where window > 0; with TQ_CHUNK_FULL every
+    row over the whole sequence (cross attention).  -> out [B, n, Hq, D]; its rows behind q_lens[b] are left as they were."""
+    if not q.is_cuda or q.dtype != torch.float16 or q.dim() != 4 or (q.numel() > 0 and q.stride(3) != 1):
+        raise ValueError("q: expected a CUDA float16 tensor [B, Hq, n, D] with a contiguous last dimension")
+    b, hq, n, d = q.shape
+    if b != cache.batch or d != cache.head_dim:
+        raise ValueError(f"q must be [B, Hq, n, D] of the cache's B and D; got {tuple(q.shape)}")
+    _need_lens(seq_lens, b, "seq_lens")
+    if q_lens is not None:
+        _need_lens(q_lens, b, "q_lens")
+    _need(workspace, torch.uint8, "workspace")
+    if status is not None:
+        _need(status, torch.int32, "status")
+    if out is None:
+        shape = (b, n, hq, d)
+        out = torch.empty(shape, dtype=torch.float16, device=q.device) if stream is None else _new(shape, torch.float16, q.device, stream)
+    _need(out, torch.float16, "out")
+    if out.shape != (b, n, hq, d):
+        raise ValueError(f"out must be [B, n, Hq, D] = {(b, n, hq, d)}; got {tuple(out.shape)}")
+    on = _on(stream, cache.buffer, q, seq_lens, q_lens, workspace, out, status)
+    if n == 0:
+        return out
+    sb, sh, st, _ = q.stride()
+    # a dimension of one is never stepped along, whatever its stride says
+    rows = tq_query_rows(q.data_ptr(), sb if b > 1 else 0, sh if hq > 1 else 0, st if n > 1 else 0, hq, n)
+    _check("tq_sdpa_chunk", _fn(cache, "sdpa_chunk")(
+        cache.ref(), rows, _at(q_lens), seq_lens.data_ptr(), int(max_seq_len), float(attn_scale), int(window), int(flags),
+        workspace.data_ptr(), workspace.numel(), out.data_ptr(), _at(status), on))
+    return out
+
+
+def page_state(cache):
+    """(refs int32 [num_pages], held int32 [B]) of a paged cache no page of which is in use."""
+    dev = cache.buffer.device
+    return (torch.zeros(cache.num_pages, dtype=torch.int32, device=dev), torch.zeros(cache.batch, dtype=torch.int32, device=dev))
+
+
+def pages_workspace(cache) -> torch.Tensor:
+    """A workspace for tq_pages_fork, tq_pages_reserve and tq_pages_compact on this paged cache."""
+    n = int(lib().tq_pages_workspace_bytes(cache.batch, cache.num_pages, cache.max_pages_per_seq))
+    if n == 0:
+        raise ValueError("invalid sizes")
+    return torch.empty(n, dtype=torch.uint8, device=cache.buffer.device)
+
+
+def _need_pages(cache, refs: torch.Tensor, held: torch.Tensor, workspace: torch.Tensor, status: Optional[torch.Tensor]) -> None:
+    if not getattr(cache, "paged", False):
+        raise ValueError("a paged cache is needed")
+    _need(refs, torch.int32, "refs")
+    if refs.numel() != cache.num_pages:
+        raise ValueError(f"refs must hold one entry per page; got {tuple(refs.shape)}")
+    _need_lens(held, cache.batch, "held")
+    _need(workspace, torch.uint8, "workspace")
+    if status is not None:
+        _need(status, torch.int32, "status")
+
+
+def tq_pages_fork(cache, refs: torch.Tensor, held: torch.Tensor, sources: torch.Tensor, workspace: torch.Tensor,
+                  lens: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Every sequence b takes over the pages of sequence sources[b] (int32 [B]; -1: none) and lets go of its own: block
+    table, held, lens and refs follow.  No row is copied; tq_pages_reserve does that for shared pages about to be written."""
+    _need_pages(cache, refs, held, workspace, status)
+    _need_lens(sources, cache.batch, "sources")
+    if lens is not None:
+        _need_lens(lens, cache.batch, "lens")
+    on = _on(stream, cache.buffer, refs, held, sources, workspace, lens, status)
+    _check("tq_pages_fork", lib().tq_pages_fork(cache.ref(), refs.data_ptr(), held.data_ptr(), _at(lens), sources.data_ptr(),
+                                                workspace.data_ptr(), workspace.numel(), _at(status), on))
+
+
+def tq_pages_reserve(cache, refs: torch.Tensor, held: torch.Tensor, start: torch.Tensor, n_rows: int, workspace: torch.Tensor,
+                     status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Pages for rows [start[b], start[b] + n_rows) of every sequence (before an append: its write_pos and n_new): free ones
+    behind the held ones, and copies of shared pages that these rows fall into.  Too few free pages: nothing changes and
+    TQ_DEV_NO_PAGE is set."""
+    _need_pages(cache, refs, held, workspace, status)
+    _need_lens(start, cache.batch, "start")
+    on = _on(stream, cache.buffer, refs, held, start, workspace, status)
+    _check("tq_pages_reserve", lib().tq_pages_reserve(cache.ref(), refs.data_ptr(), held.data_ptr(), start.data_ptr(), int(n_rows),
+                                                      workspace.data_ptr(), workspace.numel(), _at(status), on))
+
+
+def tq_pages_compact(cache, refs: torch.Tensor, held: torch.Tensor, workspace: torch.Tensor, table_out: torch.Tensor,
+                     refs_out: torch.Tensor, n_live: torch.Tensor, moved: Optional[torch.Tensor] = None,
+                     status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Move the pages in use to the lowest numbers: the rows in place, the new table and counts to ``table_out`` (may be
+    cache.block_table) and ``refs_out`` (may be refs), how many there are to n_live int32 [1], each used page's new number
+    (-1: free) to ``moved`` int32 [num_pages]."""
+    _need_pages(cache, refs, held, workspace, status)
+    _need(table_out, torch.int32, "table_out")
+    if table_out.shape != cache.block_table.shape:
+        raise ValueError(f"table_out must be [B, max_pages_per_seq]; got {tuple(table_out.shape)}")
+    for t, name in ((refs_out, "refs_out"), (moved, "moved")):
+        if t is not None:
+            _need(t, torch.int32, name)
+            if t.numel() != cache.num_pages:
+                raise ValueError(f"{name} must hold one entry per page; got {tuple(t.shape)}")
+    _need(n_live, torch.int32, "n_live")
+    on = _on(stream, cache.buffer, refs, held, workspace, table_out, refs_out, n_live, moved, status)
+    _check("tq_pages_compact", lib().tq_pages_compact(cache.ref(), refs.data_ptr(), held.data_ptr(), table_out.data_ptr(),
+                                                      refs_out.data_ptr(), n_live.data_ptr(), _at(moved), workspace.data_ptr(),
+                                                      workspace.numel(), _at(status), on))

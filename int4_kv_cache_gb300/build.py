@@ -21,7 +21,8 @@ BUILD_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(BUILD_DIR, "libtq.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["tq_api.cu", "quantize.cu", "decode_mma.cu", "decode_simt.cu", "reduce.cu", "decode_noalloc.cu", "dequant.cu", "rotate.cu", "order.cu", "selftest.cu",
-           "tq_ops.cu", "rope.cu", "bounds.cu", "select.cu", "decode_blocks.cu", "decode_scores.cu", "weights.cu", "evict.cu"]
+           "tq_ops.cu", "rope.cu", "bounds.cu", "select.cu", "decode_blocks.cu", "decode_scores.cu", "weights.cu", "evict.cu",
+           "tq_serve.cu", "chunk.cu", "pages.cu"]
 
 
 def nvcc() -> str:

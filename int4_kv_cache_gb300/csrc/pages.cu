@@ -1,0 +1,394 @@
+// pages.cu -- keeping account of the pages of a pool: forks of sequences (counted
+// references to shared pages), pages for the next rows (the free ones of the
+// lowest numbers, copies of shared pages that would be written) and compaction.
+//
+// The bookkeeping is integer work over tables of some thousand entries: bound by
+// latency, so it is done by one CTA (its phases ordered by CTA barriers), and
+// the copies of rows by a second launch over the whole device that reads the
+// list of moves the first one left.
+#include "tq_device.cuh"
+#include "tq_internal.h"
+
+namespace tq {
+
+namespace {
+
+constexpr int kPlanThreads = 1024;
+constexpr int kCopyThreads = 256;
+// Largest table that a fork stages in one CTA's shared memory.
+constexpr int kForkEntries = 8192;
+constexpr int kForkSeqs = 1024;
+
+__device__ __forceinline__ void report(int32_t* status, int bit) {
+    if (status != nullptr) atomicOr(status, bit);
+}
+
+__device__ __forceinline__ int clamp_held(const PagesParams& p, int held) {
+    if (held >= 0 && held <= p.max_pages) return held;
+    report(p.status, TQ_DEV_PAGE);
+    return held < 0 ? 0 : p.max_pages;
+}
+
+// Whether a table entry names a page (else TQ_DEV_PAGE).
+__device__ __forceinline__ bool is_page(const PagesParams& p, int page) {
+    if (static_cast<unsigned>(page) < static_cast<unsigned>(p.num_pages)) return true;
+    report(p.status, TQ_DEV_PAGE);
+    return false;
+}
+
+// Exclusive prefix sum over the CTA (kPlanThreads threads); total: the sum.
+__device__ __forceinline__ int cta_scan(int v, int* warp_sums, int& total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    __syncthreads();  // warp_sums may still be read from the last call
+    if (lane == 31) warp_sums[warp] = x;
+    __syncthreads();
+    if (warp == 0) {
+        int s = warp_sums[lane];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, s, o);
+            if (lane >= o) s += y;
+        }
+        warp_sums[lane] = s;
+    }
+    __syncthreads();
+    total = warp_sums[kPlanThreads / 32 - 1];
+    return x - v + (warp > 0 ? warp_sums[warp - 1] : 0);
+}
+
+// ------------------------------------------------------------------- fork --
+// One entry of the new table.
+__device__ __forceinline__ int source_of(const PagesParams& p, int b) {
+    const int s = p.sources[b];
+    if (s >= -1 && s < p.batch) return s;
+    report(p.status, TQ_DEV_SOURCE);
+    return b;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) fork_small_kernel(PagesParams p) {
+    __shared__ int32_t old[kForkEntries];
+    __shared__ int32_t held[kForkSeqs], lens[kForkSeqs];
+    const int entries = p.batch * p.max_pages;
+    for (int b = threadIdx.x; b < p.batch; b += kPlanThreads) {
+        held[b] = clamp_held(p, p.held[b]);
+        if (p.lens != nullptr) lens[b] = p.lens[b];
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < entries; e += kPlanThreads) {
+        const int b = e / p.max_pages, j = e - b * p.max_pages;
+        const int page = p.table[e];
+        old[e] = page;
+        if (j < held[b] && is_page(p, page)) atomicSub(p.refs + page, 1);
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < entries; e += kPlanThreads) {
+        const int b = e / p.max_pages, j = e - b * p.max_pages;
+        const int s = source_of(p, b);
+        int page = -1;
+        if (s >= 0 && j < held[s]) {
+            page = old[s * p.max_pages + j];
+            if (is_page(p, page)) atomicAdd(p.refs + page, 1);
+        }
+        p.table[e] = page;
+    }
+    for (int b = threadIdx.x; b < p.batch; b += kPlanThreads) {
+        const int s = source_of(p, b);
+        p.held[b] = s < 0 ? 0 : held[s];
+        if (p.lens != nullptr) p.lens[b] = s < 0 ? 0 : lens[s];
+    }
+}
+
+// Tables past one CTA: the old state to the workspace, then the new one from it.
+__global__ void __launch_bounds__(kCopyThreads) fork_release_kernel(PagesParams p) {
+    const long long entries = static_cast<long long>(p.batch) * p.max_pages;
+    for (long long e = static_cast<long long>(blockIdx.x) * kCopyThreads + threadIdx.x; e < entries;
+         e += static_cast<long long>(gridDim.x) * kCopyThreads) {
+        const int b = static_cast<int>(e / p.max_pages), j = static_cast<int>(e - static_cast<long long>(b) * p.max_pages);
+        const int page = p.table[e], held = clamp_held(p, p.held[b]);
+        p.old_table[e] = page;
+        if (j < held && is_page(p, page)) atomicSub(p.refs + page, 1);
+        if (j == 0) {
+            p.seq_a[b] = held;
+            p.seq_b[b] = p.lens != nullptr ? p.lens[b] : 0;
+        }
+    }
+}
+
+__global__ void __launch_bounds__(kCopyThreads) fork_take_kernel(PagesParams p) {
+    const long long entries = static_cast<long long>(p.batch) * p.max_pages;
+    for (long long e = static_cast<long long>(blockIdx.x) * kCopyThreads + threadIdx.x; e < entries;
+         e += static_cast<long long>(gridDim.x) * kCopyThreads) {
+        const int b = static_cast<int>(e / p.max_pages), j = static_cast<int>(e - static_cast<long long>(b) * p.max_pages);
+        const int s = source_of(p, b), held = s < 0 ? 0 : p.seq_a[s];
+        int page = -1;
+        if (j < held) {
+            page = p.old_table[static_cast<long long>(s) * p.max_pages + j];
+            if (is_page(p, page)) atomicAdd(p.refs + page, 1);
+        }
+        p.table[e] = page;
+        if (j == 0) {
+            p.held[b] = held;
+            if (p.lens != nullptr) p.lens[b] = s < 0 ? 0 : p.seq_b[s];
+        }
+    }
+}
+
+// ---------------------------------------------------------------- reserve --
+// The entries [first, last] that sequence b's rows fall into, and how many it holds.
+struct Range {
+    int first, last, held;
+};
+
+__device__ __forceinline__ bool range_of(const PagesParams& p, int b, Range& r) {
+    const int start = p.start[b];
+    if (start < 0 || static_cast<long long>(start) + p.n_rows > static_cast<long long>(p.max_pages) * p.page_tokens) {
+        report(p.status, TQ_DEV_WRITE_POS);
+        return false;
+    }
+    r.first = start / p.page_tokens;
+    r.last = static_cast<int>((static_cast<long long>(start) + p.n_rows - 1) / p.page_tokens);
+    r.held = clamp_held(p, p.held[b]);
+    return true;
+}
+
+// page_a counts the writers of each shared page, page_b holds the last of them.
+__global__ void __launch_bounds__(kPlanThreads) reserve_plan_kernel(PagesParams p) {
+    __shared__ int warp_sums[32];
+    __shared__ int n_moves;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    constexpr int kWarps = kPlanThreads / 32;
+    if (threadIdx.x == 0) n_moves = 0;
+    // the shared pages that would be written (a warp per sequence, a lane per entry)
+    for (int pass = 0; pass < 2; ++pass) {
+        for (int b = warp; b < p.batch; b += kWarps) {
+            Range r;
+            if (!range_of(p, b, r)) continue;
+            for (int j = r.first + lane; j <= r.last && j < r.held; j += 32) {
+                const int page = p.table[static_cast<long long>(b) * p.max_pages + j];
+                if (!is_page(p, page) || p.refs[page] <= 1) continue;
+                if (pass == 0) {
+                    p.page_a[page] = 0;
+                    p.page_b[page] = -1;
+                } else {
+                    atomicAdd(p.page_a + page, 1);
+                    atomicMax(p.page_b + page, b);
+                }
+            }
+        }
+        __syncthreads();
+    }
+    // a writer keeps the page when all that name it write and it is the last
+    auto copies = [&](int b, const Range& r, int j, int& page) {
+        if (j < r.first || j > r.last || j >= r.held) return false;
+        page = p.table[static_cast<long long>(b) * p.max_pages + j];
+        if (static_cast<unsigned>(page) >= static_cast<unsigned>(p.num_pages)) return false;
+        const int refs = p.refs[page];
+        return refs > 1 && !(__ldcg(p.page_a + page) == refs && __ldcg(p.page_b + page) == b);
+    };
+    for (int b = warp; b < p.batch; b += kWarps) {
+        Range r;
+        int wants = 0;
+        if (range_of(p, b, r)) {
+            for (int j0 = r.first; j0 <= r.last && j0 < r.held; j0 += 32) {
+                int page;
+                wants += __popc(__ballot_sync(0xffffffffu, copies(b, r, j0 + lane, page)));
+            }
+            if (r.last >= r.held) wants += r.last + 1 - r.held;
+        }
+        if (lane == 0) p.seq_a[b] = wants;
+    }
+    __syncthreads();
+    // where each sequence's pages begin in the list of free ones
+    long long carry = 0;
+    for (int b0 = 0; b0 < p.batch; b0 += kPlanThreads) {
+        const int b = b0 + threadIdx.x;
+        int total;
+        const int at = cta_scan(b < p.batch ? p.seq_a[b] : 0, warp_sums, total);
+        // more than there are pages does not fit whatever the sum is
+        if (b < p.batch) p.seq_a[b] = static_cast<int>(min(carry + at, 1LL << 30));
+        carry += total;
+    }
+    const long long want = carry;
+    if (want == 0) {
+        if (threadIdx.x == 0) p.head[0] = 0;
+        return;
+    }
+    // the lowest free pages, as many as wanted, into a list
+    int found = 0;
+    for (int q0 = 0; q0 < p.num_pages && found < want; q0 += kPlanThreads) {
+        const int page = q0 + threadIdx.x;
+        const bool free = page < p.num_pages && p.refs[page] == 0;
+        int total;
+        const int at = found + cta_scan(free ? 1 : 0, warp_sums, total);
+        if (free && at < want) p.old_table[at] = page;
+        found += total;
+    }
+    __syncthreads();
+    if (found < want) {
+        if (threadIdx.x == 0) {
+            p.head[0] = 0;
+            report(p.status, TQ_DEV_NO_PAGE);
+        }
+        return;
+    }
+    // hand them out: copies first, then the entries behind the held ones
+    for (int b = warp; b < p.batch; b += kWarps) {
+        Range r;
+        if (!range_of(p, b, r)) continue;
+        int at = p.seq_a[b];
+        int32_t* row = p.table + static_cast<long long>(b) * p.max_pages;
+        for (int j0 = r.first; j0 <= r.last && j0 < r.held; j0 += 32) {
+            int page;
+            const bool c = copies(b, r, j0 + lane, page);
+            const unsigned mask = __ballot_sync(0xffffffffu, c);
+            if (c) {
+                const int fresh = p.old_table[at + __popc(mask & ((1u << lane) - 1))];
+                const long long below = static_cast<long long>(p.start[b]) - static_cast<long long>(j0 + lane) * p.page_tokens;
+                p.moves[atomicAdd(&n_moves, 1)] = {page, fresh, static_cast<int>(max(0LL, min(below, static_cast<long long>(p.page_tokens))))};
+                row[j0 + lane] = fresh;
+            }
+            at += __popc(mask);
+        }
+        for (int j = r.held + lane; j <= r.last; j += 32) row[j] = p.old_table[at + j - r.held];
+        if (lane == 0 && r.last >= r.held) p.held[b] = r.last + 1;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < want; i += kPlanThreads) p.refs[p.old_table[i]] = 1;
+    for (int i = threadIdx.x; i < n_moves; i += kPlanThreads) atomicSub(p.refs + p.moves[i].src, 1);
+    if (threadIdx.x == 0) p.head[0] = n_moves;
+}
+
+// ---------------------------------------------------------------- compact --
+// page_a: for a moved page its place in the list of moves, for the others not set.
+__global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(PagesParams p) {
+    __shared__ int warp_sums[32];
+    int live = 0;
+    for (int q = threadIdx.x; q < p.num_pages; q += kPlanThreads) live += p.refs[q] > 0 ? 1 : 0;
+    int n;
+    cta_scan(live, warp_sums, n);
+    int holes = 0, late = 0;
+    for (int q0 = 0; q0 < p.num_pages; q0 += kPlanThreads) {
+        const int page = q0 + threadIdx.x;
+        const bool used = page < p.num_pages && p.refs[page] > 0;
+        const bool hole = page < n && !used, moves = page >= n && used;
+        int total;
+        // both in one scan: no more than 2^15 of either in a step
+        const int at = cta_scan((hole ? 1 : 0) | (moves ? 1 << 16 : 0), warp_sums, total);
+        if (hole) p.moves[holes + (at & 0xffff)].dst = page;
+        if (moves) {
+            p.moves[late + (at >> 16)].src = page;
+            p.page_a[page] = late + (at >> 16);
+        }
+        holes += total & 0xffff;
+        late += total >> 16;
+        if (page < p.num_pages && p.moved != nullptr) p.moved[page] = used ? page : -1;
+    }
+    __syncthreads();
+    // refs_out may be refs: first what stays and what moves to a hole, then the zeros
+    for (int i = threadIdx.x; i < late; i += kPlanThreads) {
+        p.moves[i].rows = p.page_tokens;
+        p.refs_out[p.moves[i].dst] = p.refs[p.moves[i].src];
+        if (p.moved != nullptr) p.moved[p.moves[i].src] = p.moves[i].dst;
+    }
+    if (p.refs_out != p.refs)
+        for (int q = threadIdx.x; q < n; q += kPlanThreads)
+            if (p.refs[q] > 0) p.refs_out[q] = p.refs[q];
+    __syncthreads();
+    for (int q = n + threadIdx.x; q < p.num_pages; q += kPlanThreads) p.refs_out[q] = 0;
+    if (threadIdx.x == 0) {
+        p.head[0] = late;
+        p.head[1] = n;
+        *p.n_live = n;
+    }
+}
+
+// ------------------------------------------------------------------- rows --
+// `bytes` bytes by the CTA's threads: 16 at a time, the last ones two at a time.
+__device__ __forceinline__ void copy_span(uint8_t* dst, const uint8_t* src, int bytes, int tid, int step) {
+    const int vecs = bytes >> 4;
+    for (int i = tid; i < vecs; i += step)
+        reinterpret_cast<uint4*>(dst)[i] = __ldcs(reinterpret_cast<const uint4*>(src) + i);
+    for (int i = vecs * 8 + tid; i < bytes >> 1; i += step)
+        reinterpret_cast<uint16_t*>(dst)[i] = reinterpret_cast<const uint16_t*>(src)[i];
+}
+
+// The listed moves: a unit is one head of a page.
+__device__ __forceinline__ void copy_moves(const PagesParams& p) {
+    const int n = p.head[0];
+    const int cw = p.head_dim * p.bits / 8, sw = p.head_dim / kGroup * 2;
+    for (long long u = blockIdx.x; u < static_cast<long long>(n) * p.num_kv_heads; u += gridDim.x) {
+        const int i = static_cast<int>(u / p.num_kv_heads), h = static_cast<int>(u - static_cast<long long>(i) * p.num_kv_heads);
+        const PageMove m = p.moves[i];
+        const long long src = (static_cast<long long>(m.src) * p.num_kv_heads + h) * p.page_tokens;
+        const long long dst = (static_cast<long long>(m.dst) * p.num_kv_heads + h) * p.page_tokens;
+#pragma unroll
+        for (int a = 0; a < 2; ++a) copy_span(p.codes[a] + dst * cw, p.codes[a] + src * cw, m.rows * cw, threadIdx.x, kCopyThreads);
+#pragma unroll
+        for (int a = 0; a < 4; ++a) {
+            uint8_t* at = reinterpret_cast<uint8_t*>(p.sb[a]);
+            copy_span(at + dst * sw, at + src * sw, m.rows * sw, threadIdx.x, kCopyThreads);
+        }
+    }
+}
+
+__global__ void __launch_bounds__(kCopyThreads) move_rows_kernel(PagesParams p) { copy_moves(p); }
+
+__global__ void __launch_bounds__(kCopyThreads) compact_rows_kernel(PagesParams p) {
+    const int n = p.head[1];
+    const long long step = static_cast<long long>(gridDim.x) * kCopyThreads, first = static_cast<long long>(blockIdx.x) * kCopyThreads + threadIdx.x;
+    const long long entries = static_cast<long long>(p.batch) * p.max_pages;
+    for (long long e = first; e < entries; e += step) {
+        const int b = static_cast<int>(e / p.max_pages), j = static_cast<int>(e - static_cast<long long>(b) * p.max_pages);
+        int page = p.table[e];
+        // (an entry whose page is counted free keeps its number: page_a holds nothing for it)
+        if (j < clamp_held(p, p.held[b]) && is_page(p, page) && page >= n) {
+            const int k = p.page_a[page];
+            if (static_cast<unsigned>(k) < static_cast<unsigned>(p.head[0]) && p.moves[k].src == page) page = p.moves[k].dst;
+        }
+        p.table_out[e] = page;
+    }
+    copy_moves(p);
+}
+
+}  // namespace
+
+cudaError_t launch_pages_fork(const PagesParams& p, int sms, cudaStream_t stream) {
+    const long long entries = static_cast<long long>(p.batch) * p.max_pages;
+    if (entries <= kForkEntries && p.batch <= kForkSeqs) {
+        fork_small_kernel<<<1, kPlanThreads, 0, stream>>>(p);
+        return cudaGetLastError();
+    }
+    const long long ctas = (entries + kCopyThreads - 1) / kCopyThreads;
+    const unsigned grid = static_cast<unsigned>(ctas < 8LL * sms ? ctas : 8LL * sms);
+    fork_release_kernel<<<grid, kCopyThreads, 0, stream>>>(p);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    fork_take_kernel<<<grid, kCopyThreads, 0, stream>>>(p);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_pages_reserve(const PagesParams& p, int sms, cudaStream_t stream) {
+    reserve_plan_kernel<<<1, kPlanThreads, 0, stream>>>(p);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    // no more units of work than heads of the pages that the rows touch
+    const long long units = static_cast<long long>(p.batch) * ((p.n_rows + p.page_tokens - 2) / p.page_tokens + 1) * p.num_kv_heads;
+    move_rows_kernel<<<static_cast<unsigned>(units < 4LL * sms ? units : 4LL * sms), kCopyThreads, 0, stream>>>(p);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_pages_compact(const PagesParams& p, int sms, cudaStream_t stream) {
+    compact_plan_kernel<<<1, kPlanThreads, 0, stream>>>(p);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    compact_rows_kernel<<<static_cast<unsigned>(8 * sms), kCopyThreads, 0, stream>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace tq

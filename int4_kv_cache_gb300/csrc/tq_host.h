@@ -18,6 +18,26 @@ inline size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255);
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Whether [a, a + na) and [b, b + nb) share a byte.
+inline bool overlap(const void* a, unsigned long long na, const void* b, unsigned long long nb) {
+    if (na == 0 || nb == 0) return false;
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + nb && y < x + na;
+}
+
+// Tokens of a cache that the operators around the step take (their index
+// arithmetic leaves room for blocks, CTAs and pieces behind the last one).
+constexpr int32_t kMaxTokens = 1 << 30;
+
+inline bool rotation_flags(uint32_t flags) { return (flags & ~(TQ_ROTATE_K | TQ_ROTATE_V)) == 0; }
+
+inline tq_status check_workspace(const void* ws, size_t have, size_t need) {
+    if (ws == nullptr || have < need) return TQ_ERR_WORKSPACE;
+    return (reinterpret_cast<uintptr_t>(ws) & 255u) != 0 ? TQ_ERR_ALIGN : TQ_OK;
+}
+
 inline bool supported_dim(int32_t d) { return d == 64 || d == 128 || d == 256; }
 
 // The cache as the kernels see it: the arrays, the sizes, and where each

@@ -306,7 +306,69 @@ struct WeightsParams {
     float rot_scale;
 };
 
+// Attention of several query rows per sequence (chunk.cu).
+struct ChunkParams {
+    const uint16_t* q;
+    long long stride_b, stride_h, stride_t;  // elements
+    const int32_t* q_lens;    // [B] or null (all n rows)
+    const int32_t* seq_lens;  // [B]
+    const uint8_t* k_codes;
+    const uint8_t* v_codes;
+    const uint16_t* k_scale;
+    const uint16_t* k_bias;
+    const uint16_t* v_scale;
+    const uint16_t* v_bias;
+    uint16_t* out;            // [B][n][Hq][D]
+    int32_t* status;
+    int32_t batch, num_q_heads, num_kv_heads, group_q, n, max_seq_len, capacity, bits;
+    int32_t window;           // 0: none
+    int32_t full;             // every row attends to the whole sequence
+    int32_t rotate_q, rotate_out;
+    float score_scale_log2;   // attn_scale * log2(e)
+    float rot_scale;
+    RowMap map;
+};
+
+// Pages of a pool (pages.cu).
+struct PageMove {
+    int32_t src, dst, rows;
+};
+struct PagesParams {
+    int32_t* table;           // [B][max_pages]
+    int32_t* refs;            // [num_pages]
+    int32_t* held;            // [B]
+    int32_t* status;
+    int32_t batch, num_pages, max_pages, page_tokens;
+    // fork
+    int32_t* lens;            // [B] or null
+    const int32_t* sources;   // [B]
+    // reserve
+    const int32_t* start;     // [B]
+    int32_t n_rows;
+    // compact
+    int32_t* table_out;
+    int32_t* refs_out;
+    int32_t* n_live;
+    int32_t* moved;           // [num_pages] or null
+    // workspace
+    int32_t* head;            // [2]: moves, used pages
+    int32_t* page_a;          // [num_pages]
+    int32_t* page_b;          // [num_pages]
+    int32_t* seq_a;           // [B + 1]
+    int32_t* seq_b;           // [B + 1]
+    int32_t* old_table;       // [B][max_pages]
+    PageMove* moves;          // [max(num_pages, B * max_pages)]
+    // the rows
+    uint8_t* codes[2];
+    uint16_t* sb[4];          // k_scale, k_bias, v_scale, v_bias
+    int32_t num_kv_heads, head_dim, bits;
+};
+
 // Launchers (return the cudaError_t of the launch).
+cudaError_t launch_chunk(const ChunkParams& p, int head_dim, cudaStream_t stream);
+cudaError_t launch_pages_fork(const PagesParams& p, int sms, cudaStream_t stream);
+cudaError_t launch_pages_reserve(const PagesParams& p, int sms, cudaStream_t stream);
+cudaError_t launch_pages_compact(const PagesParams& p, int sms, cudaStream_t stream);
 cudaError_t launch_rope(const RopeParams& p, cudaStream_t stream);
 cudaError_t launch_bounds(const BoundsParams& p, int sms, cudaStream_t stream);
 cudaError_t launch_select(const SelectParams& p, cudaStream_t stream);

@@ -11,18 +11,6 @@ using namespace tq;
 
 namespace {
 
-bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
-
-// Whether [a, a + na) and [b, b + nb) share a byte.
-bool overlap(const void* a, unsigned long long na, const void* b, unsigned long long nb) {
-    if (na == 0 || nb == 0) return false;
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return x < y + nb && y < x + na;
-}
-
-// Tokens of a cache that the operators here take (their index arithmetic leaves
-// room for blocks, CTAs and pieces behind the last one).
-constexpr int32_t kMaxTokens = 1 << 30;
 constexpr int32_t kMaxListed = 1 << 24;
 
 int block_shift_of(int32_t block_tokens) { return block_tokens == 32 ? 5 : (block_tokens == 64 ? 6 : (block_tokens == 128 ? 7 : -1)); }
@@ -212,13 +200,6 @@ tq_status run_blocks(const Store& c, const uint16_t* q, int32_t hq, const int32_
     r.rotate_out = (flags & TQ_ROTATE_V) ? 1 : 0;
     r.rot_scale = rotation_scale(c.head_dim);
     return cuda_status(launch_reduce(r, stream, true));
-}
-
-bool rotation_flags(uint32_t flags) { return (flags & ~(TQ_ROTATE_K | TQ_ROTATE_V)) == 0; }
-
-tq_status check_workspace(const void* ws, size_t have, size_t need) {
-    if (ws == nullptr || have < need) return TQ_ERR_WORKSPACE;
-    return (reinterpret_cast<uintptr_t>(ws) & 255u) != 0 ? TQ_ERR_ALIGN : TQ_OK;
 }
 
 tq_status blocks_decode(const Store& c, const uint16_t* q, int32_t hq, const int32_t* seq_lens, int32_t max_seq_len,

@@ -1,0 +1,285 @@
+// tq_serve.cu -- the extern "C" entry points for several query rows per sequence
+// and for the pages of a pool.  Argument checks and dispatch; no device
+// allocation, no host synchronisation.
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "tq_host.h"
+
+using namespace tq;
+
+namespace {
+
+// ------------------------------------------------------------ several rows --
+constexpr long long kMaxChunkRows = 1LL << 28;  // n * num_heads
+
+size_t chunk_bytes(int32_t batch, int32_t hq, int32_t hkv, int32_t head_dim, int32_t n, int32_t max_seq_len) {
+    (void)batch, (void)hq, (void)hkv, (void)head_dim, (void)n, (void)max_seq_len;
+    return 256;
+}
+
+bool chunk_sizes(int32_t batch, int32_t hq, int32_t hkv, int32_t head_dim, int32_t n, int32_t max_seq_len) {
+    return batch >= 1 && batch <= 65535 && hkv >= 1 && hkv <= 65535 && hq >= 1 && hq % hkv == 0 && hq / hkv <= 8 && supported_dim(head_dim) &&
+           n >= 1 && static_cast<long long>(n) * hq <= kMaxChunkRows && max_seq_len >= 1 && max_seq_len <= kMaxTokens;
+}
+
+tq_status chunk(const Store& c, const tq_query_rows* q, const int32_t* q_lens, const int32_t* seq_lens, int32_t max_seq_len, float attn_scale,
+                int32_t window, uint32_t flags, void* workspace, size_t workspace_bytes, uint16_t* out, int32_t* status, cudaStream_t stream) {
+    if (q == nullptr || q->x == nullptr || seq_lens == nullptr || out == nullptr) return TQ_ERR_NULL;
+    if (q->num_heads < 1 || q->num_heads % c.num_kv_heads != 0 || q->n < 0 || q->stride_b < 0 || q->stride_h < 0 || q->stride_t < 0)
+        return TQ_ERR_SHAPE;
+    if (max_seq_len < 1 || window < 0) return TQ_ERR_SHAPE;
+    if (q->num_heads / c.num_kv_heads > 8 || c.capacity > kMaxTokens) return TQ_ERR_UNSUPPORTED;
+    if (!rotation_flags(flags & ~TQ_CHUNK_FULL) || ((flags & TQ_CHUNK_FULL) && window != 0)) return TQ_ERR_UNSUPPORTED;
+    if (c.batch > 65535 || c.num_kv_heads > 65535 || static_cast<long long>(q->n) * q->num_heads > kMaxChunkRows) return TQ_ERR_SHAPE;
+    if (max_seq_len > c.capacity) return TQ_ERR_CAPACITY;
+    if (!aligned16(q->x) || !aligned16(out) || q->stride_b % 8 != 0 || q->stride_h % 8 != 0 || q->stride_t % 8 != 0 || !aligned4(seq_lens) ||
+        !aligned4(q_lens) || !aligned4(status))
+        return TQ_ERR_ALIGN;
+    if (q->n == 0) return TQ_OK;
+    const unsigned long long extent = 2ull * (static_cast<unsigned long long>(c.batch - 1) * q->stride_b + static_cast<unsigned long long>(q->n - 1) * q->stride_t +
+                                              static_cast<unsigned long long>(q->num_heads - 1) * q->stride_h + c.head_dim);
+    if (overlap(out, 2ull * c.batch * q->n * q->num_heads * c.head_dim, q->x, extent)) return TQ_ERR_SHAPE;
+    tq_status s = check_workspace(workspace, workspace_bytes, chunk_bytes(c.batch, q->num_heads, c.num_kv_heads, c.head_dim, q->n, max_seq_len));
+    if (s != TQ_OK) return s;
+    ChunkParams p{};
+    p.q = q->x;
+    p.stride_b = q->stride_b;
+    p.stride_h = q->stride_h;
+    p.stride_t = q->stride_t;
+    p.q_lens = q_lens;
+    p.seq_lens = seq_lens;
+    p.k_codes = c.k_codes;
+    p.v_codes = c.v_codes;
+    p.k_scale = c.k_scale;
+    p.k_bias = c.k_bias;
+    p.v_scale = c.v_scale;
+    p.v_bias = c.v_bias;
+    p.out = out;
+    p.status = status;
+    p.batch = c.batch;
+    p.num_q_heads = q->num_heads;
+    p.num_kv_heads = c.num_kv_heads;
+    p.group_q = q->num_heads / c.num_kv_heads;
+    p.n = q->n;
+    p.max_seq_len = max_seq_len;
+    p.capacity = c.capacity;
+    p.bits = c.bits;
+    p.window = window;
+    p.full = (flags & TQ_CHUNK_FULL) ? 1 : 0;
+    p.rotate_q = (flags & TQ_ROTATE_K) ? 1 : 0;
+    p.rotate_out = (flags & TQ_ROTATE_V) ? 1 : 0;
+    p.score_scale_log2 = attn_scale * 1.4426950408889634f;
+    p.rot_scale = rotation_scale(c.head_dim);
+    p.map = c.map;
+    return cuda_status(launch_chunk(p, c.head_dim, stream));
+}
+
+// ------------------------------------------------------------------- pages --
+constexpr long long kMaxEntries = 1LL << 30;  // table entries, pages
+
+struct PagesSpace {
+    size_t page_a, page_b, seq_a, seq_b, old_table, moves, bytes;
+};
+
+PagesSpace pages_space(int32_t batch, int32_t num_pages, int32_t max_pages) {
+    const size_t entries = static_cast<size_t>(batch) * max_pages, pages = static_cast<size_t>(num_pages);
+    PagesSpace s{};
+    size_t at = 256;
+    auto take = [&at](size_t n) {
+        const size_t here = at;
+        at += align256(n);
+        return here;
+    };
+    s.page_a = take(pages * 4);
+    s.page_b = take(pages * 4);
+    s.seq_a = take(static_cast<size_t>(batch) * 4);
+    s.seq_b = take(static_cast<size_t>(batch) * 4);
+    s.old_table = take(entries * 4);
+    s.moves = take((entries > pages ? entries : pages) * sizeof(PageMove));
+    s.bytes = at;
+    return s;
+}
+
+bool pages_sizes(int32_t batch, int32_t num_pages, int32_t max_pages) {
+    return batch >= 1 && num_pages >= 1 && num_pages <= kMaxEntries && max_pages >= 1 && static_cast<long long>(batch) * max_pages <= kMaxEntries;
+}
+
+struct Span {
+    const void* at;
+    unsigned long long bytes;
+};
+
+// Whether one of the first `writes` spans shares a byte with any other (same: two that may be one array).
+bool clash(const Span* s, int n, int writes, int same_a = -1, int same_b = -1, int same_c = -1, int same_d = -1) {
+    for (int i = 0; i < writes; ++i)
+        for (int j = 0; j < n; ++j) {
+            if (i == j) continue;
+            const bool may = (i == same_a && j == same_b) || (i == same_b && j == same_a) || (i == same_c && j == same_d) || (i == same_d && j == same_c);
+            if (may && s[i].at == s[j].at) continue;
+            if (overlap(s[i].at, s[i].bytes, s[j].at, s[j].bytes)) return true;
+        }
+    return false;
+}
+
+int arrays_of(const Store& c, Span* s) {
+    const unsigned long long rows = static_cast<unsigned long long>(c.map.num_pages) * c.num_kv_heads * c.map.page_tokens;
+    const unsigned long long codes = rows * (c.head_dim * c.bits / 8), sb = rows * (c.head_dim / kGroup * 2);
+    const void* at[6] = {c.k_codes, c.v_codes, c.k_scale, c.k_bias, c.v_scale, c.v_bias};
+    for (int i = 0; i < 6; ++i) s[i] = {at[i], i < 2 ? codes : sb};
+    return 6;
+}
+
+tq_status pages_params(const Store& c, const int32_t* refs, const int32_t* held, void* workspace, size_t workspace_bytes, int32_t* status, PagesParams* p) {
+    if (refs == nullptr || held == nullptr) return TQ_ERR_NULL;
+    if (!pages_sizes(c.batch, c.map.num_pages, c.map.max_pages)) return TQ_ERR_SHAPE;
+    if (!aligned4(refs) || !aligned4(held) || !aligned4(c.map.block_table) || !aligned4(status)) return TQ_ERR_ALIGN;
+    const PagesSpace sp = pages_space(c.batch, c.map.num_pages, c.map.max_pages);
+    const tq_status s = check_workspace(workspace, workspace_bytes, sp.bytes);
+    if (s != TQ_OK) return s;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    *p = PagesParams{};
+    p->table = const_cast<int32_t*>(c.map.block_table);
+    p->refs = const_cast<int32_t*>(refs);
+    p->held = const_cast<int32_t*>(held);
+    p->status = status;
+    p->batch = c.batch;
+    p->num_pages = c.map.num_pages;
+    p->max_pages = c.map.max_pages;
+    p->page_tokens = c.map.page_tokens;
+    p->head = reinterpret_cast<int32_t*>(ws);
+    p->page_a = reinterpret_cast<int32_t*>(ws + sp.page_a);
+    p->page_b = reinterpret_cast<int32_t*>(ws + sp.page_b);
+    p->seq_a = reinterpret_cast<int32_t*>(ws + sp.seq_a);
+    p->seq_b = reinterpret_cast<int32_t*>(ws + sp.seq_b);
+    p->old_table = reinterpret_cast<int32_t*>(ws + sp.old_table);
+    p->moves = reinterpret_cast<PageMove*>(ws + sp.moves);
+    p->codes[0] = c.k_codes;
+    p->codes[1] = c.v_codes;
+    p->sb[0] = c.k_scale;
+    p->sb[1] = c.k_bias;
+    p->sb[2] = c.v_scale;
+    p->sb[3] = c.v_bias;
+    p->num_kv_heads = c.num_kv_heads;
+    p->head_dim = c.head_dim;
+    p->bits = c.bits;
+    return TQ_OK;
+}
+
+// The spans that every call has: refs, held, the workspace, the table, the status word, then the cache's arrays.
+int common_spans(const Store& c, const PagesParams& p, size_t workspace_bytes, Span* s) {
+    s[0] = {p.refs, 4ull * p.num_pages};
+    s[1] = {p.held, 4ull * p.batch};
+    s[2] = {p.head, workspace_bytes};
+    s[3] = {p.table, 4ull * p.batch * p.max_pages};
+    s[4] = {p.status, p.status != nullptr ? 4ull : 0ull};
+    return 5 + arrays_of(c, s + 5);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t tq_chunk_workspace_bytes(int32_t batch, int32_t hq, int32_t hkv, int32_t head_dim, int32_t n, int32_t max_seq_len) {
+    return chunk_sizes(batch, hq, hkv, head_dim, n, max_seq_len) ? chunk_bytes(batch, hq, hkv, head_dim, n, max_seq_len) : 0;
+}
+
+tq_status tq_sdpa_chunk(const tq_kv_cache* cache, const tq_query_rows* q, const int32_t* q_lens, const int32_t* seq_lens, int32_t max_seq_len,
+                        float attn_scale, int32_t window, uint32_t flags, void* workspace, size_t workspace_bytes, uint16_t* out,
+                        int32_t* status, void* stream) {
+    Store st;
+    const tq_status s = store_of(cache, &st);
+    return s != TQ_OK ? s
+                      : chunk(st, q, q_lens, seq_lens, max_seq_len, attn_scale, window, flags, workspace, workspace_bytes, out, status,
+                              static_cast<cudaStream_t>(stream));
+}
+
+tq_status tq_paged_sdpa_chunk(const tq_paged_kv_cache* cache, const tq_query_rows* q, const int32_t* q_lens, const int32_t* seq_lens,
+                              int32_t max_seq_len, float attn_scale, int32_t window, uint32_t flags, void* workspace,
+                              size_t workspace_bytes, uint16_t* out, int32_t* status, void* stream) {
+    Store st;
+    const tq_status s = store_of(cache, &st);
+    return s != TQ_OK ? s
+                      : chunk(st, q, q_lens, seq_lens, max_seq_len, attn_scale, window, flags, workspace, workspace_bytes, out, status,
+                              static_cast<cudaStream_t>(stream));
+}
+
+size_t tq_pages_workspace_bytes(int32_t batch, int32_t num_pages, int32_t max_pages_per_seq) {
+    return pages_sizes(batch, num_pages, max_pages_per_seq) ? pages_space(batch, num_pages, max_pages_per_seq).bytes : 0;
+}
+
+tq_status tq_pages_fork(const tq_paged_kv_cache* cache, int32_t* refs, int32_t* held, int32_t* lens, const int32_t* sources, void* workspace,
+                        size_t workspace_bytes, int32_t* status, void* stream) {
+    Store st;
+    PagesParams p;
+    tq_status s = store_of(cache, &st);
+    if (s == TQ_OK && sources == nullptr) s = TQ_ERR_NULL;
+    if (s == TQ_OK) s = pages_params(st, refs, held, workspace, workspace_bytes, status, &p);
+    if (s != TQ_OK) return s;
+    if (!aligned4(lens) || !aligned4(sources)) return TQ_ERR_ALIGN;
+    Span sp[16];
+    int n = common_spans(st, p, workspace_bytes, sp);
+    // written: refs, held, workspace, table, status, lens
+    sp[n++] = {sources, 4ull * p.batch};
+    for (int i = n; i > 5; --i) sp[i] = sp[i - 1];
+    sp[5] = {lens, lens != nullptr ? 4ull * p.batch : 0ull};
+    ++n;
+    if (clash(sp, n, 6)) return TQ_ERR_SHAPE;
+    p.lens = lens;
+    p.sources = sources;
+    DeviceFacts* f = nullptr;
+    s = device_facts(&f);
+    return s != TQ_OK ? s : cuda_status(launch_pages_fork(p, f->sms, static_cast<cudaStream_t>(stream)));
+}
+
+tq_status tq_pages_reserve(const tq_paged_kv_cache* cache, int32_t* refs, int32_t* held, const int32_t* start, int32_t n_rows, void* workspace,
+                           size_t workspace_bytes, int32_t* status, void* stream) {
+    Store st;
+    PagesParams p;
+    tq_status s = store_of(cache, &st);
+    if (s == TQ_OK && start == nullptr) s = TQ_ERR_NULL;
+    if (s == TQ_OK) s = pages_params(st, refs, held, workspace, workspace_bytes, status, &p);
+    if (s != TQ_OK) return s;
+    if (!aligned4(start)) return TQ_ERR_ALIGN;
+    if (n_rows < 0) return TQ_ERR_SHAPE;
+    if (n_rows > st.capacity) return TQ_ERR_CAPACITY;
+    Span sp[16];
+    int n = common_spans(st, p, workspace_bytes, sp);
+    sp[n++] = {start, 4ull * p.batch};
+    if (clash(sp, n, 11)) return TQ_ERR_SHAPE;
+    if (n_rows == 0) return TQ_OK;
+    p.start = start;
+    p.n_rows = n_rows;
+    DeviceFacts* f = nullptr;
+    s = device_facts(&f);
+    return s != TQ_OK ? s : cuda_status(launch_pages_reserve(p, f->sms, static_cast<cudaStream_t>(stream)));
+}
+
+tq_status tq_pages_compact(const tq_paged_kv_cache* cache, const int32_t* refs, const int32_t* held, int32_t* table_out, int32_t* refs_out,
+                           int32_t* n_live, int32_t* moved, void* workspace, size_t workspace_bytes, int32_t* status, void* stream) {
+    Store st;
+    PagesParams p;
+    tq_status s = store_of(cache, &st);
+    if (s == TQ_OK && (table_out == nullptr || refs_out == nullptr || n_live == nullptr)) s = TQ_ERR_NULL;
+    if (s == TQ_OK) s = pages_params(st, refs, held, workspace, workspace_bytes, status, &p);
+    if (s != TQ_OK) return s;
+    if (!aligned4(table_out) || !aligned4(refs_out) || !aligned4(n_live) || !aligned4(moved)) return TQ_ERR_ALIGN;
+    // written: refs_out, table_out, n_live, moved, workspace, status, the cache's arrays
+    Span sp[16] = {{refs_out, 4ull * p.num_pages}, {table_out, 4ull * p.batch * p.max_pages}, {n_live, 4ull},
+                   {moved, moved != nullptr ? 4ull * p.num_pages : 0ull}, {p.head, workspace_bytes}, {status, status != nullptr ? 4ull : 0ull}};
+    int n = 6 + arrays_of(st, sp + 6);
+    const int refs_at = n, table_at = n + 1;
+    sp[n++] = {refs, 4ull * p.num_pages};
+    sp[n++] = {p.table, 4ull * p.batch * p.max_pages};
+    sp[n++] = {held, 4ull * p.batch};
+    if (clash(sp, n, 12, 0, refs_at, 1, table_at)) return TQ_ERR_SHAPE;
+    p.table_out = table_out;
+    p.refs_out = refs_out;
+    p.n_live = n_live;
+    p.moved = moved;
+    DeviceFacts* f = nullptr;
+    s = device_facts(&f);
+    return s != TQ_OK ? s : cuda_status(launch_pages_compact(p, f->sms, static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"
