@@ -1,115 +1,832 @@
 // chunk.cu -- attention of several query rows per sequence over the cache: a
 // chunk of new tokens in causal order (optionally the last `window` tokens
 // only), or every row over the whole sequence.  For row r = (token i, head g) of
-// (sequence b, kv head h):
-//   out = sum_t p_t V_t / sum_t p_t,  p_t = 2^(c q.K_t - m),  lo_i <= t < hi_i,
-// with c = attn_scale log2(e) and m the running maximum.
+// (sequence b, kv head h), r = i * G + g:
+//   out_r = sum_t p_t V_t / sum_t p_t,  p_t = 2^(c q_r.K_t - m_r),  lo_i <= t < hi_i,
+// with c = attn_scale log2(e) and m_r a running maximum.  Rows of all the heads
+// that share a kv head are rows of one matrix, so every cached key and value is
+// unpacked once for 256 of them.
 //
-// One warp a row: each lane holds D / 32 channels, a token at a time.
+// A CTA takes 256 rows (two tiles of 128, the M of a tcgen05.mma; one tile at
+// head_dim 256, whose output fills half of TMEM) and a run of the keys they see, in
+// tiles of 128 (64 at head_dim 256):
+//   a loader thread   copies codes, scales and biases into a ring (bulk copies)
+//   unpacking warps   turn them into fp16 operands in shared memory, laid out as
+//                     128-byte rows with the 128-byte swizzle: keys are then a
+//                     K-major operand and values an N-major one, in the same layout
+//   one MMA thread    S = Q K^T and O += P V, S, P and O in TMEM (P in S's place)
+//   softmax warps     a thread a row: maximum, 2^x, P as fp16, sum; no shuffles
+// The two row tiles take turns: while one's softmax runs the tensor core works for
+// the other.  Up to 128 rows (a few tokens) make one tile; the two halves then take
+// every other tile of keys and are merged in the end.  O is rescaled only when a
+// row's maximum grows by more than 2^8 (P stays below 2^8, exact enough in fp16's
+// range; the method of the published conditional-rescaling softmax), which is
+// rare after the first tiles.
+// Where rows are few the keys are split over CTAs and the partial states
+// merged by a second kernel.
 #include "tq_device.cuh"
 #include "tq_hadamard.cuh"
 #include "tq_internal.h"
+#include "tq_tcgen05.cuh"
 
 namespace tq {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 512;
+constexpr int kRowTile = 128;
+constexpr float kLazy = 8.f;  // log2 of how far P may grow before O is rescaled
 
-// The cached keys [lo, hi) that row i of a sequence with ql rows and `len` cached ones sees.
-__device__ __forceinline__ void row_span(const ChunkParams& p, int i, int ql, int len, int& lo, int& hi) {
-    lo = 0;
-    hi = len;
-    if (p.full) return;
+template <int D, int BITS>
+struct Cfg {
+    static constexpr int kStreams = D == 256 ? 1 : 2;         // softmax warpgroups, output accumulators
+    static constexpr int kTile = D == 256 ? 64 : 128;         // keys
+    static constexpr int kUnpackWarp = kStreams * 4;          // first unpacking warp
+    static constexpr int kUnpackWarps = 12 - kUnpackWarp;     // 4 (8 at head_dim 256)
+    static constexpr int kBlocks = D / 64;                    // blocks of 64 channels: 128-byte rows
+    static constexpr int kSlot = kTile * D * 2;               // one unpacked tile of keys or values
+    static constexpr int kSlots = D == 64 ? 6 : 3;
+    static constexpr int kCodes = kTile * D * BITS / 8;
+    static constexpr int kScales = kTile * kBlocks * 2;       // scales (and as many biases) of a tile
+    static constexpr int kEntry = kCodes + 2 * kScales;
+    static constexpr int kRing = D == 64 ? 6 : (BITS == 8 ? 3 : 6);
+    static constexpr int kQ = kStreams * kRowTile * D * 2;
+    static constexpr int kSmem = 1024 + kQ + kSlots * kSlot + kRing * kEntry;
+    static constexpr uint32_t kS = kTile;                     // TMEM columns of S (and P)
+    static constexpr uint32_t kO = 256;                       // first TMEM column of O
+    static_assert(kSmem + 512 <= 232448, "shared memory of a CTA");
+    static_assert(kO + kStreams * D <= 512 && 2 * kS <= kO, "TMEM");
+};
+
+struct Bars {
+    uint64_t ring_full[6], ring_empty[6], slot_full[6], slot_empty[6];
+    uint64_t s_full[2], p_full[2], o_full[2], q_full, drain;
+    uint32_t tmem;
+    int32_t abort;
+};
+
+// What a CTA works on.
+struct Work {
+    int b, h, part;         // part: (item, split), where partial states go
+    int row0, rows;         // first row, valid rows from it on (up to kStreams * 128)
+    int ql, len;
+    int klo, khi;           // the keys that any of the rows sees
+    int tile0, tiles;       // this CTA's tiles of keys
+};
+
+__device__ __forceinline__ int first_key(const ChunkParams& p, int i, int ql, int len) {
     const int pos = len - ql + i;
-    hi = pos + 1 > 0 ? pos + 1 : 0;
-    if (p.window > 0 && pos - p.window + 1 > 0) lo = pos - p.window + 1;
+    return !p.full && p.window > 0 && pos - p.window + 1 > 0 ? pos - p.window + 1 : 0;
+}
+__device__ __forceinline__ int end_key(const ChunkParams& p, int i, int ql, int len) {
+    if (p.full) return len;
+    const int pos = len - ql + i;
+    return pos + 1 > 0 ? pos + 1 : 0;
 }
 
-// E channels from channel E * lane on of cached row `row`, rounded to fp16.
-template <int D, int BITS>
-__device__ __forceinline__ void load_row(const uint8_t* codes, const uint16_t* scale, const uint16_t* bias, long long row,
-                                         int lane, float (&x)[D / 32]) {
-    constexpr int E = D / 32;
-    const long long g = row * (D / kGroup) + lane * E / kGroup;
-    const float s = __half2float(__ushort_as_half(scale[g])), z = __half2float(__ushort_as_half(bias[g]));
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-        const int d = lane * E + e;
-        const int code = BITS == 8 ? codes[row * D + d] : (codes[row * (D / 2) + d / 2] >> ((d & 1) * 4)) & 15;
-        x[e] = __half2float(__float2half_rn(fminf(fmaxf(fmaf(s, static_cast<float>(code), z), -65504.f), 65504.f)));
-    }
-}
-
-template <int D, int BITS>
-__global__ void __launch_bounds__(kThreads) chunk_kernel(ChunkParams p) {
-    constexpr int E = D / 32;
-    const int lane = threadIdx.x & 31;
-    const long long w = static_cast<long long>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
-    const long long rows = static_cast<long long>(p.n) * p.num_q_heads;
-    const int b = static_cast<int>(w / rows);
-    if (b >= p.batch) return;
-    const int hq = static_cast<int>(w % rows % p.num_q_heads), i = static_cast<int>(w % rows / p.num_q_heads);
-    const int h = hq / p.group_q;
-    int len = p.seq_lens[b], ql = p.q_lens != nullptr ? p.q_lens[b] : p.n;
+template <int TILE>
+__device__ __forceinline__ bool find_work(const ChunkParams& p, int rows_per_item, Work& w) {
+    // the last rows' items first: in causal order they see the most keys
+    int id = blockIdx.x;
+    const int per = p.batch * p.num_kv_heads * p.n_splits;
+    const int m = p.m_items - 1 - id / per;
+    id %= per;
+    const int split = id % p.n_splits;
+    const int bh = id / p.n_splits;
+    w.h = bh % p.num_kv_heads;
+    w.b = bh / p.num_kv_heads;
+    w.part = (bh * p.m_items + m) * p.n_splits + split;
+    int len = p.seq_lens[w.b], ql = p.q_lens != nullptr ? p.q_lens[w.b] : p.n;
     if (len < 0 || len > p.max_seq_len || ql < 0 || ql > p.n) {
-        if (p.status != nullptr && lane == 0) atomicOr(p.status, TQ_DEV_SEQ_LEN);
+        if (p.status != nullptr && threadIdx.x == 0) atomicOr(p.status, TQ_DEV_SEQ_LEN);
         len = min(max(len, 0), p.max_seq_len);
         ql = min(max(ql, 0), p.n);
     }
+    w.len = len;
+    w.ql = ql;
+    w.row0 = m * rows_per_item;
+    w.rows = min(rows_per_item, ql * p.group_q - w.row0);
+    if (w.rows <= 0) return false;
+    w.klo = first_key(p, w.row0 / p.group_q, ql, len);
+    w.khi = end_key(p, (w.row0 + w.rows - 1) / p.group_q, ql, len);
+    w.tile0 = w.klo / TILE;
+    const int all = w.khi > w.klo ? (w.khi + TILE - 1) / TILE - w.tile0 : 0;
+    const int t0 = static_cast<int>(static_cast<long long>(all) * split / p.n_splits);
+    w.tiles = static_cast<int>(static_cast<long long>(all) * (split + 1) / p.n_splits) - t0;
+    w.tile0 += t0;
+    return true;
+}
+
+// Entry e of the ring holds the keys or the values of tile `tile`.  pair: both row
+// tiles use a tile of keys, then its values (K0 V0 K1 V1 ...); else the next
+// keys come ahead of the values (K0 K1 V0 K2 V1 ... V_last).
+__device__ __forceinline__ bool entry_of(int e, int tiles, bool pair, int& tile) {
+    if (pair) {
+        tile = e >> 1;
+        return (e & 1) != 0;
+    }
+    if (e == 0) {
+        tile = 0;
+        return false;
+    }
+    if (e & 1) {
+        tile = (e + 1) >> 1;
+        if (tile < tiles) return false;
+        tile = tiles - 1;
+        return true;
+    }
+    tile = (e >> 1) - 1;
+    return true;
+}
+__device__ __forceinline__ int key_entry(int tile, bool pair) { return pair ? 2 * tile : (tile == 0 ? 0 : 2 * tile - 1); }
+__device__ __forceinline__ int value_entry(int tile, int tiles, bool pair) {
+    return pair ? 2 * tile + 1 : (tile == tiles - 1 ? 2 * tiles - 1 : 2 * tile + 2);
+}
+
+// Waits for a phase; false when it took too long or another warp has given up.
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, Bars* bars, int32_t* status) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = globaltimer_ns();
+    for (uint32_t it = 1;; ++it) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((it & 63u) == 0) {
+            if (*reinterpret_cast<volatile int32_t*>(&bars->abort) != 0) return false;
+            if (globaltimer_ns() - t0 > 2000000000ull) {
+                *reinterpret_cast<volatile int32_t*>(&bars->abort) = 1;
+                if (status != nullptr) atomicOr(status, TQ_DEV_TIMEOUT);
+                return false;
+            }
+        }
+    }
+}
+
+// ------------------------------------------------------------------ loader --
+template <int D, int BITS>
+__device__ __forceinline__ void load_role(const ChunkParams& p, const Work& w, uint8_t* ring, Bars* bars, bool pair) {
+    using C = Cfg<D, BITS>;
+    const uint64_t policy = policy_evict_first();
+    int e = 0;
+    for (; e < 2 * w.tiles; ++e) {
+        const int r = e % C::kRing, n = e / C::kRing;
+        if (n > 0 && !wait(&bars->ring_empty[r], (n - 1) & 1, bars, p.status)) break;
+        int tile;
+        const bool value = entry_of(e, w.tiles, pair, tile);
+        const int t0 = (w.tile0 + tile) * C::kTile;
+        const int rows = min(C::kTile, (w.khi - t0 + 15) & ~15);  // capacities are whole 16s
+        const long long at = kv_row(p.map, p.num_kv_heads, w.b, w.h, t0, p.status);
+        uint8_t* dst = ring + r * C::kEntry;
+        const uint32_t cb = rows * (D * BITS / 8), sb = rows * (C::kBlocks * 2);
+        mbar_arrive_expect_tx(&bars->ring_full[r], cb + 2 * sb);
+        bulk_load(dst, (value ? p.v_codes : p.k_codes) + at * (D * BITS / 8), cb, &bars->ring_full[r], policy);
+        bulk_load(dst + C::kCodes, (value ? p.v_scale : p.k_scale) + at * C::kBlocks, sb, &bars->ring_full[r], policy);
+        bulk_load(dst + C::kCodes + C::kScales, (value ? p.v_bias : p.k_bias) + at * C::kBlocks, sb, &bars->ring_full[r], policy);
+    }
+    if (e < 2 * w.tiles)  // given up: the copies in flight land before the CTA leaves
+        for (int k = max(0, e - C::kRing); k < e; ++k) mbar_wait_bounded(&bars->ring_full[k % C::kRing], (k / C::kRing) & 1);
+}
+
+// ---------------------------------------------------------------- unpacking --
+// Eight codes as four pairs of fp16.  int4: pairs (0,4), (1,5), (2,6), (3,7) of a
+// word, the order that shifts and masks give; queries and outputs follow it.
+template <int BITS>
+__device__ __forceinline__ void unpack8(uint32_t w0, uint32_t w1, __half2 (&c)[4]) {
+    auto h2 = [](uint32_t x) { return *reinterpret_cast<__half2*>(&x); };
+    const __half2 k1024 = __floats2half2_rn(1024.f, 1024.f), k64 = __floats2half2_rn(64.f, 64.f);
+    if (BITS == 4) {
+        // a nibble in the low bits of 0x6400 counts from 1,024 on, four bits up in 0x5400 from 64 on
+        const uint32_t hi = w0 >> 8;
+        c[0] = __hsub2(h2((w0 & 0x000f000fu) | 0x64006400u), k1024);
+        c[1] = __hsub2(h2((w0 & 0x00f000f0u) | 0x54005400u), k64);
+        c[2] = __hsub2(h2((hi & 0x000f000fu) | 0x64006400u), k1024);
+        c[3] = __hsub2(h2((hi & 0x00f000f0u) | 0x54005400u), k64);
+    } else {
+        c[0] = __hsub2(h2(__byte_perm(w0, 0x64646464u, 0x4140)), k1024);
+        c[1] = __hsub2(h2(__byte_perm(w0, 0x64646464u, 0x4342)), k1024);
+        c[2] = __hsub2(h2(__byte_perm(w1, 0x64646464u, 0x4140)), k1024);
+        c[3] = __hsub2(h2(__byte_perm(w1, 0x64646464u, 0x4342)), k1024);
+    }
+}
+
+template <int D, int BITS>
+__device__ __forceinline__ void unpack_role(const ChunkParams& p, const Work& w, const uint8_t* ring, uint8_t* slots, Bars* bars, bool pair) {
+    using C = Cfg<D, BITS>;
+    constexpr int kUnits = BITS == 4 ? 4 : 2;             // 16-byte pieces of fp16 that 16 bytes of codes give
+    constexpr int kChunks = D * BITS / 8 / 16;            // 16-byte pieces of codes per key
+    constexpr int kT = C::kUnpackWarps * 32;
+    const int tid = threadIdx.x - C::kUnpackWarp * 32, lane = threadIdx.x & 31;
+    for (int e = 0; e < 2 * w.tiles; ++e) {
+        const int r = e % C::kRing, s = e % C::kSlots;
+        if (!wait(&bars->ring_full[r], (e / C::kRing) & 1, bars, p.status)) return;
+        if (e >= C::kSlots && !wait(&bars->slot_empty[s], (e / C::kSlots - 1) & 1, bars, p.status)) return;
+        int tile;
+        const bool value = entry_of(e, w.tiles, pair, tile);
+        const int t0 = (w.tile0 + tile) * C::kTile;
+        const bool edge = t0 < w.klo || t0 + C::kTile > w.khi;
+        const uint8_t* codes = ring + r * C::kEntry;
+        const __half* scales = reinterpret_cast<const __half*>(codes + C::kCodes);
+        const __half* biases = reinterpret_cast<const __half*>(codes + C::kCodes + C::kScales);
+        uint8_t* dst = slots + s * C::kSlot;
+#pragma unroll
+        for (int it = 0; it < C::kTile * kChunks / kT; ++it) {
+            const int c = it * kT + tid, t = c / kChunks, ck = c % kChunks;
+            const int g = ck * kUnits / 8, u0 = ck * kUnits % 8;
+            const uint4 word = reinterpret_cast<const uint4*>(codes)[c];
+            const __half sc = scales[t * C::kBlocks + g], bi = biases[t * C::kBlocks + g];
+            // eight lanes write eight different 16-byte columns: pieces of other
+            // blocks are taken in another order
+            const int x = BITS == 4 ? (D == 128 ? g * 2 : (D == 256 ? g : 0)) : g & 1;
+            uint32_t v[4] = {word.x, word.y, word.z, word.w};
+            if (BITS == 4) {
+                if (D == 256 && (x & 1)) {
+                    uint32_t y = v[0]; v[0] = v[1]; v[1] = y;
+                    y = v[2]; v[2] = v[3]; v[3] = y;
+                }
+                if (D >= 128 && (x & 2)) {
+                    uint32_t y = v[0]; v[0] = v[2]; v[2] = y;
+                    y = v[1]; v[1] = v[3]; v[3] = y;
+                }
+            } else if (D >= 128 && x) {
+                uint32_t y = v[0]; v[0] = v[2]; v[2] = y;
+                y = v[1]; v[1] = v[3]; v[3] = y;
+            }
+            uint8_t* row = dst + g * (C::kTile * 128) + t * 128;
+            const int swz = t & 7;
+            const __half2 s2 = __half2half2(sc), b2 = __half2half2(bi);
+            // values past fp16's range and scales or biases that are no numbers
+            const bool odd = !(__hfma(__habs(sc), __float2half_rn(BITS == 4 ? 15.f : 255.f), __habs(bi)) <= __float2half_rn(65504.f));
+            const bool drop = (edge && (t0 + t < w.klo || t0 + t >= w.khi)) || (odd && value && (__hisnan(sc) || __hisinf(sc) || __hisnan(bi) || __hisinf(bi)));
+#pragma unroll
+            for (int j = 0; j < kUnits; ++j) {
+                __half2 h[4];
+                if (BITS == 4)
+                    unpack8<4>(v[j], 0, h);
+                else
+                    unpack8<8>(v[2 * j], v[2 * j + 1], h);
+                if (drop || odd) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float2 f = __half22float2(h[k]);
+                        const float fs = __half2float(sc), fb = __half2float(bi);
+                        h[k] = drop ? __floats2half2_rn(0.f, 0.f)
+                                    : __floats2half2_rn(fminf(fmaxf(fmaf(f.x, fs, fb), -65504.f), 65504.f), fminf(fmaxf(fmaf(f.y, fs, fb), -65504.f), 65504.f));
+                    }
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) h[k] = __hfma2(h[k], s2, b2);
+                }
+                const int u = u0 + (j ^ x);
+                *reinterpret_cast<uint4*>(row + ((u ^ swz) << 4)) = *reinterpret_cast<uint4*>(h);
+            }
+        }
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (lane == 0) {
+            mbar_arrive(&bars->ring_empty[r]);
+            mbar_arrive(&bars->slot_full[s]);
+        }
+    }
+}
+
+// ---------------------------------------------------------------------- MMA --
+template <int D, int BITS>
+__device__ __forceinline__ bool mma_loop(const ChunkParams& p, const Work& w, uint32_t q, uint32_t slots, Bars* bars, bool pair) {
+    using C = Cfg<D, BITS>;
+    const uint32_t tmem = bars->tmem;
+    auto slot_wait = [&](int e) { return wait(&bars->slot_full[e % C::kSlots], (e / C::kSlots) & 1, bars, p.status); };
+    auto release = [&](int e) { tc_commit(&bars->slot_empty[e % C::kSlots]); };
+    // S[buf] = Q[qt] K^T, K in the slot of entry e
+    auto qk = [&](int e, int qt, int buf) {
+        const uint32_t kb = slots + (e % C::kSlots) * C::kSlot, qb = q + qt * (kRowTile * D * 2);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k)
+            tc_mma_ss(tmem + buf * C::kS, smem_operand(qb + (k / 4) * (kRowTile * 128) + (k % 4) * 32, 16),
+                      smem_operand(kb + (k / 4) * (C::kTile * 128) + (k % 4) * 32, 16), mma_desc(kRowTile, C::kTile, false), k > 0);
+        tc_commit(&bars->s_full[buf]);
+    };
+    // O[o] += P[buf] V, V in the slot of entry e
+    auto pv = [&](int e, int buf, int o, bool add) {
+        const uint32_t vb = slots + (e % C::kSlots) * C::kSlot;
+#pragma unroll
+        for (int k = 0; k < C::kTile / 16; ++k)
+            tc_mma_ts(tmem + C::kO + o * D, tmem + buf * C::kS + k * 8, smem_operand(vb + k * 2048, C::kTile * 128),
+                      mma_desc(kRowTile, D, true), add || k > 0);
+    };
+    if (!wait(&bars->q_full, 0, bars, p.status)) return false;
+    const int T = w.tiles;
+    if (pair) {
+        if (!slot_wait(0)) return false;
+        tc_fence_after();
+        qk(0, 0, 0);
+        qk(0, 1, 1);
+        release(0);
+        for (int j = 0; j < T; ++j) {
+            const int ve = 2 * j + 1, ke = 2 * j + 2;
+            if (!slot_wait(ve)) return false;
+            if (!wait(&bars->p_full[0], j & 1, bars, p.status)) return false;
+            tc_fence_after();
+            pv(ve, 0, 0, j > 0);
+            if (j + 1 < T) {
+                if (!slot_wait(ke)) return false;
+                tc_fence_after();
+                qk(ke, 0, 0);
+            } else {
+                tc_commit(&bars->o_full[0]);
+            }
+            if (!wait(&bars->p_full[1], j & 1, bars, p.status)) return false;
+            tc_fence_after();
+            pv(ve, 1, 1, j > 0);
+            release(ve);
+            if (j + 1 < T) {
+                qk(ke, 1, 1);
+                release(ke);
+            } else {
+                tc_commit(&bars->o_full[1]);
+            }
+        }
+        return true;
+    }
+    for (int j = 0; j < 2 && j < T; ++j) {
+        if (!slot_wait(key_entry(j, false))) return false;
+        tc_fence_after();
+        qk(key_entry(j, false), 0, j);
+        release(key_entry(j, false));
+    }
+    for (int j = 0; j < T; ++j) {
+        const int ve = value_entry(j, T, false), buf = j & 1, o = C::kStreams == 2 ? buf : 0;
+        if (!slot_wait(ve)) return false;
+        if (!wait(&bars->p_full[buf], (j >> 1) & 1, bars, p.status)) return false;
+        tc_fence_after();
+        pv(ve, buf, o, C::kStreams == 2 ? j > 1 : j > 0);
+        release(ve);
+        // (one accumulator: the softmax may have to rescale it before the next product)
+        if (C::kStreams == 1 || j + 2 >= T) tc_commit(&bars->o_full[o]);
+        if (j + 2 < T) {
+            const int ke = key_entry(j + 2, false);
+            if (!slot_wait(ke)) return false;
+            tc_fence_after();
+            qk(ke, 0, buf);
+            release(ke);
+        }
+    }
+    return true;
+}
+
+// ------------------------------------------------------------------ softmax --
+// Position of channel c in the order of the operands (see unpack8).
+template <int BITS>
+__device__ __forceinline__ constexpr int place(int c) {
+    return BITS == 4 ? (c & ~7) | ((c & 3) << 1) | ((c >> 2) & 1) : c;
+}
+
+// The fast transform of N values in one thread's registers.
+template <int N>
+__device__ __forceinline__ void hadamard_thread(float (&v)[N]) {
+#pragma unroll
+    for (int h = 1; h < N; h <<= 1) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            if ((i & h) == 0) {
+                const float u = v[i], x = v[i + h];
+                v[i] = u + x;
+                v[i + h] = u - x;
+            }
+        }
+    }
+}
+
+// 64 channels (a 128-byte row of one block) of row `row` of a query tile.
+template <int BITS>
+__device__ __forceinline__ void store_q64(uint8_t* block, int row, const __half2 (&x)[32]) {
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+        uint4 o;
+        uint32_t* w = reinterpret_cast<uint32_t*>(&o);
+        const uint32_t* s = reinterpret_cast<const uint32_t*>(x) + u * 4;
+        if (BITS == 4) {
+            w[0] = __byte_perm(s[0], s[2], 0x5410);
+            w[1] = __byte_perm(s[0], s[2], 0x7632);
+            w[2] = __byte_perm(s[1], s[3], 0x5410);
+            w[3] = __byte_perm(s[1], s[3], 0x7632);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) w[k] = s[k];
+        }
+        *reinterpret_cast<uint4*>(block + row * 128 + ((u ^ (row & 7)) << 4)) = o;
+    }
+}
+
+template <int D, int BITS>
+__device__ __forceinline__ void load_query(const ChunkParams& p, const Work& w, uint8_t* tile, int row, int tile_row0) {
+    const int r = tile_row0 + row;
+    const bool valid = r < w.rows;
+    const int flat = w.row0 + (valid ? r : 0), i = flat / p.group_q, g = flat - i * p.group_q;
+    const uint4* src = reinterpret_cast<const uint4*>(p.q + w.b * p.stride_b + (w.h * p.group_q + g) * p.stride_h + i * p.stride_t);
+    if (!p.rotate_q) {
+#pragma unroll
+        for (int blk = 0; blk < D / 64; ++blk) {
+            __half2 x[32];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) reinterpret_cast<uint4*>(x)[u] = valid ? __ldg(src + blk * 8 + u) : make_uint4(0, 0, 0, 0);
+            if (p.negate_q) {
+#pragma unroll
+                for (int k = 0; k < 32; ++k) x[k] = __hneg2(x[k]);
+            }
+            store_q64<BITS>(tile + blk * (kRowTile * 128), row, x);
+        }
+        return;
+    }
+    constexpr int N = D < 128 ? D : 128;
+    for (int half = 0; half < D / N; ++half) {
+        float v[N];
+#pragma unroll
+        for (int u = 0; u < N / 8; ++u) {
+            uint4 x = valid ? __ldg(src + u) : make_uint4(0, 0, 0, 0);
+            halves_to_floats<8>(&x, *reinterpret_cast<float(*)[8]>(v + u * 8));
+            if (D == 256) {  // the stage of 128 first: sums for the first half, differences for the second
+                float y[8];
+                x = valid ? __ldg(src + 16 + u) : make_uint4(0, 0, 0, 0);
+                halves_to_floats<8>(&x, y);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) v[u * 8 + k] = half ? v[u * 8 + k] - y[k] : v[u * 8 + k] + y[k];
+            }
+        }
+        hadamard_thread<N>(v);
+        const float scale = p.negate_q ? -p.rot_scale : p.rot_scale;
+#pragma unroll
+        for (int blk = 0; blk < N / 64; ++blk) {
+            __half2 x[32];
+#pragma unroll
+            for (int k = 0; k < 32; ++k) x[k] = __floats2half2_rn(v[blk * 64 + 2 * k] * scale, v[blk * 64 + 2 * k + 1] * scale);
+            store_q64<BITS>(tile + (half * (N / 64) + blk) * (kRowTile * 128), row, x);
+        }
+    }
+}
+
+struct State {
+    float m, l;  // maximum that P counts from (log2 units, -inf: none yet), sum
+};
+
+// One warpgroup's tiles: j = first, first + step, ...
+template <int D, int BITS>
+__device__ __forceinline__ bool softmax_loop(const ChunkParams& p, const Work& w, Bars* bars, int stream, bool pair, bool active, int lo, int hi, State& st) {
+    using C = Cfg<D, BITS>;
+    constexpr int N = C::kTile;
+    const int lane = threadIdx.x & 31;
+    const uint32_t lanes = static_cast<uint32_t>((threadIdx.x >> 5) & 3) << 21;
+    const uint32_t tmem = bars->tmem + lanes;
+    const float c = p.score_scale_log2;
+    const int step = pair || C::kStreams == 1 ? 1 : 2;
+    for (int j = step == 2 ? stream : 0, k = 0; j < w.tiles; j += step, ++k) {
+        const int buf = pair || C::kStreams == 2 ? stream : j & 1;
+        const uint32_t phase = C::kStreams == 1 ? (j >> 1) & 1 : k & 1;
+        if (!wait(&bars->s_full[buf], phase, bars, p.status)) return false;
+        tc_fence_after();
+        if (active) {
+            const uint32_t sa = tmem + buf * C::kS;
+            const int t0 = (w.tile0 + j) * C::kTile;
+            float s[N];
+#pragma unroll
+            for (int x = 0; x < N; x += 32) tmem_ld32(sa + x, s + x);
+            tmem_wait_ld();
+            if (__any_sync(0xffffffffu, t0 < lo || t0 + N > hi)) {
+                const unsigned span = static_cast<unsigned>(hi > lo ? hi - lo : 0);
+#pragma unroll
+                for (int x = 0; x < N; ++x) s[x] = static_cast<unsigned>(t0 + x - lo) < span ? s[x] : -INFINITY;
+            }
+            float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+            for (int x = 4; x < N; ++x) mx[x & 3] = fmaxf(mx[x & 3], s[x]);
+            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+            const bool grow = k == 0 ? top > st.m : top > st.m + kLazy;
+            if (__any_sync(0xffffffffu, grow)) {
+                const float f = grow ? ex2_approx(st.m - top) : 1.f;
+                if (grow) st.m = top;
+                st.l *= f;
+                if (k > 0) {
+                    // O holds the products up to the tile before; with one accumulator the
+                    // last of them may still run (with two, this S came after it)
+                    if (C::kStreams == 1) {
+                        if (!wait(&bars->o_full[0], (j - 1) & 1, bars, p.status)) return false;
+                        tc_fence_after();
+                    }
+                    const uint32_t oa = tmem + C::kO + (C::kStreams == 2 ? stream * D : 0);
+                    for (int x = 0; x < D; x += 32) {
+                        float o[32];
+                        tmem_ld32(oa + x, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int y = 0; y < 32; ++y) o[y] *= f;
+                        tmem_st32(oa + x, o);
+                    }
+                }
+            }
+            const float base = st.m == -INFINITY ? 0.f : -st.m;
+            float2 sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
+#pragma unroll
+            for (int x = 0; x < N; x += 32) {
+                uint32_t pk[16];
+#pragma unroll
+                for (int y = 0; y < 16; ++y) {
+                    float2 e = fma2(make_float2(s[x + 2 * y], s[x + 2 * y + 1]), make_float2(c, c), make_float2(base, base));
+                    e.x = ex2_approx(e.x);
+                    e.y = ex2_approx(e.y);
+                    sum[y & 1] = add2(sum[y & 1], e);
+                    pk[y] = pack_half2(e.x, e.y);
+                }
+                tmem_st16(sa + x / 2, pk);
+            }
+            sum[0] = add2(sum[0], sum[1]);
+            st.l += sum[0].x + sum[0].y;
+            tmem_wait_st();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->p_full[buf]);
+    }
+    return true;
+}
+
+// The output row of one thread, from TMEM (merge: + other's columns in shared memory).
+template <int D, int BITS>
+__device__ __forceinline__ void write_row(const ChunkParams& p, const Work& w, uint32_t oa, bool has, bool valid, int r, const State& st, float f,
+                                          const float* other, float fo) {
+    const int flat = w.row0 + r, i = flat / p.group_q, g = flat - i * p.group_q;
+    // 32 columns of O, scaled, by channel
+    auto columns = [&](int x, float (&v)[32]) {
+        float o[32];
+        if (has) {
+            tmem_ld32(oa + x, o);
+            tmem_wait_ld();
+        }
+#pragma unroll
+        for (int y = 0; y < 32; ++y) {
+            const int at = place<BITS>(y);
+            v[y] = has ? o[at] * f : 0.f;
+            if (other != nullptr) v[y] += other[(x + at) * kRowTile] * fo;
+        }
+    };
+    if (p.n_splits > 1) {
+        const long long at = static_cast<long long>(w.part) * p.rows_per_item + r;
+        if (valid) {
+            p.part_m[at] = st.m;
+            p.part_l[at] = st.l;
+        }
+        for (int x = 0; x < D; x += 32) {
+            float v[32];
+            columns(x, v);
+            if (valid) {
+#pragma unroll
+                for (int y = 0; y < 32; y += 4)
+                    *reinterpret_cast<float4*>(p.part_acc + at * D + x + y) = make_float4(v[y], v[y + 1], v[y + 2], v[y + 3]);
+            }
+        }
+        return;
+    }
+    uint16_t* out = p.out + ((static_cast<long long>(w.b) * p.n + i) * p.num_q_heads + w.h * p.group_q + g) * D;
+    if (!p.rotate_out) {
+        for (int x = 0; x < D; x += 32) {
+            float v[32];
+            columns(x, v);
+            if (valid) {
+#pragma unroll
+                for (int y = 0; y < 32; y += 8) {
+                    uint4 o;
+                    floats_to_halves<8>(*reinterpret_cast<float(*)[8]>(v + y), &o);
+                    *reinterpret_cast<uint4*>(out + x + y) = o;
+                }
+            }
+        }
+        return;
+    }
+    constexpr int N = D < 128 ? D : 128;
+    for (int half = 0; half < D / N; ++half) {
+        float v[N];
+#pragma unroll
+        for (int x = 0; x < N; x += 32) {
+            columns(x, *reinterpret_cast<float(*)[32]>(v + x));
+            if (D == 256) {
+                float y[32];
+                columns(128 + x, y);
+#pragma unroll
+                for (int k = 0; k < 32; ++k) v[x + k] = half ? v[x + k] - y[k] : v[x + k] + y[k];
+            }
+        }
+        hadamard_thread<N>(v);
+        if (valid) {
+#pragma unroll
+            for (int y = 0; y < N; y += 8) {
+                float x[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) x[k] = v[y + k] * p.rot_scale;
+                uint4 o;
+                floats_to_halves<8>(x, &o);
+                *reinterpret_cast<uint4*>(out + half * N + y) = o;
+            }
+        }
+    }
+}
+
+template <int D, int BITS>
+__device__ __forceinline__ void softmax_role(const ChunkParams& p, const Work& w, uint8_t* qs, uint8_t* slots, Bars* bars, int stream, bool pair) {
+    using C = Cfg<D, BITS>;
+    const int row = threadIdx.x & 127, lane = threadIdx.x & 31;
+    const int tile_row0 = pair ? stream * kRowTile : 0;
+    const int r = tile_row0 + row;  // row of the item
+    const bool valid = r < w.rows;
+    const bool active = __any_sync(0xffffffffu, valid);
+    if (pair || stream == 0) load_query<D, BITS>(p, w, qs + (pair ? stream : 0) * (kRowTile * D * 2), row, tile_row0);
+    fence_proxy_async_shared();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bars->q_full);
+    const int i = (w.row0 + (valid ? r : 0)) / p.group_q;
+    // (rows behind the last are zeros that see everything: they ask for no masks)
+    const int lo = valid ? first_key(p, i, w.ql, w.len) : 0, hi = valid ? end_key(p, i, w.ql, w.len) : 0x7fffffff;
+    State st{-INFINITY, 0.f};
+    const bool done = softmax_loop<D, BITS>(p, w, bars, stream, pair, active, lo, hi, st);
+    const bool split_keys = !pair && C::kStreams == 2;
+    // tiles of this stream, and the phase of its accumulator's last barrier
+    const int mine = split_keys ? (w.tiles + 1 - stream) / 2 : w.tiles;
+    bool ok = done;
+    if (ok && mine > 0) {
+        // (one accumulator: a phase a tile, of which the last score tile shows all but the last two to be over)
+        if (C::kStreams == 1 && mine > 1) ok = wait(&bars->o_full[0], (mine - 2) & 1, bars, p.status);
+        ok = ok && wait(&bars->o_full[C::kStreams == 2 ? stream : 0], C::kStreams == 1 ? (mine - 1) & 1 : 0, bars, p.status);
+        tc_fence_after();
+    }
+    const uint32_t oa = bars->tmem + (static_cast<uint32_t>((threadIdx.x >> 5) & 3) << 21) + C::kO + (C::kStreams == 2 ? stream * D : 0);
+    if (split_keys) {
+        // the second half's state through shared memory (the operands' place: no product is left that reads them)
+        float* buf = reinterpret_cast<float*>(slots);  // [D][128], then m and l
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        if (stream == 1 && ok && active) {
+            for (int x = 0; x < D && mine > 0; x += 32) {
+                float o[32];
+                tmem_ld32(oa + x, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int y = 0; y < 32; ++y) buf[(x + y) * kRowTile + row] = o[y];
+            }
+            buf[D * kRowTile + row] = st.m;
+            buf[(D + 1) * kRowTile + row] = st.l;
+        }
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        if (stream == 1 || !ok || !active) return;
+        const bool both = w.tiles > 1;
+        const float m1 = both ? buf[D * kRowTile + row] : -INFINITY, l1 = both ? buf[(D + 1) * kRowTile + row] : 0.f;
+        const float m = fmaxf(st.m, m1);
+        float f = st.m == -INFINITY ? 0.f : ex2_approx(st.m - m), fo = m1 == -INFINITY ? 0.f : ex2_approx(m1 - m);
+        State sum{m, st.l * f + l1 * fo};
+        if (p.n_splits == 1) {
+            const float inv = sum.l > 0.f || sum.l != sum.l ? 1.f / sum.l : 0.f;
+            f *= inv;
+            fo *= inv;
+        }
+        write_row<D, BITS>(p, w, oa, w.tiles > 0, valid, r, sum, f, both ? buf + row : nullptr, fo);
+        return;
+    }
+    if (!ok || !active) return;
+    const float f = p.n_splits > 1 ? 1.f : (st.l > 0.f || st.l != st.l ? 1.f / st.l : 0.f);
+    write_row<D, BITS>(p, w, oa, w.tiles > 0, valid, r, st, f, nullptr, 0.f);
+}
+
+// ------------------------------------------------------------------- kernel --
+template <int D, int BITS>
+__global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constant__ ChunkParams p) {
+    using C = Cfg<D, BITS>;
+    extern __shared__ uint8_t raw[];
+    __shared__ Bars bars;
+    uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    uint8_t* qs = base;
+    uint8_t* slots = base + C::kQ;
+    uint8_t* ring = slots + C::kSlots * C::kSlot;
+    const bool pair = C::kStreams == 2 && p.pair;
+    Work w;
+    if (!find_work<C::kTile>(p, p.rows_per_item, w)) return;  // the whole CTA
+    const int warp = threadIdx.x >> 5;
+    if (warp == 12) {
+        tmem_alloc(&bars.tmem, 512);
+    } else if (threadIdx.x == 13 * 32) {
+        for (int i = 0; i < 6; ++i) {
+            mbar_init(&bars.ring_full[i], 1);
+            mbar_init(&bars.ring_empty[i], C::kUnpackWarps);
+            mbar_init(&bars.slot_full[i], C::kUnpackWarps);
+            mbar_init(&bars.slot_empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bars.s_full[i], 1);
+            mbar_init(&bars.p_full[i], 4);
+            mbar_init(&bars.o_full[i], 1);
+        }
+        mbar_init(&bars.q_full, C::kStreams * 4);
+        mbar_init(&bars.drain, 1);
+        bars.abort = 0;
+        fence_mbarrier_init();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    // registers: 512 x 128 at launch
+    if (warp < C::kStreams * 4) {
+        regs_raise<200>();
+        softmax_role<D, BITS>(p, w, qs, slots, &bars, warp >> 2, pair);
+    } else if (warp < 12) {
+        regs_lower<C::kStreams == 2 ? 72 : 104>();
+        unpack_role<D, BITS>(p, w, ring, slots, &bars, pair);
+    } else {
+        regs_lower<40>();
+        if (warp == 12) {
+            if ((threadIdx.x & 31) == 0 && w.tiles > 0 && !mma_loop<D, BITS>(p, w, smem_u32(qs), smem_u32(slots), &bars, pair)) {
+                tc_commit(&bars.drain);  // given up: products in flight end before the CTA leaves
+                mbar_wait_bounded(&bars.drain, 0);
+            }
+        } else if (threadIdx.x == 13 * 32) {
+            load_role<D, BITS>(p, w, ring, &bars, pair);
+        }
+        __syncwarp();
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 12) {
+        tc_fence_after();
+        tmem_free(bars.tmem, 512);
+    }
+}
+
+// -------------------------------------------------------------------- merge --
+// A warp a row: the weights 2^(m_s - M) of the parts, then their sums.
+constexpr int kMergeThreads = 256;
+
+template <int D>
+__global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const __grid_constant__ ChunkParams p) {
+    constexpr int E = D / 32;
+    const int lane = threadIdx.x & 31;
+    const long long wid = static_cast<long long>(blockIdx.x) * (kMergeThreads / 32) + (threadIdx.x >> 5);
+    const int per = p.n * p.group_q;  // rows of a (sequence, kv head)
+    const int bh = static_cast<int>(wid / per), flat = static_cast<int>(wid - static_cast<long long>(bh) * per);
+    if (bh >= p.batch * p.num_kv_heads) return;
+    const int b = bh / p.num_kv_heads, h = bh - b * p.num_kv_heads, i = flat / p.group_q, g = flat - i * p.group_q;
+    const int ql = p.q_lens != nullptr ? min(max(p.q_lens[b], 0), p.n) : p.n;
     if (i >= ql) return;
-    int lo, hi;
-    row_span(p, i, ql, len, lo, hi);
-    float q[E], acc[E] = {};
-    const uint16_t* x = p.q + b * p.stride_b + hq * p.stride_h + i * p.stride_t + lane * E;
-    halves_to_floats<E>(x, q);
-    if (p.rotate_q) {
-        hadamard_warp<E>(q, lane, p.rot_scale);
+    const int m = flat / p.rows_per_item, r = flat - m * p.rows_per_item;
+    const long long part0 = (static_cast<long long>(bh) * p.m_items + m) * p.n_splits;
+    float top = -INFINITY;
+    for (int s = lane; s < p.n_splits; s += 32) top = fmaxf(top, p.part_m[(part0 + s) * p.rows_per_item + r]);
 #pragma unroll
-        for (int e = 0; e < E; ++e) q[e] = __half2float(__float2half_rn(q[e]));
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    float acc[E] = {}, l = 0.f;
+    for (int s0 = 0; s0 < p.n_splits; s0 += 32) {
+        float f = 0.f, pl = 0.f;
+        if (s0 + lane < p.n_splits) {
+            const long long at = (part0 + s0 + lane) * p.rows_per_item + r;
+            const float pm = p.part_m[at];
+            f = pm == -INFINITY ? 0.f : ex2_approx(pm - top);
+            pl = f == 0.f ? 0.f : f * p.part_l[at];
+        }
+        const int n = min(32, p.n_splits - s0);
+#pragma unroll 4
+        for (int s = 0; s < n; ++s) {
+            const float fs = __shfl_sync(0xffffffffu, f, s);
+            l += __shfl_sync(0xffffffffu, pl, s);
+            if (fs == 0.f) continue;  // (an empty part's sums were not written)
+            const float* a = p.part_acc + ((part0 + s0 + s) * p.rows_per_item + r) * D + lane * E;
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[e] = fmaf(fs, a[e], acc[e]);
+        }
     }
-    float m = -INFINITY, l = 0.f;
-    for (int t = lo; t < hi; ++t) {
-        const long long row = kv_row(p.map, p.num_kv_heads, b, h, t, p.status);
-        float k[E], v[E];
-        load_row<D, BITS>(p.k_codes, p.k_scale, p.k_bias, row, lane, k);
-        load_row<D, BITS>(p.v_codes, p.v_scale, p.v_bias, row, lane, v);
-        float s = 0.f;
+    const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
 #pragma unroll
-        for (int e = 0; e < E; ++e) s = fmaf(q[e], k[e], s);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        s *= p.score_scale_log2;
-        const float mn = fmaxf(m, s);
-        const float f = m == mn ? 1.f : exp2f(m - mn), w1 = mn == -INFINITY ? 0.f : exp2f(s - mn);
-        l = l * f + w1;
-#pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = fmaf(acc[e], f, w1 * v[e]);
-        m = mn;
-    }
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = l > 0.f ? acc[e] / l : 0.f;
+    for (int e = 0; e < E; ++e) acc[e] *= inv;
     if (p.rotate_out) hadamard_warp<E>(acc, lane, p.rot_scale);
-    uint16_t* o = p.out + ((static_cast<long long>(b) * p.n + i) * p.num_q_heads + hq) * D + lane * E;
-    floats_to_halves<E>(acc, o);
+    uint16_t* out = p.out + ((static_cast<long long>(b) * p.n + i) * p.num_q_heads + h * p.group_q + g) * D + lane * E;
+    floats_to_halves<E>(acc, out);
+}
+
+template <int D, int BITS>
+cudaError_t launch_main(const ChunkParams& p, cudaStream_t stream) {
+    using C = Cfg<D, BITS>;
+    cudaError_t e = cudaFuncSetAttribute(chunk_kernel<D, BITS>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (e != cudaSuccess) return e;
+    const long long ctas = static_cast<long long>(p.batch) * p.num_kv_heads * p.m_items * p.n_splits;
+    chunk_kernel<D, BITS><<<static_cast<unsigned>(ctas), kThreads, C::kSmem, stream>>>(p);
+    return cudaGetLastError();
 }
 
 template <int D>
-cudaError_t launch_bits(const ChunkParams& p, cudaStream_t stream) {
-    const long long warps = static_cast<long long>(p.batch) * p.n * p.num_q_heads;
-    const dim3 grid(static_cast<unsigned>((warps + kThreads / 32 - 1) / (kThreads / 32)));
-    if (p.bits == 8)
-        chunk_kernel<D, 8><<<grid, kThreads, 0, stream>>>(p);
-    else
-        chunk_kernel<D, 4><<<grid, kThreads, 0, stream>>>(p);
+cudaError_t launch_dim(const ChunkParams& p, cudaStream_t stream) {
+    cudaError_t e = p.bits == 8 ? launch_main<D, 8>(p, stream) : launch_main<D, 4>(p, stream);
+    if (e != cudaSuccess || p.n_splits == 1) return e;
+    const long long rows = static_cast<long long>(p.batch) * p.n * p.num_q_heads, each = kMergeThreads / 32;
+    chunk_merge_kernel<D><<<static_cast<unsigned>((rows + each - 1) / each), kMergeThreads, 0, stream>>>(p);
     return cudaGetLastError();
 }
 
 }  // namespace
 
+int chunk_tile_tokens(int head_dim) { return head_dim == 256 ? 64 : 128; }
+
 cudaError_t launch_chunk(const ChunkParams& p, int head_dim, cudaStream_t stream) {
-    if (head_dim == 64) return launch_bits<64>(p, stream);
-    return head_dim == 128 ? launch_bits<128>(p, stream) : launch_bits<256>(p, stream);
+    if (head_dim == 64) return launch_dim<64>(p, stream);
+    return head_dim == 128 ? launch_dim<128>(p, stream) : launch_dim<256>(p, stream);
 }
 
 }  // namespace tq

@@ -324,9 +324,17 @@ struct ChunkParams {
     int32_t window;           // 0: none
     int32_t full;             // every row attends to the whole sequence
     int32_t rotate_q, rotate_out;
-    float score_scale_log2;   // attn_scale * log2(e)
+    float score_scale_log2;   // |attn_scale| * log2(e), above 0
+    int32_t negate_q;         // attn_scale below 0
     float rot_scale;
     RowMap map;
+    // The rows of a (sequence, kv head), n * group_q, are cut into m_items items of
+    // rows_per_item rows, each item's keys into n_splits runs.
+    int32_t m_items, rows_per_item, n_splits;
+    int32_t pair;             // an item is two tiles of 128 rows (else one)
+    float* part_m;            // [items * n_splits][rows_per_item], log2 units (n_splits > 1)
+    float* part_l;
+    float* part_acc;          // [items * n_splits][rows_per_item][D]
 };
 
 // Pages of a pool (pages.cu).
@@ -366,6 +374,7 @@ struct PagesParams {
 
 // Launchers (return the cudaError_t of the launch).
 cudaError_t launch_chunk(const ChunkParams& p, int head_dim, cudaStream_t stream);
+int chunk_tile_tokens(int head_dim);  // keys per tile
 cudaError_t launch_pages_fork(const PagesParams& p, int sms, cudaStream_t stream);
 cudaError_t launch_pages_reserve(const PagesParams& p, int sms, cudaStream_t stream);
 cudaError_t launch_pages_compact(const PagesParams& p, int sms, cudaStream_t stream);

@@ -13,9 +13,41 @@ namespace {
 // ------------------------------------------------------------ several rows --
 constexpr long long kMaxChunkRows = 1LL << 28;  // n * num_heads
 
+// Most CTAs of a call that splits keys (bounds its workspace independently of the device).
+constexpr int kMaxChunkParts = 640;
+
+int chunk_rows(int32_t group, int32_t head_dim, int32_t n) {
+    return head_dim != 256 && static_cast<long long>(n) * group > 128 ? 256 : 128;
+}
+
+// Rows of partial states at most: every part of a call that splits, or every row's of one of each tile.
+size_t chunk_part_rows(int32_t batch, int32_t hq, int32_t hkv, int32_t head_dim, int32_t n, int32_t max_seq_len) {
+    const long long per = chunk_rows(hq / hkv, head_dim, n), most = kMaxChunkParts * (head_dim == 256 ? 128LL : 256LL);
+    const long long items = static_cast<long long>(batch) * hkv * ((static_cast<long long>(n) * (hq / hkv) + per - 1) / per);
+    const long long tiles = ceil_div(max_seq_len, chunk_tile_tokens(head_dim));
+    return static_cast<size_t>(items > most / per / tiles ? most : items * tiles * per);
+}
+
 size_t chunk_bytes(int32_t batch, int32_t hq, int32_t hkv, int32_t head_dim, int32_t n, int32_t max_seq_len) {
-    (void)batch, (void)hq, (void)hkv, (void)head_dim, (void)n, (void)max_seq_len;
-    return 256;
+    const size_t rows = chunk_part_rows(batch, hq, hkv, head_dim, n, max_seq_len);
+    return 2 * align256(rows * sizeof(float)) + align256(rows * head_dim * sizeof(float));
+}
+
+// How many runs the keys of each item are cut into: the fewest CTA-times, in
+// tiles, with what a CTA costs beside its tiles (start, first copies, output: some
+// four tiles' time) and what merging costs (a launch, the parts' way through memory).
+int chunk_splits(long long items, int tiles, int sms) {
+    int best = 1;
+    long long cost = -1;
+    for (int n = 1; n <= tiles && (n == 1 || items * n <= kMaxChunkParts); ++n) {
+        const long long waves = (items * n + sms - 1) / sms;
+        const long long c = waves * ((tiles + n - 1) / n + 4) + (n > 1 ? 4 + n / 8 : 0);
+        if (cost < 0 || c < cost) {
+            cost = c;
+            best = n;
+        }
+    }
+    return best;
 }
 
 bool chunk_sizes(int32_t batch, int32_t hq, int32_t hkv, int32_t head_dim, int32_t n, int32_t max_seq_len) {
@@ -69,9 +101,31 @@ tq_status chunk(const Store& c, const tq_query_rows* q, const int32_t* q_lens, c
     p.full = (flags & TQ_CHUNK_FULL) ? 1 : 0;
     p.rotate_q = (flags & TQ_ROTATE_K) ? 1 : 0;
     p.rotate_out = (flags & TQ_ROTATE_V) ? 1 : 0;
-    p.score_scale_log2 = attn_scale * 1.4426950408889634f;
+    // (a scale of 0 as one that makes every score vanish: minus infinity stays what it is)
+    const float scale = (attn_scale < 0.f ? -attn_scale : attn_scale) * 1.4426950408889634f;
+    p.score_scale_log2 = scale > 1e-30f ? scale : 1e-30f;
+    p.negate_q = attn_scale < 0.f ? 1 : 0;
     p.rot_scale = rotation_scale(c.head_dim);
     p.map = c.map;
+    DeviceFacts* f = nullptr;
+    s = device_facts(&f);
+    if (s != TQ_OK) return s;
+    const long long rows = static_cast<long long>(p.n) * p.group_q;
+    const int tile = chunk_tile_tokens(c.head_dim);
+    p.rows_per_item = chunk_rows(p.group_q, c.head_dim, p.n);
+    p.pair = p.rows_per_item == 256 ? 1 : 0;
+    p.m_items = ceil_div(rows, p.rows_per_item);
+    const long long items = static_cast<long long>(c.batch) * c.num_kv_heads * p.m_items;
+    // the most keys an item sees: all of them, or a window behind each of its tokens
+    long long keys = max_seq_len;
+    if (window > 0 && window + static_cast<long long>(p.rows_per_item / p.group_q) + 1 < keys) keys = window + p.rows_per_item / p.group_q + 1;
+    p.n_splits = chunk_splits(items, ceil_div(keys, tile), f->sms);
+    if (items * p.n_splits >= (1LL << 31)) return TQ_ERR_SHAPE;
+    const size_t part_rows = chunk_part_rows(c.batch, q->num_heads, c.num_kv_heads, c.head_dim, q->n, max_seq_len);
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    p.part_m = reinterpret_cast<float*>(ws);
+    p.part_l = reinterpret_cast<float*>(ws + align256(part_rows * sizeof(float)));
+    p.part_acc = reinterpret_cast<float*>(ws + 2 * align256(part_rows * sizeof(float)));
     return cuda_status(launch_chunk(p, c.head_dim, stream));
 }
 
