@@ -252,28 +252,32 @@ __device__ __forceinline__ void unpack_role(const ChunkParams& p, const Work& w,
             uint8_t* row = dst + g * (C::kTile * 128) + t * 128;
             const int swz = t & 7;
             const __half2 s2 = __half2half2(sc), b2 = __half2half2(bi);
-            // values past fp16's range and scales or biases that are no numbers
+            // values past fp16's range, scales or biases that are no numbers, keys that no row sees: apart
             const bool odd = !(__hfma(__habs(sc), __float2half_rn(BITS == 4 ? 15.f : 255.f), __habs(bi)) <= __float2half_rn(65504.f));
-            const bool drop = (edge && (t0 + t < w.klo || t0 + t >= w.khi)) || (odd && value && (__hisnan(sc) || __hisinf(sc) || __hisnan(bi) || __hisinf(bi)));
-#pragma unroll
-            for (int j = 0; j < kUnits; ++j) {
-                __half2 h[4];
-                if (BITS == 4)
-                    unpack8<4>(v[j], 0, h);
-                else
-                    unpack8<8>(v[2 * j], v[2 * j + 1], h);
-                if (drop || odd) {
+            const bool drop = edge && (t0 + t < w.klo || t0 + t >= w.khi);
+            if (__any_sync(0xffffffffu, odd || drop)) {
+                const float fs = __half2float(sc), fb = __half2float(bi);
+                const bool none = drop || (value && !(fabsf(fs) <= 65504.f && fabsf(fb) <= 65504.f));
+                for (int j = 0; j < kUnits; ++j) {
+                    __half2 h[4];
+                    unpack8<BITS>(v[BITS == 4 ? j : 2 * j], v[BITS == 4 ? j : 2 * j + 1], h);
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         const float2 f = __half22float2(h[k]);
-                        const float fs = __half2float(sc), fb = __half2float(bi);
-                        h[k] = drop ? __floats2half2_rn(0.f, 0.f)
+                        h[k] = none ? __floats2half2_rn(0.f, 0.f)
                                     : __floats2half2_rn(fminf(fmaxf(fmaf(f.x, fs, fb), -65504.f), 65504.f), fminf(fmaxf(fmaf(f.y, fs, fb), -65504.f), 65504.f));
                     }
-                } else {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) h[k] = __hfma2(h[k], s2, b2);
+                    const int u = u0 + (j ^ x);
+                    *reinterpret_cast<uint4*>(row + ((u ^ swz) << 4)) = *reinterpret_cast<uint4*>(h);
                 }
+                continue;
+            }
+#pragma unroll
+            for (int j = 0; j < kUnits; ++j) {
+                __half2 h[4];
+                unpack8<BITS>(v[BITS == 4 ? j : 2 * j], v[BITS == 4 ? j : 2 * j + 1], h);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) h[k] = __hfma2(h[k], s2, b2);
                 const int u = u0 + (j ^ x);
                 *reinterpret_cast<uint4*>(row + ((u ^ swz) << 4)) = *reinterpret_cast<uint4*>(h);
             }
@@ -293,23 +297,32 @@ __device__ __forceinline__ bool mma_loop(const ChunkParams& p, const Work& w, ui
     using C = Cfg<D, BITS>;
     const uint32_t tmem = bars->tmem;
     auto slot_wait = [&](int e) { return wait(&bars->slot_full[e % C::kSlots], (e / C::kSlots) & 1, bars, p.status); };
-    auto release = [&](int e) { tc_commit(&bars->slot_empty[e % C::kSlots]); };
+    auto commit = [&](uint64_t* bar) {
+        if (elect_one()) tc_commit(bar);
+        __syncwarp();
+    };
+    auto release = [&](int e) { commit(&bars->slot_empty[e % C::kSlots]); };
     // S[buf] = Q[qt] K^T, K in the slot of entry e
     auto qk = [&](int e, int qt, int buf) {
-        const uint32_t kb = slots + (e % C::kSlots) * C::kSlot, qb = q + qt * (kRowTile * D * 2);
+        const uint64_t kd = smem_operand(slots + (e % C::kSlots) * C::kSlot, 16), qd = smem_operand(q + qt * (kRowTile * D * 2), 16);
+        if (elect_one()) {
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-            tc_mma_ss(tmem + buf * C::kS, smem_operand(qb + (k / 4) * (kRowTile * 128) + (k % 4) * 32, 16),
-                      smem_operand(kb + (k / 4) * (C::kTile * 128) + (k % 4) * 32, 16), mma_desc(kRowTile, C::kTile, false), k > 0);
-        tc_commit(&bars->s_full[buf]);
+            for (int k = 0; k < D / 16; ++k)
+                tc_mma_ss(tmem + buf * C::kS, qd + (((k / 4) * (kRowTile * 128) + (k % 4) * 32) >> 4),
+                          kd + (((k / 4) * (C::kTile * 128) + (k % 4) * 32) >> 4), mma_desc(kRowTile, C::kTile, false), k > 0);
+            tc_commit(&bars->s_full[buf]);
+        }
+        __syncwarp();
     };
     // O[o] += P[buf] V, V in the slot of entry e
     auto pv = [&](int e, int buf, int o, bool add) {
-        const uint32_t vb = slots + (e % C::kSlots) * C::kSlot;
+        const uint64_t vd = smem_operand(slots + (e % C::kSlots) * C::kSlot, C::kTile * 128);
+        if (elect_one()) {
 #pragma unroll
-        for (int k = 0; k < C::kTile / 16; ++k)
-            tc_mma_ts(tmem + C::kO + o * D, tmem + buf * C::kS + k * 8, smem_operand(vb + k * 2048, C::kTile * 128),
-                      mma_desc(kRowTile, D, true), add || k > 0);
+            for (int k = 0; k < C::kTile / 16; ++k)
+                tc_mma_ts(tmem + C::kO + o * D, tmem + buf * C::kS + k * 8, vd + ((k * 2048) >> 4), mma_desc(kRowTile, D, true), add || k > 0);
+        }
+        __syncwarp();
     };
     if (!wait(&bars->q_full, 0, bars, p.status)) return false;
     const int T = w.tiles;
@@ -330,7 +343,7 @@ __device__ __forceinline__ bool mma_loop(const ChunkParams& p, const Work& w, ui
                 tc_fence_after();
                 qk(ke, 0, 0);
             } else {
-                tc_commit(&bars->o_full[0]);
+                commit(&bars->o_full[0]);
             }
             if (!wait(&bars->p_full[1], j & 1, bars, p.status)) return false;
             tc_fence_after();
@@ -340,7 +353,7 @@ __device__ __forceinline__ bool mma_loop(const ChunkParams& p, const Work& w, ui
                 qk(ke, 1, 1);
                 release(ke);
             } else {
-                tc_commit(&bars->o_full[1]);
+                commit(&bars->o_full[1]);
             }
         }
         return true;
@@ -359,7 +372,7 @@ __device__ __forceinline__ bool mma_loop(const ChunkParams& p, const Work& w, ui
         pv(ve, buf, o, C::kStreams == 2 ? j > 1 : j > 0);
         release(ve);
         // (one accumulator: the softmax may have to rescale it before the next product)
-        if (C::kStreams == 1 || j + 2 >= T) tc_commit(&bars->o_full[o]);
+        if (C::kStreams == 1 || j + 2 >= T) commit(&bars->o_full[o]);
         if (j + 2 < T) {
             const int ke = key_entry(j + 2, false);
             if (!slot_wait(ke)) return false;
@@ -735,8 +748,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     } else {
         regs_lower<40>();
         if (warp == 12) {
-            if ((threadIdx.x & 31) == 0 && w.tiles > 0 && !mma_loop<D, BITS>(p, w, smem_u32(qs), smem_u32(slots), &bars, pair)) {
-                tc_commit(&bars.drain);  // given up: products in flight end before the CTA leaves
+            if (w.tiles > 0 && !mma_loop<D, BITS>(p, w, smem_u32(qs), smem_u32(slots), &bars, pair)) {
+                __syncwarp();
+                if (elect_one()) tc_commit(&bars.drain);  // given up: products in flight end before the CTA leaves
                 mbar_wait_bounded(&bars.drain, 0);
             }
         } else if (threadIdx.x == 13 * 32) {

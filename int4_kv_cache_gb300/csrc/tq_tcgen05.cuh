@@ -39,6 +39,14 @@ __host__ __device__ constexpr uint32_t mma_desc(int m, int n, bool b_mn) {
     return 1u << 4 | (b_mn ? 1u << 16 : 0u) | static_cast<uint32_t>(n >> 3) << 17 | static_cast<uint32_t>(m >> 4) << 24;
 }
 
+// One lane of a converged warp, the same one every time.  (The warp runs the loop
+// around the products together, so that their operands stay in uniform registers.)
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+    return one != 0;
+}
+
 // D[tmem] (+)= A[smem] B[smem], one K step of 16.
 __device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t desc, bool add) {
     asm volatile(
