@@ -33,7 +33,7 @@ namespace tq {
 
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 640;       // 8 softmax warps, 8 that unpack, 4 of which one issues products and one copies
 constexpr int kRowTile = 128;
 constexpr float kLazy = 8.f;  // log2 of how far P may grow before O is rescaled
 
@@ -41,8 +41,8 @@ template <int D, int BITS>
 struct Cfg {
     static constexpr int kStreams = D == 256 ? 1 : 2;         // softmax warpgroups, output accumulators
     static constexpr int kTile = D == 256 ? 64 : 128;         // keys
-    static constexpr int kUnpackWarp = kStreams * 4;          // first unpacking warp
-    static constexpr int kUnpackWarps = 12 - kUnpackWarp;     // 4 (8 at head_dim 256)
+    static constexpr int kUnpackWarp = 8;                     // first unpacking warp
+    static constexpr int kUnpackWarps = 8;
     static constexpr int kBlocks = D / 64;                    // blocks of 64 channels: 128-byte rows
     static constexpr int kSlot = kTile * D * 2;               // one unpacked tile of keys or values
     static constexpr int kSlots = D == 64 ? 6 : 3;
@@ -52,7 +52,7 @@ struct Cfg {
     static constexpr int kRing = D == 64 ? 6 : (BITS == 8 ? 3 : 6);
     static constexpr int kQ = kStreams * kRowTile * D * 2;
     static constexpr int kSmem = 1024 + kQ + kSlots * kSlot + kRing * kEntry;
-    static constexpr uint32_t kS = kTile;                     // TMEM columns of S (and P)
+    static constexpr uint32_t kS = kTile;                     // TMEM columns of S; P lies in their upper half
     static constexpr uint32_t kO = 256;                       // first TMEM column of O
     static_assert(kSmem + 512 <= 232448, "shared memory of a CTA");
     static_assert(kO + kStreams * D <= 512 && 2 * kS <= kO, "TMEM");
@@ -143,13 +143,25 @@ __device__ __forceinline__ int value_entry(int tile, int tiles, bool pair) {
     return pair ? 2 * tile + 1 : (tile == tiles - 1 ? 2 * tiles - 1 : 2 * tile + 2);
 }
 
-// Waits for a phase; false when it took too long or another warp has given up.
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, Bars* bars, int32_t* status) {
-    if (mbar_try_wait(bar, parity)) return true;
+// Whether a phase is over; the hardware holds the warp for a while if it is not.
+// (With a time limit of its own, as mbar_try_wait asks for, the wait becomes a loop that
+// polls and sleeps: 350 sleeps and 700 polls a tile of keys, in the way of the warps that work.)
+__device__ __forceinline__ bool over(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
+// The rest of a wait that did not end at once; false when it took too long or another warp has given up.
+__device__ __forceinline__ bool wait_on(uint32_t bar, uint32_t parity, Bars* bars, int32_t* status) {
     const uint64_t t0 = globaltimer_ns();
     for (uint32_t it = 1;; ++it) {
-        if (mbar_try_wait(bar, parity)) return true;
-        if ((it & 63u) == 0) {
+        if (over(bar, parity)) return true;
+        if ((it & 15u) == 0) {
             if (*reinterpret_cast<volatile int32_t*>(&bars->abort) != 0) return false;
             if (globaltimer_ns() - t0 > 2000000000ull) {
                 *reinterpret_cast<volatile int32_t*>(&bars->abort) = 1;
@@ -158,6 +170,12 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, Bars* bars,
             }
         }
     }
+}
+
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, Bars* bars, int32_t* status) {
+    const uint32_t at = smem_u32(bar);
+    if (over(at, parity) || over(at, parity)) return true;
+    return wait_on(at, parity, bars, status);
 }
 
 // ------------------------------------------------------------------ loader --
@@ -320,65 +338,36 @@ __device__ __forceinline__ bool mma_loop(const ChunkParams& p, const Work& w, ui
         if (elect_one()) {
 #pragma unroll
             for (int k = 0; k < C::kTile / 16; ++k)
-                tc_mma_ts(tmem + C::kO + o * D, tmem + buf * C::kS + k * 8, vd + ((k * 2048) >> 4), mma_desc(kRowTile, D, true), add || k > 0);
+                tc_mma_ts(tmem + C::kO + o * D, tmem + buf * C::kS + C::kS / 2 + k * 8, vd + ((k * 2048) >> 4), mma_desc(kRowTile, D, true), add || k > 0);
         }
         __syncwarp();
     };
     if (!wait(&bars->q_full, 0, bars, p.status)) return false;
-    const int T = w.tiles;
-    if (pair) {
-        if (!slot_wait(0)) return false;
-        tc_fence_after();
-        qk(0, 0, 0);
-        qk(0, 1, 1);
-        release(0);
-        for (int j = 0; j < T; ++j) {
-            const int ve = 2 * j + 1, ke = 2 * j + 2;
+    // Step s works on buffer s & 1: P V of its tile, then Q K^T of step s + 2 into the
+    // place that P leaves.  pair: a tile of keys takes two steps, one for each row
+    // tile; else steps and tiles of keys are the same.
+    const int steps = pair ? 2 * w.tiles : w.tiles;
+#pragma unroll 1
+    for (int s = -2; s < steps; ++s) {
+        const int buf = s & 1;
+        const bool last_user = !pair || buf == 1;
+        if (s >= 0) {
+            const int ve = pair ? s | 1 : value_entry(s, w.tiles, false);
             if (!slot_wait(ve)) return false;
-            if (!wait(&bars->p_full[0], j & 1, bars, p.status)) return false;
+            if (!wait(&bars->p_full[buf], (s >> 1) & 1, bars, p.status)) return false;
             tc_fence_after();
-            pv(ve, 0, 0, j > 0);
-            if (j + 1 < T) {
-                if (!slot_wait(ke)) return false;
-                tc_fence_after();
-                qk(ke, 0, 0);
-            } else {
-                commit(&bars->o_full[0]);
-            }
-            if (!wait(&bars->p_full[1], j & 1, bars, p.status)) return false;
-            tc_fence_after();
-            pv(ve, 1, 1, j > 0);
-            release(ve);
-            if (j + 1 < T) {
-                qk(ke, 1, 1);
-                release(ke);
-            } else {
-                commit(&bars->o_full[1]);
-            }
+            const int o = C::kStreams == 2 ? buf : 0;
+            pv(ve, buf, o, C::kStreams == 2 ? s > 1 : s > 0);
+            if (last_user) release(ve);
+            // (one accumulator: the softmax may have to rescale it before the next product)
+            if (C::kStreams == 1 || s + 2 >= steps) commit(&bars->o_full[o]);
         }
-        return true;
-    }
-    for (int j = 0; j < 2 && j < T; ++j) {
-        if (!slot_wait(key_entry(j, false))) return false;
-        tc_fence_after();
-        qk(key_entry(j, false), 0, j);
-        release(key_entry(j, false));
-    }
-    for (int j = 0; j < T; ++j) {
-        const int ve = value_entry(j, T, false), buf = j & 1, o = C::kStreams == 2 ? buf : 0;
-        if (!slot_wait(ve)) return false;
-        if (!wait(&bars->p_full[buf], (j >> 1) & 1, bars, p.status)) return false;
-        tc_fence_after();
-        pv(ve, buf, o, C::kStreams == 2 ? j > 1 : j > 0);
-        release(ve);
-        // (one accumulator: the softmax may have to rescale it before the next product)
-        if (C::kStreams == 1 || j + 2 >= T) commit(&bars->o_full[o]);
-        if (j + 2 < T) {
-            const int ke = key_entry(j + 2, false);
+        if (s + 2 < steps) {
+            const int ke = key_entry(pair ? (s + 2) >> 1 : s + 2, pair);
             if (!slot_wait(ke)) return false;
             tc_fence_after();
-            qk(ke, 0, buf);
-            release(ke);
+            qk(ke, pair ? buf : 0, buf);
+            if (last_user) release(ke);
         }
     }
     return true;
@@ -428,13 +417,13 @@ __device__ __forceinline__ void store_q64(uint8_t* block, int row, const __half2
     }
 }
 
-template <int D, int BITS>
+template <int D, int BITS, bool ROT>
 __device__ __forceinline__ void load_query(const ChunkParams& p, const Work& w, uint8_t* tile, int row, int tile_row0) {
     const int r = tile_row0 + row;
     const bool valid = r < w.rows;
     const int flat = w.row0 + (valid ? r : 0), i = flat / p.group_q, g = flat - i * p.group_q;
     const uint4* src = reinterpret_cast<const uint4*>(p.q + w.b * p.stride_b + (w.h * p.group_q + g) * p.stride_h + i * p.stride_t);
-    if (!p.rotate_q) {
+    if (!ROT || !p.rotate_q) {
 #pragma unroll
         for (int blk = 0; blk < D / 64; ++blk) {
             __half2 x[32];
@@ -497,19 +486,30 @@ __device__ __forceinline__ bool softmax_loop(const ChunkParams& p, const Work& w
         if (active) {
             const uint32_t sa = tmem + buf * C::kS;
             const int t0 = (w.tile0 + j) * C::kTile;
-            float s[N];
+            // 64 columns at a time: the first half (of two) is read twice, so that
+            // a row's scores need not fit in registers; P goes where the second
+            // half's scores were
+            constexpr int H = N / 64;
+            const bool mask = __any_sync(0xffffffffu, t0 < lo || t0 + N > hi);
+            const unsigned span = static_cast<unsigned>(hi > lo ? hi - lo : 0);
+            float s[64];
+            auto load = [&](int half) {
+                tmem_ld64(sa + half * 64, s);
+                tmem_wait_ld();
+                if (mask) {
+                    const int at = t0 + half * 64 - lo;
 #pragma unroll
-            for (int x = 0; x < N; x += 32) tmem_ld32(sa + x, s + x);
-            tmem_wait_ld();
-            if (__any_sync(0xffffffffu, t0 < lo || t0 + N > hi)) {
-                const unsigned span = static_cast<unsigned>(hi > lo ? hi - lo : 0);
+                    for (int x = 0; x < 64; ++x) s[x] = static_cast<unsigned>(at + x) < span ? s[x] : -INFINITY;
+                }
+            };
+            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int x = 0; x < N; ++x) s[x] = static_cast<unsigned>(t0 + x - lo) < span ? s[x] : -INFINITY;
+            for (int half = 0; half < H; ++half) {
+                load(half);
+#pragma unroll
+                for (int x = 0; x < 64; x += 2) mx[(x >> 1) & 3] = max3(mx[(x >> 1) & 3], s[x], s[x + 1]);
             }
-            float mx[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-            for (int x = 4; x < N; ++x) mx[x & 3] = fmaxf(mx[x & 3], s[x]);
-            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+            const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * c;
             const bool grow = k == 0 ? top > st.m : top > st.m + kLazy;
             if (__any_sync(0xffffffffu, grow)) {
                 const float f = grow ? ex2_approx(st.m - top) : 1.f;
@@ -536,17 +536,21 @@ __device__ __forceinline__ bool softmax_loop(const ChunkParams& p, const Work& w
             const float base = st.m == -INFINITY ? 0.f : -st.m;
             float2 sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
 #pragma unroll
-            for (int x = 0; x < N; x += 32) {
-                uint32_t pk[16];
+            for (int half = H - 1; half >= 0; --half) {
+                if (half < H - 1) load(half);
 #pragma unroll
-                for (int y = 0; y < 16; ++y) {
-                    float2 e = fma2(make_float2(s[x + 2 * y], s[x + 2 * y + 1]), make_float2(c, c), make_float2(base, base));
-                    e.x = ex2_approx(e.x);
-                    e.y = ex2_approx(e.y);
-                    sum[y & 1] = add2(sum[y & 1], e);
-                    pk[y] = pack_half2(e.x, e.y);
+                for (int x = 0; x < 64; x += 32) {
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int y = 0; y < 16; ++y) {
+                        float2 e = fma2(make_float2(s[x + 2 * y], s[x + 2 * y + 1]), make_float2(c, c), make_float2(base, base));
+                        e.x = ex2_approx(e.x);
+                        e.y = ex2_approx(e.y);
+                        sum[y & 1] = add2(sum[y & 1], e);
+                        pk[y] = pack_half2(e.x, e.y);
+                    }
+                    tmem_st16(sa + C::kS / 2 + half * 32 + x / 2, pk);
                 }
-                tmem_st16(sa + x / 2, pk);
             }
             sum[0] = add2(sum[0], sum[1]);
             st.l += sum[0].x + sum[0].y;
@@ -560,7 +564,7 @@ __device__ __forceinline__ bool softmax_loop(const ChunkParams& p, const Work& w
 }
 
 // The output row of one thread, from TMEM (merge: + other's columns in shared memory).
-template <int D, int BITS>
+template <int D, int BITS, bool ROT>
 __device__ __forceinline__ void write_row(const ChunkParams& p, const Work& w, uint32_t oa, bool has, bool valid, int r, const State& st, float f,
                                           const float* other, float fo) {
     const int flat = w.row0 + r, i = flat / p.group_q, g = flat - i * p.group_q;
@@ -596,7 +600,7 @@ __device__ __forceinline__ void write_row(const ChunkParams& p, const Work& w, u
         return;
     }
     uint16_t* out = p.out + ((static_cast<long long>(w.b) * p.n + i) * p.num_q_heads + w.h * p.group_q + g) * D;
-    if (!p.rotate_out) {
+    if (!ROT || !p.rotate_out) {
         for (int x = 0; x < D; x += 32) {
             float v[32];
             columns(x, v);
@@ -639,7 +643,7 @@ __device__ __forceinline__ void write_row(const ChunkParams& p, const Work& w, u
     }
 }
 
-template <int D, int BITS>
+template <int D, int BITS, bool ROT>
 __device__ __forceinline__ void softmax_role(const ChunkParams& p, const Work& w, uint8_t* qs, uint8_t* slots, Bars* bars, int stream, bool pair) {
     using C = Cfg<D, BITS>;
     const int row = threadIdx.x & 127, lane = threadIdx.x & 31;
@@ -647,7 +651,7 @@ __device__ __forceinline__ void softmax_role(const ChunkParams& p, const Work& w
     const int r = tile_row0 + row;  // row of the item
     const bool valid = r < w.rows;
     const bool active = __any_sync(0xffffffffu, valid);
-    if (pair || stream == 0) load_query<D, BITS>(p, w, qs + (pair ? stream : 0) * (kRowTile * D * 2), row, tile_row0);
+    if (pair || stream == 0) load_query<D, BITS, ROT>(p, w, qs + (pair ? stream : 0) * (kRowTile * D * 2), row, tile_row0);
     fence_proxy_async_shared();
     __syncwarp();
     if (lane == 0) mbar_arrive(&bars->q_full);
@@ -694,21 +698,22 @@ __device__ __forceinline__ void softmax_role(const ChunkParams& p, const Work& w
             f *= inv;
             fo *= inv;
         }
-        write_row<D, BITS>(p, w, oa, w.tiles > 0, valid, r, sum, f, both ? buf + row : nullptr, fo);
+        write_row<D, BITS, ROT>(p, w, oa, w.tiles > 0, valid, r, sum, f, both ? buf + row : nullptr, fo);
         return;
     }
     if (!ok || !active) return;
     const float f = p.n_splits > 1 ? 1.f : (st.l > 0.f || st.l != st.l ? 1.f / st.l : 0.f);
-    write_row<D, BITS>(p, w, oa, w.tiles > 0, valid, r, st, f, nullptr, 0.f);
+    write_row<D, BITS, ROT>(p, w, oa, w.tiles > 0, valid, r, st, f, nullptr, 0.f);
 }
 
 // ------------------------------------------------------------------- kernel --
-template <int D, int BITS>
+// ROT: with the transforms of rotated caches (apart, as they take registers and code).
+template <int D, int BITS, bool ROT>
 __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constant__ ChunkParams p) {
     using C = Cfg<D, BITS>;
     extern __shared__ uint8_t raw[];
     __shared__ Bars bars;
-    uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    uint8_t* base = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);  // (an offset, so that it stays a shared-memory pointer)
     uint8_t* qs = base;
     uint8_t* slots = base + C::kQ;
     uint8_t* ring = slots + C::kSlots * C::kSlot;
@@ -716,9 +721,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     Work w;
     if (!find_work<C::kTile>(p, p.rows_per_item, w)) return;  // the whole CTA
     const int warp = threadIdx.x >> 5;
-    if (warp == 12) {
+    if (warp == 16) {
         tmem_alloc(&bars.tmem, 512);
-    } else if (threadIdx.x == 13 * 32) {
+    } else if (threadIdx.x == 17 * 32) {
         for (int i = 0; i < 6; ++i) {
             mbar_init(&bars.ring_full[i], 1);
             mbar_init(&bars.ring_empty[i], C::kUnpackWarps);
@@ -738,29 +743,32 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    // registers: 512 x 128 at launch
+    // registers: 640 x 96 at launch; 256 x 144 + 256 x 72 + 128 x 48 (one
+    // accumulator: 128 x 200 + 128 x 48 + 256 x 72 + 128 x 48)
     if (warp < C::kStreams * 4) {
-        regs_raise<200>();
-        softmax_role<D, BITS>(p, w, qs, slots, &bars, warp >> 2, pair);
-    } else if (warp < 12) {
-        regs_lower<C::kStreams == 2 ? 72 : 104>();
+        regs_raise<C::kStreams == 2 ? 144 : 200>();
+        softmax_role<D, BITS, ROT>(p, w, qs, slots, &bars, warp >> 2, pair);
+    } else if (warp < 8) {
+        regs_lower<48>();
+    } else if (warp < 16) {
+        regs_lower<72>();
         unpack_role<D, BITS>(p, w, ring, slots, &bars, pair);
     } else {
-        regs_lower<40>();
-        if (warp == 12) {
+        regs_lower<48>();
+        if (warp == 16) {
             if (w.tiles > 0 && !mma_loop<D, BITS>(p, w, smem_u32(qs), smem_u32(slots), &bars, pair)) {
                 __syncwarp();
                 if (elect_one()) tc_commit(&bars.drain);  // given up: products in flight end before the CTA leaves
                 mbar_wait_bounded(&bars.drain, 0);
             }
-        } else if (threadIdx.x == 13 * 32) {
+        } else if (threadIdx.x == 17 * 32) {
             load_role<D, BITS>(p, w, ring, &bars, pair);
         }
         __syncwarp();
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 12) {
+    if (warp == 16) {
         tc_fence_after();
         tmem_free(bars.tmem, 512);
     }
@@ -815,19 +823,21 @@ __global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const __grid
     floats_to_halves<E>(acc, out);
 }
 
-template <int D, int BITS>
+template <int D, int BITS, bool ROT>
 cudaError_t launch_main(const ChunkParams& p, cudaStream_t stream) {
     using C = Cfg<D, BITS>;
-    cudaError_t e = cudaFuncSetAttribute(chunk_kernel<D, BITS>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    cudaError_t e = cudaFuncSetAttribute(chunk_kernel<D, BITS, ROT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
     const long long ctas = static_cast<long long>(p.batch) * p.num_kv_heads * p.m_items * p.n_splits;
-    chunk_kernel<D, BITS><<<static_cast<unsigned>(ctas), kThreads, C::kSmem, stream>>>(p);
+    chunk_kernel<D, BITS, ROT><<<static_cast<unsigned>(ctas), kThreads, C::kSmem, stream>>>(p);
     return cudaGetLastError();
 }
 
 template <int D>
 cudaError_t launch_dim(const ChunkParams& p, cudaStream_t stream) {
-    cudaError_t e = p.bits == 8 ? launch_main<D, 8>(p, stream) : launch_main<D, 4>(p, stream);
+    const bool rot = p.rotate_q || (p.rotate_out && p.n_splits == 1);
+    cudaError_t e = p.bits == 8 ? (rot ? launch_main<D, 8, true>(p, stream) : launch_main<D, 8, false>(p, stream))
+                                : (rot ? launch_main<D, 4, true>(p, stream) : launch_main<D, 4, false>(p, stream));
     if (e != cudaSuccess || p.n_splits == 1) return e;
     const long long rows = static_cast<long long>(p.batch) * p.n * p.num_q_heads, each = kMergeThreads / 32;
     chunk_merge_kernel<D><<<static_cast<unsigned>((rows + each - 1) / each), kMergeThreads, 0, stream>>>(p);

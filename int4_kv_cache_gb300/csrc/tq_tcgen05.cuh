@@ -81,6 +81,10 @@ __device__ __forceinline__ void tmem_ld32(uint32_t addr, float* v) {
           "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
         : "r"(addr));
 }
+__device__ __forceinline__ void tmem_ld64(uint32_t addr, float* v) {
+    tmem_ld32(addr, v);
+    tmem_ld32(addr + 32, v + 32);
+}
 __device__ __forceinline__ void tmem_st32(uint32_t addr, const float* v) {
     const uint32_t* r = reinterpret_cast<const uint32_t*>(v);
     asm volatile(
@@ -99,6 +103,12 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
         "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
         "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
 }
 
 // Two fp32 operations an instruction.
