@@ -138,10 +138,6 @@ __device__ __forceinline__ bool entry_of(int e, int tiles, bool pair, int& tile)
     tile = (e >> 1) - 1;
     return true;
 }
-__device__ __forceinline__ int key_entry(int tile, bool pair) { return pair ? 2 * tile : (tile == 0 ? 0 : 2 * tile - 1); }
-__device__ __forceinline__ int value_entry(int tile, int tiles, bool pair) {
-    return pair ? 2 * tile + 1 : (tile == tiles - 1 ? 2 * tiles - 1 : 2 * tile + 2);
-}
 
 // Whether a phase is over; the hardware holds the warp for a while if it is not.
 // (With a time limit of its own, as mbar_try_wait asks for, the wait becomes a loop that
@@ -172,10 +168,11 @@ __device__ __forceinline__ bool wait_on(uint32_t bar, uint32_t parity, Bars* bar
     }
 }
 
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, Bars* bars, int32_t* status) {
+    return over(bar, parity) || wait_on(bar, parity, bars, status);
+}
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, Bars* bars, int32_t* status) {
-    const uint32_t at = smem_u32(bar);
-    if (over(at, parity) || over(at, parity)) return true;
-    return wait_on(at, parity, bars, status);
+    return wait(smem_u32(bar), parity, bars, status);
 }
 
 // ------------------------------------------------------------------ loader --
@@ -206,6 +203,12 @@ __device__ __forceinline__ void load_role(const ChunkParams& p, const Work& w, u
 // ---------------------------------------------------------------- unpacking --
 // Eight codes as four pairs of fp16.  int4: pairs (0,4), (1,5), (2,6), (3,7) of a
 // word, the order that shifts and masks give; queries and outputs follow it.
+__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t mask, uint32_t bits) {
+    uint32_t d;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(a), "r"(mask), "r"(bits));
+    return d;
+}
+
 template <int BITS>
 __device__ __forceinline__ void unpack8(uint32_t w0, uint32_t w1, __half2 (&c)[4]) {
     auto h2 = [](uint32_t x) { return *reinterpret_cast<__half2*>(&x); };
@@ -213,10 +216,10 @@ __device__ __forceinline__ void unpack8(uint32_t w0, uint32_t w1, __half2 (&c)[4
     if (BITS == 4) {
         // a nibble in the low bits of 0x6400 counts from 1,024 on, four bits up in 0x5400 from 64 on
         const uint32_t hi = w0 >> 8;
-        c[0] = __hsub2(h2((w0 & 0x000f000fu) | 0x64006400u), k1024);
-        c[1] = __hsub2(h2((w0 & 0x00f000f0u) | 0x54005400u), k64);
-        c[2] = __hsub2(h2((hi & 0x000f000fu) | 0x64006400u), k1024);
-        c[3] = __hsub2(h2((hi & 0x00f000f0u) | 0x54005400u), k64);
+        c[0] = __hsub2(h2(and_or(w0, 0x000f000fu, 0x64006400u)), k1024);
+        c[1] = __hsub2(h2(and_or(w0, 0x00f000f0u, 0x54005400u)), k64);
+        c[2] = __hsub2(h2(and_or(hi, 0x000f000fu, 0x64006400u)), k1024);
+        c[3] = __hsub2(h2(and_or(hi, 0x00f000f0u, 0x54005400u)), k64);
     } else {
         c[0] = __hsub2(h2(__byte_perm(w0, 0x64646464u, 0x4140)), k1024);
         c[1] = __hsub2(h2(__byte_perm(w0, 0x64646464u, 0x4342)), k1024);
@@ -225,57 +228,83 @@ __device__ __forceinline__ void unpack8(uint32_t w0, uint32_t w1, __half2 (&c)[4
     }
 }
 
+__device__ __forceinline__ uint4 lds128(uint32_t at) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
+    return v;
+}
+__device__ __forceinline__ __half lds16(uint32_t at) {
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(at));
+    return __ushort_as_half(v);
+}
+__device__ __forceinline__ void sts128(uint32_t at, const __half2 (&h)[4]) {
+    const uint32_t* v = reinterpret_cast<const uint32_t*>(h);
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
+}
+
+// A thread takes the same 16-byte piece of every 2^n-th key's codes: where its
+// outputs go, and in which order, is the same for all of them.
 template <int D, int BITS>
-__device__ __forceinline__ void unpack_role(const ChunkParams& p, const Work& w, const uint8_t* ring, uint8_t* slots, Bars* bars, bool pair) {
+__device__ __forceinline__ void unpack_role(const ChunkParams& p, const Work& w, uint32_t ring, uint32_t slots, Bars* bars, bool pair) {
     using C = Cfg<D, BITS>;
     constexpr int kUnits = BITS == 4 ? 4 : 2;             // 16-byte pieces of fp16 that 16 bytes of codes give
     constexpr int kChunks = D * BITS / 8 / 16;            // 16-byte pieces of codes per key
     constexpr int kT = C::kUnpackWarps * 32;
+    constexpr int kKeys = kT / kChunks;                   // keys from one piece of a thread to its next
+    constexpr int kIts = C::kTile / kKeys;
+    static_assert(kKeys % 8 == 0 && kIts * kKeys == C::kTile, "pieces of a thread");
     const int tid = threadIdx.x - C::kUnpackWarp * 32, lane = threadIdx.x & 31;
+    const int t = tid / kChunks, ck = tid % kChunks, g = ck * kUnits / 8, u0 = ck * kUnits % 8;
+    // eight lanes write eight different 16-byte columns: pieces of other blocks are
+    // taken in another order
+    const int x = BITS == 4 ? (D == 128 ? g * 2 : (D == 256 ? g : 0)) : g & 1;
+    uint32_t to[kUnits];
+#pragma unroll
+    for (int j = 0; j < kUnits; ++j) to[j] = slots + g * (C::kTile * 128) + t * 128 + (((u0 + (j ^ x)) ^ (t & 7)) << 4);
+    auto in_order = [x](const uint4& word, uint32_t (&v)[4]) {
+        v[0] = word.x, v[1] = word.y, v[2] = word.z, v[3] = word.w;
+        auto swap = [&v](int a, int b) {
+            const uint32_t y = v[a];
+            v[a] = v[b];
+            v[b] = y;
+        };
+        if (BITS == 4 && D == 256 && (x & 1)) swap(0, 1), swap(2, 3);
+        if (D >= 128 && (BITS == 4 ? (x & 2) != 0 : x != 0)) swap(0, 2), swap(1, 3);
+    };
+    const uint32_t from = ring + tid * 16, from_scale = ring + C::kCodes + (t * C::kBlocks + g) * 2;
+    int r = 0, s = 0;
+    uint32_t r_parity = 0, s_parity = 1;
+#pragma unroll 1
     for (int e = 0; e < 2 * w.tiles; ++e) {
-        const int r = e % C::kRing, s = e % C::kSlots;
-        if (!wait(&bars->ring_full[r], (e / C::kRing) & 1, bars, p.status)) return;
-        if (e >= C::kSlots && !wait(&bars->slot_empty[s], (e / C::kSlots - 1) & 1, bars, p.status)) return;
+        if (!wait(&bars->ring_full[r], r_parity, bars, p.status)) return;
+        if (!wait(&bars->slot_empty[s], s_parity, bars, p.status)) return;  // (a fresh barrier's phase before the first is over)
         int tile;
         const bool value = entry_of(e, w.tiles, pair, tile);
         const int t0 = (w.tile0 + tile) * C::kTile;
-        const bool edge = t0 < w.klo || t0 + C::kTile > w.khi;
-        const uint8_t* codes = ring + r * C::kEntry;
-        const __half* scales = reinterpret_cast<const __half*>(codes + C::kCodes);
-        const __half* biases = reinterpret_cast<const __half*>(codes + C::kCodes + C::kScales);
-        uint8_t* dst = slots + s * C::kSlot;
+        const uint32_t src = from + r * C::kEntry, src_scale = from_scale + r * C::kEntry, dst = s * C::kSlot;
+        uint4 word[kIts];
+        __half sc[kIts], bi[kIts];
+        // values past fp16's range, scales or biases that are no numbers, keys that no row sees: apart
+        bool odd = t0 < w.klo || t0 + C::kTile > w.khi;
 #pragma unroll
-        for (int it = 0; it < C::kTile * kChunks / kT; ++it) {
-            const int c = it * kT + tid, t = c / kChunks, ck = c % kChunks;
-            const int g = ck * kUnits / 8, u0 = ck * kUnits % 8;
-            const uint4 word = reinterpret_cast<const uint4*>(codes)[c];
-            const __half sc = scales[t * C::kBlocks + g], bi = biases[t * C::kBlocks + g];
-            // eight lanes write eight different 16-byte columns: pieces of other
-            // blocks are taken in another order
-            const int x = BITS == 4 ? (D == 128 ? g * 2 : (D == 256 ? g : 0)) : g & 1;
-            uint32_t v[4] = {word.x, word.y, word.z, word.w};
-            if (BITS == 4) {
-                if (D == 256 && (x & 1)) {
-                    uint32_t y = v[0]; v[0] = v[1]; v[1] = y;
-                    y = v[2]; v[2] = v[3]; v[3] = y;
-                }
-                if (D >= 128 && (x & 2)) {
-                    uint32_t y = v[0]; v[0] = v[2]; v[2] = y;
-                    y = v[1]; v[1] = v[3]; v[3] = y;
-                }
-            } else if (D >= 128 && x) {
-                uint32_t y = v[0]; v[0] = v[2]; v[2] = y;
-                y = v[1]; v[1] = v[3]; v[3] = y;
-            }
-            uint8_t* row = dst + g * (C::kTile * 128) + t * 128;
-            const int swz = t & 7;
-            const __half2 s2 = __half2half2(sc), b2 = __half2half2(bi);
-            // values past fp16's range, scales or biases that are no numbers, keys that no row sees: apart
-            const bool odd = !(__hfma(__habs(sc), __float2half_rn(BITS == 4 ? 15.f : 255.f), __habs(bi)) <= __float2half_rn(65504.f));
-            const bool drop = edge && (t0 + t < w.klo || t0 + t >= w.khi);
-            if (__any_sync(0xffffffffu, odd || drop)) {
-                const float fs = __half2float(sc), fb = __half2float(bi);
-                const bool none = drop || (value && !(fabsf(fs) <= 65504.f && fabsf(fb) <= 65504.f));
+        for (int it = 0; it < kIts; ++it) {
+            word[it] = lds128(src + it * kT * 16);
+            sc[it] = lds16(src_scale + it * kKeys * C::kBlocks * 2);
+            bi[it] = lds16(src_scale + C::kScales + it * kKeys * C::kBlocks * 2);
+            odd = odd || !(__hfma(__habs(sc[it]), __float2half_rn(BITS == 4 ? 15.f : 255.f), __habs(bi[it])) <= __float2half_rn(65504.f));
+        }
+        if (__any_sync(0xffffffffu, odd)) {
+#pragma unroll 1
+            for (int it = 0; it < kIts; ++it) {
+                const uint4 again = lds128(src + it * kT * 16);
+                const float fs = __half2float(lds16(src_scale + it * kKeys * C::kBlocks * 2)),
+                            fb = __half2float(lds16(src_scale + C::kScales + it * kKeys * C::kBlocks * 2));
+                const int key = t0 + t + it * kKeys;
+                const bool none = key < w.klo || key >= w.khi || (value && !(fabsf(fs) <= 65504.f && fabsf(fb) <= 65504.f));
+                uint32_t v[4];
+                in_order(again, v);
+#pragma unroll
                 for (int j = 0; j < kUnits; ++j) {
                     __half2 h[4];
                     unpack8<BITS>(v[BITS == 4 ? j : 2 * j], v[BITS == 4 ? j : 2 * j + 1], h);
@@ -285,19 +314,23 @@ __device__ __forceinline__ void unpack_role(const ChunkParams& p, const Work& w,
                         h[k] = none ? __floats2half2_rn(0.f, 0.f)
                                     : __floats2half2_rn(fminf(fmaxf(fmaf(f.x, fs, fb), -65504.f), 65504.f), fminf(fmaxf(fmaf(f.y, fs, fb), -65504.f), 65504.f));
                     }
-                    const int u = u0 + (j ^ x);
-                    *reinterpret_cast<uint4*>(row + ((u ^ swz) << 4)) = *reinterpret_cast<uint4*>(h);
+                    sts128(dst + to[j] + it * kKeys * 128, h);
                 }
-                continue;
             }
+        } else {
 #pragma unroll
-            for (int j = 0; j < kUnits; ++j) {
-                __half2 h[4];
-                unpack8<BITS>(v[BITS == 4 ? j : 2 * j], v[BITS == 4 ? j : 2 * j + 1], h);
+            for (int it = 0; it < kIts; ++it) {
+                uint32_t v[4];
+                in_order(word[it], v);
+                const __half2 s2 = __half2half2(sc[it]), b2 = __half2half2(bi[it]);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) h[k] = __hfma2(h[k], s2, b2);
-                const int u = u0 + (j ^ x);
-                *reinterpret_cast<uint4*>(row + ((u ^ swz) << 4)) = *reinterpret_cast<uint4*>(h);
+                for (int j = 0; j < kUnits; ++j) {
+                    __half2 h[4];
+                    unpack8<BITS>(v[BITS == 4 ? j : 2 * j], v[BITS == 4 ? j : 2 * j + 1], h);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) h[k] = __hfma2(h[k], s2, b2);
+                    sts128(dst + to[j] + it * kKeys * 128, h);
+                }
             }
         }
         fence_proxy_async_shared();
@@ -306,68 +339,79 @@ __device__ __forceinline__ void unpack_role(const ChunkParams& p, const Work& w,
             mbar_arrive(&bars->ring_empty[r]);
             mbar_arrive(&bars->slot_full[s]);
         }
+        if (++r == C::kRing) {
+            r = 0;
+            r_parity ^= 1;
+        }
+        if (++s == C::kSlots) {
+            s = 0;
+            s_parity ^= 1;
+        }
     }
 }
 
 // ---------------------------------------------------------------------- MMA --
+// Run by a whole warp, whose elected lane issues.  (What is between two products
+// is in the way of the next one: slots are counted, not computed.)
 template <int D, int BITS>
 __device__ __forceinline__ bool mma_loop(const ChunkParams& p, const Work& w, uint32_t q, uint32_t slots, Bars* bars, bool pair) {
     using C = Cfg<D, BITS>;
     const uint32_t tmem = bars->tmem;
-    auto slot_wait = [&](int e) { return wait(&bars->slot_full[e % C::kSlots], (e / C::kSlots) & 1, bars, p.status); };
-    auto commit = [&](uint64_t* bar) {
-        if (elect_one()) tc_commit(bar);
-        __syncwarp();
-    };
-    auto release = [&](int e) { commit(&bars->slot_empty[e % C::kSlots]); };
-    // S[buf] = Q[qt] K^T, K in the slot of entry e
-    auto qk = [&](int e, int qt, int buf) {
-        const uint64_t kd = smem_operand(slots + (e % C::kSlots) * C::kSlot, 16), qd = smem_operand(q + qt * (kRowTile * D * 2), 16);
-        if (elect_one()) {
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k)
-                tc_mma_ss(tmem + buf * C::kS, qd + (((k / 4) * (kRowTile * 128) + (k % 4) * 32) >> 4),
-                          kd + (((k / 4) * (C::kTile * 128) + (k % 4) * 32) >> 4), mma_desc(kRowTile, C::kTile, false), k > 0);
-            tc_commit(&bars->s_full[buf]);
-        }
-        __syncwarp();
-    };
-    // O[o] += P[buf] V, V in the slot of entry e
-    auto pv = [&](int e, int buf, int o, bool add) {
-        const uint64_t vd = smem_operand(slots + (e % C::kSlots) * C::kSlot, C::kTile * 128);
-        if (elect_one()) {
-#pragma unroll
-            for (int k = 0; k < C::kTile / 16; ++k)
-                tc_mma_ts(tmem + C::kO + o * D, tmem + buf * C::kS + C::kS / 2 + k * 8, vd + ((k * 2048) >> 4), mma_desc(kRowTile, D, true), add || k > 0);
-        }
-        __syncwarp();
-    };
+    const uint32_t slot_full = smem_u32(bars->slot_full), slot_empty = smem_u32(bars->slot_empty), s_full = smem_u32(bars->s_full),
+                   p_full = smem_u32(bars->p_full), o_full = smem_u32(bars->o_full);
+    const uint32_t q_op = smem_operand(q, 16), k_op = smem_operand(slots, 16), v_op = smem_operand(slots, C::kTile * 128);
     if (!wait(&bars->q_full, 0, bars, p.status)) return false;
     // Step s works on buffer s & 1: P V of its tile, then Q K^T of step s + 2 into the
     // place that P leaves.  pair: a tile of keys takes two steps, one for each row
-    // tile; else steps and tiles of keys are the same.
+    // tile; else steps and tiles of keys are the same.  Entries are used in order,
+    // each first at a step of an even buffer where two steps use it.
     const int steps = pair ? 2 * w.tiles : w.tiles;
+    uint32_t next = 0, parity = 0, v = 0, k = 0;
+    auto take = [&](uint32_t& slot) {
+        slot = next;
+        const bool ok = wait(slot_full + next * 8, parity, bars, p.status);
+        if (++next == C::kSlots) {
+            next = 0;
+            parity ^= 1;
+        }
+        return ok;
+    };
 #pragma unroll 1
     for (int s = -2; s < steps; ++s) {
-        const int buf = s & 1;
-        const bool last_user = !pair || buf == 1;
+        const uint32_t buf = s & 1;
+        const bool first_user = !pair || buf == 0, last_user = !pair || buf == 1;
+        const uint32_t sa = tmem + buf * C::kS;
         if (s >= 0) {
-            const int ve = pair ? s | 1 : value_entry(s, w.tiles, false);
-            if (!slot_wait(ve)) return false;
-            if (!wait(&bars->p_full[buf], (s >> 1) & 1, bars, p.status)) return false;
+            if (first_user && !take(v)) return false;
+            if (!wait(p_full + buf * 8, (s >> 1) & 1, bars, p.status)) return false;
             tc_fence_after();
-            const int o = C::kStreams == 2 ? buf : 0;
-            pv(ve, buf, o, C::kStreams == 2 ? s > 1 : s > 0);
-            if (last_user) release(ve);
+            const uint32_t o = C::kStreams == 2 ? buf : 0;
+            const bool add = C::kStreams == 2 ? s > 1 : s > 0;
             // (one accumulator: the softmax may have to rescale it before the next product)
-            if (C::kStreams == 1 || s + 2 >= steps) commit(&bars->o_full[o]);
+            const bool told = C::kStreams == 1 || s + 2 >= steps;
+            const uint32_t b = v_op + v * (C::kSlot >> 4), oa = tmem + C::kO + o * D;
+            if (elect_one()) {
+#pragma unroll
+                for (int i = 0; i < C::kTile / 16; ++i)
+                    tc_mma_ts(oa, sa + C::kS / 2 + i * 8, b + ((i * 2048) >> 4), mma_desc(kRowTile, D, true), i > 0 || add);
+                if (last_user) tc_commit(slot_empty + v * 8);
+                if (told) tc_commit(o_full + o * 8);
+            }
+            __syncwarp();
         }
         if (s + 2 < steps) {
-            const int ke = key_entry(pair ? (s + 2) >> 1 : s + 2, pair);
-            if (!slot_wait(ke)) return false;
+            if (first_user && !take(k)) return false;
             tc_fence_after();
-            qk(ke, pair ? buf : 0, buf);
-            if (last_user) release(ke);
+            const uint32_t a = q_op + (pair ? buf : 0) * ((kRowTile * D * 2) >> 4), b = k_op + k * (C::kSlot >> 4);
+            if (elect_one()) {
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i)
+                    tc_mma_ss(sa, a + (((i / 4) * (kRowTile * 128) + (i % 4) * 32) >> 4), b + (((i / 4) * (C::kTile * 128) + (i % 4) * 32) >> 4),
+                              mma_desc(kRowTile, C::kTile, false), i > 0);
+                tc_commit(s_full + buf * 8);
+                if (last_user) tc_commit(slot_empty + k * 8);
+            }
+            __syncwarp();
         }
     }
     return true;
@@ -752,13 +796,13 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         regs_lower<48>();
     } else if (warp < 16) {
         regs_lower<72>();
-        unpack_role<D, BITS>(p, w, ring, slots, &bars, pair);
+        unpack_role<D, BITS>(p, w, smem_u32(ring), smem_u32(slots), &bars, pair);
     } else {
         regs_lower<48>();
         if (warp == 16) {
             if (w.tiles > 0 && !mma_loop<D, BITS>(p, w, smem_u32(qs), smem_u32(slots), &bars, pair)) {
                 __syncwarp();
-                if (elect_one()) tc_commit(&bars.drain);  // given up: products in flight end before the CTA leaves
+                if (elect_one()) tc_commit(smem_u32(&bars.drain));  // given up: products in flight end before the CTA leaves
                 mbar_wait_bounded(&bars.drain, 0);
             }
         } else if (threadIdx.x == 17 * 32) {

@@ -25,14 +25,14 @@ __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// Shared-memory operand in 128-byte rows with the 128-byte swizzle, 8-row atoms
-// of 1,024 bytes that follow one another.  `lbo`: bytes between blocks of 64
-// elements along M or N of an operand stored with that dimension contiguous (not used
-// by K-contiguous ones, whose blocks of 64 along K are addressed one by one).
-__device__ __forceinline__ uint64_t smem_operand(uint32_t addr, uint32_t lbo) {
-    return static_cast<uint64_t>((addr >> 4) & 0x3fff) | static_cast<uint64_t>((lbo >> 4) & 0x3fff) << 16 | static_cast<uint64_t>(1024 >> 4) << 32 |
-           1ull << 46 | 2ull << 61;
-}
+// Descriptor of a shared-memory operand in 128-byte rows with the 128-byte swizzle,
+// 8-row atoms of 1,024 bytes that follow one another: the low word holds the address
+// (and `lbo`, the bytes between blocks of 64 elements along M or N of an operand
+// stored with that dimension contiguous; not used by K-contiguous ones, whose
+// blocks of 64 along K are addressed one by one), the high word is a constant.
+// Steps along an operand add bytes / 16 to the low word.
+__device__ __forceinline__ uint32_t smem_operand(uint32_t addr, uint32_t lbo) { return (addr >> 4) | (lbo >> 4) << 16; }
+constexpr uint32_t kOperandHigh = (1024 >> 4) | 1u << 14 | 2u << 29;
 
 // kind::f16 with fp16 A and B, fp32 D, M x N; b_mn: B is stored with N contiguous.
 __host__ __device__ constexpr uint32_t mma_desc(int m, int n, bool b_mn) {
@@ -48,24 +48,24 @@ __device__ __forceinline__ bool elect_one() {
 }
 
 // D[tmem] (+)= A[smem] B[smem], one K step of 16.
-__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t desc, bool add) {
+__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t desc, bool add) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(desc), "r"(static_cast<uint32_t>(add))
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(desc), "r"(static_cast<uint32_t>(add)), "r"(kOperandHigh)
         : "memory");
 }
 // The same with A in TMEM (two fp16 values per column, K along columns).
-__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t desc, bool add) {
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t desc, bool add) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(desc), "r"(static_cast<uint32_t>(add))
+        "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 b, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(desc), "r"(static_cast<uint32_t>(add)), "r"(kOperandHigh)
         : "memory");
 }
 // Arrives on `bar` once all tcgen05 operations this thread issued before have finished.
-__device__ __forceinline__ void tc_commit(uint64_t* bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+__device__ __forceinline__ void tc_commit(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
 
 // 32 columns of the warp's 32 TMEM lanes: thread l gets lane l's.
