@@ -391,7 +391,7 @@ __device__ __forceinline__ bool mma_loop(const ChunkParams& p, const Work& w, ui
             const bool told = C::kStreams == 1 || s + 2 >= steps;
             const uint32_t b = v_op + v * (C::kSlot >> 4), oa = tmem + C::kO + o * D;
             if (elect_one()) {
-#pragma unroll
+#pragma unroll 2
                 for (int i = 0; i < C::kTile / 16; ++i)
                     tc_mma_ts(oa, sa + C::kS / 2 + i * 8, b + ((i * 2048) >> 4), mma_desc(kRowTile, D, true), i > 0 || add);
                 if (last_user) tc_commit(slot_empty + v * 8);
@@ -404,7 +404,7 @@ __device__ __forceinline__ bool mma_loop(const ChunkParams& p, const Work& w, ui
             tc_fence_after();
             const uint32_t a = q_op + (pair ? buf : 0) * ((kRowTile * D * 2) >> 4), b = k_op + k * (C::kSlot >> 4);
             if (elect_one()) {
-#pragma unroll
+#pragma unroll 2
                 for (int i = 0; i < D / 16; ++i)
                     tc_mma_ss(sa, a + (((i / 4) * (kRowTile * 128) + (i % 4) * 32) >> 4), b + (((i / 4) * (C::kTile * 128) + (i % 4) * 32) >> 4),
                               mma_desc(kRowTile, C::kTile, false), i > 0);
@@ -461,26 +461,34 @@ __device__ __forceinline__ void store_q64(uint8_t* block, int row, const __half2
     }
 }
 
-template <int D, int BITS, bool ROT>
+// The 128 rows of a query tile from row tile_row0 of the item on, by one warpgroup
+// (thread `row`): 16 bytes a thread, rows behind the last as zeros.
+template <int D, int BITS>
 __device__ __forceinline__ void load_query(const ChunkParams& p, const Work& w, uint8_t* tile, int row, int tile_row0) {
+    constexpr int kPieces = D / 8;  // 16-byte pieces of a row: eight channels
+    const int u = row % kPieces;
+#pragma unroll 8
+    for (int it = 0; it < kPieces; ++it) {
+        const int at = it * (128 / kPieces) + row / kPieces, r = tile_row0 + at;
+        uint4 x = make_uint4(0, 0, 0, 0);
+        if (r < w.rows) {
+            const int flat = w.row0 + r, i = flat / p.group_q, g = flat - i * p.group_q;
+            x = __ldg(reinterpret_cast<const uint4*>(p.q + w.b * p.stride_b + (w.h * p.group_q + g) * p.stride_h + i * p.stride_t) + u);
+        }
+        if (p.negate_q) x.x ^= 0x80008000u, x.y ^= 0x80008000u, x.z ^= 0x80008000u, x.w ^= 0x80008000u;
+        if (BITS == 4)
+            x = make_uint4(__byte_perm(x.x, x.z, 0x5410), __byte_perm(x.x, x.z, 0x7632), __byte_perm(x.y, x.w, 0x5410), __byte_perm(x.y, x.w, 0x7632));
+        *reinterpret_cast<uint4*>(tile + (u / 8) * (kRowTile * 128) + at * 128 + (((u % 8) ^ (at & 7)) << 4)) = x;
+    }
+}
+
+// The same for a cache of rotated keys: a thread a row.
+template <int D, int BITS>
+__device__ __forceinline__ void load_query_rotated(const ChunkParams& p, const Work& w, uint8_t* tile, int row, int tile_row0) {
     const int r = tile_row0 + row;
     const bool valid = r < w.rows;
     const int flat = w.row0 + (valid ? r : 0), i = flat / p.group_q, g = flat - i * p.group_q;
     const uint4* src = reinterpret_cast<const uint4*>(p.q + w.b * p.stride_b + (w.h * p.group_q + g) * p.stride_h + i * p.stride_t);
-    if (!ROT || !p.rotate_q) {
-#pragma unroll
-        for (int blk = 0; blk < D / 64; ++blk) {
-            __half2 x[32];
-#pragma unroll
-            for (int u = 0; u < 8; ++u) reinterpret_cast<uint4*>(x)[u] = valid ? __ldg(src + blk * 8 + u) : make_uint4(0, 0, 0, 0);
-            if (p.negate_q) {
-#pragma unroll
-                for (int k = 0; k < 32; ++k) x[k] = __hneg2(x[k]);
-            }
-            store_q64<BITS>(tile + blk * (kRowTile * 128), row, x);
-        }
-        return;
-    }
     constexpr int N = D < 128 ? D : 128;
     for (int half = 0; half < D / N; ++half) {
         float v[N];
@@ -530,29 +538,40 @@ __device__ __forceinline__ bool softmax_loop(const ChunkParams& p, const Work& w
         if (active) {
             const uint32_t sa = tmem + buf * C::kS;
             const int t0 = (w.tile0 + j) * C::kTile;
-            // 64 columns at a time: the first half (of two) is read twice, so that
-            // a row's scores need not fit in registers; P goes where the second
-            // half's scores were
-            constexpr int H = N / 64;
-            const bool mask = __any_sync(0xffffffffu, t0 < lo || t0 + N > hi);
-            const unsigned span = static_cast<unsigned>(hi > lo ? hi - lo : 0);
-            float s[64];
-            auto load = [&](int half) {
-                tmem_ld64(sa + half * 64, s);
-                tmem_wait_ld();
-                if (mask) {
-                    const int at = t0 + half * 64 - lo;
+            if (__any_sync(0xffffffffu, t0 < lo || t0 + N > hi)) {
+                // scores of keys that the row does not see: minus infinity, once and for both passes
+                const unsigned span = static_cast<unsigned>(hi > lo ? hi - lo : 0);
+#pragma unroll 1
+                for (int x = 0; x < N; x += 32) {
+                    float s[32];
+                    tmem_ld32(sa + x, s);
+                    tmem_wait_ld();
 #pragma unroll
-                    for (int x = 0; x < 64; ++x) s[x] = static_cast<unsigned>(at + x) < span ? s[x] : -INFINITY;
+                    for (int y = 0; y < 32; ++y) s[y] = static_cast<unsigned>(t0 + x + y - lo) < span ? s[y] : -INFINITY;
+                    tmem_st32(sa + x, s);
                 }
-            };
-            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-            for (int half = 0; half < H; ++half) {
-                load(half);
-#pragma unroll
-                for (int x = 0; x < 64; x += 2) mx[(x >> 1) & 3] = max3(mx[(x >> 1) & 3], s[x], s[x + 1]);
+                tmem_wait_st();
             }
+            // Two passes over the scores in TMEM, 32 columns at a time with the next 32 on
+            // their way, in loops (unrolled, the code of the roles that share an
+            // instruction cache did not fit it: products were issued at half the rate).
+            float u[32], v[32];
+            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            auto highest = [&mx](const float (&s)[32]) {
+#pragma unroll
+                for (int x = 0; x < 32; x += 2) mx[(x >> 1) & 3] = max3(mx[(x >> 1) & 3], s[x], s[x + 1]);
+            };
+            tmem_ld32(sa, u);
+#pragma unroll 1
+            for (int x = 0; x < N; x += 64) {
+                tmem_wait_ld();
+                tmem_ld32(sa + x + 32, v);
+                highest(u);
+                tmem_wait_ld();
+                tmem_ld32(sa + (x + 64) % N, u);
+                highest(v);
+            }
+            tmem_wait_ld();
             const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * c;
             const bool grow = k == 0 ? top > st.m : top > st.m + kLazy;
             if (__any_sync(0xffffffffu, grow)) {
@@ -567,6 +586,7 @@ __device__ __forceinline__ bool softmax_loop(const ChunkParams& p, const Work& w
                         tc_fence_after();
                     }
                     const uint32_t oa = tmem + C::kO + (C::kStreams == 2 ? stream * D : 0);
+#pragma unroll 1
                     for (int x = 0; x < D; x += 32) {
                         float o[32];
                         tmem_ld32(oa + x, o);
@@ -579,22 +599,28 @@ __device__ __forceinline__ bool softmax_loop(const ChunkParams& p, const Work& w
             }
             const float base = st.m == -INFINITY ? 0.f : -st.m;
             float2 sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
+            // from the last column down: P's columns are those of scores already read
+            auto weights = [&](const float (&s)[32], int x) {
+                uint32_t pk[16];
 #pragma unroll
-            for (int half = H - 1; half >= 0; --half) {
-                if (half < H - 1) load(half);
-#pragma unroll
-                for (int x = 0; x < 64; x += 32) {
-                    uint32_t pk[16];
-#pragma unroll
-                    for (int y = 0; y < 16; ++y) {
-                        float2 e = fma2(make_float2(s[x + 2 * y], s[x + 2 * y + 1]), make_float2(c, c), make_float2(base, base));
-                        e.x = ex2_approx(e.x);
-                        e.y = ex2_approx(e.y);
-                        sum[y & 1] = add2(sum[y & 1], e);
-                        pk[y] = pack_half2(e.x, e.y);
-                    }
-                    tmem_st16(sa + C::kS / 2 + half * 32 + x / 2, pk);
+                for (int y = 0; y < 16; ++y) {
+                    float2 e = fma2(make_float2(s[2 * y], s[2 * y + 1]), make_float2(c, c), make_float2(base, base));
+                    e.x = ex2_approx(e.x);
+                    e.y = ex2_approx(e.y);
+                    sum[y & 1] = add2(sum[y & 1], e);
+                    pk[y] = pack_half2(e.x, e.y);
                 }
+                tmem_st16(sa + C::kS / 2 + x / 2, pk);
+            };
+            tmem_ld32(sa + N - 32, u);
+#pragma unroll 1
+            for (int x = N - 32; x > 0; x -= 64) {
+                tmem_wait_ld();
+                tmem_ld32(sa + x - 32, v);
+                weights(u, x);
+                tmem_wait_ld();
+                if (x > 64) tmem_ld32(sa + x - 64, u);
+                weights(v, x - 32);
             }
             sum[0] = add2(sum[0], sum[1]);
             st.l += sum[0].x + sum[0].y;
@@ -632,6 +658,7 @@ __device__ __forceinline__ void write_row(const ChunkParams& p, const Work& w, u
             p.part_m[at] = st.m;
             p.part_l[at] = st.l;
         }
+#pragma unroll 1
         for (int x = 0; x < D; x += 32) {
             float v[32];
             columns(x, v);
@@ -645,6 +672,7 @@ __device__ __forceinline__ void write_row(const ChunkParams& p, const Work& w, u
     }
     uint16_t* out = p.out + ((static_cast<long long>(w.b) * p.n + i) * p.num_q_heads + w.h * p.group_q + g) * D;
     if (!ROT || !p.rotate_out) {
+#pragma unroll 1
         for (int x = 0; x < D; x += 32) {
             float v[32];
             columns(x, v);
@@ -695,7 +723,13 @@ __device__ __forceinline__ void softmax_role(const ChunkParams& p, const Work& w
     const int r = tile_row0 + row;  // row of the item
     const bool valid = r < w.rows;
     const bool active = __any_sync(0xffffffffu, valid);
-    if (pair || stream == 0) load_query<D, BITS, ROT>(p, w, qs + (pair ? stream : 0) * (kRowTile * D * 2), row, tile_row0);
+    if (pair || stream == 0) {
+        uint8_t* tile = qs + (pair ? stream : 0) * (kRowTile * D * 2);
+        if (ROT && p.rotate_q)
+            load_query_rotated<D, BITS>(p, w, tile, row, tile_row0);
+        else
+            load_query<D, BITS>(p, w, tile, row, tile_row0);
+    }
     fence_proxy_async_shared();
     __syncwarp();
     if (lane == 0) mbar_arrive(&bars->q_full);
@@ -720,6 +754,7 @@ __device__ __forceinline__ void softmax_role(const ChunkParams& p, const Work& w
         float* buf = reinterpret_cast<float*>(slots);  // [D][128], then m and l
         asm volatile("bar.sync 1, 256;" ::: "memory");
         if (stream == 1 && ok && active) {
+#pragma unroll 1
             for (int x = 0; x < D && mine > 0; x += 32) {
                 float o[32];
                 tmem_ld32(oa + x, o);
