@@ -14,7 +14,7 @@
 //   unpacking warps   turn them into fp16 operands in shared memory, laid out as
 //                     128-byte rows with the 128-byte swizzle: keys are then a
 //                     K-major operand and values an N-major one, in the same layout
-//   one MMA thread    S = Q K^T and O += P V, S, P and O in TMEM (P in S's place)
+//   MMA warps         S = Q K^T and O += P V, S, P and O in TMEM (P in S's place)
 //   softmax warps     a thread a row: maximum, 2^x, P as fp16, sum; no shuffles
 // The two row tiles take turns: while one's softmax runs the tensor core works for
 // the other.  Up to 128 rows (a few tokens) make one tile; the two halves then take
@@ -24,6 +24,8 @@
 // rare after the first tiles.
 // Where rows are few the keys are split over CTAs and the partial states
 // merged by a second kernel.
+#include <stddef.h>
+
 #include "tq_device.cuh"
 #include "tq_hadamard.cuh"
 #include "tq_internal.h"
@@ -33,7 +35,7 @@ namespace tq {
 
 namespace {
 
-constexpr int kThreads = 640;       // 8 softmax warps, 8 that unpack, 4 of which one issues products and one copies
+constexpr int kThreads = 640;       // 8 softmax warps, 8 that unpack, 2 that issue products, one that copies
 constexpr int kRowTile = 128;
 constexpr float kLazy = 8.f;  // log2 of how far P may grow before O is rescaled
 
@@ -60,10 +62,41 @@ struct Cfg {
 
 struct Bars {
     uint64_t ring_full[6], ring_empty[6], slot_full[6], slot_empty[6];
-    uint64_t s_full[2], p_full[2], o_full[2], q_full, drain;
+    uint64_t s_full[2], p_full[2], o_full[2], q_full, drain[2], half;
     uint32_t tmem;
     int32_t abort;
 };
+
+// Addresses of the barriers from that of the first.  (Each role takes the first one's
+// once, in a way that the compiler cannot repeat: left to it, it forms a shared
+// variable's address anew wherever it is used, from a special register that takes
+// tens of cycles to read, which between two products is time lost.)
+enum : uint32_t {
+    kRingFull = 0,
+    kRingEmpty = 6 * 8,
+    kSlotFull = 12 * 8,
+    kSlotEmpty = 18 * 8,
+    kSFull = 24 * 8,
+    kPFull = 26 * 8,
+    kOFull = 28 * 8,
+    kQFull = 30 * 8,
+    kDrain = 31 * 8,
+    kHalf = 33 * 8,
+    kTmemAt = 34 * 8,
+    kAbort = 34 * 8 + 4,
+};
+__device__ __forceinline__ uint32_t fixed(uint32_t x) {
+    asm volatile("" : "+r"(x));
+    return x;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t at) {
+    uint32_t v;
+    asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+    return v;
+}
+__device__ __forceinline__ void arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
 
 // What a CTA works on.
 struct Work {
@@ -138,6 +171,10 @@ __device__ __forceinline__ bool entry_of(int e, int tiles, bool pair, int& tile)
     tile = (e >> 1) - 1;
     return true;
 }
+__device__ __forceinline__ int key_entry(int tile, bool pair) { return pair ? 2 * tile : (tile == 0 ? 0 : 2 * tile - 1); }
+__device__ __forceinline__ int value_entry(int tile, int tiles, bool pair) {
+    return pair ? 2 * tile + 1 : (tile == tiles - 1 ? 2 * tiles - 1 : 2 * tile + 2);
+}
 
 // Whether a phase is over; the hardware holds the warp for a while if it is not.
 // (With a time limit of its own, as mbar_try_wait asks for, the wait becomes a loop that
@@ -152,15 +189,20 @@ __device__ __forceinline__ bool over(uint32_t bar, uint32_t parity) {
     return ok != 0;
 }
 
-// The rest of a wait that did not end at once; false when it took too long or another warp has given up.
-__device__ __forceinline__ bool wait_on(uint32_t bar, uint32_t parity, Bars* bars, int32_t* status) {
-    const uint64_t t0 = globaltimer_ns();
+// Waits for a phase of the barrier at `bar`; false when it took too long or another
+// warp has given up.  (The timer is read rarely: that takes longer than most waits.)
+__device__ __forceinline__ bool wait(uint32_t bars, uint32_t bar, uint32_t parity, int32_t* status) {
+    if (over(bars + bar, parity)) return true;
+    uint64_t t0 = 0;
+#pragma unroll 1
     for (uint32_t it = 1;; ++it) {
-        if (over(bar, parity)) return true;
-        if ((it & 15u) == 0) {
-            if (*reinterpret_cast<volatile int32_t*>(&bars->abort) != 0) return false;
-            if (globaltimer_ns() - t0 > 2000000000ull) {
-                *reinterpret_cast<volatile int32_t*>(&bars->abort) = 1;
+        if (over(bars + bar, parity)) return true;
+        if ((it & 63u) == 0) {
+            if (lds32(bars + kAbort) != 0) return false;
+            const uint64_t now = (it & 1023u) == 0 ? globaltimer_ns() : 0;
+            if (now != 0 && t0 == 0) t0 = now;
+            if (now != 0 && now - t0 > 2000000000ull) {
+                asm volatile("st.volatile.shared.u32 [%0], 1;" ::"r"(bars + kAbort) : "memory");
                 if (status != nullptr) atomicOr(status, TQ_DEV_TIMEOUT);
                 return false;
             }
@@ -168,33 +210,28 @@ __device__ __forceinline__ bool wait_on(uint32_t bar, uint32_t parity, Bars* bar
     }
 }
 
-__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, Bars* bars, int32_t* status) {
-    return over(bar, parity) || wait_on(bar, parity, bars, status);
-}
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, Bars* bars, int32_t* status) {
-    return wait(smem_u32(bar), parity, bars, status);
-}
-
 // ------------------------------------------------------------------ loader --
 template <int D, int BITS>
 __device__ __forceinline__ void load_role(const ChunkParams& p, const Work& w, uint8_t* ring, Bars* bars, bool pair) {
     using C = Cfg<D, BITS>;
     const uint64_t policy = policy_evict_first();
+    const uint32_t at = fixed(smem_u32(bars));
     int e = 0;
+#pragma unroll 1
     for (; e < 2 * w.tiles; ++e) {
         const int r = e % C::kRing, n = e / C::kRing;
-        if (n > 0 && !wait(&bars->ring_empty[r], (n - 1) & 1, bars, p.status)) break;
+        if (n > 0 && !wait(at, kRingEmpty + r * 8, (n - 1) & 1, p.status)) break;
         int tile;
         const bool value = entry_of(e, w.tiles, pair, tile);
         const int t0 = (w.tile0 + tile) * C::kTile;
         const int rows = min(C::kTile, (w.khi - t0 + 15) & ~15);  // capacities are whole 16s
-        const long long at = kv_row(p.map, p.num_kv_heads, w.b, w.h, t0, p.status);
+        const long long row = kv_row(p.map, p.num_kv_heads, w.b, w.h, t0, p.status);
         uint8_t* dst = ring + r * C::kEntry;
         const uint32_t cb = rows * (D * BITS / 8), sb = rows * (C::kBlocks * 2);
         mbar_arrive_expect_tx(&bars->ring_full[r], cb + 2 * sb);
-        bulk_load(dst, (value ? p.v_codes : p.k_codes) + at * (D * BITS / 8), cb, &bars->ring_full[r], policy);
-        bulk_load(dst + C::kCodes, (value ? p.v_scale : p.k_scale) + at * C::kBlocks, sb, &bars->ring_full[r], policy);
-        bulk_load(dst + C::kCodes + C::kScales, (value ? p.v_bias : p.k_bias) + at * C::kBlocks, sb, &bars->ring_full[r], policy);
+        bulk_load(dst, (value ? p.v_codes : p.k_codes) + row * (D * BITS / 8), cb, &bars->ring_full[r], policy);
+        bulk_load(dst + C::kCodes, (value ? p.v_scale : p.k_scale) + row * C::kBlocks, sb, &bars->ring_full[r], policy);
+        bulk_load(dst + C::kCodes + C::kScales, (value ? p.v_bias : p.k_bias) + row * C::kBlocks, sb, &bars->ring_full[r], policy);
     }
     if (e < 2 * w.tiles)  // given up: the copies in flight land before the CTA leaves
         for (int k = max(0, e - C::kRing); k < e; ++k) mbar_wait_bounded(&bars->ring_full[k % C::kRing], (k / C::kRing) & 1);
@@ -246,7 +283,7 @@ __device__ __forceinline__ void sts128(uint32_t at, const __half2 (&h)[4]) {
 // A thread takes the same 16-byte piece of every 2^n-th key's codes: where its
 // outputs go, and in which order, is the same for all of them.
 template <int D, int BITS>
-__device__ __forceinline__ void unpack_role(const ChunkParams& p, const Work& w, uint32_t ring, uint32_t slots, Bars* bars, bool pair) {
+__device__ __forceinline__ void unpack_role(const ChunkParams& p, const Work& w, uint32_t ring, uint32_t slots, uint32_t bars, bool pair) {
     using C = Cfg<D, BITS>;
     constexpr int kUnits = BITS == 4 ? 4 : 2;             // 16-byte pieces of fp16 that 16 bytes of codes give
     constexpr int kChunks = D * BITS / 8 / 16;            // 16-byte pieces of codes per key
@@ -277,8 +314,8 @@ __device__ __forceinline__ void unpack_role(const ChunkParams& p, const Work& w,
     uint32_t r_parity = 0, s_parity = 1;
 #pragma unroll 1
     for (int e = 0; e < 2 * w.tiles; ++e) {
-        if (!wait(&bars->ring_full[r], r_parity, bars, p.status)) return;
-        if (!wait(&bars->slot_empty[s], s_parity, bars, p.status)) return;  // (a fresh barrier's phase before the first is over)
+        if (!wait(bars, kRingFull + r * 8, r_parity, p.status)) return;
+        if (!wait(bars, kSlotEmpty + s * 8, s_parity, p.status)) return;  // (a fresh barrier's phase before the first is over)
         int tile;
         const bool value = entry_of(e, w.tiles, pair, tile);
         const int t0 = (w.tile0 + tile) * C::kTile;
@@ -336,8 +373,8 @@ __device__ __forceinline__ void unpack_role(const ChunkParams& p, const Work& w,
         fence_proxy_async_shared();
         __syncwarp();
         if (lane == 0) {
-            mbar_arrive(&bars->ring_empty[r]);
-            mbar_arrive(&bars->slot_full[s]);
+            arrive(bars + kRingEmpty + r * 8);
+            arrive(bars + kSlotFull + s * 8);
         }
         if (++r == C::kRing) {
             r = 0;
@@ -351,67 +388,110 @@ __device__ __forceinline__ void unpack_role(const ChunkParams& p, const Work& w,
 }
 
 // ---------------------------------------------------------------------- MMA --
-// Run by a whole warp, whose elected lane issues.  (What is between two products
-// is in the way of the next one: slots are counted, not computed.)
+// Run by whole warps, an elected lane of which issues.  The tensor core takes in few
+// products ahead, so what is between two of them (waits of 70 cycles even when there
+// is nothing to wait for, commits of 50) is time that it stands still: with two
+// accumulators a warp for each issues, one's products filling the other's gaps.
 template <int D, int BITS>
-__device__ __forceinline__ bool mma_loop(const ChunkParams& p, const Work& w, uint32_t q, uint32_t slots, Bars* bars, bool pair) {
+struct Products {
     using C = Cfg<D, BITS>;
-    const uint32_t tmem = bars->tmem;
-    const uint32_t slot_full = smem_u32(bars->slot_full), slot_empty = smem_u32(bars->slot_empty), s_full = smem_u32(bars->s_full),
-                   p_full = smem_u32(bars->p_full), o_full = smem_u32(bars->o_full);
-    const uint32_t q_op = smem_operand(q, 16), k_op = smem_operand(slots, 16), v_op = smem_operand(slots, C::kTile * 128);
-    if (!wait(&bars->q_full, 0, bars, p.status)) return false;
-    // Step s works on buffer s & 1: P V of its tile, then Q K^T of step s + 2 into the
-    // place that P leaves.  pair: a tile of keys takes two steps, one for each row
-    // tile; else steps and tiles of keys are the same.  Entries are used in order,
-    // each first at a step of an even buffer where two steps use it.
-    const int steps = pair ? 2 * w.tiles : w.tiles;
-    uint32_t next = 0, parity = 0, v = 0, k = 0;
-    auto take = [&](uint32_t& slot) {
-        slot = next;
-        const bool ok = wait(slot_full + next * 8, parity, bars, p.status);
-        if (++next == C::kSlots) {
-            next = 0;
-            parity ^= 1;
-        }
-        return ok;
-    };
+    uint32_t bars, tmem, q_op, k_op, v_op;
+    int32_t* status;
+    // the slot that an entry is in: entries are visited in order, some left out
+    int entry;
+    uint32_t slot, parity;
+    __device__ __forceinline__ bool ready(int e) {
 #pragma unroll 1
-    for (int s = -2; s < steps; ++s) {
-        const uint32_t buf = s & 1;
-        const bool first_user = !pair || buf == 0, last_user = !pair || buf == 1;
-        const uint32_t sa = tmem + buf * C::kS;
-        if (s >= 0) {
-            if (first_user && !take(v)) return false;
-            if (!wait(p_full + buf * 8, (s >> 1) & 1, bars, p.status)) return false;
-            tc_fence_after();
-            const uint32_t o = C::kStreams == 2 ? buf : 0;
-            const bool add = C::kStreams == 2 ? s > 1 : s > 0;
-            // (one accumulator: the softmax may have to rescale it before the next product)
-            const bool told = C::kStreams == 1 || s + 2 >= steps;
-            const uint32_t b = v_op + v * (C::kSlot >> 4), oa = tmem + C::kO + o * D;
-            if (elect_one()) {
-#pragma unroll 2
-                for (int i = 0; i < C::kTile / 16; ++i)
-                    tc_mma_ts(oa, sa + C::kS / 2 + i * 8, b + ((i * 2048) >> 4), mma_desc(kRowTile, D, true), i > 0 || add);
-                if (last_user) tc_commit(slot_empty + v * 8);
-                if (told) tc_commit(o_full + o * 8);
+        for (; entry < e; ++entry)
+            if (++slot == C::kSlots) {
+                slot = 0;
+                parity ^= 1;
             }
-            __syncwarp();
+        const bool ok = wait(bars, kSlotFull + slot * 8, parity, status);
+        tc_fence_after();
+        return ok;
+    }
+    // S[buf] = Q[qt] K^T, the keys in the current slot
+    __device__ __forceinline__ void scores(uint32_t qt, uint32_t buf) const {
+        uint32_t a = q_op + qt * ((kRowTile * D * 2) >> 4), b = k_op + slot * (C::kSlot >> 4);
+        const uint32_t s = tmem + buf * C::kS;
+        if (elect_one()) {
+#pragma unroll 1
+            for (int i = 0; i < D / 64; ++i) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) tc_mma_ss(s, a + k * 2, b + k * 2, mma_desc(kRowTile, C::kTile, false), k > 0 || i > 0);
+                a += (kRowTile * 128) >> 4;
+                b += (C::kTile * 128) >> 4;
+            }
+            tc_commit(bars + kSFull + buf * 8);
+            tc_commit(bars + kSlotEmpty + slot * 8);
         }
-        if (s + 2 < steps) {
-            if (first_user && !take(k)) return false;
-            tc_fence_after();
-            const uint32_t a = q_op + (pair ? buf : 0) * ((kRowTile * D * 2) >> 4), b = k_op + k * (C::kSlot >> 4);
-            if (elect_one()) {
-#pragma unroll 2
-                for (int i = 0; i < D / 16; ++i)
-                    tc_mma_ss(sa, a + (((i / 4) * (kRowTile * 128) + (i % 4) * 32) >> 4), b + (((i / 4) * (C::kTile * 128) + (i % 4) * 32) >> 4),
-                              mma_desc(kRowTile, C::kTile, false), i > 0);
-                tc_commit(s_full + buf * 8);
-                if (last_user) tc_commit(slot_empty + k * 8);
+        __syncwarp();
+    }
+    // O[o] (+)= P[buf] V, the values in the current slot
+    __device__ __forceinline__ void outputs(uint32_t buf, uint32_t o, bool add, bool told) const {
+        uint32_t b = v_op + slot * (C::kSlot >> 4), s = tmem + buf * C::kS + C::kS / 2;
+        const uint32_t d = tmem + C::kO + o * D;
+        if (elect_one()) {
+#pragma unroll 1
+            for (int i = 0; i < C::kTile / 64; ++i) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) tc_mma_ts(d, s + k * 8, b + ((k * 2048) >> 4), mma_desc(kRowTile, D, true), k > 0 || i > 0 || add);
+                s += 32;
+                b += (4 * 2048) >> 4;
             }
-            __syncwarp();
+            tc_commit(bars + kSlotEmpty + slot * 8);
+            if (told) tc_commit(bars + kOFull + o * 8);
+        }
+        __syncwarp();
+    }
+};
+
+// The tiles of one accumulator: all (pair) or every other one.
+template <int D, int BITS>
+__device__ __forceinline__ bool mma_loop(const ChunkParams& p, const Work& w, uint32_t q, uint32_t slots, uint32_t bars, bool pair, uint32_t stream) {
+    using C = Cfg<D, BITS>;
+    Products<D, BITS> x{bars, fixed(lds32(bars + kTmemAt)), fixed(smem_operand(q, 16)), fixed(smem_operand(slots, 16)), fixed(smem_operand(slots, C::kTile * 128)),
+                        p.status, 0, 0, 0};
+    if (!wait(bars, kQFull, 0, p.status)) return false;
+    const int T = w.tiles;
+    if (C::kStreams == 2) {
+        const int step = pair ? 1 : 2;
+        const uint32_t qt = pair ? stream : 0;
+        int j = pair ? 0 : stream;
+        if (j >= T) return true;
+        // the second row tile half a turn behind the first: in step, both would wait for
+        // their softmax at the same time
+        if (pair && stream == 1 && !wait(bars, kHalf, 0, p.status)) return false;
+        if (!x.ready(key_entry(j, pair))) return false;
+        tc_fence_after();
+        x.scores(qt, stream);
+#pragma unroll 1
+        for (uint32_t k = 0; j < T; ++k, j += step) {
+            if (!x.ready(value_entry(j, T, pair)) || !wait(bars, kPFull + stream * 8, k & 1, p.status)) return false;
+            tc_fence_after();
+            x.outputs(stream, stream, k > 0, j + step >= T);
+            if (j + step < T) {
+                if (!x.ready(key_entry(j + step, pair))) return false;
+                x.scores(qt, stream);
+            }
+        }
+        return true;
+    }
+    // one accumulator, two places for scores
+    for (int j = 0; j < 2 && j < T; ++j) {
+        if (!x.ready(key_entry(j, false))) return false;
+        tc_fence_after();
+        x.scores(0, j);
+    }
+#pragma unroll 1
+    for (int j = 0; j < T; ++j) {
+        if (!x.ready(value_entry(j, T, false)) || !wait(bars, kPFull + (j & 1) * 8, (j >> 1) & 1, p.status)) return false;
+        tc_fence_after();
+        x.outputs(j & 1, 0, j > 0, true);  // (told of every one: the softmax may have to rescale the sums before the next)
+        if (j + 2 < T) {
+            if (!x.ready(key_entry(j + 2, false))) return false;
+            x.scores(0, j & 1);
         }
     }
     return true;
@@ -522,18 +602,18 @@ struct State {
 
 // One warpgroup's tiles: j = first, first + step, ...
 template <int D, int BITS>
-__device__ __forceinline__ bool softmax_loop(const ChunkParams& p, const Work& w, Bars* bars, int stream, bool pair, bool active, int lo, int hi, State& st) {
+__device__ __forceinline__ bool softmax_loop(const ChunkParams& p, const Work& w, uint32_t bars, uint32_t tmem0, int stream, bool pair, bool active, int lo, int hi, State& st) {
     using C = Cfg<D, BITS>;
     constexpr int N = C::kTile;
     const int lane = threadIdx.x & 31;
     const uint32_t lanes = static_cast<uint32_t>((threadIdx.x >> 5) & 3) << 21;
-    const uint32_t tmem = bars->tmem + lanes;
+    const uint32_t tmem = tmem0 + lanes;
     const float c = p.score_scale_log2;
     const int step = pair || C::kStreams == 1 ? 1 : 2;
     for (int j = step == 2 ? stream : 0, k = 0; j < w.tiles; j += step, ++k) {
         const int buf = pair || C::kStreams == 2 ? stream : j & 1;
         const uint32_t phase = C::kStreams == 1 ? (j >> 1) & 1 : k & 1;
-        if (!wait(&bars->s_full[buf], phase, bars, p.status)) return false;
+        if (!wait(bars, kSFull + buf * 8, phase, p.status)) return false;
         tc_fence_after();
         if (active) {
             const uint32_t sa = tmem + buf * C::kS;
@@ -582,7 +662,7 @@ __device__ __forceinline__ bool softmax_loop(const ChunkParams& p, const Work& w
                     // O holds the products up to the tile before; with one accumulator the
                     // last of them may still run (with two, this S came after it)
                     if (C::kStreams == 1) {
-                        if (!wait(&bars->o_full[0], (j - 1) & 1, bars, p.status)) return false;
+                        if (!wait(bars, kOFull, (j - 1) & 1, p.status)) return false;
                         tc_fence_after();
                     }
                     const uint32_t oa = tmem + C::kO + (C::kStreams == 2 ? stream * D : 0);
@@ -628,7 +708,10 @@ __device__ __forceinline__ bool softmax_loop(const ChunkParams& p, const Work& w
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->p_full[buf]);
+        if (lane == 0) {
+            arrive(bars + kPFull + buf * 8);
+            if (C::kStreams == 2 && stream == 0 && k == 0) arrive(bars + kHalf);
+        }
     }
     return true;
 }
@@ -716,7 +799,7 @@ __device__ __forceinline__ void write_row(const ChunkParams& p, const Work& w, u
 }
 
 template <int D, int BITS, bool ROT>
-__device__ __forceinline__ void softmax_role(const ChunkParams& p, const Work& w, uint8_t* qs, uint8_t* slots, Bars* bars, int stream, bool pair) {
+__device__ __forceinline__ void softmax_role(const ChunkParams& p, const Work& w, uint8_t* qs, uint8_t* slots, uint32_t bars, int stream, bool pair) {
     using C = Cfg<D, BITS>;
     const int row = threadIdx.x & 127, lane = threadIdx.x & 31;
     const int tile_row0 = pair ? stream * kRowTile : 0;
@@ -732,23 +815,24 @@ __device__ __forceinline__ void softmax_role(const ChunkParams& p, const Work& w
     }
     fence_proxy_async_shared();
     __syncwarp();
-    if (lane == 0) mbar_arrive(&bars->q_full);
+    if (lane == 0) arrive(bars + kQFull);
     const int i = (w.row0 + (valid ? r : 0)) / p.group_q;
     // (rows behind the last are zeros that see everything: they ask for no masks)
     const int lo = valid ? first_key(p, i, w.ql, w.len) : 0, hi = valid ? end_key(p, i, w.ql, w.len) : 0x7fffffff;
+    const uint32_t tmem = fixed(lds32(bars + kTmemAt));
     State st{-INFINITY, 0.f};
-    const bool done = softmax_loop<D, BITS>(p, w, bars, stream, pair, active, lo, hi, st);
+    const bool done = softmax_loop<D, BITS>(p, w, bars, tmem, stream, pair, active, lo, hi, st);
     const bool split_keys = !pair && C::kStreams == 2;
     // tiles of this stream, and the phase of its accumulator's last barrier
     const int mine = split_keys ? (w.tiles + 1 - stream) / 2 : w.tiles;
     bool ok = done;
     if (ok && mine > 0) {
         // (one accumulator: a phase a tile, of which the last score tile shows all but the last two to be over)
-        if (C::kStreams == 1 && mine > 1) ok = wait(&bars->o_full[0], (mine - 2) & 1, bars, p.status);
-        ok = ok && wait(&bars->o_full[C::kStreams == 2 ? stream : 0], C::kStreams == 1 ? (mine - 1) & 1 : 0, bars, p.status);
+        if (C::kStreams == 1 && mine > 1) ok = wait(bars, kOFull, (mine - 2) & 1, p.status);
+        ok = ok && wait(bars, kOFull + (C::kStreams == 2 ? stream : 0) * 8, C::kStreams == 1 ? (mine - 1) & 1 : 0, p.status);
         tc_fence_after();
     }
-    const uint32_t oa = bars->tmem + (static_cast<uint32_t>((threadIdx.x >> 5) & 3) << 21) + C::kO + (C::kStreams == 2 ? stream * D : 0);
+    const uint32_t oa = tmem + (static_cast<uint32_t>((threadIdx.x >> 5) & 3) << 21) + C::kO + (C::kStreams == 2 ? stream * D : 0);
     if (split_keys) {
         // the second half's state through shared memory (the operands' place: no product is left that reads them)
         float* buf = reinterpret_cast<float*>(slots);  // [D][128], then m and l
@@ -792,6 +876,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     using C = Cfg<D, BITS>;
     extern __shared__ uint8_t raw[];
     __shared__ Bars bars;
+    static_assert(offsetof(Bars, slot_empty) == kSlotEmpty && offsetof(Bars, q_full) == kQFull && offsetof(Bars, abort) == kAbort, "addresses");
     uint8_t* base = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);  // (an offset, so that it stays a shared-memory pointer)
     uint8_t* qs = base;
     uint8_t* slots = base + C::kQ;
@@ -807,15 +892,16 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             mbar_init(&bars.ring_full[i], 1);
             mbar_init(&bars.ring_empty[i], C::kUnpackWarps);
             mbar_init(&bars.slot_full[i], C::kUnpackWarps);
-            mbar_init(&bars.slot_empty[i], 1);
+            mbar_init(&bars.slot_empty[i], pair ? 2 : 1);  // the products that use it
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bars.s_full[i], 1);
             mbar_init(&bars.p_full[i], 4);
             mbar_init(&bars.o_full[i], 1);
+            mbar_init(&bars.drain[i], 1);
         }
         mbar_init(&bars.q_full, C::kStreams * 4);
-        mbar_init(&bars.drain, 1);
+        mbar_init(&bars.half, 4);
         bars.abort = 0;
         fence_mbarrier_init();
     }
@@ -826,19 +912,20 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     // accumulator: 128 x 200 + 128 x 48 + 256 x 72 + 128 x 48)
     if (warp < C::kStreams * 4) {
         regs_raise<C::kStreams == 2 ? 144 : 200>();
-        softmax_role<D, BITS, ROT>(p, w, qs, slots, &bars, warp >> 2, pair);
+        softmax_role<D, BITS, ROT>(p, w, qs, slots, fixed(smem_u32(&bars)), warp >> 2, pair);
     } else if (warp < 8) {
         regs_lower<48>();
     } else if (warp < 16) {
         regs_lower<72>();
-        unpack_role<D, BITS>(p, w, smem_u32(ring), smem_u32(slots), &bars, pair);
+        unpack_role<D, BITS>(p, w, fixed(smem_u32(ring)), fixed(smem_u32(slots)), fixed(smem_u32(&bars)), pair);
     } else {
         regs_lower<48>();
-        if (warp == 16) {
-            if (w.tiles > 0 && !mma_loop<D, BITS>(p, w, smem_u32(qs), smem_u32(slots), &bars, pair)) {
+        if (warp == 16 || (C::kStreams == 2 && warp == 18)) {
+            const uint32_t stream = warp == 18 ? 1 : 0;
+            if (w.tiles > 0 && !mma_loop<D, BITS>(p, w, smem_u32(qs), smem_u32(slots), fixed(smem_u32(&bars)), pair, stream)) {
                 __syncwarp();
-                if (elect_one()) tc_commit(smem_u32(&bars.drain));  // given up: products in flight end before the CTA leaves
-                mbar_wait_bounded(&bars.drain, 0);
+                if (elect_one()) tc_commit(smem_u32(&bars.drain[stream]));  // given up: products in flight end before the CTA leaves
+                mbar_wait_bounded(&bars.drain[stream], 0);
             }
         } else if (threadIdx.x == 17 * 32) {
             load_role<D, BITS>(p, w, ring, &bars, pair);
