@@ -54,15 +54,19 @@ struct Cfg {
     static constexpr int kRing = D == 64 ? 6 : (BITS == 8 ? 3 : 6);
     static constexpr int kQ = kStreams * kRowTile * D * 2;
     static constexpr int kSmem = 1024 + kQ + kSlots * kSlot + kRing * kEntry;
-    static constexpr uint32_t kS = kTile;                     // TMEM columns of S; P lies in their upper half
-    static constexpr uint32_t kO = 256;                       // first TMEM column of O
+    // TMEM columns: scores (one place for both accumulators at head_dim 128, else two),
+    // weights P of either parity as fp16, outputs
+    static constexpr int kPlaces = D == 128 ? 1 : 2;
+    static constexpr uint32_t kS1 = D == 64 ? 384 : 64;       // the second place for scores
+    static constexpr uint32_t kP = 128, kPStep = kTile / 2;
+    static constexpr uint32_t kO = 256;
     static_assert(kSmem + 512 <= 232448, "shared memory of a CTA");
-    static_assert(kO + kStreams * D <= 512 && 2 * kS <= kO, "TMEM");
+    static_assert(kO + kStreams * D <= (D == 64 ? kS1 : 512u) && kP + 2 * kPStep <= kO && kTile <= 128, "TMEM");
 };
 
 struct Bars {
     uint64_t ring_full[6], ring_empty[6], slot_full[6], slot_empty[6];
-    uint64_t s_full[2], p_full[2], o_full[2], q_full, drain[2], half;
+    uint64_t s_full[2], s_free[2], p_full[2], pv_done[2], q_full, drain[2];
     uint32_t tmem;
     int32_t abort;
 };
@@ -77,13 +81,13 @@ enum : uint32_t {
     kSlotFull = 12 * 8,
     kSlotEmpty = 18 * 8,
     kSFull = 24 * 8,
-    kPFull = 26 * 8,
-    kOFull = 28 * 8,
-    kQFull = 30 * 8,
-    kDrain = 31 * 8,
-    kHalf = 33 * 8,
-    kTmemAt = 34 * 8,
-    kAbort = 34 * 8 + 4,
+    kSFree = 26 * 8,
+    kPFull = 28 * 8,
+    kPvDone = 30 * 8,
+    kQFull = 32 * 8,
+    kDrain = 33 * 8,
+    kTmemAt = 35 * 8,
+    kAbort = 35 * 8 + 4,
 };
 __device__ __forceinline__ uint32_t fixed(uint32_t x) {
     asm volatile("" : "+r"(x));
@@ -150,14 +154,9 @@ __device__ __forceinline__ bool find_work(const ChunkParams& p, int rows_per_ite
     return true;
 }
 
-// Entry e of the ring holds the keys or the values of tile `tile`.  pair: both row
-// tiles use a tile of keys, then its values (K0 V0 K1 V1 ...); else the next
-// keys come ahead of the values (K0 K1 V0 K2 V1 ... V_last).
-__device__ __forceinline__ bool entry_of(int e, int tiles, bool pair, int& tile) {
-    if (pair) {
-        tile = e >> 1;
-        return (e & 1) != 0;
-    }
+// Entry e of the ring and of the slots: the keys or the values of tile `tile`.  The
+// next keys come ahead of the values (K0 K1 V0 K2 V1 ... V_last).
+__device__ __forceinline__ bool entry_of(int e, int tiles, int& tile) {
     if (e == 0) {
         tile = 0;
         return false;
@@ -171,10 +170,8 @@ __device__ __forceinline__ bool entry_of(int e, int tiles, bool pair, int& tile)
     tile = (e >> 1) - 1;
     return true;
 }
-__device__ __forceinline__ int key_entry(int tile, bool pair) { return pair ? 2 * tile : (tile == 0 ? 0 : 2 * tile - 1); }
-__device__ __forceinline__ int value_entry(int tile, int tiles, bool pair) {
-    return pair ? 2 * tile + 1 : (tile == tiles - 1 ? 2 * tiles - 1 : 2 * tile + 2);
-}
+__device__ __forceinline__ int key_entry(int tile) { return tile == 0 ? 0 : 2 * tile - 1; }
+__device__ __forceinline__ int value_entry(int tile, int tiles) { return tile == tiles - 1 ? 2 * tiles - 1 : 2 * tile + 2; }
 
 // Whether a phase is over; the hardware holds the warp for a while if it is not.
 // (With a time limit of its own, as mbar_try_wait asks for, the wait becomes a loop that
@@ -212,7 +209,7 @@ __device__ __forceinline__ bool wait(uint32_t bars, uint32_t bar, uint32_t parit
 
 // ------------------------------------------------------------------ loader --
 template <int D, int BITS>
-__device__ __forceinline__ void load_role(const ChunkParams& p, const Work& w, uint8_t* ring, Bars* bars, bool pair) {
+__device__ __forceinline__ void load_role(const ChunkParams& p, const Work& w, uint8_t* ring, Bars* bars) {
     using C = Cfg<D, BITS>;
     const uint64_t policy = policy_evict_first();
     const uint32_t at = fixed(smem_u32(bars));
@@ -222,7 +219,7 @@ __device__ __forceinline__ void load_role(const ChunkParams& p, const Work& w, u
         const int r = e % C::kRing, n = e / C::kRing;
         if (n > 0 && !wait(at, kRingEmpty + r * 8, (n - 1) & 1, p.status)) break;
         int tile;
-        const bool value = entry_of(e, w.tiles, pair, tile);
+        const bool value = entry_of(e, w.tiles, tile);
         const int t0 = (w.tile0 + tile) * C::kTile;
         const int rows = min(C::kTile, (w.khi - t0 + 15) & ~15);  // capacities are whole 16s
         const long long row = kv_row(p.map, p.num_kv_heads, w.b, w.h, t0, p.status);
@@ -283,7 +280,7 @@ __device__ __forceinline__ void sts128(uint32_t at, const __half2 (&h)[4]) {
 // A thread takes the same 16-byte piece of every 2^n-th key's codes: where its
 // outputs go, and in which order, is the same for all of them.
 template <int D, int BITS>
-__device__ __forceinline__ void unpack_role(const ChunkParams& p, const Work& w, uint32_t ring, uint32_t slots, uint32_t bars, bool pair) {
+__device__ __forceinline__ void unpack_role(const ChunkParams& p, const Work& w, uint32_t ring, uint32_t slots, uint32_t bars) {
     using C = Cfg<D, BITS>;
     constexpr int kUnits = BITS == 4 ? 4 : 2;             // 16-byte pieces of fp16 that 16 bytes of codes give
     constexpr int kChunks = D * BITS / 8 / 16;            // 16-byte pieces of codes per key
@@ -317,7 +314,7 @@ __device__ __forceinline__ void unpack_role(const ChunkParams& p, const Work& w,
         if (!wait(bars, kRingFull + r * 8, r_parity, p.status)) return;
         if (!wait(bars, kSlotEmpty + s * 8, s_parity, p.status)) return;  // (a fresh barrier's phase before the first is over)
         int tile;
-        const bool value = entry_of(e, w.tiles, pair, tile);
+        const bool value = entry_of(e, w.tiles, tile);
         const int t0 = (w.tile0 + tile) * C::kTile;
         const uint32_t src = from + r * C::kEntry, src_scale = from_scale + r * C::kEntry, dst = s * C::kSlot;
         uint4 word[kIts];
@@ -388,33 +385,51 @@ __device__ __forceinline__ void unpack_role(const ChunkParams& p, const Work& w,
 }
 
 // ---------------------------------------------------------------------- MMA --
-// Run by whole warps, an elected lane of which issues.  The tensor core takes in few
-// products ahead, so what is between two of them (waits of 70 cycles even when there
-// is nothing to wait for, commits of 50) is time that it stands still: with two
-// accumulators a warp for each issues, one's products filling the other's gaps.
+// Products come in turns n = 0, 1, ...: scores S(n) = Q K^T and outputs O += P(n) V.
+// With two row tiles (pair) turns 2j and 2j + 1 are theirs for tile j of the keys; with
+// one, turn n is tile n of the keys.  With two accumulators, turns of either parity have
+// one each.  Barriers come in twos as well, one for each parity, whose phase n >> 1 is
+// turn n's; only the one place for scores at head_dim 128 has a phase a turn.
+//   S(n) goes where S(n - places) was: that has been read into registers by then (s_free)
+//   P(n) goes where P(n - 2) was: its product has to be over (pv_done)
+// Scores and outputs are issued by a warp each, so that scores run ahead of the softmax
+// and neither's waits (70 cycles even where there is nothing to wait for; the tensor
+// core takes in few products ahead) are in the other's way.
 template <int D, int BITS>
-struct Products {
+struct Slots {
     using C = Cfg<D, BITS>;
-    uint32_t bars, tmem, q_op, k_op, v_op;
-    int32_t* status;
-    // the slot that an entry is in: entries are visited in order, some left out
-    int entry;
-    uint32_t slot, parity;
-    __device__ __forceinline__ bool ready(int e) {
+    int entry = 0;
+    uint32_t slot = 0, parity = 0;
+    // Waits for entry e (entries are visited in order).
+    __device__ __forceinline__ bool ready(int e, uint32_t bars, int32_t* status) {
 #pragma unroll 1
         for (; entry < e; ++entry)
             if (++slot == C::kSlots) {
                 slot = 0;
                 parity ^= 1;
             }
-        const bool ok = wait(bars, kSlotFull + slot * 8, parity, status);
-        tc_fence_after();
-        return ok;
+        return wait(bars, kSlotFull + slot * 8, parity, status);
     }
-    // S[buf] = Q[qt] K^T, the keys in the current slot
-    __device__ __forceinline__ void scores(uint32_t qt, uint32_t buf) const {
-        uint32_t a = q_op + qt * ((kRowTile * D * 2) >> 4), b = k_op + slot * (C::kSlot >> 4);
-        const uint32_t s = tmem + buf * C::kS;
+};
+
+template <int D, int BITS>
+__device__ __forceinline__ bool scores_role(const ChunkParams& p, const Work& w, uint32_t q, uint32_t slots, uint32_t bars, bool pair) {
+    using C = Cfg<D, BITS>;
+    const uint32_t tmem = fixed(lds32(bars + kTmemAt)), q_op = fixed(smem_operand(q, 16)), k_op = fixed(smem_operand(slots, 16));
+    const int turns = pair ? 2 * w.tiles : w.tiles;
+    Slots<D, BITS> in;
+    if (!wait(bars, kQFull, 0, p.status)) return false;
+#pragma unroll 1
+    for (int n = 0; n < turns; ++n) {
+        const bool first = !pair || (n & 1) == 0, last = !pair || (n & 1) != 0;
+        if (first && !in.ready(key_entry(pair ? n >> 1 : n), bars, p.status)) return false;
+        if (n >= C::kPlaces) {
+            const bool ok = C::kPlaces == 1 ? wait(bars, kSFree, (n - 1) & 1, p.status) : wait(bars, kSFree + (n & 1) * 8, ((n >> 1) - 1) & 1, p.status);
+            if (!ok) return false;
+        }
+        tc_fence_after();
+        uint32_t a = q_op + (pair ? n & 1 : 0) * ((kRowTile * D * 2) >> 4), b = k_op + in.slot * (C::kSlot >> 4);
+        const uint32_t s = tmem + (C::kPlaces == 2 ? (n & 1) * C::kS1 : 0);
         if (elect_one()) {
 #pragma unroll 1
             for (int i = 0; i < D / 64; ++i) {
@@ -423,76 +438,41 @@ struct Products {
                 a += (kRowTile * 128) >> 4;
                 b += (C::kTile * 128) >> 4;
             }
-            tc_commit(bars + kSFull + buf * 8);
-            tc_commit(bars + kSlotEmpty + slot * 8);
+            tc_commit(bars + kSFull + (n & 1) * 8);
+            if (last) tc_commit(bars + kSlotEmpty + in.slot * 8);
         }
         __syncwarp();
     }
-    // O[o] (+)= P[buf] V, the values in the current slot
-    __device__ __forceinline__ void outputs(uint32_t buf, uint32_t o, bool add, bool told) const {
-        uint32_t b = v_op + slot * (C::kSlot >> 4), s = tmem + buf * C::kS + C::kS / 2;
-        const uint32_t d = tmem + C::kO + o * D;
+    return true;
+}
+
+template <int D, int BITS>
+__device__ __forceinline__ bool outputs_role(const ChunkParams& p, const Work& w, uint32_t slots, uint32_t bars, bool pair) {
+    using C = Cfg<D, BITS>;
+    const uint32_t tmem = fixed(lds32(bars + kTmemAt)), v_op = fixed(smem_operand(slots, C::kTile * 128));
+    const int turns = pair ? 2 * w.tiles : w.tiles;
+    Slots<D, BITS> in;
+#pragma unroll 1
+    for (int n = 0; n < turns; ++n) {
+        const bool first = !pair || (n & 1) == 0, last = !pair || (n & 1) != 0;
+        if (first && !in.ready(value_entry(pair ? n >> 1 : n, w.tiles), bars, p.status)) return false;
+        if (!wait(bars, kPFull + (n & 1) * 8, (n >> 1) & 1, p.status)) return false;
+        tc_fence_after();
+        uint32_t b = v_op + in.slot * (C::kSlot >> 4), a = tmem + C::kP + (n & 1) * C::kPStep;
+        const uint32_t o = tmem + C::kO + (C::kStreams == 2 ? (n & 1) * D : 0);
+        const bool add = n >= C::kStreams;
         if (elect_one()) {
 #pragma unroll 1
             for (int i = 0; i < C::kTile / 64; ++i) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) tc_mma_ts(d, s + k * 8, b + ((k * 2048) >> 4), mma_desc(kRowTile, D, true), k > 0 || i > 0 || add);
-                s += 32;
+                for (int k = 0; k < 4; ++k) tc_mma_ts(o, a + k * 8, b + ((k * 2048) >> 4), mma_desc(kRowTile, D, true), k > 0 || i > 0 || add);
+                a += 32;
                 b += (4 * 2048) >> 4;
             }
-            tc_commit(bars + kSlotEmpty + slot * 8);
-            if (told) tc_commit(bars + kOFull + o * 8);
+            tc_commit(bars + kPvDone + (n & 1) * 8);
+            if (last) tc_commit(bars + kSlotEmpty + in.slot * 8);
         }
         __syncwarp();
-    }
-};
-
-// The tiles of one accumulator: all (pair) or every other one.
-template <int D, int BITS>
-__device__ __forceinline__ bool mma_loop(const ChunkParams& p, const Work& w, uint32_t q, uint32_t slots, uint32_t bars, bool pair, uint32_t stream) {
-    using C = Cfg<D, BITS>;
-    Products<D, BITS> x{bars, fixed(lds32(bars + kTmemAt)), fixed(smem_operand(q, 16)), fixed(smem_operand(slots, 16)), fixed(smem_operand(slots, C::kTile * 128)),
-                        p.status, 0, 0, 0};
-    if (!wait(bars, kQFull, 0, p.status)) return false;
-    const int T = w.tiles;
-    if (C::kStreams == 2) {
-        const int step = pair ? 1 : 2;
-        const uint32_t qt = pair ? stream : 0;
-        int j = pair ? 0 : stream;
-        if (j >= T) return true;
-        // the second row tile half a turn behind the first: in step, both would wait for
-        // their softmax at the same time
-        if (pair && stream == 1 && !wait(bars, kHalf, 0, p.status)) return false;
-        if (!x.ready(key_entry(j, pair))) return false;
-        tc_fence_after();
-        x.scores(qt, stream);
-#pragma unroll 1
-        for (uint32_t k = 0; j < T; ++k, j += step) {
-            if (!x.ready(value_entry(j, T, pair)) || !wait(bars, kPFull + stream * 8, k & 1, p.status)) return false;
-            tc_fence_after();
-            x.outputs(stream, stream, k > 0, j + step >= T);
-            if (j + step < T) {
-                if (!x.ready(key_entry(j + step, pair))) return false;
-                x.scores(qt, stream);
-            }
-        }
-        return true;
-    }
-    // one accumulator, two places for scores
-    for (int j = 0; j < 2 && j < T; ++j) {
-        if (!x.ready(key_entry(j, false))) return false;
-        tc_fence_after();
-        x.scores(0, j);
-    }
-#pragma unroll 1
-    for (int j = 0; j < T; ++j) {
-        if (!x.ready(value_entry(j, T, false)) || !wait(bars, kPFull + (j & 1) * 8, (j >> 1) & 1, p.status)) return false;
-        tc_fence_after();
-        x.outputs(j & 1, 0, j > 0, true);  // (told of every one: the softmax may have to rescale the sums before the next)
-        if (j + 2 < T) {
-            if (!x.ready(key_entry(j + 2, false))) return false;
-            x.scores(0, j & 1);
-        }
     }
     return true;
 }
@@ -600,107 +580,84 @@ struct State {
     float m, l;  // maximum that P counts from (log2 units, -inf: none yet), sum
 };
 
-// One warpgroup's tiles: j = first, first + step, ...
+// One warpgroup's turns: all, or (two accumulators) those of its parity.
 template <int D, int BITS>
 __device__ __forceinline__ bool softmax_loop(const ChunkParams& p, const Work& w, uint32_t bars, uint32_t tmem0, int stream, bool pair, bool active, int lo, int hi, State& st) {
     using C = Cfg<D, BITS>;
     constexpr int N = C::kTile;
     const int lane = threadIdx.x & 31;
-    const uint32_t lanes = static_cast<uint32_t>((threadIdx.x >> 5) & 3) << 21;
-    const uint32_t tmem = tmem0 + lanes;
+    const uint32_t tmem = tmem0 + (static_cast<uint32_t>((threadIdx.x >> 5) & 3) << 21);
     const float c = p.score_scale_log2;
-    const int step = pair || C::kStreams == 1 ? 1 : 2;
-    for (int j = step == 2 ? stream : 0, k = 0; j < w.tiles; j += step, ++k) {
-        const int buf = pair || C::kStreams == 2 ? stream : j & 1;
-        const uint32_t phase = C::kStreams == 1 ? (j >> 1) & 1 : k & 1;
-        if (!wait(bars, kSFull + buf * 8, phase, p.status)) return false;
+    const int turns = pair ? 2 * w.tiles : w.tiles;
+#pragma unroll 1
+    for (int n = stream; n < turns; n += C::kStreams) {
+        const uint32_t odd = n & 1, phase = (n >> 1) & 1;
+        if (!wait(bars, kSFull + odd * 8, phase, p.status)) return false;
         tc_fence_after();
+        float s[N];
         if (active) {
-            const uint32_t sa = tmem + buf * C::kS;
-            const int t0 = (w.tile0 + j) * C::kTile;
-            if (__any_sync(0xffffffffu, t0 < lo || t0 + N > hi)) {
-                // scores of keys that the row does not see: minus infinity, once and for both passes
-                const unsigned span = static_cast<unsigned>(hi > lo ? hi - lo : 0);
-#pragma unroll 1
-                for (int x = 0; x < N; x += 32) {
-                    float s[32];
-                    tmem_ld32(sa + x, s);
-                    tmem_wait_ld();
+            const uint32_t sa = tmem + (C::kPlaces == 2 ? odd * C::kS1 : 0);
 #pragma unroll
-                    for (int y = 0; y < 32; ++y) s[y] = static_cast<unsigned>(t0 + x + y - lo) < span ? s[y] : -INFINITY;
-                    tmem_st32(sa + x, s);
-                }
-                tmem_wait_st();
-            }
-            // Two passes over the scores in TMEM, 32 columns at a time with the next 32 on
-            // their way, in loops (unrolled, the code of the roles that share an
-            // instruction cache did not fit it: products were issued at half the rate).
-            float u[32], v[32];
-            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-            auto highest = [&mx](const float (&s)[32]) {
-#pragma unroll
-                for (int x = 0; x < 32; x += 2) mx[(x >> 1) & 3] = max3(mx[(x >> 1) & 3], s[x], s[x + 1]);
-            };
-            tmem_ld32(sa, u);
-#pragma unroll 1
-            for (int x = 0; x < N; x += 64) {
-                tmem_wait_ld();
-                tmem_ld32(sa + x + 32, v);
-                highest(u);
-                tmem_wait_ld();
-                tmem_ld32(sa + (x + 64) % N, u);
-                highest(v);
-            }
+            for (int x = 0; x < N; x += 32) tmem_ld32(sa + x, s + x);
             tmem_wait_ld();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive(bars + kSFree + (C::kPlaces == 2 ? odd * 8 : 0));
+        // P's columns are free once the product before the last is over
+        if (n >= 2 && !wait(bars, kPvDone + odd * 8, phase ^ 1, p.status)) return false;
+        if (active) {
+            tc_fence_after();
+            const int t0 = (w.tile0 + (pair ? n >> 1 : n)) * N;
+            if (__any_sync(0xffffffffu, t0 < lo || t0 + N > hi)) {
+                const unsigned span = static_cast<unsigned>(hi > lo ? hi - lo : 0);
+#pragma unroll
+                for (int x = 0; x < N; ++x) s[x] = static_cast<unsigned>(t0 + x - lo) < span ? s[x] : -INFINITY;
+            }
+            float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+            for (int x = 4; x < N; x += 2) mx[(x >> 1) & 3] = max3(mx[(x >> 1) & 3], s[x], s[x + 1]);
             const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * c;
-            const bool grow = k == 0 ? top > st.m : top > st.m + kLazy;
+            const bool fresh = n < C::kStreams;  // nothing in O yet
+            const bool grow = fresh ? top > st.m : top > st.m + kLazy;
             if (__any_sync(0xffffffffu, grow)) {
                 const float f = grow ? ex2_approx(st.m - top) : 1.f;
                 if (grow) st.m = top;
                 st.l *= f;
-                if (k > 0) {
-                    // O holds the products up to the tile before; with one accumulator the
-                    // last of them may still run (with two, this S came after it)
+                if (!fresh) {
+                    // O holds the products of the turns before, all of them over (one accumulator:
+                    // once the last turn's is)
                     if (C::kStreams == 1) {
-                        if (!wait(bars, kOFull, (j - 1) & 1, p.status)) return false;
+                        if (!wait(bars, kPvDone + (odd ^ 1) * 8, ((n - 1) >> 1) & 1, p.status)) return false;
                         tc_fence_after();
                     }
                     const uint32_t oa = tmem + C::kO + (C::kStreams == 2 ? stream * D : 0);
 #pragma unroll 1
-                    for (int x = 0; x < D; x += 32) {
-                        float o[32];
-                        tmem_ld32(oa + x, o);
+                    for (int x = 0; x < D; x += 16) {
+                        float o[16];
+                        tmem_ld16(oa + x, o);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int y = 0; y < 32; ++y) o[y] *= f;
-                        tmem_st32(oa + x, o);
+                        for (int y = 0; y < 16; ++y) o[y] *= f;
+                        tmem_st16(oa + x, reinterpret_cast<const uint32_t*>(o));
                     }
                 }
             }
             const float base = st.m == -INFINITY ? 0.f : -st.m;
             float2 sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
-            // from the last column down: P's columns are those of scores already read
-            auto weights = [&](const float (&s)[32], int x) {
+            const uint32_t pa = tmem + C::kP + odd * C::kPStep;
+#pragma unroll
+            for (int x = 0; x < N; x += 32) {
                 uint32_t pk[16];
 #pragma unroll
                 for (int y = 0; y < 16; ++y) {
-                    float2 e = fma2(make_float2(s[2 * y], s[2 * y + 1]), make_float2(c, c), make_float2(base, base));
+                    float2 e = fma2(make_float2(s[x + 2 * y], s[x + 2 * y + 1]), make_float2(c, c), make_float2(base, base));
                     e.x = ex2_approx(e.x);
                     e.y = ex2_approx(e.y);
                     sum[y & 1] = add2(sum[y & 1], e);
                     pk[y] = pack_half2(e.x, e.y);
                 }
-                tmem_st16(sa + C::kS / 2 + x / 2, pk);
-            };
-            tmem_ld32(sa + N - 32, u);
-#pragma unroll 1
-            for (int x = N - 32; x > 0; x -= 64) {
-                tmem_wait_ld();
-                tmem_ld32(sa + x - 32, v);
-                weights(u, x);
-                tmem_wait_ld();
-                if (x > 64) tmem_ld32(sa + x - 64, u);
-                weights(v, x - 32);
+                tmem_st16(pa + x / 2, pk);
             }
             sum[0] = add2(sum[0], sum[1]);
             st.l += sum[0].x + sum[0].y;
@@ -708,10 +665,7 @@ __device__ __forceinline__ bool softmax_loop(const ChunkParams& p, const Work& w
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) {
-            arrive(bars + kPFull + buf * 8);
-            if (C::kStreams == 2 && stream == 0 && k == 0) arrive(bars + kHalf);
-        }
+        if (lane == 0) arrive(bars + kPFull + odd * 8);
     }
     return true;
 }
@@ -823,13 +777,11 @@ __device__ __forceinline__ void softmax_role(const ChunkParams& p, const Work& w
     State st{-INFINITY, 0.f};
     const bool done = softmax_loop<D, BITS>(p, w, bars, tmem, stream, pair, active, lo, hi, st);
     const bool split_keys = !pair && C::kStreams == 2;
-    // tiles of this stream, and the phase of its accumulator's last barrier
-    const int mine = split_keys ? (w.tiles + 1 - stream) / 2 : w.tiles;
+    // the last of this accumulator's products
+    const int turns = pair ? 2 * w.tiles : w.tiles, last = C::kStreams == 1 ? turns - 1 : ((turns - 1 - stream) & ~1) + stream;
     bool ok = done;
-    if (ok && mine > 0) {
-        // (one accumulator: a phase a tile, of which the last score tile shows all but the last two to be over)
-        if (C::kStreams == 1 && mine > 1) ok = wait(bars, kOFull, (mine - 2) & 1, p.status);
-        ok = ok && wait(bars, kOFull + (C::kStreams == 2 ? stream : 0) * 8, C::kStreams == 1 ? (mine - 1) & 1 : 0, p.status);
+    if (ok && turns > stream) {
+        ok = wait(bars, kPvDone + (last & 1) * 8, (last >> 1) & 1, p.status);
         tc_fence_after();
     }
     const uint32_t oa = tmem + (static_cast<uint32_t>((threadIdx.x >> 5) & 3) << 21) + C::kO + (C::kStreams == 2 ? stream * D : 0);
@@ -839,7 +791,7 @@ __device__ __forceinline__ void softmax_role(const ChunkParams& p, const Work& w
         asm volatile("bar.sync 1, 256;" ::: "memory");
         if (stream == 1 && ok && active) {
 #pragma unroll 1
-            for (int x = 0; x < D && mine > 0; x += 32) {
+            for (int x = 0; x < D && turns > 1; x += 32) {
                 float o[32];
                 tmem_ld32(oa + x, o);
                 tmem_wait_ld();
@@ -876,7 +828,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     using C = Cfg<D, BITS>;
     extern __shared__ uint8_t raw[];
     __shared__ Bars bars;
-    static_assert(offsetof(Bars, slot_empty) == kSlotEmpty && offsetof(Bars, q_full) == kQFull && offsetof(Bars, abort) == kAbort, "addresses");
+    static_assert(offsetof(Bars, slot_empty) == kSlotEmpty && offsetof(Bars, s_full) == kSFull && offsetof(Bars, q_full) == kQFull && offsetof(Bars, abort) == kAbort, "addresses");
     uint8_t* base = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);  // (an offset, so that it stays a shared-memory pointer)
     uint8_t* qs = base;
     uint8_t* slots = base + C::kQ;
@@ -892,43 +844,46 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             mbar_init(&bars.ring_full[i], 1);
             mbar_init(&bars.ring_empty[i], C::kUnpackWarps);
             mbar_init(&bars.slot_full[i], C::kUnpackWarps);
-            mbar_init(&bars.slot_empty[i], pair ? 2 : 1);  // the products that use it
+            mbar_init(&bars.slot_empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bars.s_full[i], 1);
             mbar_init(&bars.p_full[i], 4);
-            mbar_init(&bars.o_full[i], 1);
+            mbar_init(&bars.s_free[i], 4);
+            mbar_init(&bars.pv_done[i], 1);
             mbar_init(&bars.drain[i], 1);
         }
         mbar_init(&bars.q_full, C::kStreams * 4);
-        mbar_init(&bars.half, 4);
         bars.abort = 0;
         fence_mbarrier_init();
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    // registers: 640 x 96 at launch; 256 x 144 + 256 x 72 + 128 x 48 (one
-    // accumulator: 128 x 200 + 128 x 48 + 256 x 72 + 128 x 48)
+    // registers: 640 x 96 at launch; 256 x 160 + 256 x 64 + 128 x 32 (one
+    // accumulator: 128 x 200 + 128 x 32 + 256 x 64 + 128 x 32)
     if (warp < C::kStreams * 4) {
-        regs_raise<C::kStreams == 2 ? 144 : 200>();
+        regs_raise<C::kStreams == 2 ? 160 : 200>();
         softmax_role<D, BITS, ROT>(p, w, qs, slots, fixed(smem_u32(&bars)), warp >> 2, pair);
     } else if (warp < 8) {
-        regs_lower<48>();
+        regs_lower<32>();
     } else if (warp < 16) {
-        regs_lower<72>();
-        unpack_role<D, BITS>(p, w, fixed(smem_u32(ring)), fixed(smem_u32(slots)), fixed(smem_u32(&bars)), pair);
+        regs_lower<64>();
+        unpack_role<D, BITS>(p, w, fixed(smem_u32(ring)), fixed(smem_u32(slots)), fixed(smem_u32(&bars)));
     } else {
-        regs_lower<48>();
-        if (warp == 16 || (C::kStreams == 2 && warp == 18)) {
-            const uint32_t stream = warp == 18 ? 1 : 0;
-            if (w.tiles > 0 && !mma_loop<D, BITS>(p, w, smem_u32(qs), smem_u32(slots), fixed(smem_u32(&bars)), pair, stream)) {
+        regs_lower<32>();
+        if (warp == 16 || warp == 18) {
+            const uint32_t at = fixed(smem_u32(&bars)), in = fixed(smem_u32(slots));
+            if (!(warp == 16 ? scores_role<D, BITS>(p, w, fixed(smem_u32(qs)), in, at, pair) : outputs_role<D, BITS>(p, w, in, at, pair))) {
                 __syncwarp();
-                if (elect_one()) tc_commit(smem_u32(&bars.drain[stream]));  // given up: products in flight end before the CTA leaves
-                mbar_wait_bounded(&bars.drain[stream], 0);
+                const uint32_t bar = at + kDrain + (warp == 18 ? 8 : 0);
+                if (elect_one()) tc_commit(bar);  // given up: products in flight end before the CTA leaves
+                __syncwarp();
+                for (int it = 0; it < 1 << 20 && !over(bar, 0); ++it) {
+                }
             }
         } else if (threadIdx.x == 17 * 32) {
-            load_role<D, BITS>(p, w, ring, &bars, pair);
+            load_role<D, BITS>(p, w, ring, &bars);
         }
         __syncwarp();
     }
