@@ -15,7 +15,7 @@
 //                     128-byte rows with the 128-byte swizzle: keys are then a
 //                     K-major operand and values an N-major one, in the same layout
 //   MMA warps         S = Q K^T and O += P V, S, P and O in TMEM (P in S's place)
-//   softmax warps     a thread a row: maximum, 2^x, P as fp16, sum; no shuffles
+//   softmax warps     two threads a row: maximum, 2^x, P as fp16, sum; no shuffles
 // The two row tiles take turns: while one's softmax runs the tensor core works for
 // the other.  Up to 128 rows (a few tokens) make one tile; the two halves then take
 // every other tile of keys and are merged in the end.  O is rescaled only when a
@@ -35,7 +35,7 @@ namespace tq {
 
 namespace {
 
-constexpr int kThreads = 640;       // 8 softmax warps, 8 that unpack, 2 that issue products, one that copies
+constexpr int kThreads = 896;       // 16 softmax warps, 8 that unpack, 2 that issue products, one that copies
 constexpr int kRowTile = 128;
 constexpr float kLazy = 8.f;  // log2 of how far P may grow before O is rescaled
 
@@ -43,7 +43,8 @@ template <int D, int BITS>
 struct Cfg {
     static constexpr int kStreams = D == 256 ? 1 : 2;         // softmax warpgroups, output accumulators
     static constexpr int kTile = D == 256 ? 64 : 128;         // keys
-    static constexpr int kUnpackWarp = 8;                     // first unpacking warp
+    static constexpr int kSoftmax = kStreams * 256;           // softmax threads: two for each row, half of a tile's keys each
+    static constexpr int kUnpackWarp = 16;                    // first unpacking warp
     static constexpr int kUnpackWarps = 8;
     static constexpr int kBlocks = D / 64;                    // blocks of 64 channels: 128-byte rows
     static constexpr int kSlot = kTile * D * 2;               // one unpacked tile of keys or values
@@ -54,13 +55,14 @@ struct Cfg {
     static constexpr int kRing = D == 64 ? 6 : (BITS == 8 ? 3 : 6);
     static constexpr int kQ = kStreams * kRowTile * D * 2;
     static constexpr int kSmem = 1024 + kQ + kSlots * kSlot + kRing * kEntry;
+    static_assert(kQ + kSlots * kSlot >= kStreams * D * (kRowTile + 1) * 4, "rows on their way out");
     // TMEM columns: scores (one place for both accumulators at head_dim 128, else two),
     // weights P of either parity as fp16, outputs
     static constexpr int kPlaces = D == 128 ? 1 : 2;
     static constexpr uint32_t kS1 = D == 64 ? 384 : 64;       // the second place for scores
     static constexpr uint32_t kP = 128, kPStep = kTile / 2;
     static constexpr uint32_t kO = 256;
-    static_assert(kSmem + 512 <= 232448, "shared memory of a CTA");
+    static_assert(kSmem + 6144 <= 232448, "shared memory of a CTA");
     static_assert(kO + kStreams * D <= (D == 64 ? kS1 : 512u) && kP + 2 * kPStep <= kO && kTile <= 128, "TMEM");
 };
 
@@ -69,6 +71,9 @@ struct Bars {
     uint64_t s_full[2], s_free[2], p_full[2], pv_done[2], q_full, drain[2];
     uint32_t tmem;
     int32_t abort;
+    float top[2][2][kRowTile];  // [accumulator][half of the keys][row]: maxima of a turn
+    float sum[2][2][kRowTile];  // sums in the end
+    float max[kRowTile];        // the second accumulator's maxima
 };
 
 // Addresses of the barriers from that of the first.  (Each role takes the first one's
@@ -484,52 +489,15 @@ __device__ __forceinline__ constexpr int place(int c) {
     return BITS == 4 ? (c & ~7) | ((c & 3) << 1) | ((c >> 2) & 1) : c;
 }
 
-// The fast transform of N values in one thread's registers.
-template <int N>
-__device__ __forceinline__ void hadamard_thread(float (&v)[N]) {
-#pragma unroll
-    for (int h = 1; h < N; h <<= 1) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            if ((i & h) == 0) {
-                const float u = v[i], x = v[i + h];
-                v[i] = u + x;
-                v[i + h] = u - x;
-            }
-        }
-    }
-}
-
-// 64 channels (a 128-byte row of one block) of row `row` of a query tile.
-template <int BITS>
-__device__ __forceinline__ void store_q64(uint8_t* block, int row, const __half2 (&x)[32]) {
-#pragma unroll
-    for (int u = 0; u < 8; ++u) {
-        uint4 o;
-        uint32_t* w = reinterpret_cast<uint32_t*>(&o);
-        const uint32_t* s = reinterpret_cast<const uint32_t*>(x) + u * 4;
-        if (BITS == 4) {
-            w[0] = __byte_perm(s[0], s[2], 0x5410);
-            w[1] = __byte_perm(s[0], s[2], 0x7632);
-            w[2] = __byte_perm(s[1], s[3], 0x5410);
-            w[3] = __byte_perm(s[1], s[3], 0x7632);
-        } else {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) w[k] = s[k];
-        }
-        *reinterpret_cast<uint4*>(block + row * 128 + ((u ^ (row & 7)) << 4)) = o;
-    }
-}
-
-// The 128 rows of a query tile from row tile_row0 of the item on, by one warpgroup
-// (thread `row`): 16 bytes a thread, rows behind the last as zeros.
+// The 128 rows of a query tile from row tile_row0 of the item on, by 256 threads:
+// 16 bytes a thread, rows behind the last as zeros.
 template <int D, int BITS>
-__device__ __forceinline__ void load_query(const ChunkParams& p, const Work& w, uint8_t* tile, int row, int tile_row0) {
+__device__ __forceinline__ void load_query(const ChunkParams& p, const Work& w, uint8_t* tile, int tid, int tile_row0) {
     constexpr int kPieces = D / 8;  // 16-byte pieces of a row: eight channels
-    const int u = row % kPieces;
-#pragma unroll 8
-    for (int it = 0; it < kPieces; ++it) {
-        const int at = it * (128 / kPieces) + row / kPieces, r = tile_row0 + at;
+    const int u = tid % kPieces;
+#pragma unroll
+    for (int it = 0; it < kPieces / 2; ++it) {
+        const int at = it * (256 / kPieces) + tid / kPieces, r = tile_row0 + at;
         uint4 x = make_uint4(0, 0, 0, 0);
         if (r < w.rows) {
             const int flat = w.row0 + r, i = flat / p.group_q, g = flat - i * p.group_q;
@@ -542,36 +510,24 @@ __device__ __forceinline__ void load_query(const ChunkParams& p, const Work& w, 
     }
 }
 
-// The same for a cache of rotated keys: a thread a row.
+// The same for a cache of rotated keys: a warp a row.
 template <int D, int BITS>
-__device__ __forceinline__ void load_query_rotated(const ChunkParams& p, const Work& w, uint8_t* tile, int row, int tile_row0) {
-    const int r = tile_row0 + row;
-    const bool valid = r < w.rows;
-    const int flat = w.row0 + (valid ? r : 0), i = flat / p.group_q, g = flat - i * p.group_q;
-    const uint4* src = reinterpret_cast<const uint4*>(p.q + w.b * p.stride_b + (w.h * p.group_q + g) * p.stride_h + i * p.stride_t);
-    constexpr int N = D < 128 ? D : 128;
-    for (int half = 0; half < D / N; ++half) {
-        float v[N];
-#pragma unroll
-        for (int u = 0; u < N / 8; ++u) {
-            uint4 x = valid ? __ldg(src + u) : make_uint4(0, 0, 0, 0);
-            halves_to_floats<8>(&x, *reinterpret_cast<float(*)[8]>(v + u * 8));
-            if (D == 256) {  // the stage of 128 first: sums for the first half, differences for the second
-                float y[8];
-                x = valid ? __ldg(src + 16 + u) : make_uint4(0, 0, 0, 0);
-                halves_to_floats<8>(&x, y);
-#pragma unroll
-                for (int k = 0; k < 8; ++k) v[u * 8 + k] = half ? v[u * 8 + k] - y[k] : v[u * 8 + k] + y[k];
-            }
+__device__ __forceinline__ void load_query_rotated(const ChunkParams& p, const Work& w, uint8_t* tile, int tid, int tile_row0) {
+    constexpr int E = D / 32;
+    const int lane = tid & 31;
+    for (int at = tid >> 5; at < kRowTile; at += 8) {
+        const int r = tile_row0 + at;
+        float v[E] = {};
+        if (r < w.rows) {
+            const int flat = w.row0 + r, i = flat / p.group_q, g = flat - i * p.group_q;
+            halves_to_floats<E>(p.q + w.b * p.stride_b + (w.h * p.group_q + g) * p.stride_h + i * p.stride_t + lane * E, v);
+            hadamard_warp<E>(v, lane, p.rot_scale);
         }
-        hadamard_thread<N>(v);
-        const float scale = p.negate_q ? -p.rot_scale : p.rot_scale;
 #pragma unroll
-        for (int blk = 0; blk < N / 64; ++blk) {
-            __half2 x[32];
-#pragma unroll
-            for (int k = 0; k < 32; ++k) x[k] = __floats2half2_rn(v[blk * 64 + 2 * k] * scale, v[blk * 64 + 2 * k + 1] * scale);
-            store_q64<BITS>(tile + (half * (N / 64) + blk) * (kRowTile * 128), row, x);
+        for (int e = 0; e < E; ++e) {
+            const int c = lane * E + e, x = (c & ~63) | place<BITS>(c & 63);
+            const __half q = __float2half_rn(p.negate_q ? -v[e] : v[e]);
+            *reinterpret_cast<__half*>(tile + (x / 64) * (kRowTile * 128) + at * 128 + (((x / 8 % 8) ^ (at & 7)) << 4) + (x & 7) * 2) = q;
         }
     }
 }
@@ -580,12 +536,27 @@ struct State {
     float m, l;  // maximum that P counts from (log2 units, -inf: none yet), sum
 };
 
-// One warpgroup's turns: all, or (two accumulators) those of its parity.
+// Two warps that have the same 32 rows, one for each half of the keys, meet; whether
+// either has something to tell.
+__device__ __forceinline__ bool either(int id, bool pred) {
+    uint32_t any;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %2, 0;\n\tbarrier.cta.red.or.pred q, %1, 64, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(any)
+        : "r"(id), "r"(static_cast<uint32_t>(pred))
+        : "memory");
+    return any != 0;
+}
+
+// One accumulator's turns: all, or (two accumulators) those of its parity.  A thread has
+// one half of a row's keys; row maxima are exchanged only where one of the 64 threads
+// of the same 32 rows sees its row outgrow what P counts from.
 template <int D, int BITS>
-__device__ __forceinline__ bool softmax_loop(const ChunkParams& p, const Work& w, uint32_t bars, uint32_t tmem0, int stream, bool pair, bool active, int lo, int hi, State& st) {
+__device__ __forceinline__ bool softmax_loop(const ChunkParams& p, const Work& w, uint32_t bars, Bars* shared, uint32_t tmem0, int stream, int half, bool pair, bool active,
+                                             int lo, int hi, State& st) {
     using C = Cfg<D, BITS>;
-    constexpr int N = C::kTile;
-    const int lane = threadIdx.x & 31;
+    constexpr int N = C::kTile / 2;
+    const int lane = threadIdx.x & 31, row = threadIdx.x & 127, id = 1 + stream * 4 + ((threadIdx.x >> 5) & 3);
     const uint32_t tmem = tmem0 + (static_cast<uint32_t>((threadIdx.x >> 5) & 3) << 21);
     const float c = p.score_scale_log2;
     const int turns = pair ? 2 * w.tiles : w.tiles;
@@ -596,7 +567,7 @@ __device__ __forceinline__ bool softmax_loop(const ChunkParams& p, const Work& w
         tc_fence_after();
         float s[N];
         if (active) {
-            const uint32_t sa = tmem + (C::kPlaces == 2 ? odd * C::kS1 : 0);
+            const uint32_t sa = tmem + (C::kPlaces == 2 ? odd * C::kS1 : 0) + half * N;
 #pragma unroll
             for (int x = 0; x < N; x += 32) tmem_ld32(sa + x, s + x);
             tmem_wait_ld();
@@ -604,11 +575,9 @@ __device__ __forceinline__ bool softmax_loop(const ChunkParams& p, const Work& w
         tc_fence_before();
         __syncwarp();
         if (lane == 0) arrive(bars + kSFree + (C::kPlaces == 2 ? odd * 8 : 0));
-        // P's columns are free once the product before the last is over
-        if (n >= 2 && !wait(bars, kPvDone + odd * 8, phase ^ 1, p.status)) return false;
         if (active) {
-            tc_fence_after();
-            const int t0 = (w.tile0 + (pair ? n >> 1 : n)) * N;
+            if (lds32(bars + kAbort) != 0) return false;  // (the other half's warp may have left)
+            const int t0 = (w.tile0 + (pair ? n >> 1 : n)) * C::kTile + half * N;
             if (__any_sync(0xffffffffu, t0 < lo || t0 + N > hi)) {
                 const unsigned span = static_cast<unsigned>(hi > lo ? hi - lo : 0);
 #pragma unroll
@@ -617,23 +586,26 @@ __device__ __forceinline__ bool softmax_loop(const ChunkParams& p, const Work& w
             float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
             for (int x = 4; x < N; x += 2) mx[(x >> 1) & 3] = max3(mx[(x >> 1) & 3], s[x], s[x + 1]);
-            const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * c;
+            float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * c;
             const bool fresh = n < C::kStreams;  // nothing in O yet
-            const bool grow = fresh ? top > st.m : top > st.m + kLazy;
-            if (__any_sync(0xffffffffu, grow)) {
+            const float limit = fresh ? st.m : st.m + kLazy;
+            if (either(id, top > limit)) {
+                shared->top[stream][half][row] = top;
+                asm volatile("barrier.cta.sync %0, 64;" ::"r"(id) : "memory");
+                top = fmaxf(top, shared->top[stream][half ^ 1][row]);
+                const bool grow = top > limit;
                 const float f = grow ? ex2_approx(st.m - top) : 1.f;
                 if (grow) st.m = top;
                 st.l *= f;
                 if (!fresh) {
-                    // O holds the products of the turns before, all of them over (one accumulator:
-                    // once the last turn's is)
-                    if (C::kStreams == 1) {
-                        if (!wait(bars, kPvDone + (odd ^ 1) * 8, ((n - 1) >> 1) & 1, p.status)) return false;
-                        tc_fence_after();
-                    }
-                    const uint32_t oa = tmem + C::kO + (C::kStreams == 2 ? stream * D : 0);
+                    // O holds the products of the turns before (each half of the threads rescales
+                    // half of its columns): all of them have to be over
+                    const uint32_t before = C::kStreams == 1 ? n - 1 : n - 2;
+                    if (!wait(bars, kPvDone + (before & 1) * 8, (before >> 1) & 1, p.status)) return false;
+                    tc_fence_after();
+                    const uint32_t oa = tmem + C::kO + (C::kStreams == 2 ? stream * D : 0) + half * (D / 2);
 #pragma unroll 1
-                    for (int x = 0; x < D; x += 16) {
+                    for (int x = 0; x < D / 2; x += 16) {
                         float o[16];
                         tmem_ld16(oa + x, o);
                         tmem_wait_ld();
@@ -643,9 +615,14 @@ __device__ __forceinline__ bool softmax_loop(const ChunkParams& p, const Work& w
                     }
                 }
             }
+        }
+        // P's columns are free once the product before the last is over
+        if (n >= 2 && !wait(bars, kPvDone + odd * 8, phase ^ 1, p.status)) return false;
+        if (active) {
+            tc_fence_after();
             const float base = st.m == -INFINITY ? 0.f : -st.m;
             float2 sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
-            const uint32_t pa = tmem + C::kP + odd * C::kPStep;
+            const uint32_t pa = tmem + C::kP + odd * C::kPStep + half * (N / 2);
 #pragma unroll
             for (int x = 0; x < N; x += 32) {
                 uint32_t pk[16];
@@ -670,52 +647,105 @@ __device__ __forceinline__ bool softmax_loop(const ChunkParams& p, const Work& w
     return true;
 }
 
-// The output row of one thread, from TMEM (merge: + other's columns in shared memory).
 template <int D, int BITS, bool ROT>
-__device__ __forceinline__ void write_row(const ChunkParams& p, const Work& w, uint32_t oa, bool has, bool valid, int r, const State& st, float f,
-                                          const float* other, float fo) {
-    const int flat = w.row0 + r, i = flat / p.group_q, g = flat - i * p.group_q;
-    // 32 columns of O, scaled, by channel
-    auto columns = [&](int x, float (&v)[32]) {
-        float o[32];
-        if (has) {
-            tmem_ld32(oa + x, o);
+__device__ __forceinline__ void softmax_role(const ChunkParams& p, const Work& w, uint8_t* qs, uint8_t* slots, uint32_t bars, Bars* shared, int stream, bool pair) {
+    using C = Cfg<D, BITS>;
+    const int row = threadIdx.x & 127, half = (threadIdx.x >> 7) & 1, lane = threadIdx.x & 31;
+    const int tile_row0 = pair ? stream * kRowTile : 0;
+    const int r = tile_row0 + row;  // row of the item
+    const bool valid = r < w.rows;
+    const bool active = __any_sync(0xffffffffu, valid);
+    if (pair || stream == 0) {
+        uint8_t* tile = qs + (pair ? stream : 0) * (kRowTile * D * 2);
+        if (ROT && p.rotate_q)
+            load_query_rotated<D, BITS>(p, w, tile, threadIdx.x & 255, tile_row0);
+        else
+            load_query<D, BITS>(p, w, tile, threadIdx.x & 255, tile_row0);
+    }
+    fence_proxy_async_shared();
+    __syncwarp();
+    if (lane == 0) arrive(bars + kQFull);
+    const int flat = w.row0 + (valid ? r : 0), i = flat / p.group_q, g = flat - i * p.group_q;
+    // (rows behind the last are zeros that see everything: they ask for no masks)
+    const int lo = valid ? first_key(p, i, w.ql, w.len) : 0, hi = valid ? end_key(p, i, w.ql, w.len) : 0x7fffffff;
+    const uint32_t tmem = fixed(lds32(bars + kTmemAt));
+    State st{-INFINITY, 0.f};
+    bool ok = softmax_loop<D, BITS>(p, w, bars, shared, tmem, stream, half, pair, active, lo, hi, st);
+    // the last of this accumulator's products
+    const int turns = pair ? 2 * w.tiles : w.tiles, last = C::kStreams == 1 ? turns - 1 : ((turns - 1 - stream) & ~1) + stream;
+    if (ok && turns > stream) {
+        ok = wait(bars, kPvDone + (last & 1) * 8, (last >> 1) & 1, p.status);
+        tc_fence_after();
+    }
+    // Sums of both halves; and where the accumulators are those of one row tile, the
+    // second one's state through shared memory (the operands' place: once all softmax
+    // threads are here no product is left that reads them).
+    const bool merge = !pair && C::kStreams == 2 && turns > 1;
+    const uint32_t oa = tmem + (static_cast<uint32_t>((threadIdx.x >> 5) & 3) << 21) + C::kO + (C::kStreams == 2 ? stream * D : 0);
+    shared->sum[stream][half][row] = st.l;
+    if (merge && stream == 1 && half == 0) shared->max[row] = st.m;
+    asm volatile("barrier.cta.sync 9, %0;" ::"n"(C::kSoftmax) : "memory");
+    float l = shared->sum[stream][0][row] + shared->sum[stream][1][row];
+    float* apart = reinterpret_cast<float*>(qs);  // [D][129]
+    constexpr int kPad = kRowTile + 1;
+    float f = 1.f, fo = 0.f, m = st.m;
+    if (merge) {
+        if (stream == 1 && ok && active) {
+#pragma unroll 1
+            for (int x = half * (D / 2); x < (half + 1) * (D / 2); x += 16) {
+                float o[16];
+                tmem_ld16(oa + x, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int y = 0; y < 16; ++y) apart[(x + y) * kPad + row] = o[y];
+            }
+        }
+        asm volatile("barrier.cta.sync 9, %0;" ::"n"(C::kSoftmax) : "memory");
+        const float m1 = shared->max[row], l1 = shared->sum[1][0][row] + shared->sum[1][1][row];
+        m = fmaxf(st.m, m1);
+        f = st.m == -INFINITY ? 0.f : ex2_approx(st.m - m);
+        fo = m1 == -INFINITY ? 0.f : ex2_approx(m1 - m);
+        l = l * f + l1 * fo;
+    }
+    const bool mine = (pair || stream == 0) && ok && active;
+    if (p.n_splits == 1) {
+        const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+        f *= inv;
+        fo *= inv;
+    }
+    // 16 columns of the output at a time
+    auto columns = [&](int x, float (&v)[16]) {
+        float o[16];
+        if (turns > 0) {
+            tmem_ld16(oa + x, o);
             tmem_wait_ld();
         }
 #pragma unroll
-        for (int y = 0; y < 32; ++y) {
+        for (int y = 0; y < 16; ++y) {
             const int at = place<BITS>(y);
-            v[y] = has ? o[at] * f : 0.f;
-            if (other != nullptr) v[y] += other[(x + at) * kRowTile] * fo;
+            v[y] = turns > 0 ? o[at] * f : 0.f;
+            if (merge) v[y] += apart[(x + at) * kPad + row] * fo;
         }
     };
-    if (p.n_splits > 1) {
-        const long long at = static_cast<long long>(w.part) * p.rows_per_item + r;
-        if (valid) {
-            p.part_m[at] = st.m;
-            p.part_l[at] = st.l;
-        }
-#pragma unroll 1
-        for (int x = 0; x < D; x += 32) {
-            float v[32];
-            columns(x, v);
-            if (valid) {
-#pragma unroll
-                for (int y = 0; y < 32; y += 4)
-                    *reinterpret_cast<float4*>(p.part_acc + at * D + x + y) = make_float4(v[y], v[y + 1], v[y + 2], v[y + 3]);
-            }
-        }
-        return;
-    }
+    const long long part = static_cast<long long>(w.part) * p.rows_per_item + r;
     uint16_t* out = p.out + ((static_cast<long long>(w.b) * p.n + i) * p.num_q_heads + w.h * p.group_q + g) * D;
-    if (!ROT || !p.rotate_out) {
+    if (!ROT || !p.rotate_out || p.n_splits > 1) {
+        if (!mine) return;
+        if (p.n_splits > 1 && valid && half == 0) {
+            p.part_m[part] = m;
+            p.part_l[part] = l;
+        }
 #pragma unroll 1
-        for (int x = 0; x < D; x += 32) {
-            float v[32];
+        for (int x = half * (D / 2); x < (half + 1) * (D / 2); x += 16) {
+            float v[16];
             columns(x, v);
-            if (valid) {
+            if (!valid) continue;
+            if (p.n_splits > 1) {
 #pragma unroll
-                for (int y = 0; y < 32; y += 8) {
+                for (int y = 0; y < 16; y += 4) *reinterpret_cast<float4*>(p.part_acc + part * D + x + y) = make_float4(v[y], v[y + 1], v[y + 2], v[y + 3]);
+            } else {
+#pragma unroll
+                for (int y = 0; y < 16; y += 8) {
                     uint4 o;
                     floats_to_halves<8>(*reinterpret_cast<float(*)[8]>(v + y), &o);
                     *reinterpret_cast<uint4*>(out + x + y) = o;
@@ -724,101 +754,28 @@ __device__ __forceinline__ void write_row(const ChunkParams& p, const Work& w, u
         }
         return;
     }
-    constexpr int N = D < 128 ? D : 128;
-    for (int half = 0; half < D / N; ++half) {
-        float v[N];
-#pragma unroll
-        for (int x = 0; x < N; x += 32) {
-            columns(x, *reinterpret_cast<float(*)[32]>(v + x));
-            if (D == 256) {
-                float y[32];
-                columns(128 + x, y);
-#pragma unroll
-                for (int k = 0; k < 32; ++k) v[x + k] = half ? v[x + k] - y[k] : v[x + k] + y[k];
-            }
-        }
-        hadamard_thread<N>(v);
-        if (valid) {
-#pragma unroll
-            for (int y = 0; y < N; y += 8) {
-                float x[8];
-#pragma unroll
-                for (int k = 0; k < 8; ++k) x[k] = v[y + k] * p.rot_scale;
-                uint4 o;
-                floats_to_halves<8>(x, &o);
-                *reinterpret_cast<uint4*>(out + half * N + y) = o;
-            }
-        }
-    }
-}
-
-template <int D, int BITS, bool ROT>
-__device__ __forceinline__ void softmax_role(const ChunkParams& p, const Work& w, uint8_t* qs, uint8_t* slots, uint32_t bars, int stream, bool pair) {
-    using C = Cfg<D, BITS>;
-    const int row = threadIdx.x & 127, lane = threadIdx.x & 31;
-    const int tile_row0 = pair ? stream * kRowTile : 0;
-    const int r = tile_row0 + row;  // row of the item
-    const bool valid = r < w.rows;
-    const bool active = __any_sync(0xffffffffu, valid);
-    if (pair || stream == 0) {
-        uint8_t* tile = qs + (pair ? stream : 0) * (kRowTile * D * 2);
-        if (ROT && p.rotate_q)
-            load_query_rotated<D, BITS>(p, w, tile, row, tile_row0);
-        else
-            load_query<D, BITS>(p, w, tile, row, tile_row0);
-    }
-    fence_proxy_async_shared();
-    __syncwarp();
-    if (lane == 0) arrive(bars + kQFull);
-    const int i = (w.row0 + (valid ? r : 0)) / p.group_q;
-    // (rows behind the last are zeros that see everything: they ask for no masks)
-    const int lo = valid ? first_key(p, i, w.ql, w.len) : 0, hi = valid ? end_key(p, i, w.ql, w.len) : 0x7fffffff;
-    const uint32_t tmem = fixed(lds32(bars + kTmemAt));
-    State st{-INFINITY, 0.f};
-    const bool done = softmax_loop<D, BITS>(p, w, bars, tmem, stream, pair, active, lo, hi, st);
-    const bool split_keys = !pair && C::kStreams == 2;
-    // the last of this accumulator's products
-    const int turns = pair ? 2 * w.tiles : w.tiles, last = C::kStreams == 1 ? turns - 1 : ((turns - 1 - stream) & ~1) + stream;
-    bool ok = done;
-    if (ok && turns > stream) {
-        ok = wait(bars, kPvDone + (last & 1) * 8, (last >> 1) & 1, p.status);
-        tc_fence_after();
-    }
-    const uint32_t oa = tmem + (static_cast<uint32_t>((threadIdx.x >> 5) & 3) << 21) + C::kO + (C::kStreams == 2 ? stream * D : 0);
-    if (split_keys) {
-        // the second half's state through shared memory (the operands' place: no product is left that reads them)
-        float* buf = reinterpret_cast<float*>(slots);  // [D][128], then m and l
-        asm volatile("bar.sync 1, 256;" ::: "memory");
-        if (stream == 1 && ok && active) {
+    // Values stored rotated: the rows through shared memory, then a warp a row.
+    float* rows = reinterpret_cast<float*>(qs) + (pair ? stream : 0) * (D * kPad);
+    if (mine) {
 #pragma unroll 1
-            for (int x = 0; x < D && turns > 1; x += 32) {
-                float o[32];
-                tmem_ld32(oa + x, o);
-                tmem_wait_ld();
+        for (int x = half * (D / 2); x < (half + 1) * (D / 2); x += 16) {
+            float v[16];
+            columns(x, v);
 #pragma unroll
-                for (int y = 0; y < 32; ++y) buf[(x + y) * kRowTile + row] = o[y];
-            }
-            buf[D * kRowTile + row] = st.m;
-            buf[(D + 1) * kRowTile + row] = st.l;
+            for (int y = 0; y < 16; ++y) rows[(x + y) * kPad + row] = v[y];
         }
-        asm volatile("bar.sync 1, 256;" ::: "memory");
-        if (stream == 1 || !ok || !active) return;
-        const bool both = w.tiles > 1;
-        const float m1 = both ? buf[D * kRowTile + row] : -INFINITY, l1 = both ? buf[(D + 1) * kRowTile + row] : 0.f;
-        const float m = fmaxf(st.m, m1);
-        float f = st.m == -INFINITY ? 0.f : ex2_approx(st.m - m), fo = m1 == -INFINITY ? 0.f : ex2_approx(m1 - m);
-        State sum{m, st.l * f + l1 * fo};
-        if (p.n_splits == 1) {
-            const float inv = sum.l > 0.f || sum.l != sum.l ? 1.f / sum.l : 0.f;
-            f *= inv;
-            fo *= inv;
-        }
-        write_row<D, BITS, ROT>(p, w, oa, w.tiles > 0, valid, r, sum, f, both ? buf + row : nullptr, fo);
-        return;
     }
-    if (!ok || !active) return;
-    const float f = p.n_splits > 1 ? 1.f : (st.l > 0.f || st.l != st.l ? 1.f / st.l : 0.f);
-    write_row<D, BITS, ROT>(p, w, oa, w.tiles > 0, valid, r, st, f, nullptr, 0.f);
+    asm volatile("barrier.cta.sync 9, %0;" ::"n"(C::kSoftmax) : "memory");
+    if (!ok || (!pair && stream == 1)) return;
+    constexpr int E = D / 32;
+    for (int at = (threadIdx.x & 255) >> 5; at < kRowTile && tile_row0 + at < w.rows; at += 8) {
+        float v[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[e] = rows[(lane * E + e) * kPad + at];
+        hadamard_warp<E>(v, lane, p.rot_scale);
+        const int fl = w.row0 + tile_row0 + at, ti = fl / p.group_q, tg = fl - ti * p.group_q;
+        floats_to_halves<E>(v, p.out + ((static_cast<long long>(w.b) * p.n + ti) * p.num_q_heads + w.h * p.group_q + tg) * D + lane * E);
+    }
 }
 
 // ------------------------------------------------------------------- kernel --
@@ -837,9 +794,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     Work w;
     if (!find_work<C::kTile>(p, p.rows_per_item, w)) return;  // the whole CTA
     const int warp = threadIdx.x >> 5;
-    if (warp == 16) {
+    if (warp == 24) {
         tmem_alloc(&bars.tmem, 512);
-    } else if (threadIdx.x == 17 * 32) {
+    } else if (threadIdx.x == 25 * 32) {
         for (int i = 0; i < 6; ++i) {
             mbar_init(&bars.ring_full[i], 1);
             mbar_init(&bars.ring_empty[i], C::kUnpackWarps);
@@ -848,48 +805,48 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bars.s_full[i], 1);
-            mbar_init(&bars.p_full[i], 4);
-            mbar_init(&bars.s_free[i], 4);
+            mbar_init(&bars.p_full[i], 8);
+            mbar_init(&bars.s_free[i], 8);
             mbar_init(&bars.pv_done[i], 1);
             mbar_init(&bars.drain[i], 1);
         }
-        mbar_init(&bars.q_full, C::kStreams * 4);
+        mbar_init(&bars.q_full, C::kStreams * 8);
         bars.abort = 0;
         fence_mbarrier_init();
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    // registers: 640 x 96 at launch; 256 x 160 + 256 x 64 + 128 x 32 (one
-    // accumulator: 128 x 200 + 128 x 32 + 256 x 64 + 128 x 32)
-    if (warp < C::kStreams * 4) {
-        regs_raise<C::kStreams == 2 ? 160 : 200>();
-        softmax_role<D, BITS, ROT>(p, w, qs, slots, fixed(smem_u32(&bars)), warp >> 2, pair);
-    } else if (warp < 8) {
-        regs_lower<32>();
+    // registers: 896 x 72 at launch; 512 x 88 + 256 x 56 + 128 x 40 (one
+    // accumulator: 256 x 128 + 256 x 24 + 256 x 56 + 128 x 40)
+    if (warp < C::kSoftmax / 32) {
+        regs_raise<C::kStreams == 2 ? 88 : 128>();
+        softmax_role<D, BITS, ROT>(p, w, qs, slots, fixed(smem_u32(&bars)), &bars, warp >> 3, pair);
     } else if (warp < 16) {
-        regs_lower<64>();
+        regs_lower<24>();
+    } else if (warp < 24) {
+        regs_lower<56>();
         unpack_role<D, BITS>(p, w, fixed(smem_u32(ring)), fixed(smem_u32(slots)), fixed(smem_u32(&bars)));
     } else {
-        regs_lower<32>();
-        if (warp == 16 || warp == 18) {
+        regs_lower<40>();
+        if (warp == 24 || warp == 26) {
             const uint32_t at = fixed(smem_u32(&bars)), in = fixed(smem_u32(slots));
-            if (!(warp == 16 ? scores_role<D, BITS>(p, w, fixed(smem_u32(qs)), in, at, pair) : outputs_role<D, BITS>(p, w, in, at, pair))) {
+            if (!(warp == 24 ? scores_role<D, BITS>(p, w, fixed(smem_u32(qs)), in, at, pair) : outputs_role<D, BITS>(p, w, in, at, pair))) {
                 __syncwarp();
-                const uint32_t bar = at + kDrain + (warp == 18 ? 8 : 0);
+                const uint32_t bar = at + kDrain + (warp == 26 ? 8 : 0);
                 if (elect_one()) tc_commit(bar);  // given up: products in flight end before the CTA leaves
                 __syncwarp();
                 for (int it = 0; it < 1 << 20 && !over(bar, 0); ++it) {
                 }
             }
-        } else if (threadIdx.x == 17 * 32) {
+        } else if (threadIdx.x == 25 * 32) {
             load_role<D, BITS>(p, w, ring, &bars);
         }
         __syncwarp();
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 16) {
+    if (warp == 24) {
         tc_fence_after();
         tmem_free(bars.tmem, 512);
     }
