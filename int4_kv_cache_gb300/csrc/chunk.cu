@@ -107,9 +107,16 @@ __device__ __forceinline__ void arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
+// Token and head of row `flat` of a (sequence, kv head): flat / group_q (rows fewer than 2^28 * 8).
+__device__ __forceinline__ void row_of(const ChunkParams& p, int flat, int& i, int& g) {
+    i = p.group_magic == 0 ? flat : static_cast<int>(__umulhi(static_cast<unsigned>(flat), p.group_magic) >> p.group_shift);
+    g = flat - i * p.group_q;
+}
+
 // What a CTA works on.
 struct Work {
-    int b, h, part;         // part: (item, split), where partial states go
+    int b, h;
+    int part;               // where partial states go (-1: the output is written)
     int row0, rows;         // first row, valid rows from it on (up to kStreams * 128)
     int ql, len;
     int klo, khi;           // the keys that any of the rows sees
@@ -128,16 +135,20 @@ __device__ __forceinline__ int end_key(const ChunkParams& p, int i, int ql, int 
 
 template <int TILE>
 __device__ __forceinline__ bool find_work(const ChunkParams& p, int rows_per_item, Work& w) {
-    // the last rows' items first: in causal order they see the most keys
-    int id = blockIdx.x;
-    const int per = p.batch * p.num_kv_heads * p.n_splits;
-    const int m = p.m_items - 1 - id / per;
-    id %= per;
-    const int split = id % p.n_splits;
-    const int bh = id / p.n_splits;
-    w.h = bh % p.num_kv_heads;
+    // The last rows' items first (in causal order they see the most keys), the first
+    // p.whole of them whole, the others in n_splits runs.
+    int id = blockIdx.x, split = 0, splits = 1;
+    w.part = -1;
+    if (id >= p.whole) {
+        w.part = id - p.whole;
+        id = p.whole + w.part / p.n_splits;
+        split = w.part - (id - p.whole) * p.n_splits;
+        splits = p.n_splits;
+        if (splits == 1) w.part = -1;
+    }
+    const int per = p.batch * p.num_kv_heads, above = id / per, bh = id - above * per, m = p.m_items - 1 - above;
     w.b = bh / p.num_kv_heads;
-    w.part = (bh * p.m_items + m) * p.n_splits + split;
+    w.h = bh - w.b * p.num_kv_heads;
     int len = p.seq_lens[w.b], ql = p.q_lens != nullptr ? p.q_lens[w.b] : p.n;
     if (len < 0 || len > p.max_seq_len || ql < 0 || ql > p.n) {
         if (p.status != nullptr && threadIdx.x == 0) atomicOr(p.status, TQ_DEV_SEQ_LEN);
@@ -149,12 +160,15 @@ __device__ __forceinline__ bool find_work(const ChunkParams& p, int rows_per_ite
     w.row0 = m * rows_per_item;
     w.rows = min(rows_per_item, ql * p.group_q - w.row0);
     if (w.rows <= 0) return false;
-    w.klo = first_key(p, w.row0 / p.group_q, ql, len);
-    w.khi = end_key(p, (w.row0 + w.rows - 1) / p.group_q, ql, len);
+    int i0, i1, g;
+    row_of(p, w.row0, i0, g);
+    row_of(p, w.row0 + w.rows - 1, i1, g);
+    w.klo = first_key(p, i0, ql, len);
+    w.khi = end_key(p, i1, ql, len);
     w.tile0 = w.klo / TILE;
     const int all = w.khi > w.klo ? (w.khi + TILE - 1) / TILE - w.tile0 : 0;
-    const int t0 = static_cast<int>(static_cast<long long>(all) * split / p.n_splits);
-    w.tiles = static_cast<int>(static_cast<long long>(all) * (split + 1) / p.n_splits) - t0;
+    const int t0 = static_cast<int>(static_cast<long long>(all) * split / splits);
+    w.tiles = static_cast<int>(static_cast<long long>(all) * (split + 1) / splits) - t0;
     w.tile0 += t0;
     return true;
 }
@@ -493,20 +507,32 @@ __device__ __forceinline__ constexpr int place(int c) {
 // 16 bytes a thread, rows behind the last as zeros.
 template <int D, int BITS>
 __device__ __forceinline__ void load_query(const ChunkParams& p, const Work& w, uint8_t* tile, int tid, int tile_row0) {
-    constexpr int kPieces = D / 8;  // 16-byte pieces of a row: eight channels
-    const int u = tid % kPieces;
+    constexpr int kPieces = D / 8;       // 16-byte pieces of a row: eight channels
+    constexpr int kRows = 32 / kPieces;  // rows that a warp loads at a time
+    const int lane = tid & 31, u = lane % kPieces, row0 = (tid >> 5) * 16;
+    // lane l finds the warp's row l
+    const int r = tile_row0 + row0 + (lane & 15);
+    long long from = -1;
+    if (r < w.rows) {
+        int i, g;
+        row_of(p, w.row0 + r, i, g);
+        from = (w.h * p.group_q + g) * p.stride_h + i * p.stride_t;
+    }
+    const uint16_t* base = p.q + w.b * p.stride_b;
+    uint4 x[16 / kRows];
 #pragma unroll
-    for (int it = 0; it < kPieces / 2; ++it) {
-        const int at = it * (256 / kPieces) + tid / kPieces, r = tile_row0 + at;
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (r < w.rows) {
-            const int flat = w.row0 + r, i = flat / p.group_q, g = flat - i * p.group_q;
-            x = __ldg(reinterpret_cast<const uint4*>(p.q + w.b * p.stride_b + (w.h * p.group_q + g) * p.stride_h + i * p.stride_t) + u);
-        }
-        if (p.negate_q) x.x ^= 0x80008000u, x.y ^= 0x80008000u, x.z ^= 0x80008000u, x.w ^= 0x80008000u;
+    for (int it = 0; it < 16 / kRows; ++it) {
+        const long long at = __shfl_sync(0xffffffffu, from, it * kRows + lane / kPieces);
+        x[it] = at >= 0 ? __ldg(reinterpret_cast<const uint4*>(base + at) + u) : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int it = 0; it < 16 / kRows; ++it) {
+        const int at = row0 + it * kRows + lane / kPieces;
+        uint4 y = x[it];
+        if (p.negate_q) y.x ^= 0x80008000u, y.y ^= 0x80008000u, y.z ^= 0x80008000u, y.w ^= 0x80008000u;
         if (BITS == 4)
-            x = make_uint4(__byte_perm(x.x, x.z, 0x5410), __byte_perm(x.x, x.z, 0x7632), __byte_perm(x.y, x.w, 0x5410), __byte_perm(x.y, x.w, 0x7632));
-        *reinterpret_cast<uint4*>(tile + (u / 8) * (kRowTile * 128) + at * 128 + (((u % 8) ^ (at & 7)) << 4)) = x;
+            y = make_uint4(__byte_perm(y.x, y.z, 0x5410), __byte_perm(y.x, y.z, 0x7632), __byte_perm(y.y, y.w, 0x5410), __byte_perm(y.y, y.w, 0x7632));
+        *reinterpret_cast<uint4*>(tile + (u / 8) * (kRowTile * 128) + at * 128 + (((u % 8) ^ (at & 7)) << 4)) = y;
     }
 }
 
@@ -519,7 +545,8 @@ __device__ __forceinline__ void load_query_rotated(const ChunkParams& p, const W
         const int r = tile_row0 + at;
         float v[E] = {};
         if (r < w.rows) {
-            const int flat = w.row0 + r, i = flat / p.group_q, g = flat - i * p.group_q;
+            int i, g;
+            row_of(p, w.row0 + r, i, g);
             halves_to_floats<E>(p.q + w.b * p.stride_b + (w.h * p.group_q + g) * p.stride_h + i * p.stride_t + lane * E, v);
             hadamard_warp<E>(v, lane, p.rot_scale);
         }
@@ -665,7 +692,8 @@ __device__ __forceinline__ void softmax_role(const ChunkParams& p, const Work& w
     fence_proxy_async_shared();
     __syncwarp();
     if (lane == 0) arrive(bars + kQFull);
-    const int flat = w.row0 + (valid ? r : 0), i = flat / p.group_q, g = flat - i * p.group_q;
+    int i, g;
+    row_of(p, w.row0 + (valid ? r : 0), i, g);
     // (rows behind the last are zeros that see everything: they ask for no masks)
     const int lo = valid ? first_key(p, i, w.ql, w.len) : 0, hi = valid ? end_key(p, i, w.ql, w.len) : 0x7fffffff;
     const uint32_t tmem = fixed(lds32(bars + kTmemAt));
@@ -686,7 +714,7 @@ __device__ __forceinline__ void softmax_role(const ChunkParams& p, const Work& w
     if (merge && stream == 1 && half == 0) shared->max[row] = st.m;
     asm volatile("barrier.cta.sync 9, %0;" ::"n"(C::kSoftmax) : "memory");
     float l = shared->sum[stream][0][row] + shared->sum[stream][1][row];
-    float* apart = reinterpret_cast<float*>(qs);  // [D][129]
+    float* apart = reinterpret_cast<float*>(qs);  // [D][129] of the second accumulator
     constexpr int kPad = kRowTile + 1;
     float f = 1.f, fo = 0.f, m = st.m;
     if (merge) {
@@ -708,7 +736,7 @@ __device__ __forceinline__ void softmax_role(const ChunkParams& p, const Work& w
         l = l * f + l1 * fo;
     }
     const bool mine = (pair || stream == 0) && ok && active;
-    if (p.n_splits == 1) {
+    if (w.part < 0) {
         const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
         f *= inv;
         fo *= inv;
@@ -727,30 +755,39 @@ __device__ __forceinline__ void softmax_role(const ChunkParams& p, const Work& w
             if (merge) v[y] += apart[(x + at) * kPad + row] * fo;
         }
     };
-    const long long part = static_cast<long long>(w.part) * p.rows_per_item + r;
-    uint16_t* out = p.out + ((static_cast<long long>(w.b) * p.n + i) * p.num_q_heads + w.h * p.group_q + g) * D;
-    if (!ROT || !p.rotate_out || p.n_splits > 1) {
-        if (!mine) return;
-        if (p.n_splits > 1 && valid && half == 0) {
-            p.part_m[part] = m;
-            p.part_l[part] = l;
-        }
+    if (!ROT || !p.rotate_out || w.part >= 0) {
+        // Rows to shared memory (16 bytes apart from what would be the same banks), then
+        // each to its place as one bulk copy: a thread's own stores, 16 bytes in each
+        // of 32 rows at a time, took 10,000 cycles.
+        const uint32_t stride = w.part >= 0 ? D * 4 + 16 : D * 2 + 16;
+        uint8_t* to = (merge ? slots + C::kSlots * C::kSlot - kRowTile * (D * 4 + 16) : qs) + r * stride;
+        if (merge) asm volatile("" ::: "memory");
+        if (mine) {
 #pragma unroll 1
-        for (int x = half * (D / 2); x < (half + 1) * (D / 2); x += 16) {
-            float v[16];
-            columns(x, v);
-            if (!valid) continue;
-            if (p.n_splits > 1) {
+            for (int x = half * (D / 2); x < (half + 1) * (D / 2); x += 16) {
+                float v[16];
+                columns(x, v);
+                if (w.part >= 0) {
 #pragma unroll
-                for (int y = 0; y < 16; y += 4) *reinterpret_cast<float4*>(p.part_acc + part * D + x + y) = make_float4(v[y], v[y + 1], v[y + 2], v[y + 3]);
-            } else {
+                    for (int y = 0; y < 16; y += 4) *reinterpret_cast<float4*>(to + (x + y) * 4) = make_float4(v[y], v[y + 1], v[y + 2], v[y + 3]);
+                } else {
 #pragma unroll
-                for (int y = 0; y < 16; y += 8) {
-                    uint4 o;
-                    floats_to_halves<8>(*reinterpret_cast<float(*)[8]>(v + y), &o);
-                    *reinterpret_cast<uint4*>(out + x + y) = o;
+                    for (int y = 0; y < 16; y += 8) floats_to_halves<8>(*reinterpret_cast<float(*)[8]>(v + y), to + (x + y) * 2);
                 }
             }
+        }
+        fence_proxy_async_shared();
+        asm volatile("barrier.cta.sync 9, %0;" ::"n"(C::kSoftmax) : "memory");
+        if (mine && valid && half == 0) {
+            const long long part = static_cast<long long>(w.part) * p.rows_per_item + r;
+            void* dst = p.out + ((static_cast<long long>(w.b) * p.n + i) * p.num_q_heads + w.h * p.group_q + g) * D;
+            if (w.part >= 0) {
+                p.part_m[part] = m;
+                p.part_l[part] = l;
+                dst = p.part_acc + part * D;
+            }
+            bulk_store(dst, to, stride - 16);
+            bulk_store_wait();
         }
         return;
     }
@@ -773,7 +810,8 @@ __device__ __forceinline__ void softmax_role(const ChunkParams& p, const Work& w
 #pragma unroll
         for (int e = 0; e < E; ++e) v[e] = rows[(lane * E + e) * kPad + at];
         hadamard_warp<E>(v, lane, p.rot_scale);
-        const int fl = w.row0 + tile_row0 + at, ti = fl / p.group_q, tg = fl - ti * p.group_q;
+        int ti, tg;
+        row_of(p, w.row0 + tile_row0 + at, ti, tg);
         floats_to_halves<E>(v, p.out + ((static_cast<long long>(w.b) * p.n + ti) * p.num_q_heads + w.h * p.group_q + tg) * D + lane * E);
     }
 }
@@ -861,14 +899,17 @@ __global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const __grid
     constexpr int E = D / 32;
     const int lane = threadIdx.x & 31;
     const long long wid = static_cast<long long>(blockIdx.x) * (kMergeThreads / 32) + (threadIdx.x >> 5);
-    const int per = p.n * p.group_q;  // rows of a (sequence, kv head)
-    const int bh = static_cast<int>(wid / per), flat = static_cast<int>(wid - static_cast<long long>(bh) * per);
-    if (bh >= p.batch * p.num_kv_heads) return;
-    const int b = bh / p.num_kv_heads, h = bh - b * p.num_kv_heads, i = flat / p.group_q, g = flat - i * p.group_q;
+    // row r of the item-th split item
+    const int item = static_cast<int>(wid / p.rows_per_item), r = static_cast<int>(wid - static_cast<long long>(item) * p.rows_per_item);
+    const int id = p.whole + item, all = p.batch * p.num_kv_heads;
+    if (id >= all * p.m_items) return;
+    const int above = id / all, bh = id - above * all, b = bh / p.num_kv_heads, h = bh - b * p.num_kv_heads;
+    const int flat = (p.m_items - 1 - above) * p.rows_per_item + r;
+    int i, g;
+    row_of(p, flat, i, g);
     const int ql = p.q_lens != nullptr ? min(max(p.q_lens[b], 0), p.n) : p.n;
     if (i >= ql) return;
-    const int m = flat / p.rows_per_item, r = flat - m * p.rows_per_item;
-    const long long part0 = (static_cast<long long>(bh) * p.m_items + m) * p.n_splits;
+    const long long part0 = static_cast<long long>(item) * p.n_splits;
     float top = -INFINITY;
     for (int s = lane; s < p.n_splits; s += 32) top = fmaxf(top, p.part_m[(part0 + s) * p.rows_per_item + r]);
 #pragma unroll
@@ -906,18 +947,18 @@ cudaError_t launch_main(const ChunkParams& p, cudaStream_t stream) {
     using C = Cfg<D, BITS>;
     cudaError_t e = cudaFuncSetAttribute(chunk_kernel<D, BITS, ROT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
-    const long long ctas = static_cast<long long>(p.batch) * p.num_kv_heads * p.m_items * p.n_splits;
+    const long long ctas = p.whole + (static_cast<long long>(p.batch) * p.num_kv_heads * p.m_items - p.whole) * p.n_splits;
     chunk_kernel<D, BITS, ROT><<<static_cast<unsigned>(ctas), kThreads, C::kSmem, stream>>>(p);
     return cudaGetLastError();
 }
 
 template <int D>
 cudaError_t launch_dim(const ChunkParams& p, cudaStream_t stream) {
-    const bool rot = p.rotate_q || (p.rotate_out && p.n_splits == 1);
+    const bool rot = p.rotate_q || (p.rotate_out && (p.n_splits == 1 || p.whole > 0));
     cudaError_t e = p.bits == 8 ? (rot ? launch_main<D, 8, true>(p, stream) : launch_main<D, 8, false>(p, stream))
                                 : (rot ? launch_main<D, 4, true>(p, stream) : launch_main<D, 4, false>(p, stream));
     if (e != cudaSuccess || p.n_splits == 1) return e;
-    const long long rows = static_cast<long long>(p.batch) * p.n * p.num_q_heads, each = kMergeThreads / 32;
+    const long long rows = (static_cast<long long>(p.batch) * p.num_kv_heads * p.m_items - p.whole) * p.rows_per_item, each = kMergeThreads / 32;
     chunk_merge_kernel<D><<<static_cast<unsigned>((rows + each - 1) / each), kMergeThreads, 0, stream>>>(p);
     return cudaGetLastError();
 }

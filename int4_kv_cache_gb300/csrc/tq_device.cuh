@@ -88,6 +88,15 @@ __device__ __forceinline__ void bulk_load(void* smem_dst, const void* gsrc, uint
         : "memory");
 }
 
+// 1-D bulk copy shared -> global (16-byte aligned addresses, size % 16 == 0), and
+// the wait of the thread that issued it until it has been read from shared memory.
+__device__ __forceinline__ void bulk_store(void* gdst, const void* smem_src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(gdst), "r"(smem_u32(smem_src)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void bulk_store_wait() {
+    asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group.read 0;" ::: "memory");
+}
+
 // 16 bytes global -> shared (both 16-byte aligned), asynchronous; copies are
 // waited for in committed groups, each thread for its own: until at most N of
 // its newest groups are outstanding.

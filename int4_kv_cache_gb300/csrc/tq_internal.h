@@ -329,10 +329,13 @@ struct ChunkParams {
     float rot_scale;
     RowMap map;
     // The rows of a (sequence, kv head), n * group_q, are cut into m_items items of
-    // rows_per_item rows, each item's keys into n_splits runs.
-    int32_t m_items, rows_per_item, n_splits;
+    // rows_per_item rows; in the order they are taken, the first `whole` items have a CTA
+    // each and the others one for each of n_splits runs of their keys.
+    int32_t m_items, rows_per_item, n_splits, whole;
+    uint32_t group_magic;     // floor(t / group_q) = umulhi(t, magic) >> shift for 0 <= t < 2^31 (0: group_q = 1)
+    int32_t group_shift;
     int32_t pair;             // an item is two tiles of 128 rows (else one)
-    float* part_m;            // [items * n_splits][rows_per_item], log2 units (n_splits > 1)
+    float* part_m;            // [(items - whole) * n_splits][rows_per_item], log2 units (n_splits > 1)
     float* part_l;
     float* part_acc;          // [items * n_splits][rows_per_item][D]
 };

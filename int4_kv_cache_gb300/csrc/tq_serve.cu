@@ -33,18 +33,30 @@ size_t chunk_bytes(int32_t batch, int32_t hq, int32_t hkv, int32_t head_dim, int
     return 2 * align256(rows * sizeof(float)) + align256(rows * head_dim * sizeof(float));
 }
 
-// How many runs the keys of each item are cut into: the fewest CTA-times, in
-// tiles, with what a CTA costs beside its tiles (start, first copies, output: some
-// four tiles' time) and what merging costs (a launch, the parts' way through memory).
-int chunk_splits(long long items, int tiles, int sms) {
-    int best = 1;
+// Items with a CTA each, and how many runs the keys of each of the others are cut into.
+// Times in tiles: a CTA costs its tiles and some four more (start, first copies,
+// output), merging a launch and the parts' way through memory.  Either all items are
+// cut, or those that are left behind the last full wave of whole ones: 512 items of 508
+// tiles on 152 SMs take 3 whole waves and the rest of their time in an eighth of
+// another one, where a fourth whole wave would leave most SMs idle.
+struct ChunkPlan {
+    long long whole;
+    int splits;
+};
+
+ChunkPlan chunk_plan(long long items, int tiles, int sms) {
+    ChunkPlan best{0, 1};
     long long cost = -1;
-    for (int n = 1; n <= tiles && (n == 1 || items * n <= kMaxChunkParts); ++n) {
-        const long long waves = (items * n + sms - 1) / sms;
-        const long long c = waves * ((tiles + n - 1) / n + 4) + (n > 1 ? 4 + n / 8 : 0);
-        if (cost < 0 || c < cost) {
-            cost = c;
-            best = n;
+    for (int full = 0; full < 2; ++full) {
+        const long long whole = full ? items / sms * sms : 0, rest = items - whole;
+        if (full && (whole == 0 || rest == 0)) continue;
+        for (int n = 1; n <= tiles && (n == 1 || rest * n <= kMaxChunkParts); ++n) {
+            const long long waves = (rest * n + sms - 1) / sms;
+            const long long c = whole / sms * (tiles + 4) + waves * ((tiles + n - 1) / n + 4) + (n > 1 ? 4 + n / 8 : 0);
+            if (cost < 0 || c < cost) {
+                cost = c;
+                best = {whole, n};
+            }
         }
     }
     return best;
@@ -119,8 +131,15 @@ tq_status chunk(const Store& c, const tq_query_rows* q, const int32_t* q_lens, c
     // the most keys an item sees: all of them, or a window behind each of its tokens
     long long keys = max_seq_len;
     if (window > 0 && window + static_cast<long long>(p.rows_per_item / p.group_q) + 1 < keys) keys = window + p.rows_per_item / p.group_q + 1;
-    p.n_splits = chunk_splits(items, ceil_div(keys, tile), f->sms);
-    if (items * p.n_splits >= (1LL << 31)) return TQ_ERR_SHAPE;
+    if (items >= (1LL << 30)) return TQ_ERR_SHAPE;
+    const ChunkPlan pl = chunk_plan(items, ceil_div(keys, tile), f->sms);
+    p.n_splits = pl.splits;
+    p.whole = pl.splits == 1 ? 0 : static_cast<int32_t>(pl.whole);
+    if (p.group_q > 1) {
+        const RowMap d = with_page_divisor({nullptr, p.group_q, 0, 0, 0, 0});
+        p.group_magic = d.page_magic;
+        p.group_shift = d.page_shift;
+    }
     const size_t part_rows = chunk_part_rows(c.batch, q->num_heads, c.num_kv_heads, c.head_dim, q->n, max_seq_len);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     p.part_m = reinterpret_cast<float*>(ws);
