@@ -15,7 +15,7 @@
 //                     128-byte rows with the 128-byte swizzle: keys are then a
 //                     K-major operand and values an N-major one, in the same layout
 //   MMA warps         S = Q K^T and O += P V, S, P and O in TMEM (P in S's place)
-//   softmax warps     two threads a row: maximum, 2^x, P as fp16, sum; no shuffles
+//   softmax warps     a thread a row: maximum, 2^x, P as fp16, sum; no shuffles
 // The two row tiles take turns: while one's softmax runs the tensor core works for
 // the other.  Up to 128 rows (a few tokens) make one tile; the two halves then take
 // every other tile of keys and are merged in the end.  O is rescaled only when a
@@ -35,7 +35,7 @@ namespace tq {
 
 namespace {
 
-constexpr int kThreads = 896;       // 16 softmax warps, 8 that unpack, 2 that issue products, one that copies
+constexpr int kThreads = 640;       // 8 softmax warps, 8 that unpack, 2 that issue products, one that copies
 constexpr int kRowTile = 128;
 constexpr float kLazy = 8.f;  // log2 of how far P may grow before O is rescaled
 
@@ -43,8 +43,8 @@ template <int D, int BITS>
 struct Cfg {
     static constexpr int kStreams = D == 256 ? 1 : 2;         // softmax warpgroups, output accumulators
     static constexpr int kTile = D == 256 ? 64 : 128;         // keys
-    static constexpr int kSoftmax = kStreams * 256;           // softmax threads: two for each row, half of a tile's keys each
-    static constexpr int kUnpackWarp = 16;                    // first unpacking warp
+    static constexpr int kSoftmax = kStreams * 128;           // softmax threads: one for each row
+    static constexpr int kUnpackWarp = 8;                     // first unpacking warp
     static constexpr int kUnpackWarps = 8;
     static constexpr int kBlocks = D / 64;                    // blocks of 64 channels: 128-byte rows
     static constexpr int kSlot = kTile * D * 2;               // one unpacked tile of keys or values
@@ -71,9 +71,7 @@ struct Bars {
     uint64_t s_full[2], s_free[2], p_full[2], pv_done[2], q_full, drain[2];
     uint32_t tmem;
     int32_t abort;
-    float top[2][2][kRowTile];  // [accumulator][half of the keys][row]: maxima of a turn
-    float sum[2][2][kRowTile];  // sums in the end
-    float max[kRowTile];        // the second accumulator's maxima
+    float max[kRowTile], sum[kRowTile];  // the second accumulator's, where both are of one row tile
 };
 
 // Addresses of the barriers from that of the first.  (Each role takes the first one's
@@ -503,15 +501,15 @@ __device__ __forceinline__ constexpr int place(int c) {
     return BITS == 4 ? (c & ~7) | ((c & 3) << 1) | ((c >> 2) & 1) : c;
 }
 
-// The 128 rows of a query tile from row tile_row0 of the item on, by 256 threads:
+// The 128 rows of a query tile from row tile_row0 of the item on, by 128 threads:
 // 16 bytes a thread, rows behind the last as zeros.
 template <int D, int BITS>
 __device__ __forceinline__ void load_query(const ChunkParams& p, const Work& w, uint8_t* tile, int tid, int tile_row0) {
     constexpr int kPieces = D / 8;       // 16-byte pieces of a row: eight channels
     constexpr int kRows = 32 / kPieces;  // rows that a warp loads at a time
-    const int lane = tid & 31, u = lane % kPieces, row0 = (tid >> 5) * 16;
+    const int lane = tid & 31, u = lane % kPieces, row0 = (tid >> 5) * 32;
     // lane l finds the warp's row l
-    const int r = tile_row0 + row0 + (lane & 15);
+    const int r = tile_row0 + row0 + lane;
     long long from = -1;
     if (r < w.rows) {
         int i, g;
@@ -519,20 +517,23 @@ __device__ __forceinline__ void load_query(const ChunkParams& p, const Work& w, 
         from = (w.h * p.group_q + g) * p.stride_h + i * p.stride_t;
     }
     const uint16_t* base = p.q + w.b * p.stride_b;
-    uint4 x[16 / kRows];
+#pragma unroll 1
+    for (int it0 = 0; it0 < 32 / kRows; it0 += 8) {
+        uint4 x[8];
 #pragma unroll
-    for (int it = 0; it < 16 / kRows; ++it) {
-        const long long at = __shfl_sync(0xffffffffu, from, it * kRows + lane / kPieces);
-        x[it] = at >= 0 ? __ldg(reinterpret_cast<const uint4*>(base + at) + u) : make_uint4(0, 0, 0, 0);
-    }
+        for (int it = 0; it < 8; ++it) {
+            const long long at = __shfl_sync(0xffffffffu, from, (it0 + it) * kRows + lane / kPieces);
+            x[it] = at >= 0 ? __ldg(reinterpret_cast<const uint4*>(base + at) + u) : make_uint4(0, 0, 0, 0);
+        }
 #pragma unroll
-    for (int it = 0; it < 16 / kRows; ++it) {
-        const int at = row0 + it * kRows + lane / kPieces;
-        uint4 y = x[it];
-        if (p.negate_q) y.x ^= 0x80008000u, y.y ^= 0x80008000u, y.z ^= 0x80008000u, y.w ^= 0x80008000u;
-        if (BITS == 4)
-            y = make_uint4(__byte_perm(y.x, y.z, 0x5410), __byte_perm(y.x, y.z, 0x7632), __byte_perm(y.y, y.w, 0x5410), __byte_perm(y.y, y.w, 0x7632));
-        *reinterpret_cast<uint4*>(tile + (u / 8) * (kRowTile * 128) + at * 128 + (((u % 8) ^ (at & 7)) << 4)) = y;
+        for (int it = 0; it < 8; ++it) {
+            const int at = row0 + (it0 + it) * kRows + lane / kPieces;
+            uint4 y = x[it];
+            if (p.negate_q) y.x ^= 0x80008000u, y.y ^= 0x80008000u, y.z ^= 0x80008000u, y.w ^= 0x80008000u;
+            if (BITS == 4)
+                y = make_uint4(__byte_perm(y.x, y.z, 0x5410), __byte_perm(y.x, y.z, 0x7632), __byte_perm(y.y, y.w, 0x5410), __byte_perm(y.y, y.w, 0x7632));
+            *reinterpret_cast<uint4*>(tile + (u / 8) * (kRowTile * 128) + at * 128 + (((u % 8) ^ (at & 7)) << 4)) = y;
+        }
     }
 }
 
@@ -541,7 +542,7 @@ template <int D, int BITS>
 __device__ __forceinline__ void load_query_rotated(const ChunkParams& p, const Work& w, uint8_t* tile, int tid, int tile_row0) {
     constexpr int E = D / 32;
     const int lane = tid & 31;
-    for (int at = tid >> 5; at < kRowTile; at += 8) {
+    for (int at = tid >> 5; at < kRowTile; at += 4) {
         const int r = tile_row0 + at;
         float v[E] = {};
         if (r < w.rows) {
@@ -563,28 +564,12 @@ struct State {
     float m, l;  // maximum that P counts from (log2 units, -inf: none yet), sum
 };
 
-// Two warps that have the same 32 rows, one for each half of the keys, meet; whether
-// either has something to tell.
-__device__ __forceinline__ bool either(int id, bool pred) {
-    uint32_t any;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %2, 0;\n\tbarrier.cta.red.or.pred q, %1, 64, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-        : "=r"(any)
-        : "r"(id), "r"(static_cast<uint32_t>(pred))
-        : "memory");
-    return any != 0;
-}
-
-// One accumulator's turns: all, or (two accumulators) those of its parity.  A thread has
-// one half of a row's keys; row maxima are exchanged only where one of the 64 threads
-// of the same 32 rows sees its row outgrow what P counts from.
+// One accumulator's turns: all, or (two accumulators) those of its parity; a thread a row.
 template <int D, int BITS>
-__device__ __forceinline__ bool softmax_loop(const ChunkParams& p, const Work& w, uint32_t bars, Bars* shared, uint32_t tmem0, int stream, int half, bool pair, bool active,
-                                             int lo, int hi, State& st) {
+__device__ __forceinline__ bool softmax_loop(const ChunkParams& p, const Work& w, uint32_t bars, uint32_t tmem, int stream, bool pair, bool active, int lo, int hi, State& st) {
     using C = Cfg<D, BITS>;
-    constexpr int N = C::kTile / 2;
-    const int lane = threadIdx.x & 31, row = threadIdx.x & 127, id = 1 + stream * 4 + ((threadIdx.x >> 5) & 3);
-    const uint32_t tmem = tmem0 + (static_cast<uint32_t>((threadIdx.x >> 5) & 3) << 21);
+    constexpr int N = C::kTile;
+    const int lane = threadIdx.x & 31;
     const float c = p.score_scale_log2;
     const int turns = pair ? 2 * w.tiles : w.tiles;
 #pragma unroll 1
@@ -594,17 +579,16 @@ __device__ __forceinline__ bool softmax_loop(const ChunkParams& p, const Work& w
         tc_fence_after();
         float s[N];
         if (active) {
-            const uint32_t sa = tmem + (C::kPlaces == 2 ? odd * C::kS1 : 0) + half * N;
+            const uint32_t sa = tmem + (C::kPlaces == 2 ? odd * C::kS1 : 0);
 #pragma unroll
             for (int x = 0; x < N; x += 32) tmem_ld32(sa + x, s + x);
-            tmem_wait_ld();
         }
+        if (active) tmem_wait_ld();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) arrive(bars + kSFree + (C::kPlaces == 2 ? odd * 8 : 0));
         if (active) {
-            if (lds32(bars + kAbort) != 0) return false;  // (the other half's warp may have left)
-            const int t0 = (w.tile0 + (pair ? n >> 1 : n)) * C::kTile + half * N;
+            const int t0 = (w.tile0 + (pair ? n >> 1 : n)) * N;
             if (__any_sync(0xffffffffu, t0 < lo || t0 + N > hi)) {
                 const unsigned span = static_cast<unsigned>(hi > lo ? hi - lo : 0);
 #pragma unroll
@@ -613,26 +597,21 @@ __device__ __forceinline__ bool softmax_loop(const ChunkParams& p, const Work& w
             float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
             for (int x = 4; x < N; x += 2) mx[(x >> 1) & 3] = max3(mx[(x >> 1) & 3], s[x], s[x + 1]);
-            float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * c;
+            const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * c;
             const bool fresh = n < C::kStreams;  // nothing in O yet
-            const float limit = fresh ? st.m : st.m + kLazy;
-            if (either(id, top > limit)) {
-                shared->top[stream][half][row] = top;
-                asm volatile("barrier.cta.sync %0, 64;" ::"r"(id) : "memory");
-                top = fmaxf(top, shared->top[stream][half ^ 1][row]);
-                const bool grow = top > limit;
+            const bool grow = top > (fresh ? st.m : st.m + kLazy);
+            if (__any_sync(0xffffffffu, grow)) {
                 const float f = grow ? ex2_approx(st.m - top) : 1.f;
                 if (grow) st.m = top;
                 st.l *= f;
                 if (!fresh) {
-                    // O holds the products of the turns before (each half of the threads rescales
-                    // half of its columns): all of them have to be over
+                    // O holds the products of the turns before: all of them have to be over
                     const uint32_t before = C::kStreams == 1 ? n - 1 : n - 2;
                     if (!wait(bars, kPvDone + (before & 1) * 8, (before >> 1) & 1, p.status)) return false;
                     tc_fence_after();
-                    const uint32_t oa = tmem + C::kO + (C::kStreams == 2 ? stream * D : 0) + half * (D / 2);
+                    const uint32_t oa = tmem + C::kO + (C::kStreams == 2 ? stream * D : 0);
 #pragma unroll 1
-                    for (int x = 0; x < D / 2; x += 16) {
+                    for (int x = 0; x < D; x += 16) {
                         float o[16];
                         tmem_ld16(oa + x, o);
                         tmem_wait_ld();
@@ -649,7 +628,7 @@ __device__ __forceinline__ bool softmax_loop(const ChunkParams& p, const Work& w
             tc_fence_after();
             const float base = st.m == -INFINITY ? 0.f : -st.m;
             float2 sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
-            const uint32_t pa = tmem + C::kP + odd * C::kPStep + half * (N / 2);
+            const uint32_t pa = tmem + C::kP + odd * C::kPStep;
 #pragma unroll
             for (int x = 0; x < N; x += 32) {
                 uint32_t pk[16];
@@ -677,7 +656,7 @@ __device__ __forceinline__ bool softmax_loop(const ChunkParams& p, const Work& w
 template <int D, int BITS, bool ROT>
 __device__ __forceinline__ void softmax_role(const ChunkParams& p, const Work& w, uint8_t* qs, uint8_t* slots, uint32_t bars, Bars* shared, int stream, bool pair) {
     using C = Cfg<D, BITS>;
-    const int row = threadIdx.x & 127, half = (threadIdx.x >> 7) & 1, lane = threadIdx.x & 31;
+    const int row = threadIdx.x & 127, lane = threadIdx.x & 31;
     const int tile_row0 = pair ? stream * kRowTile : 0;
     const int r = tile_row0 + row;  // row of the item
     const bool valid = r < w.rows;
@@ -685,9 +664,9 @@ __device__ __forceinline__ void softmax_role(const ChunkParams& p, const Work& w
     if (pair || stream == 0) {
         uint8_t* tile = qs + (pair ? stream : 0) * (kRowTile * D * 2);
         if (ROT && p.rotate_q)
-            load_query_rotated<D, BITS>(p, w, tile, threadIdx.x & 255, tile_row0);
+            load_query_rotated<D, BITS>(p, w, tile, row, tile_row0);
         else
-            load_query<D, BITS>(p, w, tile, threadIdx.x & 255, tile_row0);
+            load_query<D, BITS>(p, w, tile, row, tile_row0);
     }
     fence_proxy_async_shared();
     __syncwarp();
@@ -696,31 +675,30 @@ __device__ __forceinline__ void softmax_role(const ChunkParams& p, const Work& w
     row_of(p, w.row0 + (valid ? r : 0), i, g);
     // (rows behind the last are zeros that see everything: they ask for no masks)
     const int lo = valid ? first_key(p, i, w.ql, w.len) : 0, hi = valid ? end_key(p, i, w.ql, w.len) : 0x7fffffff;
-    const uint32_t tmem = fixed(lds32(bars + kTmemAt));
+    const uint32_t tmem = fixed(lds32(bars + kTmemAt) + (static_cast<uint32_t>((threadIdx.x >> 5) & 3) << 21));  // the warp's lanes
     State st{-INFINITY, 0.f};
-    bool ok = softmax_loop<D, BITS>(p, w, bars, shared, tmem, stream, half, pair, active, lo, hi, st);
+    bool ok = softmax_loop<D, BITS>(p, w, bars, tmem, stream, pair, active, lo, hi, st);
     // the last of this accumulator's products
     const int turns = pair ? 2 * w.tiles : w.tiles, last = C::kStreams == 1 ? turns - 1 : ((turns - 1 - stream) & ~1) + stream;
     if (ok && turns > stream) {
         ok = wait(bars, kPvDone + (last & 1) * 8, (last >> 1) & 1, p.status);
         tc_fence_after();
     }
-    // Sums of both halves; and where the accumulators are those of one row tile, the
-    // second one's state through shared memory (the operands' place: once all softmax
-    // threads are here no product is left that reads them).
+    // Where both accumulators are those of one row tile, the second one's state through
+    // shared memory (the operands' place: once all softmax threads are here no product
+    // is left that reads them).
     const bool merge = !pair && C::kStreams == 2 && turns > 1;
-    const uint32_t oa = tmem + (static_cast<uint32_t>((threadIdx.x >> 5) & 3) << 21) + C::kO + (C::kStreams == 2 ? stream * D : 0);
-    shared->sum[stream][half][row] = st.l;
-    if (merge && stream == 1 && half == 0) shared->max[row] = st.m;
+    const uint32_t oa = tmem + C::kO + (C::kStreams == 2 ? stream * D : 0);
     asm volatile("barrier.cta.sync 9, %0;" ::"n"(C::kSoftmax) : "memory");
-    float l = shared->sum[stream][0][row] + shared->sum[stream][1][row];
     float* apart = reinterpret_cast<float*>(qs);  // [D][129] of the second accumulator
     constexpr int kPad = kRowTile + 1;
-    float f = 1.f, fo = 0.f, m = st.m;
+    float f = 1.f, fo = 0.f, m = st.m, l = st.l;
     if (merge) {
         if (stream == 1 && ok && active) {
+            shared->max[row] = st.m;
+            shared->sum[row] = st.l;
 #pragma unroll 1
-            for (int x = half * (D / 2); x < (half + 1) * (D / 2); x += 16) {
+            for (int x = 0; x < D; x += 16) {
                 float o[16];
                 tmem_ld16(oa + x, o);
                 tmem_wait_ld();
@@ -729,7 +707,7 @@ __device__ __forceinline__ void softmax_role(const ChunkParams& p, const Work& w
             }
         }
         asm volatile("barrier.cta.sync 9, %0;" ::"n"(C::kSoftmax) : "memory");
-        const float m1 = shared->max[row], l1 = shared->sum[1][0][row] + shared->sum[1][1][row];
+        const float m1 = shared->max[row], l1 = shared->sum[row];
         m = fmaxf(st.m, m1);
         f = st.m == -INFINITY ? 0.f : ex2_approx(st.m - m);
         fo = m1 == -INFINITY ? 0.f : ex2_approx(m1 - m);
@@ -761,10 +739,9 @@ __device__ __forceinline__ void softmax_role(const ChunkParams& p, const Work& w
         // of 32 rows at a time, took 10,000 cycles.
         const uint32_t stride = w.part >= 0 ? D * 4 + 16 : D * 2 + 16;
         uint8_t* to = (merge ? slots + C::kSlots * C::kSlot - kRowTile * (D * 4 + 16) : qs) + r * stride;
-        if (merge) asm volatile("" ::: "memory");
         if (mine) {
 #pragma unroll 1
-            for (int x = half * (D / 2); x < (half + 1) * (D / 2); x += 16) {
+            for (int x = 0; x < D; x += 16) {
                 float v[16];
                 columns(x, v);
                 if (w.part >= 0) {
@@ -778,7 +755,7 @@ __device__ __forceinline__ void softmax_role(const ChunkParams& p, const Work& w
         }
         fence_proxy_async_shared();
         asm volatile("barrier.cta.sync 9, %0;" ::"n"(C::kSoftmax) : "memory");
-        if (mine && valid && half == 0) {
+        if (mine && valid) {
             const long long part = static_cast<long long>(w.part) * p.rows_per_item + r;
             void* dst = p.out + ((static_cast<long long>(w.b) * p.n + i) * p.num_q_heads + w.h * p.group_q + g) * D;
             if (w.part >= 0) {
@@ -795,7 +772,7 @@ __device__ __forceinline__ void softmax_role(const ChunkParams& p, const Work& w
     float* rows = reinterpret_cast<float*>(qs) + (pair ? stream : 0) * (D * kPad);
     if (mine) {
 #pragma unroll 1
-        for (int x = half * (D / 2); x < (half + 1) * (D / 2); x += 16) {
+        for (int x = 0; x < D; x += 16) {
             float v[16];
             columns(x, v);
 #pragma unroll
@@ -805,7 +782,7 @@ __device__ __forceinline__ void softmax_role(const ChunkParams& p, const Work& w
     asm volatile("barrier.cta.sync 9, %0;" ::"n"(C::kSoftmax) : "memory");
     if (!ok || (!pair && stream == 1)) return;
     constexpr int E = D / 32;
-    for (int at = (threadIdx.x & 255) >> 5; at < kRowTile && tile_row0 + at < w.rows; at += 8) {
+    for (int at = row >> 5; at < kRowTile && tile_row0 + at < w.rows; at += 4) {
         float v[E];
 #pragma unroll
         for (int e = 0; e < E; ++e) v[e] = rows[(lane * E + e) * kPad + at];
@@ -832,9 +809,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     Work w;
     if (!find_work<C::kTile>(p, p.rows_per_item, w)) return;  // the whole CTA
     const int warp = threadIdx.x >> 5;
-    if (warp == 24) {
+    if (warp == 16) {
         tmem_alloc(&bars.tmem, 512);
-    } else if (threadIdx.x == 25 * 32) {
+    } else if (threadIdx.x == 17 * 32) {
         for (int i = 0; i < 6; ++i) {
             mbar_init(&bars.ring_full[i], 1);
             mbar_init(&bars.ring_empty[i], C::kUnpackWarps);
@@ -843,48 +820,48 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bars.s_full[i], 1);
-            mbar_init(&bars.p_full[i], 8);
-            mbar_init(&bars.s_free[i], 8);
+            mbar_init(&bars.p_full[i], 4);
+            mbar_init(&bars.s_free[i], 4);
             mbar_init(&bars.pv_done[i], 1);
             mbar_init(&bars.drain[i], 1);
         }
-        mbar_init(&bars.q_full, C::kStreams * 8);
+        mbar_init(&bars.q_full, C::kStreams * 4);
         bars.abort = 0;
         fence_mbarrier_init();
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    // registers: 896 x 72 at launch; 512 x 88 + 256 x 56 + 128 x 40 (one
-    // accumulator: 256 x 128 + 256 x 24 + 256 x 56 + 128 x 40)
+    // registers: 640 x 96 at launch; 256 x 160 + 256 x 64 + 128 x 32 (one
+    // accumulator: 128 x 160 + 128 x 24 + 256 x 64 + 128 x 32)
     if (warp < C::kSoftmax / 32) {
-        regs_raise<C::kStreams == 2 ? 88 : 128>();
-        softmax_role<D, BITS, ROT>(p, w, qs, slots, fixed(smem_u32(&bars)), &bars, warp >> 3, pair);
-    } else if (warp < 16) {
+        regs_raise<160>();
+        softmax_role<D, BITS, ROT>(p, w, qs, slots, fixed(smem_u32(&bars)), &bars, warp >> 2, pair);
+    } else if (warp < 8) {
         regs_lower<24>();
-    } else if (warp < 24) {
-        regs_lower<56>();
+    } else if (warp < 16) {
+        regs_lower<64>();
         unpack_role<D, BITS>(p, w, fixed(smem_u32(ring)), fixed(smem_u32(slots)), fixed(smem_u32(&bars)));
     } else {
-        regs_lower<40>();
-        if (warp == 24 || warp == 26) {
+        regs_lower<32>();
+        if (warp == 16 || warp == 18) {
             const uint32_t at = fixed(smem_u32(&bars)), in = fixed(smem_u32(slots));
-            if (!(warp == 24 ? scores_role<D, BITS>(p, w, fixed(smem_u32(qs)), in, at, pair) : outputs_role<D, BITS>(p, w, in, at, pair))) {
+            if (!(warp == 16 ? scores_role<D, BITS>(p, w, fixed(smem_u32(qs)), in, at, pair) : outputs_role<D, BITS>(p, w, in, at, pair))) {
                 __syncwarp();
-                const uint32_t bar = at + kDrain + (warp == 26 ? 8 : 0);
+                const uint32_t bar = at + kDrain + (warp == 18 ? 8 : 0);
                 if (elect_one()) tc_commit(bar);  // given up: products in flight end before the CTA leaves
                 __syncwarp();
                 for (int it = 0; it < 1 << 20 && !over(bar, 0); ++it) {
                 }
             }
-        } else if (threadIdx.x == 25 * 32) {
+        } else if (threadIdx.x == 17 * 32) {
             load_role<D, BITS>(p, w, ring, &bars);
         }
         __syncwarp();
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 24) {
+    if (warp == 16) {
         tc_fence_after();
         tmem_free(bars.tmem, 512);
     }
