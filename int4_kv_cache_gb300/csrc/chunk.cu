@@ -507,6 +507,7 @@ template <int D, int BITS>
 __device__ __forceinline__ void load_query(const ChunkParams& p, const Work& w, uint8_t* tile, int tid, int tile_row0) {
     constexpr int kPieces = D / 8;       // 16-byte pieces of a row: eight channels
     constexpr int kRows = 32 / kPieces;  // rows that a warp loads at a time
+    constexpr int kAhead = 32 / kRows < 16 ? 32 / kRows : 16;
     const int lane = tid & 31, u = lane % kPieces, row0 = (tid >> 5) * 32;
     // lane l finds the warp's row l
     const int r = tile_row0 + row0 + lane;
@@ -518,15 +519,15 @@ __device__ __forceinline__ void load_query(const ChunkParams& p, const Work& w, 
     }
     const uint16_t* base = p.q + w.b * p.stride_b;
 #pragma unroll 1
-    for (int it0 = 0; it0 < 32 / kRows; it0 += 8) {
-        uint4 x[8];
+    for (int it0 = 0; it0 < 32 / kRows; it0 += kAhead) {
+        uint4 x[kAhead];
 #pragma unroll
-        for (int it = 0; it < 8; ++it) {
+        for (int it = 0; it < kAhead; ++it) {
             const long long at = __shfl_sync(0xffffffffu, from, (it0 + it) * kRows + lane / kPieces);
             x[it] = at >= 0 ? __ldg(reinterpret_cast<const uint4*>(base + at) + u) : make_uint4(0, 0, 0, 0);
         }
 #pragma unroll
-        for (int it = 0; it < 8; ++it) {
+        for (int it = 0; it < kAhead; ++it) {
             const int at = row0 + (it0 + it) * kRows + lane / kPieces;
             uint4 y = x[it];
             if (p.negate_q) y.x ^= 0x80008000u, y.y ^= 0x80008000u, y.z ^= 0x80008000u, y.w ^= 0x80008000u;
@@ -811,22 +812,12 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     const int warp = threadIdx.x >> 5;
     if (warp == 16) {
         tmem_alloc(&bars.tmem, 512);
-    } else if (threadIdx.x == 17 * 32) {
-        for (int i = 0; i < 6; ++i) {
-            mbar_init(&bars.ring_full[i], 1);
-            mbar_init(&bars.ring_empty[i], C::kUnpackWarps);
-            mbar_init(&bars.slot_full[i], C::kUnpackWarps);
-            mbar_init(&bars.slot_empty[i], 1);
+    } else if (warp == 17) {
+        for (uint32_t at = (threadIdx.x & 31) * 8; at < kTmemAt; at += 32 * 8) {
+            const bool by_unpack = at >= kRingEmpty && at < kSlotEmpty, by_softmax = (at >= kSFree && at < kSFree + 16) || (at >= kPFull && at < kPFull + 16);
+            mbar_init(&bars.ring_full[0] + at / 8, by_unpack ? C::kUnpackWarps : (by_softmax ? 4 : (at == kQFull ? C::kStreams * 4 : 1)));
         }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&bars.s_full[i], 1);
-            mbar_init(&bars.p_full[i], 4);
-            mbar_init(&bars.s_free[i], 4);
-            mbar_init(&bars.pv_done[i], 1);
-            mbar_init(&bars.drain[i], 1);
-        }
-        mbar_init(&bars.q_full, C::kStreams * 4);
-        bars.abort = 0;
+        if (threadIdx.x == 17 * 32) bars.abort = 0;
         fence_mbarrier_init();
     }
     tc_fence_before();

@@ -309,35 +309,46 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(PagesParams 
 }
 
 // ------------------------------------------------------------------- rows --
-// `bytes` bytes by the CTA's threads: 16 at a time, the last ones two at a time.
-__device__ __forceinline__ void copy_span(uint8_t* dst, const uint8_t* src, int bytes, int tid, int step) {
+// `bytes` bytes by the CTA's threads: 16 at a time, four of a thread's in flight, the
+// last ones two at a time.
+__device__ __forceinline__ void copy_span(uint8_t* dst, const uint8_t* src, int bytes) {
     const int vecs = bytes >> 4;
-    for (int i = tid; i < vecs; i += step)
-        reinterpret_cast<uint4*>(dst)[i] = __ldcs(reinterpret_cast<const uint4*>(src) + i);
-    for (int i = vecs * 8 + tid; i < bytes >> 1; i += step)
+    uint4* d = reinterpret_cast<uint4*>(dst);
+    const uint4* s = reinterpret_cast<const uint4*>(src);
+    int i = threadIdx.x;
+    for (; i + 3 * kCopyThreads < vecs; i += 4 * kCopyThreads) {
+        uint4 v[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] = __ldcs(s + i + k * kCopyThreads);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) __stcs(d + i + k * kCopyThreads, v[k]);
+    }
+    for (; i < vecs; i += kCopyThreads) __stcs(d + i, __ldcs(s + i));
+    for (i = vecs * 8 + threadIdx.x; i < bytes >> 1; i += kCopyThreads)
         reinterpret_cast<uint16_t*>(dst)[i] = reinterpret_cast<const uint16_t*>(src)[i];
 }
 
-// The listed moves: a unit is one head of a page.
+// The listed moves.  A unit is one of the six arrays of a page, or (heads: first rows
+// of a page, few moves) of one head of it.
+template <bool HEADS>
 __device__ __forceinline__ void copy_moves(const PagesParams& p) {
-    const int n = p.head[0];
+    const int n = p.head[0], each = HEADS ? p.num_kv_heads : 1;
     const int cw = p.head_dim * p.bits / 8, sw = p.head_dim / kGroup * 2;
-    for (long long u = blockIdx.x; u < static_cast<long long>(n) * p.num_kv_heads; u += gridDim.x) {
-        const int i = static_cast<int>(u / p.num_kv_heads), h = static_cast<int>(u - static_cast<long long>(i) * p.num_kv_heads);
-        const PageMove m = p.moves[i];
-        const long long src = (static_cast<long long>(m.src) * p.num_kv_heads + h) * p.page_tokens;
-        const long long dst = (static_cast<long long>(m.dst) * p.num_kv_heads + h) * p.page_tokens;
-#pragma unroll
-        for (int a = 0; a < 2; ++a) copy_span(p.codes[a] + dst * cw, p.codes[a] + src * cw, m.rows * cw, threadIdx.x, kCopyThreads);
-#pragma unroll
-        for (int a = 0; a < 4; ++a) {
-            uint8_t* at = reinterpret_cast<uint8_t*>(p.sb[a]);
-            copy_span(at + dst * sw, at + src * sw, m.rows * sw, threadIdx.x, kCopyThreads);
-        }
+    const long long codes = 2LL * n * each;  // codes first: most of the bytes are theirs
+    for (long long u = blockIdx.x; u < 3 * codes; u += gridDim.x) {
+        const bool scale = u >= codes;
+        const long long v = (scale ? u - codes : u) / each;
+        const int h = HEADS ? static_cast<int>(u % each) : 0;
+        const int a = scale ? static_cast<int>(v % 4) : static_cast<int>(v % 2), width = scale ? sw : cw;
+        const PageMove m = p.moves[scale ? v / 4 : v / 2];
+        uint8_t* at = scale ? reinterpret_cast<uint8_t*>(p.sb[a]) : p.codes[a];
+        const long long head = static_cast<long long>(p.page_tokens) * width, page = head * p.num_kv_heads;
+        // (a page's codes are at most 2^31 bytes: its host check)
+        copy_span(at + m.dst * page + h * head, at + m.src * page + h * head, HEADS ? m.rows * width : static_cast<int>(page));
     }
 }
 
-__global__ void __launch_bounds__(kCopyThreads) move_rows_kernel(PagesParams p) { copy_moves(p); }
+__global__ void __launch_bounds__(kCopyThreads) move_rows_kernel(PagesParams p) { copy_moves<true>(p); }
 
 __global__ void __launch_bounds__(kCopyThreads) compact_rows_kernel(PagesParams p) {
     const int n = p.head[1];
@@ -353,7 +364,7 @@ __global__ void __launch_bounds__(kCopyThreads) compact_rows_kernel(PagesParams 
         }
         p.table_out[e] = page;
     }
-    copy_moves(p);
+    copy_moves<false>(p);
 }
 
 }  // namespace
@@ -377,8 +388,8 @@ cudaError_t launch_pages_reserve(const PagesParams& p, int sms, cudaStream_t str
     reserve_plan_kernel<<<1, kPlanThreads, 0, stream>>>(p);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    // no more units of work than heads of the pages that the rows touch
-    const long long units = static_cast<long long>(p.batch) * ((p.n_rows + p.page_tokens - 2) / p.page_tokens + 1) * p.num_kv_heads;
+    // no more units of work than heads of the arrays of the pages that the rows touch
+    const long long units = 6LL * p.num_kv_heads * p.batch * ((p.n_rows + p.page_tokens - 2) / p.page_tokens + 1);
     move_rows_kernel<<<static_cast<unsigned>(units < 4LL * sms ? units : 4LL * sms), kCopyThreads, 0, stream>>>(p);
     return cudaGetLastError();
 }

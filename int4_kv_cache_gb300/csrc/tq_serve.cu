@@ -30,7 +30,9 @@ size_t chunk_part_rows(int32_t batch, int32_t hq, int32_t hkv, int32_t head_dim,
 
 size_t chunk_bytes(int32_t batch, int32_t hq, int32_t hkv, int32_t head_dim, int32_t n, int32_t max_seq_len) {
     const size_t rows = chunk_part_rows(batch, hq, hkv, head_dim, n, max_seq_len);
-    return 2 * align256(rows * sizeof(float)) + align256(rows * head_dim * sizeof(float));
+    const size_t parts = 2 * align256(rows * sizeof(float)) + align256(rows * head_dim * sizeof(float));
+    const size_t decode = tq_sdpa_workspace_bytes(batch, hq, hkv, head_dim, max_seq_len, TQ_DEFAULT_CHUNK);
+    return parts > decode ? parts : decode;
 }
 
 // Items with a CTA each, and how many runs the keys of each of the others are cut into.
@@ -67,8 +69,8 @@ bool chunk_sizes(int32_t batch, int32_t hq, int32_t hkv, int32_t head_dim, int32
            n >= 1 && static_cast<long long>(n) * hq <= kMaxChunkRows && max_seq_len >= 1 && max_seq_len <= kMaxTokens;
 }
 
-tq_status chunk(const Store& c, const tq_query_rows* q, const int32_t* q_lens, const int32_t* seq_lens, int32_t max_seq_len, float attn_scale,
-                int32_t window, uint32_t flags, void* workspace, size_t workspace_bytes, uint16_t* out, int32_t* status, cudaStream_t stream) {
+tq_status check_chunk(const Store& c, const tq_query_rows* q, const int32_t* q_lens, const int32_t* seq_lens, int32_t max_seq_len, int32_t window,
+                      uint32_t flags, const void* workspace, size_t workspace_bytes, const uint16_t* out, const int32_t* status) {
     if (q == nullptr || q->x == nullptr || seq_lens == nullptr || out == nullptr) return TQ_ERR_NULL;
     if (q->num_heads < 1 || q->num_heads % c.num_kv_heads != 0 || q->n < 0 || q->stride_b < 0 || q->stride_h < 0 || q->stride_t < 0)
         return TQ_ERR_SHAPE;
@@ -84,8 +86,11 @@ tq_status chunk(const Store& c, const tq_query_rows* q, const int32_t* q_lens, c
     const unsigned long long extent = 2ull * (static_cast<unsigned long long>(c.batch - 1) * q->stride_b + static_cast<unsigned long long>(q->n - 1) * q->stride_t +
                                               static_cast<unsigned long long>(q->num_heads - 1) * q->stride_h + c.head_dim);
     if (overlap(out, 2ull * c.batch * q->n * q->num_heads * c.head_dim, q->x, extent)) return TQ_ERR_SHAPE;
-    tq_status s = check_workspace(workspace, workspace_bytes, chunk_bytes(c.batch, q->num_heads, c.num_kv_heads, c.head_dim, q->n, max_seq_len));
-    if (s != TQ_OK) return s;
+    return check_workspace(workspace, workspace_bytes, chunk_bytes(c.batch, q->num_heads, c.num_kv_heads, c.head_dim, q->n, max_seq_len));
+}
+
+tq_status chunk(const Store& c, const tq_query_rows* q, const int32_t* q_lens, const int32_t* seq_lens, int32_t max_seq_len, float attn_scale,
+                int32_t window, uint32_t flags, void* workspace, uint16_t* out, int32_t* status, cudaStream_t stream) {
     ChunkParams p{};
     p.q = q->x;
     p.stride_b = q->stride_b;
@@ -120,7 +125,7 @@ tq_status chunk(const Store& c, const tq_query_rows* q, const int32_t* q_lens, c
     p.rot_scale = rotation_scale(c.head_dim);
     p.map = c.map;
     DeviceFacts* f = nullptr;
-    s = device_facts(&f);
+    const tq_status s = device_facts(&f);
     if (s != TQ_OK) return s;
     const long long rows = static_cast<long long>(p.n) * p.group_q;
     const int tile = chunk_tile_tokens(c.head_dim);
@@ -146,6 +151,13 @@ tq_status chunk(const Store& c, const tq_query_rows* q, const int32_t* q_lens, c
     p.part_l = reinterpret_cast<float*>(ws + align256(part_rows * sizeof(float)));
     p.part_acc = reinterpret_cast<float*>(ws + 2 * align256(part_rows * sizeof(float)));
     return cuda_status(launch_chunk(p, c.head_dim, stream));
+}
+
+// One row a sequence, contiguous: what the decode is for (a 128-row tile would hold
+// group_q rows; 16 sequences of 16 heads over up to 1,500 tokens: 31 us in tiles).
+bool is_decode(const Store& c, const tq_query_rows* q, const int32_t* q_lens, int32_t window) {
+    return q->n == 1 && q_lens == nullptr && window == 0 && (q->num_heads == 1 || q->stride_h == c.head_dim) &&
+           (c.batch == 1 || q->stride_b == static_cast<int64_t>(q->num_heads) * c.head_dim);
 }
 
 // ------------------------------------------------------------------- pages --
@@ -206,6 +218,7 @@ int arrays_of(const Store& c, Span* s) {
 tq_status pages_params(const Store& c, const int32_t* refs, const int32_t* held, void* workspace, size_t workspace_bytes, int32_t* status, PagesParams* p) {
     if (refs == nullptr || held == nullptr) return TQ_ERR_NULL;
     if (!pages_sizes(c.batch, c.map.num_pages, c.map.max_pages)) return TQ_ERR_SHAPE;
+    if (static_cast<long long>(c.num_kv_heads) * c.map.page_tokens * c.head_dim * c.bits / 8 >= (1LL << 31)) return TQ_ERR_SHAPE;
     if (!aligned4(refs) || !aligned4(held) || !aligned4(c.map.block_table) || !aligned4(status)) return TQ_ERR_ALIGN;
     const PagesSpace sp = pages_space(c.batch, c.map.num_pages, c.map.max_pages);
     const tq_status s = check_workspace(workspace, workspace_bytes, sp.bytes);
@@ -261,20 +274,26 @@ tq_status tq_sdpa_chunk(const tq_kv_cache* cache, const tq_query_rows* q, const 
                         float attn_scale, int32_t window, uint32_t flags, void* workspace, size_t workspace_bytes, uint16_t* out,
                         int32_t* status, void* stream) {
     Store st;
-    const tq_status s = store_of(cache, &st);
-    return s != TQ_OK ? s
-                      : chunk(st, q, q_lens, seq_lens, max_seq_len, attn_scale, window, flags, workspace, workspace_bytes, out, status,
-                              static_cast<cudaStream_t>(stream));
+    tq_status s = store_of(cache, &st);
+    if (s == TQ_OK) s = check_chunk(st, q, q_lens, seq_lens, max_seq_len, window, flags, workspace, workspace_bytes, out, status);
+    if (s != TQ_OK || q->n == 0) return s;
+    if (is_decode(st, q, q_lens, window))
+        return tq_sdpa_int4_decode_ex(cache, q->x, q->num_heads, seq_lens, max_seq_len, attn_scale, TQ_DEFAULT_CHUNK, flags & ~TQ_CHUNK_FULL, workspace, workspace_bytes,
+                                      out, status, stream);
+    return chunk(st, q, q_lens, seq_lens, max_seq_len, attn_scale, window, flags, workspace, out, status, static_cast<cudaStream_t>(stream));
 }
 
 tq_status tq_paged_sdpa_chunk(const tq_paged_kv_cache* cache, const tq_query_rows* q, const int32_t* q_lens, const int32_t* seq_lens,
                               int32_t max_seq_len, float attn_scale, int32_t window, uint32_t flags, void* workspace,
                               size_t workspace_bytes, uint16_t* out, int32_t* status, void* stream) {
     Store st;
-    const tq_status s = store_of(cache, &st);
-    return s != TQ_OK ? s
-                      : chunk(st, q, q_lens, seq_lens, max_seq_len, attn_scale, window, flags, workspace, workspace_bytes, out, status,
-                              static_cast<cudaStream_t>(stream));
+    tq_status s = store_of(cache, &st);
+    if (s == TQ_OK) s = check_chunk(st, q, q_lens, seq_lens, max_seq_len, window, flags, workspace, workspace_bytes, out, status);
+    if (s != TQ_OK || q->n == 0) return s;
+    if (is_decode(st, q, q_lens, window))
+        return tq_paged_sdpa_int4_decode(cache, q->x, q->num_heads, seq_lens, max_seq_len, attn_scale, TQ_DEFAULT_CHUNK, flags & ~TQ_CHUNK_FULL, workspace, workspace_bytes,
+                                         out, status, stream);
+    return chunk(st, q, q_lens, seq_lens, max_seq_len, attn_scale, window, flags, workspace, out, status, static_cast<cudaStream_t>(stream));
 }
 
 size_t tq_pages_workspace_bytes(int32_t batch, int32_t num_pages, int32_t max_pages_per_seq) {
