@@ -54,6 +54,10 @@ struct Cfg {
     static constexpr int kEntry = kCodes + 2 * kScales;
     static constexpr int kRing = D == 64 ? 6 : (BITS == 8 ? 3 : 6);
     static constexpr int kQ = kStreams * kRowTile * D * 2;
+    // one row tile: the other's place holds more of the ring (few rows: what bounds is how
+    // many bytes are on their way)
+    static constexpr int kMoreRing = kStreams == 2 ? kRowTile * D * 2 / kEntry : 0;
+    static_assert(kRing + kMoreRing <= 10, "barriers");
     static constexpr int kSmem = 1024 + kQ + kSlots * kSlot + kRing * kEntry;
     static_assert(kQ + kSlots * kSlot >= kStreams * D * (kRowTile + 1) * 4, "rows on their way out");
     // TMEM columns: scores (one place for both accumulators at head_dim 128, else two),
@@ -67,7 +71,7 @@ struct Cfg {
 };
 
 struct Bars {
-    uint64_t ring_full[6], ring_empty[6], slot_full[6], slot_empty[6];
+    uint64_t ring_full[10], ring_empty[10], slot_full[6], slot_empty[6];
     uint64_t s_full[2], s_free[2], p_full[2], pv_done[2], q_full, drain[2];
     uint32_t tmem;
     int32_t abort;
@@ -80,17 +84,17 @@ struct Bars {
 // tens of cycles to read, which between two products is time lost.)
 enum : uint32_t {
     kRingFull = 0,
-    kRingEmpty = 6 * 8,
-    kSlotFull = 12 * 8,
-    kSlotEmpty = 18 * 8,
-    kSFull = 24 * 8,
-    kSFree = 26 * 8,
-    kPFull = 28 * 8,
-    kPvDone = 30 * 8,
-    kQFull = 32 * 8,
-    kDrain = 33 * 8,
-    kTmemAt = 35 * 8,
-    kAbort = 35 * 8 + 4,
+    kRingEmpty = 10 * 8,
+    kSlotFull = 20 * 8,
+    kSlotEmpty = 26 * 8,
+    kSFull = 32 * 8,
+    kSFree = 34 * 8,
+    kPFull = 36 * 8,
+    kPvDone = 38 * 8,
+    kQFull = 40 * 8,
+    kDrain = 41 * 8,
+    kTmemAt = 43 * 8,
+    kAbort = 43 * 8 + 4,
 };
 __device__ __forceinline__ uint32_t fixed(uint32_t x) {
     asm volatile("" : "+r"(x));
@@ -225,30 +229,59 @@ __device__ __forceinline__ bool wait(uint32_t bars, uint32_t bar, uint32_t parit
 }
 
 // ------------------------------------------------------------------ loader --
+// Where entry r of the ring lies.
 template <int D, int BITS>
-__device__ __forceinline__ void load_role(const ChunkParams& p, const Work& w, uint8_t* ring, Bars* bars) {
+__device__ __forceinline__ uint32_t ring_at(uint32_t ring, uint32_t more, int r) {
+    using C = Cfg<D, BITS>;
+    return r < C::kRing ? ring + r * C::kEntry : more + (r - C::kRing) * C::kEntry;
+}
+
+// One warp: its first three lanes copy an entry's codes, scales and biases.
+template <int D, int BITS>
+__device__ __forceinline__ void load_role(const ChunkParams& p, const Work& w, uint32_t ring, uint32_t more, int ring_entries, uint32_t bars) {
     using C = Cfg<D, BITS>;
     const uint64_t policy = policy_evict_first();
-    const uint32_t at = fixed(smem_u32(bars));
-    int e = 0;
+    const int lane = threadIdx.x & 31;
+    const uint32_t width = lane == 0 ? D * BITS / 8 : C::kBlocks * 2, offset = lane == 0 ? 0 : (lane == 1 ? C::kCodes : C::kCodes + C::kScales);
+    const uint8_t* keys = lane == 0 ? p.k_codes : reinterpret_cast<const uint8_t*>(lane == 1 ? p.k_scale : p.k_bias);
+    const uint8_t* values = lane == 0 ? p.v_codes : reinterpret_cast<const uint8_t*>(lane == 1 ? p.v_scale : p.v_bias);
+    int r = 0, issued = 0;
+    uint32_t parity = 1;
+    bool ok = true;
+    auto issue = [&](const uint8_t* from, int tile, long long row) {
+        if (!wait(bars, kRingEmpty + r * 8, parity, p.status)) return false;
+        const int rows = min(C::kTile, (w.khi - (w.tile0 + tile) * C::kTile + 15) & ~15);  // capacities are whole 16s
+        const uint32_t bar = bars + kRingFull + r * 8;
+        if (lane == 0) asm volatile("mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(rows * (D * BITS / 8 + C::kBlocks * 4)) : "memory");
+        __syncwarp();
+        if (lane < 3)
+            asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(
+                             ring_at<D, BITS>(ring, more, r) + offset),
+                         "l"(from + row * width), "r"(rows * width), "r"(bar), "l"(policy)
+                         : "memory");
+        ++issued;
+        if (++r == ring_entries) {
+            r = 0;
+            parity ^= 1;
+        }
+        return true;
+    };
+    // rows of the next tile are looked up (a table entry's latency) ahead of its copies
+    long long row = 0, next = w.tiles > 0 ? kv_row(p.map, p.num_kv_heads, w.b, w.h, w.tile0 * C::kTile, p.status) : 0;
 #pragma unroll 1
-    for (; e < 2 * w.tiles; ++e) {
-        const int r = e % C::kRing, n = e / C::kRing;
-        if (n > 0 && !wait(at, kRingEmpty + r * 8, (n - 1) & 1, p.status)) break;
-        int tile;
-        const bool value = entry_of(e, w.tiles, tile);
-        const int t0 = (w.tile0 + tile) * C::kTile;
-        const int rows = min(C::kTile, (w.khi - t0 + 15) & ~15);  // capacities are whole 16s
-        const long long row = kv_row(p.map, p.num_kv_heads, w.b, w.h, t0, p.status);
-        uint8_t* dst = ring + r * C::kEntry;
-        const uint32_t cb = rows * (D * BITS / 8), sb = rows * (C::kBlocks * 2);
-        mbar_arrive_expect_tx(&bars->ring_full[r], cb + 2 * sb);
-        bulk_load(dst, (value ? p.v_codes : p.k_codes) + row * (D * BITS / 8), cb, &bars->ring_full[r], policy);
-        bulk_load(dst + C::kCodes, (value ? p.v_scale : p.k_scale) + row * C::kBlocks, sb, &bars->ring_full[r], policy);
-        bulk_load(dst + C::kCodes + C::kScales, (value ? p.v_bias : p.k_bias) + row * C::kBlocks, sb, &bars->ring_full[r], policy);
+    for (int j = -1; j < w.tiles && ok; ++j) {
+        long long after = 0;
+        if (j + 2 < w.tiles) after = kv_row(p.map, p.num_kv_heads, w.b, w.h, (w.tile0 + j + 2) * C::kTile, p.status);
+        if (j + 1 < w.tiles) ok = issue(keys, j + 1, next);
+        if (j >= 0 && ok) ok = issue(values, j, row);
+        row = next;
+        next = after;
     }
-    if (e < 2 * w.tiles)  // given up: the copies in flight land before the CTA leaves
-        for (int k = max(0, e - C::kRing); k < e; ++k) mbar_wait_bounded(&bars->ring_full[k % C::kRing], (k / C::kRing) & 1);
+    if (!ok) {  // given up: the copies in flight land before the CTA leaves
+        for (int k = max(0, issued - ring_entries); k < issued; ++k)
+            for (int it = 0; it < 1 << 20 && !over(bars + kRingFull + k % ring_entries * 8, (k / ring_entries) & 1); ++it) {
+            }
+    }
 }
 
 // ---------------------------------------------------------------- unpacking --
@@ -297,7 +330,7 @@ __device__ __forceinline__ void sts128(uint32_t at, const __half2 (&h)[4]) {
 // A thread takes the same 16-byte piece of every 2^n-th key's codes: where its
 // outputs go, and in which order, is the same for all of them.
 template <int D, int BITS>
-__device__ __forceinline__ void unpack_role(const ChunkParams& p, const Work& w, uint32_t ring, uint32_t slots, uint32_t bars) {
+__device__ __forceinline__ void unpack_role(const ChunkParams& p, const Work& w, uint32_t ring, uint32_t more, int ring_entries, uint32_t slots, uint32_t bars) {
     using C = Cfg<D, BITS>;
     constexpr int kUnits = BITS == 4 ? 4 : 2;             // 16-byte pieces of fp16 that 16 bytes of codes give
     constexpr int kChunks = D * BITS / 8 / 16;            // 16-byte pieces of codes per key
@@ -323,7 +356,7 @@ __device__ __forceinline__ void unpack_role(const ChunkParams& p, const Work& w,
         if (BITS == 4 && D == 256 && (x & 1)) swap(0, 1), swap(2, 3);
         if (D >= 128 && (BITS == 4 ? (x & 2) != 0 : x != 0)) swap(0, 2), swap(1, 3);
     };
-    const uint32_t from = ring + tid * 16, from_scale = ring + C::kCodes + (t * C::kBlocks + g) * 2;
+    const uint32_t from = tid * 16, from_scale = C::kCodes + (t * C::kBlocks + g) * 2;
     int r = 0, s = 0;
     uint32_t r_parity = 0, s_parity = 1;
 #pragma unroll 1
@@ -333,7 +366,7 @@ __device__ __forceinline__ void unpack_role(const ChunkParams& p, const Work& w,
         int tile;
         const bool value = entry_of(e, w.tiles, tile);
         const int t0 = (w.tile0 + tile) * C::kTile;
-        const uint32_t src = from + r * C::kEntry, src_scale = from_scale + r * C::kEntry, dst = s * C::kSlot;
+        const uint32_t at = ring_at<D, BITS>(ring, more, r), src = at + from, src_scale = at + from_scale, dst = s * C::kSlot;
         uint4 word[kIts];
         __half sc[kIts], bi[kIts];
         // values past fp16's range, scales or biases that are no numbers, keys that no row sees: apart
@@ -390,7 +423,7 @@ __device__ __forceinline__ void unpack_role(const ChunkParams& p, const Work& w,
             arrive(bars + kRingEmpty + r * 8);
             arrive(bars + kSlotFull + s * 8);
         }
-        if (++r == C::kRing) {
+        if (++r == ring_entries) {
             r = 0;
             r_parity ^= 1;
         }
@@ -807,6 +840,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     uint8_t* slots = base + C::kQ;
     uint8_t* ring = slots + C::kSlots * C::kSlot;
     const bool pair = C::kStreams == 2 && p.pair;
+    const int ring_entries = C::kRing + (pair ? 0 : C::kMoreRing);
     Work w;
     if (!find_work<C::kTile>(p, p.rows_per_item, w)) return;  // the whole CTA
     const int warp = threadIdx.x >> 5;
@@ -823,18 +857,18 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    // registers: 640 x 96 at launch; 256 x 160 + 256 x 64 + 128 x 32 (one
-    // accumulator: 128 x 160 + 128 x 24 + 256 x 64 + 128 x 32)
+    // registers: 640 x 96 at launch; 256 x 160 + 256 x 56 + 128 x 48 (one
+    // accumulator: 128 x 160 + 128 x 24 + 256 x 56 + 128 x 48)
     if (warp < C::kSoftmax / 32) {
         regs_raise<160>();
         softmax_role<D, BITS, ROT>(p, w, qs, slots, fixed(smem_u32(&bars)), &bars, warp >> 2, pair);
     } else if (warp < 8) {
         regs_lower<24>();
     } else if (warp < 16) {
-        regs_lower<64>();
-        unpack_role<D, BITS>(p, w, fixed(smem_u32(ring)), fixed(smem_u32(slots)), fixed(smem_u32(&bars)));
+        regs_lower<56>();
+        unpack_role<D, BITS>(p, w, fixed(smem_u32(ring)), fixed(smem_u32(qs + kRowTile * D * 2)), ring_entries, fixed(smem_u32(slots)), fixed(smem_u32(&bars)));
     } else {
-        regs_lower<32>();
+        regs_lower<48>();
         if (warp == 16 || warp == 18) {
             const uint32_t at = fixed(smem_u32(&bars)), in = fixed(smem_u32(slots));
             if (!(warp == 16 ? scores_role<D, BITS>(p, w, fixed(smem_u32(qs)), in, at, pair) : outputs_role<D, BITS>(p, w, in, at, pair))) {
@@ -845,8 +879,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                 for (int it = 0; it < 1 << 20 && !over(bar, 0); ++it) {
                 }
             }
-        } else if (threadIdx.x == 17 * 32) {
-            load_role<D, BITS>(p, w, ring, &bars);
+        } else if (warp == 17) {
+            load_role<D, BITS>(p, w, fixed(smem_u32(ring)), fixed(smem_u32(qs + kRowTile * D * 2)), ring_entries, fixed(smem_u32(&bars)));
         }
         __syncwarp();
     }
