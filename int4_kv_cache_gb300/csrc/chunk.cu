@@ -753,15 +753,15 @@ __device__ __forceinline__ void softmax_role(const ChunkParams& p, const Work& w
         f *= inv;
         fo *= inv;
     }
-    // 16 columns of the output at a time
-    auto columns = [&](int x, float (&v)[16]) {
-        float o[16];
+    // 32 columns of the output at a time
+    auto columns = [&](int x, float (&v)[32]) {
+        float o[32];
         if (turns > 0) {
-            tmem_ld16(oa + x, o);
+            tmem_ld32(oa + x, o);
             tmem_wait_ld();
         }
 #pragma unroll
-        for (int y = 0; y < 16; ++y) {
+        for (int y = 0; y < 32; ++y) {
             const int at = place<BITS>(y);
             v[y] = turns > 0 ? o[at] * f : 0.f;
             if (merge) v[y] += apart[(x + at) * kPad + row] * fo;
@@ -775,15 +775,15 @@ __device__ __forceinline__ void softmax_role(const ChunkParams& p, const Work& w
         uint8_t* to = (merge ? slots + C::kSlots * C::kSlot - kRowTile * (D * 4 + 16) : qs) + r * stride;
         if (mine) {
 #pragma unroll 1
-            for (int x = 0; x < D; x += 16) {
-                float v[16];
+            for (int x = 0; x < D; x += 32) {
+                float v[32];
                 columns(x, v);
                 if (w.part >= 0) {
 #pragma unroll
-                    for (int y = 0; y < 16; y += 4) *reinterpret_cast<float4*>(to + (x + y) * 4) = make_float4(v[y], v[y + 1], v[y + 2], v[y + 3]);
+                    for (int y = 0; y < 32; y += 4) *reinterpret_cast<float4*>(to + (x + y) * 4) = make_float4(v[y], v[y + 1], v[y + 2], v[y + 3]);
                 } else {
 #pragma unroll
-                    for (int y = 0; y < 16; y += 8) floats_to_halves<8>(*reinterpret_cast<float(*)[8]>(v + y), to + (x + y) * 2);
+                    for (int y = 0; y < 32; y += 8) floats_to_halves<8>(*reinterpret_cast<float(*)[8]>(v + y), to + (x + y) * 2);
                 }
             }
         }
@@ -806,11 +806,11 @@ __device__ __forceinline__ void softmax_role(const ChunkParams& p, const Work& w
     float* rows = reinterpret_cast<float*>(qs) + (pair ? stream : 0) * (D * kPad);
     if (mine) {
 #pragma unroll 1
-        for (int x = 0; x < D; x += 16) {
-            float v[16];
+        for (int x = 0; x < D; x += 32) {
+            float v[32];
             columns(x, v);
 #pragma unroll
-            for (int y = 0; y < 16; ++y) rows[(x + y) * kPad + row] = v[y];
+            for (int y = 0; y < 32; ++y) rows[(x + y) * kPad + row] = v[y];
         }
     }
     asm volatile("barrier.cta.sync 9, %0;" ::"n"(C::kSoftmax) : "memory");
@@ -897,9 +897,10 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
 constexpr int kMergeThreads = 256;
 
 template <int D>
-__global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const __grid_constant__ ChunkParams p) {
+__global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(ChunkParams p) {
     constexpr int E = D / 32;
     const int lane = threadIdx.x & 31;
+    pdl_wait_primary();
     const long long wid = static_cast<long long>(blockIdx.x) * (kMergeThreads / 32) + (threadIdx.x >> 5);
     // row r of the item-th split item
     const int item = static_cast<int>(wid / p.rows_per_item), r = static_cast<int>(wid - static_cast<long long>(item) * p.rows_per_item);
@@ -961,8 +962,7 @@ cudaError_t launch_dim(const ChunkParams& p, cudaStream_t stream) {
                                 : (rot ? launch_main<D, 4, true>(p, stream) : launch_main<D, 4, false>(p, stream));
     if (e != cudaSuccess || p.n_splits == 1) return e;
     const long long rows = (static_cast<long long>(p.batch) * p.num_kv_heads * p.m_items - p.whole) * p.rows_per_item, each = kMergeThreads / 32;
-    chunk_merge_kernel<D><<<static_cast<unsigned>((rows + each - 1) / each), kMergeThreads, 0, stream>>>(p);
-    return cudaGetLastError();
+    return launch_after(chunk_merge_kernel<D>, static_cast<unsigned>((rows + each - 1) / each), kMergeThreads, stream, p);
 }
 
 }  // namespace

@@ -121,6 +121,7 @@ __global__ void __launch_bounds__(kCopyThreads) fork_release_kernel(PagesParams 
 }
 
 __global__ void __launch_bounds__(kCopyThreads) fork_take_kernel(PagesParams p) {
+    pdl_wait_primary();
     const long long entries = static_cast<long long>(p.batch) * p.max_pages;
     for (long long e = static_cast<long long>(blockIdx.x) * kCopyThreads + threadIdx.x; e < entries;
          e += static_cast<long long>(gridDim.x) * kCopyThreads) {
@@ -348,9 +349,13 @@ __device__ __forceinline__ void copy_moves(const PagesParams& p) {
     }
 }
 
-__global__ void __launch_bounds__(kCopyThreads) move_rows_kernel(PagesParams p) { copy_moves<true>(p); }
+__global__ void __launch_bounds__(kCopyThreads) move_rows_kernel(PagesParams p) {
+    pdl_wait_primary();
+    copy_moves<true>(p);
+}
 
 __global__ void __launch_bounds__(kCopyThreads) compact_rows_kernel(PagesParams p) {
+    pdl_wait_primary();
     const int n = p.head[1];
     const long long step = static_cast<long long>(gridDim.x) * kCopyThreads, first = static_cast<long long>(blockIdx.x) * kCopyThreads + threadIdx.x;
     const long long entries = static_cast<long long>(p.batch) * p.max_pages;
@@ -380,8 +385,7 @@ cudaError_t launch_pages_fork(const PagesParams& p, int sms, cudaStream_t stream
     fork_release_kernel<<<grid, kCopyThreads, 0, stream>>>(p);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    fork_take_kernel<<<grid, kCopyThreads, 0, stream>>>(p);
-    return cudaGetLastError();
+    return launch_after(fork_take_kernel, grid, kCopyThreads, stream, p);
 }
 
 cudaError_t launch_pages_reserve(const PagesParams& p, int sms, cudaStream_t stream) {
@@ -390,16 +394,14 @@ cudaError_t launch_pages_reserve(const PagesParams& p, int sms, cudaStream_t str
     if (e != cudaSuccess) return e;
     // no more units of work than heads of the arrays of the pages that the rows touch
     const long long units = 6LL * p.num_kv_heads * p.batch * ((p.n_rows + p.page_tokens - 2) / p.page_tokens + 1);
-    move_rows_kernel<<<static_cast<unsigned>(units < 4LL * sms ? units : 4LL * sms), kCopyThreads, 0, stream>>>(p);
-    return cudaGetLastError();
+    return launch_after(move_rows_kernel, static_cast<unsigned>(units < 4LL * sms ? units : 4LL * sms), kCopyThreads, stream, p);
 }
 
 cudaError_t launch_pages_compact(const PagesParams& p, int sms, cudaStream_t stream) {
     compact_plan_kernel<<<1, kPlanThreads, 0, stream>>>(p);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    compact_rows_kernel<<<static_cast<unsigned>(8 * sms), kCopyThreads, 0, stream>>>(p);
-    return cudaGetLastError();
+    return launch_after(compact_rows_kernel, static_cast<unsigned>(8 * sms), kCopyThreads, stream, p);
 }
 
 }  // namespace tq

@@ -375,6 +375,24 @@ struct PagesParams {
     int32_t num_kv_heads, head_dim, bits;
 };
 
+#ifdef __CUDACC__
+// A launch that is set up while the kernel ahead of it on the stream still runs; the
+// kernel waits for that one (pdl_wait_primary) before it reads what it wrote.
+template <class Params>
+inline cudaError_t launch_after(void (*kernel)(Params), unsigned grid, int threads, cudaStream_t stream, const Params& p) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+#endif
+
 // Launchers (return the cudaError_t of the launch).
 cudaError_t launch_chunk(const ChunkParams& p, int head_dim, cudaStream_t stream);
 int chunk_tile_tokens(int head_dim);  // keys per tile
