@@ -688,8 +688,10 @@ tq_status tq_paged_kv_evict(const tq_paged_kv_cache* src, const tq_paged_kv_cach
  * distributed rows, up to 1.5e-3 with a key channel twenty times as large).  Cached rows whose scale or bias is not finite leave the
  * outputs of the rows that attend to them undefined, and no others; so do query rows
  * that are not finite for themselves.
+ * One contiguous row per sequence (n = 1, no q_lens, no window) is that decode itself.
  * workspace: tq_chunk_workspace_bytes(...) bytes, 256-byte aligned, one per call in
- * flight (0 bytes where n = 0).  n = 0 launches nothing.  batch and kv heads up to
+ * flight (not looked at where n = 0); it also serves fewer rows, sequences and tokens of
+ * the same heads.  n = 0 launches nothing.  batch and kv heads up to
  * 65,535, n * num_heads up to 2^28, caches up to 2^30 tokens. */
 #define TQ_CHUNK_FULL 0x200u
 typedef struct tq_query_rows {
@@ -717,7 +719,9 @@ tq_status tq_paged_sdpa_chunk(const tq_paged_kv_cache* cache, const tq_query_row
  *          row of cache->block_table, which these calls write
  * all zeros for a pool without sequences.  A pool that several caches share (tables
  * of their own over the same arrays) takes one refs.  Entries outside the pool and
- * held[b] outside [0, max_pages_per_seq] set TQ_DEV_PAGE and count for nothing.
+ * held[b] outside [0, max_pages_per_seq] set TQ_DEV_PAGE and count for nothing (held[b]
+ * as the nearest bound).  A page's codes are below 2^31 bytes, tables and pools of up to
+ * 2^30 entries (TQ_ERR_SHAPE).
  * The arrays, the workspace, the tables and the cache's arrays must not overlap
  * (TQ_ERR_SHAPE; but see tq_pages_compact).
  * workspace: tq_pages_workspace_bytes(...) bytes, 256-byte aligned, one per call in

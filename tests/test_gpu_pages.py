@@ -317,3 +317,40 @@ def test_a_serving_loop(bits, rotate):
     tq.tq_pages_compact(c, refs, held, ws, c.block_table, refs, n_live)
     assert int(n_live) < 24
     both(40, lens, lens + 40)
+
+
+def test_pools_past_32_bits():
+    """Pages whose codes lie behind 2^32 bytes."""
+    torch = need_gpu()
+    import int4_kv_cache_gb300 as tq
+
+    pages = (1 << 32) // (4 * 128 * 128) + 40  # 64 KB of codes a page
+    c = tq.PagedKVCache(2, 4, 128, 128, pages, 8, bits=8)
+    refs, held = tq.page_state(c)
+    ws = tq.pages_workspace(c)
+    refs.fill_(1)
+    refs[pages - 30:] = 0  # all but the last pages are someone else's
+    tq.tq_pages_reserve(c, refs, held, i32(torch, [0, -1]), 200, ws)
+    assert c.block_table[0, :2].tolist() == [pages - 30, pages - 29]
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    rows = {}
+    for a in ARRAYS:
+        t = getattr(c, a)
+        for p in (pages - 30, pages - 29):
+            t[p].view(torch.uint8).copy_(torch.randint(0, 256, t[p].view(torch.uint8).shape, generator=g, device="cuda", dtype=torch.uint8))
+        rows[a] = t[pages - 30:pages - 28].clone()
+    # the second sequence takes both over and writes to the second
+    tq.tq_pages_fork(c, refs, held, i32(torch, [0, 0]), ws)
+    tq.tq_pages_reserve(c, refs, held, i32(torch, [-1, 200]), 1, ws)
+    p = int(c.block_table[1, 1])
+    assert p == pages - 28 and int(c.block_table[1, 0]) == pages - 30
+    for a in ARRAYS:
+        assert torch.equal(getattr(c, a)[p, :, :72].view(torch.uint8), rows[a][1, :, :72].view(torch.uint8))
+    # the others let go: the three move to the front
+    refs[:pages - 30] = 0
+    n_live = torch.zeros(1, dtype=torch.int32, device="cuda")
+    tq.tq_pages_compact(c, refs, held, ws, c.block_table, refs, n_live)
+    assert int(n_live) == 3 and c.block_table[:, :2].tolist() == [[0, 1], [0, 2]] and refs[:4].tolist() == [2, 1, 1, 0]
+    for a in ARRAYS:
+        assert torch.equal(getattr(c, a)[:2].view(torch.uint8), rows[a].view(torch.uint8))
