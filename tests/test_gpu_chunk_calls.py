@@ -118,3 +118,35 @@ def test_steep_scores():
         for scale in (0.5, -0.5):
             got = attend(torch, tq, c, q, [1500], scale=scale)
             check(torch, got, reference(torch, c, q, [1500], [200], scale), [200])
+
+
+def test_binding_refusals():
+    """What the binding refuses before the library is called."""
+    torch = need_gpu()
+    import int4_kv_cache_gb300 as tq
+
+    c = make_cache(tq, torch, 2, 2, 64, 64, seed=1)
+    q = queries(torch, (2, 4, 8, 64), 1)
+    lens = torch.tensor([64, 64], dtype=torch.int32, device="cuda")
+    ws = tq.chunk_workspace(2, 4, 2, 64, 8, 64)
+    for kw in (dict(q=q.float()), dict(q=q[:1]), dict(q=q.transpose(2, 3)), dict(q=q[..., :32]), dict(q=q[0]), dict(seq_lens=lens[:1]), dict(seq_lens=lens.long()),
+               dict(q_lens=lens[:1]), dict(workspace=ws.float()), dict(out=torch.empty_like(q)), dict(status=lens.long()), dict(seq_lens=lens.cpu())):
+        a = dict(dict(cache=c, q=q, seq_lens=lens, max_seq_len=64, attn_scale=1.0, workspace=ws), **kw)
+        with pytest.raises(ValueError):
+            tq.tq_sdpa_chunk(**a)
+    with pytest.raises(tq.TQError):
+        tq.tq_sdpa_chunk(c, q, lens, 65, 1.0, ws)
+    with pytest.raises(tq.TQError):
+        tq.tq_sdpa_chunk(c, q, lens, 64, 1.0, ws[:256])
+    with pytest.raises(ValueError):
+        tq.chunk_workspace(2, 5, 2, 64, 8, 64)
+    refs, held = lens.clone(), lens.clone()
+    with pytest.raises(ValueError):
+        tq.tq_pages_fork(c, refs, held, lens, ws)  # not a paged cache
+    p = tq.PagedKVCache(2, 2, 64, 128, 5, 3)
+    refs, held = tq.page_state(p)
+    pw = tq.pages_workspace(p)
+    for call in (lambda: tq.tq_pages_fork(p, held, held, lens, pw), lambda: tq.tq_pages_reserve(p, refs, held, lens[:1], 1, pw),
+                 lambda: tq.tq_pages_compact(p, refs, held, pw, p.block_table[:1], refs, lens[:1])):
+        with pytest.raises(ValueError):
+            call()
