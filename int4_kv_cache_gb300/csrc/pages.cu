@@ -5,7 +5,7 @@
 // The bookkeeping is integer work over tables of some thousand entries: bound by
 // latency, so it is done by one CTA (its phases ordered by CTA barriers), and
 // the copies of rows by a second launch over the whole device that reads the
-// list of moves the first one left.  (32 beams forked and given room for a token: 14.9 us
+// list of moves the first one left.  (32 beams forked and given room for a token: 11.8 us
 // in three launches; half of 4,096 pages of 147 KB compacted: 54.7 us, 47 of them
 // copies at 6.4 TB/s, 7 the list.)
 #include "tq_device.cuh"
@@ -17,9 +17,11 @@ namespace {
 
 constexpr int kPlanThreads = 1024;
 constexpr int kCopyThreads = 256;
-// Largest table that a fork stages in one CTA's shared memory.
+// Largest table that a fork stages in one CTA's shared memory: one launch instead of two (32 x 65
+// entries), but one CTA's reads and atomics (64 x 131 entries and the reservation behind
+// them: 23.8 us in one CTA, 17.8 over the device).
 constexpr int kForkEntries = 8192;
-constexpr int kForkSeqs = 1024;
+constexpr int kForkSeqs = kPlanThreads;
 
 __device__ __forceinline__ void report(int32_t* status, int bit) {
     if (status != nullptr) atomicOr(status, bit);
@@ -75,11 +77,16 @@ __device__ __forceinline__ int source_of(const PagesParams& p, int b) {
 
 __global__ void __launch_bounds__(kPlanThreads) fork_small_kernel(PagesParams p) {
     __shared__ int32_t old[kForkEntries];
-    __shared__ int32_t held[kForkSeqs], lens[kForkSeqs];
+    __shared__ int16_t from[kForkSeqs];
+    __shared__ int32_t held[kForkSeqs];
     const int entries = p.batch * p.max_pages;
-    for (int b = threadIdx.x; b < p.batch; b += kPlanThreads) {
-        held[b] = clamp_held(p, p.held[b]);
-        if (p.lens != nullptr) lens[b] = p.lens[b];
+    // (up to kForkSeqs sequences: a thread each)
+    int len = 0;
+    if (static_cast<int>(threadIdx.x) < p.batch) {
+        const int s = source_of(p, threadIdx.x);
+        held[threadIdx.x] = clamp_held(p, p.held[threadIdx.x]);
+        from[threadIdx.x] = static_cast<int16_t>(s);
+        if (p.lens != nullptr && s >= 0) len = p.lens[s];
     }
     __syncthreads();
     for (int e = threadIdx.x; e < entries; e += kPlanThreads) {
@@ -91,7 +98,7 @@ __global__ void __launch_bounds__(kPlanThreads) fork_small_kernel(PagesParams p)
     __syncthreads();
     for (int e = threadIdx.x; e < entries; e += kPlanThreads) {
         const int b = e / p.max_pages, j = e - b * p.max_pages;
-        const int s = source_of(p, b);
+        const int s = from[b];
         int page = -1;
         if (s >= 0 && j < held[s]) {
             page = old[s * p.max_pages + j];
@@ -99,10 +106,10 @@ __global__ void __launch_bounds__(kPlanThreads) fork_small_kernel(PagesParams p)
         }
         p.table[e] = page;
     }
-    for (int b = threadIdx.x; b < p.batch; b += kPlanThreads) {
-        const int s = source_of(p, b);
-        p.held[b] = s < 0 ? 0 : held[s];
-        if (p.lens != nullptr) p.lens[b] = s < 0 ? 0 : lens[s];
+    if (static_cast<int>(threadIdx.x) < p.batch) {
+        const int s = from[threadIdx.x];
+        p.held[threadIdx.x] = s < 0 ? 0 : held[s];
+        if (p.lens != nullptr) p.lens[threadIdx.x] = len;
     }
 }
 
@@ -267,6 +274,126 @@ __global__ void __launch_bounds__(kPlanThreads) reserve_plan_kernel(PagesParams 
     if (threadIdx.x == 0) p.head[0] = n_moves;
 }
 
+// The same for up to 128 sequences whose rows fall into at most 32 entries each (a
+// step's): what each warp reads of its sequences stays in registers, wants and free
+// pages in shared memory.  (32 beams, caches cold: 6 us instead of 11.)
+constexpr int kSmallSeqs = 128;
+
+__global__ void __launch_bounds__(kPlanThreads) reserve_small_kernel(PagesParams p) {
+    constexpr int kWarps = kPlanThreads / 32, kEach = kSmallSeqs / kWarps;
+    __shared__ int warp_sums[32], offset[kSmallSeqs], list[kPlanThreads], n_moves, total;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int first_refs = static_cast<int>(threadIdx.x) < p.num_pages ? p.refs[threadIdx.x] : 1;
+    if (threadIdx.x == 0) n_moves = 0;
+    Range r[kEach];
+    bool in[kEach], copied[kEach];
+    int page[kEach], refs[kEach], start[kEach];
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) {
+        const int b = warp + k * kWarps;
+        in[k] = b < p.batch && range_of(p, b, r[k]);
+        start[k] = in[k] ? p.start[b] : 0;
+    }
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) {
+        const int j = in[k] ? r[k].first + lane : 0;
+        page[k] = in[k] && j <= r[k].last && j < r[k].held ? p.table[static_cast<long long>(warp + k * kWarps) * p.max_pages + j] : -1;
+        // (no entry at all is not an entry outside the pool)
+        if (in[k] && j <= r[k].last && j < r[k].held && !is_page(p, page[k])) page[k] = -1;
+    }
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) {
+        refs[k] = page[k] >= 0 ? p.refs[page[k]] : 0;
+        if (refs[k] > 1) {
+            p.page_a[page[k]] = 0;
+            p.page_b[page[k]] = -1;
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kEach; ++k)
+        if (refs[k] > 1) {
+            atomicAdd(p.page_a + page[k], 1);
+            atomicMax(p.page_b + page[k], warp + k * kWarps);
+        }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) {
+        const int b = warp + k * kWarps;
+        copied[k] = refs[k] > 1 && !(__ldcg(p.page_a + page[k]) == refs[k] && __ldcg(p.page_b + page[k]) == b);
+        const int copies = __popc(__ballot_sync(0xffffffffu, copied[k]));
+        if (lane == 0) offset[b] = in[k] ? copies + (r[k].last >= r[k].held ? r[k].last + 1 - r[k].held : 0) : 0;
+    }
+    __syncthreads();
+    if (warp == 0) {
+        // (sums: at most 128 sequences of 2^30 entries in all)
+        int v[kEach], sum = 0;
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) {
+            v[k] = offset[lane * kEach + k];
+            sum += v[k];
+        }
+        int x = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+        }
+        if (lane == 31) total = x;
+        x -= sum;
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) {
+            offset[lane * kEach + k] = x;
+            x += v[k];
+        }
+    }
+    __syncthreads();
+    const int want = total;
+    if (want == 0) {
+        if (threadIdx.x == 0) p.head[0] = 0;
+        return;
+    }
+    int32_t* fresh = want <= kPlanThreads ? list : p.old_table;
+    int found = 0;
+    for (int q0 = 0; q0 < p.num_pages && found < want; q0 += kPlanThreads) {
+        const int q = q0 + threadIdx.x;
+        const bool free = q < p.num_pages && (q0 == 0 ? first_refs : p.refs[q]) == 0;
+        int sum;
+        const int at = found + cta_scan(free ? 1 : 0, warp_sums, sum);
+        if (free && at < want) fresh[at] = q;
+        found += sum;
+    }
+    __syncthreads();
+    if (found < want) {
+        if (threadIdx.x == 0) {
+            p.head[0] = 0;
+            report(p.status, TQ_DEV_NO_PAGE);
+        }
+        return;
+    }
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) {
+        if (!in[k]) continue;
+        const int b = warp + k * kWarps;
+        int at = offset[b];
+        int32_t* row = p.table + static_cast<long long>(b) * p.max_pages;
+        const unsigned mask = __ballot_sync(0xffffffffu, copied[k]);
+        if (copied[k]) {
+            const int to = fresh[at + __popc(mask & ((1u << lane) - 1))], j = r[k].first + lane;
+            const long long below = static_cast<long long>(start[k]) - static_cast<long long>(j) * p.page_tokens;
+            p.moves[atomicAdd(&n_moves, 1)] = {page[k], to, static_cast<int>(max(0LL, min(below, static_cast<long long>(p.page_tokens))))};
+            row[j] = to;
+            atomicSub(p.refs + page[k], 1);
+        }
+        at += __popc(mask);
+        for (int j = r[k].held + lane; j <= r[k].last; j += 32) row[j] = fresh[at + j - r[k].held];
+        if (lane == 0 && r[k].last >= r[k].held) p.held[b] = r[k].last + 1;
+    }
+    for (int i = threadIdx.x; i < want; i += kPlanThreads) p.refs[fresh[i]] = 1;
+    __syncthreads();
+    if (threadIdx.x == 0) p.head[0] = n_moves;
+}
+
 // ---------------------------------------------------------------- compact --
 // page_a: for a moved page its place in the list of moves, for the others not set.
 __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(PagesParams p) {
@@ -391,7 +518,10 @@ cudaError_t launch_pages_fork(const PagesParams& p, int sms, cudaStream_t stream
 }
 
 cudaError_t launch_pages_reserve(const PagesParams& p, int sms, cudaStream_t stream) {
-    reserve_plan_kernel<<<1, kPlanThreads, 0, stream>>>(p);
+    if (p.batch <= kSmallSeqs && (p.n_rows + p.page_tokens - 2) / p.page_tokens + 1 <= 32)
+        reserve_small_kernel<<<1, kPlanThreads, 0, stream>>>(p);
+    else
+        reserve_plan_kernel<<<1, kPlanThreads, 0, stream>>>(p);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     // no more units of work than heads of the arrays of the pages that the rows touch

@@ -91,7 +91,7 @@ def i32(torch, x):
 
 
 @pytest.mark.parametrize("Hkv,D,page,bits", [(2, 64, 128, 4), (8, 128, 128, 4), (1, 64, 256, 8), (3, 256, 128, 8), (5, 128, 384, 4)])
-@pytest.mark.parametrize("B,per,pages", [(6, 8, 60), (1, 3, 4), (33, 300, 1500)])
+@pytest.mark.parametrize("B,per,pages", [(6, 8, 60), (1, 3, 4), (33, 300, 1500), (140, 9, 900)])
 def test_a_life_of_a_pool(B, per, pages, Hkv, D, page, bits):
     """Prompts, forks, steps, ends and compaction in random order."""
     torch = need_gpu()
@@ -354,3 +354,23 @@ def test_pools_past_32_bits():
     assert int(n_live) == 3 and c.block_table[:, :2].tolist() == [[0, 1], [0, 2]] and refs[:4].tolist() == [2, 1, 1, 0]
     for a in ARRAYS:
         assert torch.equal(getattr(c, a)[:2].view(torch.uint8), rows[a].view(torch.uint8))
+
+
+def test_long_prompts():
+    """Rows that fall into more entries than a step's."""
+    torch = need_gpu()
+    import int4_kv_cache_gb300 as tq
+
+    c, refs, held, lens, ws = pool(torch, tq, 3, pages=170, per=60)  # 157 in use at most
+    ref = Pool(c, refs, held, lens)
+    for start, n in (([0, -1, 0], 5000), ([100, 4990, 5100], 2200), ([0, 7300, 200], 1)):
+        tq.tq_pages_reserve(c, refs, held, i32(torch, start), n, ws)
+        assert ref.reserve(np.array(start), n)
+        ref.same(c, refs, held, lens)
+    src = np.array([2, 2, 2])
+    tq.tq_pages_fork(c, refs, held, i32(torch, src), ws)
+    ref.fork(src)
+    tq.tq_pages_reserve(c, refs, held, i32(torch, [0, 128, -1]), 4300, ws)  # whole shared prompts written over
+    assert ref.reserve(np.array([0, 128, -1]), 4300)
+    ref.lens = lens.cpu().numpy()
+    ref.same(c, refs, held, lens)
