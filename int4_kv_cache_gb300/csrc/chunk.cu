@@ -849,10 +849,11 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     uint8_t* qs = base;
     uint8_t* slots = base + C::kQ;
     uint8_t* ring = slots + C::kSlots * C::kSlot;
-    const bool pair = C::kStreams == 2 && p.pair;
-    const int ring_entries = C::kRing + (pair ? 0 : C::kMoreRing);
     Work w;
     if (!find_work<C::kTile>(p, p.rows_per_item, w)) return;  // the whole CTA
+    // (an item's rows may be fewer than its place has: one tile of them then)
+    const bool pair = C::kStreams == 2 && w.rows > kRowTile;
+    const int ring_entries = C::kRing + (pair ? 0 : C::kMoreRing);
     const int warp = threadIdx.x >> 5;
     if (warp == 16) {
         tmem_alloc(&bars.tmem, 512);

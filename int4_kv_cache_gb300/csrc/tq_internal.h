@@ -334,7 +334,6 @@ struct ChunkParams {
     int32_t m_items, rows_per_item, n_splits, whole;
     uint32_t group_magic;     // floor(t / group_q) = umulhi(t, magic) >> shift for 0 <= t < 2^31 (0: group_q = 1)
     int32_t group_shift;
-    int32_t pair;             // an item is two tiles of 128 rows (else one)
     float* part_m;            // [(items - whole) * n_splits][rows_per_item], log2 units (n_splits > 1)
     float* part_l;
     float* part_acc;          // [items * n_splits][rows_per_item][D]

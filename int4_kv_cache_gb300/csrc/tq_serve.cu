@@ -130,7 +130,6 @@ tq_status chunk(const Store& c, const tq_query_rows* q, const int32_t* q_lens, c
     const long long rows = static_cast<long long>(p.n) * p.group_q;
     const int tile = chunk_tile_tokens(c.head_dim);
     p.rows_per_item = chunk_rows(p.group_q, c.head_dim, p.n);
-    p.pair = p.rows_per_item == 256 ? 1 : 0;
     p.m_items = ceil_div(rows, p.rows_per_item);
     const long long items = static_cast<long long>(c.batch) * c.num_kv_heads * p.m_items;
     // the most keys an item sees: all of them, or a window behind each of its tokens
