@@ -120,6 +120,27 @@ def test_steep_scores():
             check(torch, got, reference(torch, c, q, [1500], [200], scale), [200])
 
 
+@pytest.mark.parametrize("paged", [False, True])
+@pytest.mark.parametrize("D,bits", [(64, 8), (128, 4), (256, 4)])
+def test_one_row_either_way(D, bits, paged):
+    """One row a sequence is the decode, with row counts it is not: the same rows, zeros and reports."""
+    torch = need_gpu()
+    import int4_kv_cache_gb300 as tq
+
+    lens = [500, 0, 1, 700, -3]  # the last two: past max_seq_len, below none
+    held = [500, 0, 1, 512, 0]
+    c = make_cache(tq, torch, 5, 2, D, 512, bits, paged, seed=D)
+    q = queries(torch, (5, 8, 1, D), 11)
+    for scale in (1 / math.sqrt(D), -0.05):
+        for full in (False, True):
+            ref = reference(torch, c, q, held, [1] * 5, scale, full=full)
+            for rows in (None, [1] * 5):
+                st = torch.zeros(1, dtype=torch.int32, device="cuda")
+                out = attend(torch, tq, c, q, lens, rows, full=full, scale=scale, max_len=512, status=st)
+                check(torch, out, ref, [1] * 5)
+                assert int(st) == tq.TQ_DEV_SEQ_LEN and not bool(out[1].any()) and not bool(out[4].any())
+
+
 def test_binding_refusals():
     """What the binding refuses before the library is called."""
     torch = need_gpu()
