@@ -36,11 +36,14 @@ size_t chunk_bytes(int32_t batch, int32_t hq, int32_t hkv, int32_t head_dim, int
 }
 
 // Items with a CTA each, and how many runs the keys of each of the others are cut into.
-// Times in tiles: a CTA costs its tiles and some four more (start, first copies,
-// output), merging a launch and the parts' way through memory.  Either all items are
-// cut, or those that are left behind the last full wave of whole ones: 512 items of 508
-// tiles on 152 SMs take 3 whole waves and the rest of their time in an eighth of
-// another one, where a fourth whole wave would leave most SMs idle.
+// Times in tiles: a CTA costs its tiles and some six more (start, first copies, output;
+// with four in their place 1,024 tokens of two sequences over 8,192 were cut more than
+// pays: 229 us for 210, and 300 of three over 5,000 at head_dim 256: 191 for 179), merging
+// a launch and the parts' way through memory.  Either all items are cut, or those that
+// are left behind the last full wave of whole ones: 512 items of 508 tiles on 152 SMs
+// take 3 whole waves and the rest of their time in an eighth of another one, where a
+// fourth whole wave would leave most SMs idle.
+constexpr int kCtaTiles = 6;
 struct ChunkPlan {
     long long whole;
     int splits;
@@ -54,7 +57,7 @@ ChunkPlan chunk_plan(long long items, int tiles, int sms) {
         if (full && (whole == 0 || rest == 0)) continue;
         for (int n = 1; n <= tiles && (n == 1 || rest * n <= kMaxChunkParts); ++n) {
             const long long waves = (rest * n + sms - 1) / sms;
-            const long long c = whole / sms * (tiles + 4) + waves * ((tiles + n - 1) / n + 4) + (n > 1 ? 4 + n / 8 : 0);
+            const long long c = whole / sms * (tiles + kCtaTiles) + waves * ((tiles + n - 1) / n + kCtaTiles) + (n > 1 ? 4 + n / 8 : 0);
             if (cost < 0 || c < cost) {
                 cost = c;
                 best = {whole, n};
