@@ -117,7 +117,8 @@ tq_status chunk(const Store& c, const tq_query_rows* q, const int32_t* q_lens, c
     p.max_seq_len = max_seq_len;
     p.capacity = c.capacity;
     p.bits = c.bits;
-    p.window = window;
+    // (a window past the longest sequence is one of that length, so that positions less a window stay within 32 bits)
+    p.window = window = window < max_seq_len ? window : max_seq_len;
     p.full = (flags & TQ_CHUNK_FULL) ? 1 : 0;
     p.rotate_q = (flags & TQ_ROTATE_K) ? 1 : 0;
     p.rotate_out = (flags & TQ_ROTATE_V) ? 1 : 0;
