@@ -685,7 +685,10 @@ tq_status tq_paged_kv_evict(const tq_paged_kv_cache* src, const tq_paged_kv_cach
  * attention over the dequantised cache a score is off by 2^-11 attn_scale
  * sum_d |q_d K_d| at most, and an output by what such scores make of it, 2^-10
  * sum_t p_t |V_t| and its own rounding (all rows together: 4e-4 rel-L2 for normally
- * distributed rows, up to 1.5e-3 with a key channel twenty times as large).  Cached rows whose scale or bias is not finite leave the
+ * distributed rows, up to 1.5e-3 with a key channel twenty times as large).  Weights
+ * below 2^-21 of a row's largest, p_max, have fewer bits: the tokens t that hold them
+ * add up to 2^-32 p_max sum_t |V_t|.  Scores from some 10^6 on in magnitude leave fp32 too few
+ * bits for a softmax: rows that have such are undefined.  Cached rows whose scale or bias is not finite leave the
  * outputs of the rows that attend to them undefined, and no others; so do query rows
  * that are not finite for themselves.
  * One contiguous row per sequence (n = 1, no q_lens, no window) is that decode itself.

@@ -3,7 +3,7 @@
 // only), or every row over the whole sequence.  For row r = (token i, head g) of
 // (sequence b, kv head h), r = i * G + g:
 //   out_r = sum_t p_t V_t / sum_t p_t,  p_t = 2^(c q_r.K_t - m_r),  lo_i <= t < hi_i,
-// with c = attn_scale log2(e) and m_r a running maximum.  Rows of all the heads
+// with c = attn_scale log2(e) and m_r a running maximum less seven.  Rows of all the heads
 // that share a kv head are rows of one matrix, so every cached key and value is
 // unpacked once for 256 of them.
 //
@@ -19,13 +19,17 @@
 // S is read into registers as soon as it is there, so that one place for it serves both
 // row tiles in turn and their scores run ahead of the softmax.  Up to 128 rows (a few
 // tokens) make one tile; the two accumulators then take every other tile of keys and are
-// merged in the end.  O is rescaled only when a row's maximum grows by more than 2^8 (P
-// stays below that, well inside fp16's range; the published conditional rescaling of
-// online softmax), which is rare after the first tiles.  Where there are few items
+// merged in the end.  P starts at 2^7, and O is rescaled only when a row's maximum grows by
+// more than 2^8 (the published conditional rescaling of online softmax), which is rare
+// after the first tiles: P uses fp16's range up to 2^15, so that weights down to 2^-21 of a
+// row's largest keep all their bits and those down to 2^-32 of it are more than zero.  (With P
+// from 1 up, a key that took most of a row's weight left nothing of the others 25
+// powers of two below it, however many.)  Where there are few items
 // for the SMs their keys are cut into runs, whose states a second kernel merges.
 //
 // Rounding: cached values enter the products as fp16 (half a step of 2^-11, what
-// the tensor core takes), P as fp16; S, O, maxima and sums are fp32.
+// the tensor core takes), P as fp16 (the sums take it unrounded); S, O, maxima and sums
+// are fp32.
 //
 // What bounds it (GB300, 64 query and 8 kv heads of 128, int4): for long chunks the
 // turn of the one place for S (a product of 512 cycles, then some 800 of commits, waits
@@ -47,7 +51,9 @@ namespace {
 
 constexpr int kThreads = 640;       // 8 softmax warps, 8 that unpack, 2 that issue products, one that copies
 constexpr int kRowTile = 128;
-constexpr float kLazy = 8.f;  // log2 of how far P may grow before O is rescaled
+constexpr float kHead = 7.f;  // log2 of a row's largest P when its maximum is new
+constexpr float kLazy = 8.f;  // log2 of how far P may grow from there before O is rescaled
+static_assert(kHead + kLazy <= 15.f, "P in fp16");
 
 template <int D, int BITS>
 struct Cfg {
@@ -605,7 +611,7 @@ __device__ __forceinline__ void load_query_rotated(const ChunkParams& p, const W
 }
 
 struct State {
-    float m, l;  // maximum that P counts from (log2 units, -inf: none yet), sum
+    float m, l;  // what P counts from (log2 units: a maximum less kHead, -inf: none yet), sum
 };
 
 // One accumulator's turns: all, or (two accumulators) those of its parity; a thread a row.
@@ -641,7 +647,7 @@ __device__ __forceinline__ bool softmax_loop(const ChunkParams& p, const Work& w
             float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
             for (int x = 4; x < N; x += 2) mx[(x >> 1) & 3] = max3(mx[(x >> 1) & 3], s[x], s[x + 1]);
-            const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * c;
+            const float top = fmaf(fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]), c, -kHead);
             const bool fresh = n < C::kStreams;  // nothing in O yet
             const bool grow = top > (fresh ? st.m : st.m + kLazy);
             if (__any_sync(0xffffffffu, grow)) {

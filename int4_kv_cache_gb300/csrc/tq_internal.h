@@ -334,7 +334,7 @@ struct ChunkParams {
     int32_t m_items, rows_per_item, n_splits, whole;
     uint32_t group_magic;     // floor(t / group_q) = umulhi(t, magic) >> shift for 0 <= t < 2^31 (0: group_q = 1)
     int32_t group_shift;
-    float* part_m;            // [(items - whole) * n_splits][rows_per_item], log2 units (n_splits > 1)
+    float* part_m;            // [(items - whole) * n_splits][rows_per_item], log2 units: what the part's weights count from (n_splits > 1)
     float* part_l;
     float* part_acc;          // [items * n_splits][rows_per_item][D]
 };
