@@ -687,13 +687,15 @@ tq_status tq_paged_kv_evict(const tq_paged_kv_cache* src, const tq_paged_kv_cach
  * sum_t p_t |V_t| and its own rounding (all rows together: 4e-4 rel-L2 for normally
  * distributed rows, up to 1.5e-3 with a key channel twenty times as large).  Weights
  * below 2^-21 of a row's largest, p_max, have fewer bits: the tokens t that hold them
- * add up to 2^-32 p_max sum_t |V_t|.  Scores from some 10^6 on in magnitude leave fp32 too few
+ * add up to 2^-32 p_max sum_t |V_t|.  The tensor cores' sums are cut off, not rounded: at
+ * most 2^-11 sum_t p_t |V_t| of an output (5e-5 of it where all values have one sign), whatever the length.  Scores from some 10^6 on in magnitude leave fp32 too few
  * bits for a softmax: rows that have such are undefined.  Cached rows whose scale or bias is not finite leave the
  * outputs of the rows that attend to them undefined, and no others; so do query rows
  * that are not finite for themselves.
  * One contiguous row per sequence (n = 1, no q_lens, no window) is that decode itself.
  * workspace: tq_chunk_workspace_bytes(...) bytes, 256-byte aligned, one per call in
- * flight (not looked at where n = 0); it also serves fewer rows, sequences and tokens of
+ * flight (not looked at where n = 0; past 8,192 tokens it holds the output's rows in
+ * fp32); it also serves fewer rows, sequences and tokens of
  * the same heads.  n = 0 launches nothing.  batch and kv heads up to
  * 65,535, n * num_heads up to 2^28, caches up to 2^30 tokens. */
 #define TQ_CHUNK_FULL 0x200u

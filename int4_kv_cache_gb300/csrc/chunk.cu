@@ -27,6 +27,9 @@
 // powers of two below it, however many.)  Where there are few items
 // for the SMs their keys are cut into runs, whose states a second kernel merges.
 //
+// An accumulator takes 8,192 keys at most before it is emptied into sums in memory: the
+// tensor cores' sums are not rounded to nearest, and what they lose grows with the length.
+//
 // Rounding: cached values enter the products as fp16 (half a step of 2^-11, what
 // the tensor core takes), P as fp16 (the sums take it unrounded); S, O, maxima and sums
 // are fp32.
@@ -68,6 +71,8 @@ struct Cfg {
     static constexpr int kCodes = kTile * D * BITS / 8;
     static constexpr int kScales = kTile * kBlocks * 2;       // scales (and as many biases) of a tile
     static constexpr int kEntry = kCodes + 2 * kScales;
+    static constexpr int kChain = kChunkChainKeys / kTile;    // turns of an accumulator between its emptyings
+    static_assert((kChain & (kChain - 1)) == 0, "a mask tells where a chain begins");
     static constexpr int kRing = D == 64 ? 6 : (BITS == 8 ? 3 : 6);
     static constexpr int kQ = kStreams * kRowTile * D * 2;
     // one row tile: the other's place holds more of the ring (few rows: what bounds is how
@@ -526,7 +531,7 @@ __device__ __forceinline__ bool outputs_role(const ChunkParams& p, const Work& w
         tc_fence_after();
         uint32_t b = v_op + in.slot * (C::kSlot >> 4), a = tmem + C::kP + (n & 1) * C::kPStep;
         const uint32_t o = tmem + C::kO + (C::kStreams == 2 ? (n & 1) * D : 0);
-        const bool add = n >= C::kStreams;
+        const bool add = (n / C::kStreams & (C::kChain - 1)) != 0;  // (emptied accumulators begin anew)
         if (elect_one()) {
 #pragma unroll 1
             for (int i = 0; i < C::kTile / 64; ++i) {
@@ -614,6 +619,71 @@ struct State {
     float m, l;  // what P counts from (log2 units: a maximum less kHead, -inf: none yet), sum
 };
 
+// Where a thread's row of an accumulator is emptied into: its sums as float4 [D / 4][128 rows],
+// then what its weights count from and their sum, [2][128 rows].
+template <int D, int BITS>
+__device__ __forceinline__ float* chain_at(const ChunkParams& p, int stream) {
+    return p.chains + (static_cast<long long>(blockIdx.x) * Cfg<D, BITS>::kStreams + stream) * (kRowTile * (D + 2));
+}
+
+// Empties an accumulator: its sums join those of the chains before.  A tensor core cuts
+// sums off instead of rounding them: a step of 16 keys took 1.0e-7 off a sum of positive
+// values (262,144 keys in one chain: 1.7e-3 of the output); a chain of 8,192 keys takes
+// 5e-5, and chains are added in fp32 that rounds to nearest.  The sums count from where the
+// first chain did, so that joining them reads nothing of them (loads in place of reductions,
+// with the registers they take, made calls 5 to 12 % longer, this 0 to 3.5 %); weights that have
+// grown by more than 2^64 start them anew (what they held is then below 2^-56 of the
+// largest weight a key).
+template <int D, int BITS>
+__device__ __forceinline__ void empty_chain(const ChunkParams& p, uint32_t oa, int stream, bool first, State& st) {
+    float* at = chain_at<D, BITS>(p, stream);
+    float* own = at + kRowTile * D + (threadIdx.x & 127);
+    const float up = first ? INFINITY : st.m - own[0];
+    const bool anew = !(up <= 64.f);
+    const float g = anew ? 1.f : ex2_approx(up);
+    float4* sums = reinterpret_cast<float4*>(at) + (threadIdx.x & 127);
+#pragma unroll 1
+    for (int x = 0; x < D; x += 16, sums += 4 * kRowTile) {
+        float o[16];
+        tmem_ld16(oa + x, o);
+        tmem_wait_ld();
+        if (anew) {
+#pragma unroll
+            for (int y = 0; y < 4; ++y) sums[y * kRowTile] = make_float4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
+        } else {
+#pragma unroll
+            for (int y = 0; y < 4; ++y) red_add4(sums + y * kRowTile, o[4 * y] * g, o[4 * y + 1] * g, o[4 * y + 2] * g, o[4 * y + 3] * g);
+        }
+    }
+    if (anew) own[0] = st.m;
+    own[kRowTile] = anew ? st.l : fmaf(st.l, g, own[kRowTile]);
+    st.l = 0.f;
+}
+
+// The end of an accumulator that was emptied on its way: its sums come back into it.
+template <int D, int BITS>
+__device__ __forceinline__ void restore_chains(const ChunkParams& p, uint32_t oa, int stream, State& st) {
+    __threadfence();  // the thread's own reductions are in what it reads
+    const float* at = chain_at<D, BITS>(p, stream);
+    const float* own = at + kRowTile * D + (threadIdx.x & 127);
+    const float g = own[0] == -INFINITY ? 0.f : ex2_approx(own[0] - st.m);
+    st.l = fmaf(own[kRowTile], g, st.l);
+    const float4* sums = reinterpret_cast<const float4*>(at) + (threadIdx.x & 127);
+#pragma unroll 1
+    for (int x = 0; x < D; x += 16, sums += 4 * kRowTile) {
+        float4 s[4];
+#pragma unroll
+        for (int y = 0; y < 4; ++y) s[y] = __ldcg(sums + y * kRowTile);
+        float o[16];
+        tmem_ld16(oa + x, o);
+        tmem_wait_ld();
+#pragma unroll
+        for (int y = 0; y < 16; ++y) o[y] = fmaf(reinterpret_cast<const float*>(s)[y], g, o[y]);
+        tmem_st16(oa + x, reinterpret_cast<const uint32_t*>(o));
+    }
+    tmem_wait_st();
+}
+
 // One accumulator's turns: all, or (two accumulators) those of its parity; a thread a row.
 template <int D, int BITS>
 __device__ __forceinline__ bool softmax_loop(const ChunkParams& p, const Work& w, uint32_t bars, uint32_t tmem, int stream, bool pair, bool active, int lo, int hi, State& st) {
@@ -648,18 +718,22 @@ __device__ __forceinline__ bool softmax_loop(const ChunkParams& p, const Work& w
 #pragma unroll
             for (int x = 4; x < N; x += 2) mx[(x >> 1) & 3] = max3(mx[(x >> 1) & 3], s[x], s[x + 1]);
             const float top = fmaf(fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]), c, -kHead);
-            const bool fresh = n < C::kStreams;  // nothing in O yet
+            const bool fresh = n < C::kStreams;                                             // nothing in O yet
+            const bool begins = (n & (C::kChain * C::kStreams - 1)) < C::kStreams;          // a chain: the next product replaces O
             const bool grow = top > (fresh ? st.m : st.m + kLazy);
-            if (__any_sync(0xffffffffu, grow)) {
-                const float f = grow ? ex2_approx(st.m - top) : 1.f;
-                if (grow) st.m = top;
-                st.l *= f;
+            if (begins || __any_sync(0xffffffffu, grow)) {
+                const uint32_t oa = tmem + C::kO + (C::kStreams == 2 ? stream * D : 0);
                 if (!fresh) {
                     // O holds the products of the turns before: all of them have to be over
                     const uint32_t before = C::kStreams == 1 ? n - 1 : n - 2;
                     if (!wait(bars, kPvDone + (before & 1) * 8, (before >> 1) & 1, p.status)) return false;
                     tc_fence_after();
-                    const uint32_t oa = tmem + C::kO + (C::kStreams == 2 ? stream * D : 0);
+                    if (begins) empty_chain<D, BITS>(p, oa, stream, n / C::kStreams == C::kChain, st);
+                }
+                const float f = grow ? ex2_approx(st.m - top) : 1.f;
+                if (grow) st.m = top;
+                st.l *= f;
+                if (!begins) {
 #pragma unroll 1
                     for (int x = 0; x < D; x += 16) {
                         float o[16];
@@ -739,10 +813,11 @@ __device__ __forceinline__ void softmax_role(const ChunkParams& p, const Work& w
     // is left that reads them).
     const bool merge = !pair && C::kStreams == 2 && turns > 1;
     const uint32_t oa = tmem + C::kO + (C::kStreams == 2 ? stream * D : 0);
+    if (ok && active && last >= C::kChain * C::kStreams) restore_chains<D, BITS>(p, oa, stream, st);
+    float f = 1.f, fo = 0.f, m = st.m, l = st.l;
     asm volatile("barrier.cta.sync 9, %0;" ::"n"(C::kSoftmax) : "memory");
     float* apart = reinterpret_cast<float*>(qs);  // [D][129] of the second accumulator
     constexpr int kPad = kRowTile + 1;
-    float f = 1.f, fo = 0.f, m = st.m, l = st.l;
     if (merge) {
         if (stream == 1 && ok && active) {
             shared->max[row] = st.m;
@@ -1001,7 +1076,9 @@ cudaError_t launch_dim(const ChunkParams& p, cudaStream_t stream) {
 
 }  // namespace
 
-int chunk_tile_tokens(int head_dim) { return head_dim == 256 ? 64 : 128; }
+int chunk_tile_tokens(int head_dim) { return head_dim == 256 ? Cfg<256, 4>::kTile : Cfg<128, 4>::kTile; }
+
+size_t chunk_chain_floats(int head_dim) { return static_cast<size_t>(head_dim == 256 ? Cfg<256, 4>::kStreams : Cfg<128, 4>::kStreams) * kRowTile * (head_dim + 2); }
 
 cudaError_t launch_chunk(const ChunkParams& p, int head_dim, cudaStream_t stream) {
     if (head_dim == 64) return launch_dim<64>(p, stream);

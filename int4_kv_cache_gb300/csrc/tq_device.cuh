@@ -97,6 +97,11 @@ __device__ __forceinline__ void bulk_store_wait() {
     asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group.read 0;" ::: "memory");
 }
 
+// Four fp32 values added to 16 aligned bytes of global memory (rounded to nearest).
+__device__ __forceinline__ void red_add4(float4* at, float a, float b, float c, float d) {
+    asm volatile("red.relaxed.gpu.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(at), "f"(a), "f"(b), "f"(c), "f"(d) : "memory");
+}
+
 // 16 bytes global -> shared (both 16-byte aligned), asynchronous; copies are
 // waited for in committed groups, each thread for its own: until at most N of
 // its newest groups are outstanding.

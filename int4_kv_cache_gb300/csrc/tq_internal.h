@@ -336,7 +336,8 @@ struct ChunkParams {
     int32_t group_shift;
     float* part_m;            // [(items - whole) * n_splits][rows_per_item], log2 units: what the part's weights count from (n_splits > 1)
     float* part_l;
-    float* part_acc;          // [items * n_splits][rows_per_item][D]
+    float* part_acc;          // [(items - whole) * n_splits][rows_per_item][D]
+    float* chains;            // [CTAs][chunk_chain_floats]: what accumulators were emptied into (runs longer than a chain)
 };
 
 // Pages of a pool (pages.cu).
@@ -395,6 +396,8 @@ inline cudaError_t launch_after(void (*kernel)(Params), unsigned grid, int threa
 // Launchers (return the cudaError_t of the launch).
 cudaError_t launch_chunk(const ChunkParams& p, int head_dim, cudaStream_t stream);
 int chunk_tile_tokens(int head_dim);  // keys per tile
+constexpr int kChunkChainKeys = 8192;    // most keys that an accumulator takes in one chain
+size_t chunk_chain_floats(int head_dim);  // what a CTA's accumulators are emptied into
 cudaError_t launch_pages_fork(const PagesParams& p, int sms, cudaStream_t stream);
 cudaError_t launch_pages_reserve(const PagesParams& p, int sms, cudaStream_t stream);
 cudaError_t launch_pages_compact(const PagesParams& p, int sms, cudaStream_t stream);

@@ -28,9 +28,20 @@ size_t chunk_part_rows(int32_t batch, int32_t hq, int32_t hkv, int32_t head_dim,
     return static_cast<size_t>(items > most / per / tiles ? most : items * tiles * per);
 }
 
+size_t part_bytes(size_t rows, int32_t head_dim) { return 2 * align256(rows * sizeof(float)) + align256(rows * head_dim * sizeof(float)); }
+
+// What the CTAs' accumulators are emptied into, where a run can be longer than a chain: a
+// place for each whole item and for each part of those that are cut into runs of more than a chain.
+size_t chain_bytes(int32_t batch, int32_t hq, int32_t hkv, int32_t head_dim, int32_t n, int32_t max_seq_len) {
+    const long long chains = ceil_div(max_seq_len, kChunkChainKeys), per = chunk_rows(hq / hkv, head_dim, n);
+    if (chains == 1) return 0;
+    const long long items = static_cast<long long>(batch) * hkv * ((static_cast<long long>(n) * (hq / hkv) + per - 1) / per);
+    const long long cut = items < kMaxChunkParts / chains ? items * chains : kMaxChunkParts;
+    return static_cast<size_t>(items + cut) * chunk_chain_floats(head_dim) * sizeof(float);
+}
+
 size_t chunk_bytes(int32_t batch, int32_t hq, int32_t hkv, int32_t head_dim, int32_t n, int32_t max_seq_len) {
-    const size_t rows = chunk_part_rows(batch, hq, hkv, head_dim, n, max_seq_len);
-    const size_t parts = 2 * align256(rows * sizeof(float)) + align256(rows * head_dim * sizeof(float));
+    const size_t parts = part_bytes(chunk_part_rows(batch, hq, hkv, head_dim, n, max_seq_len), head_dim) + chain_bytes(batch, hq, hkv, head_dim, n, max_seq_len);
     const size_t decode = tq_sdpa_workspace_bytes(batch, hq, hkv, head_dim, max_seq_len, TQ_DEFAULT_CHUNK);
     return parts > decode ? parts : decode;
 }
@@ -153,6 +164,7 @@ tq_status chunk(const Store& c, const tq_query_rows* q, const int32_t* q_lens, c
     p.part_m = reinterpret_cast<float*>(ws);
     p.part_l = reinterpret_cast<float*>(ws + align256(part_rows * sizeof(float)));
     p.part_acc = reinterpret_cast<float*>(ws + 2 * align256(part_rows * sizeof(float)));
+    p.chains = reinterpret_cast<float*>(ws + part_bytes(part_rows, c.head_dim));
     return cuda_status(launch_chunk(p, c.head_dim, stream));
 }
 

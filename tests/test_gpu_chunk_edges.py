@@ -36,7 +36,8 @@ def steps_of_weight(torch, tq, D, bits, L, n, G, keys, seed):
     c.v_codes.copy_(torch.randint(0, 256, c.v_codes.shape, generator=g, device="cuda", dtype=torch.uint8))
     c.v_scale.fill_(1 / 8)
     c.v_bias.fill_(0.5)
-    c.k_bias[0, 0] = keys.half().unsqueeze(-1)
+    keys = keys.half()  # (steps of 1/16 up to 128, of 1/4 up to 512)
+    c.k_bias[0, 0] = keys.unsqueeze(-1)
     none = keys == keys.max()  # what holds most of the weight has nothing to add
     for a in (c.v_scale, c.v_bias):
         a[0, 0, none] = 0
@@ -86,3 +87,74 @@ def test_maxima_that_grow(D, bits, up):
     assert bool(torch.isfinite(got).all())
     bound = want.abs() * 2 ** -11 + weight * (2 ** -11 + 2 ** -12 + 2 ** -16) + total * 2.0 ** -32
     assert float(((got.double() - want).abs() / bound).max()) <= 1.0
+
+
+# A chain of an accumulator is 8,192 keys, 512 steps of 17 terms (16 products and the sum so far), each cut off by less
+# than a unit of fp32's last place, 2^-23 of the sum so far, which is half the whole one on average.
+CHAIN = 512 * 17 * 2.0 ** -23 / 2
+
+
+@pytest.mark.parametrize("D,bits,Hkv,n,G,L", [(128, 4, 1, 4864, 8, 262144), (64, 8, 1, 4864, 8, 262144), (256, 4, 1, 2432, 8, 262144),  # uncut
+                                              (128, 8, 1, 3200, 8, 65536), (256, 8, 1, 1600, 8, 65536),  # cut into runs that are longer than a chain
+                                              (64, 4, 160, 3, 8, 65536), (128, 4, 160, 1, 8, 65536)])    # one row tile, keys in turn to two accumulators
+def test_long_runs(D, bits, Hkv, n, G, L):
+    """Values around 1 under weights of many sizes: nothing adds up along a sequence.  (Products are exact in fp16 but for
+    the weights; every row is the same one.)"""
+    torch = need_gpu()
+    import int4_kv_cache_gb300 as tq
+
+    c = tq.KVCache(1, Hkv, D, L, bits=bits)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(L + D)
+    for a in (c.k_codes, c.v_codes):
+        a.copy_(torch.randint(0, 256, a[:, :1].shape, generator=g, device="cuda", dtype=torch.uint8).expand_as(a))
+    step = 1 / 16 if bits == 4 else 1 / 256
+    for a, x in ((c.k_scale, 4 * step), (c.k_bias, -2.0), (c.v_scale, step), (c.v_bias, 0.5)):
+        a.fill_(x)
+    q = (torch.randn((1, 1, 1, D), generator=g, device="cuda").half() * 0.3).expand(1, Hkv * G, n, D)
+    rows = [n] if n == 1 else None  # (single rows as a chunk's)
+    got = attend(torch, tq, c, q, [L], rows, full=True)[0].double()
+
+    def exact(codes, scale, bias):
+        codes = torch.stack((codes & 15, codes >> 4), -1).flatten(-2) if bits == 4 else codes
+        return codes.double() * scale + bias
+
+    p = torch.softmax(exact(c.k_codes[0, 0], 4 * step, -2.0) @ q[0, 0, 0].double() / math.sqrt(D), 0)
+    want = p @ exact(c.v_codes[0, 0], step, 0.5)  # positive values: also the weights' sum of them
+    assert float(((got - want).abs() / want).max()) <= 2 * 2 ** -11 + CHAIN + 2 ** -16
+    # Signed, over all channels: half of what is cut off, and what is left of 64 or more roundings of the output, even
+    # over half a step either way (six times 2^-11 / sqrt(3 * 64)).
+    assert abs(float((got - want).mean() / want.mean())) <= CHAIN / 2 + 6 * 2 ** -11 / math.sqrt(3 * 64)
+
+
+@pytest.mark.parametrize("rise", [30, -30, 0.5, 90, 400])
+@pytest.mark.parametrize("D,bits,n,G", [(64, 8, 4864, 8), (128, 4, 4864, 8), (256, 4, 2432, 8), (128, 4, 3200, 8), (128, 4, 1, 4)])
+def test_long_runs_of_growing_weights(D, bits, n, G, rise):
+    """Weights that grow, or fall, over five chains, also by more than fp32 holds."""
+    torch = need_gpu()
+    import int4_kv_cache_gb300 as tq
+
+    L = 40960
+    keys = (torch.arange(L, device="cuda") * (16 * rise) / L).floor() / 16
+    got, want, weight, total = steps_of_weight(torch, tq, D, bits, L, n, G, keys, n)
+    bound = want.abs() * 2 ** -11 + weight * (2 ** -11 + CHAIN + 2 ** -16) + total * 2.0 ** -32
+    assert float(((got.double() - want).abs() / bound).max()) <= 1.0
+
+
+@pytest.mark.parametrize("D,n", [(64, 4864), (128, 4864), (256, 2432)])
+def test_workspace_of_long_runs_holds_anything(D, n):
+    """What accumulators are emptied into is written before it is read."""
+    torch = need_gpu()
+    import int4_kv_cache_gb300 as tq
+
+    L = 30000
+    c = make_cache(tq, torch, 1, 1, D, L, seed=n)
+    q = queries(torch, (1, 8, n, D), n)
+    lens = torch.tensor([L], dtype=torch.int32, device="cuda")
+    ws = tq.chunk_workspace(1, 8, 1, D, n, L)
+    outs = []
+    for fill in (0, 0xFF, 0x7F):
+        ws.fill_(fill)
+        outs.append(tq.tq_sdpa_chunk(c, q, lens, L, 0.1, ws))
+    assert bool(torch.isfinite(outs[0]).all()) and torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+    check(torch, outs[0][:, -64:], reference(torch, c, q[:, :, -64:], [L], [64], 0.1), [64])
