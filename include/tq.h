@@ -716,6 +716,18 @@ tq_status tq_paged_sdpa_chunk(const tq_paged_kv_cache* cache, const tq_query_row
                               int32_t window, uint32_t flags, void* workspace, size_t workspace_bytes,
                               uint16_t* out, int32_t* status, void* stream);
 
+/* Diagnostic of the failure path inside the kernel of tq_sdpa_chunk: the same call
+ * (causal, no q_lens, no window, every n in tiles) whose CTAs bring `copies` tiles of
+ * keys and values each (0 and up) and then no more.  What waits for the next ones gives up
+ * after limit_us microseconds (1..100000; tq_sdpa_chunk itself: 2 s) and sets
+ * TQ_DEV_TIMEOUT in *status (not NULL); nothing is in flight when the kernel ends, and
+ * what it wrote to out is undefined.  With no fewer copies than there are (two for each
+ * 128 tokens, or 64 at head_dim 256) it is that call's result. */
+tq_status tq_chunk_timeout_selftest(const tq_kv_cache* cache, const tq_query_rows* q, const int32_t* seq_lens,
+                                    int32_t max_seq_len, float attn_scale, uint32_t limit_us, int32_t copies,
+                                    void* workspace, size_t workspace_bytes, uint16_t* out, int32_t* status,
+                                    void* stream);
+
 /* --------------------------------------------------------- pages of a pool --
  * Keeps account of a paged cache's pages on the device.  The caller owns
  *   refs   int32 [num_pages]: how many table entries name each page (0: free); a

@@ -25,6 +25,7 @@ __all__ = [
     "TQ_DEV_BLOCK", "TQ_ROPE_PAIRS", "TQ_ROPE_INVERSE", "tq_rope_axes", "block_bounds", "tq_kv_block_bounds",
     "sparse_workspace", "tq_select_blocks", "tq_sdpa_blocks_decode", "tq_sparse_decode", "weights_workspace",
     "tq_sdpa_decode_weights", "tq_kv_evict", "TQ_DEV_NO_PAGE", "TQ_DEV_SOURCE", "TQ_CHUNK_FULL", "chunk_workspace", "tq_sdpa_chunk",
+    "tq_chunk_timeout_selftest",
     "page_state", "pages_workspace", "tq_pages_fork", "tq_pages_reserve", "tq_pages_compact",
 ]
 
@@ -157,6 +158,7 @@ def lib() -> ctypes.CDLL:
         sig["tq_sparse_workspace_bytes"] = ([i32] * 7, sz)
         sig["tq_select_blocks"] = ([P, P] + [i32] * 5 + [P] + [i32] * 5 + [u32, P, sz, P, P, P], i32)
         sig["tq_weights_workspace_bytes"] = ([i32] * 5, sz)
+        sig["tq_chunk_timeout_selftest"] = ([C, ctypes.POINTER(tq_query_rows), P, i32, f32, u32, i32, P, sz, P, P, P], i32)
         sig["tq_chunk_workspace_bytes"] = ([i32] * 6, sz)
         sig["tq_pages_workspace_bytes"] = ([i32] * 3, sz)
         sig["tq_pages_fork"] = ([PC, P, P, P, P, P, sz, P, P], i32)
@@ -902,6 +904,27 @@ def tq_sdpa_chunk(cache, q: torch.Tensor, seq_lens: torch.Tensor, max_seq_len: i
         cache.ref(), rows, _at(q_lens), seq_lens.data_ptr(), int(max_seq_len), float(attn_scale), int(window), int(flags),
         workspace.data_ptr(), workspace.numel(), out.data_ptr(), _at(status), on))
     return out
+
+
+def tq_chunk_timeout_selftest(cache: KVCache, q: torch.Tensor, seq_lens: torch.Tensor, max_seq_len: int, attn_scale: float,
+                              limit_us: int, copies: int, workspace: torch.Tensor, out: torch.Tensor, status: torch.Tensor, stream=None) -> None:
+    """The diagnostic of the chunk kernel's bounded waits: tq_sdpa_chunk of contiguous rows q [B, Hq, n, D] over a contiguous
+    cache whose CTAs copy ``copies`` tiles and then no more; the waits for the next ones give up after ``limit_us``."""
+    _need(q, torch.float16, "q")
+    if cache.paged or q.dim() != 4 or q.shape[0] != cache.batch or q.shape[3] != cache.head_dim:
+        raise ValueError(f"q must be [B, Hq, n, D] of a contiguous cache's B and D; got {tuple(q.shape)}")
+    b, hq, n, d = q.shape
+    _need_lens(seq_lens, b, "seq_lens")
+    _need(workspace, torch.uint8, "workspace")
+    _need(out, torch.float16, "out")
+    _need(status, torch.int32, "status")
+    if out.shape != (b, n, hq, d):
+        raise ValueError(f"out must be [B, n, Hq, D] = {(b, n, hq, d)}; got {tuple(out.shape)}")
+    on = _on(stream, cache.buffer, q, seq_lens, workspace, out, status)
+    rows = tq_query_rows(q.data_ptr(), hq * n * d, n * d, d, hq, n)
+    _check("tq_chunk_timeout_selftest", lib().tq_chunk_timeout_selftest(
+        cache.ref(), rows, seq_lens.data_ptr(), int(max_seq_len), float(attn_scale), int(limit_us), int(copies), workspace.data_ptr(),
+        workspace.numel(), out.data_ptr(), status.data_ptr(), on))
 
 
 def page_state(cache):

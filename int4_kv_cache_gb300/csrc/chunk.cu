@@ -228,23 +228,31 @@ __device__ __forceinline__ bool over(uint32_t bar, uint32_t parity) {
     return ok != 0;
 }
 
-// Waits for a phase of the barrier at `bar`; false when it took too long or another
-// warp has given up.  (The timer is read rarely: that takes longer than most waits.)
-__device__ __forceinline__ bool wait(uint32_t bars, uint32_t bar, uint32_t parity, int32_t* status) {
-    if (over(bars + bar, parity)) return true;
-    uint64_t t0 = 0;
+// Microseconds of a sort (1,024 ns each), never 0.
+__device__ __forceinline__ uint32_t globaltimer_us() { return static_cast<uint32_t>(globaltimer_ns() >> 10) | 1u; }
+
+// Waits for a phase of the barrier at `bar`; false when it took too long or another warp
+// has given up.  All lanes of a warp are here together, and get one answer: where a lane
+// gave up as its neighbours went on, these would wait for it at their next warp-wide
+// instruction.  (The timer is read rarely: that takes longer than most waits.)
+__device__ __forceinline__ bool wait(const ChunkParams& p, uint32_t bars, uint32_t bar, uint32_t parity) {
+    if (__all_sync(0xffffffffu, over(bars + bar, parity))) return true;
+    uint32_t since = 0;
 #pragma unroll 1
     for (uint32_t it = 1;; ++it) {
-        if (over(bars + bar, parity)) return true;
+        if (__all_sync(0xffffffffu, over(bars + bar, parity))) return true;
         if ((it & 63u) == 0) {
-            if (lds32(bars + kAbort) != 0) return false;
-            const uint64_t now = (it & 1023u) == 0 ? globaltimer_ns() : 0;
-            if (now != 0 && t0 == 0) t0 = now;
-            if (now != 0 && now - t0 > 2000000000ull) {
-                asm volatile("st.volatile.shared.u32 [%0], 1;" ::"r"(bars + kAbort) : "memory");
-                if (status != nullptr) atomicOr(status, TQ_DEV_TIMEOUT);
-                return false;
+            bool stop = lds32(bars + kAbort) != 0;
+            if ((it & 1023u) == 0) {
+                const uint32_t now = globaltimer_us();
+                if (since == 0) since = now;
+                if (now - since > p.limit_us) {
+                    stop = true;
+                    asm volatile("st.volatile.shared.u32 [%0], 1;" ::"r"(bars + kAbort) : "memory");
+                    if (p.status != nullptr) atomicOr(p.status, TQ_DEV_TIMEOUT);
+                }
             }
+            if (__any_sync(0xffffffffu, stop)) return false;
         }
     }
 }
@@ -270,7 +278,7 @@ __device__ __forceinline__ void load_role(const ChunkParams& p, const Work& w, u
     uint32_t parity = 1;
     bool ok = true;
     auto issue = [&](const uint8_t* from, int tile, long long row) {
-        if (!wait(bars, kRingEmpty + r * 8, parity, p.status)) return false;
+        if (issued == p.copies || !wait(p, bars, kRingEmpty + r * 8, parity)) return false;
         const int rows = min(C::kTile, (w.khi - (w.tile0 + tile) * C::kTile + 15) & ~15);  // capacities are whole 16s
         const uint32_t bar = bars + kRingFull + r * 8;
         if (lane == 0) asm volatile("mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(rows * (D * BITS / 8 + C::kBlocks * 4)) : "memory");
@@ -298,11 +306,10 @@ __device__ __forceinline__ void load_role(const ChunkParams& p, const Work& w, u
         row = next;
         next = after;
     }
-    if (!ok) {  // given up: the copies in flight land before the CTA leaves
-        for (int k = max(0, issued - ring_entries); k < issued; ++k)
-            for (int it = 0; it < 1 << 20 && !over(bars + kRingFull + k % ring_entries * 8, (k / ring_entries) & 1); ++it) {
-            }
-    }
+    // the copies in flight land before the CTA leaves (also where other warps have given up)
+    for (int k = max(0, issued - ring_entries); k < issued; ++k)
+        for (int it = 0; it < 1 << 20 && !over(bars + kRingFull + k % ring_entries * 8, (k / ring_entries) & 1); ++it) {
+        }
 }
 
 // ---------------------------------------------------------------- unpacking --
@@ -382,8 +389,8 @@ __device__ __forceinline__ void unpack_role(const ChunkParams& p, const Work& w,
     uint32_t r_parity = 0, s_parity = 1;
 #pragma unroll 1
     for (int e = 0; e < 2 * w.tiles; ++e) {
-        if (!wait(bars, kRingFull + r * 8, r_parity, p.status)) return;
-        if (!wait(bars, kSlotEmpty + s * 8, s_parity, p.status)) return;  // (a fresh barrier's phase before the first is over)
+        if (!wait(p, bars, kRingFull + r * 8, r_parity)) return;
+        if (!wait(p, bars, kSlotEmpty + s * 8, s_parity)) return;  // (a fresh barrier's phase before the first is over)
         int tile;
         const bool value = entry_of(e, w.tiles, tile);
         const int t0 = (w.tile0 + tile) * C::kTile;
@@ -472,31 +479,31 @@ struct Slots {
     int entry = 0;
     uint32_t slot = 0, parity = 0;
     // Waits for entry e (entries are visited in order).
-    __device__ __forceinline__ bool ready(int e, uint32_t bars, int32_t* status) {
+    __device__ __forceinline__ bool ready(const ChunkParams& p, int e, uint32_t bars) {
 #pragma unroll 1
         for (; entry < e; ++entry)
             if (++slot == C::kSlots) {
                 slot = 0;
                 parity ^= 1;
             }
-        return wait(bars, kSlotFull + slot * 8, parity, status);
+        return wait(p, bars, kSlotFull + slot * 8, parity);
     }
 };
 
 template <int D, int BITS>
-__device__ __forceinline__ bool scores_role(const ChunkParams& p, const Work& w, uint32_t q, uint32_t slots, uint32_t bars, bool pair) {
+__device__ __forceinline__ void scores_role(const ChunkParams& p, const Work& w, uint32_t q, uint32_t slots, uint32_t bars, bool pair) {
     using C = Cfg<D, BITS>;
     const uint32_t tmem = fixed(lds32(bars + kTmemAt)), q_op = fixed(smem_operand(q, 16)), k_op = fixed(smem_operand(slots, 16));
     const int turns = pair ? 2 * w.tiles : w.tiles;
     Slots<D, BITS> in;
-    if (!wait(bars, kQFull, 0, p.status)) return false;
+    if (!wait(p, bars, kQFull, 0)) return;
 #pragma unroll 1
     for (int n = 0; n < turns; ++n) {
         const bool first = !pair || (n & 1) == 0, last = !pair || (n & 1) != 0;
-        if (first && !in.ready(key_entry(pair ? n >> 1 : n), bars, p.status)) return false;
+        if (first && !in.ready(p, key_entry(pair ? n >> 1 : n), bars)) return;
         if (n >= C::kPlaces) {
-            const bool ok = C::kPlaces == 1 ? wait(bars, kSFree, (n - 1) & 1, p.status) : wait(bars, kSFree + (n & 1) * 8, ((n >> 1) - 1) & 1, p.status);
-            if (!ok) return false;
+            const bool ok = C::kPlaces == 1 ? wait(p, bars, kSFree, (n - 1) & 1) : wait(p, bars, kSFree + (n & 1) * 8, ((n >> 1) - 1) & 1);
+            if (!ok) return;
         }
         tc_fence_after();
         uint32_t a = q_op + (pair ? n & 1 : 0) * ((kRowTile * D * 2) >> 4), b = k_op + in.slot * (C::kSlot >> 4);
@@ -514,11 +521,10 @@ __device__ __forceinline__ bool scores_role(const ChunkParams& p, const Work& w,
         }
         __syncwarp();
     }
-    return true;
 }
 
 template <int D, int BITS>
-__device__ __forceinline__ bool outputs_role(const ChunkParams& p, const Work& w, uint32_t slots, uint32_t bars, bool pair) {
+__device__ __forceinline__ void outputs_role(const ChunkParams& p, const Work& w, uint32_t slots, uint32_t bars, bool pair) {
     using C = Cfg<D, BITS>;
     const uint32_t tmem = fixed(lds32(bars + kTmemAt)), v_op = fixed(smem_operand(slots, C::kTile * 128));
     const int turns = pair ? 2 * w.tiles : w.tiles;
@@ -526,8 +532,8 @@ __device__ __forceinline__ bool outputs_role(const ChunkParams& p, const Work& w
 #pragma unroll 1
     for (int n = 0; n < turns; ++n) {
         const bool first = !pair || (n & 1) == 0, last = !pair || (n & 1) != 0;
-        if (first && !in.ready(value_entry(pair ? n >> 1 : n, w.tiles), bars, p.status)) return false;
-        if (!wait(bars, kPFull + (n & 1) * 8, (n >> 1) & 1, p.status)) return false;
+        if (first && !in.ready(p, value_entry(pair ? n >> 1 : n, w.tiles), bars)) return;
+        if (!wait(p, bars, kPFull + (n & 1) * 8, (n >> 1) & 1)) return;
         tc_fence_after();
         uint32_t b = v_op + in.slot * (C::kSlot >> 4), a = tmem + C::kP + (n & 1) * C::kPStep;
         const uint32_t o = tmem + C::kO + (C::kStreams == 2 ? (n & 1) * D : 0);
@@ -545,7 +551,6 @@ __device__ __forceinline__ bool outputs_role(const ChunkParams& p, const Work& w
         }
         __syncwarp();
     }
-    return true;
 }
 
 // ------------------------------------------------------------------ softmax --
@@ -695,7 +700,7 @@ __device__ __forceinline__ bool softmax_loop(const ChunkParams& p, const Work& w
 #pragma unroll 1
     for (int n = stream; n < turns; n += C::kStreams) {
         const uint32_t odd = n & 1, phase = (n >> 1) & 1;
-        if (!wait(bars, kSFull + odd * 8, phase, p.status)) return false;
+        if (!wait(p, bars, kSFull + odd * 8, phase)) return false;
         tc_fence_after();
         float s[N];
         if (active) {
@@ -726,7 +731,7 @@ __device__ __forceinline__ bool softmax_loop(const ChunkParams& p, const Work& w
                 if (!fresh) {
                     // O holds the products of the turns before: all of them have to be over
                     const uint32_t before = C::kStreams == 1 ? n - 1 : n - 2;
-                    if (!wait(bars, kPvDone + (before & 1) * 8, (before >> 1) & 1, p.status)) return false;
+                    if (!wait(p, bars, kPvDone + (before & 1) * 8, (before >> 1) & 1)) return false;
                     tc_fence_after();
                     if (begins) empty_chain<D, BITS>(p, oa, stream, n / C::kStreams == C::kChain, st);
                 }
@@ -747,7 +752,7 @@ __device__ __forceinline__ bool softmax_loop(const ChunkParams& p, const Work& w
             }
         }
         // P's columns are free once the product before the last is over
-        if (n >= 2 && !wait(bars, kPvDone + odd * 8, phase ^ 1, p.status)) return false;
+        if (n >= 2 && !wait(p, bars, kPvDone + odd * 8, phase ^ 1)) return false;
         if (active) {
             tc_fence_after();
             const float base = st.m == -INFINITY ? 0.f : -st.m;
@@ -802,10 +807,11 @@ __device__ __forceinline__ void softmax_role(const ChunkParams& p, const Work& w
     const uint32_t tmem = fixed(lds32(bars + kTmemAt) + (static_cast<uint32_t>((threadIdx.x >> 5) & 3) << 21));  // the warp's lanes
     State st{-INFINITY, 0.f};
     bool ok = softmax_loop<D, BITS>(p, w, bars, tmem, stream, pair, active, lo, hi, st);
+    if (!ok) tmem_wait_st();  // given up: nothing is on its way to TMEM when it is freed
     // the last of this accumulator's products
     const int turns = pair ? 2 * w.tiles : w.tiles, last = C::kStreams == 1 ? turns - 1 : ((turns - 1 - stream) & ~1) + stream;
     if (ok && turns > stream) {
-        ok = wait(bars, kPvDone + (last & 1) * 8, (last >> 1) & 1, p.status);
+        ok = wait(p, bars, kPvDone + (last & 1) * 8, (last >> 1) & 1);
         tc_fence_after();
     }
     // Where both accumulators are those of one row tile, the second one's state through
@@ -963,13 +969,16 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         regs_lower<48>();
         if (warp == 16 || warp == 18) {
             const uint32_t at = fixed(smem_u32(&bars)), in = fixed(smem_u32(slots));
-            if (!(warp == 16 ? scores_role<D, BITS>(p, w, fixed(smem_u32(qs)), in, at, pair) : outputs_role<D, BITS>(p, w, in, at, pair))) {
-                __syncwarp();
-                const uint32_t bar = at + kDrain + (warp == 18 ? 8 : 0);
-                if (elect_one()) tc_commit(bar);  // given up: products in flight end before the CTA leaves
-                __syncwarp();
-                for (int it = 0; it < 1 << 20 && !over(bar, 0); ++it) {
-                }
+            if (warp == 16)
+                scores_role<D, BITS>(p, w, fixed(smem_u32(qs)), in, at, pair);
+            else
+                outputs_role<D, BITS>(p, w, in, at, pair);
+            __syncwarp();
+            // products in flight end before the CTA leaves (they may be where a warp has given up)
+            const uint32_t bar = at + kDrain + (warp == 18 ? 8 : 0);
+            if (elect_one()) tc_commit(bar);
+            __syncwarp();
+            for (int it = 0; it < 1 << 20 && !over(bar, 0); ++it) {
             }
         } else if (warp == 17) {
             load_role<D, BITS>(p, w, fixed(smem_u32(ring)), fixed(smem_u32(qs + kRowTile * D * 2)), ring_entries, fixed(smem_u32(&bars)));

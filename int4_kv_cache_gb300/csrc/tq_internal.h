@@ -334,6 +334,8 @@ struct ChunkParams {
     int32_t m_items, rows_per_item, n_splits, whole;
     uint32_t group_magic;     // floor(t / group_q) = umulhi(t, magic) >> shift for 0 <= t < 2^31 (0: group_q = 1)
     int32_t group_shift;
+    uint32_t limit_us;        // longest wait inside the kernel, 1,024 ns each
+    int32_t copies;           // the diagnostic: entries that a CTA's copying warp brings before it stops
     float* part_m;            // [(items - whole) * n_splits][rows_per_item], log2 units: what the part's weights count from (n_splits > 1)
     float* part_l;
     float* part_acc;          // [(items - whole) * n_splits][rows_per_item][D]

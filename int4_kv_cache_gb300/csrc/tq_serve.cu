@@ -13,6 +13,10 @@ namespace {
 // ------------------------------------------------------------ several rows --
 constexpr long long kMaxChunkRows = 1LL << 28;  // n * num_heads
 
+// Longest wait inside the kernel (a tile of keys takes microseconds).
+constexpr uint32_t kChunkLimitUs = 2000000;
+constexpr int32_t kAllCopies = 0x7fffffff;
+
 // Most CTAs of a call that splits keys (bounds its workspace independently of the device).
 constexpr int kMaxChunkParts = 640;
 
@@ -104,8 +108,11 @@ tq_status check_chunk(const Store& c, const tq_query_rows* q, const int32_t* q_l
 }
 
 tq_status chunk(const Store& c, const tq_query_rows* q, const int32_t* q_lens, const int32_t* seq_lens, int32_t max_seq_len, float attn_scale,
-                int32_t window, uint32_t flags, void* workspace, uint16_t* out, int32_t* status, cudaStream_t stream) {
+                int32_t window, uint32_t flags, void* workspace, uint16_t* out, int32_t* status, cudaStream_t stream, uint32_t limit_us = kChunkLimitUs,
+                int32_t copies = kAllCopies) {
     ChunkParams p{};
+    p.limit_us = limit_us;
+    p.copies = copies;
     p.q = q->x;
     p.stride_b = q->stride_b;
     p.stride_h = q->stride_h;
@@ -309,6 +316,18 @@ tq_status tq_paged_sdpa_chunk(const tq_paged_kv_cache* cache, const tq_query_row
         return tq_paged_sdpa_int4_decode(cache, q->x, q->num_heads, seq_lens, max_seq_len, attn_scale, TQ_DEFAULT_CHUNK, flags & ~TQ_CHUNK_FULL, workspace, workspace_bytes,
                                          out, status, stream);
     return chunk(st, q, q_lens, seq_lens, max_seq_len, attn_scale, window, flags, workspace, out, status, static_cast<cudaStream_t>(stream));
+}
+
+tq_status tq_chunk_timeout_selftest(const tq_kv_cache* cache, const tq_query_rows* q, const int32_t* seq_lens, int32_t max_seq_len, float attn_scale,
+                                    uint32_t limit_us, int32_t copies, void* workspace, size_t workspace_bytes, uint16_t* out, int32_t* status,
+                                    void* stream) {
+    Store st;
+    tq_status s = store_of(cache, &st);
+    if (s == TQ_OK && status == nullptr) s = TQ_ERR_NULL;
+    if (s == TQ_OK) s = check_chunk(st, q, nullptr, seq_lens, max_seq_len, 0, 0, workspace, workspace_bytes, out, status);
+    if (s == TQ_OK && (limit_us < 1 || limit_us > 100000 || copies < 0)) s = TQ_ERR_SHAPE;
+    if (s != TQ_OK || q->n == 0) return s;
+    return chunk(st, q, nullptr, seq_lens, max_seq_len, attn_scale, 0, 0, workspace, out, status, static_cast<cudaStream_t>(stream), limit_us, copies);
 }
 
 size_t tq_pages_workspace_bytes(int32_t batch, int32_t num_pages, int32_t max_pages_per_seq) {
