@@ -676,7 +676,9 @@ tq_status tq_paged_kv_evict(const tq_paged_kv_cache* src, const tq_paged_kv_cach
  * TQ_CHUNK_FULL: every row attends to all of [0, seq_lens[b]) (window must be 0).
  * A row with nothing to attend to (p < 0, an empty sequence) is a row of zeros.
  *   out       fp16 [batch][n][num_heads][head_dim], contiguous: the rows that an
- *             output projection takes; must not overlap q's rows
+ *             output projection takes
+ * out, the workspace and the status word must not overlap one another, the span from
+ * q's first row to its last, the lengths or the cache (TQ_ERR_SHAPE).
  * Head grouping, lengths and max_seq_len, attn_scale and the rotation flags as in
  * tq_sdpa_int4_decode_ex; lengths outside [0, n] and [0, max_seq_len] are clamped
  * and set TQ_DEV_SEQ_LEN.

@@ -10,6 +10,32 @@ using namespace tq;
 
 namespace {
 
+// ---------------------------------------------------------------- overlaps --
+struct Span {
+    const void* at;
+    unsigned long long bytes;
+};
+
+// Whether one of the first `writes` spans shares a byte with any other (same: two that may be one array).
+bool clash(const Span* s, int n, int writes, int same_a = -1, int same_b = -1, int same_c = -1, int same_d = -1) {
+    for (int i = 0; i < writes; ++i)
+        for (int j = 0; j < n; ++j) {
+            if (i == j) continue;
+            const bool may = (i == same_a && j == same_b) || (i == same_b && j == same_a) || (i == same_c && j == same_d) || (i == same_d && j == same_c);
+            if (may && s[i].at == s[j].at) continue;
+            if (overlap(s[i].at, s[i].bytes, s[j].at, s[j].bytes)) return true;
+        }
+    return false;
+}
+
+int arrays_of(const Store& c, Span* s) {
+    const unsigned long long rows = static_cast<unsigned long long>(c.map.num_pages) * c.num_kv_heads * c.map.page_tokens;
+    const unsigned long long codes = rows * (c.head_dim * c.bits / 8), sb = rows * (c.head_dim / kGroup * 2);
+    const void* at[6] = {c.k_codes, c.v_codes, c.k_scale, c.k_bias, c.v_scale, c.v_bias};
+    for (int i = 0; i < 6; ++i) s[i] = {at[i], i < 2 ? codes : sb};
+    return 6;
+}
+
 // ------------------------------------------------------------ several rows --
 constexpr long long kMaxChunkRows = 1LL << 28;  // n * num_heads
 
@@ -101,10 +127,17 @@ tq_status check_chunk(const Store& c, const tq_query_rows* q, const int32_t* q_l
         !aligned4(q_lens) || !aligned4(status))
         return TQ_ERR_ALIGN;
     if (q->n == 0) return TQ_OK;
+    const size_t need = chunk_bytes(c.batch, q->num_heads, c.num_kv_heads, c.head_dim, q->n, max_seq_len);
+    const tq_status s = check_workspace(workspace, workspace_bytes, need);
+    if (s != TQ_OK) return s;
     const unsigned long long extent = 2ull * (static_cast<unsigned long long>(c.batch - 1) * q->stride_b + static_cast<unsigned long long>(q->n - 1) * q->stride_t +
                                               static_cast<unsigned long long>(q->num_heads - 1) * q->stride_h + c.head_dim);
-    if (overlap(out, 2ull * c.batch * q->n * q->num_heads * c.head_dim, q->x, extent)) return TQ_ERR_SHAPE;
-    return check_workspace(workspace, workspace_bytes, chunk_bytes(c.batch, q->num_heads, c.num_kv_heads, c.head_dim, q->n, max_seq_len));
+    // written: out, workspace, status
+    Span sp[16] = {{out, 2ull * c.batch * q->n * q->num_heads * c.head_dim}, {workspace, need}, {status, status != nullptr ? 4ull : 0ull}, {q->x, extent},
+                   {seq_lens, 4ull * c.batch}, {q_lens, q_lens != nullptr ? 4ull * c.batch : 0ull},
+                   {c.map.block_table, c.paged ? 4ull * c.batch * c.map.max_pages : 0ull}};
+    const int n = 7 + arrays_of(c, sp + 7);
+    return clash(sp, n, 3) ? TQ_ERR_SHAPE : TQ_OK;
 }
 
 tq_status chunk(const Store& c, const tq_query_rows* q, const int32_t* q_lens, const int32_t* seq_lens, int32_t max_seq_len, float attn_scale,
@@ -210,31 +243,6 @@ PagesSpace pages_space(int32_t batch, int32_t num_pages, int32_t max_pages) {
 
 bool pages_sizes(int32_t batch, int32_t num_pages, int32_t max_pages) {
     return batch >= 1 && num_pages >= 1 && num_pages <= kMaxEntries && max_pages >= 1 && static_cast<long long>(batch) * max_pages <= kMaxEntries;
-}
-
-struct Span {
-    const void* at;
-    unsigned long long bytes;
-};
-
-// Whether one of the first `writes` spans shares a byte with any other (same: two that may be one array).
-bool clash(const Span* s, int n, int writes, int same_a = -1, int same_b = -1, int same_c = -1, int same_d = -1) {
-    for (int i = 0; i < writes; ++i)
-        for (int j = 0; j < n; ++j) {
-            if (i == j) continue;
-            const bool may = (i == same_a && j == same_b) || (i == same_b && j == same_a) || (i == same_c && j == same_d) || (i == same_d && j == same_c);
-            if (may && s[i].at == s[j].at) continue;
-            if (overlap(s[i].at, s[i].bytes, s[j].at, s[j].bytes)) return true;
-        }
-    return false;
-}
-
-int arrays_of(const Store& c, Span* s) {
-    const unsigned long long rows = static_cast<unsigned long long>(c.map.num_pages) * c.num_kv_heads * c.map.page_tokens;
-    const unsigned long long codes = rows * (c.head_dim * c.bits / 8), sb = rows * (c.head_dim / kGroup * 2);
-    const void* at[6] = {c.k_codes, c.v_codes, c.k_scale, c.k_bias, c.v_scale, c.v_bias};
-    for (int i = 0; i < 6; ++i) s[i] = {at[i], i < 2 ? codes : sb};
-    return 6;
 }
 
 tq_status pages_params(const Store& c, const int32_t* refs, const int32_t* held, void* workspace, size_t workspace_bytes, int32_t* status, PagesParams* p) {
