@@ -683,9 +683,9 @@ tq_status tq_paged_kv_evict(const tq_paged_kv_cache* src, const tq_paged_kv_cach
  * tq_sdpa_int4_decode_ex; lengths outside [0, n] and [0, max_seq_len] are clamped
  * and set TQ_DEV_SEQ_LEN.
  * Cached values enter as scale * code + bias rounded to fp16 (above 65,504: that),
- * softmax weights as fp16; sums and softmax states are fp32.  So against fp64
- * attention over the dequantised cache a score is off by 2^-11 attn_scale
- * sum_d |q_d K_d| at most, and an output by what such scores make of it, 2^-10
+ * softmax weights as fp16, queries turned for TQ_ROTATE_K as fp16 again; sums and
+ * softmax states are fp32.  So against fp64 attention over the dequantised cache a score
+ * is off by 2^-11 attn_scale sum_d |q_d K_d| at most (with TQ_ROTATE_K by twice that), and an output by what such scores make of it, 2^-10
  * sum_t p_t |V_t| and its own rounding (all rows together: 4e-4 rel-L2 for normally
  * distributed rows, up to 1.5e-3 with a key channel twenty times as large).  Weights
  * below 2^-21 of a row's largest, p_max, have fewer bits: the tokens t that hold them

@@ -597,7 +597,8 @@ __device__ __forceinline__ void load_query(const ChunkParams& p, const Work& w, 
     }
 }
 
-// The same for a cache of rotated keys: a warp a row.
+// The same for a cache of rotated keys: a warp a row, turned in fp32 and rounded to fp16,
+// the operand's type, once more.
 template <int D, int BITS>
 __device__ __forceinline__ void load_query_rotated(const ChunkParams& p, const Work& w, uint8_t* tile, int tid, int tile_row0) {
     constexpr int E = D / 32;
