@@ -518,14 +518,16 @@ cudaError_t launch_pages_fork(const PagesParams& p, int sms, cudaStream_t stream
 }
 
 cudaError_t launch_pages_reserve(const PagesParams& p, int sms, cudaStream_t stream) {
-    if (p.batch <= kSmallSeqs && (p.n_rows + p.page_tokens - 2) / p.page_tokens + 1 <= 32)
+    // the most entries that a sequence's rows fall into (rows and a page may pass 2^31 together)
+    const long long entries = (static_cast<long long>(p.n_rows) + p.page_tokens - 2) / p.page_tokens + 1;
+    if (p.batch <= kSmallSeqs && entries <= 32)
         reserve_small_kernel<<<1, kPlanThreads, 0, stream>>>(p);
     else
         reserve_plan_kernel<<<1, kPlanThreads, 0, stream>>>(p);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     // no more units of work than heads of the arrays of the pages that the rows touch
-    const long long units = 6LL * p.num_kv_heads * p.batch * ((p.n_rows + p.page_tokens - 2) / p.page_tokens + 1);
+    const long long units = 6LL * p.num_kv_heads * p.batch * entries;
     return launch_after(move_rows_kernel, static_cast<unsigned>(units < 4LL * sms ? units : 4LL * sms), kCopyThreads, stream, p);
 }
 
