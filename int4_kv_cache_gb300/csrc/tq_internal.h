@@ -367,8 +367,8 @@ struct PagesParams {
     int32_t* head;            // [2]: moves, used pages
     int32_t* page_a;          // [num_pages]
     int32_t* page_b;          // [num_pages]
-    int32_t* seq_a;           // [B + 1]
-    int32_t* seq_b;           // [B + 1]
+    int32_t* seq_a;           // [B]
+    int32_t* seq_b;           // [B]
     int32_t* old_table;       // [B][max_pages]
     PageMove* moves;          // [max(num_pages, B * max_pages)]
     // the rows
