@@ -694,12 +694,14 @@ tq_status tq_paged_kv_evict(const tq_paged_kv_cache* src, const tq_paged_kv_cach
  * bits for a softmax: rows that have such are undefined.  Cached rows whose scale or bias is not finite leave the
  * outputs of the rows that attend to them undefined, and no others; so do query rows
  * that are not finite for themselves.
- * One contiguous row per sequence (n = 1, no q_lens, no window) is that decode itself.
+ * One contiguous row per sequence (n = 1, no q_lens, no window) is that decode itself,
+ * which rounds no key: closer than the same row passed in another way.
  * workspace: tq_chunk_workspace_bytes(...) bytes, 256-byte aligned, one per call in
  * flight (not looked at where n = 0; past 8,192 tokens it holds the output's rows in
  * fp32); it also serves fewer rows, sequences and tokens of
  * the same heads.  n = 0 launches nothing.  batch and kv heads up to
- * 65,535, n * num_heads up to 2^28, caches up to 2^30 tokens. */
+ * 65,535, n * num_heads up to 2^28, tiles of 128 rows over all sequences and kv heads below
+ * 2^30, caches up to 2^30 tokens. */
 #define TQ_CHUNK_FULL 0x200u
 typedef struct tq_query_rows {
     const uint16_t* x;

@@ -37,10 +37,11 @@
 // What bounds it (GB300, 64 query and 8 kv heads of 128, int4): for long chunks the
 // turn of the one place for S (a product of 512 cycles, then some 800 of commits, waits
 // and reads until it is free again) and the instructions of softmax and unpacking (65 %
-// of the issue slots): 2,048 tokens over 65,536 in 2.67 ms, 1.62 PFLOP/s; a prompt of 8,192
-// in 0.83 ms, 1.33 PFLOP/s with 16,000 cycles of start and end in each CTA.  For eight
-// tokens over 131,072 it is the unpacking (2,090 cycles a tile of 128 keys, 800 of HBM
-// time): 71.3 us, of which 23 are what the cache's bytes take.
+// of the issue slots): 2,048 tokens over 65,536 in 2.73 ms, 1.59 PFLOP/s (3.11 ms and 1.39
+// where many such calls bring the clocks down by power); a prompt of 8,192
+// in 0.84 ms, 1.32 PFLOP/s with 16,000 cycles of start and end in each CTA.  For eight
+// tokens over 131,072 it is the unpacking (2,100 cycles a tile of 128 keys, 800 of HBM
+// time): 73.1 us, of which 23 are what the cache's bytes take.
 #include <stddef.h>
 
 #include "tq_device.cuh"

@@ -5,8 +5,8 @@
 // The bookkeeping is integer work over tables of some thousand entries: bound by
 // latency, so it is done by one CTA (its phases ordered by CTA barriers), and
 // the copies of rows by a second launch over the whole device that reads the
-// list of moves the first one left.  (32 beams forked and given room for a token: 11.8 us
-// in three launches; half of 4,096 pages of 147 KB compacted: 54.7 us, 47 of them
+// list of moves the first one left.  (32 beams forked and given room for a token: 12.2 us
+// in three launches; half of 4,096 pages of 147 KB compacted: 55.0 us, 47 of them
 // copies at 6.4 TB/s, 7 the list.)
 #include "tq_device.cuh"
 #include "tq_internal.h"
@@ -19,7 +19,7 @@ constexpr int kPlanThreads = 1024;
 constexpr int kCopyThreads = 256;
 // Largest table that a fork stages in one CTA's shared memory: one launch instead of two (32 x 65
 // entries), but one CTA's reads and atomics (64 x 131 entries and the reservation behind
-// them: 23.8 us in one CTA, 17.8 over the device).
+// them: 23.8 us in one CTA, 17.8 over the device when this was chosen).
 constexpr int kForkEntries = 8192;
 constexpr int kForkSeqs = kPlanThreads;
 
