@@ -876,7 +876,8 @@ def tq_sdpa_chunk(cache, q: torch.Tensor, seq_lens: torch.Tensor, max_seq_len: i
                   status: Optional[torch.Tensor] = None, stream=None, flags: int = 0) -> torch.Tensor:
     """Attention of the last q_lens[b] (None: n) rows of every sequence, q [B, Hq, n, D] fp16 (strides of whole 8-element
     steps), over the cache that holds them: causal, the last ``window`` rows only where window > 0; with TQ_CHUNK_FULL every
-    row over the whole sequence (cross attention).  -> out [B, n, Hq, D]; its rows behind q_lens[b] are left as they were."""
+    row over the whole sequence (cross attention).  -> out [B, n, Hq, D]; its rows behind q_lens[b] are left as they were.
+    (Windows past max_seq_len are none, also past what the library's 32 bits hold.)"""
     if not q.is_cuda or q.dtype != torch.float16 or q.dim() != 4 or (q.numel() > 0 and q.stride(3) != 1):
         raise ValueError("q: expected a CUDA float16 tensor [B, Hq, n, D] with a contiguous last dimension")
     b, hq, n, d = q.shape
@@ -901,7 +902,7 @@ def tq_sdpa_chunk(cache, q: torch.Tensor, seq_lens: torch.Tensor, max_seq_len: i
     # a dimension of one is never stepped along, whatever its stride says
     rows = tq_query_rows(q.data_ptr(), sb if b > 1 else 0, sh if hq > 1 else 0, st if n > 1 else 0, hq, n)
     _check("tq_sdpa_chunk", _fn(cache, "sdpa_chunk")(
-        cache.ref(), rows, _at(q_lens), seq_lens.data_ptr(), int(max_seq_len), float(attn_scale), int(window), int(flags),
+        cache.ref(), rows, _at(q_lens), seq_lens.data_ptr(), int(max_seq_len), float(attn_scale), min(int(window), int(max_seq_len)), int(flags),
         workspace.data_ptr(), workspace.numel(), out.data_ptr(), _at(status), on))
     return out
 

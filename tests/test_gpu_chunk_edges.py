@@ -26,6 +26,18 @@ def test_wide_windows_over_short_sequences(D, bits, paged, window):
     assert torch.equal(attend(torch, tq, c, q, lens, window=window), want)
 
 
+def test_windows_of_any_size():
+    """A window that 32 bits do not hold is none, not what is left of it."""
+    torch = need_gpu()
+    import int4_kv_cache_gb300 as tq
+
+    c = make_cache(tq, torch, 1, 2, 128, 700, seed=5)
+    q = queries(torch, (1, 8, 90, 128), 6)
+    want = attend(torch, tq, c, q, [700])
+    for window in (2 ** 31, 2 ** 32 + 10, 2 ** 63 - 1):
+        assert torch.equal(attend(torch, tq, c, q, [700], window=window), want)
+
+
 def steps_of_weight(torch, tq, D, bits, L, n, G, keys, seed):
     """(output, fp64 output, fp64 sum_t p_t |V_t|, max_t p_t sum_t |V_t|) of rows that all have the weights
     2^keys[t]: keys that hold multiples of 1/16 and values of 1/8 are exact in fp16, queries select a channel."""
