@@ -266,6 +266,7 @@ __global__ void __launch_bounds__(kPlanThreads) reserve_plan_kernel(PagesParams 
             at += __popc(mask);
         }
         for (int j = r.held + lane; j <= r.last; j += 32) row[j] = p.old_table[at + j - r.held];
+        __syncwarp();  // every lane has read the old count
         if (lane == 0 && r.last >= r.held) p.held[b] = r.last + 1;
     }
     __syncthreads();
