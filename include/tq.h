@@ -685,23 +685,24 @@ tq_status tq_paged_kv_evict(const tq_paged_kv_cache* src, const tq_paged_kv_cach
  * Cached values enter as scale * code + bias rounded to fp16 (above 65,504: that),
  * softmax weights as fp16, queries turned for TQ_ROTATE_K as fp16 again; sums and
  * softmax states are fp32.  So against fp64 attention over the dequantised cache a score
- * is off by 2^-11 attn_scale sum_d |q_d K_d| at most (with TQ_ROTATE_K by twice that), and an output by what such scores make of it, 2^-10
- * sum_t p_t |V_t| and its own rounding (all rows together: 4e-4 rel-L2 for normally
- * distributed rows, up to 1.5e-3 with a key channel twenty times as large).  Weights
- * below 2^-21 of a row's largest, p_max, have fewer bits: the tokens t that hold them
- * add up to 2^-32 p_max sum_t |V_t|.  The tensor cores' sums are cut off, not rounded: at
- * most 2^-11 sum_t p_t |V_t| of an output (5e-5 of it where all values have one sign), whatever the length.  Scores from some 10^6 on in magnitude leave fp32 too few
- * bits for a softmax: rows that have such are undefined.  Cached rows whose scale or bias is not finite leave the
- * outputs of the rows that attend to them undefined, and no others; so do query rows
- * that are not finite for themselves.
+ * is off by 2^-11 attn_scale sum_d |q_d K_d| at most (with TQ_ROTATE_K by twice that),
+ * and an output by what such scores make of it, 2^-10 sum_t p_t |V_t| and its own
+ * rounding (all rows together: 4e-4 rel-L2 for normally distributed rows, up to 1.5e-3
+ * with a key channel twenty times as large).  Weights below 2^-21 of a row's largest,
+ * p_max, have fewer bits: the tokens t that hold them add up to 2^-32 p_max sum_t |V_t|.
+ * The tensor cores' sums are cut off, not rounded: at most 2^-11 sum_t p_t |V_t| of an
+ * output (5e-5 of it where all values have one sign), whatever the length.  Scores from
+ * some 10^6 on in magnitude leave fp32 too few bits for a softmax: rows that have such
+ * are undefined.  Cached rows whose scale or bias is not finite leave the outputs of the
+ * rows that attend to them undefined, and no others; so do query rows that are not
+ * finite for themselves.
  * One contiguous row per sequence (n = 1, no q_lens, no window) is that decode itself,
  * which rounds no key: closer than the same row passed in another way.
  * workspace: tq_chunk_workspace_bytes(...) bytes, 256-byte aligned, one per call in
  * flight (not looked at where n = 0; past 8,192 tokens it holds the output's rows in
- * fp32); it also serves fewer rows, sequences and tokens of
- * the same heads.  n = 0 launches nothing.  batch and kv heads up to
- * 65,535, n * num_heads up to 2^28, tiles of 128 rows over all sequences and kv heads below
- * 2^30, caches up to 2^30 tokens. */
+ * fp32); it also serves fewer rows, sequences and tokens of the same heads.  n = 0
+ * launches nothing.  batch and kv heads up to 65,535, n * num_heads up to 2^28, tiles of
+ * 128 rows over all sequences and kv heads below 2^30, caches up to 2^30 tokens. */
 #define TQ_CHUNK_FULL 0x200u
 typedef struct tq_query_rows {
     const uint16_t* x;

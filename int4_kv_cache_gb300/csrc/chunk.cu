@@ -22,7 +22,7 @@
 // merged in the end.  P starts at 2^7, and O is rescaled only when a row's maximum grows by
 // more than 2^8 (the published conditional rescaling of online softmax), which is rare
 // after the first tiles: P uses fp16's range up to 2^15, so that weights down to 2^-21 of a
-// row's largest keep all their bits and those down to 2^-32 of it are more than zero.  (With P
+// row's largest keep all their bits and those above 2^-32 of it are more than zero.  (With P
 // from 1 up, a key that took most of a row's weight left nothing of the others 25
 // powers of two below it, however many.)  Where there are few items
 // for the SMs their keys are cut into runs, whose states a second kernel merges.
